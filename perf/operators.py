@@ -47,21 +47,21 @@ def listed():
         # one sequence's next token: only the call's latency counts
         _rope("rope 1 token", 1, 32, 8, 128, False, "none", 8192),
         # a decode batch at far positions of a long-context server, half of each head rotated
-        _rope("rope 64 far, half heads", 64, 56, 8, 64, True, "parts", 1 << 20),
+        _rope("rope 64 far half heads", 64, 56, 8, 64, True, "parts", 1 << 20),
         # a ragged step padded to a fixed size for a captured graph, an odd rotary size
-        _rope("rope 333 padded, odd size", 333, 32, 4, 50, False, "linear", 30000, pad=13, block=48),
+        _rope("rope 333 padded odd size", 333, 32, 4, 50, False, "linear", 30000, pad=13, block=48),
         # whole prompts of a batch: bandwidth
         _rope("rope 16384 prompt tokens", 16384, 32, 8, 128, False, "smooth", 131072),
 
         # one chat alone on the machine, capped scores: latency
         _decode("decode b1 capped", "paged", 1, 32, 8, 1000, 1000, softcap=50.0),
         # a full ragged batch of a model whose layers see a window, capped scores
-        _decode("decode b64 capped, window", "paged", 64, 32, 8, 16, 8192, softcap=50.0,
+        _decode("decode b64 capped window", "paged", 64, 32, 8, 16, 8192, softcap=50.0,
                 window=1024),
         # requests in contiguous rows, scores biased by distance, 8 query heads per KV head
-        _decode("decode b32 slopes, contig", "contig", 32, 32, 4, 100, 4095, slopes=True),
+        _decode("decode b32 slopes contig", "contig", 32, 32, 4, 100, 4095, slopes=True),
         # packed documents of a large batch at full contexts, 7 query heads per KV head: bandwidth
-        _decode("decode b128 documents, capped", "paged", 128, 56, 8, 8000, 8192, block=32,
+        _decode("decode b128 documents capped", "paged", 128, 56, 8, 8000, 8192, block=32,
                 softcap=30.0, documents=6000),
 
         # a few short chunks among running sequences: latency
@@ -72,7 +72,7 @@ def listed():
         # long prompts of a layer that sees a window
         _prefill("prefill 2 x 8192 window", "contig", 2, 32, 8, 8100, 8192, 0, 0, window=1024),
         # chunks after cached positions, distance bias, packed documents, bidirectional prefixes
-        _prefill("prefill chunks, all masks", "paged", 6, 56, 8, 100, 1500, 0, 3000, block=32,
+        _prefill("prefill chunks all masks", "paged", 6, 56, 8, 100, 1500, 0, 3000, block=32,
                  slopes=True, documents=1024, prefix=True),
     ]
 

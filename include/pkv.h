@@ -101,6 +101,78 @@ PKV_API pkv_status pkv_kv_append(const int64_t *slot_mapping, int64_t num_tokens
                          pkv_heads heads, void *stream);
 
 /*
+ * Rotary positions ("rotary position embedding"): each pair of elements of a
+ * query or key head is turned by an angle proportional to the token's
+ * position.  The pages have no counterpart: it is the step between a layer's
+ * Q/K/V projection and the cache.
+ *
+ * pkv_rope is a plan, a plain host struct the caller keeps next to its model
+ * and passes by pointer; fill it with one of the two calls below (they touch
+ * no device) and treat its fields as read-only.  rotary_dim (even, 2..128)
+ * elements at the front of each head are turned, the rest passes unchanged.
+ * interleaved 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1).
+ */
+typedef struct pkv_rope {
+    uint64_t turn[64];    /* pair i: turns per position, in units of 2^-64 turn */
+    float gain;           /* factor on every cosine and sine                    */
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t reserved;
+} pkv_rope;
+
+enum {
+    PKV_ROPE_LINEAR = 1,  /* every frequency divided by factor                            */
+    PKV_ROPE_BASE = 2,    /* theta multiplied by factor^(rotary_dim / (rotary_dim - 2))   */
+    PKV_ROPE_PARTS = 3,   /* divided by factor where a pair makes at most turns_low turns
+                             over original_len positions, kept where it makes at least
+                             turns_high, a linear ramp over the pair index between (its
+                             ends rounded outwards to whole pairs); gain 0.1 ln factor + 1 */
+    PKV_ROPE_SMOOTH = 4   /* the same two ends, a linear ramp over the number of turns    */
+};
+
+typedef struct pkv_rope_scaling {
+    int32_t kind;         /* PKV_ROPE_*                                         */
+    double factor;        /* >= 1                                               */
+    double original_len;  /* PARTS, SMOOTH: positions the model was trained on  */
+    double turns_low;     /* PARTS, SMOOTH                                      */
+    double turns_high;    /* PARTS, SMOOTH: > turns_low                         */
+    double gain;          /* 0: the kind's own (1, PARTS: 0.1 ln factor + 1)    */
+} pkv_rope_scaling;
+
+/* Pair i turns theta^(-2i / rotary_dim) radians per position, scaled as
+ * `scaling` says (NULL: not at all).  theta >= 1. */
+PKV_API pkv_status pkv_rope_init(pkv_rope *rope, int32_t rotary_dim, int32_t interleaved,
+                                 double theta, const pkv_rope_scaling *scaling);
+/* Pair i turns radians[i] (host array of rotary_dim / 2) per position. */
+PKV_API pkv_status pkv_rope_init_frequencies(pkv_rope *rope, int32_t rotary_dim,
+                                             int32_t interleaved, const double *radians,
+                                             double gain);
+
+/*
+ * Rotary positions and append in one pass: for each token t < num_tokens at
+ * position positions[t] (device int32, any value), every query head of q is
+ * turned into q_out, every key head of k is turned into
+ *   k_cache[slot / block_size][h][slot % block_size][:], slot = slot_mapping[t],
+ * and v is copied to the same place of v_cache.  Slots as for pkv_kv_append
+ * (negative: the token's k and v go nowhere; its q is still turned;
+ * contiguous layout: block_size = S).  The angle is exact for every int32
+ * position; the turned values are computed in fp32 and rounded once, to bf16.
+ *
+ * q, k and v are read at a stride of q_stride, k_stride and v_stride elements
+ * per token (multiples of 8, >= 0; a token's heads are adjacent), so views of
+ * one [num_tokens][(Hq + 2 Hkv) * 128] projection output need no copy.
+ * q_out is [num_tokens][Hq][128]; it may be q itself when q_stride is Hq *
+ * 128, else it must not overlap q (PKV_ERR_INVALID_ARG), and it must not
+ * overlap k, v or the caches.  Tokens of one call need distinct slots.
+ */
+PKV_API pkv_status pkv_rope_append(const int32_t *positions, const int64_t *slot_mapping,
+                                   int64_t num_tokens, const void *q, int64_t q_stride,
+                                   const void *k, int64_t k_stride, const void *v,
+                                   int64_t v_stride, void *q_out, void *k_cache, void *v_cache,
+                                   int64_t num_slots, int64_t block_size, pkv_heads heads,
+                                   const pkv_rope *rope, void *stream);
+
+/*
  * Number of context splits the decode calls use, and the fp32 workspace they
  * need, for num_seqs sequences of at most max_context positions on the
  * current device.  The split count depends only on these arguments, the

@@ -34,6 +34,7 @@ EXPORTED = ("pkv_kv_append", "pkv_decode_num_splits", "pkv_decode_uses_tensor_co
             "pkv_shared_decode_workspace_size", "pkv_shared_decode_launches",
             "pkv_paged_prefill_attention",
             "pkv_contig_prefill_attention", "pkv_block_swap",
+            "pkv_rope_init", "pkv_rope_init_frequencies", "pkv_rope_append",
             "pkv_get_device_error", "pkv_status_string", "pkv_last_error")
 
 
@@ -46,6 +47,18 @@ class PkvError(RuntimeError):
 class Heads(ctypes.Structure):
     _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("turn", ctypes.c_uint64 * 64), ("gain", ctypes.c_float),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("turns_low", ctypes.c_double),
+                ("turns_high", ctypes.c_double), ("gain", ctypes.c_double)]
 
 
 _lib = None
@@ -91,6 +104,11 @@ def lib():
                                                     vp, vp, sz, vp]
     L.pkv_debug_gather_paged.argtypes = [vp, vp, i32, i32, vp, i32, i32, i32, i32, vp, vp]
     L.pkv_debug_gather_contig.argtypes = [vp, vp, i32, vp, i32, i32, i64, i32, vp, vp]
+    f64 = ctypes.c_double
+    L.pkv_rope_init.argtypes = [ctypes.POINTER(Rope), i32, i32, f64, ctypes.POINTER(RopeScaling)]
+    L.pkv_rope_init_frequencies.argtypes = [ctypes.POINTER(Rope), i32, i32, vp, f64]
+    L.pkv_rope_append.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, i64,
+                                  Heads, ctypes.POINTER(Rope), vp]
     L.pkv_set_checked.argtypes = [ctypes.c_int]
     L.pkv_set_checked.restype = None
     L.pkv_get_checked.restype = ctypes.c_int
@@ -159,6 +177,125 @@ def kv_append(slot_mapping, k, v, k_cache, v_cache):
     _check(lib().pkv_kv_append(_ptr(slot_mapping), k.shape[0], _ptr(k), _ptr(v),
                                _ptr(k_cache), _ptr(v_cache), nb * bs, bs,
                                heads(hkv, hkv, d), _stream(k_cache)))
+
+
+_ROPE_KINDS = {"linear": 1, "base": 2, "parts": 3, "smooth": 4}
+
+
+class RopePlan:
+    """Rotary positions of one model (pkv_rope of include/pkv.h).
+
+    rotary_dim: elements at the front of each head that are turned;
+    interleaved: pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2).
+    Frequencies are theta ** (-2 i / rotary_dim) radians per position, changed
+    by `scaling`, a dict: {"kind": "linear", "factor"}, {"kind": "base",
+    "factor"}, {"kind": "parts", "factor", "original", "beta_fast" (32),
+    "beta_slow" (1)} or {"kind": "smooth", "factor", "original", "low" (1),
+    "high" (4)}, each with an optional "gain" on cosines and sines.  Or give
+    all rotary_dim / 2 of them as inv_freq (with gain)."""
+
+    def __init__(self, rotary_dim=128, theta=10000.0, interleaved=False, scaling=None,
+                 inv_freq=None, gain=None):
+        self.c = Rope()
+        rotary_dim, inter = int(rotary_dim), 1 if interleaved else 0
+        if inv_freq is not None:
+            if scaling is not None:
+                raise ValueError("inv_freq and scaling exclude one another")
+            w = [float(x) for x in inv_freq]
+            if len(w) != rotary_dim // 2:
+                raise ValueError("inv_freq must have rotary_dim / 2 entries")
+            _check(lib().pkv_rope_init_frequencies(
+                ctypes.byref(self.c), rotary_dim, inter, (ctypes.c_double * max(len(w), 1))(*w),
+                1.0 if gain is None else float(gain)))
+            return
+        if gain is not None:
+            raise ValueError("gain goes with inv_freq; a scaling has its own \"gain\"")
+        c_scaling = None
+        if scaling is not None:
+            s = dict(scaling)
+            kind = s.pop("kind", None)
+            if kind not in _ROPE_KINDS:
+                raise ValueError("scaling kind must be one of %s" % ", ".join(_ROPE_KINDS))
+            c = RopeScaling(_ROPE_KINDS[kind], float(s.pop("factor")), 0.0, 0.0, 0.0,
+                            float(s.pop("gain", 0.0)))
+            if kind in ("parts", "smooth"):
+                c.original_len = float(s.pop("original"))
+                low, high = (("beta_slow", 1.0), ("beta_fast", 32.0)) if kind == "parts" else (
+                    ("low", 1.0), ("high", 4.0))
+                c.turns_low = float(s.pop(*low))
+                c.turns_high = float(s.pop(*high))
+            if s:
+                raise ValueError("unknown scaling entries: %s" % ", ".join(sorted(s)))
+            c_scaling = ctypes.byref(c)
+        _check(lib().pkv_rope_init(ctypes.byref(self.c), rotary_dim, inter, float(theta),
+                                   c_scaling))
+
+
+def _same_device(dev, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError("%s is on %s, not on %s" % (n, t.device, dev))
+
+
+def _on_device(dev, call, *args):
+    """Run a library call with `dev` current (the library launches there) on
+    its current stream."""
+    if dev.index == torch.cuda.current_device():
+        _check(call(*args, torch.cuda.current_stream().cuda_stream))
+        return
+    with torch.cuda.device(dev):
+        _check(call(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _token_rows(t, name):
+    """Token stride (elements) of new rows [T, H, D] whose heads are adjacent;
+    tokens may be further apart (a view of a wider projection output)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.dim() != 3:
+        raise ValueError("%s must have 3 dims" % name)
+    T, H, d = t.shape
+    st, sh, sd = t.stride()
+    if T and ((d > 1 and sd != 1) or (H > 1 and sh != d)):
+        raise ValueError("%s: the heads of a token must be adjacent rows" % name)
+    return st if T > 1 else H * d
+
+
+def rope_append(positions, slot_mapping, q, k, v, k_cache, v_cache, rope, out=None):
+    """Turn q [T, Hq, D] and k [T, Hkv, D] by their positions [T] (int32),
+    write the turned k and v into the caches at slot_mapping [T] (int64, as
+    for kv_append) and return the turned q.  q, k and v may be views of one
+    projection output (any token stride that is a multiple of 8).  out: the
+    result [T, Hq, D] (q itself, if contiguous, for in place)."""
+    _need(positions, torch.int32, "positions", 1)
+    _need(slot_mapping, torch.int64, "slot_mapping", 1)
+    sq, sk, sv = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, torch.bfloat16, n, 4)
+    if not isinstance(rope, RopePlan):
+        raise TypeError("rope must be a RopePlan")
+    nb, hkv, bs, d = k_cache.shape
+    T, hq, d2 = q.shape
+    if v_cache.shape != k_cache.shape or k.shape != v.shape:
+        raise ValueError("k/v and cache shapes must match")
+    if tuple(k.shape) != (T, hkv, d) or d2 != d:
+        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D] matching the cache")
+    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("positions / slot_mapping must have one entry per token")
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, "out", 3)
+    if out.shape != q.shape:
+        raise ValueError("out must be [T, Hq, D]")
+    dev = q.device
+    _same_device(dev, positions=positions, slot_mapping=slot_mapping, k=k, v=v, k_cache=k_cache,
+                 v_cache=v_cache, out=out)
+    _on_device(dev, lib().pkv_rope_append, positions.data_ptr(), slot_mapping.data_ptr(), T,
+               q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(),
+               k_cache.data_ptr(), v_cache.data_ptr(), nb * bs, bs, Heads(hq, hkv, d), rope.c)
+    return out
 
 
 def decode_num_splits(num_seqs, num_q_heads, num_kv_heads, max_context, head_dim=128):

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -18,6 +19,7 @@
 #include "prefix.cuh"
 #include "decode_tc_launch.h"
 #include "kv_ops.cuh"
+#include "rope.cuh"
 
 namespace {
 
@@ -995,9 +997,171 @@ void* device_view(void* p, int dev) {
   }
 }
 
+// A radians-per-position frequency as a 64-bit fraction of a turn.  The
+// division by 2 pi is the only rounding (the scaling by 2^64 is exact).
+uint64_t turn_fraction(double radians) {
+  double x = radians * 0.15915494309189535;  // 1 / (2 pi)
+  x -= std::floor(x);
+  if (!(x < 1.0)) x = 0.0;  // a tiny negative frequency rounds up to a whole turn
+  return static_cast<uint64_t>(std::ldexp(x, 64));
+}
+
+pkv_status check_rope_shape(const pkv_rope* rope, int32_t rotary_dim, int32_t interleaved) {
+  if (!rope) return fail(PKV_ERR_INVALID_ARG, "rope is null");
+  if (rotary_dim < 2 || rotary_dim > pkv::kHeadDim || rotary_dim % 2 != 0)
+    return fail(PKV_ERR_INVALID_ARG, "rotary_dim %d must be even and in 2..%d", rotary_dim,
+                pkv::kHeadDim);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(PKV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  return PKV_OK;
+}
+
+// Whether the n1 bytes at a and the n2 bytes at b share any byte.
+bool overlap(const void* a, int64_t n1, const void* b, int64_t n2) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(n2) && y < x + static_cast<uintptr_t>(n1);
+}
+
 }  // namespace
 
 extern "C" {
+
+pkv_status pkv_rope_init_frequencies(pkv_rope* rope, int32_t rotary_dim, int32_t interleaved,
+                                     const double* radians, double gain) {
+  const pkv_status st = check_rope_shape(rope, rotary_dim, interleaved);
+  if (st != PKV_OK) return st;
+  if (!radians) return fail(PKV_ERR_INVALID_ARG, "radians is null");
+  if (!std::isfinite(gain) || std::fabs(gain) > FLT_MAX)
+    return fail(PKV_ERR_INVALID_ARG, "gain is not a finite fp32");
+  for (int32_t i = 0; i < rotary_dim / 2; ++i)
+    if (!std::isfinite(radians[i]) || std::fabs(radians[i]) > 1e6)
+      return fail(PKV_ERR_INVALID_ARG, "radians[%d] is not finite or above 1e6", i);
+  std::memset(rope, 0, sizeof *rope);
+  for (int32_t i = 0; i < rotary_dim / 2; ++i) rope->turn[i] = turn_fraction(radians[i]);
+  rope->gain = static_cast<float>(gain);
+  rope->rotary_dim = rotary_dim;
+  rope->interleaved = interleaved;
+  return PKV_OK;
+}
+
+pkv_status pkv_rope_init(pkv_rope* rope, int32_t rotary_dim, int32_t interleaved, double theta,
+                         const pkv_rope_scaling* s) {
+  const pkv_status st = check_rope_shape(rope, rotary_dim, interleaved);
+  if (st != PKV_OK) return st;
+  if (!std::isfinite(theta) || theta < 1.0)
+    return fail(PKV_ERR_INVALID_ARG, "theta must be finite and >= 1");
+  double gain = 1.0, w[pkv::kHeadDim / 2];
+  const int32_t half = rotary_dim / 2;
+  if (s != nullptr) {
+    if (s->kind < PKV_ROPE_LINEAR || s->kind > PKV_ROPE_SMOOTH)
+      return fail(PKV_ERR_INVALID_ARG, "unknown scaling kind %d", s->kind);
+    if (!std::isfinite(s->factor) || s->factor < 1.0)
+      return fail(PKV_ERR_INVALID_ARG, "scaling factor must be finite and >= 1");
+    if (!std::isfinite(s->gain) || s->gain < 0.0)
+      return fail(PKV_ERR_INVALID_ARG, "scaling gain must be finite and >= 0");
+    if (s->kind == PKV_ROPE_BASE) {
+      if (rotary_dim < 4) return fail(PKV_ERR_INVALID_ARG, "base scaling needs rotary_dim >= 4");
+      theta *= std::pow(s->factor, static_cast<double>(rotary_dim) / (rotary_dim - 2));
+    }
+    if (s->kind >= PKV_ROPE_PARTS) {
+      if (!std::isfinite(s->original_len) || s->original_len < 1.0)
+        return fail(PKV_ERR_INVALID_ARG, "scaling original_len must be finite and >= 1");
+      if (!std::isfinite(s->turns_low) || !std::isfinite(s->turns_high) || s->turns_low <= 0.0 ||
+          s->turns_high <= s->turns_low)
+        return fail(PKV_ERR_INVALID_ARG, "scaling needs 0 < turns_low < turns_high");
+      if (s->kind == PKV_ROPE_PARTS && theta <= 1.0)
+        return fail(PKV_ERR_INVALID_ARG, "scaling by parts needs theta > 1");
+      if (s->kind == PKV_ROPE_PARTS) gain = 0.1 * std::log(s->factor) + 1.0;
+    }
+    if (s->gain > 0.0) gain = s->gain;
+  }
+  const double two_pi = 6.283185307179586;
+  // the (fractional) pair that makes so many turns over the original length
+  auto pair_of = [&](double turns) {
+    return rotary_dim * std::log(s->original_len / (turns * two_pi)) / (2.0 * std::log(theta));
+  };
+  double ramp0 = 0.0, ramp1 = 0.0;
+  if (s != nullptr && s->kind == PKV_ROPE_PARTS) {
+    ramp0 = std::max(0.0, std::floor(pair_of(s->turns_high)));
+    ramp1 = std::min(rotary_dim - 1.0, std::ceil(pair_of(s->turns_low)));
+  }
+  for (int32_t i = 0; i < half; ++i) {
+    w[i] = std::pow(theta, -2.0 * i / rotary_dim);
+    if (s == nullptr) continue;
+    double keep = 1.0;  // share of the unscaled frequency
+    if (s->kind == PKV_ROPE_LINEAR) keep = 0.0;
+    if (s->kind == PKV_ROPE_PARTS)
+      keep = 1.0 - std::min(1.0, std::max(0.0, (i - ramp0) / std::max(ramp1 - ramp0, 0.001)));
+    if (s->kind == PKV_ROPE_SMOOTH)
+      keep = std::min(1.0, std::max(0.0, (s->original_len * w[i] / two_pi - s->turns_low) /
+                                             (s->turns_high - s->turns_low)));
+    w[i] = (1.0 - keep) * (w[i] / s->factor) + keep * w[i];
+  }
+  return pkv_rope_init_frequencies(rope, rotary_dim, interleaved, w, gain);
+}
+
+pkv_status pkv_rope_append(const int32_t* positions, const int64_t* slot_mapping,
+                           int64_t num_tokens, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                           void* k_cache, void* v_cache, int64_t num_slots, int64_t block_size,
+                           pkv_heads heads, const pkv_rope* rope, void* stream) {
+  pkv_status st = check_heads(heads);
+  if (st != PKV_OK) return st;
+  if (!rope) return fail(PKV_ERR_INVALID_ARG, "rope is null");
+  st = check_rope_shape(rope, rope->rotary_dim, rope->interleaved);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || num_slots < 0) return fail(PKV_ERR_INVALID_ARG, "negative size");
+  if (num_tokens == 0) return PKV_OK;
+  if (num_tokens > 0x7fffffffLL) return fail(PKV_ERR_UNSUPPORTED, "too many tokens");
+  if (block_size <= 0) return fail(PKV_ERR_INVALID_ARG, "block_size must be >= 1");
+  if (!positions || !slot_mapping || !q || !k || !v || !q_out || !k_cache || !v_cache)
+    return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(positions, 4) || !aligned(slot_mapping, 8))
+    return fail(PKV_ERR_INVALID_ARG, "positions or slot_mapping misaligned");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return fail(PKV_ERR_INVALID_ARG, "bf16 tensors must be 16-byte aligned");
+  const int64_t strides[3] = {q_stride, k_stride, v_stride};
+  for (int64_t x : strides)
+    if (x < 0 || x % 8 != 0 || x > (int64_t{1} << 31))
+      return fail(PKV_ERR_INVALID_ARG, "token strides must be multiples of 8 in 0..2^31");
+  const int64_t q_row = static_cast<int64_t>(heads.num_q_heads) * pkv::kRowBytes;
+  const int64_t kv_row = static_cast<int64_t>(heads.num_kv_heads) * pkv::kRowBytes;
+  const int64_t n = num_tokens;
+  const bool in_place = q_out == q && (n == 1 || 2 * q_stride == q_row);
+  if (!in_place && overlap(q_out, n * q_row, q, (n - 1) * 2 * q_stride + q_row))
+    return fail(PKV_ERR_INVALID_ARG, "q_out overlaps q (and is not q itself with stride Hq * 128)");
+  if (overlap(q_out, n * q_row, k, (n - 1) * 2 * k_stride + kv_row) ||
+      overlap(q_out, n * q_row, v, (n - 1) * 2 * v_stride + kv_row))
+    return fail(PKV_ERR_INVALID_ARG, "q_out overlaps k or v");
+  int* err = nullptr;
+  st = device_info(nullptr, &err, nullptr);
+  if (st != PKV_OK) return st;
+  pkv::RopeParams p;
+  std::memset(&p, 0, sizeof p);
+  p.positions = positions;
+  p.slot_mapping = slot_mapping;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_cache = static_cast<uint16_t*>(k_cache);
+  p.v_cache = static_cast<uint16_t*>(v_cache);
+  p.num_tokens = num_tokens;
+  p.num_slots = num_slots;
+  p.bs = block_size;
+  p.Hq = heads.num_q_heads;
+  p.Hkv = heads.num_kv_heads;
+  p.rope = *rope;
+  p.checked = g_checked.load();
+  p.err = err;
+  const cudaError_t e = pkv::launch_rope_append(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope_append launch");
+  return PKV_OK;
+}
 
 pkv_status pkv_block_copy(const int64_t* src_dst_pairs, int64_t n, void* const* k_caches,
                           void* const* v_caches, int32_t num_layers, int64_t num_blocks,

@@ -1,0 +1,191 @@
+// rope.cu -- rotary positions on new queries and keys, and the append of the
+// turned keys and of the values to the cache, in one pass over the rows.
+//
+// Pair i of a row at position p is turned by the angle p w_i:
+//   (x, y) -> gain (x cos a - y sin a, y cos a + x sin a),  a = p w_i.
+// The angle is taken in turns: the plan holds f_i = w_i / 2 pi as a 64-bit
+// fraction F_i / 2^64, and p F_i mod 2^64 is the fraction of a turn, exactly,
+// for every int32 p -- the integer product wraps as the angle does, so no
+// range reduction is needed and far positions lose nothing (the error is
+// that of F_i times p: under 2^-34 turns at a million positions).
+//
+// What bounds it: memory.  Every row is read once and written once (256 bytes
+// each way); the 64 sines and cosines of a token are computed once and serve
+// all its heads from shared memory.  A row takes 8 lanes of two 16-byte
+// chunks; in the half layout a lane's two chunks are partners (chunk c and
+// c + rotary_dim / 16), so that no lane needs another's elements.
+#include "rope.cuh"
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRowsPerPass = kRopeThreads / 8;
+
+// The turned pair (x, y) as bf16: the only rounding on the way.
+__device__ __forceinline__ float2 turned(float x, float y, float2 cs) {
+  return make_float2(x * cs.x - y * cs.y, y * cs.x + x * cs.y);
+}
+
+// Plain (coherent) load: the output may be the query tensor itself.
+__device__ __forceinline__ uint4 ld_row16(const uint16_t* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+
+// kKind 0: interleaved pairs (2i, 2i + 1); 1: half layout, rotary_dim a
+// multiple of 16 (whole chunks are partners); 2: half layout, any even
+// rotary_dim (partners read one by one).
+template <int kKind, int kTokens>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
+  __shared__ float2 cs[kTokens][64];   // (cos, sin) times gain of the rotated pairs
+  __shared__ int64_t row0[kTokens];    // cache row of KV head 0, or -1: k and v go nowhere
+  grid_dependency_trigger();
+  grid_dependency_wait();
+  const int tid = threadIdx.x;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
+  const int ntok = static_cast<int>(min(static_cast<int64_t>(kTokens), p.num_tokens - t0));
+  const int rd = p.rope.rotary_dim;
+  const int half = rd >> 1;
+
+  for (int e = tid; e < kTokens * 64; e += kRopeThreads) {
+    const int tok = e >> 6, i = e & 63;
+    float2 c = make_float2(1.f, 0.f);
+    if (tok < ntok && i < half) {
+      const int64_t pos = p.positions[t0 + tok];
+      const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * p.rope.turn[i]);
+      // a signed fraction of a turn in units of 2^-64 is 2^-63 half turns
+      sincospif(static_cast<float>(turn) * 1.0842021724855044e-19f, &c.y, &c.x);
+      c.x *= p.rope.gain;
+      c.y *= p.rope.gain;
+    }
+    cs[tok][i] = c;
+  }
+  if (tid < ntok) {
+    const int64_t slot = p.slot_mapping[t0 + tid];
+    int64_t r = -1;
+    if (slot >= 0) {
+      if (p.checked && slot >= p.num_slots) {
+        if (blockIdx.y == 0) record_error(p.err, kErrSlot);
+      } else {
+        r = cache_row(slot / p.bs, 0, p.Hkv, p.bs, slot % p.bs);
+      }
+    }
+    row0[tid] = r;
+  }
+  __syncthreads();
+
+  const int l = tid & 7;
+  const int R = p.Hq + 2 * p.Hkv;
+  const int nrows = ntok * R;
+  // the two chunks of this lane: rotated rows, and copied ones (v)
+  int ca = 2 * l, cb = 2 * l + 1;
+  if (kKind == 1) {
+    const int parts = rd >> 4;  // partner pairs of chunks
+    ca = l < parts ? l : 2 * l;  // past the rotated part: chunks 2 parts + 2 (l - parts), + 1
+    cb = l < parts ? l + parts : 2 * l + 1;
+  }
+  for (int base = blockIdx.y * kRowsPerPass; base < nrows; base += gridDim.y * kRowsPerPass) {
+    const int r = base + (tid >> 3);
+    const bool live = r < nrows;
+    const int tok = live ? r / R : 0;
+    const int h = live ? r - tok * R : 0;
+    const int64_t t = t0 + tok;
+    const int64_t kv_row = row0[tok];
+    const uint16_t* src;
+    uint16_t* dst;
+    bool move = live;
+    if (h < p.Hq) {
+      src = p.q + t * p.q_stride + h * kHeadDim;
+      dst = p.q_out + (t * p.Hq + h) * kHeadDim;
+    } else {
+      const bool is_v = h >= p.Hq + p.Hkv;
+      const int hk = h - p.Hq - (is_v ? p.Hkv : 0);
+      src = is_v ? p.v + t * p.v_stride + hk * kHeadDim : p.k + t * p.k_stride + hk * kHeadDim;
+      dst = (is_v ? p.v_cache : p.k_cache) + (kv_row + hk * p.bs) * kHeadDim;
+      move = live && kv_row >= 0;
+    }
+    const bool turn = h < p.Hq + p.Hkv;
+    uint4 oa = make_uint4(0u, 0u, 0u, 0u), ob = oa;
+    if (move) {
+      oa = ld_row16(src + ca * 8);
+      ob = ld_row16(src + cb * 8);
+      if (turn) {
+        uint32_t wa[4] = {oa.x, oa.y, oa.z, oa.w}, wb[4] = {ob.x, ob.y, ob.z, ob.w};
+        if (kKind == 0) {  // a 32-bit word is a pair
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t& w = i < 4 ? wa[i] : wb[i - 4];
+            const int pair = (i < 4 ? ca : cb) * 4 + (i & 3);
+            if (pair < half) {
+              const float2 r = turned(bf16_lo(w), bf16_hi(w), cs[tok][pair]);
+              w = pack_bf16x2(r.x, r.y);
+            }
+          }
+        } else if (kKind == 1) {
+          if (l < (rd >> 4)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 r0 = turned(bf16_lo(wa[i]), bf16_lo(wb[i]), cs[tok][l * 8 + 2 * i]);
+              const float2 r1 = turned(bf16_hi(wa[i]), bf16_hi(wb[i]), cs[tok][l * 8 + 2 * i + 1]);
+              wa[i] = pack_bf16x2(r0.x, r1.x);
+              wb[i] = pack_bf16x2(r0.y, r1.y);
+            }
+          }
+        } else {  // rotary_dim is even: a word is turned whole or not at all
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t& w = i < 4 ? wa[i] : wb[i - 4];
+            const int at = (i < 4 ? ca : cb) * 8 + 2 * (i & 3);
+            if (at >= rd) continue;
+            float r[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float x = b == 0 ? bf16_lo(w) : bf16_hi(w);
+              const bool lower = at + b < half;
+              const int other = lower ? at + b + half : at + b - half;
+              const float y = bf16_lo(src[other]);
+              const float2 f = cs[tok][lower ? at + b : other];
+              r[b] = lower ? turned(x, y, f).x : turned(y, x, f).y;
+            }
+            w = pack_bf16x2(r[0], r[1]);
+          }
+        }
+        oa = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+        ob = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+      }
+    }
+    // in place (q_out == q) a row's partners are read before any lane writes it
+    if (kKind == 2) __syncwarp();
+    if (move) {
+      *reinterpret_cast<uint4*>(dst + ca * 8) = oa;
+      *reinterpret_cast<uint4*>(dst + cb * 8) = ob;
+    }
+  }
+}
+
+template <int kKind>
+cudaError_t launch_kind(const RopeParams& p, cudaStream_t stream) {
+  const int R = p.Hq + 2 * p.Hkv;
+  if (p.num_tokens <= 512) {
+    // few tokens: one a CTA, its rows over grid y, so that every row of the
+    // call is in flight at once
+    const dim3 grid(static_cast<unsigned>(p.num_tokens), (R + kRowsPerPass - 1) / kRowsPerPass);
+    return launch_pdl(rope_append_kernel<kKind, 1>, grid, dim3(kRopeThreads), 0, stream, p);
+  }
+  constexpr int kTokens = 4;
+  const dim3 grid(static_cast<unsigned>((p.num_tokens + kTokens - 1) / kTokens), 1);
+  return launch_pdl(rope_append_kernel<kKind, kTokens>, grid, dim3(kRopeThreads), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream) {
+  if (p.num_tokens <= 0) return cudaSuccess;
+  if (p.rope.interleaved) return launch_kind<0>(p, stream);
+  return p.rope.rotary_dim % 16 == 0 ? launch_kind<1>(p, stream) : launch_kind<2>(p, stream);
+}
+
+}  // namespace pkv

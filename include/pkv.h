@@ -377,6 +377,77 @@ PKV_API pkv_status pkv_contig_prefill_attention(
     float scale, pkv_heads heads, void *out, void *stream);
 
 /*
+ * Scores beyond scale * q . k, for the four calls below.  The pages have no
+ * counterpart: these are the scores that models other than the plain one
+ * attend with.  For a token at position p, query head h and the key at
+ * position j of a sequence of ctx positions:
+ *   s = scale * q . k_j
+ *   s = softcap * tanh(s / softcap)             softcap > 0
+ *   s = s - alibi_slopes[h] * |p - j|           alibi_slopes given
+ * and the token sees j when all of these hold:
+ *   j <= p, or j < prefix_lens[i]               (bidirectional prefix)
+ *   j > p - window                              window > 0
+ *   j >= first_key[row]                         first_key given (documents)
+ *   j < ctx
+ * out = sum_j softmax_j(s) v_j over the keys it sees, zeros if it sees none.
+ * NULL in place of the struct, or a zeroed struct, is the plain causal score.
+ */
+typedef struct pkv_score {
+    float softcap;               /* 0: none; else in 2^-20 .. 2^20                       */
+    int32_t window;              /* 0: none; else the number of last positions seen,
+                                    the token's own included                             */
+    const float *alibi_slopes;   /* device fp32 [num_q_heads], finite; NULL: none        */
+    const int32_t *first_key;    /* device int32, one per row of q (decode [num_seqs],
+                                    prefill [num_tokens]); NULL: 0.  Negative: 0         */
+    const int32_t *prefix_lens;  /* device int32 [num_seqs]; NULL: none.  The decode
+                                    calls ignore it: a newest token sees every earlier
+                                    position anyway                                      */
+} pkv_score;
+
+/*
+ * Decode attention with such scores: arguments, layouts, errors and checked
+ * mode as for pkv_paged_decode_attention / pkv_contig_decode_attention, and
+ * `score`.  Blocks that hold no visible position are never read and their
+ * table entries are not either: with a window, a sequence's older blocks may
+ * have been freed.  Nothing that stands in masked positions (NaN, infinities)
+ * reaches the output.  workspace must hold
+ * pkv_scored_decode_workspace_size(num_seqs, heads, max_context, window)
+ * bytes (16-byte aligned); its contents need no initialisation.
+ */
+PKV_API size_t pkv_scored_decode_workspace_size(int32_t num_seqs, pkv_heads heads,
+                                                int32_t max_context, int32_t window);
+PKV_API pkv_status pkv_paged_decode_attention_scored(
+    const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *context_lens,
+    int32_t num_seqs, int32_t max_context, int32_t block_size, float scale,
+    const pkv_score *score, pkv_heads heads, void *out, void *workspace, size_t workspace_bytes,
+    void *stream);
+PKV_API pkv_status pkv_contig_decode_attention_scored(
+    const void *q, const void *k_buf, const void *v_buf, const int32_t *req_ids,
+    int32_t max_reqs, const int32_t *context_lens, int32_t num_seqs, int32_t max_context,
+    int64_t S, float scale, const pkv_score *score, pkv_heads heads, void *out, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/*
+ * Prefill attention with such scores: arguments, layouts, errors and checked
+ * mode as for pkv_paged_prefill_attention / pkv_contig_prefill_attention, and
+ * `score`.  What the decode calls say of unread blocks (here: those that no
+ * token of the chunk sees) and of masked positions holds too.  Rows of q and
+ * out behind the last chunk are left alone.
+ */
+PKV_API pkv_status pkv_paged_prefill_attention_scored(
+    const void *q, const int32_t *cu_seqlens_q, int32_t num_tokens, const void *k_cache,
+    const void *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+    int32_t num_blocks, const int32_t *context_lens, int32_t num_seqs, int32_t max_q_tokens,
+    int32_t block_size, float scale, const pkv_score *score, pkv_heads heads, void *out,
+    void *stream);
+PKV_API pkv_status pkv_contig_prefill_attention_scored(
+    const void *q, const int32_t *cu_seqlens_q, int32_t num_tokens, const void *k_buf,
+    const void *v_buf, const int32_t *req_ids, int32_t max_reqs, const int32_t *context_lens,
+    int32_t num_seqs, int32_t max_q_tokens, int64_t S, float scale, const pkv_score *score,
+    pkv_heads heads, void *out, void *stream);
+
+/*
  * Copy-on-write block copy.  "Running Out of Cache" (section "Fragmentation
  * is lost users") and the PagedAttention summary: sequences share physical
  * blocks and copy a block only when one of them writes into it.

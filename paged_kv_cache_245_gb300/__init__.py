@@ -13,7 +13,9 @@ from .binding import (BlockManager, PkvError, VmmBuffer, block_copy, block_swap,
                       decode_workspace_size, get_checked, get_device_error, kv_append, lib,
                       paged_decode_attention, set_checked, set_decode_variant, get_decode_variant,
                       set_split_tiles, VARIANT_AUTO, VARIANT_SPLIT, VARIANT_TC_8X3,
-                      VARIANT_TC_12X2, RopePlan, rope_append)
+                      VARIANT_TC_12X2, RopePlan, rope_append, scored_decode_workspace_size,
+                      paged_decode_attention_scored, contig_decode_attention_scored,
+                      paged_prefill_attention_scored, contig_prefill_attention_scored)
 
 __all__ = ["BlockManager", "PkvError", "VmmBuffer", "block_copy", "block_swap", "BM_RETIRED",
            "BM_RUNNING", "BM_SWAPPED", "BM_RECOMPUTE", "PREEMPT_RECOMPUTE", "PREEMPT_SWAP",
@@ -24,4 +26,6 @@ __all__ = ["BlockManager", "PkvError", "VmmBuffer", "block_copy", "block_swap", 
            "decode_workspace_size", "get_checked", "get_device_error", "kv_append", "lib",
            "paged_decode_attention", "set_checked", "set_split_tiles", "set_decode_variant",
            "get_decode_variant", "VARIANT_AUTO", "VARIANT_SPLIT", "VARIANT_TC_8X3",
-           "VARIANT_TC_12X2", "RopePlan", "rope_append"]
+           "VARIANT_TC_12X2", "RopePlan", "rope_append", "scored_decode_workspace_size",
+           "paged_decode_attention_scored", "contig_decode_attention_scored",
+           "paged_prefill_attention_scored", "contig_prefill_attention_scored"]

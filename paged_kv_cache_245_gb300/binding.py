@@ -35,6 +35,9 @@ EXPORTED = ("pkv_kv_append", "pkv_decode_num_splits", "pkv_decode_uses_tensor_co
             "pkv_paged_prefill_attention",
             "pkv_contig_prefill_attention", "pkv_block_swap",
             "pkv_rope_init", "pkv_rope_init_frequencies", "pkv_rope_append",
+            "pkv_scored_decode_workspace_size", "pkv_paged_decode_attention_scored",
+            "pkv_contig_decode_attention_scored", "pkv_paged_prefill_attention_scored",
+            "pkv_contig_prefill_attention_scored",
             "pkv_get_device_error", "pkv_status_string", "pkv_last_error")
 
 
@@ -59,6 +62,12 @@ class RopeScaling(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
                 ("original_len", ctypes.c_double), ("turns_low", ctypes.c_double),
                 ("turns_high", ctypes.c_double), ("gain", ctypes.c_double)]
+
+
+class Score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
 
 
 _lib = None
@@ -109,6 +118,17 @@ def lib():
     L.pkv_rope_init_frequencies.argtypes = [ctypes.POINTER(Rope), i32, i32, vp, f64]
     L.pkv_rope_append.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, i64,
                                   Heads, ctypes.POINTER(Rope), vp]
+    sp = ctypes.POINTER(Score)
+    L.pkv_scored_decode_workspace_size.argtypes = [i32, Heads, i32, i32]
+    L.pkv_scored_decode_workspace_size.restype = sz
+    L.pkv_paged_decode_attention_scored.argtypes = [vp, vp, vp, vp, i32, i32, vp, i32, i32, i32,
+                                                    ctypes.c_float, sp, Heads, vp, vp, sz, vp]
+    L.pkv_contig_decode_attention_scored.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, i64,
+                                                     ctypes.c_float, sp, Heads, vp, vp, sz, vp]
+    L.pkv_paged_prefill_attention_scored.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, vp, i32,
+                                                     i32, i32, ctypes.c_float, sp, Heads, vp, vp]
+    L.pkv_contig_prefill_attention_scored.argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, i32, i32,
+                                                      i64, ctypes.c_float, sp, Heads, vp, vp]
     L.pkv_set_checked.argtypes = [ctypes.c_int]
     L.pkv_set_checked.restype = None
     L.pkv_get_checked.restype = ctypes.c_int
@@ -555,6 +575,158 @@ def contig_prefill_attention(q, cu_seqlens_q, k_buf, v_buf, req_ids, context_len
         _ptr(context_lens), B, int(max_q_tokens), S, float(scale), heads(hq, hkv, d), _ptr(out),
         _stream(q)))
     return out
+
+
+def scored_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_context, window=0,
+                                 head_dim=128):
+    """Workspace bytes of the *_decode_attention_scored calls."""
+    return int(lib().pkv_scored_decode_workspace_size(
+        num_seqs, heads(num_q_heads, num_kv_heads, head_dim), int(max_context), int(window)))
+
+
+def _score(dev, hq, rows, num_seqs, softcap, window, alibi_slopes, first_key, prefix_lens):
+    """The pkv_score struct; its arrays checked (rows: of q, for first_key)."""
+    s = Score(softcap, window)
+    for t, dtype, n, name in ((alibi_slopes, torch.float32, hq, "alibi_slopes"),
+                              (first_key, torch.int32, rows, "first_key"),
+                              (prefix_lens, torch.int32, num_seqs, "prefix_lens")):
+        if t is None:
+            continue
+        _need(t, dtype, name, 1)
+        if t.shape[0] != n:
+            raise ValueError("%s must have %d entries" % (name, n))
+        if t.device != dev:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+        setattr(s, name, t.data_ptr())
+    return s
+
+
+def _decode_scored(contig, q, k, v, where, context_lens, max_context, scale, softcap, window,
+                   alibi_slopes, first_key, out, workspace):
+    _need(q, torch.bfloat16, "q", 3)
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, torch.bfloat16, n, 4)
+    if contig:
+        _need(where, torch.int32, "req_ids", 1)
+    else:
+        _need(where, torch.int32, "block_tables", 2)
+    _need(context_lens, torch.int32, "context_lens", 1)
+    B, hq, d = q.shape
+    n, hkv, bs, d2 = k.shape
+    if d != d2 or v.shape != k.shape:
+        raise ValueError("q / cache shapes disagree")
+    if where.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("block_tables / req_ids / context_lens must have num_seqs rows")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, torch.bfloat16, "out", 3)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    dev, max_context = q.device, int(max_context)
+    _same_device(dev, k=k, v=v, tables=where, context_lens=context_lens, out=out,
+                 workspace=workspace)
+    score = _score(dev, hq, B, B, softcap, window, alibi_slopes, first_key, None)
+    h = Heads(hq, hkv, d)
+    L = lib()
+    if workspace is None and B > 0:
+        # convenience for callers without their own buffer; the C ABI itself never allocates
+        with torch.cuda.device(dev):
+            size = L.pkv_scored_decode_workspace_size(B, h, max_context, score.window)
+        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+    ws = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                              workspace.numel() * workspace.element_size())
+    if contig:
+        _on_device(dev, L.pkv_contig_decode_attention_scored, q.data_ptr(), k.data_ptr(),
+                   v.data_ptr(), where.data_ptr(), n, context_lens.data_ptr(), B, max_context, bs,
+                   scale, score, h, out.data_ptr(), *ws)
+    else:
+        _on_device(dev, L.pkv_paged_decode_attention_scored, q.data_ptr(), k.data_ptr(),
+                   v.data_ptr(), where.data_ptr(), where.shape[1], n, context_lens.data_ptr(), B,
+                   max_context, bs, scale, score, h, out.data_ptr(), *ws)
+    return out
+
+
+def paged_decode_attention_scored(q, k_cache, v_cache, block_tables, context_lens, max_context,
+                                  scale, softcap=0.0, window=0, alibi_slopes=None,
+                                  first_key=None, out=None, workspace=None):
+    """paged_decode_attention whose scores are capped (softcap * tanh(s /
+    softcap)), biased by distance (alibi_slopes fp32 [Hq]: -slope * |p - j|)
+    and masked: the last `window` positions only, and positions from
+    first_key[i] (int32 [B], the start of the newest token's document)."""
+    return _decode_scored(False, q, k_cache, v_cache, block_tables, context_lens, max_context,
+                          scale, softcap, window, alibi_slopes, first_key, out, workspace)
+
+
+def contig_decode_attention_scored(q, k_buf, v_buf, req_ids, context_lens, max_context, scale,
+                                   softcap=0.0, window=0, alibi_slopes=None, first_key=None,
+                                   out=None, workspace=None):
+    """paged_decode_attention_scored over per-request sub-tensors (offset
+    reqId x S)."""
+    return _decode_scored(True, q, k_buf, v_buf, req_ids, context_lens, max_context, scale,
+                          softcap, window, alibi_slopes, first_key, out, workspace)
+
+
+def _prefill_scored(contig, q, cu_seqlens_q, k, v, where, context_lens, max_q_tokens, scale,
+                    softcap, window, alibi_slopes, first_key, prefix_lens, out):
+    _need(q, torch.bfloat16, "q", 3)
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, torch.bfloat16, n, 4)
+    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
+    if contig:
+        _need(where, torch.int32, "req_ids", 1)
+    else:
+        _need(where, torch.int32, "block_tables", 2)
+    _need(context_lens, torch.int32, "context_lens", 1)
+    T, hq, d = q.shape
+    n, hkv, bs, d2 = k.shape
+    B = context_lens.shape[0]
+    if d != d2 or v.shape != k.shape:
+        raise ValueError("q / cache shapes disagree")
+    if cu_seqlens_q.shape[0] != B + 1 or where.shape[0] != B:
+        raise ValueError("cu_seqlens_q must have num_seqs + 1 entries, block_tables / req_ids "
+                         "num_seqs rows")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, torch.bfloat16, "out", 3)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    dev = q.device
+    _same_device(dev, k=k, v=v, cu_seqlens_q=cu_seqlens_q, tables=where,
+                 context_lens=context_lens, out=out)
+    score = _score(dev, hq, T, B, softcap, window, alibi_slopes, first_key, prefix_lens)
+    h = Heads(hq, hkv, d)
+    if contig:
+        _on_device(dev, lib().pkv_contig_prefill_attention_scored, q.data_ptr(),
+                   cu_seqlens_q.data_ptr(), T, k.data_ptr(), v.data_ptr(), where.data_ptr(), n,
+                   context_lens.data_ptr(), B, int(max_q_tokens), bs, scale, score, h,
+                   out.data_ptr())
+    else:
+        _on_device(dev, lib().pkv_paged_prefill_attention_scored, q.data_ptr(),
+                   cu_seqlens_q.data_ptr(), T, k.data_ptr(), v.data_ptr(), where.data_ptr(),
+                   where.shape[1], n, context_lens.data_ptr(), B, int(max_q_tokens), bs, scale,
+                   score, h, out.data_ptr())
+    return out
+
+
+def paged_prefill_attention_scored(q, cu_seqlens_q, k_cache, v_cache, block_tables, context_lens,
+                                   max_q_tokens, scale, softcap=0.0, window=0, alibi_slopes=None,
+                                   first_key=None, prefix_lens=None, out=None):
+    """paged_prefill_attention with the scores of paged_decode_attention_scored;
+    first_key int32 [T] is per new token (packed documents), prefix_lens int32
+    [B] lets every token of sequence i see the positions below prefix_lens[i]."""
+    return _prefill_scored(False, q, cu_seqlens_q, k_cache, v_cache, block_tables, context_lens,
+                           max_q_tokens, scale, softcap, window, alibi_slopes, first_key,
+                           prefix_lens, out)
+
+
+def contig_prefill_attention_scored(q, cu_seqlens_q, k_buf, v_buf, req_ids, context_lens,
+                                    max_q_tokens, scale, softcap=0.0, window=0,
+                                    alibi_slopes=None, first_key=None, prefix_lens=None,
+                                    out=None):
+    """paged_prefill_attention_scored over per-request sub-tensors."""
+    return _prefill_scored(True, q, cu_seqlens_q, k_buf, v_buf, req_ids, context_lens,
+                           max_q_tokens, scale, softcap, window, alibi_slopes, first_key,
+                           prefix_lens, out)
 
 
 def debug_gather_paged(cache, block_tables, context_lens, max_context):

@@ -20,6 +20,8 @@
 #include "decode_tc_launch.h"
 #include "kv_ops.cuh"
 #include "rope.cuh"
+#include "score.cuh"
+#include "scored_rows.cuh"
 
 namespace {
 
@@ -174,13 +176,38 @@ bool tc_enough_tiles(int32_t num_seqs, const pkv_heads& h, int32_t max_context, 
   return tile_bound >= 8LL * tc_ctas(sms);
 }
 
+// A pkv_score checked and in the kernels' units.
+pkv_status check_score(const pkv_score* score, pkv::ScoreParams* out) {
+  std::memset(out, 0, sizeof *out);
+  if (score == nullptr) return PKV_OK;
+  const float c = score->softcap;
+  if (!std::isfinite(c) || c < 0.f) return fail(PKV_ERR_INVALID_ARG, "softcap is negative or not finite");
+  if (c > 0.f && (c < 9.5367431640625e-07f || c > 1048576.f))
+    return fail(PKV_ERR_UNSUPPORTED, "softcap outside 2^-20 .. 2^20");
+  if (score->window < 0) return fail(PKV_ERR_INVALID_ARG, "negative window");
+  if (!aligned(score->alibi_slopes, 4) || !aligned(score->first_key, 4) ||
+      !aligned(score->prefix_lens, 4))
+    return fail(PKV_ERR_INVALID_ARG, "score arrays misaligned");
+  if (c > 0.f) {
+    out->cap2 = c * pkv::kLog2e;
+    out->inv_cap2 = 1.f / out->cap2;
+    out->cap_k = 2.f / c;
+  }
+  out->window = score->window;
+  out->slopes = score->alibi_slopes;
+  out->first_key = score->first_key;
+  out->prefix = score->prefix_lens;
+  return PKV_OK;
+}
+
 pkv_status decode_common(bool contig, const void* q, const void* k, const void* v,
                          const int32_t* block_tables, int32_t max_blocks, int64_t num_blocks,
                          const int32_t* req_ids, int32_t max_reqs, const int32_t* context_lens,
                          int32_t num_seqs, int32_t max_context, int64_t bs_or_S, float scale,
                          pkv_heads h, void* out, void* workspace, size_t workspace_bytes,
                          void* stream, bool dry_run = false, bool* tc_out = nullptr,
-                         const FusedAppend* fused = nullptr) {
+                         const FusedAppend* fused = nullptr,
+                         const pkv::ScoreParams* score = nullptr) {
   if (tc_out) *tc_out = false;
   pkv_status st = check_heads(h);
   if (st != PKV_OK) return st;
@@ -212,6 +239,35 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
   int* err = nullptr;
   st = device_info(&dev, &err, &sms);
   if (st != PKV_OK) return st;
+  if (score != nullptr) {
+    const size_t need = decode_workspace_need(num_seqs, h, max_context, sms);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+      return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
+                  workspace ? workspace_bytes : size_t{0});
+    pkv::ScoredRowsParams r;
+    std::memset(&r, 0, sizeof r);
+    r.q = static_cast<const uint16_t*>(q);
+    r.out = static_cast<uint16_t*>(out);
+    r.k = static_cast<const uint16_t*>(k);
+    r.v = static_cast<const uint16_t*>(v);
+    r.tables = contig ? req_ids : block_tables;
+    r.ctx_lens = context_lens;
+    r.bs = bs_or_S;
+    r.num_blocks = contig ? max_reqs : num_blocks;
+    r.num_rows = num_seqs;
+    r.max_blocks = contig ? 1 : max_blocks;
+    r.num_seqs = num_seqs;
+    r.Hq = h.num_q_heads;
+    r.Hkv = h.num_kv_heads;
+    r.max_context = max_context;
+    r.qscale = scale * pkv::kLog2e;
+    r.sp = *score;
+    r.checked = g_checked.load();
+    r.err = err;
+    r.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
+    const cudaError_t e = pkv::launch_scored_rows(r, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "scored decode launch");
+  }
   const int group = h.num_q_heads / h.num_kv_heads;
   const int64_t rows_total = contig ? static_cast<int64_t>(max_reqs) * h.num_kv_heads * bs_or_S
                                     : static_cast<int64_t>(num_blocks) * h.num_kv_heads * bs_or_S;
@@ -625,6 +681,38 @@ pkv_status pkv_contig_decode_attention(const void* q, const void* k_buf, const v
                        stream);
 }
 
+size_t pkv_scored_decode_workspace_size(int32_t num_seqs, pkv_heads heads, int32_t max_context,
+                                        int32_t window) {
+  if (window < 0) return 0;
+  return pkv_decode_workspace_size(num_seqs, heads, max_context);
+}
+
+pkv_status pkv_paged_decode_attention_scored(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t* context_lens, int32_t num_seqs,
+    int32_t max_context, int32_t block_size, float scale, const pkv_score* score, pkv_heads heads,
+    void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  pkv::ScoreParams sp;
+  const pkv_status st = check_score(score, &sp);
+  if (st != PKV_OK) return st;
+  return decode_common(false, q, k_cache, v_cache, block_tables, max_blocks_per_seq, num_blocks,
+                       nullptr, 0, context_lens, num_seqs, max_context, block_size, scale, heads,
+                       out, workspace, workspace_bytes, stream, false, nullptr, nullptr, &sp);
+}
+
+pkv_status pkv_contig_decode_attention_scored(
+    const void* q, const void* k_buf, const void* v_buf, const int32_t* req_ids, int32_t max_reqs,
+    const int32_t* context_lens, int32_t num_seqs, int32_t max_context, int64_t S, float scale,
+    const pkv_score* score, pkv_heads heads, void* out, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  pkv::ScoreParams sp;
+  const pkv_status st = check_score(score, &sp);
+  if (st != PKV_OK) return st;
+  return decode_common(true, q, k_buf, v_buf, nullptr, 0, 0, req_ids, max_reqs, context_lens,
+                       num_seqs, max_context, S, scale, heads, out, workspace, workspace_bytes,
+                       stream, false, nullptr, nullptr, &sp);
+}
+
 int32_t pkv_shared_decode_launches(int32_t num_seqs, int32_t num_groups, int32_t max_group_size,
                                    int32_t max_blocks_per_seq, int32_t max_context,
                                    int32_t block_size, int32_t max_own_tokens, pkv_heads heads) {
@@ -811,6 +899,13 @@ pkv_status pkv_paged_decode_attention_shared(
 
 namespace {
 
+// gcd(block_size, 128): a run of rows inside one block
+int block_run_rows(int32_t block_size) {
+  int run_rows = 128;
+  while (block_size > 0 && block_size % run_rows != 0) run_rows >>= 1;
+  return run_rows;
+}
+
 // Causal prefill over rows addressed as block (or request) x block_size; a
 // TMA box covers run_rows rows of one block.
 pkv_status prefill_common(const void* q, const int32_t* cu_seqlens_q, int32_t num_tokens,
@@ -818,7 +913,8 @@ pkv_status prefill_common(const void* q, const int32_t* cu_seqlens_q, int32_t nu
                           int32_t max_blocks_per_seq, int32_t num_blocks,
                           const int32_t* context_lens, int32_t num_seqs, int32_t max_q_tokens,
                           int32_t block_size, int run_rows, float scale, pkv_heads heads,
-                          void* out, void* stream) {
+                          void* out, void* stream, const pkv::ScoreParams* score = nullptr,
+                          bool contig = false) {
   pkv_status st = check_heads(heads);
   if (st != PKV_OK) return st;
   if (num_seqs < 0 || num_tokens < 0 || max_q_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "negative size");
@@ -846,6 +942,32 @@ pkv_status prefill_common(const void* q, const int32_t* cu_seqlens_q, int32_t nu
   int* err = nullptr;
   st = device_info(&dev, &err, nullptr);
   if (st != PKV_OK) return st;
+  if (score != nullptr) {
+    pkv::ScoredRowsParams r;
+    std::memset(&r, 0, sizeof r);
+    r.q = static_cast<const uint16_t*>(q);
+    r.out = static_cast<uint16_t*>(out);
+    r.k = static_cast<const uint16_t*>(k_cache);
+    r.v = static_cast<const uint16_t*>(v_cache);
+    r.tables = block_tables;
+    r.cu_q = cu_seqlens_q;
+    r.ctx_lens = context_lens;
+    r.bs = block_size;
+    r.num_blocks = num_blocks;
+    r.num_rows = num_tokens;
+    r.max_blocks = max_blocks_per_seq;
+    r.num_seqs = num_seqs;
+    r.Hq = heads.num_q_heads;
+    r.Hkv = heads.num_kv_heads;
+    r.max_q = max_q_tokens;
+    r.qscale = scale * pkv::kLog2e;
+    r.sp = *score;
+    r.checked = g_checked.load();
+    r.err = err;
+    r.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
+    const cudaError_t e = pkv::launch_scored_rows(r, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "scored prefill launch");
+  }
   alignas(64) CUtensorMap tk;
   alignas(64) CUtensorMap tv;
   if (!pkv::encode_prefill_runs(&tk, k_cache, rows_total, run_rows) ||
@@ -898,11 +1020,9 @@ pkv_status pkv_paged_prefill_attention(const void* q, const int32_t* cu_seqlens_
                                        const int32_t* context_lens, int32_t num_seqs,
                                        int32_t max_q_tokens, int32_t block_size, float scale,
                                        pkv_heads heads, void* out, void* stream) {
-  int run_rows = 128;  // gcd(block_size, 128): a run of rows inside one block
-  while (block_size > 0 && block_size % run_rows != 0) run_rows >>= 1;
   return prefill_common(q, cu_seqlens_q, num_tokens, k_cache, v_cache, block_tables,
                         max_blocks_per_seq, num_blocks, context_lens, num_seqs, max_q_tokens,
-                        block_size, run_rows, scale, heads, out, stream);
+                        block_size, block_run_rows(block_size), scale, heads, out, stream);
 }
 
 pkv_status pkv_contig_prefill_attention(const void* q, const int32_t* cu_seqlens_q,
@@ -918,6 +1038,34 @@ pkv_status pkv_contig_prefill_attention(const void* q, const int32_t* cu_seqlens
   return prefill_common(q, cu_seqlens_q, num_tokens, k_buf, v_buf, req_ids, 1, max_reqs,
                         context_lens, num_seqs, max_q_tokens, static_cast<int32_t>(S), 16, scale,
                         heads, out, stream);
+}
+
+pkv_status pkv_paged_prefill_attention_scored(
+    const void* q, const int32_t* cu_seqlens_q, int32_t num_tokens, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    int32_t num_blocks, const int32_t* context_lens, int32_t num_seqs, int32_t max_q_tokens,
+    int32_t block_size, float scale, const pkv_score* score, pkv_heads heads, void* out,
+    void* stream) {
+  pkv::ScoreParams sp;
+  const pkv_status st = check_score(score, &sp);
+  if (st != PKV_OK) return st;
+  return prefill_common(q, cu_seqlens_q, num_tokens, k_cache, v_cache, block_tables,
+                        max_blocks_per_seq, num_blocks, context_lens, num_seqs, max_q_tokens,
+                        block_size, block_run_rows(block_size), scale, heads, out, stream, &sp);
+}
+
+pkv_status pkv_contig_prefill_attention_scored(
+    const void* q, const int32_t* cu_seqlens_q, int32_t num_tokens, const void* k_buf,
+    const void* v_buf, const int32_t* req_ids, int32_t max_reqs, const int32_t* context_lens,
+    int32_t num_seqs, int32_t max_q_tokens, int64_t S, float scale, const pkv_score* score,
+    pkv_heads heads, void* out, void* stream) {
+  if (S <= 0 || S > 0x7fffffffLL) return fail(PKV_ERR_UNSUPPORTED, "S out of range");
+  pkv::ScoreParams sp;
+  const pkv_status st = check_score(score, &sp);
+  if (st != PKV_OK) return st;
+  return prefill_common(q, cu_seqlens_q, num_tokens, k_buf, v_buf, req_ids, 1, max_reqs,
+                        context_lens, num_seqs, max_q_tokens, static_cast<int32_t>(S), 16, scale,
+                        heads, out, stream, &sp, true);
 }
 
 pkv_status pkv_debug_gather_paged(const void* cache, const int32_t* block_tables,

@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include "pkv_device.cuh"
+#include "score.cuh"
 
 namespace pkv {
 
@@ -55,6 +56,7 @@ struct DecodeParams {
   float qscale;                  // scale * log2(e): scores in base-2 units
   int32_t checked;
   int* err;
+  ScoreParams sp;                // scored kernels only
 };
 
 constexpr int kDecodeWarps = 4;
@@ -102,7 +104,20 @@ __device__ __forceinline__ int effective_context(const DecodeParams& p, int seq,
   return ctx;
 }
 
-template <int G, bool kContig, int kStages>
+// First position that sequence `seq`, whose newest token is at ctx - 1, sees;
+// ctx becomes 0 when it sees none.
+__device__ __forceinline__ int first_visible(const ScoreParams& sp, int seq, int& ctx) {
+  int lo, hi;
+  visible_keys(sp, ctx - 1, sp.first_key != nullptr ? sp.first_key[seq] : 0, 0, ctx, lo, hi);
+  if (lo <= hi) return lo;
+  ctx = 0;
+  return 0;
+}
+
+// kScored: scores are capped, biased and masked (score.cuh).  The visible
+// positions are lo .. ctx - 1; tiles start at lo / 16, rows before lo are
+// neither copied nor used.
+template <int G, bool kContig, int kStages, bool kScored = false>
 __global__ void __launch_bounds__(kDecodeThreads)
     decode_attention_kernel(const DecodeParams p) {
   using L = DecodeSmemLayout<G, kStages>;
@@ -121,9 +136,11 @@ __global__ void __launch_bounds__(kDecodeThreads)
 
   grid_dependency_trigger();
   grid_dependency_wait();
-  const int ctx = effective_context(p, seq, kContig, threadIdx.x == 0 && split == 0);
+  int ctx = effective_context(p, seq, kContig, threadIdx.x == 0 && split == 0);
+  const int lo = kScored ? first_visible(p.sp, seq, ctx) : 0;
+  const int tile0 = lo / kTileTokens;  // tiles before it hold nothing visible
   const int ntiles = ctx > 0 ? (ctx + kTileTokens - 1) / kTileTokens : 0;
-  const int t_begin = split * p.chunk_tiles;
+  const int t_begin = tile0 + split * p.chunk_tiles;
   const int t_end = min(t_begin + p.chunk_tiles, ntiles);
   if (p.nsplit > 1 && t_begin >= t_end) return;  // empty split: the combine skips it
 
@@ -166,6 +183,13 @@ __global__ void __launch_bounds__(kDecodeThreads)
     }
   }
 
+  float slope2[G];
+  if (kScored) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      slope2[g] = p.sp.slopes != nullptr ? __ldg(p.sp.slopes + kvh * G + g) * kLog2e : 0.f;
+  }
+
   // This warp's tiles: t_begin + warp + k * kDecodeWarps.
   const int first = t_begin + warp;
   const int n_my = (t_end > first) ? (t_end - first + kDecodeWarps - 1) / kDecodeWarps : 0;
@@ -176,7 +200,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
     if (kContig) return 0;
     const int pos = (first + k * kDecodeWarps) * kTileTokens + lane;
     // positions are below 2^31: divide in 32 bits
-    return (lane < kTileTokens && pos < ctx)
+    return (lane < kTileTokens && pos < ctx && pos >= lo)
                ? __ldg(bt_row + static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.bs))
                : 0;
   };
@@ -187,21 +211,23 @@ __global__ void __launch_bounds__(kDecodeThreads)
     const int s = k % kStages;
     const int row0 = tile * kTileTokens;
     const int nvalid = min(kTileTokens, ctx - row0);
+    const int nlow = kScored ? max(0, lo - row0) : 0;  // rows before the first visible
     unsigned char* kdst = stage_base + s * L::kStageBytes;
     unsigned char* vdst = kdst + kTileBytes;
     if (kContig) {
       if (lane == 0) {
-        const uint32_t bytes = static_cast<uint32_t>(nvalid) * kRowBytes;
+        const uint32_t bytes = static_cast<uint32_t>(nvalid - nlow) * kRowBytes;
+        const int64_t at = static_cast<int64_t>(row0 + nlow) * kHeadDim;
         mbar_arrive_expect_tx(&bars[s], 2 * bytes);
-        bulk_copy_g2s(kdst, kbase + static_cast<int64_t>(row0) * kHeadDim, bytes, &bars[s], policy);
-        bulk_copy_g2s(vdst, vbase + static_cast<int64_t>(row0) * kHeadDim, bytes, &bars[s], policy);
+        bulk_copy_g2s(kdst + nlow * kRowBytes, kbase + at, bytes, &bars[s], policy);
+        bulk_copy_g2s(vdst + nlow * kRowBytes, vbase + at, bytes, &bars[s], policy);
       }
     } else {
       // Lane r < nvalid holds position row0 + r; a run of rows that share a
-      // physical block starts where the in-block offset is 0 (or at r = 0).
+      // physical block starts where the in-block offset is 0 (or at the first row).
       const int64_t pos = row0 + lane;
       const int64_t off = static_cast<uint32_t>(pos) % static_cast<uint32_t>(p.bs);
-      const bool start = lane < nvalid && (lane == 0 || off == 0);
+      const bool start = lane < nvalid && (lane == nlow || (lane > nlow && off == 0));
       int len = 0;
       if (start) {
         const int64_t rest = p.bs - off;
@@ -249,7 +275,9 @@ __global__ void __launch_bounds__(kDecodeThreads)
     }
     const unsigned char* ks = stage_base + s * L::kStageBytes;
     const unsigned char* vs = ks + kTileBytes;
-    const int nvalid = min(kTileTokens, ctx - (first + k * kDecodeWarps) * kTileTokens);
+    const int row0 = (first + k * kDecodeWarps) * kTileTokens;
+    const int nvalid = min(kTileTokens, ctx - row0);
+    const int nlow = kScored ? max(0, lo - row0) : 0;
 
     // ---- scores: 8 rounds of partial dot products, then transpose-reduce
     float sc[G];
@@ -285,7 +313,15 @@ __global__ void __launch_bounds__(kDecodeThreads)
 
     // ---- online softmax update (m, l warp-uniform; p to shared memory)
     const int my_t = 2 * c + half;
-    const bool valid = my_t < nvalid;
+    const bool valid = my_t < nvalid && my_t >= nlow;
+    if (kScored) {
+      const float dist = static_cast<float>(ctx - 1 - (row0 + my_t));
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (p.sp.cap2 > 0.f) sc[g] = capped_score(p.sp, sc[g]);
+        if (p.sp.slopes != nullptr) sc[g] += fmaxf(-slope2[g] * dist, kLowBias);
+      }
+    }
     float pr[GP];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -320,7 +356,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int t = 2 * u + half;
-      if (nvalid == kTileTokens || t < nvalid) {
+      if ((nvalid == kTileTokens || t < nvalid) && t >= nlow) {
         const uint4 w = *reinterpret_cast<const uint4*>(vs + t * kRowBytes + j * 16);
         const float vf[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
                              bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
@@ -429,7 +465,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
 
 // Merge the splits of one (sequence, query head) per warp:
 //   M = max_s m_s,  w_s = l_s 2^(m_s - M),  out = sum_s w_s o_s / sum_s w_s.
-template <bool kContig>
+template <bool kContig, bool kScored = false>
 __global__ void __launch_bounds__(128) decode_combine_kernel(const DecodeParams p) {
   grid_dependency_trigger();
   grid_dependency_wait();
@@ -438,8 +474,9 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const DecodeParams 
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * 4 + warp;
   if (idx >= static_cast<int64_t>(p.num_seqs) * p.Hq) return;
   const int seq = static_cast<int>(idx / p.Hq);
-  const int ctx = effective_context(p, seq, kContig, false);
-  const int ntiles = ctx > 0 ? (ctx + kTileTokens - 1) / kTileTokens : 0;
+  int ctx = effective_context(p, seq, kContig, false);
+  const int tile0 = (kScored ? first_visible(p.sp, seq, ctx) : 0) / kTileTokens;
+  const int ntiles = (ctx > 0 ? (ctx + kTileTokens - 1) / kTileTokens : 0) - tile0;
   const int n = min(p.nsplit, (ntiles + p.chunk_tiles - 1) / p.chunk_tiles);
   const float* ml = p.part_ml + idx * p.nsplit * 2;
   const float* po = p.part_o + idx * p.nsplit * kHeadDim;

@@ -8,8 +8,7 @@
 #include <mutex>
 #include <random>
 
-#include "decode_tc.cuh"
-#include "decode_tc_launch.h"
+#include "decode_tc_host.cuh"
 
 namespace pkv {
 
@@ -47,8 +46,6 @@ bool encode_rows(CUtensorMap* map, const void* base, int64_t rows) {
   return r == CUDA_SUCCESS;
 }
 
-namespace {
-
 // Record tags of the launches: a counter from a per-process random start, so
 // that consecutive launches differ and words left in reused memory (by
 // another process or any other data) rarely carry a launch's tag.  Never 0
@@ -66,8 +63,6 @@ uint32_t next_launch_tag() {
   return t;
 }
 
-}  // namespace
-
 // Batches above kTcMaxSeqs run as consecutive chunks reusing the workspace;
 // a chunk's tile prefix (int32) must hold chunk * ceil(max_context / 16).
 int tc_chunk_seqs(int max_context) {
@@ -77,48 +72,6 @@ int tc_chunk_seqs(int max_context) {
     chunk = static_cast<int>(0x7fffffffLL / max_tiles);
   return chunk < 1 ? 1 : chunk;
 }
-
-namespace {
-
-template <bool kContig, int W, int S, bool kFuse, int MH = kTcMergeHeads, int NT = 1>
-cudaError_t launch_cfg(const CUtensorMap& tk, const CUtensorMap& tv, const TcParams& p0,
-                       int num_ctas, cudaStream_t stream) {
-  using L = TcSmem<W, S, NT, MH>;
-  static unsigned long long done_mask = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  auto kernel = decode_tc_kernel<kContig, W, S, NT, kFuse, MH>;
-  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
-    if (e != cudaSuccess) return e;
-    __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
-  }
-  const int chunk = tc_chunk_seqs(p0.max_context);
-  for (int s0 = 0; s0 < p0.num_seqs; s0 += chunk) {
-    TcParams p = p0;
-    p.num_seqs = (p0.num_seqs - s0) < chunk ? (p0.num_seqs - s0) : chunk;
-    p.q += static_cast<int64_t>(s0) * p.Hq * kHeadDim;
-    p.out += static_cast<int64_t>(s0) * p.Hq * kHeadDim;
-    if (p.rec_out != nullptr) p.rec_out += static_cast<int64_t>(s0) * p.Hq * kRecStride;
-    p.ctx_lens += s0;
-    if (p.slot_mapping != nullptr) {
-      p.slot_mapping += s0;
-      p.k_new += static_cast<int64_t>(s0) * p.Hkv * kHeadDim;
-      p.v_new += static_cast<int64_t>(s0) * p.Hkv * kHeadDim;
-    }
-    if (kContig) p.req_ids += s0;
-    else p.block_tables += static_cast<int64_t>(s0) * p.max_blocks;
-    p.tag = next_launch_tag();  // every launch writes its piece records under a fresh tag
-    e = launch_pdl_if(pdl_decode_enabled(), kernel, dim3(num_ctas), dim3(W * 32),
-                      L::kTotal, stream, tk, tv, p);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
-}
-
-}  // namespace
 
 // Per CTA: one piece record (its first segment, when that is part of a pair
 // that an earlier CTA's range began) of kTcRecHeads heads, kRecStride tagged
@@ -159,7 +112,9 @@ TcStatus launch_decode_tc(const TcParams& p_in, bool contig, const void* k, cons
 #define PKV_TC_PICK(C, F)                                                             \
   (mh == 8 ? PKV_TC_LAUNCH(C, 10, 2, F, 8)                                            \
            : (cfg == 0 ? PKV_TC_LAUNCH(C, 8, 3, F, 4) : PKV_TC_LAUNCH(C, 12, 2, F, 4)))
-  if (p.G > kTcHeads) {  // one n-tile of 8 query heads per KV head (the API allows G <= 8)
+  if (p.scored) {
+    e = launch_decode_tc_scored(tk, tv, p, contig, mh == 8, num_ctas, stream);
+  } else if (p.G > kTcHeads) {  // one n-tile of 8 query heads per KV head (the API allows G <= 8)
     e = cudaErrorInvalidValue;
   } else if (fuse) {
     e = contig ? PKV_TC_PICK(true, true) : PKV_TC_PICK(false, true);

@@ -50,7 +50,7 @@ constexpr int kTcStageBytes = 8192;   // K tile 4 KiB, V tile 4 KiB
 constexpr int kBoxBytes = 2048;       // 16 rows x 128 B: half a head_dim row
 
 
-template <int W, int S, int NT = 1, int MH = kTcMergeHeads>
+template <int W, int S, int NT = 1, int MH = kTcMergeHeads, bool kScored = false>
 struct TcSmem {
   static constexpr int kStagesOff = 0;
   static constexpr int kBarsOff = W * S * kTcStageBytes;
@@ -58,7 +58,8 @@ struct TcSmem {
   static constexpr int kMLOff = kMergeOff + W * MH * kRecStride * 4;
   static constexpr int kCtxOff = kMLOff + W * kTcHeads * NT * 2 * 4;
   static constexpr int kReqOff = kCtxOff + kTcMaxSeqs * 4;
-  static constexpr int kPrefixOff = kReqOff + kTcMaxSeqs * 4;
+  static constexpr int kLowOff = kReqOff + kTcMaxSeqs * 4;  // scored: first visible positions
+  static constexpr int kPrefixOff = kLowOff + (kScored ? kTcMaxSeqs * 4 : 0);
   static constexpr int kRangeOff = (kPrefixOff + (kTcMaxSeqs + 1) * 4 + 7) / 8 * 8;
   static constexpr int kEnd = kRangeOff + 3 * 8;
   static constexpr int kTotal = kEnd + 1024;  // slack to align the base to 1 KiB
@@ -260,15 +261,28 @@ __device__ __forceinline__ bool tc_merge_pieces(const TcParams& p, int seq, int 
   return ok;
 }
 
+// First position that sequence i, whose newest token is at ctx - 1, sees (ctx
+// becomes 0 when it sees none).
+__device__ __forceinline__ int tc_first_visible(const TcParams& p, int i, int& ctx) {
+  int lo, hi;
+  visible_keys(p.sp, ctx - 1, p.sp.first_key != nullptr ? p.sp.first_key[i] : 0, 0, ctx, lo, hi);
+  if (lo <= hi) return lo;
+  ctx = 0;
+  return 0;
+}
+
 // NT n-tiles of 8 query heads per KV head (instantiated with NT = 1: GQA
-// groups of up to 8 query heads).  kFuse: the decode step's append is done
+// groups of up to 8 query heads).  kScored: scores are capped, biased and
+// masked (score.cuh); a sequence's tiles then start at the one that holds its
+// first visible position, so a window's cost is the window's.  kFuse: the decode step's append is done
 // here too (p.slot_mapping).  MH: query heads merged per pass (4, or 8 when
 // the shared memory holds every warp's 8 partials: one pass at G = 8).
-template <bool kContig, int W, int S, int NT, bool kFuse, int MH>
+template <bool kContig, int W, int S, int NT, bool kFuse, int MH, bool kScored = false>
 __global__ void __launch_bounds__(W * 32, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const TcParams p) {
-  using L = TcSmem<W, S, NT, MH>;
+  static_assert(!(kFuse && kScored), "the fused append is the plain step's");
+  using L = TcSmem<W, S, NT, MH, kScored>;
   constexpr int H = kTcHeads * NT;  // padded query heads per KV head
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ unsigned char smem_raw[];
@@ -288,6 +302,14 @@ __global__ void __launch_bounds__(W * 32, 1)
   int32_t* ctx_s = reinterpret_cast<int32_t*>(smem + L::kCtxOff);
   int32_t* req_s = reinterpret_cast<int32_t*>(smem + L::kReqOff);
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefixOff);
+  int32_t* low_s = reinterpret_cast<int32_t*>(smem + L::kLowOff);  // kScored
+  // tiles of sequence i, and the position of the first row of its tile n
+  auto seq_tiles = [&](int i) -> int {
+    return ((ctx_s[i] + 15) >> 4) - (kScored ? low_s[i] >> 4 : 0);
+  };
+  auto tile_pos = [&](int i, int64_t n) -> int64_t {
+    return (n + (kScored ? low_s[i] >> 4 : 0)) * 16;
+  };
   // this CTA's tiles [range[0], range[1]), and the sequence of its first tile
   int64_t* range = reinterpret_cast<int64_t*>(smem + L::kRangeOff);
 
@@ -305,7 +327,8 @@ __global__ void __launch_bounds__(W * 32, 1)
 
   // ---- tile counts and their prefix over sequences (every CTA, once)
   for (int i = tid; i < B; i += W * 32) {
-    const int ctx = tc_context(p, i, kContig, c == 0);
+    int ctx = tc_context(p, i, kContig, c == 0);
+    if (kScored) low_s[i] = tc_first_visible(p, i, ctx);
     ctx_s[i] = ctx;
     if (kContig) req_s[i] = ctx > 0 ? p.req_ids[i] : 0;
   }
@@ -314,7 +337,7 @@ __global__ void __launch_bounds__(W * 32, 1)
     const int per = (B + 31) / 32;
     const int i0 = lane * per;
     int sum = 0;
-    for (int i = i0; i < i0 + per && i < B; ++i) sum += (ctx_s[i] + 15) >> 4;
+    for (int i = i0; i < i0 + per && i < B; ++i) sum += seq_tiles(i);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -324,7 +347,7 @@ __global__ void __launch_bounds__(W * 32, 1)
     int run = incl - sum;
     for (int i = i0; i < i0 + per && i < B; ++i) {
       prefix[i] = run;
-      run += (ctx_s[i] + 15) >> 4;
+      run += seq_tiles(i);
     }
     if (lane == 31) prefix[B] = incl;
     // This CTA's run of tiles [range[0], range[1]) (tc_unit_to_tile of its
@@ -350,7 +373,7 @@ __global__ void __launch_bounds__(W * 32, 1)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (vi <= u[k]) best[k] = i;
-        run += (ctx_s[i] + 15) >> 4;
+        run += seq_tiles(i);
       }
       int64_t tile[2];
 #pragma unroll
@@ -363,7 +386,7 @@ __global__ void __launch_bounds__(W * 32, 1)
           // it from shared memory (written above by that lane)
           __syncwarp();
           const uint32_t pa = static_cast<uint32_t>(prefix[a]);
-          const uint32_t n = static_cast<uint32_t>((ctx_s[a] + 15) >> 4);
+          const uint32_t n = static_cast<uint32_t>(seq_tiles(a));
           const uint32_t r = u[k] - hkv * (pa + alpha * static_cast<uint32_t>(a));
           const uint32_t h = r / (n + alpha);
           const int32_t o = static_cast<int32_t>(r - h * (n + alpha)) - static_cast<int32_t>(alpha);
@@ -375,7 +398,7 @@ __global__ void __launch_bounds__(W * 32, 1)
       run = incl - sum;
       for (int i = i0; i < i0 + per && i < B; ++i) {
         if (static_cast<int64_t>(hkv) * run <= tile[0]) seq = i;
-        run += (ctx_s[i] + 15) >> 4;
+        run += seq_tiles(i);
       }
       seq = __reduce_max_sync(kFull, seq);
       if (lane == 0) {
@@ -482,7 +505,7 @@ __global__ void __launch_bounds__(W * 32, 1)
   // block-table entry of the tile at the issue cursor (lane 0 only)
   auto load_entry = [&]() -> int32_t {
     if (kContig || lane != 0 || !ivalid) return 0;
-    const int64_t pos = (ix - iseg.pstart) * 16;
+    const int64_t pos = tile_pos(iseg.seq, ix - iseg.pstart);
     return __ldg(p.block_tables + static_cast<int64_t>(iseg.seq) * p.max_blocks + pos / p.bs);
   };
 
@@ -494,7 +517,7 @@ __global__ void __launch_bounds__(W * 32, 1)
     }
     if (lane == 0) {
       unsigned char* st = stage0 + stage * kTcStageBytes;
-      const int64_t pos = (ix - iseg.pstart) * 16;
+      const int64_t pos = tile_pos(iseg.seq, ix - iseg.pstart);
       bool kv_ok = true;
       int64_t row;
       if (kContig) {
@@ -530,7 +553,7 @@ __global__ void __launch_bounds__(W * 32, 1)
     bool cv = ivalid;
     for (int s = 0; s < S && cv; ++s) {
       if (lane == s) {
-        const int64_t pos = (cx - cs.pstart) * 16;
+        const int64_t pos = tile_pos(cs.seq, cx - cs.pstart);
         pre_entry = __ldg(p.block_tables + static_cast<int64_t>(cs.seq) * p.max_blocks + pos / p.bs);
       }
       cx += W;
@@ -580,6 +603,13 @@ __global__ void __launch_bounds__(W * 32, 1)
       for (int i = 0; i < 8; ++i) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
     }
     const int ctx = ctx_s[seg.seq];
+    const int low = kScored ? low_s[seg.seq] : 0;
+    float slope0 = 0.f, slope1 = 0.f;  // of heads 2tq, 2tq + 1
+    if (kScored && p.sp.slopes != nullptr) {
+      const float* sl = p.sp.slopes + seg.kvh * G;
+      slope0 = 2 * tq < G ? __ldg(sl + 2 * tq) * kLog2e : 0.f;
+      slope1 = 2 * tq + 1 < G ? __ldg(sl + 2 * tq + 1) * kLog2e : 0.f;
+    }
     // A segment that is only part of its pair (the CTA ranges cut the pair)
     // is a "piece"; the pair's CTAs are cf .. cl.  The piece of cf (the
     // pair's first tiles, this CTA's last segment) usually finishes last:
@@ -634,7 +664,9 @@ __global__ void __launch_bounds__(W * 32, 1)
       unsigned char* st = stage0 + stage * kTcStageBytes;
       const uint32_t kaddr = smem_addr(st);
       const uint32_t vaddr = kaddr + 2 * kBoxBytes;
-      const int nvalid = min(16, ctx - static_cast<int>((x - seg.pstart) * 16));
+      const int row0 = static_cast<int>(tile_pos(seg.seq, x - seg.pstart));
+      const int nvalid = min(16, ctx - row0);
+      const int nlow = kScored ? max(0, low - row0) : 0;  // rows before the first visible
       if (own_last && x == x_last) {  // the new rows: into the cache and over row nvalid - 1
         cp_async_wait_all();
         __syncwarp();
@@ -675,6 +707,16 @@ __global__ void __launch_bounds__(W * 32, 1)
         __syncwarp();
       }
 
+      if (kScored && nlow > 0) {  // nor rows before the first visible
+        for (int idx = lane; idx < nlow * 16; idx += 32) {
+          const int r = idx >> 4;
+          const int ch = idx & 15;
+          *reinterpret_cast<uint4*>(st + 2 * kBoxBytes + (ch >> 3) * kBoxBytes + r * 128 +
+                                    (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+      }
+
       // ---- S^T = K . Q^T  (two accumulation chains per n-tile)
       float sa[NT][4], sb[NT][4];
 #pragma unroll
@@ -691,14 +733,30 @@ __global__ void __launch_bounds__(W * 32, 1)
           else mma_bf16_16816(sa[t], a, qb[t][ks][0], qb[t][ks][1]);
         }
       }
-      const bool v0 = g < nvalid, v1 = g + 8 < nvalid;
+      const bool v0 = g < nvalid && g >= nlow, v1 = g + 8 < nvalid && g + 8 >= nlow;
       uint32_t b0[NT], b1[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float s0 = v0 ? (sa[t][0] + sb[t][0]) * p.qscale : -INFINITY;  // token g,   head 2tq
-        const float s1 = v0 ? (sa[t][1] + sb[t][1]) * p.qscale : -INFINITY;  // token g,   head 2tq+1
-        const float s2 = v1 ? (sa[t][2] + sb[t][2]) * p.qscale : -INFINITY;  // token g+8, head 2tq
-        const float s3 = v1 ? (sa[t][3] + sb[t][3]) * p.qscale : -INFINITY;  // token g+8, head 2tq+1
+        float x0 = (sa[t][0] + sb[t][0]) * p.qscale, x1 = (sa[t][1] + sb[t][1]) * p.qscale;
+        float x2 = (sa[t][2] + sb[t][2]) * p.qscale, x3 = (sa[t][3] + sb[t][3]) * p.qscale;
+        if (kScored && p.sp.cap2 > 0.f) {
+          x0 = capped_score(p.sp, x0);
+          x1 = capped_score(p.sp, x1);
+          x2 = capped_score(p.sp, x2);
+          x3 = capped_score(p.sp, x3);
+        }
+        if (kScored && p.sp.slopes != nullptr) {
+          const float d0 = static_cast<float>(ctx - 1 - (row0 + g));
+          const float d1 = static_cast<float>(ctx - 1 - (row0 + g + 8));
+          x0 += fmaxf(-slope0 * d0, kLowBias);
+          x1 += fmaxf(-slope1 * d0, kLowBias);
+          x2 += fmaxf(-slope0 * d1, kLowBias);
+          x3 += fmaxf(-slope1 * d1, kLowBias);
+        }
+        const float s0 = v0 ? x0 : -INFINITY;  // token g,   head 2tq
+        const float s1 = v0 ? x1 : -INFINITY;  // token g,   head 2tq+1
+        const float s2 = v1 ? x2 : -INFINITY;  // token g+8, head 2tq
+        const float s3 = v1 ? x3 : -INFINITY;  // token g+8, head 2tq+1
 
         // ---- online softmax, per head column
         float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "score.cuh"
+
 namespace pkv {
 
 constexpr int kTcMaxSeqs = 512;  // sequences per launch (larger batches run in chunks)
@@ -44,6 +46,8 @@ struct TcParams {
   uint16_t* v_cache;
   int64_t num_slots;        // checked mode: slots in [0, num_slots)
   int* err;
+  int32_t scored;           // 1: scores are capped, biased and masked as sp says
+  ScoreParams sp;
 };
 
 
@@ -166,6 +170,15 @@ size_t tc_workspace_bytes(int num_ctas);
 
 // Sequences per launch (a larger batch runs as consecutive launches).
 int tc_chunk_seqs(int max_context);
+
+// A fresh record tag.
+uint32_t next_launch_tag();
+
+// The scored kernels (decode_tc_scored.cu); eight_heads: the 10 x 2 shape with
+// one merge pass for groups of 5..8 query heads, else 12 x 2.
+cudaError_t launch_decode_tc_scored(const CUtensorMap& tk, const CUtensorMap& tv,
+                                    const TcParams& p, bool contig, bool eight_heads,
+                                    int num_ctas, cudaStream_t stream);
 
 // cfg 0: 8 warps x 3 stages per CTA; cfg 1: 12 warps x 2 stages; cfg 2:
 // 10 warps x 2 stages with one merge pass for groups of 5..8 query heads

@@ -176,6 +176,12 @@ bool tc_enough_tiles(int32_t num_seqs, const pkv_heads& h, int32_t max_context, 
   return tile_bound >= 8LL * tc_ctas(sms);
 }
 
+// Positions that a window lets a sequence attend, counted from the start of
+// the 16-token tile that holds the first (a bound on every sequence).
+int32_t visible_span(int32_t max_context, int32_t window) {
+  return window > 0 && window < max_context - 15 ? window + 15 : max_context;
+}
+
 // A pkv_score checked and in the kernels' units.
 pkv_status check_score(const pkv_score* score, pkv::ScoreParams* out) {
   std::memset(out, 0, sizeof *out);
@@ -239,35 +245,8 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
   int* err = nullptr;
   st = device_info(&dev, &err, &sms);
   if (st != PKV_OK) return st;
-  if (score != nullptr) {
-    const size_t need = decode_workspace_need(num_seqs, h, max_context, sms);
-    if (need > 0 && (!workspace || workspace_bytes < need))
-      return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
-                  workspace ? workspace_bytes : size_t{0});
-    pkv::ScoredRowsParams r;
-    std::memset(&r, 0, sizeof r);
-    r.q = static_cast<const uint16_t*>(q);
-    r.out = static_cast<uint16_t*>(out);
-    r.k = static_cast<const uint16_t*>(k);
-    r.v = static_cast<const uint16_t*>(v);
-    r.tables = contig ? req_ids : block_tables;
-    r.ctx_lens = context_lens;
-    r.bs = bs_or_S;
-    r.num_blocks = contig ? max_reqs : num_blocks;
-    r.num_rows = num_seqs;
-    r.max_blocks = contig ? 1 : max_blocks;
-    r.num_seqs = num_seqs;
-    r.Hq = h.num_q_heads;
-    r.Hkv = h.num_kv_heads;
-    r.max_context = max_context;
-    r.qscale = scale * pkv::kLog2e;
-    r.sp = *score;
-    r.checked = g_checked.load();
-    r.err = err;
-    r.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
-    const cudaError_t e = pkv::launch_scored_rows(r, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "scored decode launch");
-  }
+  // With a window every sequence attends at most `span` positions.
+  const int32_t span = score != nullptr ? visible_span(max_context, score->window) : max_context;
   const int group = h.num_q_heads / h.num_kv_heads;
   const int64_t rows_total = contig ? static_cast<int64_t>(max_reqs) * h.num_kv_heads * bs_or_S
                                     : static_cast<int64_t>(num_blocks) * h.num_kv_heads * bs_or_S;
@@ -275,7 +254,7 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
   const int variant = g_variant.load();
   if (variant >= 2 && !tc_ok)
     return fail(PKV_ERR_UNSUPPORTED, "tensor-core kernel needs block_size %% 16 == 0 and < 2^31 rows");
-  const bool tc_pick = variant >= 2 || (variant == 0 && tc_enough_tiles(num_seqs, h, max_context, sms));
+  const bool tc_pick = variant >= 2 || (variant == 0 && tc_enough_tiles(num_seqs, h, span, sms));
   if (tc_pick && tc_ok) {
     if (tc_out) *tc_out = true;
     const size_t need = pkv::tc_workspace_bytes(tc_ctas(sms));
@@ -313,6 +292,10 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
       t.num_slots = fused->num_slots;
     }
     t.err = err;
+    if (score != nullptr) {
+      t.scored = 1;
+      t.sp = *score;
+    }
     cudaError_t ce = cudaSuccess;
     // 8 x 3 when forced; 12 x 2 when forced or for up to 4 query heads per KV
     // head, else 10 x 2 (one merge pass for all 8 heads)
@@ -325,7 +308,7 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
     if (ts != pkv::TcStatus::kOk) return cuda_fail(ce, "decode launch");
     return PKV_OK;
   }
-  const SplitPlan plan = plan_splits(num_seqs, h, max_context, sms);
+  const SplitPlan plan = plan_splits(num_seqs, h, span, sms);
   if (plan.nsplit > 65535) return fail(PKV_ERR_UNSUPPORTED, "too many splits");
   if (plan.workspace_bytes > 0) {
     if (!workspace || workspace_bytes < plan.workspace_bytes)
@@ -362,8 +345,14 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
   p.checked = g_checked.load();
   p.err = err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = contig ? pkv::launch_decode_contig(p, group, s)
-                               : pkv::launch_decode_paged(p, group, s);
+  cudaError_t e;
+  if (score != nullptr) {
+    p.sp = *score;
+    e = contig ? pkv::launch_decode_contig_scored(p, group, s)
+               : pkv::launch_decode_paged_scored(p, group, s);
+  } else {
+    e = contig ? pkv::launch_decode_contig(p, group, s) : pkv::launch_decode_paged(p, group, s);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   return PKV_OK;
 }
@@ -683,8 +672,8 @@ pkv_status pkv_contig_decode_attention(const void* q, const void* k_buf, const v
 
 size_t pkv_scored_decode_workspace_size(int32_t num_seqs, pkv_heads heads, int32_t max_context,
                                         int32_t window) {
-  if (window < 0) return 0;
-  return pkv_decode_workspace_size(num_seqs, heads, max_context);
+  if (window < 0 || max_context < 0) return 0;
+  return pkv_decode_workspace_size(num_seqs, heads, visible_span(max_context, window));
 }
 
 pkv_status pkv_paged_decode_attention_scored(

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
   if (kScored) {
 #pragma unroll
     for (int g = 0; g < G; ++g)
-      slope2[g] = p.sp.slopes != nullptr ? __ldg(p.sp.slopes + kvh * G + g) * kLog2e : 0.f;
+      slope2[g] = p.sp.slopes != nullptr ? slope_log2(p.sp.slopes, kvh * G + g) : 0.f;
   }
 
   // This warp's tiles: t_begin + warp + k * kDecodeWarps.
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         if (p.sp.cap2 > 0.f) sc[g] = capped_score(p.sp, sc[g]);
-        if (p.sp.slopes != nullptr) sc[g] += fmaxf(-slope2[g] * dist, kLowBias);
+        if (p.sp.slopes != nullptr) sc[g] = fmaf(-slope2[g], dist, sc[g]);
       }
     }
     float pr[GP];

@@ -606,9 +606,8 @@ __global__ void __launch_bounds__(W * 32, 1)
     const int low = kScored ? low_s[seg.seq] : 0;
     float slope0 = 0.f, slope1 = 0.f;  // of heads 2tq, 2tq + 1
     if (kScored && p.sp.slopes != nullptr) {
-      const float* sl = p.sp.slopes + seg.kvh * G;
-      slope0 = 2 * tq < G ? __ldg(sl + 2 * tq) * kLog2e : 0.f;
-      slope1 = 2 * tq + 1 < G ? __ldg(sl + 2 * tq + 1) * kLog2e : 0.f;
+      slope0 = 2 * tq < G ? slope_log2(p.sp.slopes, seg.kvh * G + 2 * tq) : 0.f;
+      slope1 = 2 * tq + 1 < G ? slope_log2(p.sp.slopes, seg.kvh * G + 2 * tq + 1) : 0.f;
     }
     // A segment that is only part of its pair (the CTA ranges cut the pair)
     // is a "piece"; the pair's CTAs are cf .. cl.  The piece of cf (the
@@ -748,10 +747,10 @@ __global__ void __launch_bounds__(W * 32, 1)
         if (kScored && p.sp.slopes != nullptr) {
           const float d0 = static_cast<float>(ctx - 1 - (row0 + g));
           const float d1 = static_cast<float>(ctx - 1 - (row0 + g + 8));
-          x0 += fmaxf(-slope0 * d0, kLowBias);
-          x1 += fmaxf(-slope1 * d0, kLowBias);
-          x2 += fmaxf(-slope0 * d1, kLowBias);
-          x3 += fmaxf(-slope1 * d1, kLowBias);
+          x0 = fmaf(-slope0, d0, x0);
+          x1 = fmaf(-slope1, d0, x1);
+          x2 = fmaf(-slope0, d1, x2);
+          x3 = fmaf(-slope1, d1, x3);
         }
         const float s0 = v0 ? x0 : -INFINITY;  // token g,   head 2tq
         const float s1 = v0 ? x1 : -INFINITY;  // token g,   head 2tq+1

@@ -21,7 +21,6 @@
 #include "kv_ops.cuh"
 #include "rope.cuh"
 #include "score.cuh"
-#include "scored_rows.cuh"
 
 namespace {
 
@@ -931,32 +930,6 @@ pkv_status prefill_common(const void* q, const int32_t* cu_seqlens_q, int32_t nu
   int* err = nullptr;
   st = device_info(&dev, &err, nullptr);
   if (st != PKV_OK) return st;
-  if (score != nullptr) {
-    pkv::ScoredRowsParams r;
-    std::memset(&r, 0, sizeof r);
-    r.q = static_cast<const uint16_t*>(q);
-    r.out = static_cast<uint16_t*>(out);
-    r.k = static_cast<const uint16_t*>(k_cache);
-    r.v = static_cast<const uint16_t*>(v_cache);
-    r.tables = block_tables;
-    r.cu_q = cu_seqlens_q;
-    r.ctx_lens = context_lens;
-    r.bs = block_size;
-    r.num_blocks = num_blocks;
-    r.num_rows = num_tokens;
-    r.max_blocks = max_blocks_per_seq;
-    r.num_seqs = num_seqs;
-    r.Hq = heads.num_q_heads;
-    r.Hkv = heads.num_kv_heads;
-    r.max_q = max_q_tokens;
-    r.qscale = scale * pkv::kLog2e;
-    r.sp = *score;
-    r.checked = g_checked.load();
-    r.err = err;
-    r.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
-    const cudaError_t e = pkv::launch_scored_rows(r, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "scored prefill launch");
-  }
   alignas(64) CUtensorMap tk;
   alignas(64) CUtensorMap tv;
   if (!pkv::encode_prefill_runs(&tk, k_cache, rows_total, run_rows) ||
@@ -992,8 +965,16 @@ pkv_status prefill_common(const void* q, const int32_t* cu_seqlens_q, int32_t nu
     return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for q");
   p.out_tma = pkv::encode_prefill_rows(&to, out, num_tokens, heads.num_q_heads, G, 32) ? 1 : 0;
   p.out_v8 = aligned(out, 32) ? 1 : 0;
-  const cudaError_t e =
-      pkv::launch_prefill(tk, tv, tq, to, p, static_cast<cudaStream_t>(stream));
+  cudaError_t e;
+  if (score != nullptr) {
+    p.k = static_cast<const uint16_t*>(k_cache);
+    p.v = static_cast<const uint16_t*>(v_cache);
+    p.sp = *score;
+    p.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
+    e = pkv::launch_prefill_scored(tk, tv, tq, to, p, static_cast<cudaStream_t>(stream));
+  } else {
+    e = pkv::launch_prefill(tk, tv, tq, to, p, static_cast<cudaStream_t>(stream));
+  }
   if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
   return PKV_OK;
 }

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "score.cuh"
+
 namespace pkv {
 
 struct PrefillParams {
@@ -25,7 +27,17 @@ struct PrefillParams {
   int32_t out_v8;                // plain stores of 32 bytes (out 32-byte aligned), else 16
   int32_t checked;
   int* err;
+  // scored kernels only
+  const uint16_t* k;             // the caches, for rows recomputed one by one
+  const uint16_t* v;
+  ScoreParams sp;
+  int err_code;                  // of a table entry out of range
 };
+
+// What a launch of the kernel computes: the plain causal scores; masked by a
+// window, documents or prefixes too; capped (and masked) with a fixed offset
+// in place of the running maximum; or capped, biased and masked in any way.
+enum PrefillMode { kPrefillPlain = 0, kPrefillMasked = 1, kPrefillCapped = 2, kPrefillGeneral = 3 };
 
 // The K or V cache ([rows][128] bf16) as a 4-D tensor (64 columns, 8 rows,
 // 2 column halves, row groups of 8) whose boxes of run_rows rows land in
@@ -47,5 +59,9 @@ bool encode_prefill_rows(CUtensorMap* map, const void* base, int64_t num_tokens,
 // query rows, KV head, sequence) items.
 cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                            const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream);
+// The same with the scores of p.sp.
+cudaError_t launch_prefill_scored(const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const CUtensorMap& tq, const CUtensorMap& to,
+                                  const PrefillParams& p, cudaStream_t stream);
 
 }  // namespace pkv

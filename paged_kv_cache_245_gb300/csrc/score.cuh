@@ -24,9 +24,13 @@ struct ScoreParams {
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-// A bias below this never decides a softmax, and stays finite where slope x
-// distance would overflow (a row of -inf scores would have no maximum).
-constexpr float kLowBias = -1e30f;
+// Slope of head h in log-2 units per position.  Past 2^60 either way it would
+// only overflow (a row of -inf scores has no maximum); weights that far apart
+// are 0 or 1 long before.
+constexpr float kMaxSlope = 1152921504606846976.f;
+__device__ __forceinline__ float slope_log2(const float* slopes, int h) {
+  return fminf(fmaxf(__ldg(slopes + h) * kLog2e, -kMaxSlope), kMaxSlope);
+}
 
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
@@ -135,7 +139,7 @@ __device__ inline void attend_row(const ScoreParams& sp, const KvRows& kv, const
     if (sp.cap2 > 0.f) x = capped_score(sp, x);
     if (slope2 != 0.f) {
       const float d = static_cast<float>(j < pos ? pos - j : j - pos);
-      x += fmaxf(-slope2 * d, kLowBias);
+      x = fmaf(-slope2, d, x);
     }
     if (!(x <= m)) {  // a NaN score makes the row NaN, as the formula does
       const float a = fast_exp2(m - x);

@@ -251,31 +251,51 @@ class RopePlan:
                                    c_scaling))
 
 
-def _same_device(dev, **tensors):
-    for n, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, not on %s" % (n, t.device, dev))
+# The calls below are made several times a layer and token, so their argument
+# checks are kept to a few hundred nanoseconds a tensor, and the stream is
+# read as the integer it is (torch.cuda.current_stream builds an object: 2.9 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on_device(dev, call, *args):
-    """Run a library call with `dev` current (the library launches there) on
-    its current stream."""
-    if dev.index == torch.cuda.current_device():
-        _check(call(*args, torch.cuda.current_stream().cuda_stream))
+def _check_in(t, dtype, ndim, index, name):
+    """t is a contiguous CUDA tensor of this type and rank on device `index`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim \
+            and t.get_device() == index and t.is_contiguous():
         return
-    with torch.cuda.device(dev):
-        _check(call(*args, torch.cuda.current_stream().cuda_stream))
+    _need(t, dtype, name, ndim)
+    raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, index))
 
 
-def _token_rows(t, name):
+def _device_index(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return t.get_device()
+
+
+def _on_device(index, call, *args):
+    """Run a library call with device `index` current (the library launches
+    there) on its current stream."""
+    if index == torch.cuda.current_device():
+        status = call(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, _raw_stream(index))
+    if status:
+        _check(status)
+
+
+def _token_rows(t, index, name):
     """Token stride (elements) of new rows [T, H, D] whose heads are adjacent;
     tokens may be further apart (a view of a wider projection output)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
     if t.dim() != 3:
         raise ValueError("%s must have 3 dims" % name)
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, index))
     T, H, d = t.shape
     st, sh, sd = t.stride()
     if T and ((d > 1 and sd != 1) or (H > 1 and sh != d)):
@@ -289,29 +309,28 @@ def rope_append(positions, slot_mapping, q, k, v, k_cache, v_cache, rope, out=No
     for kv_append) and return the turned q.  q, k and v may be views of one
     projection output (any token stride that is a multiple of 8).  out: the
     result [T, Hq, D] (q itself, if contiguous, for in place)."""
-    _need(positions, torch.int32, "positions", 1)
-    _need(slot_mapping, torch.int64, "slot_mapping", 1)
-    sq, sk, sv = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, torch.bfloat16, n, 4)
+    dev = _device_index(q, "q")
+    sq, sk, sv = _token_rows(q, dev, "q"), _token_rows(k, dev, "k"), _token_rows(v, dev, "v")
+    _check_in(positions, torch.int32, 1, dev, "positions")
+    _check_in(slot_mapping, torch.int64, 1, dev, "slot_mapping")
+    _check_in(k_cache, torch.bfloat16, 4, dev, "k_cache")
+    _check_in(v_cache, torch.bfloat16, 4, dev, "v_cache")
     if not isinstance(rope, RopePlan):
         raise TypeError("rope must be a RopePlan")
     nb, hkv, bs, d = k_cache.shape
     T, hq, d2 = q.shape
     if v_cache.shape != k_cache.shape or k.shape != v.shape:
         raise ValueError("k/v and cache shapes must match")
-    if tuple(k.shape) != (T, hkv, d) or d2 != d:
+    if k.shape != (T, hkv, d) or d2 != d:
         raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D] matching the cache")
     if positions.shape[0] != T or slot_mapping.shape[0] != T:
         raise ValueError("positions / slot_mapping must have one entry per token")
     if out is None:
         out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, "out", 3)
-    if out.shape != q.shape:
-        raise ValueError("out must be [T, Hq, D]")
-    dev = q.device
-    _same_device(dev, positions=positions, slot_mapping=slot_mapping, k=k, v=v, k_cache=k_cache,
-                 v_cache=v_cache, out=out)
+    else:
+        _check_in(out, torch.bfloat16, 3, dev, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must be [T, Hq, D]")
     _on_device(dev, lib().pkv_rope_append, positions.data_ptr(), slot_mapping.data_ptr(), T,
                q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(),
                k_cache.data_ptr(), v_cache.data_ptr(), nb * bs, bs, Heads(hq, hkv, d), rope.c)
@@ -586,63 +605,75 @@ def scored_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_contex
 
 def _score(dev, hq, rows, num_seqs, softcap, window, alibi_slopes, first_key, prefix_lens):
     """The pkv_score struct; its arrays checked (rows: of q, for first_key)."""
-    s = Score(softcap, window)
-    for t, dtype, n, name in ((alibi_slopes, torch.float32, hq, "alibi_slopes"),
-                              (first_key, torch.int32, rows, "first_key"),
-                              (prefix_lens, torch.int32, num_seqs, "prefix_lens")):
-        if t is None:
-            continue
-        _need(t, dtype, name, 1)
-        if t.shape[0] != n:
-            raise ValueError("%s must have %d entries" % (name, n))
-        if t.device != dev:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
-        setattr(s, name, t.data_ptr())
+    s = Score(float(softcap), int(window))
+    if alibi_slopes is not None:
+        _check_in(alibi_slopes, torch.float32, 1, dev, "alibi_slopes")
+        if alibi_slopes.shape[0] != hq:
+            raise ValueError("alibi_slopes must have %d entries" % hq)
+        s.alibi_slopes = alibi_slopes.data_ptr()
+    if first_key is not None:
+        _check_in(first_key, torch.int32, 1, dev, "first_key")
+        if first_key.shape[0] != rows:
+            raise ValueError("first_key must have %d entries" % rows)
+        s.first_key = first_key.data_ptr()
+    if prefix_lens is not None:
+        _check_in(prefix_lens, torch.int32, 1, dev, "prefix_lens")
+        if prefix_lens.shape[0] != num_seqs:
+            raise ValueError("prefix_lens must have %d entries" % num_seqs)
+        s.prefix_lens = prefix_lens.data_ptr()
     return s
+
+
+def _check_attention(contig, q, k, v, where, context_lens, out):
+    """Device index and the output of an attention call; its tensors checked."""
+    dev = _device_index(q, "q")
+    _check_in(q, torch.bfloat16, 3, dev, "q")
+    _check_in(k, torch.bfloat16, 4, dev, "k_buf" if contig else "k_cache")
+    _check_in(v, torch.bfloat16, 4, dev, "v_buf" if contig else "v_cache")
+    if contig:
+        _check_in(where, torch.int32, 1, dev, "req_ids")
+    else:
+        _check_in(where, torch.int32, 2, dev, "block_tables")
+    _check_in(context_lens, torch.int32, 1, dev, "context_lens")
+    if q.shape[2] != k.shape[3] or v.shape != k.shape:
+        raise ValueError("q / cache shapes disagree")
+    if where.shape[0] != context_lens.shape[0]:
+        raise ValueError("block_tables / req_ids / context_lens must have num_seqs rows")
+    if out is None:
+        return dev, torch.empty_like(q)
+    _check_in(out, torch.bfloat16, 3, dev, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    return dev, out
 
 
 def _decode_scored(contig, q, k, v, where, context_lens, max_context, scale, softcap, window,
                    alibi_slopes, first_key, out, workspace):
-    _need(q, torch.bfloat16, "q", 3)
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, torch.bfloat16, n, 4)
-    if contig:
-        _need(where, torch.int32, "req_ids", 1)
-    else:
-        _need(where, torch.int32, "block_tables", 2)
-    _need(context_lens, torch.int32, "context_lens", 1)
+    dev, out = _check_attention(contig, q, k, v, where, context_lens, out)
     B, hq, d = q.shape
-    n, hkv, bs, d2 = k.shape
-    if d != d2 or v.shape != k.shape:
-        raise ValueError("q / cache shapes disagree")
-    if where.shape[0] != B or context_lens.shape[0] != B:
-        raise ValueError("block_tables / req_ids / context_lens must have num_seqs rows")
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, torch.bfloat16, "out", 3)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    dev, max_context = q.device, int(max_context)
-    _same_device(dev, k=k, v=v, tables=where, context_lens=context_lens, out=out,
-                 workspace=workspace)
+    n, hkv, bs, _ = k.shape
+    if context_lens.shape[0] != B:
+        raise ValueError("context_lens must have num_seqs rows")
     score = _score(dev, hq, B, B, softcap, window, alibi_slopes, first_key, None)
     h = Heads(hq, hkv, d)
+    max_context, scale = int(max_context), float(scale)
     L = lib()
-    if workspace is None and B > 0:
+    if workspace is None:
         # convenience for callers without their own buffer; the C ABI itself never allocates
         with torch.cuda.device(dev):
             size = L.pkv_scored_decode_workspace_size(B, h, max_context, score.window)
-        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
-    ws = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                              workspace.numel() * workspace.element_size())
+        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on cuda:%d" % dev)
     if contig:
         _on_device(dev, L.pkv_contig_decode_attention_scored, q.data_ptr(), k.data_ptr(),
                    v.data_ptr(), where.data_ptr(), n, context_lens.data_ptr(), B, max_context, bs,
-                   scale, score, h, out.data_ptr(), *ws)
+                   scale, score, h, out.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     else:
         _on_device(dev, L.pkv_paged_decode_attention_scored, q.data_ptr(), k.data_ptr(),
                    v.data_ptr(), where.data_ptr(), where.shape[1], n, context_lens.data_ptr(), B,
-                   max_context, bs, scale, score, h, out.data_ptr(), *ws)
+                   max_context, bs, scale, score, h, out.data_ptr(), workspace.data_ptr(),
+                   workspace.nbytes)
     return out
 
 
@@ -668,43 +699,25 @@ def contig_decode_attention_scored(q, k_buf, v_buf, req_ids, context_lens, max_c
 
 def _prefill_scored(contig, q, cu_seqlens_q, k, v, where, context_lens, max_q_tokens, scale,
                     softcap, window, alibi_slopes, first_key, prefix_lens, out):
-    _need(q, torch.bfloat16, "q", 3)
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, torch.bfloat16, n, 4)
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
-    if contig:
-        _need(where, torch.int32, "req_ids", 1)
-    else:
-        _need(where, torch.int32, "block_tables", 2)
-    _need(context_lens, torch.int32, "context_lens", 1)
+    dev, out = _check_attention(contig, q, k, v, where, context_lens, out)
+    _check_in(cu_seqlens_q, torch.int32, 1, dev, "cu_seqlens_q")
     T, hq, d = q.shape
-    n, hkv, bs, d2 = k.shape
+    n, hkv, bs, _ = k.shape
     B = context_lens.shape[0]
-    if d != d2 or v.shape != k.shape:
-        raise ValueError("q / cache shapes disagree")
-    if cu_seqlens_q.shape[0] != B + 1 or where.shape[0] != B:
-        raise ValueError("cu_seqlens_q must have num_seqs + 1 entries, block_tables / req_ids "
-                         "num_seqs rows")
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, torch.bfloat16, "out", 3)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    dev = q.device
-    _same_device(dev, k=k, v=v, cu_seqlens_q=cu_seqlens_q, tables=where,
-                 context_lens=context_lens, out=out)
+    if cu_seqlens_q.shape[0] != B + 1:
+        raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
     score = _score(dev, hq, T, B, softcap, window, alibi_slopes, first_key, prefix_lens)
     h = Heads(hq, hkv, d)
+    max_q_tokens, scale = int(max_q_tokens), float(scale)
     if contig:
         _on_device(dev, lib().pkv_contig_prefill_attention_scored, q.data_ptr(),
                    cu_seqlens_q.data_ptr(), T, k.data_ptr(), v.data_ptr(), where.data_ptr(), n,
-                   context_lens.data_ptr(), B, int(max_q_tokens), bs, scale, score, h,
-                   out.data_ptr())
+                   context_lens.data_ptr(), B, max_q_tokens, bs, scale, score, h, out.data_ptr())
     else:
         _on_device(dev, lib().pkv_paged_prefill_attention_scored, q.data_ptr(),
                    cu_seqlens_q.data_ptr(), T, k.data_ptr(), v.data_ptr(), where.data_ptr(),
-                   where.shape[1], n, context_lens.data_ptr(), B, int(max_q_tokens), bs, scale,
-                   score, h, out.data_ptr())
+                   where.shape[1], n, context_lens.data_ptr(), B, max_q_tokens, bs, scale, score,
+                   h, out.data_ptr())
     return out
 
 

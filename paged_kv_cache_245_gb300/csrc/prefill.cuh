@@ -10,6 +10,14 @@
 
 namespace pkv {
 
+// The capped scores' constants (prefill_scored.cuh), pairs as two equal floats.
+struct CappedScore {
+  uint64_t c[5];    // the polynomial in the raw product's square
+  uint64_t neg_m2;  // -m
+  float p_low, p_high;  // sums of P of a half tile whose products are in the polynomial's range
+  float exp_k, neg_2cap, cap_m;  // 2^(exp_k s) = e^(2y); -2 cap; cap - m
+};
+
 struct PrefillParams {
   const uint16_t* q;             // [T][Hq][128] the chunks' new tokens, packed
   uint16_t* out;                 // [T][Hq][128]
@@ -31,13 +39,14 @@ struct PrefillParams {
   const uint16_t* k;             // the caches, for rows recomputed one by one
   const uint16_t* v;
   ScoreParams sp;
+  CappedScore cap;
   int err_code;                  // of a table entry out of range
 };
 
-// What a launch of the kernel computes: the plain causal scores; masked by a
-// window, documents or prefixes too; capped (and masked) with a fixed offset
-// in place of the running maximum; or capped, biased and masked in any way.
-enum PrefillMode { kPrefillPlain = 0, kPrefillMasked = 1, kPrefillCapped = 2, kPrefillGeneral = 3 };
+// What the scored kernel (prefill_scored.cu) computes: scores masked by a
+// window, documents or prefixes; capped (and masked) against a fixed offset in
+// place of the running maximum; biased (and masked); or any of them.
+enum PrefillMode { kPrefillMasked, kPrefillCapped, kPrefillBiased, kPrefillGeneral };
 
 // The K or V cache ([rows][128] bf16) as a 4-D tensor (64 columns, 8 rows,
 // 2 column halves, row groups of 8) whose boxes of run_rows rows land in

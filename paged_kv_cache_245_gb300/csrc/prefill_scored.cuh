@@ -1,27 +1,35 @@
-// prefill_scored.cuh -- the softmax of the prefill kernel for capped, biased
-// and masked scores: one key tile of one row per thread, S in tensor memory
-// in, P = 2^(score - m) as packed bf16 pairs out (over the first 64 columns of
-// S in place).
+// prefill_scored.cuh -- the softmax of the scored prefill kernel
+// (prefill_scored.cu): one key tile of one row per thread, S in tensor memory
+// in, P = 2^(score - m) as packed bf16 pairs out, over the first 64 columns of
+// S in place.
 //
 // Masks.  What a token sees is one interval of positions, so a row's mask in
-// a tile is an interval of columns; a tile that every row of the warp sees
-// whole takes the path without masks.
+// a tile is an interval of columns.  A tile that every row of the warp sees
+// whole takes straight-line code; the others a loop over halves of 64 columns,
+// with bit tests, that skips a half no row sees.  (A loop, and one body for
+// every kind of half: code that runs once or twice an item comes out of a cold
+// instruction cache.  Unrolled over the row it cost 8 x 2048 tokens 253 -> 323
+// us, although one tile in eight takes it.)
 //
 // Capped scores (kPrefillCapped).  |score| <= cap, so no running maximum is
-// needed: P is taken against a fixed m, chosen so that the lowest score keeps
+// needed, and one pass over S does: P is taken against a fixed m, chosen so that the lowest score keeps
 // 2^-100 (26 binary digits above the smallest normal number) and the highest
-// stays at 2^50 or less, and O and l are never rescaled.  That leaves one pass
-// over S.  The tanh: three special-function operations an element (two
-// exponentials, a reciprocal) would take three times the tensor cores' time,
-// and tanh.approx is too coarse (2^-11); so where every score of the warp's
-// half tile is within the cap (|s| <= cap, |tanh| <= 0.76) it is an odd
-// polynomial on packed pairs, s (c0 + c1 w + .. + c4 w^4), w = s^2: the minimax
-// fit of tanh(y) / y over y^2 in [0, 1] (relative error 2^-17, by Remez
-// exchange; the probabilities are rounded to 2^-9 after it).  A half tile with
-// a larger score is done again with exponentials.
+// stays at 2^50 or less, and O and l are never rescaled.  The tanh: three
+// special-function operations an element (two exponentials, a reciprocal)
+// would take longer than the tensor cores, and tanh.approx is too coarse
+// (2^-11); so where every score is within the cap (|s| <= cap, |tanh| <= 0.76)
+// it is an odd polynomial on packed pairs, s (c0 + c1 w + .. + c4 w^4), w = s^2:
+// the minimax fit of tanh(y) / y over y^2 in [0, 1] (relative error 2^-17, by
+// Remez exchange; the probabilities are rounded to 2^-9 after it).  Half tiles
+// with a larger score take the exponentials.
+//
+// Biased scores (kPrefillBiased).  Up to the row's own position the bias is
+// linear in the column: one packed addition and one fused product a pair.
 #pragma once
 
 #include <limits.h>
+
+#include <type_traits>
 
 #include "prefill.cuh"
 #include "score.cuh"
@@ -29,58 +37,33 @@
 
 namespace pkv {
 
+// A thread's row of an item.
 struct ScoredRow {
-  int lo, hi;    // columns the row sees, counted from the item's first key (none: lo > hi)
-  int pos;       // the row's own position, counted the same
-  float slope2;  // its head's slope, log-2 units
+  int lo, hi;     // columns the row sees, counted from the item's first key (none: lo > hi)
+  int pos;        // the row's own position, counted the same
+  float slope2;   // its head's slope, log-2 units
+  int64_t qrow;   // row of q and out
+  bool valid;     // a row of the chunk (else padding)
 };
 
-struct ScoredConsts {
-  float sc;         // scale * log2 e
-  ScoreParams sp;
-  // kPrefillCapped
-  uint64_t c[5];    // the polynomial in the raw product's square, as pairs
-  uint64_t neg_m2;  // -m as a pair
-  float w_max;      // squares up to this are in the polynomial's range
-  float exp_k, neg_2cap, cap_m;  // 2^(exp_k s) = e^(2y); cap - m
+struct SoftState {
+  float m;  // what P is taken against (running maximum)
+  float l;  // sum of P
 };
 
-// The offset m of capped scores |x| <= cap2 (cap2 <= 75): see above.
-__host__ __device__ inline float capped_offset(float cap2) {
-  return cap2 <= 50.f ? cap2 : 100.f - cap2;
-}
-
-// Whether the capped kernel serves these scores: a cap whose range fits the
-// fixed offset, no bias, and a raw product at the cap (cap / scale) whose
-// eighth power neither overflows nor underflows in fp32.
-inline bool capped_kernel_serves(const ScoreParams& sp, float qscale) {
-  if (!(sp.cap2 > 0.f) || sp.cap2 > 75.f || sp.slopes != nullptr) return false;
-  const float r = qscale * sp.inv_cap2 < 0.f ? -qscale * sp.inv_cap2 : qscale * sp.inv_cap2;
-  return r >= 1.220703125e-4f && r <= 8192.f;  // 2^-13 .. 2^13
-}
+// The capped scores' polynomial in registers: packed products take no
+// operand from constant memory, and reloading them cost 15 % of the kernel.
+struct CappedRegs {
+  uint64_t c[5], neg_m2;
+};
 
 template <int kMode>
-__device__ __forceinline__ ScoredConsts scored_consts(const PrefillParams& p) {
-  using namespace umma;
-  ScoredConsts k;
-  k.sc = p.qscale;
-  k.sp = p.sp;
+__device__ __forceinline__ CappedRegs capped_regs(const PrefillParams& p) {
+  CappedRegs k;
   if (kMode == kPrefillCapped) {
-    const float r = k.sc * p.sp.inv_cap2;
-    const float fit[5] = {0.99999309f, -0.33298065f, 0.13036811f, -0.04481755f, 0.00903642f};
-    float power = k.sc;
 #pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      const uint32_t b = __float_as_uint(fit[i] * power);
-      k.c[i] = f2_pack(b, b);
-      power *= r * r;
-    }
-    const float m = capped_offset(p.sp.cap2);
-    k.neg_m2 = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
-    k.w_max = 1.f / (r * r);
-    k.exp_k = k.sc * p.sp.cap_k;
-    k.neg_2cap = -2.f * p.sp.cap2;
-    k.cap_m = p.sp.cap2 - m;
+    for (int i = 0; i < 5; ++i) asm volatile("mov.b64 %0, %1;" : "=l"(k.c[i]) : "l"(p.cap.c[i]));
+    asm volatile("mov.b64 %0, %1;" : "=l"(k.neg_m2) : "l"(p.cap.neg_m2));
   }
   return k;
 }
@@ -91,269 +74,491 @@ __device__ __forceinline__ uint32_t span_bits(int a, int b, int w) {
   return lo <= hi ? (0xffffffffu << lo) & (0xffffffffu >> (31 - hi)) : 0u;
 }
 
-// O *= alpha for the warp's rows.
-__device__ __forceinline__ void rescale_o(uint32_t o_tm, float alpha) {
-  using namespace umma;
-#pragma unroll 1
-  for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
-    uint32_t w[32];
-    tmem_ld32(w, o_tm + c0);
-    tmem_wait_ld(w);
-#pragma unroll
-    for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * alpha);
-    tmem_st32(o_tm + c0, w);
-  }
-}
+constexpr int kRing = 4;  // item descriptors in flight
+
+// The kernel's mbarriers.
+struct ScoredBars {
+  uint64_t kfull[2];    // K of a stage landed
+  uint64_t vfull[2];    // V of a stage landed
+  uint64_t kempty[2];   // both S products reading a stage's K completed
+  uint64_t vempty[2];   // both P V products reading a stage's V completed
+  uint64_t sfull[2];    // S_t of the next key tile (and PV_t before it) done
+  uint64_t pfull[2];    // P_t written (one arrival per warp)
+  uint64_t ofull[2];    // an item's last PV_t completed
+  uint64_t qfull[2];    // a Q slot written (every lane of warp 10 arrives)
+  uint64_t qempty[2];   // the last S product reading a Q slot completed
+  uint64_t ifull[kRing];   // an item descriptor published
+  uint64_t iempty[kRing];  // every reader is done with it
+  uint64_t drain;       // the MMA thread's final wait
+  uint32_t tmem;        // tensor-memory address
+  volatile int abort;   // a wait gave up
+};
 
 // The row's running maximum takes in the tile's; O and l are rescaled when it
 // grows by more than 2^kRescaleLog2.  Returns the offset P is taken against
 // (0 while the row has seen nothing, where every P is masked).
-__device__ __forceinline__ float take_max(float tmax, bool first, uint32_t o_tm, float& m_used,
-                                          float& l) {
+__device__ __forceinline__ float take_max(float tmax, bool first, uint32_t o_tm, SoftState& st) {
   using namespace umma;
-  const float m_new = fmaxf(m_used, tmax);
+  const float m_new = fmaxf(st.m, tmax);
   if (first) {
-    m_used = m_new;
+    st.m = m_new;
   } else {
-    const bool grow = m_new > m_used + kRescaleLog2;  // always, from -inf
+    const bool grow = m_new > st.m + kRescaleLog2;  // always, from -inf
     if (__any_sync(kFull, grow)) {
-      const float alpha = grow ? fast_exp2(m_used - m_new) : 1.f;
+      const float alpha = grow ? fast_exp2(st.m - m_new) : 1.f;
       if (grow) {
-        l *= alpha;
-        m_used = m_new;
+        st.l *= alpha;
+        st.m = m_new;
       }
-      rescale_o(o_tm, alpha);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[32];
+        tmem_ld32(w, o_tm + 32 * c);
+        tmem_wait_ld(w);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+        tmem_st32(o_tm + 32 * c, w);
+      }
     }
   }
-  return m_used == -INFINITY ? 0.f : m_used;
+  return st.m == -INFINITY ? 0.f : st.m;
 }
 
-// P of 64 columns from their scores: e(c) for column c, packed and summed.
-template <typename Score>
-__device__ __forceinline__ float masked_half(uint32_t s_tm, int h, uint32_t lo, uint32_t hi,
-                                             Score score) {
+// ---- 32 columns ("chunk") of a row, as 16 pairs in registers.  f(i, pair)
+// gives pair i's scores; called in order of i.
+__device__ __forceinline__ bool bit_of(uint32_t bits, int c) { return (bits >> c) & 1u; }
+
+template <bool kMask, typename F>
+__device__ __forceinline__ void chunk_max(const uint32_t (&a)[32], uint32_t bits, F&& f,
+                                          float (&mx)[4]) {
   using namespace umma;
-  uint32_t a[32], b[32], pk[32];
-  tmem_ld32(a, s_tm + 64 * h);
-  tmem_ld32(b, s_tm + 64 * h + 32);
-  tmem_wait_ld(a);
-  tmem_ready(b);
-  float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    const uint32_t u0 = c < 16 ? a[2 * c] : b[2 * c - 32];
-    const uint32_t u1 = c < 16 ? a[2 * c + 1] : b[2 * c - 31];
-    float e0 = fast_exp2(score(__uint_as_float(u0)));
-    float e1 = fast_exp2(score(__uint_as_float(u1)));
-    const uint32_t bits = c < 16 ? lo : hi;
-    e0 = (bits >> ((2 * c) & 31)) & 1u ? e0 : 0.f;
-    e1 = (bits >> ((2 * c + 1) & 31)) & 1u ? e1 : 0.f;
-    ls[c & 3] += e0 + e1;
-    pk[c] = pack_bf16x2(e0, e1);
+  for (int i = 0; i < 16; ++i) {
+    float x0, x1;
+    f2_unpack(f(i, f2_pack(a[2 * i], a[2 * i + 1])), x0, x1);
+    if (kMask) {
+      x0 = bit_of(bits, 2 * i) ? x0 : -INFINITY;
+      x1 = bit_of(bits, 2 * i + 1) ? x1 : -INFINITY;
+    }
+    mx[i & 3] = fmax3(mx[i & 3], x0, x1);
   }
-  tmem_st32(s_tm + 32 * h, pk);
-  return (ls[0] + ls[1]) + (ls[2] + ls[3]);
 }
 
-__device__ __forceinline__ void zero_half(uint32_t s_tm, int h) {
-  uint32_t pz[32];
-#pragma unroll
-  for (int c = 0; c < 32; ++c) pz[c] = 0u;
-  umma::tmem_st32(s_tm + 32 * h, pz);
-}
-
-// One half (64 columns) under the cap: the polynomial, or, where a score is
-// out of its range, the exponentials.
-template <bool kMasked>
-__device__ __forceinline__ float capped_half(const ScoredConsts& k, uint32_t s_tm, int h,
-                                             uint32_t lo, uint32_t hi) {
+// P = 2^f, packed into pk[0..15], summed into ls.
+template <bool kMask, typename F>
+__device__ __forceinline__ void chunk_p(const uint32_t (&a)[32], uint32_t bits, F&& f,
+                                        uint32_t* pk, uint64_t (&ls)[4]) {
   using namespace umma;
-  uint32_t a[32], b[32], pk[32];
-  tmem_ld32(a, s_tm + 64 * h);
-  tmem_ld32(b, s_tm + 64 * h + 32);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x0, x1;
+    f2_unpack(f(i, f2_pack(a[2 * i], a[2 * i + 1])), x0, x1);
+    float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+    if (kMask) {
+      e0 = bit_of(bits, 2 * i) ? e0 : 0.f;
+      e1 = bit_of(bits, 2 * i + 1) ? e1 : 0.f;
+    }
+    ls[i & 3] = f2_add(ls[i & 3], f2_pack(__float_as_uint(e0), __float_as_uint(e1)));
+    pk[i] = pack_bf16x2(e0, e1);
+  }
+}
+
+__device__ __forceinline__ float sum_of(const uint64_t (&ls)[4]) {
+  using namespace umma;
+  float l0, l1, l2, l3;
+  f2_unpack(f2_add(ls[0], ls[1]), l0, l1);
+  f2_unpack(f2_add(ls[2], ls[3]), l2, l3);
+  return (l0 + l2) + (l1 + l3);
+}
+
+// A tile as a row sees it (columns c0 .. c1) and as the rows of its warp do.
+struct TileMask {
+  int c0, c1;
+  bool whole;    // every row sees every column
+  bool none[2];  // no row sees a column of this half
+  __device__ __forceinline__ uint32_t bits(int chunk) const { return span_bits(c0, c1, chunk); }
+};
+
+__device__ __forceinline__ TileMask tile_mask(const ScoredRow& r, int kt) {
+  using namespace umma;
+  TileMask m;  // (kt is far below 2^31 where hi is not)
+  m.c0 = r.lo > kt ? (r.lo - kt > 128 ? 128 : r.lo - kt) : 0;
+  m.c1 = r.hi < kt ? -1 : (r.hi - kt > 127 ? 127 : r.hi - kt);
+  m.whole = __all_sync(kFull, m.c0 == 0 && m.c1 == 127);
+  m.none[0] = m.none[1] = false;
+  if (!m.whole) {
+    m.none[0] = !__any_sync(kFull, m.c0 < 64 && m.c1 >= 0 && m.c0 <= m.c1);
+    m.none[1] = !__any_sync(kFull, m.c1 >= 64 && m.c0 <= m.c1);
+  }
+  return m;
+}
+
+// A whole row of S, in one tensor-memory round trip (335 to 375 cycles).
+struct Row128 {
+  uint32_t a[32], b[32], c[32], d[32];
+  __device__ __forceinline__ explicit Row128(uint32_t s_tm) {
+    using namespace umma;
+    tmem_ld32(a, s_tm);
+    tmem_ld32(b, s_tm + 32);
+    tmem_ld32(c, s_tm + 64);
+    tmem_ld32(d, s_tm + 96);
+    tmem_wait_ld(a);
+    tmem_ready(b);
+    tmem_ready(c);
+    tmem_ready(d);
+  }
+};
+
+__device__ __forceinline__ void load_half(uint32_t (&a)[32], uint32_t (&b)[32], uint32_t tm) {
+  using namespace umma;
+  tmem_ld32(a, tm);
+  tmem_ld32(b, tm + 32);
   tmem_wait_ld(a);
   tmem_ready(b);
-  uint64_t ls2[2] = {0ull, 0ull};
-  float top[2] = {0.f, 0.f};
+}
+
+// The linear bias of consecutive pairs: start + slope (2i, 2i + 1), along four
+// chains of additions.
+struct BiasPairs {
+  uint64_t t[4], step;
+  __device__ __forceinline__ BiasPairs(float start, float slope) {
+    using namespace umma;
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    const uint64_t s2 = c < 16 ? f2_pack(a[2 * c], a[2 * c + 1]) : f2_pack(b[2 * c - 32], b[2 * c - 31]);
+    for (int k = 0; k < 4; ++k)
+      t[k] = f2_pack(__float_as_uint(fmaf(slope, static_cast<float>(2 * k), start)),
+                     __float_as_uint(fmaf(slope, static_cast<float>(2 * k + 1), start)));
+    const uint32_t s8 = __float_as_uint(8.f * slope);
+    step = f2_pack(s8, s8);
+  }
+  __device__ __forceinline__ uint64_t next(int i) {
+    const uint64_t r = t[i & 3];
+    t[i & 3] = umma::f2_add(r, step);
+    return r;
+  }
+};
+
+__device__ __forceinline__ void zero_p(uint32_t (&pk)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) pk[i] = 0u;
+}
+
+// A tile against the running maximum; scale >= 0, no cap.  Two passes over S:
+// with the row held in registers between them the kernel spills (measured a
+// quarter slower).
+template <int kMode>
+__device__ __forceinline__ void tile_running_max(const PrefillParams& p, const ScoredRow& r,
+                                                 uint32_t s_tm, uint32_t o_tm, int kt, bool first,
+                                                 SoftState& st) {
+  using namespace umma;
+  constexpr bool kBias = kMode == kPrefillBiased;
+  const TileMask mask = tile_mask(r, kt);
+  const uint64_t sc2 = f2_pack(__float_as_uint(p.qscale), __float_as_uint(p.qscale));
+  const float at = static_cast<float>(r.pos - kt);  // distance of column 0
+  auto raw = [](int, uint64_t s2) { return s2; };
+  float mx[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
+  uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+  // past a row's own position (seen under a prefix only) the distance grows
+  // again; up to it the bias is linear in the column
+  const bool bent = kBias && __any_sync(kFull, r.hi > r.pos && r.pos < kt + 127);
+  if (mask.whole && !bent) {
+    // Loads of S take 335 to 375 cycles.  The maximum comes from one load of
+    // the row; its last chunk stays in registers, and the others come again,
+    // each during the exponentials of the one before.
+    Row128 s(s_tm);
+    BiasPairs bias(-r.slope2 * at, r.slope2);
+    auto max_f = [&](int i, uint64_t s2) { return kBias ? f2_fma(s2, sc2, bias.next(i)) : s2; };
+    chunk_max<false>(s.a, 0u, max_f, mx);
+    chunk_max<false>(s.b, 0u, max_f, mx);
+    chunk_max<false>(s.c, 0u, max_f, mx);
+    chunk_max<false>(s.d, 0u, max_f, mx);
+    const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    const float m = take_max(kBias ? tmax : tmax * p.qscale, first, o_tm, st);
+    uint32_t x[32], y[32], p0[32], p1[32];
+    tmem_ld32(x, s_tm);
+    const uint64_t nm2 = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
+    bias = BiasPairs(fmaf(-r.slope2, at - 96.f, -m), r.slope2);
+    auto f = [&](int i, uint64_t s2) { return f2_fma(s2, sc2, kBias ? bias.next(i) : nm2); };
+    chunk_p<false>(s.d, 0u, f, p1 + 16, ls);
+    bias = BiasPairs(fmaf(-r.slope2, at, -m), r.slope2);
+    tmem_wait_ld(x);
+    tmem_ld32(y, s_tm + 32);
+    chunk_p<false>(x, 0u, f, p0, ls);
+    tmem_wait_ld(y);
+    tmem_ld32(x, s_tm + 64);
+    chunk_p<false>(y, 0u, f, p0 + 16, ls);
+    tmem_wait_ld(x);
+    tmem_st32(s_tm, p0);
+    chunk_p<false>(x, 0u, f, p1, ls);
+    tmem_st32(s_tm + 32, p1);
+    st.l += sum_of(ls);
+    return;
+  }
+  // the scores of columns from `from` away of the row on, either side of it, less m
+  auto exactly = [&](float from, float less) {
+    return [=, &p, &r](int i, uint64_t s2) {
+      float x0, x1;
+      f2_unpack(s2, x0, x1);
+      x0 = fmaf(x0, p.qscale, fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i)), -less));
+      x1 = fmaf(x1, p.qscale, fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i + 1)), -less));
+      return f2_pack(__float_as_uint(x0), __float_as_uint(x1));
+    };
+  };
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    if (h == 0 ? mask.none[0] : mask.none[1]) continue;
+    uint32_t a[32], b[32];
+    load_half(a, b, s_tm + 64 * h);
+    const float from = at - 64.f * h;
+    if (kBias && !bent) {
+      BiasPairs bias(-r.slope2 * from, r.slope2);
+      auto biased = [&](int i, uint64_t s2) { return f2_fma(s2, sc2, bias.next(i)); };
+      chunk_max<true>(a, mask.bits(2 * h), biased, mx);
+      chunk_max<true>(b, mask.bits(2 * h + 1), biased, mx);
+    } else if (kBias) {
+      chunk_max<true>(a, mask.bits(2 * h), exactly(from, 0.f), mx);
+      chunk_max<true>(b, mask.bits(2 * h + 1), exactly(from - 32.f, 0.f), mx);
+    } else {
+      chunk_max<true>(a, mask.bits(2 * h), raw, mx);
+      chunk_max<true>(b, mask.bits(2 * h + 1), raw, mx);
+    }
+  }
+  const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  const float m = take_max(kBias ? tmax : tmax * p.qscale, first, o_tm, st);
+  const uint64_t nm2 = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
+  auto plain = [&](int, uint64_t s2) { return f2_fma(s2, sc2, nm2); };
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+    if (h == 0 ? mask.none[0] : mask.none[1]) {
+      zero_p(pk);
+    } else {
+      uint32_t a[32], b[32];
+      load_half(a, b, s_tm + 64 * h);
+      const float from = at - 64.f * h;
+      if (kBias && !bent) {
+        BiasPairs bias(fmaf(-r.slope2, from, -m), r.slope2);
+        auto biased = [&](int i, uint64_t s2) { return f2_fma(s2, sc2, bias.next(i)); };
+        chunk_p<true>(a, mask.bits(2 * h), biased, pk, ls);
+        chunk_p<true>(b, mask.bits(2 * h + 1), biased, pk + 16, ls);
+      } else if (kBias) {
+        chunk_p<true>(a, mask.bits(2 * h), exactly(from, m), pk, ls);
+        chunk_p<true>(b, mask.bits(2 * h + 1), exactly(from - 32.f, m), pk + 16, ls);
+      } else {
+        chunk_p<true>(a, mask.bits(2 * h), plain, pk, ls);
+        chunk_p<true>(b, mask.bits(2 * h + 1), plain, pk + 16, ls);
+      }
+    }
+    tmem_st32(s_tm + 32 * h, pk);
+  }
+  st.l += sum_of(ls);
+}
+
+// Any score: it is written back over S in the first pass, for the second.
+__device__ __forceinline__ void tile_general(const PrefillParams& p, const ScoredRow& r,
+                                             uint32_t s_tm, uint32_t o_tm, int kt, bool first,
+                                             SoftState& st) {
+  using namespace umma;
+  const TileMask mask = tile_mask(r, kt);
+  float mx[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    if (c < 2 ? mask.none[0] : mask.none[1]) continue;
+    const uint32_t bits = mask.bits(c);
+    uint32_t a[32];
+    tmem_ld32(a, s_tm + 32 * c);
+    tmem_wait_ld(a);
+    const float at = static_cast<float>(r.pos - kt - 32 * c);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      float v = __uint_as_float(a[e]) * p.qscale;
+      if (p.sp.cap2 > 0.f) v = capped_score(p.sp, v);
+      v = fmaf(-r.slope2, fabsf(at - static_cast<float>(e)), v);
+      a[e] = __float_as_uint(v);
+      mx[e & 3] = bit_of(bits, e) ? fmaxf(mx[e & 3], v) : mx[e & 3];
+    }
+    tmem_st32(s_tm + 32 * c, a);
+  }
+  tmem_wait_st();
+  const float m = take_max(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), first, o_tm, st);
+  const uint64_t nm2 = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
+  uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+  auto less_m = [&](int, uint64_t s2) { return f2_add(s2, nm2); };
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+    if (h == 0 ? mask.none[0] : mask.none[1]) {
+      zero_p(pk);
+    } else {
+      uint32_t a[32], b[32];
+      load_half(a, b, s_tm + 64 * h);
+      chunk_p<true>(a, mask.bits(2 * h), less_m, pk, ls);
+      chunk_p<true>(b, mask.bits(2 * h + 1), less_m, pk + 16, ls);
+    }
+    tmem_st32(s_tm + 32 * h, pk);
+  }
+  st.l += sum_of(ls);
+}
+
+// Under the cap, in one pass: the polynomial, or, where a half tile is masked
+// or holds a score out of its range, the exponentials.  Past the range the polynomial
+// keeps rising (falling), so a half tile's sum of P tells: one product above
+// the cap alone makes it p_high or more, and products below -cap, whatever
+// the polynomial gives for them, are lost in a sum of p_low or more (64 of
+// them are under 2^-12 of it).
+__device__ __forceinline__ void tile_capped(const PrefillParams& p, const CappedRegs& k,
+                                            const ScoredRow& r, uint32_t s_tm, int kt,
+                                            SoftState& st) {
+  using namespace umma;
+  const TileMask mask = tile_mask(r, kt);
+  auto poly = [&](int, uint64_t s2) {
     const uint64_t w2 = f2_mul(s2, s2);
-    float w0, w1;
-    f2_unpack(w2, w0, w1);
-    top[c & 1] = fmax3(top[c & 1], w0, w1);
     uint64_t q = f2_fma(w2, k.c[4], k.c[3]);
     q = f2_fma(w2, q, k.c[2]);
     q = f2_fma(w2, q, k.c[1]);
     q = f2_fma(w2, q, k.c[0]);
-    float x0, x1;
-    f2_unpack(f2_fma(s2, q, k.neg_m2), x0, x1);
-    float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-    if (kMasked) {
-      const uint32_t bits = c < 16 ? lo : hi;
-      e0 = (bits >> ((2 * c) & 31)) & 1u ? e0 : 0.f;
-      e1 = (bits >> ((2 * c + 1) & 31)) & 1u ? e1 : 0.f;
+    return f2_fma(s2, q, k.neg_m2);
+  };
+  auto in_range = [&](float sum) { return sum >= p.cap.p_low && sum <= p.cap.p_high; };
+  bool done[2] = {false, false};
+  float sum1 = 0.f;
+  uint32_t p1[32];
+  if (mask.whole) {
+    uint32_t x[32], y[32], p0[32];
+    uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+    load_half(x, y, s_tm);
+    chunk_p<false>(x, 0u, poly, p0, ls);
+    chunk_p<false>(y, 0u, poly, p0 + 16, ls);
+    const float sum0 = sum_of(ls);
+    done[0] = __all_sync(kFull, in_range(sum0));
+    if (done[0]) {
+      tmem_st32(s_tm, p0);
+      st.l += sum0;
     }
-    ls2[c & 1] = f2_add(ls2[c & 1], f2_pack(__float_as_uint(e0), __float_as_uint(e1)));
-    pk[c] = pack_bf16x2(e0, e1);
-  }
-  if (__any_sync(kFull, fmaxf(top[0], top[1]) > k.w_max)) {
-    const uint32_t all = 0xffffffffu;
-    return masked_half(s_tm, h, kMasked ? lo : all, kMasked ? hi : all, [&](float s) {
-      return fmaf(k.neg_2cap, fast_rcp(1.f + fast_exp2(s * k.exp_k)), k.cap_m);
-    });
-  }
-  tmem_st32(s_tm + 32 * h, pk);
-  float l0, l1;
-  f2_unpack(f2_add(ls2[0], ls2[1]), l0, l1);
-  return l0 + l1;
-}
-
-// One key tile: kt is its first column counted from the item's first key.
-template <int kMode>
-__device__ __forceinline__ void scored_tile(const ScoredConsts& k, const ScoredRow& r,
-                                            uint32_t s_tm, uint32_t o_tm, int kt, bool first,
-                                            float& m_used, float& l) {
-  using namespace umma;
-  // columns of this tile the row sees (kt is far below 2^31 where hi is not)
-  const int c0 = r.lo > kt ? (r.lo - kt > 128 ? 128 : r.lo - kt) : 0;
-  const int c1 = r.hi < kt ? -1 : (r.hi - kt > 127 ? 127 : r.hi - kt);
-  const bool masked = __any_sync(kFull, c0 > 0 || c1 < 127);
-  const float sc = k.sc;
-
-  if (kMode == kPrefillCapped) {
-    if (!masked) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) l += capped_half<false>(k, s_tm, h, 0u, 0u);
-    } else {
+    for (int i = 0; i < 4; ++i) ls[i] = 0ull;
+    load_half(x, y, s_tm + 64);
+    chunk_p<false>(x, 0u, poly, p1, ls);
+    chunk_p<false>(y, 0u, poly, p1 + 16, ls);
+    sum1 = sum_of(ls);
+    done[1] = __all_sync(kFull, in_range(sum1));
+  }
+  if (!done[0] || !done[1]) {
+    auto far = [&](int, uint64_t s2) {
+      float x0, x1;
+      f2_unpack(s2, x0, x1);
+      x0 = fmaf(p.cap.neg_2cap, fast_rcp(1.f + fast_exp2(x0 * p.cap.exp_k)), p.cap.cap_m);
+      x1 = fmaf(p.cap.neg_2cap, fast_rcp(1.f + fast_exp2(x1 * p.cap.exp_k)), p.cap.cap_m);
+      return f2_pack(__float_as_uint(x0), __float_as_uint(x1));
+    };
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = span_bits(c0, c1, 2 * h), hi = span_bits(c0, c1, 2 * h + 1);
-        if (!__any_sync(kFull, (lo | hi) != 0u)) zero_half(s_tm, h);
-        else l += capped_half<true>(k, s_tm, h, lo, hi);
-      }
-    }
-    return;
-  }
-
-  if (kMode == kPrefillMasked && !masked && sc >= 0.f) {
-    // (a negative scale: the maximum of the scaled scores is not the scaled maximum)
-    float mx[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) mx[u] = -INFINITY;
-#pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t a[32], b[32];
-      tmem_ld32(a, s_tm + 64 * h);
-      tmem_ld32(b, s_tm + 64 * h + 32);
-      tmem_wait_ld(a);
-      tmem_ready(b);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        mx[c & 3] = fmax3(mx[c & 3], __uint_as_float(a[2 * c]), __uint_as_float(a[2 * c + 1]));
-        mx[(c + 2) & 3] =
-            fmax3(mx[(c + 2) & 3], __uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1]));
-      }
-    }
-    const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-    const float m = take_max(tmax, first, o_tm, m_used, l);
-    const uint64_t sc2 = f2_pack(__float_as_uint(sc), __float_as_uint(sc));
-    const uint64_t nm2 = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
-    uint64_t ls2[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) ls2[u] = 0ull;  // (+0, +0)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t a[32], b[32], pk[32];
-      tmem_ld32(a, s_tm + 64 * h);
-      tmem_ld32(b, s_tm + 64 * h + 32);
-      tmem_wait_ld(a);
-      tmem_ready(b);
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const uint64_t s2 =
-            c < 16 ? f2_pack(a[2 * c], a[2 * c + 1]) : f2_pack(b[2 * c - 32], b[2 * c - 31]);
-        float x0, x1;
-        f2_unpack(f2_fma(s2, sc2, nm2), x0, x1);
-        const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-        ls2[c & 3] = f2_add(ls2[c & 3], f2_pack(__float_as_uint(e0), __float_as_uint(e1)));
-        pk[c] = pack_bf16x2(e0, e1);
+      if (h == 0 ? done[0] : done[1]) continue;
+      uint32_t pk[32];
+      if (h == 0 ? mask.none[0] : mask.none[1]) {
+        zero_p(pk);
+      } else {
+        uint32_t a[32], b[32];
+        load_half(a, b, s_tm + 64 * h);
+        uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+        chunk_p<true>(a, mask.bits(2 * h), far, pk, ls);
+        chunk_p<true>(b, mask.bits(2 * h + 1), far, pk + 16, ls);
+        st.l += sum_of(ls);
       }
       tmem_st32(s_tm + 32 * h, pk);
     }
-    float l0, l1, l2, l3;
-    f2_unpack(f2_add(ls2[0], ls2[1]), l0, l1);
-    f2_unpack(f2_add(ls2[2], ls2[3]), l2, l3);
-    l += (l0 + l2) + (l1 + l3);
-    return;
   }
-
-  // Any score, any mask.  Pass 1: the row's maximum; where a score costs more
-  // than a product it is written back over S for pass 2.
-  constexpr bool kStore = kMode == kPrefillGeneral;
-  float mx[4];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) mx[u] = -INFINITY;
-  const float posf = static_cast<float>(r.pos - kt);
-#pragma unroll 1
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t bits = span_bits(c0, c1, w);
-    if (!__any_sync(kFull, bits != 0u)) continue;
-    uint32_t a[32];
-    tmem_ld32(a, s_tm + 32 * w);
-    tmem_wait_ld(a);
-    const float at = posf - static_cast<float>(32 * w);
-#pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      float x = __uint_as_float(a[c]) * sc;
-      if (kStore) {
-        if (k.sp.cap2 > 0.f) x = capped_score(k.sp, x);
-        x = fmaf(-r.slope2, fabsf(at - static_cast<float>(c)), x);
-        a[c] = __float_as_uint(x);
-      }
-      mx[c & 3] = (bits >> c) & 1u ? fmaxf(mx[c & 3], x) : mx[c & 3];
-    }
-    if (kStore) tmem_st32(s_tm + 32 * w, a);
-  }
-  if (kStore) tmem_wait_st();
-  const float m = take_max(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), first, o_tm, m_used, l);
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t lo = span_bits(c0, c1, 2 * h), hi = span_bits(c0, c1, 2 * h + 1);
-    if (!__any_sync(kFull, (lo | hi) != 0u)) zero_half(s_tm, h);
-    else
-      l += masked_half(s_tm, h, lo, hi,
-                       [&](float s) { return kStore ? s - m : fmaf(s, sc, -m); });
+  if (done[1]) {  // (over S of the first half, which is read by now)
+    tmem_st32(s_tm + 32, p1);
+    st.l += sum1;
   }
 }
 
-// Whether all 128 elements of this thread's row of O are finite.
-__device__ __forceinline__ bool finite_row(uint32_t o_tm) {
-  using namespace umma;
-  float z = 0.f;  // 0 x is 0 for a finite x, else NaN
-#pragma unroll 1
-  for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
-    uint32_t w[32];
-    tmem_ld32(w, o_tm + c0);
-    tmem_wait_ld(w);
+// One key tile: kt is its first key counted from the item's.
+template <int kMode>
+__device__ __forceinline__ void scored_tile(const PrefillParams& p, const CappedRegs& k, const ScoredRow& r,
+                                            uint32_t s_tm, uint32_t o_tm, int kt, bool first,
+                                            SoftState& st) {
+  if constexpr (kMode == kPrefillCapped) tile_capped(p, k, r, s_tm, kt, st);
+  else if constexpr (kMode == kPrefillGeneral) tile_general(p, r, s_tm, o_tm, kt, first, st);
+  else tile_running_max<kMode>(p, r, s_tm, o_tm, kt, first, st);
+}
+
+// Adds 0 where all 32 values are finite, NaN where one is not.
+__device__ __forceinline__ void add_finite(uint64_t& z, const uint32_t (&w)[32]) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) z = fmaf(__uint_as_float(w[c]), 0.f, z);
+  for (int c = 0; c < 16; ++c) z = umma::f2_fma(umma::f2_pack(w[2 * c], w[2 * c + 1]), 0ull, z);
+}
+
+__device__ __forceinline__ bool is_zero(uint64_t z) {
+  float z0, z1;
+  umma::f2_unpack(z, z0, z1);
+  return z0 == 0.f && z1 == 0.f;
+}
+
+// 64 columns of a row, times inv, as bf16: chunk c (0..7) of 16 bytes.
+__device__ __forceinline__ uint4 out_chunk(const uint32_t (&a)[32], const uint32_t (&b)[32],
+                                           float inv, int c) {
+  const uint32_t* x = c < 4 ? a + 8 * c : b + 8 * (c - 4);
+  return make_uint4(pack_bf16x2(__uint_as_float(x[0]) * inv, __uint_as_float(x[1]) * inv),
+                    pack_bf16x2(__uint_as_float(x[2]) * inv, __uint_as_float(x[3]) * inv),
+                    pack_bf16x2(__uint_as_float(x[4]) * inv, __uint_as_float(x[5]) * inv),
+                    pack_bf16x2(__uint_as_float(x[6]) * inv, __uint_as_float(x[7]) * inv));
+}
+
+// Column half h of the warp's 32 rows (row = lane) through its 4 KiB of
+// staging, 128-byte swizzled, and one tensor store.
+__device__ __forceinline__ void store_half_tma(const CUtensorMap* tmo, unsigned char* stg, int lane,
+                                               float inv, const uint32_t (&a)[32],
+                                               const uint32_t (&b)[32], int h, int head0,
+                                               int tok0) {
+  using namespace umma;
+  if (lane == 0) bulk_wait_read();  // the warp's last store has read the staging
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = out_chunk(a, b, inv, c);
+  fence_proxy_async_smem();  // the tensor store reads the staging through the async proxy
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_4d_at(tmo, stg, 0, h, head0, tok0);
+    bulk_commit();
   }
-  return z == 0.f;
+}
+
+// 64 columns of one row by plain stores; v8: dst is 32-byte aligned, whole
+// 32-byte sectors.
+__device__ __forceinline__ void store_half(uint4* dst, float inv, const uint32_t (&a)[32],
+                                           const uint32_t (&b)[32], bool v8) {
+#pragma unroll
+  for (int c = 0; c < 8; c += 2) {
+    const uint4 x = out_chunk(a, b, inv, c), y = out_chunk(a, b, inv, c + 1);
+    if (v8) {
+      umma::st_global_v8(dst + c, x, y);
+    } else {
+      dst[c] = x;
+      dst[c + 1] = y;
+    }
+  }
 }
 
 // Computes and writes the rows flagged in the warp, one by one.
-static __device__ __noinline__ void repair_rows(const PrefillParams& p, const KvRows& kv, bool flagged,
-                                         int64_t qrow, const ScoredRow& r, int k0, int lane) {
+static __device__ __noinline__ void repair_rows(const PrefillParams& p, const KvRows& kv,
+                                                bool flagged, const ScoredRow& r, int k0,
+                                                int lane) {
   for (uint32_t left = __ballot_sync(umma::kFull, flagged); left != 0u; left &= left - 1) {
     const int src = __ffs(left) - 1;
-    const int64_t row = __shfl_sync(umma::kFull, qrow, src);
+    const int64_t row = __shfl_sync(umma::kFull, r.qrow, src);
     const int lo = __shfl_sync(umma::kFull, r.lo, src), hi = __shfl_sync(umma::kFull, r.hi, src);
     const int pos = __shfl_sync(umma::kFull, r.pos, src);
     const float slope2 = __shfl_sync(umma::kFull, r.slope2, src);
+    const bool none = lo > hi;
     float o[16];
-    attend_row(p.sp, kv, p.q + row * kHeadDim, p.qscale, slope2, pos + k0, hi < 0 ? 0 : lo + k0,
-               hi < 0 ? -1 : hi + k0, lane, o);
+    attend_row(p.sp, kv, p.q + row * kHeadDim, p.qscale, slope2, pos + k0, none ? 0 : lo + k0,
+               none ? -1 : hi + k0, lane, o);
     if (lane < 8) {
 #pragma unroll
       for (int c = 0; c < 2; ++c)

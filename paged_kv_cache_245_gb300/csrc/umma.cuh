@@ -159,6 +159,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {  // of the absolute values
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Wait for phase `parity` of `bar`; give up when another role has given up
 // (*abort) or after kWaitLimitNs (then set *abort and record the timeout).
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity,

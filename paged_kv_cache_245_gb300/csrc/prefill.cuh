@@ -14,6 +14,7 @@ namespace pkv {
 struct CappedScore {
   uint64_t c[5];    // the polynomial in the raw product's square
   uint64_t neg_m2;  // -m
+  float s_max;      // raw products up to this are in the polynomial's range
   float p_low, p_high;  // sums of P of a half tile whose products are in the polynomial's range
   float exp_k, neg_2cap, cap_m;  // 2^(exp_k s) = e^(2y); -2 cap; cap - m
 };

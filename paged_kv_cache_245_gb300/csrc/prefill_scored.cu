@@ -673,22 +673,26 @@ uint64_t pair_of(float x) {
   return (static_cast<uint64_t>(b) << 32) | b;
 }
 
-// Whether the capped kernel serves these scores: a cap whose range fits the
-// fixed offset, no bias, and a raw product at the cap (cap / scale) whose
-// eighth power neither overflows nor underflows in fp32.  Its constants.
-bool capped_score(const PrefillParams& p, CappedScore* c) {
+// The polynomial of a cap, where a raw product at the cap (cap / scale) has an
+// eighth power that neither overflows nor underflows in fp32 (else s_max is
+// negative: no product is in range).  Returns whether the capped kernel serves these
+// scores: no bias, and a cap whose range fits the fixed offset.
+bool capped_constants(const PrefillParams& p, CappedScore* c) {
   const ScoreParams& sp = p.sp;
-  if (!(sp.cap2 > 0.f) || sp.cap2 > 75.f || sp.slopes != nullptr) return false;
+  std::memset(c, 0, sizeof *c);
+  if (!(sp.cap2 > 0.f)) return false;
   const float r = p.qscale * sp.inv_cap2;  // a raw product's share of the cap
-  if (!(std::fabs(r) >= 1.220703125e-4f && std::fabs(r) <= 8192.f)) return false;  // 2^-13 .. 2^13
-  // the offset m: the lowest score (-cap) keeps 2^-100
-  const float m = sp.cap2 <= 50.f ? sp.cap2 : 100.f - sp.cap2;
+  const bool poly = std::fabs(r) >= 1.220703125e-4f && std::fabs(r) <= 8192.f;  // 2^-13 .. 2^13
   const float fit[5] = {0.99999309f, -0.33298065f, 0.13036811f, -0.04481755f, 0.00903642f};
   float power = p.qscale;
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; poly && i < 5; ++i) {
     c->c[i] = pair_of(fit[i] * power);
     power *= r * r;
   }
+  c->s_max = poly ? std::fabs(1.f / r) : -1.f;
+  if (!poly || sp.cap2 > 75.f || sp.slopes != nullptr) return false;
+  // the offset m: the lowest score (-cap) keeps 2^-100
+  const float m = sp.cap2 <= 50.f ? sp.cap2 : 100.f - sp.cap2;
   c->neg_m2 = pair_of(-m);
   // P at +cap; 2^18 (64 scores, 2^-12) times P at -cap
   const float edge = 0.76159416f * sp.cap2;  // tanh(1)
@@ -710,7 +714,7 @@ cudaError_t launch_prefill_scored(const CUtensorMap& tk, const CUtensorMap& tv,
   if (p.sp.cap2 == 0.f && p.qscale >= 0.f)
     return p.sp.slopes == nullptr ? launch_mode<kPrefillMasked>(tk, tv, tq, to, p, stream)
                                   : launch_mode<kPrefillBiased>(tk, tv, tq, to, p, stream);
-  if (capped_score(p, &p.cap))
+  if (capped_constants(p, &p.cap))
     return launch_mode<kPrefillCapped>(tk, tv, tq, to, p, stream);
   return launch_mode<kPrefillGeneral>(tk, tv, tq, to, p, stream);
 }

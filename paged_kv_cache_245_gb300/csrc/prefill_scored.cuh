@@ -60,7 +60,7 @@ struct CappedRegs {
 template <int kMode>
 __device__ __forceinline__ CappedRegs capped_regs(const PrefillParams& p) {
   CappedRegs k;
-  if (kMode == kPrefillCapped) {
+  if (kMode == kPrefillCapped || kMode == kPrefillGeneral) {
 #pragma unroll
     for (int i = 0; i < 5; ++i) asm volatile("mov.b64 %0, %1;" : "=l"(k.c[i]) : "l"(p.cap.c[i]));
     asm volatile("mov.b64 %0, %1;" : "=l"(k.neg_m2) : "l"(p.cap.neg_m2));
@@ -355,12 +355,14 @@ __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const S
   st.l += sum_of(ls);
 }
 
-// Any score: it is written back over S in the first pass, for the second.
-__device__ __forceinline__ void tile_general(const PrefillParams& p, const ScoredRow& r,
-                                             uint32_t s_tm, uint32_t o_tm, int kt, bool first,
-                                             SoftState& st) {
+// Any score: it is written back over S in the first pass, for the second.  A
+// chunk whose products are all within the cap takes the polynomial.
+__device__ __forceinline__ void tile_general(const PrefillParams& p, const CappedRegs& k,
+                                             const ScoredRow& r, uint32_t s_tm, uint32_t o_tm,
+                                             int kt, bool first, SoftState& st) {
   using namespace umma;
   const TileMask mask = tile_mask(r, kt);
+  const uint64_t sc2 = f2_pack(__float_as_uint(p.qscale), __float_as_uint(p.qscale));
   float mx[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
@@ -371,12 +373,33 @@ __device__ __forceinline__ void tile_general(const PrefillParams& p, const Score
     uint32_t a[32];
     tmem_ld32(a, s_tm + 32 * c);
     tmem_wait_ld(a);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      top = fmax3_abs(top, __uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+    if (p.sp.cap2 > 0.f && !__all_sync(kFull, top <= p.cap.s_max)) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        a[e] = __float_as_uint(capped_score(p.sp, __uint_as_float(a[e]) * p.qscale));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint64_t s2 = f2_pack(a[2 * i], a[2 * i + 1]);
+        const uint64_t w2 = f2_mul(s2, s2);
+        uint64_t q = f2_fma(w2, k.c[4], k.c[3]);
+        q = f2_fma(w2, q, k.c[2]);
+        q = f2_fma(w2, q, k.c[1]);
+        q = f2_fma(w2, q, k.c[0]);
+        float x0, x1;
+        f2_unpack(p.sp.cap2 > 0.f ? f2_mul(s2, q) : f2_mul(s2, sc2), x0, x1);
+        a[2 * i] = __float_as_uint(x0);
+        a[2 * i + 1] = __float_as_uint(x1);
+      }
+    }
     const float at = static_cast<float>(r.pos - kt - 32 * c);
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-      float v = __uint_as_float(a[e]) * p.qscale;
-      if (p.sp.cap2 > 0.f) v = capped_score(p.sp, v);
-      v = fmaf(-r.slope2, fabsf(at - static_cast<float>(e)), v);
+      const float v = fmaf(-r.slope2, fabsf(at - static_cast<float>(e)), __uint_as_float(a[e]));
       a[e] = __float_as_uint(v);
       mx[e & 3] = bit_of(bits, e) ? fmaxf(mx[e & 3], v) : mx[e & 3];
     }
@@ -483,7 +506,7 @@ __device__ __forceinline__ void scored_tile(const PrefillParams& p, const Capped
                                             uint32_t s_tm, uint32_t o_tm, int kt, bool first,
                                             SoftState& st) {
   if constexpr (kMode == kPrefillCapped) tile_capped(p, k, r, s_tm, kt, st);
-  else if constexpr (kMode == kPrefillGeneral) tile_general(p, r, s_tm, o_tm, kt, first, st);
+  else if constexpr (kMode == kPrefillGeneral) tile_general(p, k, r, s_tm, o_tm, kt, first, st);
   else tile_running_max<kMode>(p, r, s_tm, o_tm, kt, first, st);
 }
 

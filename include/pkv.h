@@ -527,7 +527,10 @@ PKV_API pkv_status pkv_paged_decode_attention_noalloc(
  * split (CUDA-core) kernel, 2 / 3 the tensor-core kernel with 8 warps x 3
  * stages / 12 warps x 2 stages per CTA (the automatic choice uses 12 x 2;
  * PKV_ERR_UNSUPPORTED where the kernel does not apply).  Meant for tests and
- * tuning; every kernel computes the same result.
+ * tuning; every kernel computes the same result.  For the scored calls 2 and 3
+ * are their two tensor-core kernels: tiles dealt to warps in contiguous runs
+ * (the automatic choice up to 1024 visible positions a sequence), or pair by
+ * pair.
  */
 PKV_API void pkv_set_decode_variant(int variant);
 PKV_API int pkv_get_decode_variant(void);

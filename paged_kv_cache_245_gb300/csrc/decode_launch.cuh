@@ -31,12 +31,15 @@ cudaError_t launch_decode_group(const DecodeParams& p, cudaStream_t stream) {
   auto kernel = decode_attention_kernel<G, kContig, kDecodeStages, kScored>;
   cudaError_t e = ensure_smem_limit(kernel, L::kTotal, &done_mask);
   if (e != cudaSuccess) return e;
+  // the scored kernels are programmatic dependents (both wait before they
+  // read anything): small calls, where a launch's latency counts
+  const bool pdl = kScored ? pdl_decode_enabled() : pdl_enabled();
   const dim3 grid(p.nsplit, p.Hkv, p.num_seqs);
-  e = launch_pdl(kernel, grid, dim3(kDecodeThreads), L::kTotal, stream, p);
+  e = launch_pdl_if(pdl, kernel, grid, dim3(kDecodeThreads), L::kTotal, stream, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.Hq;
-  return launch_pdl(decode_combine_kernel<kContig, kScored>, dim3(static_cast<unsigned>((rows + 3) / 4)),
-                    dim3(128), 0, stream, p);
+  return launch_pdl_if(pdl, decode_combine_kernel<kContig, kScored>,
+                       dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, p);
 }
 
 template <bool kContig, bool kScored = false>

@@ -112,7 +112,9 @@ TcStatus launch_decode_tc(const TcParams& p_in, bool contig, const void* k, cons
 #define PKV_TC_PICK(C, F)                                                             \
   (mh == 8 ? PKV_TC_LAUNCH(C, 10, 2, F, 8)                                            \
            : (cfg == 0 ? PKV_TC_LAUNCH(C, 8, 3, F, 4) : PKV_TC_LAUNCH(C, 12, 2, F, 4)))
-  if (p.scored) {
+  if (p.scored == 2) {
+    e = launch_decode_runs(tk, tv, p, contig, num_ctas, stream);
+  } else if (p.scored) {
     e = launch_decode_tc_scored(tk, tv, p, contig, mh == 8, num_ctas, stream);
   } else if (p.G > kTcHeads) {  // one n-tile of 8 query heads per KV head (the API allows G <= 8)
     e = cudaErrorInvalidValue;

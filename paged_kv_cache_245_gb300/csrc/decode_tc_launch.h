@@ -46,7 +46,8 @@ struct TcParams {
   uint16_t* v_cache;
   int64_t num_slots;        // checked mode: slots in [0, num_slots)
   int* err;
-  int32_t scored;           // 1: scores are capped, biased and masked as sp says
+  int32_t scored;           // scores are capped, biased and masked as sp says: 1 by pairs
+                            // (decode_tc.cuh), 2 by warp runs (decode_runs.cu)
   ScoreParams sp;
 };
 
@@ -179,6 +180,9 @@ uint32_t next_launch_tag();
 cudaError_t launch_decode_tc_scored(const CUtensorMap& tk, const CUtensorMap& tv,
                                     const TcParams& p, bool contig, bool eight_heads,
                                     int num_ctas, cudaStream_t stream);
+// The same for short visible spans (decode_runs.cu).
+cudaError_t launch_decode_runs(const CUtensorMap& tk, const CUtensorMap& tv, const TcParams& p,
+                               bool contig, int num_ctas, cudaStream_t stream);
 
 // cfg 0: 8 warps x 3 stages per CTA; cfg 1: 12 warps x 2 stages; cfg 2:
 // 10 warps x 2 stages with one merge pass for groups of 5..8 query heads

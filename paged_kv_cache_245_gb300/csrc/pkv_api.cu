@@ -175,6 +175,17 @@ bool tc_enough_tiles(int32_t num_seqs, const pkv_heads& h, int32_t max_context, 
   return tile_bound >= 8LL * tc_ctas(sms);
 }
 
+// Scored decode on the tensor cores: by warp runs (decode_runs.cu) where a
+// sequence sees few positions and there is a (sequence, KV head) pair for every
+// SM, else pair by pair (decode_tc.cuh).  64 sequences x 8 KV heads cross
+// between 512 and 1024 positions where each sees that many (1.03 and 0.94 of
+// the other's rate); ragged ones still gain at the bound (1.14).  8 sequences
+// x 8 heads (pairs cut across CTAs) of 512 run at 0.82, 16 at 0.97.
+constexpr int32_t kRunsMaxSpan = 1024 + 15;
+bool tc_by_runs(int32_t num_seqs, const pkv_heads& h, int32_t span, int sms) {
+  return span <= kRunsMaxSpan && static_cast<int64_t>(num_seqs) * h.num_kv_heads >= tc_ctas(sms);
+}
+
 // Positions that a window lets a sequence attend, counted from the start of
 // the 16-token tile that holds the first (a bound on every sequence).
 int32_t visible_span(int32_t max_context, int32_t window) {
@@ -292,7 +303,7 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
     }
     t.err = err;
     if (score != nullptr) {
-      t.scored = 1;
+      t.scored = variant == 2 || (variant == 0 && tc_by_runs(num_seqs, h, span, sms)) ? 2 : 1;
       t.sp = *score;
     }
     cudaError_t ce = cudaSuccess;

@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
 D = 128
 SCALE = D ** -0.5
-AUTO, SPLIT, TC = pkv.VARIANT_AUTO, pkv.VARIANT_SPLIT, pkv.VARIANT_TC_12X2
+AUTO, SPLIT, RUNS, TC = (pkv.VARIANT_AUTO, pkv.VARIANT_SPLIT, pkv.VARIANT_TC_8X3,
+                         pkv.VARIANT_TC_12X2)
 
 
 @pytest.fixture(autouse=True)
@@ -89,7 +90,7 @@ def both(kw):
 
 
 @pytest.mark.parametrize("name", list(SCORES))
-@pytest.mark.parametrize("variant", [SPLIT, TC])
+@pytest.mark.parametrize("variant", [SPLIT, RUNS, TC])
 @pytest.mark.parametrize("contig", [False, True])
 def test_scores(name, variant, contig):
     s = Sequences(CTX, 8, 16, contig, seed=3)
@@ -106,12 +107,12 @@ def test_groups_and_block_sizes(hq, hkv, bs):
     q = queries(s, hq)
     ref, kw = both(make("all", s, hq))
     want = reference(s, q, **ref)
-    for variant in (SPLIT, TC) if bs % 16 == 0 else (AUTO, SPLIT):
+    for variant in (SPLIT, RUNS, TC) if bs % 16 == 0 else (AUTO, SPLIT):
         pkv.set_decode_variant(variant)
         assert_close(call(s, q, **kw), *want, what="variant %d" % variant)
 
 
-@pytest.mark.parametrize("variant", [AUTO, SPLIT, TC])
+@pytest.mark.parametrize("variant", [AUTO, SPLIT, RUNS, TC])
 @pytest.mark.parametrize("window", [0, 1000])
 def test_long_ragged_batch(variant, window):
     s = Sequences([8000, 1, 5000, 77, 1000, 1001, 3001, 999] * 3, 8, 16, seed=9)
@@ -119,6 +120,20 @@ def test_long_ragged_batch(variant, window):
     pkv.set_decode_variant(variant)
     got = call(s, q, softcap=50.0, window=window)
     assert_close(got, *reference(s, q, softcap=50.0, window=window))
+
+
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (56, 8), (4, 1)])
+@pytest.mark.parametrize("variant", [RUNS, TC])
+def test_batches_larger_and_smaller_than_the_grid(variant, hq, hkv):
+    """Hundreds of short sequences (several pairs a warp), a few long ones
+    (several CTAs a pair), more sequences than one launch takes."""
+    g = torch.Generator().manual_seed(4)
+    pkv.set_decode_variant(variant)
+    for ctx in ([int(x) for x in torch.randint(0, 60, (700,), generator=g)], [20000, 3],
+                [0] * 40 + [5000] + [0] * 40, [16] * 300):
+        s = Sequences(ctx, hkv, 16, seed=len(ctx))
+        q = queries(s, hq)
+        assert_close(call(s, q, softcap=30.0), *reference(s, q, softcap=30.0))
 
 
 @pytest.mark.parametrize("chunk", [4, 8])
@@ -137,14 +152,14 @@ def test_split_lengths(chunk):
 def test_saturating_scores(by, scale):
     s = Sequences([300, 20, 1], 2, 16, seed=11)
     q = queries(s, 8, by=by)
-    for variant in (SPLIT, TC):
+    for variant in (SPLIT, RUNS, TC):
         pkv.set_decode_variant(variant)
         for cap in (0.0, 5.0, 50.0):
             assert_close(call(s, q, scale=scale, softcap=cap),
                          *reference(s, q, softcap=cap, scale=scale), what="cap %g" % cap)
 
 
-@pytest.mark.parametrize("variant", [SPLIT, TC])
+@pytest.mark.parametrize("variant", [SPLIT, RUNS, TC])
 @pytest.mark.parametrize("contig,bs", [(False, 16), (False, 48), (True, 16)])
 def test_nothing_in_masked_places_matters(variant, contig, bs):
     s = Sequences(CTX, 2, bs, contig, seed=12)
@@ -156,7 +171,7 @@ def test_nothing_in_masked_places_matters(variant, contig, bs):
         assert_close(call(s, q, k=k, v=v, **kw), *reference(s, q, **ref), what=name)
 
 
-@pytest.mark.parametrize("variant", [SPLIT, TC])
+@pytest.mark.parametrize("variant", [SPLIT, RUNS, TC])
 def test_blocks_before_the_window_are_never_read(variant):
     """Checked mode rejects every table entry the kernel reads that is no
     block: freed entries before the window are not among them."""
@@ -180,7 +195,7 @@ def test_a_negative_slope_and_a_steep_one():
     s = Sequences([400, 3, 90], 2, 16, seed=14)
     q = queries(s, 8)
     slopes = torch.tensor([-0.3, 0.0, 1e6, 40.0, 1e30, 2.0 ** -20, 3.0, -0.01], device=DEV)
-    for variant in (SPLIT, TC):
+    for variant in (SPLIT, RUNS, TC):
         pkv.set_decode_variant(variant)
         assert_close(call(s, q, alibi_slopes=slopes), *reference(s, q, slopes=slopes))
 
@@ -188,7 +203,7 @@ def test_a_negative_slope_and_a_steep_one():
 def test_null_score_is_the_plain_call():
     s = Sequences(CTX, 8, 16, seed=15)
     q = queries(s, 32)
-    for variant in (SPLIT, TC):
+    for variant in (SPLIT, RUNS, TC):
         pkv.set_decode_variant(variant)
         plain = pkv.paged_decode_attention(q, s.k, s.v, s.where, s.ctx_t, max(s.ctx), SCALE)
         assert_close(call(s, q), plain.double(), 2.0 ** -7 * plain.double().abs() + 2.0 ** -7)
@@ -203,7 +218,7 @@ def test_cache_beyond_32_bit_offsets():
     k[nb - s.nb:], v[nb - s.nb:] = s.k, s.v
     q = queries(s, 32)
     want = reference(s, q, softcap=30.0, window=200)
-    for variant in (SPLIT, TC):
+    for variant in (SPLIT, RUNS, TC):
         pkv.set_decode_variant(variant)
         got = pkv.paged_decode_attention_scored(q, k, v, s.where + (nb - s.nb), s.ctx_t, 300, SCALE,
                                                 softcap=30.0, window=200)
@@ -221,7 +236,9 @@ def test_cache_beyond_32_bit_offsets():
     assert_close(got, *reference(c, q, window=77))
 
 
-def test_graph_streams_and_shared_workspace():
+@pytest.mark.parametrize("variant", [RUNS, TC])
+def test_graph_streams_and_shared_workspace(variant):
+    pkv.set_decode_variant(variant)
     s = Sequences([900, 31, 400, 65] * 8, 8, 16, seed=18)
     q = queries(s, 32)
     size = pkv.scored_decode_workspace_size(len(s.ctx), 32, 8, 900, 300)

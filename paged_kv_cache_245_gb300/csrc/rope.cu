@@ -13,7 +13,13 @@
 // each way); the 64 sines and cosines of a token are computed once and serve
 // all its heads from shared memory.  A row takes 8 lanes of two 16-byte
 // chunks; in the half layout a lane's two chunks are partners (chunk c and
-// c + rotary_dim / 16), so that no lane needs another's elements.
+// c + rotary_dim / 16), so that no lane needs another's elements.  A row is
+// loaded while the one before it is turned, the first while the sines are
+// computed; five CTAs an SM keep 80 KiB of rows in flight (three, with the
+// registers left alone: 5.4 for 4.2 us at 333 tokens of an odd rotary size).
+// 16384 tokens of 32 + 2 x 8 heads (403 MB) take 65.8 us, 6.1 TB/s or 0.90 of a
+// plain copy; 64 tokens 3.1 us and one 2.7 us, a launch and three dependent
+// reads (position, sines, row).
 #include "rope.cuh"
 
 #include "pkv_device.cuh"
@@ -45,7 +51,7 @@ struct RopeRow {
 // multiple of 16 (whole chunks are partners); 2: half layout, any even
 // rotary_dim (partners from shared memory, one by one).
 template <int kKind, int kTokens>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const RopeParams p) {
   __shared__ float2 cs[kTokens][64];   // (cos, sin) times gain of the rotated pairs
   __shared__ uint32_t rows[kKind == 2 ? kRowsPerPass : 1][66];  // a row of every 8 lanes
   __shared__ int64_t row0[kTokens];    // cache row of KV head 0, or -1: k and v go nowhere
@@ -198,15 +204,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
 template <int kKind>
 cudaError_t launch_kind(const RopeParams& p, cudaStream_t stream) {
   const int R = p.Hq + 2 * p.Hkv;
-  if (p.num_tokens <= 512) {
-    // few tokens: one a CTA, its rows over grid y, so that every row of the
-    // call is in flight at once
-    const dim3 grid(static_cast<unsigned>(p.num_tokens), (R + kRowsPerPass - 1) / kRowsPerPass);
-    return launch_pdl(rope_append_kernel<kKind, 1>, grid, dim3(kRopeThreads), 0, stream, p);
-  }
-  constexpr int kTokens = 4;
-  const dim3 grid(static_cast<unsigned>((p.num_tokens + kTokens - 1) / kTokens), 1);
-  return launch_pdl(rope_append_kernel<kKind, kTokens>, grid, dim3(kRopeThreads), 0, stream, p);
+  const unsigned n = static_cast<unsigned>(p.num_tokens);
+  const dim3 block(kRopeThreads);
+  // Few tokens: one a CTA, its rows over grid y, so that every row of the call
+  // is in flight at once (400 tokens x 48 rows 4.3 us, two a CTA 5.0).  Past
+  // that a CTA passes over the rows of more tokens: two up to 1024 (700 tokens
+  // 5.9 us, four a CTA 7.1), then four (4096 tokens 20.1 us, eight 19.7; 1024
+  // 7.0, eight 9.2).
+  if (n <= 512)
+    return launch_pdl(rope_append_kernel<kKind, 1>, dim3(n, (R + kRowsPerPass - 1) / kRowsPerPass),
+                      block, 0, stream, p);
+  if (n <= 1024)
+    return launch_pdl(rope_append_kernel<kKind, 2>, dim3((n + 1) / 2), block, 0, stream, p);
+  return launch_pdl(rope_append_kernel<kKind, 4>, dim3(n / 4 + (n % 4 != 0)), block, 0, stream, p);
 }
 
 }  // namespace

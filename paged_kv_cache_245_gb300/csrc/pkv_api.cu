@@ -981,6 +981,7 @@ pkv_status prefill_common(const void* q, const int32_t* cu_seqlens_q, int32_t nu
     p.k = static_cast<const uint16_t*>(k_cache);
     p.v = static_cast<const uint16_t*>(v_cache);
     p.sp = *score;
+    p.num_tokens = static_cast<int32_t>(num_tokens);
     p.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
     e = pkv::launch_prefill_scored(tk, tv, tq, to, p, static_cast<cudaStream_t>(stream));
   } else {

@@ -42,6 +42,8 @@ struct PrefillParams {
   ScoreParams sp;
   CappedScore cap;
   int err_code;                  // of a table entry out of range
+  int32_t num_tokens;            // T
+  int32_t list;                  // set by the launcher: items are sorted and dealt on demand
 };
 
 // What the scored kernel (prefill_scored.cu) computes: scores masked by a

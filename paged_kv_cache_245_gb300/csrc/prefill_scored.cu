@@ -4,12 +4,22 @@
 // For row (token, query head) r of a chunk and the keys j it sees (one
 // interval of positions lo .. hi): O_r = sum_j softmax_j(score(q_r . k_j)) v_j.
 //
-// Work items and their order are those of the plain kernel (prefill.cu): two
-// row tiles of 128 rows (whole tokens of one KV head's group), one KV head, one
-// sequence; a persistent grid of one CTA per SM, heaviest items first, dealt
-// in rounds of alternating direction.  An item's key tiles start at the first
-// position any of its rows sees (rounded down to a box), so a window's or a
-// document's cost is its own.
+// Work items are those of the plain kernel (prefill.cu): two row tiles of 128
+// rows (whole tokens of one KV head's group), one KV head, one sequence.  An
+// item's key tiles start at the first position any of its rows sees (rounded
+// down to a box), so a window's or a document's cost is its own.
+//
+// Schedule.  What an item costs depends on its masks and on its sequence's
+// length, and in a ragged batch most (row tile, sequence) pairs have no rows.
+// Up to kListMax pairs each CTA (one an SM) sorts them by key tiles, and the
+// grid has one CTA an item: a running CTA takes the place of one that has not
+// started (cluster launch control), so that the next heaviest item goes to
+// whoever is free.  Longer lists, and those of one round, are dealt to one CTA
+// an SM in rounds of alternating direction, latest rows first, which a ragged
+// batch leaves uneven.  Rounds / on demand, 32 / 8 heads, capped: 15 chunks of
+// 260 to 1040 tokens 97.8 / 84.9 us, 3 of 518 to 2072 82.4 / 59.8, 24 of 50 to
+// 150 24.6 / 20.6; 6 chunks of 56 heads under every mask 117 / 103; even
+// batches pay the sort: 8 x 2048 uncapped 247 / 250.
 //
 // Roles, tensor memory and the order of products are the plain kernel's:
 //
@@ -45,7 +55,11 @@ constexpr int kOffK = kQSlots * kOpBytes;             // after the Q slots
 constexpr int kStageBytes = 2 * kOpBytes;             // K then V
 constexpr int kOffOut = kOffK + kStages * kStageBytes;  // output staging, 4 KiB per softmax warp
 constexpr int kTilesBytes = kOffOut + 8 * 4096;       // 224 KiB
-constexpr int kSmemBytes = kTilesBytes + 512 + 1024;  // + barriers and item ring, alignment
+constexpr int kOffResponse = kTilesBytes + 480;       // 16 bytes, after barriers and item ring
+constexpr int kOffList = kTilesBytes + 512;
+constexpr int kListMax = 704;                         // sorted (row tile, sequence) pairs
+constexpr int kListScan = 2816;                       // candidates looked through for them
+constexpr int kSmemBytes = kOffList + kListMax * 2 + 1024;  // + alignment
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KiB");
 constexpr int kThreads = 352;
 constexpr int kRingUsers = 10;                        // readers: softmax, K/V and MMA warps
@@ -56,6 +70,30 @@ constexpr int kRingUsers = 10;                        // readers: softmax, K/V a
 struct Item {
   int32_t seq, kvh, row0, rows, base, ntiles, q0, ctx, k0, klo;
 };
+
+// Asks for a CTA of this grid that has not started: its index comes to `to`
+// (16 bytes of shared memory, counted on bar) in its place, or a refusal.
+__device__ __forceinline__ void take_block(void* to, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(smem_addr(to)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+
+// The answer: the CTA's blockIdx.x, or -1 (no further request may be made).
+__device__ __forceinline__ int taken_block(const void* from) {
+  int x = -1;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "+r"(x)
+      : "r"(smem_addr(from))
+      : "memory");
+  return x;
+}
 
 // A Q tile's slot in the rotation and the phase of that slot's barriers.
 struct QCursor {
@@ -71,7 +109,7 @@ struct QCursor {
   }
 };
 
-static_assert(sizeof(ScoredBars) <= 256 && 256 + kRing * sizeof(Item) <= 512,
+static_assert(sizeof(ScoredBars) <= 256 && 256 + kRing * sizeof(Item) <= 480,
               "barriers and item ring");
 
 }  // namespace
@@ -112,6 +150,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
+  // Rows and positions of row tile pair rt of a sequence; false where its rows
+  // lie past the chunk or, checked, the sequence is left unwritten.
+  const int R = (p.max_q * G + 2 * TR - 1) / (2 * TR);
+  auto describe = [&](int rt, int seq, int kvh, Item& it) -> bool {
+    it.seq = seq;
+    it.kvh = kvh;
+    it.q0 = p.cu_q[seq];
+    const int Lq = p.cu_q[seq + 1] - it.q0;
+    it.ctx = p.ctx_lens[seq];
+    if (p.checked) {
+      const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.bs;
+      if (Lq < 0 || Lq > p.max_q || it.ctx < Lq || it.ctx > cap) {
+        if (rt == 0 && kvh == 0) record_error(p.err, kErrContext);
+        return false;
+      }
+    }
+    it.rows = Lq * G;
+    it.row0 = rt * 2 * TR;
+    it.base = it.ctx - Lq;  // position of the chunk's first token
+    // (before the first position: only when ctx < Lq, caught in checked mode)
+    const int last = min(it.row0 + 2 * TR, it.rows) - 1;
+    return it.row0 < it.rows && it.base + last / G + 1 > 0;
+  };
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + kOffOut);  // (before any output)
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + kOffList);
+  if (p.list) {
+    for (int i = tid; i < kListMax + 4; i += kThreads) keys[i] = 0u;
+    if (tid == 0) B.pairs = 0;
+  }
+
   // Setup: barriers (warp 8) and the tensor memory (warp 9).
   if (warp == 8) {
     if (lane == 0) {
@@ -131,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&B.iempty[s], kRingUsers);
       }
       mbar_init(&B.drain, 1);
+      mbar_init(&B.taken, 1);
       *abort = 0;
       fence_barrier_init();
       prefetch_tensormap(&tmk);
@@ -157,6 +226,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = B.tmem;
   const uint32_t smem_base = smem_addr(smem);
+
+  if (p.list) {
+    // The (row tile, sequence) pairs that have rows, by descending key tiles
+    // (of the first and last token's positions; ties: latest rows first): the
+    // same list in every CTA.
+    for (int c = tid; c < R * p.num_seqs; c += kThreads) {
+      const int rt = c / p.num_seqs;
+      Item it;
+      if (!describe(rt, c - rt * p.num_seqs, 0, it)) continue;
+      const int t0 = it.row0 / G, t1 = (min(it.row0 + 2 * TR, it.rows) - 1) / G;
+      const int prefix = p.sp.prefix != nullptr ? p.sp.prefix[it.seq] : 0;
+      const int* fk = p.sp.first_key != nullptr ? p.sp.first_key + it.q0 : nullptr;
+      int lo, hi, lo1, hi1;
+      visible_keys(p.sp, it.base + t0, fk ? fk[t0] : 0, prefix, it.ctx, lo, hi);
+      visible_keys(p.sp, it.base + t1, fk ? fk[t1] : 0, prefix, it.ctx, lo1, hi1);
+      const int tiles = hi1 >= lo ? min((hi1 - lo) / kKeys + 1, 65535) : 1;
+      const int at = atomicAdd(&B.pairs, 1);
+      if (at < kListMax) keys[at] = static_cast<uint32_t>(tiles) << 16 | static_cast<uint32_t>(c);
+    }
+    __syncthreads();
+    const int n = min(B.pairs, kListMax);
+    for (int i = tid; i < n; i += kThreads) {
+      const uint32_t key = keys[i];
+      int rank = 0;
+      for (int j = 0; j < n; j += 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + j);
+        rank += (k.x > key) + (k.y > key) + (k.z > key) + (k.w > key);
+      }
+      list[rank] = static_cast<uint16_t>(key);
+    }
+    __syncthreads();
+  }
 
   if (warp == 8) {
     // ================= K/V producer =================
@@ -234,15 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 10) {
     // ================= item list and Q rows =================
-    // Items in order of index: row tile rt (latest first), then sequence,
-    // then KV head.  Round k deals items k P .. k P + P - 1 to the P CTAs,
-    // forwards in even rounds and backwards in odd ones.  Q tile n (row tile
-    // 0 of an item, then row tile 1 if it has rows) goes to slot n % 2 once
-    // the last S product reading tile n - 2 completed.
-    const int P = gridDim.x;
-    const int R = (p.max_q * G + 2 * TR - 1) / (2 * TR);
-    const int per = p.num_seqs * p.Hkv;
-    const int total = R * per;
+    // Q tile n (row tile 0 of an item, then row tile 1 if it has rows) goes to
+    // slot n % 2 once the last S product reading tile n - 2 completed.
     const uint64_t qpolicy = l2_policy_evict_first();  // every Q row is read once
     int published = 0;
     uint32_t nq = 0;      // Q tiles loaded
@@ -263,93 +357,115 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++published;
       return true;
     };
-    // 32 rounds at a time, one a lane, so that items whose rows lie past their
-    // chunk (most of the first rounds of a ragged batch) cost one latency
-    for (int64_t k0 = 0; ok && k0 * P < total; k0 += 32) {
-      const int64_t k = k0 + lane;
-      const int64_t slot = k * P + ((k & 1) ? P - 1 - static_cast<int>(blockIdx.x)
-                                            : static_cast<int>(blockIdx.x));
-      Item mine = {};
-      bool there = slot < total;
-      if (there) {
-        const int idx = static_cast<int>(slot);
-        const int rt = R - 1 - idx / per;
-        const int rem = idx - (idx / per) * per;
-        mine.seq = rem / p.Hkv;
-        mine.kvh = rem - mine.seq * p.Hkv;
-        mine.q0 = p.cu_q[mine.seq];
-        const int Lq = p.cu_q[mine.seq + 1] - mine.q0;
-        mine.ctx = p.ctx_lens[mine.seq];
-        if (p.checked) {
-          const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.bs;
-          if (Lq < 0 || Lq > p.max_q || mine.ctx < Lq || mine.ctx > cap) {
-            if (rt == 0 && mine.kvh == 0) record_error(p.err, kErrContext);
-            there = false;  // the sequence is left unwritten
-          }
+    // Publishes an item and brings its Q rows; false when a wait gave up.
+    auto serve = [&](Item it) -> bool {
+      const int last_row = min(it.row0 + 2 * TR, it.rows) - 1;
+      // the interval of positions that some token of the item sees
+      const int prefix = p.sp.prefix != nullptr ? p.sp.prefix[it.seq] : 0;
+      int low = INT_MAX, high = -1;
+      for (int tok = it.row0 / G + lane; tok <= last_row / G; tok += 32) {
+        int lo, hi;
+        visible_keys(p.sp, it.base + tok,
+                     p.sp.first_key != nullptr ? p.sp.first_key[it.q0 + tok] : 0, prefix,
+                     it.ctx, lo, hi);
+        if (lo <= hi) {
+          low = min(low, lo);
+          high = max(high, hi);
         }
-        mine.rows = Lq * G;
-        mine.row0 = rt * 2 * TR;
-        mine.base = mine.ctx - Lq;  // position of the chunk's first token
-        // this item's rows may lie past the chunk, and (only when ctx < Lq,
-        // caught in checked mode) before the first position
-        const int last = min(mine.row0 + 2 * TR, mine.rows) - 1;
-        there = there && mine.row0 < mine.rows && mine.base + last / G + 1 > 0;
       }
-      for (uint32_t left = __ballot_sync(kFull, there); ok && left != 0u; left &= left - 1) {
-        const int src = __ffs(left) - 1;
-        Item it;
-        it.seq = __shfl_sync(kFull, mine.seq, src);
-        it.kvh = __shfl_sync(kFull, mine.kvh, src);
-        it.q0 = __shfl_sync(kFull, mine.q0, src);
-        it.ctx = __shfl_sync(kFull, mine.ctx, src);
-        it.rows = __shfl_sync(kFull, mine.rows, src);
-        it.row0 = __shfl_sync(kFull, mine.row0, src);
-        it.base = __shfl_sync(kFull, mine.base, src);
-        const int last_row = min(it.row0 + 2 * TR, it.rows) - 1;
-        // the interval of positions that some token of the item sees
-        const int prefix = p.sp.prefix != nullptr ? p.sp.prefix[it.seq] : 0;
-        int low = INT_MAX, high = -1;
-        for (int tok = it.row0 / G + lane; tok <= last_row / G; tok += 32) {
-          int lo, hi;
-          visible_keys(p.sp, it.base + tok,
-                       p.sp.first_key != nullptr ? p.sp.first_key[it.q0 + tok] : 0, prefix,
-                       it.ctx, lo, hi);
-          if (lo <= hi) {
-            low = min(low, lo);
-            high = max(high, hi);
-          }
+      it.klo = __reduce_min_sync(kFull, low);
+      int kend = __reduce_max_sync(kFull, high) + 1;
+      it.k0 = it.klo < kend ? it.klo / p.run_rows * p.run_rows : 0;
+      kend = max(kend - it.k0, 1);  // an item that sees nothing is one tile, all masked
+      it.ntiles = (kend + kKeys - 1) / kKeys;
+      if (!publish(it)) return false;
+      const int nt = it.rows > it.row0 + TR ? 2 : 1;
+      for (int t = 0; t < nt; ++t, ++nq, qc = qc.next(kQSlots)) {
+        const int qs = qc.slot;
+        if (nq >= static_cast<uint32_t>(kQSlots) &&
+            !__all_sync(kFull, wait_or_abort(&B.qempty[qs], qc.phase ^ 1u, abort, p.err)))
+          return false;
+        last_phase = (last_phase & ~(1u << qs)) | (qc.phase << qs);
+        unsigned char* dst = smem + q_off(qs);
+        // the tile is TR / G whole tokens, each column half one box of
+        // (tokens, G heads, 64 columns); rows past the chunk bring the next
+        // tokens' rows (or zeros past the tensor) and are never written out
+        const int tok0 = it.q0 + (it.row0 + t * TR) / G;
+        if (lane == 0) {
+          // two column halves of TR rows x 128 bytes
+          mbar_arrive_expect_tx(&B.qfull[qs], static_cast<uint32_t>(TR) * kRowBytes);
+          tma_load_4d_at(dst, &tmq, 0, 0, it.kvh * G, tok0, &B.qfull[qs], qpolicy);
+          tma_load_4d_at(dst + kHalfBytes, &tmq, 0, 1, it.kvh * G, tok0, &B.qfull[qs], qpolicy);
+        } else {
+          mbar_arrive(&B.qfull[qs]);
         }
-        it.klo = __reduce_min_sync(kFull, low);
-        int kend = __reduce_max_sync(kFull, high) + 1;
-        it.k0 = it.klo < kend ? it.klo / p.run_rows * p.run_rows : 0;
-        kend = max(kend - it.k0, 1);  // an item that sees nothing is one tile, all masked
-        it.ntiles = (kend + kKeys - 1) / kKeys;
-        if (!publish(it)) {
+      }
+      return true;
+    };
+    if (p.list) {
+      // Item i is KV head i % Hkv of pair i / Hkv of the list, and CTA i's own
+      // until another takes it.  A CTA takes its next item when it starts one
+      // (the K/V producer runs ahead into it): heaviest first, to whoever is
+      // there next.
+      uint32_t phase = 0;
+      const int n = min(B.pairs, kListMax);
+      for (int i = blockIdx.x; i >= 0;) {
+        const int at = i / p.Hkv;
+        if (at < n) {
+          const int c = list[at], rt = c / p.num_seqs;
+          Item it = {};
+          ok = !describe(rt, c - rt * p.num_seqs, i - at * p.Hkv, it) || serve(it);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&B.taken, 16);
+          take_block(smem + kOffResponse, &B.taken);
+        }
+        __syncwarp();
+        if (!__all_sync(kFull, mbar_wait_bounded(&B.taken, phase))) {
+          if (lane == 0) {
+            *abort = 1;
+            record_error(p.err, kErrTimeout);
+          }
           ok = false;
           break;
         }
-        const int nt = it.rows > it.row0 + TR ? 2 : 1;
-        for (int t = 0; t < nt; ++t, ++nq, qc = qc.next(kQSlots)) {
-          const int qs = qc.slot;
-          if (nq >= static_cast<uint32_t>(kQSlots) &&
-              !__all_sync(kFull, wait_or_abort(&B.qempty[qs], qc.phase ^ 1u, abort, p.err))) {
-            ok = false;
-            break;
-          }
-          last_phase = (last_phase & ~(1u << qs)) | (qc.phase << qs);
-          unsigned char* dst = smem + q_off(qs);
-          // the tile is TR / G whole tokens, each column half one box of
-          // (tokens, G heads, 64 columns); rows past the chunk bring the next
-          // tokens' rows (or zeros past the tensor) and are never written out
-          const int tok0 = it.q0 + (it.row0 + t * TR) / G;
-          if (lane == 0) {
-            // two column halves of TR rows x 128 bytes
-            mbar_arrive_expect_tx(&B.qfull[qs], static_cast<uint32_t>(TR) * kRowBytes);
-            tma_load_4d_at(dst, &tmq, 0, 0, it.kvh * G, tok0, &B.qfull[qs], qpolicy);
-            tma_load_4d_at(dst + kHalfBytes, &tmq, 0, 1, it.kvh * G, tok0, &B.qfull[qs], qpolicy);
-          } else {
-            mbar_arrive(&B.qfull[qs]);
-          }
+        phase ^= 1u;
+        i = taken_block(smem + kOffResponse);
+        fence_proxy_async_smem();  // read before the next answer comes in
+        __syncwarp();
+      }
+    } else {
+      // Items in order of index: row tile (latest first), then sequence, then
+      // KV head.  Round k deals items k P .. k P + P - 1 to the P CTAs,
+      // forwards in even rounds and backwards in odd ones; 32 rounds at a time,
+      // one a lane, so that items whose rows lie past their chunk cost one latency.
+      const int P = gridDim.x;
+      const int per = p.num_seqs * p.Hkv;
+      const int total = R * per;
+      for (int64_t k0 = 0; ok && k0 * P < total; k0 += 32) {
+        const int64_t k = k0 + lane;
+        const int64_t slot = k * P + ((k & 1) ? P - 1 - static_cast<int>(blockIdx.x)
+                                              : static_cast<int>(blockIdx.x));
+        Item mine = {};
+        bool there = slot < total;
+        if (there) {
+          const int idx = static_cast<int>(slot);
+          const int rem = idx - (idx / per) * per;
+          const int seq = rem / p.Hkv;
+          there = describe(R - 1 - idx / per, seq, rem - seq * p.Hkv, mine);
+        }
+        for (uint32_t left = __ballot_sync(kFull, there); ok && left != 0u; left &= left - 1) {
+          const int src = __ffs(left) - 1;
+          Item it;
+          it.seq = __shfl_sync(kFull, mine.seq, src);
+          it.kvh = __shfl_sync(kFull, mine.kvh, src);
+          it.q0 = __shfl_sync(kFull, mine.q0, src);
+          it.ctx = __shfl_sync(kFull, mine.ctx, src);
+          it.rows = __shfl_sync(kFull, mine.rows, src);
+          it.row0 = __shfl_sync(kFull, mine.row0, src);
+          it.base = __shfl_sync(kFull, mine.base, src);
+          ok = serve(it);
         }
       }
     }
@@ -658,9 +774,14 @@ cudaError_t launch_mode(const CUtensorMap& tk, const CUtensorMap& tv, const CUte
   const int64_t items = row_tiles * p.Hkv * p.num_seqs;
   if (items <= 0) return cudaSuccess;
   if (items > INT32_MAX) return cudaErrorInvalidValue;
-  const int grid = static_cast<int>(items < n ? items : n);
+  // on demand over a grid of one CTA an item, or in rounds over one CTA an SM
+  const int64_t bound = static_cast<int64_t>(p.num_tokens) * p.G / (2 * p.tile_rows) + p.num_seqs;
+  const int64_t pairs = bound < row_tiles * p.num_seqs ? bound : row_tiles * p.num_seqs;
+  PrefillParams pl = p;
+  pl.list = pairs <= kListMax && row_tiles * p.num_seqs <= kListScan && pairs * p.Hkv > n;
+  const int grid = static_cast<int>(pl.list ? pairs * p.Hkv : items < n ? items : n);
   return launch_pdl(prefill_scored_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, stream,
-                    tk, tv, tq, to, p);
+                    tk, tv, tq, to, pl);
 }
 
 }  // namespace

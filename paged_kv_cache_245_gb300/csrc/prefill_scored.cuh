@@ -90,8 +90,10 @@ struct ScoredBars {
   uint64_t ifull[kRing];   // an item descriptor published
   uint64_t iempty[kRing];  // every reader is done with it
   uint64_t drain;       // the MMA thread's final wait
+  uint64_t taken;       // an answer to the request for another CTA's item
   uint32_t tmem;        // tensor-memory address
   volatile int abort;   // a wait gave up
+  int pairs;            // of the sorted list
 };
 
 // The row's running maximum takes in the tile's; O and l are rescaled when it

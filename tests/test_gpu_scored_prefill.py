@@ -139,6 +139,63 @@ def test_long_chunks(name):
     assert_close(s.call(**kw), *s.reference(**ref), what=name)
 
 
+RAGGED = ([0, 3, 700, 0, 64, 900, 17, 0, 5, 300, 0, 2], [0, 1, 500, 64, 65, 3, 700, 129, 0, 40, 900, 5])
+
+
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (56, 8), (6, 6)])
+@pytest.mark.parametrize("name", ["window 100", "cap", "slopes", "cap, documents", "all"])
+def test_more_items_than_sms(name, hq, hkv):
+    """A ragged batch whose work items are sorted and dealt on demand."""
+    s = Chunks(*RAGGED, hq, hkv, 16, seed=hq)
+    ref, kw = make(name, s)
+    assert_close(s.call(**kw), *s.reference(**ref), what=name)
+
+
+@pytest.mark.parametrize("count", [160, 700, 730])
+def test_hundreds_of_short_chunks(count):
+    """One item a sequence: up to the sorted list's length, and past it."""
+    s = Chunks([i % 50 for i in range(count)], [1 + i % 3 for i in range(count)], 8, 1, 16, seed=7)
+    for name in ("cap", "window 33", "documents"):
+        kw = dict(window=33) if name == "window 33" else make(name, s)[1]
+        ref = dict(window=33) if name == "window 33" else make(name, s)[0]
+        assert_close(s.call(**kw), *s.reference(**ref), what=name)
+
+
+def test_more_items_than_sms_checked_captured_and_on_two_streams():
+    s = Chunks(*RAGGED, 32, 8, 16, seed=21)
+    ref, kw = make("cap", s)
+    want, tol = s.reference(**ref)
+    out = torch.empty(s.T, 32, D, dtype=torch.bfloat16, device=DEV)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.call(out=out, **kw)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        s.call(out=out, **kw)
+    other = torch.empty_like(out)
+    for _ in range(5):  # each replay beside an eager call on another stream
+        out.fill_(7.0)
+        other.fill_(7.0)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            s.call(out=other, **kw)
+        graph.replay()
+        torch.cuda.current_stream().wait_stream(side)
+        assert_close(out, want, tol)
+        assert_close(other, want, tol)
+    # a sequence longer than its context is left unwritten, the others are not
+    pkv.set_checked(True)
+    s.ctx_t = s.ctx_t.clone()
+    s.ctx_t[4] = 64
+    out.fill_(7.0)
+    s.call(out=out, **kw)
+    assert pkv.get_device_error() == "context"
+    a, b = int(s.cu[4]), int(s.cu[5])
+    assert bool((out[a:b] == 7.0).all())
+    keep = torch.ones(s.T, dtype=torch.bool, device=DEV)
+    keep[a:b] = False
+    assert_close(out[keep], want[keep], tol[keep])
+
+
 @pytest.mark.parametrize("by", [0.0, 30.0, 300.0])
 @pytest.mark.parametrize("scale", [SCALE, -SCALE])
 def test_saturating_scores(by, scale):

@@ -385,11 +385,13 @@ __global__ void __launch_bounds__(W * 32, 1)
         }
         const float p0 = fast_exp2(s0 - m0), p2 = fast_exp2(s2 - m0);
         const float p1 = fast_exp2(s1 - m1), p3 = fast_exp2(s3 - m1);
-        l0 += p0 + p2;
-        l1 += p1 + p3;
-        // P^T as the B operand, rounded to bf16 (V's type) once
-        const uint32_t b0 = movmatrix_trans(pack_bf16x2(p0, p1));  // tokens 0..7
-        const uint32_t b1 = movmatrix_trans(pack_bf16x2(p2, p3));  // tokens 8..15
+        // P^T as the B operand, rounded to bf16 (V's type) once; l sums what was
+        // rounded, so that it cancels where few keys are seen
+        const uint32_t w01 = pack_bf16x2(p0, p1), w23 = pack_bf16x2(p2, p3);
+        l0 += bf16_lo(w01) + bf16_lo(w23);
+        l1 += bf16_hi(w01) + bf16_hi(w23);
+        const uint32_t b0 = movmatrix_trans(w01);  // tokens 0..7
+        const uint32_t b1 = movmatrix_trans(w23);  // tokens 8..15
 
         // ---- O^T += V^T . P^T
 #pragma unroll

@@ -781,10 +781,16 @@ __global__ void __launch_bounds__(W * 32, 1)
         }
         const float p0 = fast_exp2(s0 - m0[t]), p2 = fast_exp2(s2 - m0[t]);
         const float p1 = fast_exp2(s1 - m1[t]), p3 = fast_exp2(s3 - m1[t]);
-        l0[t] += p0 + p2;
-        l1[t] += p1 + p3;
-        b0[t] = movmatrix_trans(pack_bf16x2(p0, p1));  // P^T rows: tokens 0..7
-        b1[t] = movmatrix_trans(pack_bf16x2(p2, p3));  // tokens 8..15
+        const uint32_t w01 = pack_bf16x2(p0, p1), w23 = pack_bf16x2(p2, p3);
+        if (kScored) {  // masks leave few keys: their sum is that of the rounded P
+          l0[t] += bf16_lo(w01) + bf16_lo(w23);
+          l1[t] += bf16_hi(w01) + bf16_hi(w23);
+        } else {
+          l0[t] += p0 + p2;
+          l1[t] += p1 + p3;
+        }
+        b0[t] = movmatrix_trans(w01);  // P^T rows: tokens 0..7
+        b1[t] = movmatrix_trans(w23);  // tokens 8..15
       }
 
       // ---- O^T += V^T . P^T  (each V^T fragment serves every n-tile)

@@ -146,7 +146,10 @@ __device__ __forceinline__ void chunk_max(const uint32_t (&a)[32], uint32_t bits
   }
 }
 
-// P = 2^f, packed into pk[0..15], summed into ls.
+// P = 2^f, packed into pk[0..15], summed into ls: where columns are masked, as
+// rounded to bf16, so that the rounding cancels in a row that sees few keys
+// (one key's output is its value); over whole tiles before it (two operations
+// a pair less), where the roundings average out.
 template <bool kMask, typename F>
 __device__ __forceinline__ void chunk_p(const uint32_t (&a)[32], uint32_t bits, F&& f,
                                         uint32_t* pk, uint64_t (&ls)[4]) {
@@ -160,8 +163,9 @@ __device__ __forceinline__ void chunk_p(const uint32_t (&a)[32], uint32_t bits, 
       e0 = bit_of(bits, 2 * i) ? e0 : 0.f;
       e1 = bit_of(bits, 2 * i + 1) ? e1 : 0.f;
     }
-    ls[i & 3] = f2_add(ls[i & 3], f2_pack(__float_as_uint(e0), __float_as_uint(e1)));
     pk[i] = pack_bf16x2(e0, e1);
+    ls[i & 3] = f2_add(ls[i & 3], kMask ? f2_pack(pk[i] << 16, pk[i] & 0xffff0000u)
+                                        : f2_pack(__float_as_uint(e0), __float_as_uint(e1)));
   }
 }
 

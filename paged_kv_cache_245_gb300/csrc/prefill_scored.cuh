@@ -432,12 +432,15 @@ __device__ __forceinline__ void tile_general(const PrefillParams& p, const Cappe
   st.l += sum_of(ls);
 }
 
-// Under the cap, in one pass: the polynomial, or, where a half tile is masked
-// or holds a score out of its range, the exponentials.  Past the range the polynomial
-// keeps rising (falling), so a half tile's sum of P tells: one product above
-// the cap alone makes it p_high or more, and products below -cap, whatever
-// the polynomial gives for them, are lost in a sum of p_low or more (64 of
-// them are under 2^-12 of it).
+// Under the cap, in one pass: the polynomial, or, where a half tile holds a
+// score out of its range, the exponentials.  In a whole tile the half's sum of
+// P tells: past the range the polynomial keeps rising (falling), so one product
+// above the cap alone makes the sum p_high or more, and products below -cap,
+// whatever the polynomial gives for them, are lost in a sum of p_low or more
+// (64 of them are under 2^-12 of it).  A masked half is looked at first
+// (against exponentials for every masked half: 8 x 2048 tokens, caps 50 and 15,
+// 274 and 564 us for 277 and 523; under a window of 500 174 for 179; the whole
+// tiles' test by their largest product instead of their sum: 300 for 270).
 __device__ __forceinline__ void tile_capped(const PrefillParams& p, const CappedRegs& k,
                                             const ScoredRow& r, uint32_t s_tm, int kt,
                                             SoftState& st) {
@@ -493,8 +496,23 @@ __device__ __forceinline__ void tile_capped(const PrefillParams& p, const Capped
         uint32_t a[32], b[32];
         load_half(a, b, s_tm + 64 * h);
         uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
-        chunk_p<true>(a, mask.bits(2 * h), far, pk, ls);
-        chunk_p<true>(b, mask.bits(2 * h + 1), far, pk + 16, ls);
+        bool near = !mask.whole;
+        if (near) {
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            top = fmax3_abs(top, __uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+            top = fmax3_abs(top, __uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+          }
+          near = __all_sync(kFull, top <= p.cap.s_max);
+        }
+        if (near) {
+          chunk_p<true>(a, mask.bits(2 * h), poly, pk, ls);
+          chunk_p<true>(b, mask.bits(2 * h + 1), poly, pk + 16, ls);
+        } else {
+          chunk_p<true>(a, mask.bits(2 * h), far, pk, ls);
+          chunk_p<true>(b, mask.bits(2 * h + 1), far, pk + 16, ls);
+        }
         st.l += sum_of(ls);
       }
       tmem_st32(s_tm + 32 * h, pk);

@@ -44,6 +44,7 @@ struct PrefillParams {
   int err_code;                  // of a table entry out of range
   int32_t num_tokens;            // T
   int32_t list;                  // set by the launcher: items are sorted and dealt on demand
+  int32_t split;                 // set by the launcher: CTAs (a cluster) that share an item's keys
 };
 
 // What the scored kernel (prefill_scored.cu) computes: scores masked by a

@@ -21,6 +21,15 @@
 // 150 24.6 / 20.6; 6 chunks of 56 heads under every mask 117 / 103; even
 // batches pay the sort: 8 x 2048 uncapped 247 / 250.
 //
+// Few items (a short chunk after a long context): a cluster of 2 to 16 CTAs
+// shares an item's key tiles, as many as the device holds for all items at
+// once, and joins its parts through distributed shared memory (join_parts).
+// The join takes 5 us, a key tile 1.8 (one row tile) to 2.2 us: items of fewer
+// than kJoinTiles are the first CTA's alone.  32 / 8 heads, one CTA / a cluster
+// an item: 64 tokens after 8000 129 / 31 us, 512 after 8000 136 / 86, 2 x 256
+// after 2000 to 4000 70 / 49, 4 x 1 after 996 21.1 / 14.7.  Kernels of their own:
+// in one, the code of the join cost 2 x 8192 tokens 256 -> 262 us.
+//
 // Roles, tensor memory and the order of products are the plain kernel's:
 //
 //   warps 0-3  softmax and output of row tile 0   warps 4-7  of row tile 1
@@ -33,10 +42,12 @@
 // and slower: two warps per 32 rows, each on half the keys (+3 %); P in shared
 // memory, so that S is free once it is in registers (+15 %: each hand-over
 // waits for the proxy fence, and both softmax warpgroups run in step).
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "pkv_device.cuh"
 #include "prefill.cuh"
@@ -67,8 +78,9 @@ constexpr int kRingUsers = 10;                        // readers: softmax, K/V a
 // One work item as warp 10 publishes it; ntiles == 0 ends the list.  Its key
 // tiles start at position k0 (a multiple of run_rows); no row of it sees a
 // position before klo (INT_MAX: none sees any).
+// With `joined` the item is a part of the cluster's: its O and sums stay for the join.
 struct Item {
-  int32_t seq, kvh, row0, rows, base, ntiles, q0, ctx, k0, klo;
+  int32_t seq, kvh, row0, rows, base, ntiles, q0, ctx, k0, klo, joined;
 };
 
 // Asks for a CTA of this grid that has not started: its index comes to `to`
@@ -95,6 +107,204 @@ __device__ __forceinline__ int taken_block(const void* from) {
   return x;
 }
 
+// What a cluster's CTAs share of the item they have in parts: in the output
+// staging, which a part does not use.
+struct Join {
+  float2 sums[2 * kRowTile];  // (m, l) of every row of this CTA's part
+  Item item;                  // the whole item
+};
+constexpr int kOffJoin = kOffOut + 8192;  // (past the keys of the sort)
+constexpr int kJoinTiles = 6;             // fewer key tiles are not split
+static_assert(8192 >= (kListMax + 4) * 4 && kOffJoin + sizeof(Join) <= kTilesBytes, "join");
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// The shared-memory address `of` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t in_cta(const void* of, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(of)), "r"(rank));
+  return a;
+}
+
+__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t a) {
+  int32_t x;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+  return x;
+}
+
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
+  float2 x;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(a) : "memory");
+  return x;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(a)
+               : "memory");
+  return x;
+}
+
+// Row `row` of an item.
+__device__ __forceinline__ ScoredRow score_row(const PrefillParams& p, const Item& it, int row) {
+  ScoredRow r;
+  r.valid = true;
+  const int tok = row / p.G;
+  const int head = it.kvh * p.G + row - tok * p.G;
+  const int pos = it.base + tok;
+  r.qrow = (static_cast<int64_t>(it.q0) + tok) * p.Hq + head;
+  int lo, hi;
+  visible_keys(p.sp, pos, p.sp.first_key != nullptr ? __ldg(p.sp.first_key + it.q0 + tok) : 0,
+               p.sp.prefix != nullptr ? __ldg(p.sp.prefix + it.seq) : 0, it.ctx, lo, hi);
+  r.lo = lo <= hi ? lo - it.k0 : INT_MAX;
+  r.hi = lo <= hi ? hi - it.k0 : -1;
+  r.pos = pos - it.k0;
+  r.slope2 = p.sp.slopes != nullptr ? slope_log2(p.sp.slopes, head) : 0.f;
+  return r;
+}
+
+__device__ __forceinline__ KvRows kv_rows(const PrefillParams& p, const Item& it) {
+  KvRows kv;
+  kv.k = p.k;
+  kv.v = p.v;
+  kv.table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks;
+  kv.bs = p.bs;
+  kv.num_blocks = p.num_blocks;
+  kv.Hkv = p.Hkv;
+  kv.kvh = it.kvh;
+  kv.checked = p.checked;
+  kv.err = p.err;
+  kv.err_code = p.err_code;
+  return kv;
+}
+
+// Sums the CTAs' parts of rows rank, rank + kN, .. of an item: a warp a row, 16
+// loads in flight.
+template <int kN>
+__device__ __forceinline__ void sum_rows(const PrefillParams& p, const Item& it,
+                                         unsigned char* smem, int rank, int row_tiles) {
+  constexpr int kRows = 16 / kN, kWarps = kThreads / 32, kShare = kRowTile / kN;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i0 = warp; i0 < row_tiles * kShare; i0 += kWarps * kRows) {
+    float4 x[kRows][kN];
+    int row[kRows];  // of the item's rows, or -1
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int i = i0 + u * kWarps;
+      const int t = i / kShare, lr = (i - t * kShare) * kN + rank;
+      row[u] = it.row0 + t * p.tile_rows + lr;
+      if (i >= row_tiles * kShare || lr >= p.tile_rows || row[u] >= it.rows) row[u] = -1;
+      const unsigned char* at =
+          smem + kOffK + (row[u] < 0 ? 0 : t * 65536 + lr * 512 + ((lane ^ (lr & 31)) << 4));
+#pragma unroll
+      for (int k = 0; k < kN; ++k)
+        x[u][k] = row[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : ld_cluster_f4(in_cta(at, k));
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (row[u] < 0) continue;
+      float4 o = x[u][0];
+#pragma unroll
+      for (int k = 1; k < kN; ++k) {
+        o.x += x[u][k].x;
+        o.y += x[u][k].y;
+        o.z += x[u][k].z;
+        o.w += x[u][k].w;
+      }
+      const int tok = row[u] / p.G;
+      const int64_t qrow =
+          (static_cast<int64_t>(it.q0) + tok) * p.Hq + it.kvh * p.G + row[u] - tok * p.G;
+      *reinterpret_cast<uint2*>(p.out + qrow * kHeadDim + 4 * lane) =
+          make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+      const float z = 0.f * o.x + 0.f * o.y + 0.f * o.z + 0.f * o.w;  // 0, or NaN
+      if (__any_sync(kFull, z != 0.f)) {
+        const ScoredRow r = score_row(p, it, row[u]);
+        __syncwarp();
+        repair_rows(p, kv_rows(p, it), lane == 0, r, it.k0, lane);
+      }
+    }
+  }
+}
+
+// The parts of a cluster's item, joined through distributed shared memory:
+//   O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.
+// Every CTA scales its O into its K/V stages, idle by then, and sums its share
+// of the rows over the CTAs (pushed to the CTA that sums them, 16 bytes a lane,
+// the rows took 2 us longer).  Every CTA comes to each barrier whatever its
+// item: what goes before them waits a bounded time.
+static __device__ __noinline__ void join_parts(const PrefillParams& p, unsigned char* smem,
+                                               uint32_t tmem, const ScoredBars& B,
+                                               const Join& join, int rank) {
+  constexpr int kMost = 16;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int TR = p.tile_rows, G = p.G, n = p.split;
+  __syncwarp();
+  cluster_sync();
+  const bool on = __all_sync(
+      kFull, lane >= n || ld_cluster_s32(in_cta(&B.joined, lane < n ? lane : 0)) != 0);
+  const Item it = join.item;
+  const int row_tiles = it.rows > it.row0 + TR ? 2 : 1;
+  if (on && warp < 4 * row_tiles) {
+    tc_fence_after();
+    const int t = warp >> 2, lr = tid & (kRowTile - 1);
+    const uint32_t o_tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 + t * 128;
+    const float2* at = &join.sums[t * kRowTile + lr];
+    float2 x[kMost];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+      x[k] = k < n ? ld_cluster_f2(in_cta(at, k)) : make_float2(-INFINITY, 0.f);
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+      if (x[k].y != 0.f) M = fmaxf(M, x[k].x);
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+      if (x[k].y != 0.f) L = fmaf(x[k].y, fast_exp2(x[k].x - M), L);
+    const bool any = at->y != 0.f;  // (else O is 0 or was never written)
+    const float w = any ? fast_exp2(at->x - M) / L : 0.f;
+    unsigned char* to = smem + kOffK + t * 65536 + lr * 512;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a[32], b[32];
+      tmem_ld32(a, o_tm + 64 * h);
+      tmem_ld32(b, o_tm + 64 * h + 32);
+      tmem_wait_ld(a);
+      tmem_ready(b);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t* o = i < 8 ? a + 4 * i : b + 4 * (i - 8);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (any)
+          v = make_float4(__uint_as_float(o[0]) * w, __uint_as_float(o[1]) * w,
+                          __uint_as_float(o[2]) * w, __uint_as_float(o[3]) * w);
+        *reinterpret_cast<float4*>(to + (((16 * h + i) ^ lane) << 4)) = v;
+      }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync();
+  if (on) {
+    if (n == 2) sum_rows<2>(p, it, smem, rank, row_tiles);
+    else if (n == 4) sum_rows<4>(p, it, smem, rank, row_tiles);
+    else if (n == 8) sum_rows<8>(p, it, smem, rank, row_tiles);
+    else sum_rows<16>(p, it, smem, rank, row_tiles);
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while another reads its shared memory
+}
+
 // A Q tile's slot in the rotation and the phase of that slot's barriers.
 struct QCursor {
   int slot;
@@ -114,8 +324,8 @@ static_assert(sizeof(ScoredBars) <= 256 && 256 + kRing * sizeof(Item) <= 480,
 
 }  // namespace
 
-// kMode: a PrefillMode.
-template <int kMode>
+// kMode: a PrefillMode.  kSplit: clusters of p.split CTAs, an item each.
+template <int kMode, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_scored_kernel(const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv,
@@ -173,6 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int last = min(it.row0 + 2 * TR, it.rows) - 1;
     return it.row0 < it.rows && it.base + last / G + 1 > 0;
   };
+  Join& join = *reinterpret_cast<Join*>(smem + kOffJoin);
+  const int rank = kSplit ? static_cast<int>(cluster_rank()) : 0;
+  if (kSplit) {
+    if (tid < 2 * kRowTile) join.sums[tid] = make_float2(-INFINITY, 0.f);
+    if (tid == 0) B.joined = 0;
+  }
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem + kOffOut);  // (before any output)
   uint16_t* list = reinterpret_cast<uint16_t*>(smem + kOffList);
   if (p.list) {
@@ -378,6 +594,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.k0 = it.klo < kend ? it.klo / p.run_rows * p.run_rows : 0;
       kend = max(kend - it.k0, 1);  // an item that sees nothing is one tile, all masked
       it.ntiles = (kend + kKeys - 1) / kKeys;
+      if (kSplit) {
+        it.joined = it.ntiles >= kJoinTiles;
+        if (it.joined) {
+          if (lane == 0) {
+            join.item = it;
+            B.joined = 1;
+          }
+          __syncwarp();
+          const int from = it.ntiles * rank / p.split;
+          it.ntiles = it.ntiles * (rank + 1) / p.split - from;
+          it.k0 += from * kKeys;
+        } else if (rank > 0) {
+          it.ntiles = 0;
+        }
+        if (it.ntiles == 0) return true;
+      }
       if (!publish(it)) return false;
       const int nt = it.rows > it.row0 + TR ? 2 : 1;
       for (int t = 0; t < nt; ++t, ++nq, qc = qc.next(kQSlots)) {
@@ -402,21 +634,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    if (p.list) {
+    if (p.list || kSplit) {
       // Item i is KV head i % Hkv of pair i / Hkv of the list, and CTA i's own
       // until another takes it.  A CTA takes its next item when it starts one
       // (the K/V producer runs ahead into it): heaviest first, to whoever is
-      // there next.
+      // there next.  (A cluster has one item.)
       uint32_t phase = 0;
-      const int n = min(B.pairs, kListMax);
-      for (int i = blockIdx.x; i >= 0;) {
+      const int n = p.list ? min(B.pairs, kListMax) : R * p.num_seqs;
+      for (int i = kSplit ? blockIdx.x / p.split : blockIdx.x; i >= 0;) {
         const int at = i / p.Hkv;
         if (at < n) {
-          const int c = list[at], rt = c / p.num_seqs;
+          const int c = p.list ? list[at] : at, rt = c / p.num_seqs;
           Item it = {};
           ok = !describe(rt, c - rt * p.num_seqs, i - at * p.Hkv, it) || serve(it);
           if (!ok) break;
         }
+        if (kSplit) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&B.taken, 16);
           take_block(smem + kOffResponse, &B.taken);
@@ -618,21 +851,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto has_rows = [&](const Item& it) { return t == 0 || it.rows > it.row0 + TR; };
     auto row_of = [&](const Item& it) -> ScoredRow {
-      ScoredRow r;
       const int row = it.row0 + t * TR + lr;  // row of the chunk
-      r.valid = lr < TR && row < it.rows;
-      const int rr = r.valid ? row : it.rows - 1;  // padding rows mirror the last row
-      const int tok = rr / G;
-      const int head = it.kvh * G + rr - tok * G;
-      const int pos = it.base + tok;
-      r.qrow = (static_cast<int64_t>(it.q0) + tok) * p.Hq + head;
-      int lo, hi;
-      visible_keys(p.sp, pos, p.sp.first_key != nullptr ? __ldg(p.sp.first_key + it.q0 + tok) : 0,
-                   p.sp.prefix != nullptr ? __ldg(p.sp.prefix + it.seq) : 0, it.ctx, lo, hi);
-      r.lo = lo <= hi ? lo - it.k0 : INT_MAX;
-      r.hi = lo <= hi ? hi - it.k0 : -1;
-      r.pos = pos - it.k0;
-      r.slope2 = p.sp.slopes != nullptr ? slope_log2(p.sp.slopes, head) : 0.f;
+      const bool valid = lr < TR && row < it.rows;
+      ScoredRow r = score_row(p, it, valid ? row : it.rows - 1);  // padding mirrors the last row
+      r.valid = valid;
       return r;
     };
     uint32_t ns = 0, no = 0;  // S tiles and items this row tile took
@@ -681,7 +903,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ScoredRow next_row = row;
       if (ring[(n + 1) & (kRing - 1)].ntiles != 0) next_row = row_of(ring[(n + 1) & (kRing - 1)]);
-      if (mine) {
+      if (kSplit && mine && it.joined) {
+        ok = __all_sync(kFull, wait_or_abort(&B.ofull[t], no & 1, abort, p.err));
+        ++no;
+        if (!ok) break;
+        // (under a fixed offset every part has the same)
+        join.sums[t * kRowTile + lr] = make_float2(kMode == kPrefillCapped ? 0.f : st.m, st.l);
+      } else if (mine) {
         // the item's output rows; the next item's first P V product overwrites
         // O_t only after these warps hand over its first P
         ok = __all_sync(kFull, wait_or_abort(&B.ofull[t], no & 1, abort, p.err));
@@ -713,17 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // does not see (0 times either is NaN): it is computed again by itself.
         const bool repair = row.valid && !is_zero(z);
         if (__any_sync(kFull, repair)) {
-          KvRows kv;
-          kv.k = p.k;
-          kv.v = p.v;
-          kv.table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks;
-          kv.bs = p.bs;
-          kv.num_blocks = p.num_blocks;
-          kv.Hkv = p.Hkv;
-          kv.kvh = it.kvh;
-          kv.checked = p.checked;
-          kv.err = p.err;
-          kv.err_code = p.err_code;
+          const KvRows kv = kv_rows(p, it);
           if (lane == 0) bulk_wait_done();  // the tensor stores of these rows come first
           __syncwarp();
           repair_rows(p, kv, repair, row, it.k0, lane);
@@ -739,6 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (kSplit) join_parts(p, smem, tmem, B, join, rank);
   if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -749,39 +968,98 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
+// One CTA per SM (the shared memory admits no second): SMs of a device, and
+// clusters of 2, 4, 8 and 16 CTAs that it holds at once.
+struct Room {
+  std::atomic<int> sms;
+  int clusters[4];
+};
+
 template <int kMode>
 cudaError_t launch_mode(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                         const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
-  // one CTA per SM (the shared memory admits no second), never more than
-  // items; per device: the SM count, once the kernel's shared-memory limit is set
-  static std::atomic<int> sms[64];
+  if (p.tile_rows <= 0 || p.tile_rows > kRowTile || p.tile_rows % p.G != 0)
+    return cudaErrorInvalidValue;
+  auto kernel = prefill_scored_kernel<kMode, false>, split = prefill_scored_kernel<kMode, true>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {};
+  cfg.attrs = attr;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+
+  static Room rooms[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int n = dev < 64 ? sms[dev].load() : 0;
-  if (n == 0) {
-    e = cudaFuncSetAttribute(prefill_scored_kernel<kMode>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) sms[dev].store(n);
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  Room& room = rooms[dev];
+  if (room.sms.load(std::memory_order_acquire) == 0) {
+    static std::mutex once;
+    std::lock_guard<std::mutex> lock(once);
+    if (room.sms.load() == 0) {
+      int n = 0;
+      for (auto f : {kernel, split})
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(split, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+      if (e != cudaSuccess) return e;
+      for (int i = 0; i < 4; ++i) {
+        attr[0].val.clusterDim.x = 2u << i;
+        cfg.gridDim = dim3(2u << i);
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&room.clusters[i], split, &cfg) != cudaSuccess) {
+          room.clusters[i] = 0;  // no clusters of this size
+          cudaGetLastError();
+        }
+      }
+      room.sms.store(n, std::memory_order_release);
+    }
   }
-  if (p.tile_rows <= 0 || p.tile_rows > kRowTile || p.tile_rows % p.G != 0)
-    return cudaErrorInvalidValue;
+  const int n = room.sms.load(std::memory_order_acquire);
+
   const int64_t row_tiles =
       (static_cast<int64_t>(p.max_q) * p.G + 2 * p.tile_rows - 1) / (2 * p.tile_rows);
   const int64_t items = row_tiles * p.Hkv * p.num_seqs;
   if (items <= 0) return cudaSuccess;
   if (items > INT32_MAX) return cudaErrorInvalidValue;
-  // on demand over a grid of one CTA an item, or in rounds over one CTA an SM
   const int64_t bound = static_cast<int64_t>(p.num_tokens) * p.G / (2 * p.tile_rows) + p.num_seqs;
   const int64_t pairs = bound < row_tiles * p.num_seqs ? bound : row_tiles * p.num_seqs;
+  const bool listable = pairs <= kListMax && row_tiles * p.num_seqs <= kListScan;
   PrefillParams pl = p;
-  pl.list = pairs <= kListMax && row_tiles * p.num_seqs <= kListScan && pairs * p.Hkv > n;
-  const int grid = static_cast<int>(pl.list ? pairs * p.Hkv : items < n ? items : n);
-  return launch_pdl(prefill_scored_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, stream,
-                    tk, tv, tq, to, pl);
+  pl.split = 1;
+  // few items: the largest cluster an item that the device holds for all of them
+  // at once, and whose parts the key tiles (at most) are enough for
+  int64_t span = static_cast<int64_t>(p.max_blocks) * p.bs;
+  if (p.sp.window > 0) span = std::min<int64_t>(span, int64_t{p.sp.window} + 2 * p.tile_rows / p.G);
+  const int64_t most = span / kKeys + 1;
+  for (int i = 3; i >= 0 && pl.split == 1; --i)
+    if ((listable ? pairs * p.Hkv : items) <= room.clusters[i] && most >= kJoinTiles &&
+        most > (1 << i))
+      pl.split = 2 << i;
+  int64_t grid;
+  if (pl.split > 1) {
+    pl.list = listable && items > room.clusters[__builtin_ctz(pl.split) - 1];
+    grid = (pl.list ? pairs * p.Hkv : items) * pl.split;
+  } else {
+    // on demand over a grid of one CTA an item, or in rounds over one CTA an SM
+    pl.list = listable && pairs * p.Hkv > n;
+    grid = pl.list ? pairs * p.Hkv : std::min<int64_t>(items, n);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  int attrs = 0;
+  if (pl.split > 1) attr[attrs++].val.clusterDim.x = static_cast<unsigned>(pl.split);
+  if (pdl_enabled()) {
+    attr[attrs] = {};
+    attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[attrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.numAttrs = static_cast<unsigned>(attrs);
+  return cudaLaunchKernelEx(&cfg, pl.split > 1 ? split : kernel, tk, tv, tq, to, pl);
 }
 
 }  // namespace

@@ -94,6 +94,7 @@ struct ScoredBars {
   uint32_t tmem;        // tensor-memory address
   volatile int abort;   // a wait gave up
   int pairs;            // of the sorted list
+  int joined;           // the cluster's item is in parts
 };
 
 // The row's running maximum takes in the tile's; O and l are rescaled when it
@@ -144,6 +145,17 @@ __device__ __forceinline__ void chunk_max(const uint32_t (&a)[32], uint32_t bits
     }
     mx[i & 3] = fmax3(mx[i & 3], x0, x1);
   }
+}
+
+// The largest product of the columns in `bits`.  (The others hold whatever
+// stands in rows of K that were not loaded: no choice may hang on it.)
+__device__ __forceinline__ float seen_abs_max(const uint32_t (&a)[32], uint32_t bits) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    top = umma::fmax3_abs(top, bit_of(bits, 2 * i) ? __uint_as_float(a[2 * i]) : 0.f,
+                          bit_of(bits, 2 * i + 1) ? __uint_as_float(a[2 * i + 1]) : 0.f);
+  return top;
 }
 
 // P = 2^f, packed into pk[0..15], summed into ls: where columns are masked, as
@@ -379,11 +391,7 @@ __device__ __forceinline__ void tile_general(const PrefillParams& p, const Cappe
     uint32_t a[32];
     tmem_ld32(a, s_tm + 32 * c);
     tmem_wait_ld(a);
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      top = fmax3_abs(top, __uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
-    if (p.sp.cap2 > 0.f && !__all_sync(kFull, top <= p.cap.s_max)) {
+    if (p.sp.cap2 > 0.f && !__all_sync(kFull, seen_abs_max(a, bits) <= p.cap.s_max)) {
 #pragma unroll
       for (int e = 0; e < 32; ++e)
         a[e] = __float_as_uint(capped_score(p.sp, __uint_as_float(a[e]) * p.qscale));
@@ -433,14 +441,13 @@ __device__ __forceinline__ void tile_general(const PrefillParams& p, const Cappe
 }
 
 // Under the cap, in one pass: the polynomial, or, where a half tile holds a
-// score out of its range, the exponentials.  In a whole tile the half's sum of
-// P tells: past the range the polynomial keeps rising (falling), so one product
-// above the cap alone makes the sum p_high or more, and products below -cap,
-// whatever the polynomial gives for them, are lost in a sum of p_low or more
-// (64 of them are under 2^-12 of it).  A masked half is looked at first
-// (against exponentials for every masked half: 8 x 2048 tokens, caps 50 and 15,
-// 274 and 564 us for 277 and 523; under a window of 500 174 for 179; the whole
-// tiles' test by their largest product instead of their sum: 300 for 270).
+// score out of its range, the exponentials.  Past the range the polynomial
+// keeps rising (falling), so the sum of P that a row takes from a half tells:
+// one product above the cap alone makes it p_high or more, and products below
+// -cap, whatever the polynomial gives for them, are lost in a sum of p_low or
+// more (64 of them are under 2^-12 of it).  Masked columns add 0, so that
+// nothing that stands in them can sway the choice.  (By the largest product
+// instead, 8 x 2048 tokens took 300 us for 270.)
 __device__ __forceinline__ void tile_capped(const PrefillParams& p, const CappedRegs& k,
                                             const ScoredRow& r, uint32_t s_tm, int kt,
                                             SoftState& st) {
@@ -493,27 +500,27 @@ __device__ __forceinline__ void tile_capped(const PrefillParams& p, const Capped
       if (h == 0 ? mask.none[0] : mask.none[1]) {
         zero_p(pk);
       } else {
-        uint32_t a[32], b[32];
-        load_half(a, b, s_tm + 64 * h);
-        uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+        const uint32_t bits0 = mask.bits(2 * h), bits1 = mask.bits(2 * h + 1);
+        float sum = 0.f;
         bool near = !mask.whole;
         if (near) {
-          float top = 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            top = fmax3_abs(top, __uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
-            top = fmax3_abs(top, __uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
-          }
-          near = __all_sync(kFull, top <= p.cap.s_max);
+          uint32_t a[32], b[32];
+          load_half(a, b, s_tm + 64 * h);
+          uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+          chunk_p<true>(a, bits0, poly, pk, ls);
+          chunk_p<true>(b, bits1, poly, pk + 16, ls);
+          sum = sum_of(ls);
+          near = __all_sync(kFull, in_range(sum) || (bits0 | bits1) == 0u);
         }
-        if (near) {
-          chunk_p<true>(a, mask.bits(2 * h), poly, pk, ls);
-          chunk_p<true>(b, mask.bits(2 * h + 1), poly, pk + 16, ls);
-        } else {
-          chunk_p<true>(a, mask.bits(2 * h), far, pk, ls);
-          chunk_p<true>(b, mask.bits(2 * h + 1), far, pk + 16, ls);
+        if (!near) {
+          uint32_t a[32], b[32];
+          load_half(a, b, s_tm + 64 * h);
+          uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+          chunk_p<true>(a, bits0, far, pk, ls);
+          chunk_p<true>(b, bits1, far, pk + 16, ls);
+          sum = sum_of(ls);
         }
-        st.l += sum_of(ls);
+        st.l += sum;
       }
       tmem_st32(s_tm + 32 * h, pk);
     }

@@ -139,6 +139,63 @@ def test_long_chunks(name):
     assert_close(s.call(**kw), *s.reference(**ref), what=name)
 
 
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (7, 1), (4, 4)])
+@pytest.mark.parametrize("name", ["plain", "cap", "small cap", "window 100", "slopes", "documents", "all"])
+@pytest.mark.parametrize("contig", [False, True])
+def test_few_tokens_after_many(name, hq, hkv, contig):
+    """Few work items with many key tiles: several CTAs share an item."""
+    for cached, new in (([4000], [1]), ([3000, 0], [70, 3]), ([257, 2600, 0], [40, 1, 0])):
+        s = Chunks(cached, new, hq, hkv, 16, contig, seed=hq + len(cached))
+        ref, kw = make(name, s)
+        assert_close(s.call(**kw), *s.reference(**ref), what=name)
+
+
+def test_few_tokens_after_many_poisoned_captured_and_side_by_side():
+    s = Chunks([4000, 1500], [33, 2], 8, 2, 16, seed=31)
+    first = torch.tensor([0] * 10 + [2500] * 23 + [700, 1200], dtype=torch.int32, device=DEV)
+    want = s.reference(first=first, softcap=30.0)
+    k, v = s.poison([(0, 4032), (700, 1501)])
+    bad = (int(s.where[0, 1000 // 16]), 1000 % 16)  # seen by the first ten tokens alone
+    k[bad[0], :, bad[1]] = v[bad[0], :, bad[1]] = float("nan")
+    got = s.call(k=k, v=v, softcap=30.0, first_key=first)
+    assert bool(torch.isnan(got[:10]).all())
+    assert_close(got[10:], want[0][10:], want[1][10:])
+    k[bad[0], :, bad[1]] = s.k[bad[0], :, bad[1]]
+    v[bad[0], :, bad[1]] = s.v[bad[0], :, bad[1]]
+    out = torch.empty(s.T, 8, D, dtype=torch.bfloat16, device=DEV)
+    kw = dict(softcap=30.0, first_key=first)
+    s.call(k=k, v=v, out=out, **kw)
+    assert_close(out, *want)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        s.call(k=k, v=v, out=out, **kw)
+    other = torch.empty_like(out)
+    for _ in range(5):
+        out.fill_(7.0)
+        other.fill_(7.0)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            s.call(k=k, v=v, out=other, **kw)
+        graph.replay()
+        torch.cuda.current_stream().wait_stream(side)
+        assert_close(out, *want)
+        assert torch.equal(out, other)
+
+
+@pytest.mark.parametrize("cap", [20.0, 200.0])
+def test_results_do_not_hang_on_what_stands_in_shared_memory(cap):
+    """The same bits whatever the kernel before left behind for masked columns."""
+    s = Chunks([40, 300, 5], [100, 30, 260], 32, 8, 16, seed=33, by=1.0)
+    big = Chunks([0], [600], 32, 8, 16, seed=34, by=400.0)
+    big.k *= 20.0
+    kw = dict(softcap=cap, window=90)
+    want = s.call(**kw)
+    for _ in range(3):
+        big.call(softcap=cap)
+        assert torch.equal(s.call(**kw), want)
+
+
 RAGGED = ([0, 3, 700, 0, 64, 900, 17, 0, 5, 300, 0, 2], [0, 1, 500, 64, 65, 3, 700, 129, 0, 40, 900, 5])
 
 

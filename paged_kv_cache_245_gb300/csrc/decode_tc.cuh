@@ -41,6 +41,7 @@
 
 #include "decode_tc_launch.h"
 #include "pkv_device.cuh"
+#include "score.cuh"
 
 namespace pkv {
 

@@ -7,7 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "score.cuh"
+#include "score.h"
 
 namespace pkv {
 

@@ -10,18 +10,9 @@
 #include <stdint.h>
 
 #include "pkv_device.cuh"
+#include "score.h"
 
 namespace pkv {
-
-struct ScoreParams {
-  float cap2;                // softcap * log2 e; 0: no cap
-  float inv_cap2;            // 1 / cap2
-  float cap_k;               // 2 / softcap
-  int32_t window;            // 0: none
-  const float* slopes;       // [Hq], or null
-  const int32_t* first_key;  // decode [B], prefill [T], or null
-  const int32_t* prefix;     // [B], or null (prefill)
-};
 
 constexpr float kLog2e = 1.4426950408889634f;
 // Slope of head h in log-2 units per position.  Past 2^60 either way it would

@@ -260,9 +260,22 @@ __device__ __forceinline__ void zero_p(uint32_t (&pk)[32]) {
   for (int i = 0; i < 32; ++i) pk[i] = 0u;
 }
 
+// The largest raw product of 32 columns.
+template <bool kMask>
+__device__ __forceinline__ float chunk_top(const uint32_t (&a)[32], uint32_t bits) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  chunk_max<kMask>(a, bits, [](int, uint64_t s2) { return s2; }, mx);
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
 // A tile against the running maximum; scale >= 0, no cap.  Two passes over S:
 // with the row held in registers between them the kernel spills (measured a
 // quarter slower).
+//
+// With a bias the maximum is a bound: the largest product of 32 columns and
+// their largest bias, at most 31 slopes above the largest score (2^-62 keeps P
+// far from underflow; steeper slopes take the scores one by one).  The scores'
+// own maximum costs two more operations a pair (8 x 2048 tokens 305 us).
 template <int kMode>
 __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const ScoredRow& r,
                                                  uint32_t s_tm, uint32_t o_tm, int kt, bool first,
@@ -272,31 +285,42 @@ __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const S
   const TileMask mask = tile_mask(r, kt);
   const uint64_t sc2 = f2_pack(__float_as_uint(p.qscale), __float_as_uint(p.qscale));
   const float at = static_cast<float>(r.pos - kt);  // distance of column 0
-  auto raw = [](int, uint64_t s2) { return s2; };
-  float mx[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
   uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
   // past a row's own position (seen under a prefix only) the distance grows
   // again; up to it the bias is linear in the column
   const bool bent = kBias && __any_sync(kFull, r.hi > r.pos && r.pos < kt + 127);
-  if (mask.whole && !bent) {
+  const bool steep = kBias && __any_sync(kFull, fabsf(r.slope2) > 2.f);
+  // the largest score there can be in columns c .. c + 31, by their largest product
+  auto bound = [&](float top, int c) {
+    if (!kBias) return top * p.qscale;
+    const float d0 = fabsf(at - c), d1 = fabsf(at - (c + 31));
+    const float far = fmaxf(d0, d1);
+    const float near = at >= c && at <= c + 31 ? 0.f : fminf(d0, d1);
+    return fmaf(top, p.qscale, -r.slope2 * (r.slope2 >= 0.f ? near : far));
+  };
+  if (mask.whole && !bent && !steep) {
     // Loads of S take 335 to 375 cycles.  The maximum comes from one load of
     // the row; its last chunk stays in registers, and the others come again,
     // each during the exponentials of the one before.
     Row128 s(s_tm);
-    BiasPairs bias(-r.slope2 * at, r.slope2);
-    auto max_f = [&](int i, uint64_t s2) { return kBias ? f2_fma(s2, sc2, bias.next(i)) : s2; };
-    chunk_max<false>(s.a, 0u, max_f, mx);
-    chunk_max<false>(s.b, 0u, max_f, mx);
-    chunk_max<false>(s.c, 0u, max_f, mx);
-    chunk_max<false>(s.d, 0u, max_f, mx);
-    const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    const float m = take_max(kBias ? tmax : tmax * p.qscale, first, o_tm, st);
+    float tmax;
+    if (kBias) {
+      tmax = fmaxf(fmaxf(bound(chunk_top<false>(s.a, 0u), 0), bound(chunk_top<false>(s.b, 0u), 32)),
+                   fmaxf(bound(chunk_top<false>(s.c, 0u), 64), bound(chunk_top<false>(s.d, 0u), 96)));
+    } else {
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto raw = [](int, uint64_t s2) { return s2; };
+      chunk_max<false>(s.a, 0u, raw, mx);
+      chunk_max<false>(s.b, 0u, raw, mx);
+      chunk_max<false>(s.c, 0u, raw, mx);
+      chunk_max<false>(s.d, 0u, raw, mx);
+      tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
+    }
+    const float m = take_max(tmax, first, o_tm, st);
     uint32_t x[32], y[32], p0[32], p1[32];
     tmem_ld32(x, s_tm);
     const uint64_t nm2 = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
-    bias = BiasPairs(fmaf(-r.slope2, at - 96.f, -m), r.slope2);
+    BiasPairs bias(fmaf(-r.slope2, at - 96.f, -m), r.slope2);
     auto f = [&](int i, uint64_t s2) { return f2_fma(s2, sc2, kBias ? bias.next(i) : nm2); };
     chunk_p<false>(s.d, 0u, f, p1 + 16, ls);
     bias = BiasPairs(fmaf(-r.slope2, at, -m), r.slope2);
@@ -323,27 +347,23 @@ __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const S
       return f2_pack(__float_as_uint(x0), __float_as_uint(x1));
     };
   };
+  float tmax = -INFINITY;
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     if (h == 0 ? mask.none[0] : mask.none[1]) continue;
     uint32_t a[32], b[32];
     load_half(a, b, s_tm + 64 * h);
-    const float from = at - 64.f * h;
-    if (kBias && !bent) {
-      BiasPairs bias(-r.slope2 * from, r.slope2);
-      auto biased = [&](int i, uint64_t s2) { return f2_fma(s2, sc2, bias.next(i)); };
-      chunk_max<true>(a, mask.bits(2 * h), biased, mx);
-      chunk_max<true>(b, mask.bits(2 * h + 1), biased, mx);
-    } else if (kBias) {
-      chunk_max<true>(a, mask.bits(2 * h), exactly(from, 0.f), mx);
-      chunk_max<true>(b, mask.bits(2 * h + 1), exactly(from - 32.f, 0.f), mx);
+    if (steep) {
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      chunk_max<true>(a, mask.bits(2 * h), exactly(at - 64.f * h, 0.f), mx);
+      chunk_max<true>(b, mask.bits(2 * h + 1), exactly(at - 64.f * h - 32.f, 0.f), mx);
+      tmax = fmaxf(tmax, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
     } else {
-      chunk_max<true>(a, mask.bits(2 * h), raw, mx);
-      chunk_max<true>(b, mask.bits(2 * h + 1), raw, mx);
+      tmax = fmaxf(tmax, fmaxf(bound(chunk_top<true>(a, mask.bits(2 * h)), 64 * h),
+                               bound(chunk_top<true>(b, mask.bits(2 * h + 1)), 64 * h + 32)));
     }
   }
-  const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-  const float m = take_max(kBias ? tmax : tmax * p.qscale, first, o_tm, st);
+  const float m = take_max(tmax, first, o_tm, st);
   const uint64_t nm2 = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
   auto plain = [&](int, uint64_t s2) { return f2_fma(s2, sc2, nm2); };
 #pragma unroll 1

@@ -196,6 +196,18 @@ def test_results_do_not_hang_on_what_stands_in_shared_memory(cap):
         assert torch.equal(s.call(**kw), want)
 
 
+@pytest.mark.parametrize("name", ["plain", "documents", "prefix", "cap", "window 100"])
+def test_slopes_of_any_size(name):
+    """From none to so steep that a row sees one key, rising instead of falling too."""
+    s = Chunks([0, 500, 30], [400, 33, 200], 16, 4, 16, seed=41)
+    slopes = torch.tensor([0.0, 1e-6, 0.3, 1.3, 0.5, 1.0, 1.38, 1.4, 3.0, 100.0, 2.0, 0.1,
+                           -0.01, -0.5, -4.0, 1e4], device=DEV)
+    ref, kw = make(name, s)
+    ref["slopes"] = kw["alibi_slopes"] = slopes
+    want, tol = s.reference(**ref)
+    assert_close(s.call(**kw), want, tol)
+
+
 RAGGED = ([0, 3, 700, 0, 64, 900, 17, 0, 5, 300, 0, 2], [0, 1, 500, 64, 65, 3, 700, 129, 0, 40, 900, 5])
 
 

@@ -49,8 +49,15 @@ struct PrefillParams {
 
 // What the scored kernel (prefill_scored.cu) computes: scores masked by a
 // window, documents or prefixes; capped (and masked) against a fixed offset in
-// place of the running maximum; biased (and masked); or any of them.
-enum PrefillMode { kPrefillMasked, kPrefillCapped, kPrefillBiased, kPrefillGeneral };
+// place of the running maximum; biased (and masked); capped and biased; or any
+// score (caps above 52, which leave the offset's range, and negative scales).
+enum PrefillMode {
+  kPrefillMasked,
+  kPrefillCapped,
+  kPrefillBiased,
+  kPrefillCappedBiased,
+  kPrefillGeneral
+};
 
 // The K or V cache ([rows][128] bf16) as a 4-D tensor (64 columns, 8 rows,
 // 2 column halves, row groups of 8) whose boxes of run_rows rows land in

@@ -360,6 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
+  // The first key (from k0) of the j-th key tile an item takes.  With a bias the
+  // last come first: the nearest keys set the running maximum, and O is not
+  // rescaled at every tile on the way to them.
+  auto tile_key = [](const Item& it, int j) -> int {
+    constexpr bool kLastFirst = kMode == kPrefillBiased || kMode == kPrefillCappedBiased;
+    return (kLastFirst ? it.ntiles - 1 - j : j) * kKeys;
+  };
   // Rows and positions of row tile pair rt of a sequence; false where its rows
   // lie past the chunk or, checked, the sequence is left unwritten.
   const int R = (p.max_q * G + 2 * TR - 1) / (2 * TR);
@@ -485,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int prun = lane & 15;    // lanes 0-15 copy K of run prun, lanes 16-31 V
     // block-table entry of run prun of tile j of `it` (-1: outside the visible positions or rejected)
     auto entry = [&](const Item& it, int j) -> int32_t {
-      const int kpos = it.k0 + j * kKeys + prun * run;
+      const int kpos = it.k0 + tile_key(it, j) + prun * run;
       int32_t e = -1;
       if (prun < runs && kpos < it.ctx && kpos + run > it.klo) {
         e = p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks + kpos / p.bs];
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < cur.ntiles; ++j) {
         const int s = g & 1;
         const uint32_t loaded = __popc(__ballot_sync(kFull, lane < 16 && e >= 0));
-        const int off = (cur.k0 + j * kKeys + prun * run) % p.bs;
+        const int off = (cur.k0 + tile_key(cur, j) + prun * run) % p.bs;
         const int32_t grp =
             e >= 0 ? static_cast<int32_t>(cache_row(e, cur.kvh, p.Hkv, p.bs, off) >> 3) : 0;
         unsigned char* dst = smem + kOffK + s * kStageBytes + prun * run * kRowBytes;
@@ -872,11 +879,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
         if (!ok) break;
         tc_fence_after();
-        scored_tile<kMode>(p, cap_regs, row, s_tm, o_tm, j * kKeys, j == 0, st);
+        scored_tile<kMode>(p, cap_regs, row, s_tm, o_tm, tile_key(it, j), j == 0, st);
         // V rows that no row sees (stale or foreign bytes) must not meet a
         // zero probability: zeroed once the tile has landed, before P is
         // handed over
-        const int k0 = it.k0 + j * kKeys;
+        const int k0 = it.k0 + tile_key(it, j);
         if (t == 0 && (it.klo > k0 || it.ctx < k0 + kKeys)) {
           const int z0 = it.klo > k0 ? min(it.klo - k0, kKeys) : 0;
           const int z1 = max(min(it.ctx - k0, kKeys), z0);
@@ -1074,8 +1081,8 @@ uint64_t pair_of(float x) {
 
 // The polynomial of a cap, where a raw product at the cap (cap / scale) has an
 // eighth power that neither overflows nor underflows in fp32 (else s_max is
-// negative: no product is in range).  Returns whether the capped kernel serves these
-// scores: no bias, and a cap whose range fits the fixed offset.
+// negative: no product is in range).  Returns whether the capped kernels serve
+// the cap: one whose range fits the fixed offset.
 bool capped_constants(const PrefillParams& p, CappedScore* c) {
   const ScoreParams& sp = p.sp;
   std::memset(c, 0, sizeof *c);
@@ -1089,7 +1096,7 @@ bool capped_constants(const PrefillParams& p, CappedScore* c) {
     power *= r * r;
   }
   c->s_max = poly ? std::fabs(1.f / r) : -1.f;
-  if (!poly || sp.cap2 > 75.f || sp.slopes != nullptr) return false;
+  if (!poly || sp.cap2 > 75.f) return false;
   // the offset m: the lowest score (-cap) keeps 2^-100
   const float m = sp.cap2 <= 50.f ? sp.cap2 : 100.f - sp.cap2;
   c->neg_m2 = pair_of(-m);
@@ -1114,7 +1121,9 @@ cudaError_t launch_prefill_scored(const CUtensorMap& tk, const CUtensorMap& tv,
     return p.sp.slopes == nullptr ? launch_mode<kPrefillMasked>(tk, tv, tq, to, p, stream)
                                   : launch_mode<kPrefillBiased>(tk, tv, tq, to, p, stream);
   if (capped_constants(p, &p.cap))
-    return launch_mode<kPrefillCapped>(tk, tv, tq, to, p, stream);
+    return p.sp.slopes == nullptr
+               ? launch_mode<kPrefillCapped>(tk, tv, tq, to, p, stream)
+               : launch_mode<kPrefillCappedBiased>(tk, tv, tq, to, p, stream);
   return launch_mode<kPrefillGeneral>(tk, tv, tq, to, p, stream);
 }
 

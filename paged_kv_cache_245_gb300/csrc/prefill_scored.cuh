@@ -60,7 +60,7 @@ struct CappedRegs {
 template <int kMode>
 __device__ __forceinline__ CappedRegs capped_regs(const PrefillParams& p) {
   CappedRegs k;
-  if (kMode == kPrefillCapped || kMode == kPrefillGeneral) {
+  if (kMode == kPrefillCapped || kMode == kPrefillCappedBiased || kMode == kPrefillGeneral) {
 #pragma unroll
     for (int i = 0; i < 5; ++i) asm volatile("mov.b64 %0, %1;" : "=l"(k.c[i]) : "l"(p.cap.c[i]));
     asm volatile("mov.b64 %0, %1;" : "=l"(k.neg_m2) : "l"(p.cap.neg_m2));
@@ -155,6 +155,14 @@ __device__ __forceinline__ float seen_abs_max(const uint32_t (&a)[32], uint32_t 
   for (int i = 0; i < 16; ++i)
     top = umma::fmax3_abs(top, bit_of(bits, 2 * i) ? __uint_as_float(a[2 * i]) : 0.f,
                           bit_of(bits, 2 * i + 1) ? __uint_as_float(a[2 * i + 1]) : 0.f);
+  return top;
+}
+
+__device__ __forceinline__ float abs_max(const uint32_t (&a)[32]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    top = umma::fmax3_abs(top, __uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
   return top;
 }
 
@@ -551,12 +559,117 @@ __device__ __forceinline__ void tile_capped(const PrefillParams& p, const Capped
   }
 }
 
+// Capped and biased, in one pass: a score is at most the cap and the bias of
+// the key the row sees at the smallest distance (at the largest, where the
+// slope is negative), and its largest is at least -cap and that bias.  So the
+// running maximum is that bias alone, known without S, and the cap's offset
+// keeps P in range as it does without a bias.
+__device__ __forceinline__ void tile_capped_biased(const PrefillParams& p, const CappedRegs& k,
+                                                   const ScoredRow& r, uint32_t s_tm,
+                                                   uint32_t o_tm, int kt, bool first,
+                                                   SoftState& st) {
+  using namespace umma;
+  const TileMask mask = tile_mask(r, kt);
+  const int ati = r.pos - kt;  // distance of column 0
+  const float at = static_cast<float>(ati);
+  const int near_d = max(max(mask.c0 - ati, ati - mask.c1), 0);
+  const int far_d = max(abs(ati - mask.c0), abs(ati - mask.c1));
+  const float top_bias =
+      mask.c0 <= mask.c1 ? -r.slope2 * static_cast<float>(r.slope2 >= 0.f ? near_d : far_d)
+                         : -INFINITY;
+  const float m = take_max(top_bias, first, o_tm, st);
+  const bool bent = __any_sync(kFull, r.hi > r.pos && r.pos < kt + 127);
+  float neg_m, unused;
+  f2_unpack(k.neg_m2, neg_m, unused);
+  BiasPairs bias(0.f, 0.f);
+  auto poly = [&](int i, uint64_t s2) {
+    const uint64_t w2 = f2_mul(s2, s2);
+    uint64_t q = f2_fma(w2, k.c[4], k.c[3]);
+    q = f2_fma(w2, q, k.c[2]);
+    q = f2_fma(w2, q, k.c[1]);
+    q = f2_fma(w2, q, k.c[0]);
+    return f2_fma(s2, q, bias.next(i));
+  };
+  // (bias - m, at 64 h, of a row whose bias is linear over the tile)
+  auto linear = [&](int h) { return BiasPairs(fmaf(-r.slope2, at - 64.f * h, neg_m - m), r.slope2); };
+  bool done[2] = {false, false};
+  uint32_t p1[32];
+  float sum1 = 0.f;
+  if (mask.whole && !bent) {
+    uint32_t x[32], y[32], p0[32];
+    uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+    load_half(x, y, s_tm);
+    bias = linear(0);
+    const float top0 = fmaxf(abs_max(x), abs_max(y));
+    chunk_p<false>(x, 0u, poly, p0, ls);
+    chunk_p<false>(y, 0u, poly, p0 + 16, ls);
+    done[0] = __all_sync(kFull, top0 <= p.cap.s_max);
+    if (done[0]) {
+      tmem_st32(s_tm, p0);
+      st.l += sum_of(ls);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ls[i] = 0ull;
+    load_half(x, y, s_tm + 64);
+    bias = linear(1);
+    const float top1 = fmaxf(abs_max(x), abs_max(y));
+    chunk_p<false>(x, 0u, poly, p1, ls);
+    chunk_p<false>(y, 0u, poly, p1 + 16, ls);
+    sum1 = sum_of(ls);
+    done[1] = __all_sync(kFull, top1 <= p.cap.s_max);
+  }
+  if (!done[0] || !done[1]) {
+    auto each = [&](float from) {
+      return [=, &p, &r](int i, uint64_t s2) {
+        float x0, x1;
+        f2_unpack(s2, x0, x1);
+        const float b0 = fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i)), -m);
+        const float b1 = fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i + 1)), -m);
+        x0 = fmaf(p.cap.neg_2cap, fast_rcp(1.f + fast_exp2(x0 * p.cap.exp_k)), p.cap.cap_m);
+        x1 = fmaf(p.cap.neg_2cap, fast_rcp(1.f + fast_exp2(x1 * p.cap.exp_k)), p.cap.cap_m);
+        return f2_pack(__float_as_uint(x0 + b0), __float_as_uint(x1 + b1));
+      };
+    };
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      if (h == 0 ? done[0] : done[1]) continue;
+      uint32_t pk[32];
+      if (h == 0 ? mask.none[0] : mask.none[1]) {
+        zero_p(pk);
+      } else {
+        const uint32_t bits0 = mask.bits(2 * h), bits1 = mask.bits(2 * h + 1);
+        uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t a[32], b[32];
+        load_half(a, b, s_tm + 64 * h);
+        const bool near = !mask.whole && !bent &&
+                          fmaxf(seen_abs_max(a, bits0), seen_abs_max(b, bits1)) <= p.cap.s_max;
+        if (__all_sync(kFull, near)) {
+          bias = linear(h);
+          chunk_p<true>(a, bits0, poly, pk, ls);
+          chunk_p<true>(b, bits1, poly, pk + 16, ls);
+        } else {
+          chunk_p<true>(a, bits0, each(at - 64.f * h), pk, ls);
+          chunk_p<true>(b, bits1, each(at - 64.f * h - 32.f), pk + 16, ls);
+        }
+        st.l += sum_of(ls);
+      }
+      tmem_st32(s_tm + 32 * h, pk);
+    }
+  }
+  if (done[1]) {  // (over S of the first half, which is read by now)
+    tmem_st32(s_tm + 32, p1);
+    st.l += sum1;
+  }
+}
+
 // One key tile: kt is its first key counted from the item's.
 template <int kMode>
 __device__ __forceinline__ void scored_tile(const PrefillParams& p, const CappedRegs& k, const ScoredRow& r,
                                             uint32_t s_tm, uint32_t o_tm, int kt, bool first,
                                             SoftState& st) {
   if constexpr (kMode == kPrefillCapped) tile_capped(p, k, r, s_tm, kt, st);
+  else if constexpr (kMode == kPrefillCappedBiased)
+    tile_capped_biased(p, k, r, s_tm, o_tm, kt, first, st);
   else if constexpr (kMode == kPrefillGeneral) tile_general(p, k, r, s_tm, o_tm, kt, first, st);
   else tile_running_max<kMode>(p, r, s_tm, o_tm, kt, first, st);
 }

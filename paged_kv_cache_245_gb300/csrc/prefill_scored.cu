@@ -248,7 +248,7 @@ static __device__ __noinline__ void join_parts(const PrefillParams& p, unsigned 
                                                const Join& join, int rank) {
   constexpr int kMost = 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int TR = p.tile_rows, G = p.G, n = p.split;
+  const int TR = p.tile_rows, n = p.split;
   __syncwarp();
   cluster_sync();
   const bool on = __all_sync(

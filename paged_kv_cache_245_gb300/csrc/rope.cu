@@ -17,9 +17,10 @@
 // loaded while the one before it is turned, the first while the sines are
 // computed; five CTAs an SM keep 80 KiB of rows in flight (three, with the
 // registers left alone: 5.4 for 4.2 us at 333 tokens of an odd rotary size).
-// 16384 tokens of 32 + 2 x 8 heads (403 MB) take 65.8 us, 6.1 TB/s or 0.90 of a
-// plain copy; 64 tokens 3.1 us and one 2.7 us, a launch and three dependent
-// reads (position, sines, row).
+// The sines are padded so that a row's lanes read different banks (4096 tokens
+// 20.5 -> 16.0 us).  16384 tokens of 32 + 2 x 8 heads (403 MB) take 64.6 us, 6.2
+// TB/s or 0.92 of a plain copy; 64 tokens 3.2 us and one 2.6 us, a launch and
+// three dependent reads (position, sines, row).
 #include "rope.cuh"
 
 #include "pkv_device.cuh"
@@ -41,6 +42,10 @@ __device__ __forceinline__ uint4 ld_row16(const uint16_t* p) {
   return *reinterpret_cast<const uint4*>(p);
 }
 
+// Eight pairs, then 16 bytes of padding: lanes that read 8 pairs apart meet
+// different banks.
+__device__ __forceinline__ constexpr int cs_at(int pair) { return pair + (pair >> 3) * 2; }
+
 // A row's two chunks of this lane, its token of the CTA and its row of R.
 struct RopeRow {
   uint4 a, b;
@@ -52,7 +57,8 @@ struct RopeRow {
 // rotary_dim (partners from shared memory, one by one).
 template <int kKind, int kTokens>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const RopeParams p) {
-  __shared__ float2 cs[kTokens][64];   // (cos, sin) times gain of the rotated pairs
+  // (cos, sin) times gain of the rotated pairs; pair i at cs_at(i)
+  __shared__ __align__(16) float2 cs[kTokens][cs_at(64)];
   __shared__ uint32_t rows[kKind == 2 ? kRowsPerPass : 1][66];  // a row of every 8 lanes
   __shared__ int64_t row0[kTokens];    // cache row of KV head 0, or -1: k and v go nowhere
   grid_dependency_trigger();
@@ -108,7 +114,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const Rope
       c.x *= p.rope.gain;
       c.y *= p.rope.gain;
     }
-    cs[tok][i] = c;
+    cs[tok][cs_at(i)] = c;
   }
   if (tid < ntok) {
     const int64_t slot = p.slot_mapping[t0 + tid];
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const Rope
           uint32_t& w = i < 4 ? wa[i] : wb[i - 4];
           const int pair = (i < 4 ? ca : cb) * 4 + (i & 3);
           if (pair < half) {
-            const float2 f = turned(bf16_lo(w), bf16_hi(w), cs[tok][pair]);
+            const float2 f = turned(bf16_lo(w), bf16_hi(w), cs[tok][cs_at(pair)]);
             w = pack_bf16x2(f.x, f.y);
           }
         }
@@ -158,8 +164,9 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const Rope
         if (l < (rd >> 4)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 r0 = turned(bf16_lo(wa[i]), bf16_lo(wb[i]), cs[tok][l * 8 + 2 * i]);
-            const float2 r1 = turned(bf16_hi(wa[i]), bf16_hi(wb[i]), cs[tok][l * 8 + 2 * i + 1]);
+            const float4 f = *reinterpret_cast<const float4*>(&cs[tok][cs_at(l * 8) + 2 * i]);
+            const float2 r0 = turned(bf16_lo(wa[i]), bf16_lo(wb[i]), make_float2(f.x, f.y));
+            const float2 r1 = turned(bf16_hi(wa[i]), bf16_hi(wb[i]), make_float2(f.z, f.w));
             wa[i] = pack_bf16x2(r0.x, r1.x);
             wb[i] = pack_bf16x2(r0.y, r1.y);
           }
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const Rope
             const bool lower = at + b < half;
             const int other = lower ? at + b + half : at + b - half;
             const float y = bf16_lo(elems[other]);
-            const float2 f = cs[tok][lower ? at + b : other];
+            const float2 f = cs[tok][cs_at(lower ? at + b : other)];
             o[b] = lower ? turned(x, y, f).x : turned(y, x, f).y;
           }
           w = pack_bf16x2(o[0], o[1]);
@@ -207,14 +214,14 @@ cudaError_t launch_kind(const RopeParams& p, cudaStream_t stream) {
   const unsigned n = static_cast<unsigned>(p.num_tokens);
   const dim3 block(kRopeThreads);
   // Few tokens: one a CTA, its rows over grid y, so that every row of the call
-  // is in flight at once (400 tokens x 48 rows 4.3 us, two a CTA 5.0).  Past
-  // that a CTA passes over the rows of more tokens: two up to 1024 (700 tokens
-  // 5.9 us, four a CTA 7.1), then four (4096 tokens 20.1 us, eight 19.7; 1024
-  // 7.0, eight 9.2).
-  if (n <= 512)
+  // is in flight at once (305 tokens x 48 rows 3.4 us, two a CTA 3.8; 512 4.4
+  // and 4.1).  Past that a CTA passes over the rows of more tokens: two up to
+  // 2048 (1500 tokens 6.1 us, four a CTA 7.0), then four (4096 tokens 16.2 us,
+  // two 16.5, eight 17.3).
+  if (n <= 400)
     return launch_pdl(rope_append_kernel<kKind, 1>, dim3(n, (R + kRowsPerPass - 1) / kRowsPerPass),
                       block, 0, stream, p);
-  if (n <= 1024)
+  if (n <= 2048)
     return launch_pdl(rope_append_kernel<kKind, 2>, dim3((n + 1) / 2), block, 0, stream, p);
   return launch_pdl(rope_append_kernel<kKind, 4>, dim3(n / 4 + (n % 4 != 0)), block, 0, stream, p);
 }

@@ -10,7 +10,9 @@
  * of one layer as one call.  pkv_paged_prefill_attention /
  * pkv_contig_prefill_attention attend chunks of new tokens causally (prefill).
  * pkv_block_swap moves whole blocks between the device cache and a pool in
- * page-locked host memory (pre-emption by swapping).
+ * page-locked host memory (pre-emption by swapping).  pkv_rope_append is the
+ * append with rotary positions; the *_attention_scored calls are the attention
+ * calls with scores that are capped, biased or masked.
  *
  * Conventions for every call:
  *   - All tensor arguments are DEVICE pointers on the current CUDA device,

@@ -12,9 +12,9 @@
 // us, although one tile in eight takes it.)
 //
 // Capped scores (kPrefillCapped).  |score| <= cap, so no running maximum is
-// needed, and one pass over S does: P is taken against a fixed m, chosen so that the lowest score keeps
-// 2^-100 (26 binary digits above the smallest normal number) and the highest
-// stays at 2^50 or less, and O and l are never rescaled.  The tanh: three
+// needed, and one pass over S does: P is taken against a fixed m, chosen so that
+// the lowest score keeps 2^-100 (26 binary digits above the smallest normal
+// number) and the highest stays at 2^50 or less, and O and l are never rescaled.  The tanh: three
 // special-function operations an element (two exponentials, a reciprocal)
 // would take longer than the tensor cores, and tanh.approx is too coarse
 // (2^-11); so where every score is within the cap (|s| <= cap, |tanh| <= 0.76)
@@ -24,7 +24,10 @@
 // with a larger score take the exponentials.
 //
 // Biased scores (kPrefillBiased).  Up to the row's own position the bias is
-// linear in the column: one packed addition and one fused product a pair.
+// linear in the column: one packed addition and one fused product a pair.  The
+// key tiles come last first, so that the bias only falls (8 x 2048 tokens 288 ->
+// 272 us).  Capped and biased (kPrefillCappedBiased): the bias of the nearest key
+// stands in for the maximum, and again one pass does (522 -> 349 us).
 #pragma once
 
 #include <limits.h>

@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(W * 32, 1)
       for (int i = lane; i < B; i += 32)
         if (tc_vseq(prefix, i, Hkv, p.seg_cost) <= u) a = i;
       a = __reduce_max_sync(kFull, a);
+      if (k == 0) seq_lo = a;
       if (u >= V || a < 0) {
         tile[k] = static_cast<int64_t>(Hkv) * prefix[B];
       } else {
@@ -172,10 +173,8 @@ __global__ void __launch_bounds__(W * 32, 1)
     hi = tile[1];
     if (lane == 0 && warp == 0) cta_run[0] = lo;
     if (lane == 0 && warp == W - 1) cta_run[1] = hi;
-    int a = -1;  // the last sequence whose tiles start at or before lo
-    for (int i = lane; i < B; i += 32)
-      if (static_cast<int64_t>(Hkv) * prefix[i] <= lo) a = i;
-    seq_lo = __reduce_max_sync(kFull, a);
+    // (an empty sequence's units hold no tile: the next one's first)
+    while (lo < hi && static_cast<int64_t>(Hkv) * prefix[seq_lo + 1] <= lo) ++seq_lo;
   }
 
   const uint32_t bs32 = static_cast<uint32_t>(p.bs);  // paged: a 32-bit block size
@@ -466,73 +465,77 @@ __global__ void __launch_bounds__(W * 32, 1)
   }
   __syncthreads();
 
-  // ---- join the pieces of each pair that warps of this CTA share: group n of
-  // pieces (in warp order) and head h are task n G + h, tasks dealt to the warps
-  int task0 = 0;
-  for (int n = 0; n < 2 * W;) {
-    const int pair = piece_pair[n];
-    if (pair < 0) {
-      ++n;
-      continue;
-    }
-    int end = n + 1;  // pieces n .. end - 1 are this pair's (or empty)
-    while (end < 2 * W && (piece_pair[end] == pair || piece_pair[end] < 0)) ++end;
-    for (int hh = 0; hh < G; ++hh, ++task0) {
-      if (task0 % W != warp) continue;
-      // lane j < end - n derives the weight of piece n + j (2 W <= 32 lanes)
-      const int k = n + lane;
-      const bool have = k < end && piece_pair[k] >= 0;
-      const float* rk = piece(k < end ? k >> 1 : 0, k & 1, hh);
-      const float mj = have ? rk[128] : -INFINITY, lj = have ? rk[129] : 0.f;
-      float M = mj;
+  // ---- join the pieces of each pair that warps of this CTA share: pieces in
+  // warp order, lane j's is piece_pair[j] (2 W <= 32); consecutive ones of a pair
+  // are a group, and head h of group g is task g G + h, dealt to the warps
+  const int lane_pair = lane < 2 * W ? piece_pair[lane] : -1;
+  const uint32_t taken = __ballot_sync(kFull, lane_pair >= 0);
+  const uint32_t before = taken & ((1u << lane) - 1u);
+  const int prev_pair = __shfl_sync(kFull, lane_pair, before != 0u ? 31 - __clz(before) : lane);
+  const uint32_t starts =
+      __ballot_sync(kFull, lane_pair >= 0 && (before == 0u || prev_pair != lane_pair));
+  const int tasks = __popc(starts) * G;
+  for (int task = warp; task < tasks; task += W) {
+    const int grp = static_cast<uint32_t>(task) / static_cast<uint32_t>(G);
+    const int hh = task - grp * G;
+    uint32_t rest = starts;
+    for (int k = 0; k < grp; ++k) rest &= rest - 1;
+    const int n = __ffs(rest) - 1;  // pieces n .. end - 1 are this pair's (or empty)
+    rest &= rest - 1;
+    const int end = rest != 0u ? __ffs(rest) - 1 : 2 * W;
+    const int pair = __shfl_sync(kFull, lane_pair, n);
+    // lane j < end - n derives the weight of piece n + j (2 W <= 32 lanes)
+    const int k = n + lane;
+    const bool have = k < end && (taken >> k & 1u);
+    const float* rk = piece(k < end ? k >> 1 : 0, k & 1, hh);
+    const float mj = have ? rk[128] : -INFINITY, lj = have ? rk[129] : 0.f;
+    float M = mj;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-      // (a piece that saw scores of -inf or NaN alone has no maximum: its sum says)
-      const float fj = lj == 0.f ? 0.f : fast_exp2(mj - M);
-      float Ls = lj * fj;
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    // (a piece that saw scores of -inf or NaN alone has no maximum: its sum says)
+    const float fj = lj == 0.f ? 0.f : fast_exp2(mj - M);
+    float Ls = lj * fj;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(kFull, Ls, o);
-      const float wj = Ls != 0.f ? fj / Ls : 0.f;
-      float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(kFull, Ls, o);
+    const float wj = Ls != 0.f ? fj / Ls : 0.f;
+    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int e = n; e < end; ++e) {
-        const float w = __shfl_sync(kFull, wj, e - n);
-        if (piece_pair[e] < 0) continue;
-        const float4 v = *reinterpret_cast<const float4*>(piece(e >> 1, e & 1, hh) + lane * 4);
-        o4.x = fmaf(w, v.x, o4.x);
-        o4.y = fmaf(w, v.y, o4.y);
-        o4.z = fmaf(w, v.z, o4.z);
-        o4.w = fmaf(w, v.w, o4.w);
-      }
-      const float Mr = Ls != 0.f ? M : -INFINITY;
-      // the CTAs cf .. cl that hold tiles of the pair
-      TcSeg sg;
-      sg.seq = static_cast<uint32_t>(pair) / static_cast<uint32_t>(Hkv);
-      sg.kvh = pair - sg.seq * Hkv;
-      const int64_t tiles = prefix[sg.seq + 1] - prefix[sg.seq];
-      sg.pstart = static_cast<int64_t>(Hkv) * prefix[sg.seq] + sg.kvh * tiles;
-      sg.pend = sg.pstart + tiles;
-      sg.x0 = sg.pstart;
-      sg.x1 = sg.pend;
-      int cf = c, cl = c;
-      if (sg.pstart < cta_run[0] || sg.pend > cta_run[1])
-        tc_pair_ctas(sg, prefix, Hkv, p.seg_cost, V, P, &cf, &cl);
-      const int qh = sg.kvh * G + hh;
-      if (cf == cl) {
-        tc_write_out(p, sg.seq, qh, lane, o4, Mr, Ls);
-      } else if (cf != c) {
-        tc_store_piece(p.rec + (static_cast<int64_t>(c) * kTcRecHeads + hh) * kRecStride, p.tag,
-                       lane, o4, Mr, Ls);
-      } else {
-        TcPieceWords next = {};
-        if (tc_range_nonempty(cf + 1, V, P))
-          tc_issue_piece(p.rec + (static_cast<int64_t>(cf + 1) * kTcRecHeads + hh) * kRecStride,
-                         lane, next);
-        if (!tc_merge_pieces(p, sg.seq, qh, hh, cf, cl, V, P, lane, o4, Mr, Ls, next) && lane == 0)
-          record_error(p.err, kErrTimeout);
-      }
+    for (int e = n; e < end; ++e) {
+      const float w = __shfl_sync(kFull, wj, e - n);
+      if (!(taken >> e & 1u)) continue;
+      const float4 v = *reinterpret_cast<const float4*>(piece(e >> 1, e & 1, hh) + lane * 4);
+      o4.x = fmaf(w, v.x, o4.x);
+      o4.y = fmaf(w, v.y, o4.y);
+      o4.z = fmaf(w, v.z, o4.z);
+      o4.w = fmaf(w, v.w, o4.w);
     }
-    n = end;
+    const float Mr = Ls != 0.f ? M : -INFINITY;
+    // the CTAs cf .. cl that hold tiles of the pair
+    TcSeg sg;
+    sg.seq = static_cast<uint32_t>(pair) / static_cast<uint32_t>(Hkv);
+    sg.kvh = pair - sg.seq * Hkv;
+    const int64_t tiles = prefix[sg.seq + 1] - prefix[sg.seq];
+    sg.pstart = static_cast<int64_t>(Hkv) * prefix[sg.seq] + sg.kvh * tiles;
+    sg.pend = sg.pstart + tiles;
+    sg.x0 = sg.pstart;
+    sg.x1 = sg.pend;
+    int cf = c, cl = c;
+    if (sg.pstart < cta_run[0] || sg.pend > cta_run[1])
+      tc_pair_ctas(sg, prefix, Hkv, p.seg_cost, V, P, &cf, &cl);
+    const int qh = sg.kvh * G + hh;
+    if (cf == cl) {
+      tc_write_out(p, sg.seq, qh, lane, o4, Mr, Ls);
+    } else if (cf != c) {
+      tc_store_piece(p.rec + (static_cast<int64_t>(c) * kTcRecHeads + hh) * kRecStride, p.tag,
+                     lane, o4, Mr, Ls);
+    } else {
+      TcPieceWords next = {};
+      if (tc_range_nonempty(cf + 1, V, P))
+        tc_issue_piece(p.rec + (static_cast<int64_t>(cf + 1) * kTcRecHeads + hh) * kRecStride,
+                       lane, next);
+      if (!tc_merge_pieces(p, sg.seq, qh, hh, cf, cl, V, P, lane, o4, Mr, Ls, next) && lane == 0)
+        record_error(p.err, kErrTimeout);
+    }
   }
 }
 

@@ -143,39 +143,39 @@ __global__ void __launch_bounds__(W * 32, 1)
   const int64_t V = tc_vseq(prefix, B, Hkv, p.seg_cost);
   int64_t lo, hi;
   int seq_lo;  // the sequence that holds tile lo
-  {
-    int64_t tile[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int64_t share = static_cast<int64_t>(c) * W + warp + k;
-      const int64_t u = V < (int64_t{1} << 20) && P * W < 4096
-                            ? static_cast<uint32_t>(share * V) / static_cast<uint32_t>(P * W)
-                            : share * V / (static_cast<int64_t>(P) * W);
-      int a = -1;  // the last sequence whose units start at or before u
-      for (int i = lane; i < B; i += 32)
-        if (tc_vseq(prefix, i, Hkv, p.seg_cost) <= u) a = i;
-      a = __reduce_max_sync(kFull, a);
-      if (k == 0) seq_lo = a;
-      if (u >= V || a < 0) {
-        tile[k] = static_cast<int64_t>(Hkv) * prefix[B];
-      } else {
-        const int64_t n = prefix[a + 1] - prefix[a];
-        const int64_t r = u - tc_vseq(prefix, a, Hkv, p.seg_cost);  // < Hkv * (n + seg_cost)
-        const int64_t h = r < (int64_t{1} << 31)
-                              ? static_cast<int64_t>(static_cast<uint32_t>(r) /
-                                                     static_cast<uint32_t>(n + p.seg_cost))
-                              : r / (n + p.seg_cost);
-        const int64_t o = r - h * (n + p.seg_cost) - p.seg_cost;
-        tile[k] = static_cast<int64_t>(Hkv) * prefix[a] + h * n + (o > 0 ? o : 0);
-      }
+  const int64_t share = static_cast<int64_t>(c) * W + warp;
+  if (V < (int64_t{1} << 20) && P * W < 4096) {
+    // in 32 bits, even lanes for the run's start and odd ones for its end (the
+    // general form below takes 1 us longer)
+    const uint32_t units = static_cast<uint32_t>(V), H = Hkv, cost = p.seg_cost;
+    const uint32_t u = (static_cast<uint32_t>(share) + (lane & 1)) * units / (P * W);
+    const uint32_t u0 = __shfl_sync(kFull, u, 0), u1 = __shfl_sync(kFull, u, 1);
+    int a0 = 0, a1 = 0;  // the last sequences whose units start at or before them
+    for (int i = lane; i < B; i += 32) {
+      const uint32_t start = H * (prefix[i] + cost * i);
+      if (start <= u0) a0 = i;
+      if (start <= u1) a1 = i;
     }
-    lo = tile[0];
-    hi = tile[1];
-    if (lane == 0 && warp == 0) cta_run[0] = lo;
-    if (lane == 0 && warp == W - 1) cta_run[1] = hi;
-    // (an empty sequence's units hold no tile: the next one's first)
-    while (lo < hi && static_cast<int64_t>(Hkv) * prefix[seq_lo + 1] <= lo) ++seq_lo;
+    a0 = __reduce_max_sync(kFull, a0);
+    a1 = __reduce_max_sync(kFull, a1);
+    const int a = lane & 1 ? a1 : a0;
+    const uint32_t n = prefix[a + 1] - prefix[a];
+    const uint32_t r = u - H * (prefix[a] + cost * a);
+    const uint32_t h = r / (n + cost), o = r - h * (n + cost);
+    const uint32_t tile = u >= units ? H * prefix[B] : H * prefix[a] + h * n + (o > cost ? o - cost : 0);
+    lo = __shfl_sync(kFull, tile, 0);
+    hi = __shfl_sync(kFull, tile, 1);
+    seq_lo = a0;
+  } else {
+    const int64_t parts = static_cast<int64_t>(P) * W;
+    lo = tc_unit_to_tile(share * V / parts, prefix, B, Hkv, p.seg_cost);
+    hi = tc_unit_to_tile((share + 1) * V / parts, prefix, B, Hkv, p.seg_cost);
+    seq_lo = lo < hi ? tc_find_seg(lo, hi, prefix, B, Hkv).seq : 0;
   }
+  if (lane == 0 && warp == 0) cta_run[0] = lo;
+  if (lane == 0 && warp == W - 1) cta_run[1] = hi;
+  // (an empty sequence's units hold no tile: the next one's first)
+  while (lo < hi && static_cast<int64_t>(Hkv) * prefix[seq_lo + 1] <= lo) ++seq_lo;
 
   const uint32_t bs32 = static_cast<uint32_t>(p.bs);  // paged: a 32-bit block size
   const uint64_t policy = l2_policy_evict_first();

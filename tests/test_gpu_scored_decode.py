@@ -285,3 +285,21 @@ def test_binding_refusals():
     none = torch.empty(0, dtype=torch.int32, device=DEV)
     assert pkv.paged_decode_attention_scored(empty, s.k, s.v, s.where[:0], none, 40, SCALE,
                                              softcap=5.0).shape == (0, 8, D)
+
+
+def test_runs_of_more_than_a_million_units():
+    """So many tiles that the schedule leaves 32-bit arithmetic (the caches' blocks
+    are shared by all sequences)."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    hkv, bs, ctx, batch = 8, 16, 60000, 40
+    k, v = (torch.randn(32, hkv, bs, D, generator=g, device=DEV).bfloat16() for _ in "kv")
+    tables = torch.randint(0, 32, (1, ctx // bs), generator=g, device=DEV, dtype=torch.int32)
+    q = torch.randn(1, 8, D, generator=g, device=DEV).bfloat16()
+    ctx_t = torch.full((batch,), ctx, dtype=torch.int32, device=DEV)
+    pkv.set_decode_variant(RUNS)
+    out = pkv.paged_decode_attention_scored(q.expand(batch, -1, -1).contiguous(), k, v,
+                                            tables.expand(batch, -1).contiguous(), ctx_t, ctx,
+                                            SCALE, softcap=30.0)
+    rows = [x[tables[0].long()].transpose(0, 1).reshape(hkv, ctx, D) for x in (k, v)]
+    want, tol = attend64(q, *rows, [ctx - 1], [(0, ctx - 1)], SCALE, 30.0)
+    assert_close(out, want.expand(batch, -1, -1), tol.expand(batch, -1, -1))

@@ -531,7 +531,7 @@ PKV_API pkv_status pkv_paged_decode_attention_noalloc(
  * PKV_ERR_UNSUPPORTED where the kernel does not apply).  Meant for tests and
  * tuning; every kernel computes the same result.  For the scored calls 2 and 3
  * are their two tensor-core kernels: tiles dealt to warps in contiguous runs
- * (the automatic choice up to 1024 visible positions a sequence), or pair by
+ * (the automatic choice up to 2048 visible positions a sequence), or pair by
  * pair.
  */
 PKV_API void pkv_set_decode_variant(int variant);

@@ -19,12 +19,11 @@
 // cut by CTAs is joined through tagged records (decode_tc.cuh).
 // The kernel of long spans (decode_tc.cuh) deals a CTA's tiles round-robin to
 // its warps, which all meet at the end of every pair, so a pair of a few tiles
-// costs it 3 to 4 us; here it costs one warp its own tiles.  But the joins all
-// come at the end, where a cut pair waits for the CTA after it, 2 to 3 us.
-// 8 KV heads, group 4, us a call (that kernel / this one): 256 sequences of 128
-// positions 62.0 / 34.0; 64 of 256, 24.7 / 18.5; of 512, 32.8 / 31.6; of 1024,
-// 48.1 / 51.2; of 4096, 165 / 168; 64 ragged ones under a window of 256, 23.9 /
-// 18.4, of 1024, 31.5 / 27.7.
+// costs it 3 to 4 us; here it costs one warp its own tiles.  Both are bound by
+// HBM in between: 64 ragged sequences up to 8192 under a window of 1024, 32 / 8
+// heads (115 MB, 17.0 us at the rate of a copy) take 25.1 us, of which 2 go by
+// before the runs are known, 2 more until the first tiles are asked for, and 2.6
+// at the end for the joins.  256 sequences of 128: 30.2 us; by pairs 62.
 //
 // Data movement and the math of a tile are that kernel's: TMA boxes into
 // a per-warp ring, S^T = K Q^T and O^T += V^T P^T by mma.m16n8k16, an online
@@ -579,9 +578,10 @@ cudaError_t launch_shape(const CUtensorMap& tk, const CUtensorMap& tv, const TcP
 cudaError_t launch_decode_runs(const CUtensorMap& tk, const CUtensorMap& tv, const TcParams& p_in,
                                bool contig, int num_ctas, cudaStream_t stream) {
   TcParams p = p_in;
-  // The cost of a pair in tiles.  0, 4, 8 and 16 gave 31.7, 28.1, 27.3 and 28.2
-  // us (64 ragged sequences, window 1024), 19.7, 17.9, 18.5 and 20.5 (window 256).
-  p.seg_cost = 6;
+  // The cost of a pair in tiles: 3, 4, 6 and 9 give 25.4, 25.1, 25.3 and 24.9 us
+  // (64 ragged sequences, window 1024), 15.3, 15.5, 15.5 and 16.2 (window 256),
+  // 15.3, 15.5, 16.1 and 16.9 (64 of 256).
+  p.seg_cost = 4;
   if (p.G <= 4)
     return contig ? launch_shape<true, 12, 2, 4>(tk, tv, p, num_ctas, stream)
                   : launch_shape<false, 12, 2, 4>(tk, tv, p, num_ctas, stream);

@@ -176,15 +176,13 @@ bool tc_enough_tiles(int32_t num_seqs, const pkv_heads& h, int32_t max_context, 
 }
 
 // Scored decode on the tensor cores: by warp runs (decode_runs.cu) where a
-// sequence sees few positions and there is a (sequence, KV head) pair for every
-// SM, else pair by pair (decode_tc.cuh).  64 sequences x 8 KV heads cross
-// between 512 and 1024 positions where each sees that many (1.03 and 0.94 of
-// the other's rate); ragged ones still gain at the bound (1.14).  8 sequences
-// x 8 heads (pairs cut across CTAs) of 512 run at 0.82, 16 at 0.97.
-constexpr int32_t kRunsMaxSpan = 1024 + 15;
-bool tc_by_runs(int32_t num_seqs, const pkv_heads& h, int32_t span, int sms) {
-  return span <= kRunsMaxSpan && static_cast<int64_t>(num_seqs) * h.num_kv_heads >= tc_ctas(sms);
-}
+// sequence sees at most this many positions, else pair by pair (decode_tc.cuh).
+// 8 KV heads, us a call (runs / pairs): 64 ragged sequences under a window of
+// 256, 1024 and 2048 15.4 / 24.0, 25.2 / 31.4 and 34.0 / 38.9, without one 55.9 /
+// 58.1; 64 of 512, 1024 and 2048 28.5 / 33.0, 48.4 / 48.2 and 88.8 / 88.0; 8 of
+// 512 and 2048 11.1 / 10.9 and 15.5 / 16.8; 256 of 2048 329 / 321; 128 of 8192
+// with 56 query heads 287 / 270.
+constexpr int32_t kRunsMaxSpan = 2048 + 15;
 
 // Positions that a window lets a sequence attend, counted from the start of
 // the 16-token tile that holds the first (a bound on every sequence).
@@ -303,7 +301,7 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
     }
     t.err = err;
     if (score != nullptr) {
-      t.scored = variant == 2 || (variant == 0 && tc_by_runs(num_seqs, h, span, sms)) ? 2 : 1;
+      t.scored = variant == 2 || (variant == 0 && span <= kRunsMaxSpan) ? 2 : 1;
       t.sp = *score;
     }
     cudaError_t ce = cudaSuccess;

@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include "pkv_device.cuh"
+#include "cluster.cuh"
 #include "score.cuh"
 
 namespace pkv {
@@ -57,6 +58,7 @@ struct DecodeParams {
   int32_t checked;
   int* err;
   ScoreParams sp;                // scored kernels only
+  int32_t cluster;               // scored: CTAs of the cluster that joins the splits; 0: none
 };
 
 constexpr int kDecodeWarps = 4;
@@ -78,6 +80,9 @@ struct DecodeSmemLayout {
   // end-of-CTA merge reuses the stage region
   static constexpr int kMergeBytes = kDecodeWarps * G * (kHeadDim + 2) * 4;
   static_assert(kMergeBytes <= kStagesBytes, "merge buffer must fit");
+  // a split's result for the cluster's other CTAs: o [G][128], (m, l) [G]
+  static constexpr int kJoinOffset = (kMergeBytes + 15) / 16 * 16;
+  static_assert(kJoinOffset + G * (kHeadDim + 2) * 4 <= kStagesBytes, "join buffer must fit");
 };
 
 // Context length of sequence `seq` as the kernels use it: in checked mode a
@@ -141,8 +146,11 @@ __global__ void __launch_bounds__(kDecodeThreads)
   const int tile0 = lo / kTileTokens;  // tiles before it hold nothing visible
   const int ntiles = ctx > 0 ? (ctx + kTileTokens - 1) / kTileTokens : 0;
   const int t_begin = tile0 + split * p.chunk_tiles;
-  const int t_end = min(t_begin + p.chunk_tiles, ntiles);
-  if (p.nsplit > 1 && t_begin >= t_end) return;  // empty split: the combine skips it
+  // (a cluster's padding splits have no tiles)
+  const int t_end = kScored && split >= p.nsplit ? t_begin : min(t_begin + p.chunk_tiles, ntiles);
+  // A cluster's CTAs join their splits themselves (every one of them stays for it).
+  const bool joined = kScored && p.cluster > 0;
+  if (p.nsplit > 1 && !joined && t_begin >= t_end) return;  // empty split: the combine skips it
 
   unsigned char* stage_base = smem + (warp * kStages) * L::kStageBytes;
   float* pbuf = reinterpret_cast<float*>(smem + L::kStagesBytes) + warp * kTileTokens * GP;
@@ -450,7 +458,14 @@ __global__ void __launch_bounds__(kDecodeThreads)
     }
     const int64_t row = static_cast<int64_t>(seq) * p.Hq + kvh * G + g;
     const float o = Lsum > 0.f ? O / Lsum : 0.f;
-    if (p.nsplit == 1) {
+    if (joined) {
+      float* part = reinterpret_cast<float*>(smem + L::kJoinOffset);  // [G][128], then [G][2]
+      part[g * kHeadDim + d] = o;
+      if (d == 0) {
+        part[G * kHeadDim + 2 * g] = Lsum > 0.f ? M : -INFINITY;
+        part[G * kHeadDim + 2 * g + 1] = Lsum;
+      }
+    } else if (p.nsplit == 1) {
       p.out[row * kHeadDim + d] = f32_to_bf16_bits(o);
     } else {
       const int64_t slot = row * p.nsplit + split;
@@ -459,6 +474,49 @@ __global__ void __launch_bounds__(kDecodeThreads)
         p.part_ml[slot * 2] = Lsum > 0.f ? M : -INFINITY;
         p.part_ml[slot * 2 + 1] = Lsum;
       }
+    }
+  }
+
+  if constexpr (kScored) {
+    if (joined) {
+      // Head g is joined by warp g / n of CTA g % n of the cluster's n: lane k has
+      // (m, l) of split k, then a lane has 4 elements.  (Every CTA comes to both
+      // barriers: the waits before them are bounded.)
+      cluster_sync();
+      const int n = p.cluster;
+      const int g = warp * n + static_cast<int>(cluster_rank());
+      if (g < G) {
+        const float* part = reinterpret_cast<const float*>(smem + L::kJoinOffset);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < n) ml = ld_cluster_f2(in_cta(part + G * kHeadDim + 2 * g, lane));
+        float M = ml.x;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        M = __shfl_sync(kFull, M, 0);
+        const float w_mine = ml.y > 0.f ? ml.y * fast_exp2(ml.x - M) : 0.f;
+        float W = w_mine;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) W += __shfl_xor_sync(kFull, W, o);
+        W = __shfl_sync(kFull, W, 0);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+          const float w = __shfl_sync(kFull, w_mine, k);
+          const float4 o = ld_cluster_f4(in_cta(part + g * kHeadDim + lane * 4, k));
+          if (w > 0.f) {
+            a.x = fmaf(w, o.x, a.x);
+            a.y = fmaf(w, o.y, a.y);
+            a.z = fmaf(w, o.z, a.z);
+            a.w = fmaf(w, o.w, a.w);
+          }
+        }
+        const float inv = W > 0.f ? 1.f / W : 0.f;
+        const int64_t row = static_cast<int64_t>(seq) * p.Hq + kvh * G + g;
+        *reinterpret_cast<uint2*>(p.out + row * kHeadDim + lane * 4) =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+      }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while another reads its shared memory
     }
   }
 }

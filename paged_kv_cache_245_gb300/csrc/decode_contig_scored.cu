@@ -8,4 +8,8 @@ cudaError_t launch_decode_contig_scored(const DecodeParams& p, int group, cudaSt
   return launch_decode<true, true>(p, group, stream);
 }
 
+cudaError_t room_decode_contig_scored(int group, ClusterRoom* out) {
+  return decode_cluster_room<true>(group, out);
+}
+
 }  // namespace pkv

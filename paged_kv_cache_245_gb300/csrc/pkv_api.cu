@@ -184,6 +184,34 @@ bool tc_enough_tiles(int32_t num_seqs, const pkv_heads& h, int32_t max_context, 
 // with 56 query heads 287 / 270.
 constexpr int32_t kRunsMaxSpan = 2048 + 15;
 
+// Scored decode of few tiles: the splits of a (sequence, KV head) as a cluster
+// of up to 16 CTAs that joins them itself, where the device holds the clusters
+// of all pairs at once and a warp has few tiles; 0 if not.  8 KV heads, us a
+// call, a cluster / the better of the other kernels: 1 sequence of 1000 (16 CTAs
+// a pair, a tile a warp) 7.4 / 11.0, 2 and 4 of 1000 and 8 of 512 (two tiles) 9.1
+// / 11.9, 9.1 / 12.5 and 9.3 / 11.3, 1 of 4000 (four) 14.0 / 18.8; but 16 of 512
+// and 8 of 1000 (four, clusters of 2 and 4) 13.7 / 11.7 and 13.9 / 12.9, 1 of
+// 8192 (eight) 22.8 / 20.9; two rounds of clusters cost twice as much.
+struct JoinedSplits {
+  int32_t cluster, chunk_tiles, nsplit;
+};
+JoinedSplits joined_splits(int64_t pairs, int32_t span, const pkv::ClusterRoom& room) {
+  const int32_t ntiles = (span + 15) / 16;
+  if (ntiles <= pkv::kDecodeWarps) return {0, 0, 0};  // one split
+  for (int i = 3; i >= 0; --i) {
+    if (pairs > room.held[i]) continue;
+    const int32_t n = 2 << i;
+    const int32_t warp_tiles = (ntiles + n * pkv::kDecodeWarps - 1) / (n * pkv::kDecodeWarps);
+    if (warp_tiles > (n == 16 ? 4 : 2)) return {0, 0, 0};
+    const int32_t chunk = warp_tiles * pkv::kDecodeWarps;
+    const int32_t nsplit = (ntiles + chunk - 1) / chunk;
+    int32_t cluster = 2;
+    while (cluster < nsplit) cluster *= 2;
+    return {cluster, chunk, nsplit};
+  }
+  return {0, 0, 0};
+}
+
 // Positions that a window lets a sequence attend, counted from the start of
 // the 16-token tile that holds the first (a bound on every sequence).
 int32_t visible_span(int32_t max_context, int32_t window) {
@@ -262,7 +290,16 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
   const int variant = g_variant.load();
   if (variant >= 2 && !tc_ok)
     return fail(PKV_ERR_UNSUPPORTED, "tensor-core kernel needs block_size %% 16 == 0 and < 2^31 rows");
-  const bool tc_pick = variant >= 2 || (variant == 0 && tc_enough_tiles(num_seqs, h, span, sms));
+  JoinedSplits joined = {0, 0, 0};
+  if (score != nullptr && variant <= 1 && g_split_tiles.load() == 0) {
+    pkv::ClusterRoom room;
+    const cudaError_t ce = contig ? pkv::room_decode_contig_scored(group, &room)
+                                  : pkv::room_decode_paged_scored(group, &room);
+    if (ce != cudaSuccess) return cuda_fail(ce, "cluster query");
+    joined = joined_splits(static_cast<int64_t>(num_seqs) * h.num_kv_heads, span, room);
+  }
+  const bool tc_pick = variant >= 2 || (variant == 0 && joined.cluster == 0 &&
+                                        tc_enough_tiles(num_seqs, h, span, sms));
   if (tc_pick && tc_ok) {
     if (tc_out) *tc_out = true;
     const size_t need = pkv::tc_workspace_bytes(tc_ctas(sms));
@@ -316,7 +353,8 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
     if (ts != pkv::TcStatus::kOk) return cuda_fail(ce, "decode launch");
     return PKV_OK;
   }
-  const SplitPlan plan = plan_splits(num_seqs, h, span, sms);
+  SplitPlan plan = plan_splits(num_seqs, h, span, sms);
+  if (joined.cluster > 0) plan = {joined.chunk_tiles, joined.nsplit, 0};
   if (plan.nsplit > 65535) return fail(PKV_ERR_UNSUPPORTED, "too many splits");
   if (plan.workspace_bytes > 0) {
     if (!workspace || workspace_bytes < plan.workspace_bytes)
@@ -356,6 +394,7 @@ pkv_status decode_common(bool contig, const void* q, const void* k, const void* 
   cudaError_t e;
   if (score != nullptr) {
     p.sp = *score;
+    p.cluster = joined.cluster;
     e = contig ? pkv::launch_decode_contig_scored(p, group, s)
                : pkv::launch_decode_paged_scored(p, group, s);
   } else {

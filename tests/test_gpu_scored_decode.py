@@ -303,3 +303,39 @@ def test_runs_of_more_than_a_million_units():
     rows = [x[tables[0].long()].transpose(0, 1).reshape(hkv, ctx, D) for x in (k, v)]
     want, tol = attend64(q, *rows, [ctx - 1], [(0, ctx - 1)], SCALE, 30.0)
     assert_close(out, want.expand(batch, -1, -1), tol.expand(batch, -1, -1))
+
+
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (7, 1), (4, 4), (16, 2)])
+@pytest.mark.parametrize("contig", [False, True])
+def test_few_sequences_whose_splits_are_a_cluster(hq, hkv, contig):
+    """Small batches around the sizes where clusters of 2 to 16 CTAs join the
+    splits, with sequences that leave splits empty, and a window."""
+    for ctx in ([1000], [65], [4000], [700, 0], [1000, 3, 500], [512] * 8, [100] * 16, [900] * 20):
+        s = Sequences(ctx, hkv, 16, contig, seed=len(ctx) + ctx[0])
+        q = queries(s, hq)
+        for kw in (dict(softcap=30.0), dict(window=300, slopes=slopes_of(hq))):
+            ref = reference(s, q, **kw)
+            kw["alibi_slopes"] = kw.pop("slopes", None)
+            assert_close(call(s, q, **kw), *ref)
+
+
+def test_a_cluster_replays_beside_an_eager_call():
+    s = Sequences([1000, 20], 8, 16, seed=8)
+    q = queries(s, 32)
+    want = reference(s, q, softcap=50.0)
+    out, side = torch.empty_like(q), torch.cuda.Stream()
+    other = torch.empty_like(q)
+    call(s, q, softcap=50.0, out=out)
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(s, q, softcap=50.0, out=out)
+    for _ in range(5):
+        out.fill_(7.0)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call(s, q, softcap=50.0, out=other)
+        graph.replay()
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(out, other)
+    assert_close(out, *want)

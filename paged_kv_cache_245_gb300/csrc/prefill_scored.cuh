@@ -32,8 +32,6 @@
 
 #include <limits.h>
 
-#include <type_traits>
-
 #include "prefill.cuh"
 #include "score.cuh"
 #include "umma.cuh"

@@ -2,6 +2,10 @@
 in 64 bits: head groups, block sizes, chunks over cached positions, prefixes,
 documents, rows that see nothing, poisoned masked places, graphs, refusals;
 and a layer's flow: rotary append, prefill, decode steps."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -533,3 +537,36 @@ def test_a_layer_prefills_and_decodes():
             remember(i, k[i:i + 1], v[i:i + 1], p, slots[i:i + 1])
             check(out[i:i + 1], qt[i:i + 1], i, p, "step %d of %d" % (step, i))
     bm.close()
+
+
+FRESH = """
+import torch, paged_kv_cache_245_gb300 as pkv
+dev = torch.device("cuda:0")
+k, v = (torch.randn(80, 8, 16, 128, device=dev).bfloat16() for _ in "kv")
+tables = torch.arange(80, dtype=torch.int32, device=dev)[None]
+q1, q2 = (torch.randn(n, 32, 128, device=dev).bfloat16() for n in (1, 40))
+ctx = torch.tensor([1200], dtype=torch.int32, device=dev)
+cu = torch.tensor([0, 40], dtype=torch.int32, device=dev)
+work = torch.empty(max(pkv.scored_decode_workspace_size(1, 32, 8, 1200), 16), dtype=torch.uint8, device=dev)
+outs = [torch.zeros_like(q1), torch.zeros_like(q2)]
+graph = torch.cuda.CUDAGraph()
+def calls():
+    pkv.paged_decode_attention_scored(q1, k, v, tables, ctx, 1200, 0.1, softcap=30.0, out=outs[0], workspace=work)
+    pkv.paged_prefill_attention_scored(q2, cu, k, v, tables, ctx, 40, 0.1, softcap=30.0, out=outs[1])
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in outs]
+calls()
+assert all(torch.equal(a, b) and bool((a != 0).any()) for a, b in zip(got, outs))
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    """What a call asks the device once (shared memory, room for clusters) does not
+    break a capture."""
+    r = subprocess.run([sys.executable, "-c", FRESH], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr

@@ -16,7 +16,7 @@
 // warp's run is written by that warp.  A run's first and last tiles may be
 // pieces of a pair that other warps share: a piece's (o, m, l) goes to shared
 // memory, and the CTA joins them once, after its warps' runs.  A pair that is
-// cut by CTAs is joined through tagged records (decode_tc.cuh).
+// cut by CTAs is joined by the last of them, through tagged records (decode_tc.cuh).
 // The kernel of long spans (decode_tc.cuh) deals a CTA's tiles round-robin to
 // its warps, which all meet at the end of every pair, so a pair of a few tiles
 // costs it 3 to 4 us; here it costs one warp its own tiles.  Both are bound by
@@ -33,6 +33,59 @@
 namespace pkv {
 
 namespace {
+
+// Merges the pieces of a pair cut by the CTA ranges (CTAs cf .. c) for query
+// head hh of the group and writes the result; called by CTA c, which holds the
+// pair's last tiles, with its own piece.  Records are folded in CTA order.  One
+// not yet complete is read again until it is, for at most kWaitLimitNs: waits
+// point only to lower CTAs, which start first, so they end whatever else runs on
+// the GPU.  Returns false if it gave up.
+__device__ __forceinline__ bool merge_earlier(const TcParams& p, int seq, int qh, int hh, int cf,
+                                              int c, int64_t V, int64_t P, int lane, float4 o_own,
+                                              float m_own, float l_own) {
+  constexpr unsigned kFull = 0xffffffffu;
+  float M = -INFINITY, L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fold = [&](float m, float l, float4 o) {
+    if (!(l > 0.f)) return;
+    if (m > M) {
+      const float s = fast_exp2(M - m);  // 0 while M is -inf
+      L *= s;
+      a.x *= s; a.y *= s; a.z *= s; a.w *= s;
+      M = m;
+    }
+    const float w = l * fast_exp2(m - M);
+    a.x = fmaf(w, o.x, a.x);
+    a.y = fmaf(w, o.y, a.y);
+    a.z = fmaf(w, o.z, a.z);
+    a.w = fmaf(w, o.w, a.w);
+    L += w;
+  };
+  bool ok = true;
+  for (int k = cf; k < c; ++k) {
+    if (!tc_range_nonempty(k, V, P)) continue;
+    uint64_t* rec = p.rec + (static_cast<int64_t>(k) * kTcRecHeads + hh) * kRecStride;
+    TcPieceWords pw;
+    float m, l;
+    float4 o;
+    tc_issue_piece(rec, lane, pw);
+    bool have = __all_sync(kFull, tc_parse_piece(pw, p.tag, &o, &m, &l));
+    for (const unsigned long long t0 = global_timer_ns();
+         !have && global_timer_ns() - t0 < kWaitLimitNs;) {
+      __nanosleep(128);
+      tc_issue_piece(rec, lane, pw);
+      have = __all_sync(kFull, tc_parse_piece(pw, p.tag, &o, &m, &l));
+    }
+    ok = ok && have;
+    fold(m, l, o);
+    tc_clear_piece(rec, lane);
+  }
+  fold(m_own, l_own, o_own);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  tc_write_out(p, seq, qh, lane, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv),
+               L > 0.f ? M : -INFINITY, L);
+  return ok;
+}
 
 // W warps, S stages each; MH query heads of a KV head (4, or 8).
 template <int W, int S, int MH>
@@ -474,7 +527,8 @@ __global__ void __launch_bounds__(W * 32, 1)
   const uint32_t starts =
       __ballot_sync(kFull, lane_pair >= 0 && (before == 0u || prev_pair != lane_pair));
   const int tasks = __popc(starts) * G;
-  for (int task = warp; task < tasks; task += W) {
+  // (last group first: what a later CTA waits for goes out before a wait for earlier ones)
+  for (int task = tasks - 1 - warp; task >= 0; task -= W) {
     const int grp = static_cast<uint32_t>(task) / static_cast<uint32_t>(G);
     const int hh = task - grp * G;
     uint32_t rest = starts;
@@ -524,16 +578,11 @@ __global__ void __launch_bounds__(W * 32, 1)
     const int qh = sg.kvh * G + hh;
     if (cf == cl) {
       tc_write_out(p, sg.seq, qh, lane, o4, Mr, Ls);
-    } else if (cf != c) {
+    } else if (cl != c) {
       tc_store_piece(p.rec + (static_cast<int64_t>(c) * kTcRecHeads + hh) * kRecStride, p.tag,
                      lane, o4, Mr, Ls);
-    } else {
-      TcPieceWords next = {};
-      if (tc_range_nonempty(cf + 1, V, P))
-        tc_issue_piece(p.rec + (static_cast<int64_t>(cf + 1) * kTcRecHeads + hh) * kRecStride,
-                       lane, next);
-      if (!tc_merge_pieces(p, sg.seq, qh, hh, cf, cl, V, P, lane, o4, Mr, Ls, next) && lane == 0)
-        record_error(p.err, kErrTimeout);
+    } else if (!merge_earlier(p, sg.seq, qh, hh, cf, c, V, P, lane, o4, Mr, Ls) && lane == 0) {
+      record_error(p.err, kErrTimeout);
     }
   }
 }

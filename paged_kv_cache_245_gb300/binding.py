@@ -256,6 +256,7 @@ class RopePlan:
 # read as the integer it is (torch.cuda.current_stream builds an object: 2.9 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _check_in(t, dtype, ndim, index, name):
@@ -276,7 +277,7 @@ def _device_index(t, name):
 def _on_device(index, call, *args):
     """Run a library call with device `index` current (the library launches
     there) on its current stream."""
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = call(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -286,8 +287,8 @@ def _on_device(index, call, *args):
 
 
 def _token_rows(t, index, name):
-    """Token stride (elements) of new rows [T, H, D] whose heads are adjacent;
-    tokens may be further apart (a view of a wider projection output)."""
+    """(Token stride in elements, T, H, D) of new rows [T, H, D] whose heads are
+    adjacent; tokens may be further apart (a view of a wider projection output)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype is not torch.bfloat16:
@@ -300,7 +301,7 @@ def _token_rows(t, index, name):
     st, sh, sd = t.stride()
     if T and ((d > 1 and sd != 1) or (H > 1 and sh != d)):
         raise ValueError("%s: the heads of a token must be adjacent rows" % name)
-    return st if T > 1 else H * d
+    return (st if T > 1 else H * d), T, H, d
 
 
 def rope_append(positions, slot_mapping, q, k, v, k_cache, v_cache, rope, out=None):
@@ -310,20 +311,22 @@ def rope_append(positions, slot_mapping, q, k, v, k_cache, v_cache, rope, out=No
     projection output (any token stride that is a multiple of 8).  out: the
     result [T, Hq, D] (q itself, if contiguous, for in place)."""
     dev = _device_index(q, "q")
-    sq, sk, sv = _token_rows(q, dev, "q"), _token_rows(k, dev, "k"), _token_rows(v, dev, "v")
+    sq, T, hq, dq = _token_rows(q, dev, "q")
+    sk, *k_dims = _token_rows(k, dev, "k")
+    sv, *v_dims = _token_rows(v, dev, "v")
     _check_in(positions, torch.int32, 1, dev, "positions")
     _check_in(slot_mapping, torch.int64, 1, dev, "slot_mapping")
     _check_in(k_cache, torch.bfloat16, 4, dev, "k_cache")
     _check_in(v_cache, torch.bfloat16, 4, dev, "v_cache")
     if not isinstance(rope, RopePlan):
         raise TypeError("rope must be a RopePlan")
-    nb, hkv, bs, d = k_cache.shape
-    T, hq, d2 = q.shape
-    if v_cache.shape != k_cache.shape or k.shape != v.shape:
+    shape = k_cache.shape
+    nb, hkv, bs, d = shape
+    if v_cache.shape != shape or k_dims != v_dims:
         raise ValueError("k/v and cache shapes must match")
-    if k.shape != (T, hkv, d) or d2 != d:
+    if k_dims != [T, hkv, d] or dq != d:
         raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D] matching the cache")
-    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+    if positions.numel() != T or slot_mapping.numel() != T:
         raise ValueError("positions / slot_mapping must have one entry per token")
     if out is None:
         out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
@@ -625,7 +628,8 @@ def _score(dev, hq, rows, num_seqs, softcap, window, alibi_slopes, first_key, pr
 
 
 def _check_attention(contig, q, k, v, where, context_lens, out):
-    """Device index and the output of an attention call; its tensors checked."""
+    """(Device index, output, q's and the cache's dims, sequences) of an attention
+    call; its tensors checked."""
     dev = _device_index(q, "q")
     _check_in(q, torch.bfloat16, 3, dev, "q")
     _check_in(k, torch.bfloat16, 4, dev, "k_buf" if contig else "k_cache")
@@ -635,24 +639,25 @@ def _check_attention(contig, q, k, v, where, context_lens, out):
     else:
         _check_in(where, torch.int32, 2, dev, "block_tables")
     _check_in(context_lens, torch.int32, 1, dev, "context_lens")
-    if q.shape[2] != k.shape[3] or v.shape != k.shape:
+    q_dims, dims, B = q.shape, k.shape, context_lens.numel()
+    if q_dims[2] != dims[3] or v.shape != dims:
         raise ValueError("q / cache shapes disagree")
-    if where.shape[0] != context_lens.shape[0]:
+    if where.shape[0] != B:
         raise ValueError("block_tables / req_ids / context_lens must have num_seqs rows")
     if out is None:
-        return dev, torch.empty_like(q)
-    _check_in(out, torch.bfloat16, 3, dev, "out")
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    return dev, out
+        out = torch.empty_like(q)
+    else:
+        _check_in(out, torch.bfloat16, 3, dev, "out")
+        if out.shape != q_dims:
+            raise ValueError("out must have q's shape")
+    return dev, out, q_dims, dims, B
 
 
 def _decode_scored(contig, q, k, v, where, context_lens, max_context, scale, softcap, window,
                    alibi_slopes, first_key, out, workspace):
-    dev, out = _check_attention(contig, q, k, v, where, context_lens, out)
-    B, hq, d = q.shape
-    n, hkv, bs, _ = k.shape
-    if context_lens.shape[0] != B:
+    dev, out, (rows, hq, d), (n, hkv, bs, _), B = _check_attention(contig, q, k, v, where,
+                                                                   context_lens, out)
+    if rows != B:
         raise ValueError("context_lens must have num_seqs rows")
     score = _score(dev, hq, B, B, softcap, window, alibi_slopes, first_key, None)
     h = Heads(hq, hkv, d)
@@ -699,12 +704,10 @@ def contig_decode_attention_scored(q, k_buf, v_buf, req_ids, context_lens, max_c
 
 def _prefill_scored(contig, q, cu_seqlens_q, k, v, where, context_lens, max_q_tokens, scale,
                     softcap, window, alibi_slopes, first_key, prefix_lens, out):
-    dev, out = _check_attention(contig, q, k, v, where, context_lens, out)
+    dev, out, (T, hq, d), (n, hkv, bs, _), B = _check_attention(contig, q, k, v, where,
+                                                                context_lens, out)
     _check_in(cu_seqlens_q, torch.int32, 1, dev, "cu_seqlens_q")
-    T, hq, d = q.shape
-    n, hkv, bs, _ = k.shape
-    B = context_lens.shape[0]
-    if cu_seqlens_q.shape[0] != B + 1:
+    if cu_seqlens_q.numel() != B + 1:
         raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
     score = _score(dev, hq, T, B, softcap, window, alibi_slopes, first_key, prefix_lens)
     h = Heads(hq, hkv, d)

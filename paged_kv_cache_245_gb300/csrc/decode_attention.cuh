@@ -448,7 +448,17 @@ __global__ void __launch_bounds__(kDecodeThreads)
 #pragma unroll
     for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, red_ml[(w * G + g) * 2]);
     float Lsum = 0.f, O = 0.f;
-    if (M != -INFINITY) {
+    if (kScored) {
+      // (scores that are all NaN have a sum but no maximum)
+#pragma unroll
+      for (int w = 0; w < kDecodeWarps; ++w) {
+        const float lw = red_ml[(w * G + g) * 2 + 1];
+        if (empty_sum<true>(lw)) continue;
+        const float sc_w = fast_exp2(red_ml[(w * G + g) * 2] - M);
+        Lsum = fmaf(lw, sc_w, Lsum);
+        O = fmaf(red_acc[(w * G + g) * kHeadDim + d], sc_w, O);
+      }
+    } else if (M != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < kDecodeWarps; ++w) {
         const float sc_w = fast_exp2(red_ml[(w * G + g) * 2] - M);
@@ -457,12 +467,13 @@ __global__ void __launch_bounds__(kDecodeThreads)
       }
     }
     const int64_t row = static_cast<int64_t>(seq) * p.Hq + kvh * G + g;
-    const float o = Lsum > 0.f ? O / Lsum : 0.f;
+    const bool none = empty_sum<kScored>(Lsum);
+    const float o = none ? 0.f : O / Lsum;
     if (joined) {
       float* part = reinterpret_cast<float*>(smem + L::kJoinOffset);  // [G][128], then [G][2]
       part[g * kHeadDim + d] = o;
       if (d == 0) {
-        part[G * kHeadDim + 2 * g] = Lsum > 0.f ? M : -INFINITY;
+        part[G * kHeadDim + 2 * g] = none ? -INFINITY : M;
         part[G * kHeadDim + 2 * g + 1] = Lsum;
       }
     } else if (p.nsplit == 1) {
@@ -471,7 +482,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
       const int64_t slot = row * p.nsplit + split;
       p.part_o[slot * kHeadDim + d] = o;
       if (d == 0) {
-        p.part_ml[slot * 2] = Lsum > 0.f ? M : -INFINITY;
+        p.part_ml[slot * 2] = none ? -INFINITY : M;
         p.part_ml[slot * 2 + 1] = Lsum;
       }
     }
@@ -493,7 +504,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
         M = __shfl_sync(kFull, M, 0);
-        const float w_mine = ml.y > 0.f ? ml.y * fast_exp2(ml.x - M) : 0.f;
+        const float w_mine = empty_sum<true>(ml.y) ? 0.f : ml.y * fast_exp2(ml.x - M);
         float W = w_mine;
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) W += __shfl_xor_sync(kFull, W, o);
@@ -503,14 +514,12 @@ __global__ void __launch_bounds__(kDecodeThreads)
         for (int k = 0; k < n; ++k) {
           const float w = __shfl_sync(kFull, w_mine, k);
           const float4 o = ld_cluster_f4(in_cta(part + g * kHeadDim + lane * 4, k));
-          if (w > 0.f) {
-            a.x = fmaf(w, o.x, a.x);
-            a.y = fmaf(w, o.y, a.y);
-            a.z = fmaf(w, o.z, a.z);
-            a.w = fmaf(w, o.w, a.w);
-          }
+          a.x = fmaf(w, o.x, a.x);  // (an empty split's o is 0)
+          a.y = fmaf(w, o.y, a.y);
+          a.z = fmaf(w, o.z, a.z);
+          a.w = fmaf(w, o.w, a.w);
         }
-        const float inv = W > 0.f ? 1.f / W : 0.f;
+        const float inv = empty_sum<true>(W) ? 0.f : 1.f / W;
         const int64_t row = static_cast<int64_t>(seq) * p.Hq + kvh * G + g;
         *reinterpret_cast<uint2*>(p.out + row * kHeadDim + lane * 4) =
             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
@@ -546,10 +555,10 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const DecodeParams 
 
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float W = 0.f;
-  if (M != -INFINITY) {
+  if (kScored || M != -INFINITY) {
     for (int s = 0; s < n; ++s) {
       const float ls = ml[2 * s + 1];
-      if (ls > 0.f) {
+      if (!empty_sum<kScored>(ls)) {
         const float w = ls * fast_exp2(ml[2 * s] - M);
         const float4 o = *reinterpret_cast<const float4*>(po + s * kHeadDim + lane * 4);
         acc.x = fmaf(w, o.x, acc.x);
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const DecodeParams 
       }
     }
   }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const float inv = empty_sum<kScored>(W) ? 0.f : 1.f / W;
   const uint32_t lo = f32_to_bf16_bits(acc.x * inv) | (uint32_t(f32_to_bf16_bits(acc.y * inv)) << 16);
   const uint32_t hi = f32_to_bf16_bits(acc.z * inv) | (uint32_t(f32_to_bf16_bits(acc.w * inv)) << 16);
   *reinterpret_cast<uint2*>(p.out + idx * kHeadDim + lane * 4) = make_uint2(lo, hi);

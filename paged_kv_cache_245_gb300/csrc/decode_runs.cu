@@ -47,7 +47,7 @@ __device__ __forceinline__ bool merge_earlier(const TcParams& p, int seq, int qh
   float M = -INFINITY, L = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   auto fold = [&](float m, float l, float4 o) {
-    if (!(l > 0.f)) return;
+    if (empty_sum<true>(l)) return;
     if (m > M) {
       const float s = fast_exp2(M - m);  // 0 while M is -inf
       L *= s;
@@ -81,9 +81,9 @@ __device__ __forceinline__ bool merge_earlier(const TcParams& p, int seq, int qh
     tc_clear_piece(rec, lane);
   }
   fold(m_own, l_own, o_own);
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = empty_sum<true>(L) ? 0.f : 1.f / L;
   tc_write_out(p, seq, qh, lane, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv),
-               L > 0.f ? M : -INFINITY, L);
+               empty_sum<true>(L) ? -INFINITY : M, L);
   return ok;
 }
 

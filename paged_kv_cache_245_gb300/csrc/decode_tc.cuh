@@ -210,6 +210,7 @@ __device__ __forceinline__ void tc_clear_piece(uint64_t* w, int lane) {
 // finishes without waiting (waits point only to higher CTAs, and the last
 // CTA's last segment is never a head piece), so the wait ends.  Returns
 // false if it gave up.
+template <bool kScored>
 __device__ __forceinline__ bool tc_merge_pieces(const TcParams& p, int seq, int qh, int hh, int cf,
                                                 int cl, int64_t V, int64_t P, int lane,
                                                 float4 o_own, float m_own, float l_own,
@@ -219,7 +220,7 @@ __device__ __forceinline__ bool tc_merge_pieces(const TcParams& p, int seq, int 
   float Mr = -INFINITY, Wr = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   auto fold = [&](float m, float l, float4 o) {
-    if (!(l > 0.f)) return;
+    if (empty_sum<kScored>(l)) return;
     if (m > Mr) {
       const float s = fast_exp2(Mr - m);  // 0 while Mr is -inf
       Wr *= s;
@@ -256,9 +257,9 @@ __device__ __forceinline__ bool tc_merge_pieces(const TcParams& p, int seq, int 
     fold(m, l, o);
     tc_clear_piece(rec, lane);
   }
-  const float inv = Wr > 0.f ? 1.f / Wr : 0.f;
+  const float inv = empty_sum<kScored>(Wr) ? 0.f : 1.f / Wr;
   tc_write_out(p, seq, qh, lane, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv),
-               Wr > 0.f ? Mr : -INFINITY, Wr);
+               empty_sum<kScored>(Wr) ? -INFINITY : Mr, Wr);
   return ok;
 }
 
@@ -875,11 +876,13 @@ __global__ void __launch_bounds__(W * 32, 1)
         float M = mj;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        const float fj = mj == -INFINITY ? 0.f : fast_exp2(mj - M);
+        // (scores that are all NaN have a sum but no maximum)
+        const bool nothing = kScored ? empty_sum<true>(lj) : mj == -INFINITY;
+        const float fj = nothing ? 0.f : fast_exp2(mj - M);
         float Ls = lj * fj;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(kFull, Ls, o);
-        const float wj = Ls > 0.f ? fj / Ls : 0.f;
+        const float wj = empty_sum<kScored>(Ls) ? 0.f : fj / Ls;
         float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
@@ -891,13 +894,13 @@ __global__ void __launch_bounds__(W * 32, 1)
           o4.z = fmaf(v.z, ww, o4.z);
           o4.w = fmaf(v.w, ww, o4.w);
         }
-        const float Mr = Ls > 0.f ? M : -INFINITY;
+        const float Mr = empty_sum<kScored>(Ls) ? -INFINITY : M;
         if (whole) {
           tc_write_out(p, seg.seq, seg.kvh * G + hh, lane, o4, Mr, Ls);
         } else if (head_piece) {
           // this piece first, then the other pieces' records in CTA order
-          if (!tc_merge_pieces(p, seg.seq, seg.kvh * G + hh, hh, cf, cl, V, P, lane, o4, Mr, Ls,
-                               nxt[pass]) &&
+          if (!tc_merge_pieces<kScored>(p, seg.seq, seg.kvh * G + hh, hh, cf, cl, V, P, lane, o4, Mr,
+                                        Ls, nxt[pass]) &&
               lane == 0)
             record_error(p.err, kErrTimeout);
         } else if (!(p.drop_record_test && c == 1)) {

@@ -46,6 +46,15 @@ __device__ __forceinline__ float capped_score(const ScoreParams& sp, float x) {
   return u <= 0.25f ? x * p : far;
 }
 
+// Whether a part of a row (a warp's, a split's, a piece) has nothing in its sum l
+// of probabilities.  A NaN score makes its part's sum NaN, which is something:
+// the row becomes NaN, as the formula does, wherever the schedule cut it.  (The
+// plain kernels leave such parts out.)
+template <bool kScored>
+__device__ __forceinline__ bool empty_sum(float l) {
+  return kScored ? l == 0.f : !(l > 0.f);
+}
+
 // The keys the token at position `pos` sees: lo <= j <= hi, none if lo > hi.
 __device__ __forceinline__ void visible_keys(const ScoreParams& sp, int pos, int first, int prefix,
                                              int ctx, int& lo, int& hi) {

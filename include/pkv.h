@@ -391,7 +391,9 @@ PKV_API pkv_status pkv_contig_prefill_attention(
  *   j > p - window                              window > 0
  *   j >= first_key[row]                         first_key given (documents)
  *   j < ctx
- * out = sum_j softmax_j(s) v_j over the keys it sees, zeros if it sees none.
+ * out = sum_j softmax_j(s) v_j over the keys it sees, zeros if it sees none.  A
+ * score of -infinity has no weight (zeros where every score is); a NaN score, or
+ * one of +infinity, makes the row NaN.
  * NULL in place of the struct, or a zeroed struct, is the plain causal score.
  */
 typedef struct pkv_score {

@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
         for (int e = 0; e < 8; ++e) acc[g][e] *= alpha;
         m[g] = m_new;
       }
-      pr[g] = fast_exp2(s_val - m[g]);
+      pr[g] = fast_exp2(s_val - (kScored ? finite_max(m[g]) : m[g]));
       l[g] += pr[g];
     }
 #pragma unroll

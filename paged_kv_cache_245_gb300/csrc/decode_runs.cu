@@ -434,8 +434,9 @@ __global__ void __launch_bounds__(W * 32, 1)
           for (int i = 0; i < 8; ++i) { acc[i][1] *= a; acc[i][3] *= a; }
           m1 = n1;
         }
-        const float p0 = fast_exp2(s0 - m0), p2 = fast_exp2(s2 - m0);
-        const float p1 = fast_exp2(s1 - m1), p3 = fast_exp2(s3 - m1);
+        const float f0 = finite_max(m0), f1 = finite_max(m1);
+        const float p0 = fast_exp2(s0 - f0), p2 = fast_exp2(s2 - f0);
+        const float p1 = fast_exp2(s1 - f1), p3 = fast_exp2(s3 - f1);
         // P^T as the B operand, rounded to bf16 (V's type) once; l sums what was
         // rounded, so that it cancels where few keys are seen
         const uint32_t w01 = pack_bf16x2(p0, p1), w23 = pack_bf16x2(p2, p3);

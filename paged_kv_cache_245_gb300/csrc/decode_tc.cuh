@@ -781,8 +781,10 @@ __global__ void __launch_bounds__(W * 32, 1)
           for (int i = 0; i < 8; ++i) { acc[i][t][1] *= a; acc[i][t][3] *= a; }
           m1[t] = n1;
         }
-        const float p0 = fast_exp2(s0 - m0[t]), p2 = fast_exp2(s2 - m0[t]);
-        const float p1 = fast_exp2(s1 - m1[t]), p3 = fast_exp2(s3 - m1[t]);
+        const float f0 = kScored ? finite_max(m0[t]) : m0[t];
+        const float f1 = kScored ? finite_max(m1[t]) : m1[t];
+        const float p0 = fast_exp2(s0 - f0), p2 = fast_exp2(s2 - f0);
+        const float p1 = fast_exp2(s1 - f1), p3 = fast_exp2(s3 - f1);
         const uint32_t w01 = pack_bf16x2(p0, p1), w23 = pack_bf16x2(p2, p3);
         if (kScored) {  // masks leave few keys: their sum is that of the rounded P
           l0[t] += bf16_lo(w01) + bf16_lo(w23);

@@ -55,6 +55,10 @@ __device__ __forceinline__ bool empty_sum(float l) {
   return kScored ? l == 0.f : !(l > 0.f);
 }
 
+// What probabilities are taken against: the maximum m, or 0 while every score of
+// the part is -inf, so that such a score has no weight (not 2^(-inf + inf)).
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
+
 // The keys the token at position `pos` sees: lo <= j <= hi, none if lo > hi.
 __device__ __forceinline__ void visible_keys(const ScoreParams& sp, int pos, int first, int prefix,
                                              int ctx, int& lo, int& hi) {

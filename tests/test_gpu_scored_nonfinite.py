@@ -113,3 +113,54 @@ def test_a_nan_query_makes_its_row_nan(kernel, batch):
         assert bool(torch.isnan(got[i, 6]).all())
         got[i, 6] = want[i, 6]
         assert torch.equal(got, want)
+
+
+def infinite_keys(s, q, i, keys, sign):
+    """Key rows whose score is sign * infinity for every head of KV head 1."""
+    q[..., 5] = 1.0
+    for j in keys:
+        block, off = row(s, i, j)
+        s.k[block, 1, off, 5] = sign * float("inf")
+
+
+def without(s, q, i, keys, kvh, softcap=0.0):
+    """(out, tol) of sequence i's newest token and KV head kvh, `keys` left out."""
+    G = q.shape[1] // s.hkv
+    keep = torch.tensor([j for j in range(s.ctx[i]) if j not in set(keys)], device=DEV)
+    k, v = (s.rows(i, x)[kvh:kvh + 1, keep] for x in (s.k, s.v))
+    return attend64(q[i:i + 1, kvh * G:(kvh + 1) * G], k, v, [s.ctx[i] - 1], [(0, len(keep) - 1)],
+                    SCALE, softcap)
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("batch", ["short", "one of 1000", "two", "ragged"])
+def test_a_score_of_minus_infinity_has_no_weight(kernel, batch):
+    """One key, whole tiles (a warp's first among them), and the last tile's only key."""
+    ctx = BATCHES[batch]
+    i = ctx.index(max(ctx))
+    c = ctx[i]
+    for keys in ([0], range(0, 48), range(c - c % 16 or c - 16, c), range(16, c - 1)):
+        s = Sequences(ctx, 2, 16, seed=len(ctx))
+        q = torch.randn(len(ctx), 8, D, generator=s.g, device=DEV).bfloat16()
+        infinite_keys(s, q, i, keys, -1)
+        choose(kernel)
+        got = decode(s, q)
+        want, tol = without(s, q, i, keys, 1)
+        assert_close(got[i:i + 1, 4:], want, tol, "keys %s" % keys)
+        want, tol = without(s, q, i, (), 0)
+        assert_close(got[i:i + 1, :4], want, tol)
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+def test_a_score_of_infinity_is_the_cap_or_nan(kernel):
+    for ctx in ([700], [40, 3], [3000] * 12):
+        for sign in (1, -1):
+            s = Sequences(ctx, 2, 16, seed=len(ctx))
+            q = torch.randn(len(ctx), 8, D, generator=s.g, device=DEV).bfloat16()
+            infinite_keys(s, q, 0, (20, 33), sign)
+            choose(kernel)
+            if sign > 0:  # inf - inf
+                assert bool(torch.isnan(decode(s, q)[0, 4:]).all())
+            got = decode(s, q, softcap=5.0)
+            s.k.clamp_(-1e4, 1e4)  # far beyond the cap
+            assert_close(got[:1, 4:], *without(s, q, 0, (), 1, 5.0))

@@ -244,6 +244,10 @@ __device__ __forceinline__ void load_half(uint32_t (&a)[32], uint32_t (&b)[32], 
   tmem_ready(b);
 }
 
+__device__ __forceinline__ uint64_t f2_both(float x) {
+  return umma::f2_pack(__float_as_uint(x), __float_as_uint(x));
+}
+
 // The linear bias of consecutive pairs: start + slope (2i, 2i + 1), along four
 // chains of additions.
 struct BiasPairs {
@@ -277,13 +281,21 @@ __device__ __forceinline__ float chunk_top(const uint32_t (&a)[32], uint32_t bit
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
+// Whether a row's bias is too steep for the paths that add it up along a row or
+// take it from m in one rounding.  Sums along a row are off by the slope times
+// 2^-17, and the rounding of m by the largest bias times 2^-25: of slopes of a
+// million either moves the key of the largest score by many units, and its P
+// underflows.  Such a row's scores are each rounded once, where m is found and
+// where it is subtracted, so the largest is m to the bit.
+__device__ __forceinline__ bool steep_row(const ScoredRow& r) { return fabsf(r.slope2) > 2.f; }
+
 // A tile against the running maximum; scale >= 0, no cap.  Two passes over S:
 // with the row held in registers between them the kernel spills (measured a
 // quarter slower).
 //
 // With a bias the maximum is a bound: the largest product of 32 columns and
 // their largest bias, at most 31 slopes above the largest score (2^-62 keeps P
-// far from underflow; steeper slopes take the scores one by one).  The scores'
+// far from underflow; steeper slopes take the scores one by one, see steep_row).  The scores'
 // own maximum costs two more operations a pair (8 x 2048 tokens 305 us).
 template <int kMode>
 __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const ScoredRow& r,
@@ -298,7 +310,7 @@ __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const S
   // past a row's own position (seen under a prefix only) the distance grows
   // again; up to it the bias is linear in the column
   const bool bent = kBias && __any_sync(kFull, r.hi > r.pos && r.pos < kt + 127);
-  const bool steep = kBias && __any_sync(kFull, fabsf(r.slope2) > 2.f);
+  const bool steep = kBias && __any_sync(kFull, steep_row(r));
   // the largest score there can be in columns c .. c + 31, by their largest product
   auto bound = [&](float top, int c) {
     if (!kBias) return top * p.qscale;
@@ -346,14 +358,15 @@ __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const S
     st.l += sum_of(ls);
     return;
   }
-  // the scores of columns from `from` away of the row on, either side of it, less m
-  auto exactly = [&](float from, float less) {
+  // the scores of columns from `from` away of the row on, either side of it, less
+  // `less` in the bias's rounding, and less `after` when they are rounded
+  auto exactly = [&](float from, float less, float after) {
     return [=, &p, &r](int i, uint64_t s2) {
       float x0, x1;
       f2_unpack(s2, x0, x1);
       x0 = fmaf(x0, p.qscale, fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i)), -less));
       x1 = fmaf(x1, p.qscale, fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i + 1)), -less));
-      return f2_pack(__float_as_uint(x0), __float_as_uint(x1));
+      return f2_add(f2_pack(__float_as_uint(x0), __float_as_uint(x1)), f2_both(-after));
     };
   };
   float tmax = -INFINITY;
@@ -364,8 +377,8 @@ __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const S
     load_half(a, b, s_tm + 64 * h);
     if (steep) {
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      chunk_max<true>(a, mask.bits(2 * h), exactly(at - 64.f * h, 0.f), mx);
-      chunk_max<true>(b, mask.bits(2 * h + 1), exactly(at - 64.f * h - 32.f, 0.f), mx);
+      chunk_max<true>(a, mask.bits(2 * h), exactly(at - 64.f * h, 0.f, 0.f), mx);
+      chunk_max<true>(b, mask.bits(2 * h + 1), exactly(at - 64.f * h - 32.f, 0.f, 0.f), mx);
       tmax = fmaxf(tmax, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
     } else {
       tmax = fmaxf(tmax, fmaxf(bound(chunk_top<true>(a, mask.bits(2 * h)), 64 * h),
@@ -375,6 +388,7 @@ __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const S
   const float m = take_max(tmax, first, o_tm, st);
   const uint64_t nm2 = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
   auto plain = [&](int, uint64_t s2) { return f2_fma(s2, sc2, nm2); };
+  const float less = steep ? 0.f : m, after = steep ? m : 0.f;
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     uint32_t pk[32];
@@ -384,14 +398,14 @@ __device__ __forceinline__ void tile_running_max(const PrefillParams& p, const S
       uint32_t a[32], b[32];
       load_half(a, b, s_tm + 64 * h);
       const float from = at - 64.f * h;
-      if (kBias && !bent) {
+      if (kBias && !bent && !steep) {
         BiasPairs bias(fmaf(-r.slope2, from, -m), r.slope2);
         auto biased = [&](int i, uint64_t s2) { return f2_fma(s2, sc2, bias.next(i)); };
         chunk_p<true>(a, mask.bits(2 * h), biased, pk, ls);
         chunk_p<true>(b, mask.bits(2 * h + 1), biased, pk + 16, ls);
       } else if (kBias) {
-        chunk_p<true>(a, mask.bits(2 * h), exactly(from, m), pk, ls);
-        chunk_p<true>(b, mask.bits(2 * h + 1), exactly(from - 32.f, m), pk + 16, ls);
+        chunk_p<true>(a, mask.bits(2 * h), exactly(from, less, after), pk, ls);
+        chunk_p<true>(b, mask.bits(2 * h + 1), exactly(from - 32.f, less, after), pk + 16, ls);
       } else {
         chunk_p<true>(a, mask.bits(2 * h), plain, pk, ls);
         chunk_p<true>(b, mask.bits(2 * h + 1), plain, pk + 16, ls);
@@ -580,6 +594,8 @@ __device__ __forceinline__ void tile_capped_biased(const PrefillParams& p, const
                          : -INFINITY;
   const float m = take_max(top_bias, first, o_tm, st);
   const bool bent = __any_sync(kFull, r.hi > r.pos && r.pos < kt + 127);
+  const bool steep = __any_sync(kFull, steep_row(r));
+  const bool linear_bias = !bent && !steep;
   float neg_m, unused;
   f2_unpack(k.neg_m2, neg_m, unused);
   BiasPairs bias(0.f, 0.f);
@@ -596,7 +612,7 @@ __device__ __forceinline__ void tile_capped_biased(const PrefillParams& p, const
   bool done[2] = {false, false};
   uint32_t p1[32];
   float sum1 = 0.f;
-  if (mask.whole && !bent) {
+  if (mask.whole && linear_bias) {
     uint32_t x[32], y[32], p0[32];
     uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
     load_half(x, y, s_tm);
@@ -620,15 +636,17 @@ __device__ __forceinline__ void tile_capped_biased(const PrefillParams& p, const
     done[1] = __all_sync(kFull, top1 <= p.cap.s_max);
   }
   if (!done[0] || !done[1]) {
+    const float less = steep ? 0.f : m, after = steep ? m : 0.f;
     auto each = [&](float from) {
       return [=, &p, &r](int i, uint64_t s2) {
         float x0, x1;
         f2_unpack(s2, x0, x1);
-        const float b0 = fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i)), -m);
-        const float b1 = fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i + 1)), -m);
+        const float b0 = fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i)), -less);
+        const float b1 = fmaf(-r.slope2, fabsf(from - static_cast<float>(2 * i + 1)), -less);
         x0 = fmaf(p.cap.neg_2cap, fast_rcp(1.f + fast_exp2(x0 * p.cap.exp_k)), p.cap.cap_m);
         x1 = fmaf(p.cap.neg_2cap, fast_rcp(1.f + fast_exp2(x1 * p.cap.exp_k)), p.cap.cap_m);
-        return f2_pack(__float_as_uint(x0 + b0), __float_as_uint(x1 + b1));
+        return f2_add(f2_pack(__float_as_uint(x0), __float_as_uint(x1)),
+                      f2_add(f2_pack(__float_as_uint(b0), __float_as_uint(b1)), f2_both(-after)));
       };
     };
 #pragma unroll 1
@@ -642,7 +660,7 @@ __device__ __forceinline__ void tile_capped_biased(const PrefillParams& p, const
         uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
         uint32_t a[32], b[32];
         load_half(a, b, s_tm + 64 * h);
-        const bool near = !mask.whole && !bent &&
+        const bool near = !mask.whole && linear_bias &&
                           fmaxf(seen_abs_max(a, bits0), seen_abs_max(b, bits1)) <= p.cap.s_max;
         if (__all_sync(kFull, near)) {
           bias = linear(h);

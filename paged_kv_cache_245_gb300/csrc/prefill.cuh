@@ -45,6 +45,7 @@ struct PrefillParams {
   int32_t num_tokens;            // T
   int32_t list;                  // set by the launcher: items are sorted and dealt on demand
   int32_t split;                 // set by the launcher: CTAs (a cluster) that share an item's keys
+  unsigned long long wait_ns;    // set by the launcher: limit of a wait for another role
 };
 
 // What the scored kernel (prefill_scored.cu) computes: scores masked by a

@@ -154,10 +154,26 @@ __device__ __forceinline__ KvRows kv_rows(const PrefillParams& p, const Item& it
   return kv;
 }
 
+// Puts the rows of the warp right that are not finite, their output being on its way
+// (repair_rows).  l: the row's sum of probabilities.  A row whose sum is NaN sees a
+// NaN score, and is NaN by the formula.
+__device__ __noinline__ void repair_item(const PrefillParams& p, const Item& it, float l,
+                                         uint32_t o_tm) {
+  const int lane = threadIdx.x & 31, lr = threadIdx.x & (kRowTile - 1);
+  const int row = it.row0 + (threadIdx.x >> 7) * p.tile_rows + lr;
+  const bool valid = lr < p.tile_rows && row < it.rows;
+  const ScoredRow r = score_row(p, it, valid ? row : it.rows - 1);
+  if (lane == 0) bulk_wait_done();  // the tensor stores of these rows come first
+  __syncwarp();
+  const Columns bad = bad_columns(o_tm);
+  const bool flagged = valid && l == l && (bad.w[0] | bad.w[1] | bad.w[2] | bad.w[3]) != 0u;
+  repair_rows(p, kv_rows(p, it), flagged, bad, r, it.k0, lane);
+}
+
 // Sums the CTAs' parts of rows rank, rank + kN, .. of an item: a warp a row, 16
 // loads in flight.
 template <int kN>
-__device__ __forceinline__ void sum_rows(const PrefillParams& p, const Item& it,
+__device__ __forceinline__ void sum_rows(const PrefillParams& p, const Item& it, const Join& join,
                                          unsigned char* smem, int rank, int row_tiles) {
   constexpr int kRows = 16 / kN, kWarps = kThreads / 32, kShare = kRowTile / kN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -194,9 +210,19 @@ __device__ __forceinline__ void sum_rows(const PrefillParams& p, const Item& it,
           make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
       const float z = 0.f * o.x + 0.f * o.y + 0.f * o.z + 0.f * o.w;  // 0, or NaN
       if (__any_sync(kFull, z != 0.f)) {
+        // (a sum that is NaN: a NaN score that the row sees)
+        const int i = i0 + u * kWarps, t = i / kShare;
+        const float2* sums = &join.sums[t * kRowTile + (i - t * kShare) * kN + rank];
+        const float l = lane < kN ? ld_cluster_f2(in_cta(sums, lane)).y : 0.f;
+        if (__any_sync(kFull, l != l)) continue;
+        Columns bad;
+        bad.w[0] = __ballot_sync(kFull, !(fabsf(o.x) < INFINITY));
+        bad.w[1] = __ballot_sync(kFull, !(fabsf(o.y) < INFINITY));
+        bad.w[2] = __ballot_sync(kFull, !(fabsf(o.z) < INFINITY));
+        bad.w[3] = __ballot_sync(kFull, !(fabsf(o.w) < INFINITY));
         const ScoredRow r = score_row(p, it, row[u]);
-        __syncwarp();
-        repair_rows(p, kv_rows(p, it), lane == 0, r, it.k0, lane);
+        __syncwarp();  // the row is written
+        repair_rows(p, kv_rows(p, it), lane == 0, bad, r, it.k0, lane);
       }
     }
   }
@@ -261,10 +287,10 @@ static __device__ __noinline__ void join_parts(const PrefillParams& p, unsigned 
   __syncwarp();
   cluster_sync();
   if (on) {
-    if (n == 2) sum_rows<2>(p, it, smem, rank, row_tiles);
-    else if (n == 4) sum_rows<4>(p, it, smem, rank, row_tiles);
-    else if (n == 8) sum_rows<8>(p, it, smem, rank, row_tiles);
-    else sum_rows<16>(p, it, smem, rank, row_tiles);
+    if (n == 2) sum_rows<2>(p, it, join, smem, rank, row_tiles);
+    else if (n == 4) sum_rows<4>(p, it, join, smem, rank, row_tiles);
+    else if (n == 8) sum_rows<8>(p, it, join, smem, rank, row_tiles);
+    else sum_rows<16>(p, it, join, smem, rank, row_tiles);
   }
   __syncwarp();
   cluster_sync();  // no CTA leaves while another reads its shared memory
@@ -317,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // when a wait gave up.  The warp's lane 0 then frees its claim on the slot.
   auto read_item = [&](int n, Item& it) -> bool {
     const int slot = n & (kRing - 1);
-    if (!__all_sync(kFull, wait_or_abort(&B.ifull[slot], (n / kRing) & 1, abort, p.err)))
+    if (!__all_sync(kFull, wait_role(&B.ifull[slot], (n / kRing) & 1, abort, p)))
       return false;
     it = ring[slot];
     __syncwarp();
@@ -484,8 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             e >= 0 ? static_cast<int32_t>(cache_row(e, cur.kvh, p.Hkv, p.bs, off) >> 3) : 0;
         unsigned char* dst = smem + kOffK + s * kStageBytes + prun * run * kRowBytes;
         // K first: its stage frees once both S products of tile g - 2 are done
-        if (g >= kStages && !__all_sync(kFull, wait_or_abort(&B.kempty[s], ((g >> 1) - 1) & 1,
-                                                             abort, p.err))) {
+        if (g >= kStages && !__all_sync(kFull, wait_role(&B.kempty[s], ((g >> 1) - 1) & 1, abort, p))) {
           ok = false;
           break;
         }
@@ -493,8 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane < 16 && e >= 0) tma_load_4d(dst, &tmk, grp, &B.kfull[s], policy);
         // then V, whose stage frees after both P V products of tile g - 2
-        if (g >= kStages && !__all_sync(kFull, wait_or_abort(&B.vempty[s], ((g >> 1) - 1) & 1,
-                                                             abort, p.err))) {
+        if (g >= kStages && !__all_sync(kFull, wait_role(&B.vempty[s], ((g >> 1) - 1) & 1, abort, p))) {
           kv_half = true;
           ok = false;
           break;
@@ -534,8 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto publish = [&](const Item& it) -> bool {
       const int slot = published & (kRing - 1);
       if (published >= kRing &&
-          !__all_sync(kFull, wait_or_abort(&B.iempty[slot], ((published / kRing) - 1) & 1,
-                                           abort, p.err)))
+          !__all_sync(kFull, wait_role(&B.iempty[slot], ((published / kRing) - 1) & 1, abort, p)))
         return false;
       if (lane == 0) {
         ring[slot] = it;
@@ -587,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < nt; ++t, ++nq, qc = qc.next(kQSlots)) {
         const int qs = qc.slot;
         if (nq >= static_cast<uint32_t>(kQSlots) &&
-            !__all_sync(kFull, wait_or_abort(&B.qempty[qs], qc.phase ^ 1u, abort, p.err)))
+            !__all_sync(kFull, wait_role(&B.qempty[qs], qc.phase ^ 1u, abort, p)))
           return false;
         last_phase = (last_phase & ~(1u << qs)) | (qc.phase << qs);
         unsigned char* dst = smem + q_off(qs);
@@ -706,11 +729,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 smem_desc(v_addr + kk * 4096, 1024, 2048), kIdescPV, (acc || kk > 0));
     };
     auto waitb = [&](uint64_t* b, uint32_t parity) -> bool {
-      return wait_or_abort(b, parity, abort, p.err);
+      return wait_role(b, parity, abort, p);
     };
     auto read_item1 = [&](int n, Item& it) -> bool {
       const int slot = n & (kRing - 1);
-      if (!wait_or_abort(&B.ifull[slot], (n / kRing) & 1, abort, p.err)) return false;
+      if (!wait_role(&B.ifull[slot], (n / kRing) & 1, abort, p)) return false;
       it = ring[slot];
       mbar_arrive(&B.iempty[slot]);
       return true;
@@ -818,8 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o_tm = tmem + lane_base + 256 + t * 128;
     // descriptor n stays in the ring until this warp is done with it
     auto wait_item = [&](int n) -> bool {
-      return __all_sync(kFull, wait_or_abort(&B.ifull[n & (kRing - 1)], (n / kRing) & 1, abort,
-                                             p.err));
+      return __all_sync(kFull, wait_role(&B.ifull[n & (kRing - 1)], (n / kRing) & 1, abort, p));
     };
     auto has_rows = [&](const Item& it) { return t == 0 || it.rows > it.row0 + TR; };
     auto row_of = [&](const Item& it) -> ScoredRow {
@@ -840,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = has_rows(it);
       SoftState st = {-INFINITY, 0.f};
       for (int j = 0; mine && j < it.ntiles; ++j) {
-        ok = __all_sync(kFull, wait_or_abort(&B.sfull[t], ns & 1, abort, p.err));
+        ok = __all_sync(kFull, wait_role(&B.sfull[t], ns & 1, abort, p));
         ++ns;
         if (!ok) break;
         tc_fence_after();
@@ -853,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int z0 = it.klo > k0 ? min(it.klo - k0, kKeys) : 0;
           const int z1 = max(min(it.ctx - k0, kKeys), z0);
           const uint32_t g = ns - 1;  // row tile 0 takes every key tile
-          ok = __all_sync(kFull, wait_or_abort(&B.vfull[g & 1], (g >> 1) & 1, abort, p.err));
+          ok = __all_sync(kFull, wait_role(&B.vfull[g & 1], (g >> 1) & 1, abort, p));
           if (!ok) break;
           unsigned char* vt = smem + kOffK + (g & 1) * kStageBytes + kOpBytes;
 #pragma unroll 1
@@ -876,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ScoredRow next_row = row;
       if (ring[(n + 1) & (kRing - 1)].ntiles != 0) next_row = row_of(ring[(n + 1) & (kRing - 1)]);
       if (kSplit && mine && it.joined) {
-        ok = __all_sync(kFull, wait_or_abort(&B.ofull[t], no & 1, abort, p.err));
+        ok = __all_sync(kFull, wait_role(&B.ofull[t], no & 1, abort, p));
         ++no;
         if (!ok) break;
         // (under a fixed offset every part has the same)
@@ -884,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (mine) {
         // the item's output rows; the next item's first P V product overwrites
         // O_t only after these warps hand over its first P
-        ok = __all_sync(kFull, wait_or_abort(&B.ofull[t], no & 1, abort, p.err));
+        ok = __all_sync(kFull, wait_role(&B.ofull[t], no & 1, abort, p));
         ++no;
         if (!ok) break;
         tc_fence_after();
@@ -894,7 +916,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // are 32 / G whole tokens, stored by tensor stores
         const bool whole = p.out_tma && 32 * (warp & 3) + 32 <= TR && wrow0 + 32 <= it.rows;
         unsigned char* stg = smem + kOffOut + warp * 4096;
-        uint4* dst = reinterpret_cast<uint4*>(p.out + row.qrow * kHeadDim);
+        // (the row's place again: not kept in registers through the tiles)
+        const int own = it.row0 + t * TR + lr;
+        const bool valid = lr < TR && own < it.rows;
+        const int tok = own / G;
+        uint4* dst = reinterpret_cast<uint4*>(
+            p.out + ((static_cast<int64_t>(it.q0) + tok) * p.Hq + it.kvh * G + own - tok * G) * kHeadDim);
         uint64_t z = 0ull;  // (0, 0) while every element is finite
         // (a loop: this code runs once an item, out of a cold instruction cache)
 #pragma unroll 1
@@ -907,17 +934,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           add_finite(z, a);
           add_finite(z, b);
           if (whole) store_half_tma(&tmo, stg, lane, inv, a, b, h, it.kvh * G, it.q0 + wrow0 / G);
-          else if (row.valid) store_half(dst + 8 * h, inv, a, b, p.out_v8);
+          else if (valid) store_half(dst + 8 * h, inv, a, b, p.out_v8);
         }
-        // A row that is not finite may have met a NaN or an infinity that it
-        // does not see (0 times either is NaN): it is computed again by itself.
-        const bool repair = row.valid && !is_zero(z);
-        if (__any_sync(kFull, repair)) {
-          const KvRows kv = kv_rows(p, it);
-          if (lane == 0) bulk_wait_done();  // the tensor stores of these rows come first
-          __syncwarp();
-          repair_rows(p, kv, repair, row, it.k0, lane);
-        }
+        // A row that is not finite may have met a NaN or an infinity that it does
+        // not see (0 times either is NaN): repair_rows.  (One whose sum is NaN
+        // sees a NaN score, and is NaN by the formula.)
+        const bool repair = valid && !is_zero(z) && st.l == st.l;
+        if (__any_sync(kFull, repair)) repair_item(p, it, st.l, o_tm);
         tc_fence_before();
       }
       __syncwarp();
@@ -1004,6 +1027,10 @@ cudaError_t launch_mode(const CUtensorMap& tk, const CUtensorMap& tv, const CUte
   const bool listable = pairs <= kListMax && row_tiles * p.num_seqs <= kListScan;
   PrefillParams pl = p;
   pl.split = 1;
+  // Waits outlast rows computed again: 32 a warp, one after another, at 4 positions in
+  // 0.8 us (6.4 us a position: 50000 of them 0.32 s), after a look through V (16
+  // positions in 1 us).  The limit allows for ten times that.
+  pl.wait_ns = kWaitLimitNs + 65536ull * static_cast<unsigned long long>(p.max_blocks) * p.bs;
   // few items: the largest cluster an item that the device holds for all of them
   // at once, and whose parts the key tiles (at most) are enough for
   int64_t span = static_cast<int64_t>(p.max_blocks) * p.bs;

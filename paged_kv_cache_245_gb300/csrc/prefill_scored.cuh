@@ -98,6 +98,23 @@ struct ScoredBars {
   int joined;           // the cluster's item is in parts
 };
 
+// Wait for phase `parity` of `bar`; give up when another role has given up (*abort)
+// or after p.wait_ns (then set *abort and record the timeout).
+__device__ __forceinline__ bool wait_role(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          const PrefillParams& p) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > p.wait_ns) {
+      *abort = 1;
+      record_error(p.err, kErrTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
 // The row's running maximum takes in the tile's; O and l are rescaled when it
 // grows by more than 2^kRescaleLog2.  Returns the offset P is taken against
 // (0 while the row has seen nothing, where every P is masked).
@@ -751,11 +768,141 @@ __device__ __forceinline__ void store_half(uint4* dst, float inv, const uint32_t
   }
 }
 
-// Computes and writes the rows flagged in the warp, one by one.
+// 128 columns as bits: column d is bit d / 4 of word d % 4.
+struct Columns {
+  uint32_t w[4];
+};
+
+// The columns of this thread's row of O that are not finite (whole warp).
+__device__ __forceinline__ Columns bad_columns(uint32_t o_tm) {
+  Columns bad = {};
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t x[32];
+    umma::tmem_ld32(x, o_tm + 32 * c);
+    umma::tmem_wait_ld(x);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      bad.w[e & 3] |= (x[e] & 0x7f800000u) == 0x7f800000u ? 1u << (8 * c + (e >> 2)) : 0u;
+  }
+  return bad;
+}
+
+// What a row sees in V that is not finite, by column.
+struct SeenValues {
+  Columns nan, pos, neg;
+};
+
+// Looks through the V rows that the warp's flagged rows see, until a NaN is found
+// for each of their bad columns.  16 positions at a time (one block: their size is a
+// multiple of 16), two a load, 16 lanes each.
+static __device__ __noinline__ SeenValues scan_values(const KvRows& kv, bool flagged,
+                                                      const Columns& bad, int lo, int hi,
+                                                      int lane) {
+  constexpr unsigned kAll = 0xffffffffu;
+  SeenValues seen = {};
+  const bool on = flagged && lo <= hi;
+  const int first = __reduce_min_sync(kAll, on ? lo : INT_MAX);
+  const int last = __reduce_max_sync(kAll, on ? hi : -1);
+  const uint32_t bs = static_cast<uint32_t>(kv.bs);
+  const int half = lane >> 4, chunk = lane & 15;  // columns 8 chunk .. 8 chunk + 7
+  for (int64_t j0 = first & ~15; j0 <= last; j0 += 16) {
+    // (a block that no flagged row sees is not read, nor its table entry)
+    if (!__any_sync(kAll, on && lo < j0 + 16 && hi >= j0)) continue;
+    const uint32_t at = static_cast<uint32_t>(j0);
+    const int32_t blk = kv.table[at / bs];
+    if (kv.checked && (blk < 0 || blk >= kv.num_blocks)) {
+      record_error(kv.err, kv.err_code);
+      continue;
+    }
+    const uint16_t* v = kv.v + (cache_row(blk, kv.kvh, kv.Hkv, kv.bs, at % bs) + half) * kHeadDim +
+                        chunk * 8;
+    // an exponent of all ones carries into the sign's place
+    auto ones_of = [](const uint4& x) {
+      return ((((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+               ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) &
+              0x80008000u);
+    };
+    uint32_t hit = 0u;  // loads that bring a value that is not finite
+#pragma unroll
+    for (int g = 0; g < 8; g += 4) {
+      uint4 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = ld_global_nc_v4(v + 2 * (g + u) * kHeadDim);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) hit |= ones_of(x[u]) != 0u ? 1u << (g + u) : 0u;
+    }
+    for (hit = __reduce_or_sync(kAll, hit); hit != 0u; hit &= hit - 1) {
+      const int u = __ffs(hit) - 1;
+      const uint4 x = ld_global_nc_v4(v + 2 * u * kHeadDim);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      Columns nan = {}, pos = {}, neg = {};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t b = (e & 1 ? w[e >> 1] >> 16 : w[e >> 1]) & 0xffffu;
+        const uint32_t bit = 1u << (2 * chunk + (e >> 2));
+        if ((b & 0x7fffu) > 0x7f80u) nan.w[e & 3] |= bit;
+        else if (b == 0x7f80u) pos.w[e & 3] |= bit;
+        else if (b == 0xff80u) neg.w[e & 3] |= bit;
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {  // position j0 + 2 u + r
+        const int64_t j = j0 + 2 * u + r;
+        const bool sees = on && lo <= j && j <= hi;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t n = __reduce_or_sync(kAll, half == r ? nan.w[i] : 0u);
+          const uint32_t p = __reduce_or_sync(kAll, half == r ? pos.w[i] : 0u);
+          const uint32_t m = __reduce_or_sync(kAll, half == r ? neg.w[i] : 0u);
+          if (sees) {
+            seen.nan.w[i] |= n;
+            seen.pos.w[i] |= p;
+            seen.neg.w[i] |= m;
+          }
+        }
+      }
+      uint32_t open = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) open |= bad.w[i] & ~seen.nan.w[i];
+      if (!__any_sync(kAll, on && open != 0u)) return seen;
+    }
+  }
+  return seen;
+}
+
+// Puts the warp's flagged rows (a thread's row each, `bad` its columns that are
+// not finite) right.  Such a column holds what the formula gives where the row
+// sees a value of V that is not finite: that value (NaN where it sees several
+// kinds), which is written.  Else it met one that it does not see (0 times a
+// NaN or an infinity is NaN), and the row is computed again by itself.
+//
+// So the rows computed again are those beside a masked value that is not finite,
+// in a column where they see none: a value that every later token sees costs its
+// own work item the rows before it, and the items after it one look through V.
+// (Each row that is not finite computed again, one NaN in a prompt's first tokens
+// cost every later row its whole context.)
 static __device__ __noinline__ void repair_rows(const PrefillParams& p, const KvRows& kv,
-                                                bool flagged, const ScoredRow& r, int k0,
-                                                int lane) {
-  for (uint32_t left = __ballot_sync(umma::kFull, flagged); left != 0u; left &= left - 1) {
+                                                bool flagged, const Columns& bad,
+                                                const ScoredRow& r, int k0, int lane) {
+  const bool sees = r.lo <= r.hi;
+  const SeenValues seen = scan_values(kv, flagged, bad, sees ? r.lo + k0 : 0,
+                                      sees ? r.hi + k0 : -1, lane);
+  uint32_t unexplained = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    unexplained |= bad.w[i] & ~(seen.nan.w[i] | seen.pos.w[i] | seen.neg.w[i]);
+  if (flagged && unexplained == 0u) {
+    uint16_t* out = p.out + r.qrow * kHeadDim;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      for (uint32_t left = bad.w[i]; left != 0u; left &= left - 1) {
+        const int b = __ffs(left) - 1;
+        const bool nan = (seen.nan.w[i] | (seen.pos.w[i] & seen.neg.w[i])) >> b & 1u;
+        out[4 * b + i] = nan ? 0x7fffu : seen.pos.w[i] >> b & 1u ? 0x7f80u : 0xff80u;
+      }
+  }
+  for (uint32_t left = __ballot_sync(umma::kFull, flagged && unexplained != 0u); left != 0u;
+       left &= left - 1) {
     const int src = __ffs(left) - 1;
     const int64_t row = __shfl_sync(umma::kFull, r.qrow, src);
     const int lo = __shfl_sync(umma::kFull, r.lo, src), hi = __shfl_sync(umma::kFull, r.hi, src);

@@ -85,14 +85,16 @@ struct KvRows {
 // Attention of one query row over its keys [lo, hi] by one warp: four keys at
 // a time, 8 lanes a key, 16 head elements a lane; an online softmax per lane
 // group, joined at the end.  Reads visible rows only, so nothing that stands
-// in masked places matters.  Result: lane group 0's lanes (lane < 8) hold
-// elements 8 lane .. and 64 + 8 lane .. in o[0..7] and o[8..15], normalised;
-// zeros for an empty row.
+// in masked places matters.  (Few registers on purpose: a larger function called
+// from the prefill kernel, though never run, cost that 6 %.)  Result: lane group
+// 0's lanes (lane < 8) hold elements 8 lane .. and 64 + 8 lane .. in o[0..7] and
+// o[8..15], normalised; zeros for an empty row.
 __device__ inline void attend_row(const ScoreParams& sp, const KvRows& kv, const uint16_t* q,
                                   float qscale, float slope2, int pos, int lo, int hi, int lane,
                                   float (&o)[16]) {
   constexpr unsigned kAll = 0xffffffffu;
   const int grp = lane >> 3, sub = lane & 7;
+  const uint32_t bs = static_cast<uint32_t>(kv.bs);  // (positions and blocks are below 2^31)
   float qf[16];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
@@ -112,12 +114,13 @@ __device__ inline void attend_row(const ScoreParams& sp, const KvRows& kv, const
     bool seen = j <= hi;
     int64_t row = 0;
     if (seen) {
-      const int32_t blk = kv.table[j / kv.bs];
+      const uint32_t at = static_cast<uint32_t>(j);
+      const int32_t blk = kv.table[at / bs];
       if (kv.checked && (blk < 0 || blk >= kv.num_blocks)) {
         record_error(kv.err, kv.err_code);
         seen = false;
       } else {
-        row = cache_row(blk, kv.kvh, kv.Hkv, kv.bs, j % kv.bs) * kHeadDim;
+        row = cache_row(blk, kv.kvh, kv.Hkv, kv.bs, at % bs) * kHeadDim;
       }
     }
     float x = 0.f;

@@ -5,6 +5,7 @@ import torch
 
 import paged_kv_cache_245_gb300 as pkv
 from scored_ref import Sequences, assert_close, attend64
+from test_gpu_scored_prefill import Chunks, make, slopes_of
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +165,164 @@ def test_a_score_of_infinity_is_the_cap_or_nan(kernel):
             got = decode(s, q, softcap=5.0)
             s.k.clamp_(-1e4, 1e4)  # far beyond the cap
             assert_close(got[:1, 4:], *without(s, q, 0, (), 1, 5.0))
+
+
+# ------------------------------------------------------------------ prefill
+
+PREFILL = {"chunks": ([0, 300, 40], [500, 70, 260]), "after many": ([3000, 200], [40, 3]),
+           "single": ([0, 130, 700], [1, 1, 1])}
+MODES = {"masked": dict(), "capped": dict(softcap=30.0), "biased": dict(slopes=True),
+         "capped and biased": dict(softcap=30.0, slopes=True), "any": dict(softcap=200.0)}
+BAD = {"nan": float("nan"), "inf": float("inf"), "-inf": -float("inf")}
+
+
+def expected(s, ref, bad):
+    """(out, tol, kind) with values `bad` [(sequence, KV head, position, column, kind)]
+    in V: kind is 0 where an output is finite (out holds it), 1 NaN, 2 inf, 3 -inf."""
+    kept = s.v.clone()
+    for i, h, j, column, _ in bad:
+        block, off = row(s, i, j)
+        s.v[block, h, off, column] = 0.0
+    out, tol = s.reference(**ref)
+    s.v = kept
+    rng = s.ranges(ref.get("window", 0), None if "first" not in ref else ref["first"].tolist(),
+                   ref.get("prefix"))
+    kinds = torch.zeros(s.T, s.hq, D, dtype=torch.int64, device=DEV)
+    G = s.hq // s.hkv
+    met = {}
+    for i, h, j, column, name in bad:
+        for t, (seq, _) in enumerate(s.positions()):
+            if seq == i and rng[t][0] <= j <= rng[t][1]:
+                met.setdefault((t, h, column), set()).add(name)
+    for (t, h, column), names in met.items():
+        one = {"nan": 1, "inf": 2, "-inf": 3}[next(iter(names))] if len(names) == 1 else 1
+        kinds[t, h * G:(h + 1) * G, column] = one
+    return out, tol, kinds
+
+
+@pytest.mark.parametrize("mode", list(MODES))
+@pytest.mark.parametrize("masks", ["plain", "documents", "prefix", "window 100"])
+@pytest.mark.parametrize("batch", list(PREFILL))
+@pytest.mark.parametrize("hq,contig", [(8, False), (14, True)])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(batch, masks, mode, hq, contig):
+    """NaN and infinities scattered over V, several kinds in a column, seen by some
+    rows of a work item and masked for others."""
+    s = Chunks(*PREFILL[batch], hq, 2, 16, contig, seed=61, by=1.0)
+    ref, kw = make(masks, s)
+    m = MODES[mode]
+    if m.get("slopes"):  # gentle: every weight stays above 2^-126
+        ref["slopes"] = kw["alibi_slopes"] = slopes_of(hq) / 64
+    ref["softcap"] = kw["softcap"] = m.get("softcap", 0.0)
+    g = torch.Generator().manual_seed(62)
+    bad = []
+    for i, c in enumerate(s.ctx):
+        for n in range(24):
+            j, column, h = (int(torch.randint(0, x, (1,), generator=g)) for x in (c, D, 2))
+            column = column if n % 2 else 64  # many in one column
+            bad.append((i, h, j, column, list(BAD)[int(torch.randint(0, 3, (1,), generator=g))]))
+    bad = list({b[:4]: b for b in bad}.values())
+    for i, h, j, column, name in bad:
+        block, off = row(s, i, j)
+        s.v[block, h, off, column] = BAD[name]
+    out, tol, kinds = expected(s, ref, bad)
+    got = s.call(**kw).float()
+    assert bool(torch.isnan(got[kinds == 1]).all())
+    assert bool((got[kinds == 2] == float("inf")).all())
+    assert bool((got[kinds == 3] == -float("inf")).all())
+    finite = kinds == 0
+    assert_close(got[finite], out[finite], tol[finite])
+
+
+@pytest.mark.parametrize("mode", list(MODES))
+@pytest.mark.parametrize("batch", list(PREFILL))
+def test_a_nan_key_or_query_in_prefill(batch, mode):
+    s = Chunks(*PREFILL[batch], 8, 2, 16, seed=63, by=1.0)
+    m = MODES[mode]
+    kw = dict(softcap=m.get("softcap", 0.0), window=250,
+              alibi_slopes=slopes_of(8) if m.get("slopes") else None)
+    # Rows beside it are held to the formula's bound, not to the same bits: where one row
+    # of a warp needs the exponentials, its other rows take them in place of the polynomial.
+    want, tol = s.reference(softcap=kw["softcap"], window=250, slopes=kw["alibi_slopes"])
+    i = 1
+    for j in (s.ctx[i] - 1, max(0, s.ctx[i] - 100)):
+        block, off = row(s, i, j)
+        kept = s.k[block, 1, off].clone()
+        s.k[block, 1, off, 3] = float("nan")
+        got = s.call(**kw)
+        s.k[block, 1, off] = kept
+        sees = torch.tensor([seq == i and lo <= j <= hi for (seq, _), (lo, hi) in
+                             zip(s.positions(), s.ranges(250))], device=DEV)
+        assert bool(torch.isnan(got[sees][:, 4:]).all())
+        rest = torch.ones_like(got, dtype=torch.bool)
+        rest[sees, 4:] = False
+        assert_close(got[rest], want[rest], tol[rest])
+    q = s.q.clone()
+    q[0, 5, 9] = float("nan")
+    got = s.call(q=q, **kw)
+    assert bool(torch.isnan(got[0, 5]).all())
+    rest = torch.ones_like(got, dtype=torch.bool)
+    rest[0, 5] = False
+    assert_close(got[rest], want[rest], tol[rest])
+
+
+def timed(run):
+    best = float("inf")
+    for _ in range(4):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+        a.record()
+        run()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("mode", ["masked", "capped", "biased"])
+def test_a_value_that_every_later_token_sees_costs_little(mode):
+    """One NaN among a prompt's first values: every row after it is NaN in a column,
+    which is found by a look through V, not by computing the rows again."""
+    s = Chunks([0] * 4, [2048] * 4, 32, 8, 16, seed=64)
+    m = MODES[mode]
+    kw = dict(softcap=m.get("softcap", 0.0), alibi_slopes=slopes_of(32) if m.get("slopes") else None)
+    out = torch.empty_like(s.q)
+    s.call(out=out, **kw)
+    clean, time = out.clone(), timed(lambda: s.call(out=out, **kw))
+    for bad, at in ((float("nan"), 5), (float("inf"), 5)):
+        block, off = row(s, 0, at)
+        s.v[block, :, off, 40] = bad
+        slow = timed(lambda: s.call(out=out, **kw))
+        s.v[block, :, off, 40] = 0.5
+        # a look through 2048 rows of V an item and warp at worst: about ten times; computed
+        # again, the rows took over a hundred times as long
+        assert slow < 20 * time, "%.3f ms, %.3f ms without" % (slow, time)
+        column = out[at:2048, :, 40]
+        assert not bool(torch.isfinite(column).any())
+        other = torch.arange(D, device=DEV) != 40
+        close = (out[:, :, other].float() - clean[:, :, other].float()).abs()
+        assert bool((close <= 2.0 ** -6 * clean[:, :, other].float().abs() + 2.0 ** -7).all())
+
+
+def test_rows_computed_again_over_long_contexts():
+    """Half of each chunk's rows beside a masked NaN, over fifty thousand positions, in
+    more work items than the device has SMs: every one is written."""
+    hkv, hq, bs, ctx, new, batch = 1, 4, 16, 50000, 64, 160
+    s = Chunks([ctx - new], [new], hq, hkv, bs, seed=65, by=1.0)
+    first = torch.zeros(new, dtype=torch.int32, device=DEV)
+    want, tol = s.reference(softcap=30.0)
+    at = ctx - new // 2
+    block, off = row(s, 0, at)
+    s.v[block, 0, off, 9] = float("nan")
+    cu = torch.arange(batch + 1, dtype=torch.int32, device=DEV) * new
+    pkv.set_checked(True)
+    out = pkv.paged_prefill_attention_scored(
+        s.q.repeat(batch, 1, 1), cu, s.k, s.v, s.where.repeat(batch, 1), s.ctx_t.repeat(batch), new,
+        SCALE, softcap=30.0, first_key=first.repeat(batch))
+    error = pkv.get_device_error()
+    pkv.set_checked(False)
+    assert error == "none"
+    out = out.view(batch, new, hq, D)
+    assert bool(torch.isnan(out[:, new // 2:, :, 9]).all())
+    out[:, new // 2:, :, 9] = 0
+    want[new // 2:, :, 9] = 0
+    assert torch.equal(out, out[:1].expand_as(out))
+    assert_close(out[0], want, tol)

@@ -534,7 +534,9 @@ PKV_API pkv_status pkv_paged_decode_attention_noalloc(
  * tuning; every kernel computes the same result.  For the scored calls 2 and 3
  * are their two tensor-core kernels: tiles dealt to warps in contiguous runs
  * (the automatic choice up to 2048 visible positions a sequence), or pair by
- * pair.
+ * pair; and with 1 the splits of small batches are clusters that join them, as
+ * with 0, unless pkv_set_split_tiles sets their length (then they are combined
+ * by a second kernel).
  */
 PKV_API void pkv_set_decode_variant(int variant);
 PKV_API int pkv_get_decode_variant(void);

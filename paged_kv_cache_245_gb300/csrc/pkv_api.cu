@@ -997,7 +997,9 @@ pkv_status prefill_common(const void* q, const int32_t* cu_seqlens_q, int32_t nu
   p.Hq = heads.num_q_heads;
   p.Hkv = heads.num_kv_heads;
   p.G = G;
-  p.max_q = max_q_tokens;
+  // No chunk is longer than q: rows of a chunk, max_q G, then fit 32 bits however
+  // generous the bound is.
+  p.max_q = std::min(max_q_tokens, num_tokens);
   p.run_rows = run_rows;
   p.qscale = scale * 1.4426950408889634f;  // log2(e)
   p.checked = g_checked.load();

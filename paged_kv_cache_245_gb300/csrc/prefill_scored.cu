@@ -1029,8 +1029,9 @@ cudaError_t launch_mode(const CUtensorMap& tk, const CUtensorMap& tv, const CUte
   pl.split = 1;
   // Waits outlast rows computed again: 32 a warp, one after another, at 4 positions in
   // 0.8 us (6.4 us a position: 50000 of them 0.32 s), after a look through V (16
-  // positions in 1 us).  The limit allows for ten times that.
-  pl.wait_ns = kWaitLimitNs + 65536ull * static_cast<unsigned long long>(p.max_blocks) * p.bs;
+  // positions in 1 us).  A role may wait for two such items in a row; the limit allows
+  // for 2.5 times that.
+  pl.wait_ns = kWaitLimitNs + 32768ull * static_cast<unsigned long long>(p.max_blocks) * p.bs;
   // few items: the largest cluster an item that the device holds for all of them
   // at once, and whose parts the key tiles (at most) are enough for
   int64_t span = static_cast<int64_t>(p.max_blocks) * p.bs;

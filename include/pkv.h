@@ -157,8 +157,11 @@ PKV_API pkv_status pkv_rope_init_frequencies(pkv_rope *rope, int32_t rotary_dim,
  *   k_cache[slot / block_size][h][slot % block_size][:], slot = slot_mapping[t],
  * and v is copied to the same place of v_cache.  Slots as for pkv_kv_append
  * (negative: the token's k and v go nowhere; its q is still turned;
- * contiguous layout: block_size = S).  The angle is exact for every int32
- * position; the turned values are computed in fp32 and rounded once, to bf16.
+ * contiguous layout: block_size = S).  The angle loses nothing at far positions:
+ * position times the plan's frequency is exact modulo a turn, for every int32.
+ * What is left is the frequency's own rounding (2^-54 turns a position up to one
+ * radian, in proportion above it: 2^-34 turns at a million positions).  The turned
+ * values are computed in fp32 and rounded once, to bf16.
  *
  * q, k and v are read at a stride of q_stride, k_stride and v_stride elements
  * per token (multiples of 8, >= 0; a token's heads are adjacent), so views of

@@ -21,7 +21,7 @@
 // its warps, which all meet at the end of every pair, so a pair of a few tiles
 // costs it 3 to 4 us; here it costs one warp its own tiles.  Both are bound by
 // HBM in between: 64 ragged sequences up to 8192 under a window of 1024, 32 / 8
-// heads (115 MB, 17.0 us at the rate of a copy) take 25.1 us, of which 2 go by
+// heads (115 MB, 17.0 us at the rate of a copy) take 25.6 us, of which 2 go by
 // before the runs are known, 2 more until the first tiles are asked for, and 2.6
 // at the end for the joins.  256 sequences of 128: 30.2 us; by pairs 62.
 //

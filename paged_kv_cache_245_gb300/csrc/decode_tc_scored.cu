@@ -3,7 +3,7 @@
 // ones).  The scores are capped, biased and masked on the accumulators, under the
 // memory's time: 128 sequences of 8000 to 8192 positions in documents of about
 // 6000, 56 / 8 heads, capped (1.84 GB): 270 us, 6.8 TB/s, 1.00 of a plain copy;
-// 32 contiguous of 100 to 4095, 32 / 4 heads, with slopes (72 MB): 19.9 us, of
+// 32 contiguous of 100 to 4095, 32 / 4 heads, with slopes (72 MB): 20.0 us, of
 // which 10.6 are the bytes; the rest is the launch, the schedule (three dependent
 // reads) and the pairs' merges.
 #include "decode_tc_host.cuh"

@@ -181,7 +181,10 @@ bool tc_enough_tiles(int32_t num_seqs, const pkv_heads& h, int32_t max_context, 
 // 256, 1024 and 2048 15.4 / 24.0, 25.2 / 31.4 and 34.0 / 38.9, without one 55.9 /
 // 58.1; 64 of 512, 1024 and 2048 28.5 / 33.0, 48.4 / 48.2 and 88.8 / 88.0; 8 of
 // 512 and 2048 11.1 / 10.9 and 15.5 / 16.8; 256 of 2048 329 / 321; 128 of 8192
-// with 56 query heads 287 / 270.
+// with 56 query heads 287 / 270.  What decides is how many tiles a pair has, which
+// lies in context lengths that only the device knows; the bound that the host
+// knows picks the slower kernel by 2 to 4 % in the ragged batch without a window
+// (pairs) and in the even ones of 2048 (runs).
 constexpr int32_t kRunsMaxSpan = 2048 + 15;
 
 // Scored decode of few tiles: the splits of a (sequence, KV head) as a cluster

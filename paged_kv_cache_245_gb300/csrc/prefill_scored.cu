@@ -26,8 +26,8 @@
 // once, and joins its parts through distributed shared memory (join_parts).
 // The join takes 5 us, a key tile 1.8 (one row tile) to 2.2 us: items of fewer
 // than kJoinTiles are the first CTA's alone.  32 / 8 heads, one CTA / a cluster
-// an item: 64 tokens after 8000 129 / 31 us, 512 after 8000 136 / 86, 2 x 256
-// after 2000 to 4000 70 / 49, 4 x 1 after 996 21.1 / 14.7.  Kernels of their own:
+// an item: 64 tokens after 8000 129 / 30 us, 512 after 8000 136 / 81, 2 x 256
+// after 2000 to 4000 70 / 46, 4 x 1 after 996 21.1 / 13.9.  Kernels of their own:
 // in one, the code of the join cost 2 x 8192 tokens 256 -> 262 us.
 //
 // Roles, tensor memory and the order of products are the plain kernel's:
@@ -42,9 +42,11 @@
 // and slower: two warps per 32 rows, each on half the keys (+3 %); P in shared
 // memory, so that S is free once it is in registers (+15 %: each hand-over
 // waits for the proxy fence, and both softmax warpgroups run in step).  32 / 8
-// heads, 8 chunks of 2048: masks alone 253 us (1090 TFLOP/s), capped 273 (1007),
-// with slopes 272, capped with slopes 349, any score 508; contiguous 2 x 8192
-// under a window of 1024: 257 us (1000 TFLOP/s).
+// heads, 8 chunks of 2048: masks alone 254 us (1083 TFLOP/s), capped 273 (1007),
+// with slopes 273, capped with slopes 335, any score 509; contiguous 2 x 8192
+// under a window of 1024: 258 us (996 TFLOP/s).  The plain kernel takes 238 us for
+// the first: what its softmax does not do (masks, the cap, the check of the output
+// rows) is the rest, and two exposed loads of S a tile.
 #include <algorithm>
 #include <atomic>
 #include <climits>

@@ -21,13 +21,17 @@
 // it is an odd polynomial on packed pairs, s (c0 + c1 w + .. + c4 w^4), w = s^2:
 // the minimax fit of tanh(y) / y over y^2 in [0, 1] (relative error 2^-17, by
 // Remez exchange; the probabilities are rounded to 2^-9 after it).  Half tiles
-// with a larger score take the exponentials.
+// with a larger score take the exponentials, after the polynomial that told so.
+// Caps below 11 always do: 64 scores of 0 fall outside the sums that tile_capped
+// accepts, and below 8.2 no sum is inside.  8 x 2048 tokens: caps of 2 to 10 554
+// us whatever the scores; 12 and 15 285 us for scores of 0.25 and 554 for scores
+// of 4 (most half tiles hold one beyond the cap); 30 and 50 273 us.
 //
 // Biased scores (kPrefillBiased).  Up to the row's own position the bias is
 // linear in the column: one packed addition and one fused product a pair.  The
 // key tiles come last first, so that the bias only falls (8 x 2048 tokens 288 ->
 // 272 us).  Capped and biased (kPrefillCappedBiased): the bias of the nearest key
-// stands in for the maximum, and again one pass does (522 -> 349 us).
+// stands in for the maximum, and again one pass does (522 -> 335 us).
 #pragma once
 
 #include <limits.h>

@@ -12,7 +12,8 @@
  * pkv_block_swap moves whole blocks between the device cache and a pool in
  * page-locked host memory (pre-emption by swapping).  pkv_rope_append is the
  * append with rotary positions; the *_attention_scored calls are the attention
- * calls with scores that are capped, biased or masked.
+ * calls with scores that are capped, biased or masked; the *_q8 calls are the
+ * append and the attention over a cache held in 8 bits.
  *
  * Conventions for every call:
  *   - All tensor arguments are DEVICE pointers on the current CUDA device,
@@ -453,6 +454,102 @@ PKV_API pkv_status pkv_contig_prefill_attention_scored(
     const void *v_buf, const int32_t *req_ids, int32_t max_reqs, const int32_t *context_lens,
     int32_t num_seqs, int32_t max_q_tokens, int64_t S, float scale, const pkv_score *score,
     pkv_heads heads, void *out, void *stream);
+
+/*
+ * The cache in 8 bits.  The pages have no counterpart: it is the same cache at
+ * about half the bytes.  K and V are codes of one byte in the layouts above
+ * ([num_blocks][Hkv][block_size][128], contiguous [max_reqs][Hkv][S][128]) with
+ * one fp32 scale for every group of 16 rows of a block and KV head:
+ *   k_scale, v_scale   [num_blocks][Hkv][block_size / 16]  (contiguous: S / 16)
+ *   value = code * scale
+ * block_size (S) must be a multiple of 16.  Codes are 16-byte aligned, scales
+ * 4-byte.  Copy-on-write copies and swaps go through pkv_block_copy /
+ * pkv_block_swap, once over the codes and once over the scales (whose block is
+ * Hkv * block_size / 4 bytes, which those calls want to be a multiple of 16).
+ */
+typedef struct pkv_q8_cache {
+    void *k, *v;                /* codes                                        */
+    float *k_scale, *v_scale;
+    int32_t format;             /* PKV_Q8_*                                     */
+    int32_t reserved;
+} pkv_q8_cache;
+
+enum {
+    PKV_Q8_INT8 = 1,   /* -127 .. 127, round to nearest even                     */
+    PKV_Q8_E4M3 = 2    /* 1 sign, 4 exponent, 3 mantissa bits, largest 448       */
+};
+
+/*
+ * Append to it.  Slots as for pkv_kv_append (negative: the token's rows go
+ * nowhere; contiguous layout: block_size = S), in any order.  For each group
+ * that the call writes to, each head, K and V by themselves, in fp32:
+ *   a    = largest |x| of the new rows (infinities and NaN aside)
+ *   old  = 0 if the group's row 0 is written (it starts anew), else its scale
+ *   s    = max(old, a / qmax), qmax 127 or 448, is the new scale
+ *   inv  = 1 / s, or 0 for s < 2^-100
+ *   new rows:           code = round(x * inv)
+ *   the other rows:     code = round(code * old * inv) where s > old; as they
+ *                       were where s = old; 0 where the group starts anew
+ * each operation rounded once, so the codes are exact.  Appending position by
+ * position therefore needs no preparation of a block (its first row starts each
+ * group), and zeroed scales where a group's row 0 is never written.  Infinities
+ * become the largest code; NaN stays NaN in e4m3 and becomes 0 in int8.  A slot
+ * that two tokens of a call share takes the later one's row (both count for a).
+ * k and v are read at k_stride and v_stride elements per token as for
+ * pkv_rope_append.  num_tokens is at most 2^30.
+ */
+PKV_API pkv_status pkv_kv_append_q8(const int64_t *slot_mapping, int64_t num_tokens,
+                                    const void *k, int64_t k_stride, const void *v,
+                                    int64_t v_stride, const pkv_q8_cache *cache,
+                                    int64_t num_slots, int64_t block_size, pkv_heads heads,
+                                    void *stream);
+
+/*
+ * The same with rotary positions on the way: arguments as for pkv_rope_append.
+ * The turned keys are quantised from fp32 (not rounded to bf16 first).
+ */
+PKV_API pkv_status pkv_rope_append_q8(const int32_t *positions, const int64_t *slot_mapping,
+                                      int64_t num_tokens, const void *q, int64_t q_stride,
+                                      const void *k, int64_t k_stride, const void *v,
+                                      int64_t v_stride, void *q_out, const pkv_q8_cache *cache,
+                                      int64_t num_slots, int64_t block_size, pkv_heads heads,
+                                      const pkv_rope *rope, void *stream);
+
+/*
+ * Decode attention over it: arguments, layouts, errors and checked mode as for
+ * pkv_paged_decode_attention / pkv_contig_decode_attention, with
+ * K_j = code * scale (and block_size, S multiples of 16:
+ * PKV_ERR_UNSUPPORTED otherwise).  Rows at or past a context are not read into
+ * the result, whatever stands there.  workspace must hold
+ * pkv_q8_decode_workspace_size(num_seqs, heads, max_context) bytes (16-byte
+ * aligned) when that is not 0; its contents need no initialisation.
+ */
+PKV_API size_t pkv_q8_decode_workspace_size(int32_t num_seqs, pkv_heads heads,
+                                            int32_t max_context);
+PKV_API pkv_status pkv_paged_decode_attention_q8(
+    const void *q, const pkv_q8_cache *cache, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *context_lens,
+    int32_t num_seqs, int32_t max_context, int32_t block_size, float scale, pkv_heads heads,
+    void *out, void *workspace, size_t workspace_bytes, void *stream);
+PKV_API pkv_status pkv_contig_decode_attention_q8(
+    const void *q, const pkv_q8_cache *cache, const int32_t *req_ids, int32_t max_reqs,
+    const int32_t *context_lens, int32_t num_seqs, int32_t max_context, int64_t S, float scale,
+    pkv_heads heads, void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Causal prefill attention over it: arguments, layouts, errors and checked mode
+ * as for pkv_paged_prefill_attention / pkv_contig_prefill_attention.  Rows of
+ * q and out behind the last chunk are left alone.
+ */
+PKV_API pkv_status pkv_paged_prefill_attention_q8(
+    const void *q, const int32_t *cu_seqlens_q, int32_t num_tokens, const pkv_q8_cache *cache,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t num_blocks,
+    const int32_t *context_lens, int32_t num_seqs, int32_t max_q_tokens, int32_t block_size,
+    float scale, pkv_heads heads, void *out, void *stream);
+PKV_API pkv_status pkv_contig_prefill_attention_q8(
+    const void *q, const int32_t *cu_seqlens_q, int32_t num_tokens, const pkv_q8_cache *cache,
+    const int32_t *req_ids, int32_t max_reqs, const int32_t *context_lens, int32_t num_seqs,
+    int32_t max_q_tokens, int64_t S, float scale, pkv_heads heads, void *out, void *stream);
 
 /*
  * Copy-on-write block copy.  "Running Out of Cache" (section "Fragmentation

@@ -15,7 +15,10 @@ from .binding import (BlockManager, PkvError, VmmBuffer, block_copy, block_swap,
                       set_split_tiles, VARIANT_AUTO, VARIANT_SPLIT, VARIANT_TC_8X3,
                       VARIANT_TC_12X2, RopePlan, rope_append, scored_decode_workspace_size,
                       paged_decode_attention_scored, contig_decode_attention_scored,
-                      paged_prefill_attention_scored, contig_prefill_attention_scored)
+                      paged_prefill_attention_scored, contig_prefill_attention_scored,
+                      kv_append_q8, rope_append_q8, q8_decode_workspace_size,
+                      paged_decode_attention_q8, contig_decode_attention_q8,
+                      paged_prefill_attention_q8, contig_prefill_attention_q8)
 
 __all__ = ["BlockManager", "PkvError", "VmmBuffer", "block_copy", "block_swap", "BM_RETIRED",
            "BM_RUNNING", "BM_SWAPPED", "BM_RECOMPUTE", "PREEMPT_RECOMPUTE", "PREEMPT_SWAP",
@@ -28,4 +31,7 @@ __all__ = ["BlockManager", "PkvError", "VmmBuffer", "block_copy", "block_swap", 
            "get_decode_variant", "VARIANT_AUTO", "VARIANT_SPLIT", "VARIANT_TC_8X3",
            "VARIANT_TC_12X2", "RopePlan", "rope_append", "scored_decode_workspace_size",
            "paged_decode_attention_scored", "contig_decode_attention_scored",
-           "paged_prefill_attention_scored", "contig_prefill_attention_scored"]
+           "paged_prefill_attention_scored", "contig_prefill_attention_scored", "kv_append_q8",
+           "rope_append_q8", "q8_decode_workspace_size", "paged_decode_attention_q8",
+           "contig_decode_attention_q8", "paged_prefill_attention_q8",
+           "contig_prefill_attention_q8"]

@@ -38,6 +38,9 @@ EXPORTED = ("pkv_kv_append", "pkv_decode_num_splits", "pkv_decode_uses_tensor_co
             "pkv_scored_decode_workspace_size", "pkv_paged_decode_attention_scored",
             "pkv_contig_decode_attention_scored", "pkv_paged_prefill_attention_scored",
             "pkv_contig_prefill_attention_scored",
+            "pkv_kv_append_q8", "pkv_rope_append_q8", "pkv_q8_decode_workspace_size",
+            "pkv_paged_decode_attention_q8", "pkv_contig_decode_attention_q8",
+            "pkv_paged_prefill_attention_q8", "pkv_contig_prefill_attention_q8",
             "pkv_get_device_error", "pkv_status_string", "pkv_last_error")
 
 
@@ -68,6 +71,12 @@ class Score(ctypes.Structure):
     _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
                 ("alibi_slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p),
                 ("prefix_lens", ctypes.c_void_p)]
+
+
+class Q8Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -129,6 +138,20 @@ def lib():
                                                      i32, i32, ctypes.c_float, sp, Heads, vp, vp]
     L.pkv_contig_prefill_attention_scored.argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, i32, i32,
                                                       i64, ctypes.c_float, sp, Heads, vp, vp]
+    qp = ctypes.POINTER(Q8Cache)
+    L.pkv_kv_append_q8.argtypes = [vp, i64, vp, i64, vp, i64, qp, i64, i64, Heads, vp]
+    L.pkv_rope_append_q8.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, qp, i64, i64,
+                                     Heads, ctypes.POINTER(Rope), vp]
+    L.pkv_q8_decode_workspace_size.argtypes = [i32, Heads, i32]
+    L.pkv_q8_decode_workspace_size.restype = sz
+    L.pkv_paged_decode_attention_q8.argtypes = [vp, qp, vp, i32, i32, vp, i32, i32, i32,
+                                                ctypes.c_float, Heads, vp, vp, sz, vp]
+    L.pkv_contig_decode_attention_q8.argtypes = [vp, qp, vp, i32, vp, i32, i32, i64,
+                                                 ctypes.c_float, Heads, vp, vp, sz, vp]
+    L.pkv_paged_prefill_attention_q8.argtypes = [vp, vp, i32, qp, vp, i32, i32, vp, i32, i32, i32,
+                                                 ctypes.c_float, Heads, vp, vp]
+    L.pkv_contig_prefill_attention_q8.argtypes = [vp, vp, i32, qp, vp, i32, vp, i32, i32, i64,
+                                                  ctypes.c_float, Heads, vp, vp]
     L.pkv_set_checked.argtypes = [ctypes.c_int]
     L.pkv_set_checked.restype = None
     L.pkv_get_checked.restype = ctypes.c_int
@@ -745,6 +768,181 @@ def contig_prefill_attention_scored(q, cu_seqlens_q, k_buf, v_buf, req_ids, cont
                            prefix_lens, out)
 
 
+_Q8_FORMATS = {torch.int8: 1, torch.float8_e4m3fn: 2}
+
+
+def _q8_cache(dev, k, v, k_scale, v_scale):
+    """(Q8Cache, shape [blocks, Hkv, rows, D]) of an 8-bit cache on device `dev`."""
+    if not isinstance(k, torch.Tensor) or k.dtype not in _Q8_FORMATS:
+        raise TypeError("the cache's codes must be torch.int8 or torch.float8_e4m3fn")
+    _check_in(k, k.dtype, 4, dev, "k_cache")
+    _check_in(v, k.dtype, 4, dev, "v_cache")
+    _check_in(k_scale, torch.float32, 3, dev, "k_scale")
+    _check_in(v_scale, torch.float32, 3, dev, "v_scale")
+    shape = k.shape
+    n, hkv, rows, d = shape
+    if v.shape != shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    if rows % 16:
+        raise ValueError("an 8-bit cache needs a block size (S) that is a multiple of 16")
+    if k_scale.shape != (n, hkv, rows // 16) or v_scale.shape != k_scale.shape:
+        raise ValueError("k_scale and v_scale must be [blocks, Hkv, block_size / 16]")
+    return Q8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                   _Q8_FORMATS[k.dtype], 0), shape
+
+
+def kv_append_q8(slot_mapping, k, v, k_cache, v_cache, k_scale, v_scale):
+    """Quantise new rows k, v [T, Hkv, D] (any token stride that is a multiple
+    of 8) into an 8-bit cache at slot_mapping [T] (int64, as for kv_append).
+    The caches are [num_blocks, Hkv, block_size, D] (or [max_reqs, Hkv, S, D])
+    of torch.int8 or torch.float8_e4m3fn, their scales fp32 [num_blocks, Hkv,
+    block_size / 16]: value = code * scale.  A group of 16 rows starts anew when
+    its first row is written; its scale grows, and the rows that it holds are
+    rounded again, when a larger row comes."""
+    dev = _device_index(k, "k")
+    sk, T, *dims = _token_rows(k, dev, "k")
+    sv, *v_dims = _token_rows(v, dev, "v")
+    _check_in(slot_mapping, torch.int64, 1, dev, "slot_mapping")
+    cache, (nb, hkv, bs, d) = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if dims != [hkv, d] or v_dims != [T, hkv, d]:
+        raise ValueError("k and v must be [T, Hkv, D] matching the cache")
+    if slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must have one entry per token")
+    _on_device(dev, lib().pkv_kv_append_q8, slot_mapping.data_ptr(), T, k.data_ptr(), sk,
+               v.data_ptr(), sv, cache, nb * bs, bs, Heads(hkv, hkv, d))
+
+
+def rope_append_q8(positions, slot_mapping, q, k, v, k_cache, v_cache, k_scale, v_scale, rope,
+                   out=None):
+    """rope_append into an 8-bit cache (kv_append_q8): turn q [T, Hq, D] and k
+    by their positions [T] (int32), quantise the turned k and v into the cache
+    and return the turned q (bf16)."""
+    dev = _device_index(q, "q")
+    sq, T, hq, dq = _token_rows(q, dev, "q")
+    sk, *k_dims = _token_rows(k, dev, "k")
+    sv, *v_dims = _token_rows(v, dev, "v")
+    _check_in(positions, torch.int32, 1, dev, "positions")
+    _check_in(slot_mapping, torch.int64, 1, dev, "slot_mapping")
+    cache, (nb, hkv, bs, d) = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if not isinstance(rope, RopePlan):
+        raise TypeError("rope must be a RopePlan")
+    if k_dims != [T, hkv, d] or v_dims != k_dims or dq != d:
+        raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D] matching the cache")
+    if positions.numel() != T or slot_mapping.numel() != T:
+        raise ValueError("positions / slot_mapping must have one entry per token")
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _check_in(out, torch.bfloat16, 3, dev, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must be [T, Hq, D]")
+    _on_device(dev, lib().pkv_rope_append_q8, positions.data_ptr(), slot_mapping.data_ptr(), T,
+               q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(), cache,
+               nb * bs, bs, Heads(hq, hkv, d), rope.c)
+    return out
+
+
+def q8_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_context, head_dim=128):
+    """Bytes of workspace that decode attention over an 8-bit cache needs."""
+    return int(lib().pkv_q8_decode_workspace_size(
+        num_seqs, heads(num_q_heads, num_kv_heads, head_dim), max_context))
+
+
+def _attention_q8(contig, q, k, v, k_scale, v_scale, where, context_lens, out):
+    """Checks shared by the calls over an 8-bit cache: (device, B, Q8Cache, its
+    shape, heads, out)."""
+    dev = _device_index(q, "q")
+    _check_in(q, torch.bfloat16, 3, dev, "q")
+    cache, shape = _q8_cache(dev, k, v, k_scale, v_scale)
+    _check_in(where, torch.int32, 1 if contig else 2, dev, "req_ids" if contig else "block_tables")
+    _check_in(context_lens, torch.int32, 1, dev, "context_lens")
+    rows, hq, d = q.shape
+    if d != shape[3]:
+        raise ValueError("q / cache shapes disagree")
+    B = context_lens.shape[0]
+    if where.shape[0] != B:
+        raise ValueError("%s must have num_seqs rows" % ("req_ids" if contig else "block_tables"))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_in(out, torch.bfloat16, 3, dev, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must be like q")
+    return dev, B, cache, shape, Heads(hq, shape[1], d), out
+
+
+def _decode_q8(contig, q, k, v, k_scale, v_scale, where, context_lens, max_context, scale, out,
+               workspace):
+    dev, B, cache, (n, _, rows, _), h, out = _attention_q8(contig, q, k, v, k_scale, v_scale,
+                                                           where, context_lens, out)
+    if q.shape[0] != B:
+        raise ValueError("q must have one row per sequence")
+    ws, ws_len = 0, 0
+    if workspace is None:
+        size = lib().pkv_q8_decode_workspace_size(B, h, max_context)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    if workspace is not None:
+        ws, ws_len = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if contig:
+        _on_device(dev, lib().pkv_contig_decode_attention_q8, q.data_ptr(), cache,
+                   where.data_ptr(), n, context_lens.data_ptr(), B, max_context, rows, scale, h,
+                   out.data_ptr(), ws, ws_len)
+    else:
+        _on_device(dev, lib().pkv_paged_decode_attention_q8, q.data_ptr(), cache,
+                   where.data_ptr(), where.shape[1], n, context_lens.data_ptr(), B, max_context,
+                   rows, scale, h, out.data_ptr(), ws, ws_len)
+    return out
+
+
+def paged_decode_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                              max_context, scale, out=None, workspace=None):
+    """paged_decode_attention over an 8-bit cache (kv_append_q8)."""
+    return _decode_q8(False, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                      max_context, scale, out, workspace)
+
+
+def contig_decode_attention_q8(q, k_buf, v_buf, k_scale, v_scale, req_ids, context_lens,
+                               max_context, scale, out=None, workspace=None):
+    """contig_decode_attention over an 8-bit cache [max_reqs, Hkv, S, D]."""
+    return _decode_q8(True, q, k_buf, v_buf, k_scale, v_scale, req_ids, context_lens, max_context,
+                      scale, out, workspace)
+
+
+def _prefill_q8(contig, q, cu_seqlens_q, k, v, k_scale, v_scale, where, context_lens,
+                max_q_tokens, scale, out):
+    dev, B, cache, (n, _, rows, _), h, out = _attention_q8(contig, q, k, v, k_scale, v_scale,
+                                                           where, context_lens, out)
+    _check_in(cu_seqlens_q, torch.int32, 1, dev, "cu_seqlens_q")
+    if cu_seqlens_q.numel() != B + 1:
+        raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
+    if contig:
+        _on_device(dev, lib().pkv_contig_prefill_attention_q8, q.data_ptr(),
+                   cu_seqlens_q.data_ptr(), q.shape[0], cache, where.data_ptr(), n,
+                   context_lens.data_ptr(), B, max_q_tokens, rows, scale, h, out.data_ptr())
+    else:
+        _on_device(dev, lib().pkv_paged_prefill_attention_q8, q.data_ptr(),
+                   cu_seqlens_q.data_ptr(), q.shape[0], cache, where.data_ptr(), where.shape[1],
+                   n, context_lens.data_ptr(), B, max_q_tokens, rows, scale, h, out.data_ptr())
+    return out
+
+
+def paged_prefill_attention_q8(q, cu_seqlens_q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                               context_lens, max_q_tokens, scale, out=None):
+    """paged_prefill_attention over an 8-bit cache (kv_append_q8)."""
+    return _prefill_q8(False, q, cu_seqlens_q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                       context_lens, max_q_tokens, scale, out)
+
+
+def contig_prefill_attention_q8(q, cu_seqlens_q, k_buf, v_buf, k_scale, v_scale, req_ids,
+                                context_lens, max_q_tokens, scale, out=None):
+    """contig_prefill_attention over an 8-bit cache [max_reqs, Hkv, S, D]."""
+    return _prefill_q8(True, q, cu_seqlens_q, k_buf, v_buf, k_scale, v_scale, req_ids,
+                       context_lens, max_q_tokens, scale, out)
+
+
 def debug_gather_paged(cache, block_tables, context_lens, max_context):
     """Test-only: the logical rows [B, Hkv, max_context, D] the decode kernels
     read through block_tables (zeros past each context)."""
@@ -773,20 +971,29 @@ def debug_gather_contig(buf, req_ids, context_lens, max_context):
     return out
 
 
+def _block_dtype(t):
+    """The type of a pool whose blocks are copied: bf16, or a part of an 8-bit cache."""
+    return t.dtype if t.dtype in (torch.int8, torch.float8_e4m3fn, torch.float32) \
+        else torch.bfloat16
+
+
 def block_copy(src_dst_pairs, k_caches, v_caches):
     """Copy whole blocks src -> dst (pairs [n, 2] int64 on the device) in every
-    layer's K and V cache (lists of [num_blocks, ...] bf16 tensors)."""
+    layer's K and V cache (lists of [num_blocks, ...] tensors of one type: bf16,
+    or an 8-bit cache's codes, and in a call of their own its scales, whose block
+    must be a multiple of 16 bytes)."""
     _need(src_dst_pairs, torch.int64, "src_dst_pairs", 2)
     L = len(k_caches)
     if L != len(v_caches) or L == 0:
         raise ValueError("need one K and one V cache per layer")
     shape = tuple(k_caches[0].shape)
+    dtype = _block_dtype(k_caches[0])
     for t in list(k_caches) + list(v_caches):
-        _need(t, torch.bfloat16, "cache")
+        _need(t, dtype, "cache")
         if tuple(t.shape) != shape:
             raise ValueError("all caches must have one shape")
     nb = shape[0]
-    block_bytes = k_caches[0][0].numel() * 2
+    block_bytes = k_caches[0][0].numel() * dtype.itemsize
     kp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_caches])
     vp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_caches])
     _check(lib().pkv_block_copy(_ptr(src_dst_pairs), src_dst_pairs.shape[0], kp, vp, L, nb,
@@ -796,7 +1003,7 @@ def block_copy(src_dst_pairs, k_caches, v_caches):
 def block_swap(pairs, src_k, src_v, dst_k, dst_v):
     """Copy whole blocks from one pool to another, pairs [n, 2] int64 of
     (src block, dst block), in every layer's K and V (lists of [blocks, ...]
-    bf16 tensors, one shape per side).  Either side may be page-locked host
+    tensors of one type, as for block_copy, one shape per side).  Either side may be page-locked host
     memory (``tensor.pin_memory()``): that is the swap of pre-empted
     sequences out of, and back into, the device cache.  pairs may be a
     device tensor or a pinned host tensor."""
@@ -807,15 +1014,17 @@ def block_swap(pairs, src_k, src_v, dst_k, dst_v):
     if not (L == len(src_v) == len(dst_k) == len(dst_v)) or L == 0:
         raise ValueError("need one K and one V pool per layer on each side")
     blocks = []
+    dtype = _block_dtype(src_k[0])
     for side in ((src_k, src_v), (dst_k, dst_v)):
         shape = tuple(side[0][0].shape)
         for t in list(side[0]) + list(side[1]):
-            if t.dtype != torch.bfloat16 or not t.is_contiguous() or tuple(t.shape) != shape:
-                raise ValueError("pools must be contiguous bf16 tensors of one shape per side")
+            if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape:
+                raise ValueError("pools must be contiguous %s tensors of one shape per side"
+                                 % dtype)
         blocks.append(shape)
     if blocks[0][1:] != blocks[1][1:]:
         raise ValueError("the two sides must have the same block shape")
-    block_bytes = src_k[0][0].numel() * 2
+    block_bytes = src_k[0][0].numel() * dtype.itemsize
     arr = [(ctypes.c_void_p * L)(*[t.data_ptr() for t in x]) for x in (src_k, src_v, dst_k, dst_v)]
     dev = next((t for t in (src_k[0], dst_k[0], pairs) if t.is_cuda), None)
     if dev is None:

@@ -19,6 +19,7 @@
 #include "prefix.cuh"
 #include "decode_tc_launch.h"
 #include "kv_ops.cuh"
+#include "q8.cuh"
 #include "rope.cuh"
 #include "score.cuh"
 
@@ -1333,6 +1334,236 @@ pkv_status pkv_rope_append(const int32_t* positions, const int64_t* slot_mapping
   const cudaError_t e = pkv::launch_rope_append(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rope_append launch");
   return PKV_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+pkv_status check_q8(const pkv_q8_cache* c, int64_t block_size) {
+  if (!c) return fail(PKV_ERR_INVALID_ARG, "cache is null");
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale)
+    return fail(PKV_ERR_INVALID_ARG, "null cache pointer");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16))
+    return fail(PKV_ERR_INVALID_ARG, "codes must be 16-byte aligned");
+  if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    return fail(PKV_ERR_INVALID_ARG, "scales misaligned");
+  if (c->format != PKV_Q8_INT8 && c->format != PKV_Q8_E4M3)
+    return fail(PKV_ERR_INVALID_ARG, "unknown 8-bit format %d", c->format);
+  if (block_size <= 0) return fail(PKV_ERR_INVALID_ARG, "block_size must be >= 1");
+  if (block_size % pkv::kGroupRows != 0)
+    return fail(PKV_ERR_UNSUPPORTED, "the 8-bit cache needs block_size %% 16 == 0");
+  return PKV_OK;
+}
+
+// Appends to the 8-bit cache; rope (and positions, q, q_out) null: no positions.
+pkv_status append_q8_common(const int32_t* positions, const int64_t* slot_mapping,
+                            int64_t num_tokens, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                            const pkv_q8_cache* cache, int64_t num_slots, int64_t block_size,
+                            pkv_heads heads, const pkv_rope* rope, void* stream) {
+  if (num_tokens < 0 || num_slots < 0) return fail(PKV_ERR_INVALID_ARG, "negative size");
+  if (num_tokens == 0) return PKV_OK;
+  if (num_tokens > (int64_t{1} << 30)) return fail(PKV_ERR_UNSUPPORTED, "too many tokens");
+  pkv_status st = check_q8(cache, block_size);
+  if (st != PKV_OK) return st;
+  if (!slot_mapping || !k || !v) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(slot_mapping, 8)) return fail(PKV_ERR_INVALID_ARG, "slot_mapping misaligned");
+  if (!aligned(k, 16) || !aligned(v, 16))
+    return fail(PKV_ERR_INVALID_ARG, "bf16 tensors must be 16-byte aligned");
+  const int64_t strides[3] = {rope ? q_stride : 0, k_stride, v_stride};
+  for (int64_t x : strides)
+    if (x < 0 || x % 8 != 0 || x > (int64_t{1} << 31))
+      return fail(PKV_ERR_INVALID_ARG, "token strides must be multiples of 8 in 0..2^31");
+  if (rope) {
+    if (!positions || !q || !q_out) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(positions, 4)) return fail(PKV_ERR_INVALID_ARG, "positions misaligned");
+    if (!aligned(q, 16) || !aligned(q_out, 16))
+      return fail(PKV_ERR_INVALID_ARG, "bf16 tensors must be 16-byte aligned");
+    const int64_t q_row = static_cast<int64_t>(heads.num_q_heads) * pkv::kRowBytes;
+    const int64_t kv_row = static_cast<int64_t>(heads.num_kv_heads) * pkv::kRowBytes;
+    const int64_t n = num_tokens;
+    const bool in_place = q_out == q && (n == 1 || 2 * q_stride == q_row);
+    if (!in_place && overlap(q_out, n * q_row, q, (n - 1) * 2 * q_stride + q_row))
+      return fail(PKV_ERR_INVALID_ARG, "q_out overlaps q (and is not q itself with stride Hq * 128)");
+    if (overlap(q_out, n * q_row, k, (n - 1) * 2 * k_stride + kv_row) ||
+        overlap(q_out, n * q_row, v, (n - 1) * 2 * v_stride + kv_row))
+      return fail(PKV_ERR_INVALID_ARG, "q_out overlaps k or v");
+  }
+  int* err = nullptr;
+  st = device_info(nullptr, &err, nullptr);
+  if (st != PKV_OK) return st;
+  pkv::AppendQ8Params p;
+  std::memset(&p, 0, sizeof p);
+  p.slot_mapping = slot_mapping;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.k_codes = static_cast<uint8_t*>(cache->k);
+  p.v_codes = static_cast<uint8_t*>(cache->v);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.num_slots = num_slots;
+  p.bs = block_size;
+  p.num_tokens = static_cast<int32_t>(num_tokens);
+  p.Hkv = heads.num_kv_heads;
+  if (rope) {
+    p.positions = positions;
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.q_stride = q_stride;
+    p.Hq = heads.num_q_heads;
+    p.rope = *rope;
+  }
+  p.checked = g_checked.load();
+  p.err = err;
+  const cudaError_t e = pkv::launch_append_q8(p, cache->format == PKV_Q8_E4M3, rope != nullptr,
+                                              static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "append_q8 launch");
+  return PKV_OK;
+}
+
+// Attention over the 8-bit cache.  cu_q null: decode, a row of q per sequence.
+// contig: tables are request ids, max_blocks 1, num_blocks the requests, bs = S.
+pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_tokens,
+                               const pkv_q8_cache* cache, bool contig, const int32_t* tables,
+                               int32_t max_blocks, int64_t num_blocks, const int32_t* context_lens,
+                               int32_t num_seqs, int32_t max_q, int32_t max_context, int64_t bs,
+                               float scale, pkv_heads h, void* out, void* stream) {
+  pkv_status st = check_heads(h);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || num_tokens < 0 || max_q < 0 || max_context < 0)
+    return fail(PKV_ERR_INVALID_ARG, "negative size");
+  if (num_seqs == 0 || num_tokens == 0 || max_q == 0) return PKV_OK;
+  if (num_seqs > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_seqs > 65535");
+  st = check_q8(cache, bs);
+  if (st != PKV_OK) return st;
+  if (!q || !tables || !context_lens || !out) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(q, 16) || !aligned(out, 16))
+    return fail(PKV_ERR_INVALID_ARG, "bf16 tensors must be 16-byte aligned");
+  if (!aligned(tables, 4) || !aligned(context_lens, 4) || !aligned(cu_q, 4))
+    return fail(PKV_ERR_INVALID_ARG, "int32 arrays misaligned");
+  if (!std::isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  if (max_blocks <= 0 || num_blocks <= 0)
+    return fail(PKV_ERR_INVALID_ARG, contig ? "max_reqs must be >= 1" : "empty block table or pool");
+  if (num_blocks * h.num_kv_heads > (int64_t{1} << 40) / bs)
+    return fail(PKV_ERR_UNSUPPORTED, "cache too large");
+  const int64_t holds = max_blocks * bs;
+  if (cu_q == nullptr) {
+    if (max_context > holds)
+      return fail(PKV_ERR_INVALID_ARG, contig ? "max_context > S"
+                                              : "max_blocks_per_seq * block_size < max_context");
+  } else {
+    if (holds > 0x7fffffffLL)
+      return fail(PKV_ERR_UNSUPPORTED, "block table longer than 2^31 positions");
+    max_context = static_cast<int32_t>(holds);
+  }
+  int dev = 0, sms = 0;
+  int* err = nullptr;
+  st = device_info(&dev, &err, &sms);
+  if (st != PKV_OK) return st;
+  pkv::AttentionQ8Params p;
+  std::memset(&p, 0, sizeof p);
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.cu_q = cu_q;
+  p.ctx_lens = context_lens;
+  p.tables = tables;
+  p.k_codes = static_cast<const uint8_t*>(cache->k);
+  p.v_codes = static_cast<const uint8_t*>(cache->v);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.bs = bs;
+  p.num_blocks = num_blocks;
+  p.max_blocks = max_blocks;
+  p.num_seqs = num_seqs;
+  p.Hq = h.num_q_heads;
+  p.Hkv = h.num_kv_heads;
+  p.G = h.num_q_heads / h.num_kv_heads;
+  p.max_q = cu_q != nullptr ? std::min(max_q, num_tokens) : 1;
+  p.max_context = max_context;
+  p.qscale = scale * 1.4426950408889634f;  // log2(e)
+  p.checked = g_checked.load();
+  p.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
+  p.err = err;
+  const cudaError_t e = pkv::launch_attention_q8(p, cache->format == PKV_Q8_E4M3,
+                                                 static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "q8 attention launch");
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_kv_append_q8(const int64_t* slot_mapping, int64_t num_tokens, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride,
+                            const pkv_q8_cache* cache, int64_t num_slots, int64_t block_size,
+                            pkv_heads heads, void* stream) {
+  if (heads.num_kv_heads <= 0) return fail(PKV_ERR_INVALID_ARG, "num_kv_heads must be positive");
+  if (heads.head_dim != pkv::kHeadDim)
+    return fail(PKV_ERR_UNSUPPORTED, "head_dim %d (only 128 is built)", heads.head_dim);
+  if (heads.num_kv_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads > 65535");
+  return append_q8_common(nullptr, slot_mapping, num_tokens, nullptr, 0, k, k_stride, v, v_stride,
+                          nullptr, cache, num_slots, block_size, heads, nullptr, stream);
+}
+
+pkv_status pkv_rope_append_q8(const int32_t* positions, const int64_t* slot_mapping,
+                              int64_t num_tokens, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                              const pkv_q8_cache* cache, int64_t num_slots, int64_t block_size,
+                              pkv_heads heads, const pkv_rope* rope, void* stream) {
+  pkv_status st = check_heads(heads);
+  if (st != PKV_OK) return st;
+  if (!rope) return fail(PKV_ERR_INVALID_ARG, "rope is null");
+  st = check_rope_shape(rope, rope->rotary_dim, rope->interleaved);
+  if (st != PKV_OK) return st;
+  return append_q8_common(positions, slot_mapping, num_tokens, q, q_stride, k, k_stride, v,
+                          v_stride, q_out, cache, num_slots, block_size, heads, rope, stream);
+}
+
+size_t pkv_q8_decode_workspace_size(int32_t num_seqs, pkv_heads heads, int32_t max_context) {
+  if (check_heads(heads) != PKV_OK || num_seqs <= 0 || max_context <= 0) return 0;
+  return 0;
+}
+
+pkv_status pkv_paged_decode_attention_q8(
+    const void* q, const pkv_q8_cache* cache, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t* context_lens,
+    int32_t num_seqs, int32_t max_context, int32_t block_size, float scale, pkv_heads heads,
+    void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return attention_q8_common(q, nullptr, num_seqs, cache, false, block_tables, max_blocks_per_seq,
+                             num_blocks, context_lens, num_seqs, 1, max_context, block_size, scale,
+                             heads, out, stream);
+}
+
+pkv_status pkv_contig_decode_attention_q8(
+    const void* q, const pkv_q8_cache* cache, const int32_t* req_ids, int32_t max_reqs,
+    const int32_t* context_lens, int32_t num_seqs, int32_t max_context, int64_t S, float scale,
+    pkv_heads heads, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return attention_q8_common(q, nullptr, num_seqs, cache, true, req_ids, 1, max_reqs, context_lens,
+                             num_seqs, 1, max_context, S, scale, heads, out, stream);
+}
+
+pkv_status pkv_paged_prefill_attention_q8(
+    const void* q, const int32_t* cu_seqlens_q, int32_t num_tokens, const pkv_q8_cache* cache,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t num_blocks,
+    const int32_t* context_lens, int32_t num_seqs, int32_t max_q_tokens, int32_t block_size,
+    float scale, pkv_heads heads, void* out, void* stream) {
+  if (num_seqs > 0 && !cu_seqlens_q) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+  return attention_q8_common(q, cu_seqlens_q, num_tokens, cache, false, block_tables,
+                             max_blocks_per_seq, num_blocks, context_lens, num_seqs, max_q_tokens,
+                             0, block_size, scale, heads, out, stream);
+}
+
+pkv_status pkv_contig_prefill_attention_q8(
+    const void* q, const int32_t* cu_seqlens_q, int32_t num_tokens, const pkv_q8_cache* cache,
+    const int32_t* req_ids, int32_t max_reqs, const int32_t* context_lens, int32_t num_seqs,
+    int32_t max_q_tokens, int64_t S, float scale, pkv_heads heads, void* out, void* stream) {
+  if (num_seqs > 0 && !cu_seqlens_q) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+  return attention_q8_common(q, cu_seqlens_q, num_tokens, cache, true, req_ids, 1, max_reqs,
+                             context_lens, num_seqs, max_q_tokens, 0, S, scale, heads, out, stream);
 }
 
 pkv_status pkv_block_copy(const int64_t* src_dst_pairs, int64_t n, void* const* k_caches,

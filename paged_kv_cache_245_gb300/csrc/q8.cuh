@@ -1,0 +1,89 @@
+// q8.cuh -- the 8-bit KV cache: codes (int8 or e4m3) with one fp32 scale for
+// every 16 rows of a (block, KV head), value = code * scale.  Parameters and
+// launchers of its append (append_q8.cu) and attention kernels.
+//
+// Row r (pkv_device.cuh: cache_row) holds 128 code bytes at codes + 128 r.
+// Block sizes are multiples of 16, so rows 16 n .. 16 n + 15 lie in one
+// (block, head): group n, with its scale at scale[n].
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/pkv.h"
+
+namespace pkv {
+
+constexpr int kGroupRows = 16;
+constexpr int kCodeRowBytes = 128;
+constexpr float kInt8Max = 127.f;
+constexpr float kE4m3Max = 448.f;
+// A scale below this holds zeros (its reciprocal would leave fp32's range).
+constexpr float kScaleTiny = 7.888609052210118e-31f;  // 2^-100
+
+struct AppendQ8Params {
+  const int64_t* slot_mapping;  // [T]
+  const uint16_t* k;            // [Hkv][128] at k + t * k_stride
+  const uint16_t* v;
+  int64_t k_stride, v_stride;   // elements
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_slots, bs;
+  int32_t num_tokens, Hkv;
+  // with rotary positions
+  const int32_t* positions;     // [T]
+  const uint16_t* q;            // [Hq][128] at q + t * q_stride
+  uint16_t* q_out;              // [T][Hq][128] (may be q)
+  int64_t q_stride;
+  int32_t Hq;
+  pkv_rope rope;
+  int32_t checked;
+  int* err;
+};
+
+// rope: turn queries and keys on the way.
+cudaError_t launch_append_q8(const AppendQ8Params& p, bool e4m3, bool rope, cudaStream_t stream);
+
+struct AttentionQ8Params {
+  const uint16_t* q;            // [T][Hq][128]
+  uint16_t* out;                // [T][Hq][128]
+  const int32_t* cu_q;          // prefill [B + 1]; null: one row per sequence
+  const int32_t* ctx_lens;      // [B]
+  const int32_t* tables;        // [B][max_blocks]; contiguous: request ids, max_blocks 1, bs = S
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t bs, num_blocks;
+  int32_t max_blocks, num_seqs, Hq, Hkv, G;
+  int32_t max_q;                // host bound on any chunk's length (decode: 1)
+  int32_t max_context;          // decode: host bound on any context; prefill: what a table holds
+  float qscale;                 // scale * log2(e)
+  int32_t checked, err_code;    // err_code: of a table entry out of range
+  int* err;
+};
+
+cudaError_t launch_attention_q8(const AttentionQ8Params& p, bool e4m3, cudaStream_t stream);
+
+#ifdef __CUDACC__
+
+// Two e4m3 codes (the low 16 bits) as two halves; exact, NaN codes stay NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(codes));
+  return h;
+}
+
+// Two values as e4m3 codes, `lo` in the low byte: nearest, ties to even,
+// saturated; NaN stays NaN.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+  return c;
+}
+
+#endif
+
+}  // namespace pkv

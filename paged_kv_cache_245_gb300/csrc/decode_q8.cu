@@ -1,0 +1,711 @@
+// decode_q8.cu -- decode attention over the 8-bit KV cache (q8.cuh), paged or
+// contiguous: warp-level tensor-core math on 16-token tiles, each of which has
+// one scale for K and one for V, and a persistent schedule balanced over every
+// warp of the GPU.  sm_103a.
+//
+// For sequence i, query head h and KV head h / G:
+//   out[i][h] = sum_j softmax_j(scale q . k_j) v_j,  k_j = kcode_j ks, v_j = vcode_j vs
+// with ks and vs of the tile that holds j.  So
+//   S = (q . kcode) (scale ks),   O += vs (P vcode)
+// and the matrix products run on the codes themselves, which fp16 holds exactly
+// (e4m3 by the conversion instruction; int8 as 1024 + 128 + code, put together
+// from bytes, less 1152).  Queries enter as fp16 too: each row times a power of
+// two that puts its largest element at 2^14 .. 2^15, exact for bf16 elements down
+// to 2^-28 of that.  P is rounded to fp16 (2^-11 at most); a tile's product is
+// added to O in fp32 with its vs.
+//
+// Schedule: that of decode_runs.cu -- the flattened list of tiles of every
+// (sequence, KV head) pair cut evenly over the warps of the grid, pieces of a
+// pair joined in shared memory within a CTA and through tagged records across.
+//
+// Data movement.  A tile is 16 rows x 128 bytes of K and as much of V, one TMA
+// box each, 128-byte swizzled, into a per-warp ring of stages; the two scales
+// come by cp.async and arrive on the same mbarrier.
+//
+// Math of a tile (one warp).  A lane takes two 16-byte chunks of K rows g and
+// g + 8; which element of the head a k-slot of the product stands for is free, so
+// word w of a lane's chunks is k-step w (elements 32 tq + 4 w ..) and Q's
+// fragments are loaded in the same order.  V comes by ldmatrix.trans on pairs of
+// codes: of elements 2g and 2g + 1 the lane gets keys 2tq and 2tq + 1, and rows g
+// and g + 8 of the product stand for those two elements, so that the output's
+// neighbours meet in one lane.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "decode_tc.cuh"
+#include "q8.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kTileCodes = 16 * kCodeRowBytes;  // 2 KiB
+constexpr int kStageQ8 = 2 * kTileCodes;        // K then V
+
+struct DecodeQ8Params : TcParams {
+  const float* k_scale;
+  const float* v_scale;
+};
+
+// W warps, S stages each; MH query heads of a KV head (4, or 8).
+template <int W, int S, int MH>
+struct Q8Smem {
+  static constexpr int kPieceFloats = MH * kRecStride;  // o[128], m, l of each head
+  static constexpr int kStagesOff = 0;                  // (a run's last piece goes over its stages)
+  static constexpr int kBarsOff = W * S * kStageQ8;
+  static constexpr int kScalesOff = kBarsOff + W * S * 8;        // (K, V) of each stage
+  static constexpr int kFirstOff = kScalesOff + W * S * 8;       // a run's first piece
+  static constexpr int kRunOff = kFirstOff + W * kPieceFloats * 4;  // the CTA's tiles [lo, hi)
+  static constexpr int kPairOff = kRunOff + 2 * 8;               // pairs of the pieces [W][2]
+  static constexpr int kCtxOff = kPairOff + W * 2 * 4;
+  static constexpr int kReqOff = kCtxOff + kTcMaxSeqs * 4;
+  static constexpr int kPrefixOff = kReqOff + kTcMaxSeqs * 4;
+  static constexpr int kTotal = kPrefixOff + (kTcMaxSeqs + 1) * 4 + 1024;  // + 1 KiB alignment
+  static_assert(kTotal <= 232448, "shared memory per CTA exceeds 227 KiB");
+  static_assert(kPieceFloats * 4 <= S * kStageQ8, "a piece fits a warp's stages");
+  static_assert(kFirstOff % 16 == 0 && kRunOff % 8 == 0, "float4 records, 64-bit runs");
+};
+
+// d = a(16x16, row) * b(16x8, col) + c, fp16 inputs, fp32 accumulation.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+      "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], const uint32_t (&a)[4],
+                                                   uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+      "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 1152 in both halves taken off: int8 code + 1152 -> code, exact.
+__device__ __forceinline__ uint32_t less_1152(uint32_t h) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+  return r;
+}
+
+// Codes (0, 1) and (2, 3) of a word as halves.
+template <bool kE4m3>
+__device__ __forceinline__ void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (kE4m3) {
+    lo = e4m3x2_to_half2(w);
+    hi = e4m3x2_to_half2(w >> 16);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    lo = less_1152(__byte_perm(u, 0x64646464u, 0x4140));
+    hi = less_1152(__byte_perm(u, 0x64646464u, 0x4342));
+  }
+}
+
+// Codes (0, 2) and (1, 3): one element of two keys each (V).
+template <bool kE4m3>
+__device__ __forceinline__ void halves_across(uint32_t w, uint32_t& even, uint32_t& odd) {
+  if (kE4m3) {
+    const uint32_t t = __byte_perm(w, 0u, 0x3120);
+    even = e4m3x2_to_half2(t);
+    odd = e4m3x2_to_half2(t >> 16);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    even = less_1152(__byte_perm(u, 0x64646464u, 0x4240));
+    odd = less_1152(__byte_perm(u, 0x64646464u, 0x4341));
+  }
+}
+
+// The mbarrier counts one arrival more: when this thread's cp.async copies land.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+}  // namespace
+
+template <bool kContig, bool kE4m3, int W, int S, int MH>
+__global__ void __launch_bounds__(W * 32, 1)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv,
+                     const __grid_constant__ DecodeQ8Params p) {
+  using L = Q8Smem<W, S, MH>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int tid = threadIdx.x;
+  const int c = blockIdx.x;
+  const int P = gridDim.x;
+  const int B = p.num_seqs;
+  const int G = p.G;
+  const int Hkv = p.Hkv;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarsOff) + warp * S;
+  float2* scales = reinterpret_cast<float2*>(smem + L::kScalesOff) + warp * S;
+  int64_t* cta_run = reinterpret_cast<int64_t*>(smem + L::kRunOff);
+  int32_t* piece_pair = reinterpret_cast<int32_t*>(smem + L::kPairOff);  // [W][first, last]
+  int32_t* ctx_s = reinterpret_cast<int32_t*>(smem + L::kCtxOff);
+  int32_t* req_s = reinterpret_cast<int32_t*>(smem + L::kReqOff);
+  int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefixOff);
+  // the record of head h of a run's first (0) or last (1) piece
+  auto piece = [&](int w, int last, int h) -> float* {
+    unsigned char* base = last ? smem + L::kStagesOff + w * S * kStageQ8
+                               : smem + L::kFirstOff + w * L::kPieceFloats * 4;
+    return reinterpret_cast<float*>(base) + h * kRecStride;
+  };
+
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&bars[s], 2);  // the boxes', and the scales'
+    fence_barrier_init();
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+    piece_pair[2 * warp] = piece_pair[2 * warp + 1] = -1;
+  }
+  // wait for the previous kernel in the stream before reading any input, then
+  // let the next one get scheduled (no-ops without the launch attribute)
+  grid_dependency_wait();
+  grid_dependency_trigger();
+
+  // ---- tile counts and their prefix over sequences
+  for (int i = tid; i < B; i += W * 32) {
+    const int ctx = tc_context(p, i, kContig, c == 0);
+    ctx_s[i] = ctx;
+    if (kContig) req_s[i] = ctx > 0 ? p.req_ids[i] : 0;
+  }
+  __syncthreads();
+  auto seq_tiles = [&](int i) -> int { return (ctx_s[i] + 15) >> 4; };
+  if (warp == 0) {
+    const int per = (B + 31) / 32;
+    const int i0 = lane * per;
+    int sum = 0;
+    for (int i = i0; i < i0 + per && i < B; ++i) sum += seq_tiles(i);
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int run = incl - sum;
+    for (int i = i0; i < i0 + per && i < B; ++i) {
+      prefix[i] = run;
+      run += seq_tiles(i);
+    }
+    if (lane == 31) prefix[B] = incl;
+  }
+  __syncthreads();
+
+  // outputs of empty contexts are zeros (sequences c, c + P, ... of this CTA)
+  for (int i = c; i < B; i += P) {
+    if (ctx_s[i] != 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(i) * p.Hq * kHeadDim);
+    for (int k = tid; k < p.Hq * kHeadDim / 8; k += W * 32) o[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+
+  // ---- this warp's run of tiles [lo, hi): that of its share of the units
+  const int64_t V = tc_vseq(prefix, B, Hkv, p.seg_cost);
+  int64_t lo, hi;
+  int seq_lo;  // the sequence that holds tile lo
+  const int64_t share = static_cast<int64_t>(c) * W + warp;
+  if (V < (int64_t{1} << 20) && P * W < 4096) {
+    // in 32 bits, even lanes for the run's start and odd ones for its end (the
+    // general form below takes 1 us longer)
+    const uint32_t units = static_cast<uint32_t>(V), H = Hkv, cost = p.seg_cost;
+    const uint32_t u = (static_cast<uint32_t>(share) + (lane & 1)) * units / (P * W);
+    const uint32_t u0 = __shfl_sync(kFull, u, 0), u1 = __shfl_sync(kFull, u, 1);
+    int a0 = 0, a1 = 0;  // the last sequences whose units start at or before them
+    for (int i = lane; i < B; i += 32) {
+      const uint32_t start = H * (prefix[i] + cost * i);
+      if (start <= u0) a0 = i;
+      if (start <= u1) a1 = i;
+    }
+    a0 = __reduce_max_sync(kFull, a0);
+    a1 = __reduce_max_sync(kFull, a1);
+    const int a = lane & 1 ? a1 : a0;
+    const uint32_t n = prefix[a + 1] - prefix[a];
+    const uint32_t r = u - H * (prefix[a] + cost * a);
+    const uint32_t h = r / (n + cost), o = r - h * (n + cost);
+    const uint32_t tile = u >= units ? H * prefix[B] : H * prefix[a] + h * n + (o > cost ? o - cost : 0);
+    lo = __shfl_sync(kFull, tile, 0);
+    hi = __shfl_sync(kFull, tile, 1);
+    seq_lo = a0;
+  } else {
+    const int64_t parts = static_cast<int64_t>(P) * W;
+    lo = tc_unit_to_tile(share * V / parts, prefix, B, Hkv, p.seg_cost);
+    hi = tc_unit_to_tile((share + 1) * V / parts, prefix, B, Hkv, p.seg_cost);
+    seq_lo = lo < hi ? tc_find_seg(lo, hi, prefix, B, Hkv).seq : 0;
+  }
+  if (lane == 0 && warp == 0) cta_run[0] = lo;
+  if (lane == 0 && warp == W - 1) cta_run[1] = hi;
+  // (an empty sequence's units hold no tile: the next one's first)
+  while (lo < hi && static_cast<int64_t>(Hkv) * prefix[seq_lo + 1] <= lo) ++seq_lo;
+
+  const uint32_t bs32 = static_cast<uint32_t>(p.bs);  // paged: a 32-bit block size
+  const uint64_t policy = l2_policy_evict_first();
+  unsigned char* stage0 = smem + L::kStagesOff + warp * S * kStageQ8;
+  const int g = lane >> 2;   // accumulator row group
+  const int tq = lane & 3;   // accumulator column pair
+
+  // Elements 32 tq .. + 31 of head g's query row (zeros for g >= G), as loaded.
+  auto load_q = [&](uint4 (&qr)[4], int seq, int kvh) {
+    const uint4* row = reinterpret_cast<const uint4*>(
+        p.q + (static_cast<int64_t>(seq) * p.Hq + kvh * G + (g < G ? g : 0)) * kHeadDim + 32 * tq);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) qr[k] = g < G ? __ldg(row + k) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  // the pair after `sg` (its tiles start at sg.pend < hi)
+  auto next_seg = [&](const TcSeg& sg) -> TcSeg {
+    int a = sg.seq;
+    if (sg.kvh + 1 == Hkv)
+      do ++a; while (prefix[a + 1] == prefix[a]);
+    return tc_seg_at(sg.pend, hi, a, prefix, Hkv);
+  };
+
+  int issued = 0, consumed = 0;
+  bool dead = false;
+  if (lo < hi) {
+    // ---- the issue cursor: tile ix of pair iseg
+    TcSeg iseg = tc_seg_at(lo, hi, seq_lo, prefix, Hkv);
+    int64_t ix = lo;
+    // The next pair's query rows are fetched into qn when the cursor first
+    // reaches it (if qn is free), so its start does not wait on them.
+    uint4 qn[4];
+    int64_t qn_pair = -1;
+    auto load_entry = [&]() -> int32_t {  // block-table entry of tile ix (lane 0)
+      if (kContig || lane != 0 || ix >= hi) return 0;
+      const uint32_t pos = static_cast<uint32_t>(ix - iseg.pstart) * 16;
+      return __ldg(p.block_tables + static_cast<int64_t>(iseg.seq) * p.max_blocks + pos / bs32);
+    };
+    auto issue = [&](int stage, int32_t entry) {
+      if (ix == iseg.x0 && qn_pair < 0) {  // whole warp
+        load_q(qn, iseg.seq, iseg.kvh);
+        qn_pair = iseg.pstart;
+      }
+      if (lane == 0) {
+        unsigned char* st = stage0 + stage * kStageQ8;
+        const int64_t pos = (ix - iseg.pstart) * 16;
+        bool kv_ok = true;
+        int64_t row;
+        if (kContig) {
+          row = cache_row(req_s[iseg.seq], iseg.kvh, Hkv, p.bs, pos);
+        } else {
+          if (p.checked && (entry < 0 || entry >= p.num_blocks)) {
+            record_error(p.err, kErrBlockId);
+            kv_ok = false;  // skip the copy: stale rows, undefined output, no fault
+          }
+          row = cache_row(entry, iseg.kvh, Hkv, p.bs, static_cast<uint32_t>(pos) % bs32);
+        }
+        mbar_arrive_expect_tx(&bars[stage], kv_ok ? static_cast<uint32_t>(kStageQ8) : 0u);
+        if (kv_ok) {
+          const int32_t y = static_cast<int32_t>(row);
+          tma_load_2d(st, &tmk, 0, y, &bars[stage], policy);
+          tma_load_2d(st + kTileCodes, &tmv, 0, y, &bars[stage], policy);
+          cp_async_4(&scales[stage].x, p.k_scale + (row >> 4));
+          cp_async_4(&scales[stage].y, p.v_scale + (row >> 4));
+        }
+        cp_async_arrive(&bars[stage]);
+      }
+      ++issued;
+      if (++ix >= iseg.x1 && ix < hi) iseg = next_seg(iseg);
+    };
+
+    // Prologue: lane s fetches the table entry of tile lo + s (one memory
+    // latency for all of them), then the stages fill.
+    int32_t pre = 0;
+    if (!kContig) {
+      TcSeg cs = iseg;
+      for (int s = 0; s < S && lo + s < hi; ++s) {
+        if (lo + s >= cs.x1) cs = next_seg(cs);
+        if (lane == s) {
+          const uint32_t pos = static_cast<uint32_t>(lo + s - cs.pstart) * 16;
+          pre = __ldg(p.block_tables + static_cast<int64_t>(cs.seq) * p.max_blocks + pos / bs32);
+        }
+      }
+    }
+    for (int s = 0; s < S && ix < hi; ++s) issue(s, __shfl_sync(kFull, pre, s));
+    int32_t next_entry = load_entry();
+
+    // ---- per-lane offsets inside a 128-byte-swizzled 16 x 128 B box
+    // K: chunks 2 tq and 2 tq + 1 of row g (row g + 8: 1 KiB on)
+    const uint32_t koff0 = g * 128 + (((2 * tq) ^ g) << 4);
+    const uint32_t koff1 = g * 128 + (((2 * tq + 1) ^ g) << 4);
+    // V: lanes 0-7 address keys 0-7 of chunk c, 8-15 keys 8-15, 16-31 chunk c + 1
+    const int vrow = lane & 15, vch = lane >> 4;
+
+    TcSeg seg = tc_seg_at(lo, hi, seq_lo, prefix, Hkv);
+    while (true) {
+      uint32_t qb[8][2];
+      float qs0, qs1;  // score units of heads 2 tq and 2 tq + 1
+      {
+        if (qn_pair != seg.pstart) load_q(qn, seg.seq, seg.kvh);
+        qn_pair = -1;
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w[4] = {qn[k].x, qn[k].y, qn[k].z, qn[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        // 2^n, n = 14 - exponent of the largest element (at most 126)
+        const int n = min(126, 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23));
+        const float up = __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - n) << 23);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w[4] = {qn[k].x, qn[k].y, qn[k].z, qn[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            qb[2 * k + (e >> 1)][e & 1] = pack_half2(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
+        }
+        qs0 = __shfl_sync(kFull, down, 8 * tq) * p.qscale;
+        qs1 = __shfl_sync(kFull, down, 8 * tq + 4) * p.qscale;
+      }
+      const int ctx = ctx_s[seg.seq];
+      float acc[8][4];
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+
+      for (int64_t x = seg.x0; x < seg.x1 && !dead; ++x) {
+        const int stage = consumed % S;
+        if (!__all_sync(kFull, mbar_wait_bounded(&bars[stage],
+                                                 static_cast<uint32_t>(consumed / S) & 1u))) {
+          dead = true;
+          if (lane == 0) record_error(p.err, kErrTimeout);
+          break;
+        }
+        ++consumed;
+        unsigned char* st = stage0 + stage * kStageQ8;
+        const float2 sc = scales[stage];
+        const int row0 = static_cast<int>(x - seg.pstart) * 16;
+        const int nvalid = min(16, ctx - row0);
+        if (kE4m3 && nvalid < 16) {  // rows past the context may hold NaN: 0 * NaN
+          for (int idx = lane; idx < (16 - nvalid) * 8; idx += 32)
+            *reinterpret_cast<uint4*>(st + kTileCodes + nvalid * 128 + idx * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          __syncwarp();
+        }
+
+        // ---- S^T = K . Q^T  (two accumulation chains)
+        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const unsigned char* at = st + (half ? koff1 : koff0);
+          const uint4 r0 = *reinterpret_cast<const uint4*>(at);
+          const uint4 r1 = *reinterpret_cast<const uint4*>(at + 1024);
+          const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t a[4];
+            halves_of<kE4m3>(w0[e], a[0], a[2]);
+            halves_of<kE4m3>(w1[e], a[1], a[3]);
+            const int ks = 4 * half + e;
+            if (ks & 1) mma_f16_16816(sb, a, qb[ks][0], qb[ks][1]);
+            else mma_f16_16816(sa, a, qb[ks][0], qb[ks][1]);
+          }
+        }
+        // scores of tokens g (s0, s1) and g + 8 (s2, s3), heads 2tq and 2tq + 1
+        const float f0 = qs0 * sc.x, f1 = qs1 * sc.x;
+        const bool v0 = g < nvalid, v1 = g + 8 < nvalid;
+        const float s0 = v0 ? (sa[0] + sb[0]) * f0 : -INFINITY;
+        const float s1 = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;
+        const float s2 = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;
+        const float s3 = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;
+
+        // ---- online softmax, per head column
+        float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, o));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, o));
+        }
+        if (mx0 > m0) {
+          const float a = fast_exp2(m0 - mx0);
+          l0 *= a;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) { acc[i][0] *= a; acc[i][2] *= a; }
+          m0 = mx0;
+        }
+        if (mx1 > m1) {
+          const float a = fast_exp2(m1 - mx1);
+          l1 *= a;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) { acc[i][1] *= a; acc[i][3] *= a; }
+          m1 = mx1;
+        }
+        const float p0 = fast_exp2(s0 - m0), p2 = fast_exp2(s2 - m0);
+        const float p1 = fast_exp2(s1 - m1), p3 = fast_exp2(s3 - m1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        // P^T as the B operand, rounded to fp16 once
+        const uint32_t b0 = movmatrix_trans(pack_half2(p0, p1));  // tokens 0..7
+        const uint32_t b1 = movmatrix_trans(pack_half2(p2, p3));  // tokens 8..15
+
+        // ---- O^T += vs (V^T . P^T)
+        const uint32_t vaddr = smem_addr(st) + kTileCodes + vrow * 128;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          uint32_t r[4];  // keys 0-7 and 8-15 of elements 16i .., then of 16(i + 1) ..
+          ldmatrix_x4_trans(r, vaddr + (((i + vch) ^ (vrow & 7)) << 4));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t a[4];
+            halves_across<kE4m3>(r[2 * k], a[0], a[1]);
+            halves_across<kE4m3>(r[2 * k + 1], a[2], a[3]);
+            float d[4];
+            mma_f16_16816_zero(d, a, b0, b1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i + k][e] = fmaf(d[e], sc.y, acc[i + k][e]);
+          }
+        }
+        __syncwarp();
+
+        // ---- refill this stage with the next tile of the run
+        if (ix < hi) {
+          fence_proxy_async_smem();
+          issue(stage, next_entry);
+          next_entry = load_entry();
+        }
+      }
+      if (dead) break;
+
+      // ---- the pair's part in this run is done
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        l0 += __shfl_xor_sync(kFull, l0, o);
+        l1 += __shfl_xor_sync(kFull, l1, o);
+      }
+      if (seg.x0 == seg.pstart && seg.x1 == seg.pend) {  // whole
+        const float inv0 = l0 != 0.f ? 1.f / l0 : 0.f, inv1 = l1 != 0.f ? 1.f / l1 : 0.f;
+        uint16_t* row = p.out + (static_cast<int64_t>(seg.seq) * p.Hq + seg.kvh * G + 2 * tq) *
+                                    kHeadDim + 2 * g;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (2 * tq < G)
+            *reinterpret_cast<uint32_t*>(row + 16 * i) = pack_bf16x2(acc[i][0] * inv0, acc[i][2] * inv0);
+          if (2 * tq + 1 < G)
+            *reinterpret_cast<uint32_t*>(row + kHeadDim + 16 * i) =
+                pack_bf16x2(acc[i][1] * inv1, acc[i][3] * inv1);
+        }
+      } else {
+        const int last = seg.x0 != lo;  // a run's first piece, or (not first) its last
+        if (2 * tq < MH) {
+          float* r0 = piece(warp, last, 2 * tq);
+          float* r1 = r0 + kRecStride;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            *reinterpret_cast<float2*>(r0 + 16 * i + 2 * g) = make_float2(acc[i][0], acc[i][2]);
+            *reinterpret_cast<float2*>(r1 + 16 * i + 2 * g) = make_float2(acc[i][1], acc[i][3]);
+          }
+          if (g == 0) {
+            r0[128] = m0;
+            r0[129] = l0;
+            r1[128] = m1;
+            r1[129] = l1;
+          }
+        }
+        if (lane == 0) piece_pair[2 * warp + last] = seg.seq * Hkv + seg.kvh;
+      }
+      if (seg.x1 >= hi) break;
+      seg = next_seg(seg);
+    }
+    if (dead) {
+      // give the copies still in flight a bounded chance to land
+      for (int k = consumed; k < issued; ++k)
+        mbar_wait_bounded(&bars[k % S], static_cast<uint32_t>(k / S) & 1u);
+    }
+  }
+  __syncthreads();
+
+  // ---- join the pieces of each pair that warps of this CTA share: pieces in
+  // warp order, lane j's is piece_pair[j] (2 W <= 32); consecutive ones of a pair
+  // are a group, and head h of group g is task g G + h, dealt to the warps
+  const int lane_pair = lane < 2 * W ? piece_pair[lane] : -1;
+  const uint32_t taken = __ballot_sync(kFull, lane_pair >= 0);
+  const uint32_t before = taken & ((1u << lane) - 1u);
+  const int prev_pair = __shfl_sync(kFull, lane_pair, before != 0u ? 31 - __clz(before) : lane);
+  const uint32_t starts =
+      __ballot_sync(kFull, lane_pair >= 0 && (before == 0u || prev_pair != lane_pair));
+  const int tasks = __popc(starts) * G;
+  // (last group first: what a later CTA waits for goes out before a wait for earlier ones)
+  for (int task = tasks - 1 - warp; task >= 0; task -= W) {
+    const int grp = static_cast<uint32_t>(task) / static_cast<uint32_t>(G);
+    const int hh = task - grp * G;
+    uint32_t rest = starts;
+    for (int k = 0; k < grp; ++k) rest &= rest - 1;
+    const int n = __ffs(rest) - 1;  // pieces n .. end - 1 are this pair's (or empty)
+    rest &= rest - 1;
+    const int end = rest != 0u ? __ffs(rest) - 1 : 2 * W;
+    const int pair = __shfl_sync(kFull, lane_pair, n);
+    // lane j < end - n derives the weight of piece n + j (2 W <= 32 lanes)
+    const int k = n + lane;
+    const bool have = k < end && (taken >> k & 1u);
+    const float* rk = piece(k < end ? k >> 1 : 0, k & 1, hh);
+    const float mj = have ? rk[128] : -INFINITY, lj = have ? rk[129] : 0.f;
+    float M = mj;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    const float fj = lj == 0.f ? 0.f : fast_exp2(mj - M);
+    float Ls = lj * fj;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(kFull, Ls, o);
+    const float wj = Ls != 0.f ? fj / Ls : 0.f;
+    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int e = n; e < end; ++e) {
+      const float w = __shfl_sync(kFull, wj, e - n);
+      if (!(taken >> e & 1u)) continue;
+      const float4 v = *reinterpret_cast<const float4*>(piece(e >> 1, e & 1, hh) + lane * 4);
+      o4.x = fmaf(w, v.x, o4.x);
+      o4.y = fmaf(w, v.y, o4.y);
+      o4.z = fmaf(w, v.z, o4.z);
+      o4.w = fmaf(w, v.w, o4.w);
+    }
+    const float Mr = Ls != 0.f ? M : -INFINITY;
+    // the CTAs cf .. cl that hold tiles of the pair
+    TcSeg sg;
+    sg.seq = static_cast<uint32_t>(pair) / static_cast<uint32_t>(Hkv);
+    sg.kvh = pair - sg.seq * Hkv;
+    const int64_t tiles = prefix[sg.seq + 1] - prefix[sg.seq];
+    sg.pstart = static_cast<int64_t>(Hkv) * prefix[sg.seq] + sg.kvh * tiles;
+    sg.pend = sg.pstart + tiles;
+    sg.x0 = sg.pstart;
+    sg.x1 = sg.pend;
+    int cf = c, cl = c;
+    if (sg.pstart < cta_run[0] || sg.pend > cta_run[1])
+      tc_pair_ctas(sg, prefix, Hkv, p.seg_cost, V, P, &cf, &cl);
+    const int qh = sg.kvh * G + hh;
+    if (cf == cl) {
+      tc_write_out(p, sg.seq, qh, lane, o4, Mr, Ls);
+    } else if (cl != c) {
+      tc_store_piece(p.rec + (static_cast<int64_t>(c) * kTcRecHeads + hh) * kRecStride, p.tag,
+                     lane, o4, Mr, Ls);
+    } else if (!tc_merge_earlier(p, sg.seq, qh, hh, cf, c, V, P, lane, o4, Mr, Ls) && lane == 0) {
+      record_error(p.err, kErrTimeout);
+    }
+  }
+}
+
+namespace {
+
+template <bool kContig, bool kE4m3, int W, int S, int MH>
+cudaError_t launch_shape(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& p0,
+                         int num_ctas, cudaStream_t stream) {
+  using L = Q8Smem<W, S, MH>;
+  static unsigned long long done_mask = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  auto kernel = decode_q8_kernel<kContig, kE4m3, W, S, MH>;
+  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+    if (e != cudaSuccess) return e;
+    __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
+  }
+  const int chunk = tc_chunk_seqs(p0.max_context);
+  for (int s0 = 0; s0 < p0.num_seqs; s0 += chunk) {
+    DecodeQ8Params p = p0;
+    p.num_seqs = (p0.num_seqs - s0) < chunk ? (p0.num_seqs - s0) : chunk;
+    p.q += static_cast<int64_t>(s0) * p.Hq * kHeadDim;
+    p.out += static_cast<int64_t>(s0) * p.Hq * kHeadDim;
+    p.ctx_lens += s0;
+    if (kContig) p.req_ids += s0;
+    else p.block_tables += static_cast<int64_t>(s0) * p.max_blocks;
+    p.tag = next_launch_tag();  // every launch writes its piece records under a fresh tag
+    e = launch_pdl_if(pdl_decode_enabled(), kernel, dim3(num_ctas), dim3(W * 32), L::kTotal,
+                      stream, tk, tv, p);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <bool kContig, bool kE4m3>
+cudaError_t launch_heads(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& p,
+                         int num_ctas, cudaStream_t stream) {
+  return p.G <= 4 ? launch_shape<kContig, kE4m3, 12, 4, 4>(tk, tv, p, num_ctas, stream)
+                  : launch_shape<kContig, kE4m3, 10, 4, 8>(tk, tv, p, num_ctas, stream);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// Codes [rows][128] as a 2-D tensor; boxes of 16 rows, 128-byte swizzle.
+bool encode_codes(CUtensorMap* map, const void* base, int64_t rows) {
+  auto enc = map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kCodeRowBytes), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kCodeRowBytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kCodeRowBytes), 16u};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+TcStatus launch_decode_q8(const AttentionQ8Params& a, bool e4m3, bool contig, int num_ctas,
+                          void* workspace, cudaStream_t stream, cudaError_t* cuda_err) {
+  *cuda_err = cudaSuccess;
+  const int64_t rows = a.num_blocks * a.Hkv * a.bs;
+  alignas(64) CUtensorMap tk;
+  alignas(64) CUtensorMap tv;
+  if (!encode_codes(&tk, a.k_codes, rows) || !encode_codes(&tv, a.v_codes, rows))
+    return TcStatus::kEncodeFailed;
+  DecodeQ8Params p = {};
+  p.q = a.q;
+  p.out = a.out;
+  p.ctx_lens = a.ctx_lens;
+  p.block_tables = contig ? nullptr : a.tables;
+  p.req_ids = contig ? a.tables : nullptr;
+  p.rec = static_cast<uint64_t*>(workspace);
+  p.seg_cost = 4;
+  p.bs = a.bs;
+  p.num_blocks = a.num_blocks;
+  p.max_blocks = a.max_blocks;
+  p.max_reqs = static_cast<int32_t>(a.num_blocks);
+  p.num_seqs = a.num_seqs;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = a.G;
+  p.max_context = a.max_context;
+  p.qscale = a.qscale;
+  p.checked = a.checked;
+  p.err = a.err;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  if (contig)
+    *cuda_err = e4m3 ? launch_heads<true, true>(tk, tv, p, num_ctas, stream)
+                     : launch_heads<true, false>(tk, tv, p, num_ctas, stream);
+  else
+    *cuda_err = e4m3 ? launch_heads<false, true>(tk, tv, p, num_ctas, stream)
+                     : launch_heads<false, false>(tk, tv, p, num_ctas, stream);
+  return *cuda_err == cudaSuccess ? TcStatus::kOk : TcStatus::kCudaError;
+}
+
+}  // namespace pkv

@@ -263,6 +263,59 @@ __device__ __forceinline__ bool tc_merge_pieces(const TcParams& p, int seq, int 
   return ok;
 }
 
+// Merges the pieces of a pair cut by the CTA ranges (CTAs cf .. c) for query
+// head hh of the group and writes the result; called by CTA c, which holds the
+// pair's last tiles, with its own piece.  Records are folded in CTA order.  One
+// not yet complete is read again until it is, for at most kWaitLimitNs: waits
+// point only to lower CTAs, which start first, so they end whatever else runs on
+// the GPU.  Returns false if it gave up.
+__device__ __forceinline__ bool tc_merge_earlier(const TcParams& p, int seq, int qh, int hh,
+                                                 int cf, int c, int64_t V, int64_t P, int lane,
+                                                 float4 o_own, float m_own, float l_own) {
+  constexpr unsigned kFull = 0xffffffffu;
+  float M = -INFINITY, L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fold = [&](float m, float l, float4 o) {
+    if (empty_sum<true>(l)) return;
+    if (m > M) {
+      const float s = fast_exp2(M - m);  // 0 while M is -inf
+      L *= s;
+      a.x *= s; a.y *= s; a.z *= s; a.w *= s;
+      M = m;
+    }
+    const float w = l * fast_exp2(m - M);
+    a.x = fmaf(w, o.x, a.x);
+    a.y = fmaf(w, o.y, a.y);
+    a.z = fmaf(w, o.z, a.z);
+    a.w = fmaf(w, o.w, a.w);
+    L += w;
+  };
+  bool ok = true;
+  for (int k = cf; k < c; ++k) {
+    if (!tc_range_nonempty(k, V, P)) continue;
+    uint64_t* rec = p.rec + (static_cast<int64_t>(k) * kTcRecHeads + hh) * kRecStride;
+    TcPieceWords pw;
+    float m, l;
+    float4 o;
+    tc_issue_piece(rec, lane, pw);
+    bool have = __all_sync(kFull, tc_parse_piece(pw, p.tag, &o, &m, &l));
+    for (const unsigned long long t0 = global_timer_ns();
+         !have && global_timer_ns() - t0 < kWaitLimitNs;) {
+      __nanosleep(128);
+      tc_issue_piece(rec, lane, pw);
+      have = __all_sync(kFull, tc_parse_piece(pw, p.tag, &o, &m, &l));
+    }
+    ok = ok && have;
+    fold(m, l, o);
+    tc_clear_piece(rec, lane);
+  }
+  fold(m_own, l_own, o_own);
+  const float inv = empty_sum<true>(L) ? 0.f : 1.f / L;
+  tc_write_out(p, seq, qh, lane, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv),
+               empty_sum<true>(L) ? -INFINITY : M, L);
+  return ok;
+}
+
 // First position that sequence i, whose newest token is at ctx - 1, sees (ctx
 // becomes 0 when it sees none).
 __device__ __forceinline__ int tc_first_visible(const TcParams& p, int i, int& ctx) {

@@ -1430,7 +1430,8 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
                                const pkv_q8_cache* cache, bool contig, const int32_t* tables,
                                int32_t max_blocks, int64_t num_blocks, const int32_t* context_lens,
                                int32_t num_seqs, int32_t max_q, int32_t max_context, int64_t bs,
-                               float scale, pkv_heads h, void* out, void* stream) {
+                               float scale, pkv_heads h, void* out, void* workspace,
+                               size_t workspace_bytes, void* stream) {
   pkv_status st = check_heads(h);
   if (st != PKV_OK) return st;
   if (num_seqs < 0 || num_tokens < 0 || max_q < 0 || max_context < 0)
@@ -1447,8 +1448,8 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
   if (!std::isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
   if (max_blocks <= 0 || num_blocks <= 0)
     return fail(PKV_ERR_INVALID_ARG, contig ? "max_reqs must be >= 1" : "empty block table or pool");
-  if (num_blocks * h.num_kv_heads > (int64_t{1} << 40) / bs)
-    return fail(PKV_ERR_UNSUPPORTED, "cache too large");
+  if (num_blocks * h.num_kv_heads > 0x7fffffffLL / bs)
+    return fail(PKV_ERR_UNSUPPORTED, "cache of 2^31 rows or more");
   const int64_t holds = max_blocks * bs;
   if (cu_q == nullptr) {
     if (max_context > holds)
@@ -1487,6 +1488,21 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
   p.checked = g_checked.load();
   p.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
   p.err = err;
+  if (cu_q == nullptr) {
+    const size_t need = pkv::tc_workspace_bytes(tc_ctas(sms));
+    if (!workspace || workspace_bytes < need)
+      return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
+                  workspace ? workspace_bytes : size_t{0});
+    if (!aligned(workspace, 16)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    cudaError_t ce = cudaSuccess;
+    const pkv::TcStatus ts =
+        pkv::launch_decode_q8(p, cache->format == PKV_Q8_E4M3, contig, tc_ctas(sms), workspace,
+                              static_cast<cudaStream_t>(stream), &ce);
+    if (ts == pkv::TcStatus::kEncodeFailed)
+      return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for the K/V cache");
+    if (ts != pkv::TcStatus::kOk) return cuda_fail(ce, "q8 decode launch");
+    return PKV_OK;
+  }
   const cudaError_t e = pkv::launch_attention_q8(p, cache->format == PKV_Q8_E4M3,
                                                  static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "q8 attention launch");
@@ -1524,8 +1540,11 @@ pkv_status pkv_rope_append_q8(const int32_t* positions, const int64_t* slot_mapp
 }
 
 size_t pkv_q8_decode_workspace_size(int32_t num_seqs, pkv_heads heads, int32_t max_context) {
-  if (check_heads(heads) != PKV_OK || num_seqs <= 0 || max_context <= 0) return 0;
-  return 0;
+  int sms = 0;
+  if (check_heads(heads) != PKV_OK || num_seqs <= 0 || max_context < 0 ||
+      device_info(nullptr, nullptr, &sms) != PKV_OK)
+    return 0;
+  return pkv::tc_workspace_bytes(tc_ctas(sms));
 }
 
 pkv_status pkv_paged_decode_attention_q8(
@@ -1535,7 +1554,7 @@ pkv_status pkv_paged_decode_attention_q8(
     void* out, void* workspace, size_t workspace_bytes, void* stream) {
   return attention_q8_common(q, nullptr, num_seqs, cache, false, block_tables, max_blocks_per_seq,
                              num_blocks, context_lens, num_seqs, 1, max_context, block_size, scale,
-                             heads, out, stream);
+                             heads, out, workspace, workspace_bytes, stream);
 }
 
 pkv_status pkv_contig_decode_attention_q8(
@@ -1543,7 +1562,8 @@ pkv_status pkv_contig_decode_attention_q8(
     const int32_t* context_lens, int32_t num_seqs, int32_t max_context, int64_t S, float scale,
     pkv_heads heads, void* out, void* workspace, size_t workspace_bytes, void* stream) {
   return attention_q8_common(q, nullptr, num_seqs, cache, true, req_ids, 1, max_reqs, context_lens,
-                             num_seqs, 1, max_context, S, scale, heads, out, stream);
+                             num_seqs, 1, max_context, S, scale, heads, out, workspace,
+                             workspace_bytes, stream);
 }
 
 pkv_status pkv_paged_prefill_attention_q8(
@@ -1554,7 +1574,7 @@ pkv_status pkv_paged_prefill_attention_q8(
   if (num_seqs > 0 && !cu_seqlens_q) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
   return attention_q8_common(q, cu_seqlens_q, num_tokens, cache, false, block_tables,
                              max_blocks_per_seq, num_blocks, context_lens, num_seqs, max_q_tokens,
-                             0, block_size, scale, heads, out, stream);
+                             0, block_size, scale, heads, out, nullptr, 0, stream);
 }
 
 pkv_status pkv_contig_prefill_attention_q8(
@@ -1563,7 +1583,8 @@ pkv_status pkv_contig_prefill_attention_q8(
     int32_t max_q_tokens, int64_t S, float scale, pkv_heads heads, void* out, void* stream) {
   if (num_seqs > 0 && !cu_seqlens_q) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
   return attention_q8_common(q, cu_seqlens_q, num_tokens, cache, true, req_ids, 1, max_reqs,
-                             context_lens, num_seqs, max_q_tokens, 0, S, scale, heads, out, stream);
+                             context_lens, num_seqs, max_q_tokens, 0, S, scale, heads, out, nullptr,
+                             0, stream);
 }
 
 pkv_status pkv_block_copy(const int64_t* src_dst_pairs, int64_t n, void* const* k_caches,

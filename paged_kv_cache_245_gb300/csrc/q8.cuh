@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "../../include/pkv.h"
+#include "decode_tc_launch.h"
 
 namespace pkv {
 
@@ -65,6 +66,9 @@ struct AttentionQ8Params {
   int* err;
 };
 
+// Decode (cu_q null): workspace of tc_workspace_bytes(num_ctas).
+TcStatus launch_decode_q8(const AttentionQ8Params& p, bool e4m3, bool contig, int num_ctas,
+                          void* workspace, cudaStream_t stream, cudaError_t* cuda_err);
 cudaError_t launch_attention_q8(const AttentionQ8Params& p, bool e4m3, cudaStream_t stream);
 
 #ifdef __CUDACC__

@@ -20,7 +20,9 @@
 //
 // Data movement.  A tile is 16 rows x 128 bytes of K and as much of V, one TMA
 // box each, 128-byte swizzled, into a per-warp ring of stages; the two scales
-// come by cp.async and arrive on the same mbarrier.
+// come by cp.async and arrive on the same mbarrier.  A stage holds two tiles,
+// which lanes 0 and 1 look up and ask for side by side, so that what is done once
+// a stage (waits, the running maximum, the cursor) is done once for 32 positions.
 //
 // Math of a tile (one warp).  A lane takes two 16-byte chunks of K rows g and
 // g + 8; which element of the head a k-slot of the product stands for is free, so
@@ -35,6 +37,7 @@
 
 #include "decode_tc.cuh"
 #include "q8.cuh"
+#include "umma.cuh"
 
 namespace pkv {
 
@@ -42,7 +45,8 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kTileCodes = 16 * kCodeRowBytes;  // 2 KiB
-constexpr int kStageQ8 = 2 * kTileCodes;        // K then V
+constexpr int kStageTiles = 2;                  // tiles of a stage, each K then V
+constexpr int kStageQ8 = kStageTiles * 2 * kTileCodes;
 
 struct DecodeQ8Params : TcParams {
   const float* k_scale;
@@ -55,8 +59,8 @@ struct Q8Smem {
   static constexpr int kPieceFloats = MH * kRecStride;  // o[128], m, l of each head
   static constexpr int kStagesOff = 0;                  // (a run's last piece goes over its stages)
   static constexpr int kBarsOff = W * S * kStageQ8;
-  static constexpr int kScalesOff = kBarsOff + W * S * 8;        // (K, V) of each stage
-  static constexpr int kFirstOff = kScalesOff + W * S * 8;       // a run's first piece
+  static constexpr int kScalesOff = kBarsOff + W * S * 8;        // (K, V) of each tile
+  static constexpr int kFirstOff = kScalesOff + W * S * kStageTiles * 8;  // a run's first piece
   static constexpr int kRunOff = kFirstOff + W * kPieceFloats * 4;  // the CTA's tiles [lo, hi)
   static constexpr int kPairOff = kRunOff + 2 * 8;               // pairs of the pieces [W][2]
   static constexpr int kCtxOff = kPairOff + W * 2 * 4;
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(W * 32, 1)
   const int Hkv = p.Hkv;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarsOff) + warp * S;
-  float2* scales = reinterpret_cast<float2*>(smem + L::kScalesOff) + warp * S;
+  float2* scales = reinterpret_cast<float2*>(smem + L::kScalesOff) + warp * S * kStageTiles;
   int64_t* cta_run = reinterpret_cast<int64_t*>(smem + L::kRunOff);
   int32_t* piece_pair = reinterpret_cast<int32_t*>(smem + L::kPairOff);  // [W][first, last]
   int32_t* ctx_s = reinterpret_cast<int32_t*>(smem + L::kCtxOff);
@@ -167,7 +171,8 @@ __global__ void __launch_bounds__(W * 32, 1)
   };
 
   if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&bars[s], 2);  // the boxes', and the scales'
+    // the boxes', and each tile's scales'
+    for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1 + kStageTiles);
     fence_barrier_init();
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
@@ -251,18 +256,14 @@ __global__ void __launch_bounds__(W * 32, 1)
   // (an empty sequence's units hold no tile: the next one's first)
   while (lo < hi && static_cast<int64_t>(Hkv) * prefix[seq_lo + 1] <= lo) ++seq_lo;
 
-  const uint32_t bs32 = static_cast<uint32_t>(p.bs);  // paged: a 32-bit block size
   const uint64_t policy = l2_policy_evict_first();
   unsigned char* stage0 = smem + L::kStagesOff + warp * S * kStageQ8;
   const int g = lane >> 2;   // accumulator row group
   const int tq = lane & 3;   // accumulator column pair
 
-  // Elements 32 tq .. + 31 of head g's query row (zeros for g >= G), as loaded.
-  auto load_q = [&](uint4 (&qr)[4], int seq, int kvh) {
-    const uint4* row = reinterpret_cast<const uint4*>(
-        p.q + (static_cast<int64_t>(seq) * p.Hq + kvh * G + (g < G ? g : 0)) * kHeadDim + 32 * tq);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) qr[k] = g < G ? __ldg(row + k) : make_uint4(0u, 0u, 0u, 0u);
+  // Elements 32 tq .. + 31 of head g's query row (g < G).
+  auto q_row = [&](int seq, int kvh) {
+    return p.q + (static_cast<int64_t>(seq) * p.Hq + kvh * G + (g < G ? g : 0)) * kHeadDim + 32 * tq;
   };
   // the pair after `sg` (its tiles start at sg.pend < hi)
   auto next_seg = [&](const TcSeg& sg) -> TcSeg {
@@ -272,69 +273,84 @@ __global__ void __launch_bounds__(W * 32, 1)
     return tc_seg_at(sg.pend, hi, a, prefix, Hkv);
   };
 
-  int issued = 0, consumed = 0;
+  int issued = 0, consumed = 0;  // stages
   bool dead = false;
   if (lo < hi) {
-    // ---- the issue cursor: tile ix of pair iseg
+    // ---- the issue cursor: tiles in .. of pair iseg, in_end of them in this run.
+    // Lane l (0, 1) has the position of tile in + l: entry `blk` of the table, row
+    // `off` of its block (contiguous: row off of the request).
+    const uint32_t bs32 = static_cast<uint32_t>(p.bs);
+    const uint32_t step_blk = 16 * kStageTiles / bs32, step_off = 16 * kStageTiles % bs32;
     TcSeg iseg = tc_seg_at(lo, hi, seq_lo, prefix, Hkv);
-    int64_t ix = lo;
-    // The next pair's query rows are fetched into qn when the cursor first
-    // reaches it (if qn is free), so its start does not wait on them.
-    uint4 qn[4];
-    int64_t qn_pair = -1;
-    auto load_entry = [&]() -> int32_t {  // block-table entry of tile ix (lane 0)
-      if (kContig || lane != 0 || ix >= hi) return 0;
-      const uint32_t pos = static_cast<uint32_t>(ix - iseg.pstart) * 16;
-      return __ldg(p.block_tables + static_cast<int64_t>(iseg.seq) * p.max_blocks + pos / bs32);
+    int in = 0, in_end = 0;
+    uint32_t blk = 0, off = 0;
+    const int32_t* table = nullptr;  // of iseg's sequence
+    int32_t entry = 0;  // of this lane's tile
+    bool more = true;   // tiles are left to ask for
+    auto look_up = [&]() {
+      if (kContig) return;
+      if (lane < kStageTiles && more && in + lane < in_end) entry = __ldg(table + blk);
     };
-    auto issue = [&](int stage, int32_t entry) {
-      if (ix == iseg.x0 && qn_pair < 0) {  // whole warp
-        load_q(qn, iseg.seq, iseg.kvh);
-        qn_pair = iseg.pstart;
+    auto at_seg = [&]() {
+      in = static_cast<int>(iseg.x0 - iseg.pstart);
+      in_end = static_cast<int>(iseg.x1 - iseg.pstart);
+      // its query rows, which the pair's start waits for
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q_row(iseg.seq, iseg.kvh)));
+      const uint32_t pos = static_cast<uint32_t>(in + lane) * 16;
+      if (kContig) {
+        off = pos;
+        entry = req_s[iseg.seq];
+      } else {
+        blk = pos / bs32;
+        off = pos - blk * bs32;
+        table = p.block_tables + static_cast<int64_t>(iseg.seq) * p.max_blocks;
       }
-      if (lane == 0) {
-        unsigned char* st = stage0 + stage * kStageQ8;
-        const int64_t pos = (ix - iseg.pstart) * 16;
-        bool kv_ok = true;
-        int64_t row;
-        if (kContig) {
-          row = cache_row(req_s[iseg.seq], iseg.kvh, Hkv, p.bs, pos);
-        } else {
-          if (p.checked && (entry < 0 || entry >= p.num_blocks)) {
-            record_error(p.err, kErrBlockId);
-            kv_ok = false;  // skip the copy: stale rows, undefined output, no fault
-          }
-          row = cache_row(entry, iseg.kvh, Hkv, p.bs, static_cast<uint32_t>(pos) % bs32);
+    };
+    auto issue = [&](int stage) {
+      if (lane < kStageTiles) {
+        unsigned char* st = stage0 + stage * kStageQ8 + lane * 2 * kTileCodes;
+        bool ok = in + lane < in_end;
+        if (!kContig && p.checked && ok && (entry < 0 || entry >= p.num_blocks)) {
+          record_error(p.err, kErrBlockId);
+          ok = false;  // skip the copy: stale rows, undefined output, no fault
         }
-        mbar_arrive_expect_tx(&bars[stage], kv_ok ? static_cast<uint32_t>(kStageQ8) : 0u);
-        if (kv_ok) {
+        // (rows of the whole cache are fewer than 2^31)
+        const uint32_t row = (static_cast<uint32_t>(entry) * static_cast<uint32_t>(Hkv) +
+                              static_cast<uint32_t>(iseg.kvh)) * bs32 + off;
+        const uint32_t tiles = __popc(__ballot_sync((1u << kStageTiles) - 1u, ok));
+        if (lane == 0) mbar_arrive_expect_tx(&bars[stage], tiles * 2 * kTileCodes);
+        __syncwarp((1u << kStageTiles) - 1u);
+        if (ok) {
           const int32_t y = static_cast<int32_t>(row);
           tma_load_2d(st, &tmk, 0, y, &bars[stage], policy);
           tma_load_2d(st + kTileCodes, &tmv, 0, y, &bars[stage], policy);
-          cp_async_4(&scales[stage].x, p.k_scale + (row >> 4));
-          cp_async_4(&scales[stage].y, p.v_scale + (row >> 4));
+          float2* sc = &scales[stage * kStageTiles + lane];
+          cp_async_4(&sc->x, p.k_scale + (row >> 4));
+          cp_async_4(&sc->y, p.v_scale + (row >> 4));
         }
         cp_async_arrive(&bars[stage]);
       }
+      __syncwarp();
       ++issued;
-      if (++ix >= iseg.x1 && ix < hi) iseg = next_seg(iseg);
-    };
-
-    // Prologue: lane s fetches the table entry of tile lo + s (one memory
-    // latency for all of them), then the stages fill.
-    int32_t pre = 0;
-    if (!kContig) {
-      TcSeg cs = iseg;
-      for (int s = 0; s < S && lo + s < hi; ++s) {
-        if (lo + s >= cs.x1) cs = next_seg(cs);
-        if (lane == s) {
-          const uint32_t pos = static_cast<uint32_t>(lo + s - cs.pstart) * 16;
-          pre = __ldg(p.block_tables + static_cast<int64_t>(cs.seq) * p.max_blocks + pos / bs32);
+      in += kStageTiles;
+      off += step_off;
+      blk += step_blk;
+      if (!kContig && off >= bs32) {
+        off -= bs32;
+        ++blk;
+      }
+      if (in >= in_end) {
+        more = iseg.x1 < hi;
+        if (more) {
+          iseg = next_seg(iseg);
+          at_seg();
         }
       }
-    }
-    for (int s = 0; s < S && ix < hi; ++s) issue(s, __shfl_sync(kFull, pre, s));
-    int32_t next_entry = load_entry();
+      look_up();
+    };
+    at_seg();
+    look_up();
+    for (int s = 0; s < S && more; ++s) issue(s);
 
     // ---- per-lane offsets inside a 128-byte-swizzled 16 x 128 B box
     // K: chunks 2 tq and 2 tq + 1 of row g (row g + 8: 1 KiB on)
@@ -348,8 +364,10 @@ __global__ void __launch_bounds__(W * 32, 1)
       uint32_t qb[8][2];
       float qs0, qs1;  // score units of heads 2 tq and 2 tq + 1
       {
-        if (qn_pair != seg.pstart) load_q(qn, seg.seq, seg.kvh);
-        qn_pair = -1;
+        uint4 qn[4];
+        const uint4* row = reinterpret_cast<const uint4*>(q_row(seg.seq, seg.kvh));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) qn[k] = g < G ? __ldg(row + k) : make_uint4(0u, 0u, 0u, 0u);
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -374,12 +392,14 @@ __global__ void __launch_bounds__(W * 32, 1)
         qs1 = __shfl_sync(kFull, down, 8 * tq + 4) * p.qscale;
       }
       const int ctx = ctx_s[seg.seq];
-      float acc[8][4];
+      // O^T of elements 16 i + 2 g (0) and + 1 (1): heads 2 tq and 2 tq + 1 as a pair
+      uint64_t acc[8][2];
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+      for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = 0ull;
 
-      for (int64_t x = seg.x0; x < seg.x1 && !dead; ++x) {
+      const int x_end = static_cast<int>(seg.x1 - seg.pstart);
+      for (int x = static_cast<int>(seg.x0 - seg.pstart); x < x_end; x += kStageTiles) {
         const int stage = consumed % S;
         if (!__all_sync(kFull, mbar_wait_bounded(&bars[stage],
                                                  static_cast<uint32_t>(consumed / S) & 1u))) {
@@ -389,95 +409,119 @@ __global__ void __launch_bounds__(W * 32, 1)
         }
         ++consumed;
         unsigned char* st = stage0 + stage * kStageQ8;
-        const float2 sc = scales[stage];
-        const int row0 = static_cast<int>(x - seg.pstart) * 16;
-        const int nvalid = min(16, ctx - row0);
-        if (kE4m3 && nvalid < 16) {  // rows past the context may hold NaN: 0 * NaN
-          for (int idx = lane; idx < (16 - nvalid) * 8; idx += 32)
-            *reinterpret_cast<uint4*>(st + kTileCodes + nvalid * 128 + idx * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+        // rows of the stage that hold positions of the run's part of the pair
+        const int nvalid = min(16 * min(kStageTiles, x_end - x), ctx - x * 16);
+        const bool two = nvalid > 16;
+        if (kE4m3 && (nvalid & 15) != 0) {  // rows past the context may hold NaN: 0 * NaN
+          unsigned char* vt = st + kTileCodes + (two ? 2 * kTileCodes : 0);
+          const int first = nvalid & 15;
+          for (int idx = lane; idx < (16 - first) * 8; idx += 32)
+            *reinterpret_cast<uint4*>(vt + first * 128 + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
           __syncwarp();
         }
 
-        // ---- S^T = K . Q^T  (two accumulation chains)
-        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        // ---- S^T = K . Q^T; s[t]: scores of tokens g (0, 1) and g + 8 (2, 3) of tile
+        // t, heads 2tq and 2tq + 1
+        float s[kStageTiles][4];
+        float vs[kStageTiles];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const unsigned char* at = st + (half ? koff1 : koff0);
-          const uint4 r0 = *reinterpret_cast<const uint4*>(at);
-          const uint4 r1 = *reinterpret_cast<const uint4*>(at + 1024);
-          const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t a[4];
-            halves_of<kE4m3>(w0[e], a[0], a[2]);
-            halves_of<kE4m3>(w1[e], a[1], a[3]);
-            const int ks = 4 * half + e;
-            if (ks & 1) mma_f16_16816(sb, a, qb[ks][0], qb[ks][1]);
-            else mma_f16_16816(sa, a, qb[ks][0], qb[ks][1]);
+        for (int t = 0; t < kStageTiles; ++t) {
+          if (t > 0 && !two) {
+            s[t][0] = s[t][1] = s[t][2] = s[t][3] = -INFINITY;
+            continue;
           }
+          const float2 sc = scales[stage * kStageTiles + t];
+          vs[t] = sc.y;
+          const unsigned char* kt = st + t * 2 * kTileCodes;
+          float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const unsigned char* at = kt + (half ? koff1 : koff0);
+            const uint4 r0 = *reinterpret_cast<const uint4*>(at);
+            const uint4 r1 = *reinterpret_cast<const uint4*>(at + 1024);
+            const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t a[4];
+              halves_of<kE4m3>(w0[e], a[0], a[2]);
+              halves_of<kE4m3>(w1[e], a[1], a[3]);
+              const int ks = 4 * half + e;
+              if (ks & 1) mma_f16_16816(sb, a, qb[ks][0], qb[ks][1]);
+              else mma_f16_16816(sa, a, qb[ks][0], qb[ks][1]);
+            }
+          }
+          const float f0 = qs0 * sc.x, f1 = qs1 * sc.x;
+          const bool v0 = g + 16 * t < nvalid, v1 = g + 16 * t + 8 < nvalid;
+          s[t][0] = v0 ? (sa[0] + sb[0]) * f0 : -INFINITY;
+          s[t][1] = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;
+          s[t][2] = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;
+          s[t][3] = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;
         }
-        // scores of tokens g (s0, s1) and g + 8 (s2, s3), heads 2tq and 2tq + 1
-        const float f0 = qs0 * sc.x, f1 = qs1 * sc.x;
-        const bool v0 = g < nvalid, v1 = g + 8 < nvalid;
-        const float s0 = v0 ? (sa[0] + sb[0]) * f0 : -INFINITY;
-        const float s1 = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;
-        const float s2 = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;
-        const float s3 = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;
 
         // ---- online softmax, per head column
-        float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
+        float mx0 = m0, mx1 = m1;
+#pragma unroll
+        for (int t = 0; t < kStageTiles; ++t) {
+          mx0 = fmaxf(mx0, fmaxf(s[t][0], s[t][2]));
+          mx1 = fmaxf(mx1, fmaxf(s[t][1], s[t][3]));
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, o));
           mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, o));
         }
-        if (mx0 > m0) {
-          const float a = fast_exp2(m0 - mx0);
-          l0 *= a;
+        if (mx0 > m0 || mx1 > m1) {
+          // (a maximum of -inf stays; 0 where it was that and no longer is)
+          const float a0 = mx0 > m0 ? fast_exp2(m0 - mx0) : 1.f;
+          const float a1 = mx1 > m1 ? fast_exp2(m1 - mx1) : 1.f;
+          const uint64_t a2 = umma::f2_pack(__float_as_uint(a0), __float_as_uint(a1));
+          l0 *= a0;
+          l1 *= a1;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) { acc[i][0] *= a; acc[i][2] *= a; }
+          for (int i = 0; i < 8; ++i) {
+            acc[i][0] = umma::f2_mul(acc[i][0], a2);
+            acc[i][1] = umma::f2_mul(acc[i][1], a2);
+          }
           m0 = mx0;
-        }
-        if (mx1 > m1) {
-          const float a = fast_exp2(m1 - mx1);
-          l1 *= a;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) { acc[i][1] *= a; acc[i][3] *= a; }
           m1 = mx1;
         }
-        const float p0 = fast_exp2(s0 - m0), p2 = fast_exp2(s2 - m0);
-        const float p1 = fast_exp2(s1 - m1), p3 = fast_exp2(s3 - m1);
-        l0 += p0 + p2;
-        l1 += p1 + p3;
-        // P^T as the B operand, rounded to fp16 once
-        const uint32_t b0 = movmatrix_trans(pack_half2(p0, p1));  // tokens 0..7
-        const uint32_t b1 = movmatrix_trans(pack_half2(p2, p3));  // tokens 8..15
-
         // ---- O^T += vs (V^T . P^T)
-        const uint32_t vaddr = smem_addr(st) + kTileCodes + vrow * 128;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          uint32_t r[4];  // keys 0-7 and 8-15 of elements 16i .., then of 16(i + 1) ..
-          ldmatrix_x4_trans(r, vaddr + (((i + vch) ^ (vrow & 7)) << 4));
+        for (int t = 0; t < kStageTiles; ++t) {
+          if (t > 0 && !two) break;
+          const float p0 = fast_exp2(s[t][0] - m0), p2 = fast_exp2(s[t][2] - m0);
+          const float p1 = fast_exp2(s[t][1] - m1), p3 = fast_exp2(s[t][3] - m1);
+          l0 += p0 + p2;
+          l1 += p1 + p3;
+          // P^T as the B operand, rounded to fp16 once
+          const uint32_t b0 = movmatrix_trans(pack_half2(p0, p1));  // tokens 0..7
+          const uint32_t b1 = movmatrix_trans(pack_half2(p2, p3));  // tokens 8..15
+          const uint64_t vs2 = umma::f2_pack(__float_as_uint(vs[t]), __float_as_uint(vs[t]));
+          const uint32_t vaddr = smem_addr(st) + (2 * t + 1) * kTileCodes + vrow * 128;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t a[4];
-            halves_across<kE4m3>(r[2 * k], a[0], a[1]);
-            halves_across<kE4m3>(r[2 * k + 1], a[2], a[3]);
-            float d[4];
-            mma_f16_16816_zero(d, a, b0, b1);
+          for (int i = 0; i < 8; i += 2) {
+            uint32_t r[4];  // keys 0-7 and 8-15 of elements 16i .., then of 16(i + 1) ..
+            ldmatrix_x4_trans(r, vaddr + (((i + vch) ^ (vrow & 7)) << 4));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i + k][e] = fmaf(d[e], sc.y, acc[i + k][e]);
+            for (int k = 0; k < 2; ++k) {
+              uint32_t a[4];
+              halves_across<kE4m3>(r[2 * k], a[0], a[1]);
+              halves_across<kE4m3>(r[2 * k + 1], a[2], a[3]);
+              float d[4];
+              mma_f16_16816_zero(d, a, b0, b1);
+              acc[i + k][0] = umma::f2_fma(
+                  umma::f2_pack(__float_as_uint(d[0]), __float_as_uint(d[1])), vs2, acc[i + k][0]);
+              acc[i + k][1] = umma::f2_fma(
+                  umma::f2_pack(__float_as_uint(d[2]), __float_as_uint(d[3])), vs2, acc[i + k][1]);
+            }
           }
         }
         __syncwarp();
 
-        // ---- refill this stage with the next tile of the run
-        if (ix < hi) {
+        // ---- refill this stage with the next tiles of the run
+        if (more) {
           fence_proxy_async_smem();
-          issue(stage, next_entry);
-          next_entry = load_entry();
+          issue(stage);
         }
       }
       if (dead) break;
@@ -494,11 +538,12 @@ __global__ void __launch_bounds__(W * 32, 1)
                                     kHeadDim + 2 * g;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (2 * tq < G)
-            *reinterpret_cast<uint32_t*>(row + 16 * i) = pack_bf16x2(acc[i][0] * inv0, acc[i][2] * inv0);
+          float x0, x1, y0, y1;
+          umma::f2_unpack(acc[i][0], x0, x1);
+          umma::f2_unpack(acc[i][1], y0, y1);
+          if (2 * tq < G) *reinterpret_cast<uint32_t*>(row + 16 * i) = pack_bf16x2(x0 * inv0, y0 * inv0);
           if (2 * tq + 1 < G)
-            *reinterpret_cast<uint32_t*>(row + kHeadDim + 16 * i) =
-                pack_bf16x2(acc[i][1] * inv1, acc[i][3] * inv1);
+            *reinterpret_cast<uint32_t*>(row + kHeadDim + 16 * i) = pack_bf16x2(x1 * inv1, y1 * inv1);
         }
       } else {
         const int last = seg.x0 != lo;  // a run's first piece, or (not first) its last
@@ -507,8 +552,11 @@ __global__ void __launch_bounds__(W * 32, 1)
           float* r1 = r0 + kRecStride;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            *reinterpret_cast<float2*>(r0 + 16 * i + 2 * g) = make_float2(acc[i][0], acc[i][2]);
-            *reinterpret_cast<float2*>(r1 + 16 * i + 2 * g) = make_float2(acc[i][1], acc[i][3]);
+            float x0, x1, y0, y1;
+            umma::f2_unpack(acc[i][0], x0, x1);
+            umma::f2_unpack(acc[i][1], y0, y1);
+            *reinterpret_cast<float2*>(r0 + 16 * i + 2 * g) = make_float2(x0, y0);
+            *reinterpret_cast<float2*>(r1 + 16 * i + 2 * g) = make_float2(x1, y1);
           }
           if (g == 0) {
             r0[128] = m0;
@@ -636,8 +684,8 @@ cudaError_t launch_shape(const CUtensorMap& tk, const CUtensorMap& tv, const Dec
 template <bool kContig, bool kE4m3>
 cudaError_t launch_heads(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& p,
                          int num_ctas, cudaStream_t stream) {
-  return p.G <= 4 ? launch_shape<kContig, kE4m3, 12, 4, 4>(tk, tv, p, num_ctas, stream)
-                  : launch_shape<kContig, kE4m3, 10, 4, 8>(tk, tv, p, num_ctas, stream);
+  return p.G <= 4 ? launch_shape<kContig, kE4m3, 12, 2, 4>(tk, tv, p, num_ctas, stream)
+                  : launch_shape<kContig, kE4m3, 10, 2, 8>(tk, tv, p, num_ctas, stream);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {

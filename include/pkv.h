@@ -636,7 +636,8 @@ PKV_API pkv_status pkv_paged_decode_attention_noalloc(
  * (the automatic choice up to 2048 visible positions a sequence), or pair by
  * pair; and with 1 the splits of small batches are clusters that join them, as
  * with 0, unless pkv_set_split_tiles sets their length (then they are combined
- * by a second kernel).
+ * by a second kernel).  For decode over an 8-bit cache 1 is its kernel of
+ * clusters, 2 and 3 the one by warp runs.
  */
 PKV_API void pkv_set_decode_variant(int variant);
 PKV_API int pkv_get_decode_variant(void);

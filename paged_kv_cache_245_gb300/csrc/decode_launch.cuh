@@ -31,7 +31,7 @@ struct ClusterRoom {
 };
 
 template <typename Kernel>
-cudaError_t cluster_room(Kernel kernel, int bytes, ClusterRoom (&rooms)[64],
+cudaError_t cluster_room(Kernel kernel, int threads, int bytes, ClusterRoom (&rooms)[64],
                          unsigned long long* asked, ClusterRoom* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -44,7 +44,7 @@ cudaError_t cluster_room(Kernel kernel, int bytes, ClusterRoom (&rooms)[64],
     for (int i = 0; i < 4; ++i) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2u << i);
-      cfg.blockDim = dim3(kDecodeThreads);
+      cfg.blockDim = dim3(threads);
       cfg.dynamicSmemBytes = bytes;
       cudaLaunchAttribute attr[1] = {};
       attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -130,7 +130,8 @@ cudaError_t room_of_group(ClusterRoom* out) {
   static ClusterRoom rooms[64];
   auto kernel = decode_attention_kernel<G, kContig, kDecodeStages, true>;
   const cudaError_t e = ensure_smem_limit(kernel, L::kTotal, &done_mask);
-  return e != cudaSuccess ? e : cluster_room(kernel, L::kTotal, rooms, &asked, out);
+  return e != cudaSuccess ? e : cluster_room(kernel, kDecodeThreads, L::kTotal, rooms,
+                                                 &asked, out);
 }
 
 template <bool kContig>

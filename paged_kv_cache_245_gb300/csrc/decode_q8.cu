@@ -37,6 +37,7 @@
 
 #include "decode_tc.cuh"
 #include "q8.cuh"
+#include "q8_math.cuh"
 #include "umma.cuh"
 
 namespace pkv {
@@ -71,64 +72,6 @@ struct Q8Smem {
   static_assert(kPieceFloats * 4 <= S * kStageQ8, "a piece fits a warp's stages");
   static_assert(kFirstOff % 16 == 0 && kRunOff % 8 == 0, "float4 records, 64-bit runs");
 };
-
-// d = a(16x16, row) * b(16x8, col) + c, fp16 inputs, fp32 accumulation.
-__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                              uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
-      "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], const uint32_t (&a)[4],
-                                                   uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
-      "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// 1152 in both halves taken off: int8 code + 1152 -> code, exact.
-__device__ __forceinline__ uint32_t less_1152(uint32_t h) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
-  return r;
-}
-
-// Codes (0, 1) and (2, 3) of a word as halves.
-template <bool kE4m3>
-__device__ __forceinline__ void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if (kE4m3) {
-    lo = e4m3x2_to_half2(w);
-    hi = e4m3x2_to_half2(w >> 16);
-  } else {
-    const uint32_t u = w ^ 0x80808080u;
-    lo = less_1152(__byte_perm(u, 0x64646464u, 0x4140));
-    hi = less_1152(__byte_perm(u, 0x64646464u, 0x4342));
-  }
-}
-
-// Codes (0, 2) and (1, 3): one element of two keys each (V).
-template <bool kE4m3>
-__device__ __forceinline__ void halves_across(uint32_t w, uint32_t& even, uint32_t& odd) {
-  if (kE4m3) {
-    const uint32_t t = __byte_perm(w, 0u, 0x3120);
-    even = e4m3x2_to_half2(t);
-    odd = e4m3x2_to_half2(t >> 16);
-  } else {
-    const uint32_t u = w ^ 0x80808080u;
-    even = less_1152(__byte_perm(u, 0x64646464u, 0x4240));
-    odd = less_1152(__byte_perm(u, 0x64646464u, 0x4341));
-  }
-}
 
 // The mbarrier counts one arrival more: when this thread's cp.async copies land.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -368,26 +311,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         const uint4* row = reinterpret_cast<const uint4*>(q_row(seg.seq, seg.kvh));
 #pragma unroll
         for (int k = 0; k < 4; ++k) qn[k] = g < G ? __ldg(row + k) : make_uint4(0u, 0u, 0u, 0u);
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t w[4] = {qn[k].x, qn[k].y, qn[k].z, qn[k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-        }
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-        // 2^n, n = 14 - exponent of the largest element (at most 126)
-        const int n = min(126, 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23));
-        const float up = __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - n) << 23);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t w[4] = {qn[k].x, qn[k].y, qn[k].z, qn[k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            qb[2 * k + (e >> 1)][e & 1] = pack_half2(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
-        }
+        const float down = queries_to_half(qn, qb);
         qs0 = __shfl_sync(kFull, down, 8 * tq) * p.qscale;
         qs1 = __shfl_sync(kFull, down, 8 * tq + 4) * p.qscale;
       }

@@ -1424,6 +1424,29 @@ pkv_status append_q8_common(const int32_t* positions, const int64_t* slot_mappin
   return PKV_OK;
 }
 
+// Decode over the 8-bit cache by clusters (decode_q8_cluster.cu): the largest
+// cluster of 8-warp CTAs that the device holds for every pair at once, or, past one
+// such CTA an SM, 4-warp CTAs alone; where a warp then has at most 8 tiles (warps 0
+// if not).  8 KV heads, us a call, that kernel / the other: 8 tiles a warp (1
+// sequence of 8000, 4 of 4000, 8 of 2000) 12.0 / 21.3, 12.3 / 16.6, 12.1 / 15.6, 4
+// heads and 32 ragged sequences up to 4095 (32 tiles) 27.4 / 17.8; 4-warp CTAs: 32
+// of 128 (2) 5.6 / 8.9, 32 of 512 (8) 13.0 / 14.3.  In two rounds of CTAs it is the
+// slower one: 64 of 256 18.1 / 15.1.
+struct Q8Cluster {
+  int cluster, warps;
+};
+Q8Cluster q8_cluster(int64_t pairs, int32_t max_context, int sms, const pkv::ClusterRoom& room) {
+  Q8Cluster s = {1, 8};
+  if (pairs > sms) {
+    if (pairs > static_cast<int64_t>(pkv::kQ8SmallCtas) * sms) return {0, 0};
+    s.warps = 4;
+  }
+  for (int i = 0; i < 3; ++i)  // 2, 4, 8
+    if (s.warps == 8 && pairs <= room.held[i]) s.cluster = 2 << i;
+  const int64_t tiles = (static_cast<int64_t>(max_context) + 15) / 16;
+  return tiles > 8 * s.cluster * s.warps ? Q8Cluster{0, 0} : s;
+}
+
 // Attention over the 8-bit cache.  cu_q null: decode, a row of q per sequence.
 // contig: tables are request ids, max_blocks 1, num_blocks the requests, bs = S.
 pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_tokens,
@@ -1494,9 +1517,25 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
       return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
                   workspace ? workspace_bytes : size_t{0});
     if (!aligned(workspace, 16)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    const bool e4m3 = cache->format == PKV_Q8_E4M3;
+    const int variant = g_variant.load();
+    if (variant <= 1) {
+      pkv::ClusterRoom room;
+      const cudaError_t re = pkv::room_decode_q8_cluster(e4m3, &room);
+      if (re != cudaSuccess) return cuda_fail(re, "cluster query");
+      const Q8Cluster small =
+          q8_cluster(static_cast<int64_t>(num_seqs) * h.num_kv_heads, max_context, sms, room);
+      if (small.warps > 0 || variant == 1) {
+        const cudaError_t ke = pkv::launch_decode_q8_cluster(
+            p, e4m3, small.warps > 0 ? small.cluster : 1, small.warps > 0 ? small.warps : 8,
+            static_cast<cudaStream_t>(stream));
+        if (ke != cudaSuccess) return cuda_fail(ke, "q8 decode launch");
+        return PKV_OK;
+      }
+    }
     cudaError_t ce = cudaSuccess;
     const pkv::TcStatus ts =
-        pkv::launch_decode_q8(p, cache->format == PKV_Q8_E4M3, contig, tc_ctas(sms), workspace,
+        pkv::launch_decode_q8(p, e4m3, contig, tc_ctas(sms), workspace,
                               static_cast<cudaStream_t>(stream), &ce);
     if (ts == pkv::TcStatus::kEncodeFailed)
       return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for the K/V cache");

@@ -69,6 +69,14 @@ struct AttentionQ8Params {
 // Decode (cu_q null): workspace of tc_workspace_bytes(num_ctas).
 TcStatus launch_decode_q8(const AttentionQ8Params& p, bool e4m3, bool contig, int num_ctas,
                           void* workspace, cudaStream_t stream, cudaError_t* cuda_err);
+// The same for small batches: a cluster of 1, 2, 4 or 8 CTAs of 4 or 8 warps a
+// (sequence, KV head); no workspace.  The room on the current device for clusters of
+// 8-warp CTAs, of which an SM holds one (of 4-warp CTAs: kQ8SmallCtas).
+struct ClusterRoom;
+constexpr int kQ8SmallCtas = 3;
+cudaError_t room_decode_q8_cluster(bool e4m3, ClusterRoom* out);
+cudaError_t launch_decode_q8_cluster(const AttentionQ8Params& p, bool e4m3, int cluster, int warps,
+                                     cudaStream_t stream);
 cudaError_t launch_attention_q8(const AttentionQ8Params& p, bool e4m3, cudaStream_t stream);
 
 #ifdef __CUDACC__

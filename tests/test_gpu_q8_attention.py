@@ -20,7 +20,18 @@ def _reset():
     pkv.set_checked(False)
     yield
     pkv.set_checked(False)
+    pkv.set_decode_variant(pkv.VARIANT_AUTO)
     torch.cuda.synchronize()
+
+
+# decode's kernels: the call's own choice, by clusters, by warp runs
+VARIANTS = [pkv.VARIANT_AUTO, pkv.VARIANT_SPLIT, pkv.VARIANT_TC_12X2]
+
+
+@pytest.fixture(params=VARIANTS)
+def variant(request):
+    pkv.set_decode_variant(request.param)
+    return request.param
 
 
 class Batch:
@@ -113,27 +124,27 @@ HEADS = [(4, 4), (10, 2), (20, 4), (32, 8), (6, 1), (14, 2), (8, 1)]
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
 @pytest.mark.parametrize("layout", ["paged", "contig"])
 @pytest.mark.parametrize("hq,hkv", HEADS)
-def test_decode_heads(dtype, layout, hq, hkv):
+def test_decode_heads(variant, dtype, layout, hq, hkv):
     b = Batch(dtype, layout, hq, hkv, [1, 15, 16, 17, 0, 100, 257, 640])
     b.check(b.decode())
 
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
 @pytest.mark.parametrize("bs", [16, 32, 48, 64, 128, 272])
-def test_decode_block_sizes(dtype, bs):
+def test_decode_block_sizes(variant, dtype, bs):
     b = Batch(dtype, "paged", 8, 2, [bs - 1, bs, bs + 1, 3 * bs + 5, 1], bs=bs)
     b.check(b.decode())
 
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
 @pytest.mark.parametrize("ctx", [[1], [16], [1000], [4000], [9001], [300] * 4, [700] * 40,
-                                 [1, 8192] + [50] * 30, [2500] * 64, [5] * 600])
-def test_decode_lengths(dtype, ctx):
+                                 [1, 8192] + [50] * 30, [2500] * 64, [5] * 600, [300] * 19 + [1] * 19, [200] * 90])
+def test_decode_lengths(variant, dtype, ctx):
     b = Batch(dtype, "paged", 8, 2, ctx, bs=32)
     b.check(b.decode())
 
 
-def test_decode_wide_bound():
+def test_decode_wide_bound(variant):
     """A max_context far above the contexts."""
     b = Batch(torch.int8, "paged", 8, 2, [40, 3, 900], bs=16)
     b.where = torch.cat([b.where, torch.full((3, 3000), -7, dtype=torch.int32, device=DEV)], 1)
@@ -142,7 +153,7 @@ def test_decode_wide_bound():
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0, 1e-6])
-def test_decode_scales(dtype, scale):
+def test_decode_scales(variant, dtype, scale):
     b = Batch(dtype, "paged", 8, 2, [70, 1, 333], by=1.0)
     b.check(b.decode(scale=scale), scale=scale)
 
@@ -157,21 +168,21 @@ def spread_scales(b, low, high):
 
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
-def test_decode_uneven_groups(dtype):
+def test_decode_uneven_groups(variant, dtype):
     """Neighbouring groups whose scales differ by orders of magnitude, zeros among them."""
     b = Batch(dtype, "paged", 8, 2, [500, 37, 2100], by=0.01)
     spread_scales(b, -24, 4)
     b.check(b.decode())
 
 
-def test_decode_large_queries():
+def test_decode_large_queries(variant):
     b = Batch(torch.int8, "paged", 8, 2, [200, 17], by=2.0 ** 18)
     b.check(b.decode(scale=2.0 ** -24), scale=2.0 ** -24)
     b = Batch(torch.int8, "paged", 8, 2, [200, 17], by=2.0 ** -40)
     b.check(b.decode(scale=2.0 ** 37), scale=2.0 ** 37)
 
 
-def test_decode_streams_and_capture():
+def test_decode_streams_and_capture(variant):
     b = Batch(torch.float8_e4m3fn, "paged", 8, 2, [900, 40, 1, 2000])
     b.check(b.decode())
     out = torch.empty_like(b.q)
@@ -190,7 +201,7 @@ def test_decode_streams_and_capture():
         b.check(out)
 
 
-def test_decode_checked():
+def test_decode_checked(variant):
     b = Batch(torch.int8, "paged", 8, 2, [100, 60])
     pkv.set_checked(True)
     b.check(b.decode())
@@ -200,6 +211,9 @@ def test_decode_checked():
     assert pkv.get_device_error() == "block_id"
     b.decode(max_context=90)
     assert pkv.get_device_error() in ("context", "block_id")
+    b.where[0, 2] = 0
+    b.decode(max_context=90)
+    assert pkv.get_device_error() == "context"
     c = Batch(torch.int8, "contig", 8, 2, [100, 60])
     c.where[1] = 99
     c.decode()

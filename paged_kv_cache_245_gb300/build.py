@@ -18,8 +18,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["pkv_api.cu", "kv_ops.cu", "decode_paged.cu", "decode_contig.cu", "decode_tc.cu",
            "pkv_noalloc.cu", "block_manager.cpp", "vmm.cpp", "cascade.cu", "prefill.cu", "prefix.cu",
            "rope.cu", "prefill_scored.cu", "decode_paged_scored.cu", "decode_contig_scored.cu",
-           "decode_tc_scored.cu", "decode_runs.cu", "append_q8.cu", "attention_q8.cu",
-           "decode_q8.cu", "decode_q8_cluster.cu"]
+           "decode_tc_scored.cu", "decode_runs.cu", "append_q8.cu", "decode_q8.cu",
+           "decode_q8_cluster.cu", "prefill_q8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

@@ -1542,9 +1542,13 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
     if (ts != pkv::TcStatus::kOk) return cuda_fail(ce, "q8 decode launch");
     return PKV_OK;
   }
-  const cudaError_t e = pkv::launch_attention_q8(p, cache->format == PKV_Q8_E4M3,
-                                                 static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "q8 attention launch");
+  cudaError_t ce = cudaSuccess;
+  const pkv::TcStatus ts =
+      pkv::launch_prefill_q8(p, cache->format == PKV_Q8_E4M3, contig, num_tokens, sms,
+                             static_cast<cudaStream_t>(stream), &ce);
+  if (ts == pkv::TcStatus::kEncodeFailed)
+    return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for q");
+  if (ts != pkv::TcStatus::kOk) return cuda_fail(ce, "q8 prefill launch");
   return PKV_OK;
 }
 

@@ -77,7 +77,9 @@ constexpr int kQ8SmallCtas = 3;
 cudaError_t room_decode_q8_cluster(bool e4m3, ClusterRoom* out);
 cudaError_t launch_decode_q8_cluster(const AttentionQ8Params& p, bool e4m3, int cluster, int warps,
                                      cudaStream_t stream);
-cudaError_t launch_attention_q8(const AttentionQ8Params& p, bool e4m3, cudaStream_t stream);
+// Prefill (prefill_q8.cu).
+TcStatus launch_prefill_q8(const AttentionQ8Params& p, bool e4m3, bool contig, int num_tokens,
+                           int sms, cudaStream_t stream, cudaError_t* cuda_err);
 
 #ifdef __CUDACC__
 

@@ -53,17 +53,22 @@ def values(cache, scale):
     return cache.to(torch.float32).double() * scale.double().repeat_interleave(16, 2)[..., None]
 
 
-def attend64(q, k, v, pos, scale, rounded=0):
-    """q [n, Hq, D], k and v [Hkv, c, D] fp64, pos [n] -> (out, tol) [n, Hq, D].
-    rounded: how often each key and value element is rounded to fp16 on the way."""
+# What a probability is rounded to on its way into the product with V, half a step: the
+# decode kernels round it to fp16, the prefill kernel rounds it times its group's scale
+# to bf16 (whose range holds every scale).  Neither rounds keys or values: a code has at
+# most 8 significant bits, which fp16 (11) and bf16 (8) hold exactly.
+DECODE, PREFILL = 2.0 ** -11, 2.0 ** -8
+
+
+def attend64(q, k, v, pos, scale, half_step=DECODE):
+    """q [n, Hq, D], k and v [Hkv, c, D] fp64, pos [n] -> (out, tol) [n, Hq, D]."""
     n, hq, D = q.shape
     hkv, c, _ = k.shape
     q, k, v = q.double(), k.repeat_interleave(hq // hkv, 0), v.repeat_interleave(hq // hkv, 0)
     z = torch.einsum("nhd,hcd->hnc", q, k) * scale
     # fp32 dot products of 128 terms (at most 128 roundings of 2^-24 of the sum of
-    # sizes, the group's scale and the softmax's factor among them) and the keys' own
-    ez = torch.einsum("nhd,hcd->hnc", q.abs(), k.abs()) * abs(scale) * (
-        2.0 ** -16 + rounded * 2.0 ** -11)
+    # sizes, the group's scale and the softmax's factor among them)
+    ez = torch.einsum("nhd,hcd->hnc", q.abs(), k.abs()) * (abs(scale) * 2.0 ** -16)
     seen = torch.arange(c, device=q.device) <= torch.as_tensor(pos, device=q.device)[:, None]
     z = z.masked_fill(~seen, -math.inf)
     top = z.amax(-1, keepdim=True)
@@ -75,9 +80,9 @@ def attend64(q, k, v, pos, scale, rounded=0):
     size = torch.einsum("hnc,hcd->nhd", w, v.abs())
     err = torch.einsum("hnc,hcd->nhd", w * (2 * ez) + small * 2.0 ** -25, v.abs())
     werr = (w * 2 * ez).sum(-1).transpose(0, 1)[..., None]
-    # a probability rounded to fp16 (2^-11), its exponential and the sums (2^-18),
-    # the values' own roundings, and the output's to bf16
-    tol = (2.0 ** -11 * (1 + rounded) + 2.0 ** -18) * size + err + werr * size \
+    # a probability's rounding, its exponential and the sums (2^-18), and the output's
+    # rounding to bf16
+    tol = (half_step + 2.0 ** -18) * size + err + werr * size \
         + out.abs() * 2.0 ** -8 + 1e-30
     return out, tol
 

@@ -93,7 +93,7 @@ class Batch:
             out.append(torch.cat(list(q8_ref.values(x, s[b])), 1)[:, :c])
         return out
 
-    def check(self, got, scale=SCALE, rounded=0):
+    def check(self, got, scale=SCALE, half_step=q8_ref.DECODE):
         at = 0
         for i, (c, n) in enumerate(zip(self.lens, self.new)):
             mine = got[at:at + n]
@@ -101,7 +101,8 @@ class Batch:
                 assert bool((mine == 0).all())
             elif n:
                 k, v = self.rows(i)
-                want, tol = q8_ref.attend64(self.q[at:at + n], k, v, range(c - n, c), scale, rounded)
+                want, tol = q8_ref.attend64(self.q[at:at + n], k, v, range(c - n, c), scale,
+                                            half_step)
                 q8_ref.assert_close(mine, want, tol, "sequence %d (context %d)" % (i, c))
             at += n
 
@@ -228,7 +229,7 @@ def test_decode_checked(variant):
 def test_prefill_heads(dtype, layout, hq, hkv):
     new = [1, 5, 17, 64, 130, 33]
     b = Batch(dtype, layout, hq, hkv, [n + c for n, c in zip(new, [0, 20, 0, 127, 300, 1])], new)
-    b.check(b.prefill(), rounded=2)
+    b.check(b.prefill(), half_step=q8_ref.PREFILL)
 
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
@@ -236,7 +237,7 @@ def test_prefill_heads(dtype, layout, hq, hkv):
 def test_prefill_block_sizes(dtype, bs):
     b = Batch(dtype, "paged", 8, 2, [bs - 1, 2 * bs + 3, 3 * bs, 500 + bs], [bs - 1, bs + 3, 1, 77],
               bs=bs)
-    b.check(b.prefill(), rounded=2)
+    b.check(b.prefill(), half_step=q8_ref.PREFILL)
 
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
@@ -245,28 +246,28 @@ def test_prefill_block_sizes(dtype, bs):
                                         ([1500, 2, 1], [7, 2500, 0]), ([300] * 40, [10] * 40)])
 def test_prefill_lengths(dtype, new, cached):
     b = Batch(dtype, "paged", 8, 2, [n + c for n, c in zip(new, cached)], new, bs=32)
-    b.check(b.prefill(), rounded=2)
+    b.check(b.prefill(), half_step=q8_ref.PREFILL)
 
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0, 1e-6])
 def test_prefill_scales(dtype, scale):
     b = Batch(dtype, "paged", 8, 2, [70, 1, 333], [70, 1, 140], by=1.0)
-    b.check(b.prefill(scale=scale), scale=scale, rounded=2)
+    b.check(b.prefill(scale=scale), scale=scale, half_step=q8_ref.PREFILL)
 
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
 def test_prefill_uneven_groups(dtype):
     b = Batch(dtype, "paged", 8, 2, [500, 37, 2100], [500, 20, 60], by=0.01)
     spread_scales(b, -24, 4)
-    b.check(b.prefill(), rounded=2)
+    b.check(b.prefill(), half_step=q8_ref.PREFILL)
 
 
 def test_prefill_large_queries():
     b = Batch(torch.int8, "paged", 8, 2, [200, 17], [150, 17], by=2.0 ** 18)
-    b.check(b.prefill(scale=2.0 ** -24), scale=2.0 ** -24, rounded=2)
+    b.check(b.prefill(scale=2.0 ** -24), scale=2.0 ** -24, half_step=q8_ref.PREFILL)
     b = Batch(torch.int8, "paged", 8, 2, [200, 17], [150, 17], by=2.0 ** -40)
-    b.check(b.prefill(scale=2.0 ** 37), scale=2.0 ** 37, rounded=2)
+    b.check(b.prefill(scale=2.0 ** 37), scale=2.0 ** 37, half_step=q8_ref.PREFILL)
 
 
 def test_prefill_rows_behind_the_last_chunk():
@@ -276,17 +277,17 @@ def test_prefill_rows_behind_the_last_chunk():
     out = torch.full_like(b.q, 3.0)
     b.prefill(max_new=2 ** 31 - 1, out=out)
     assert bool((out[70:] == 3.0).all())
-    b.check(out, rounded=2)
+    b.check(out, half_step=q8_ref.PREFILL)
 
 
 def test_prefill_empty_chunks():
     b = Batch(torch.int8, "paged", 8, 2, [40, 70, 0, 5], [0, 30, 0, 5])
-    b.check(b.prefill(), rounded=2)
+    b.check(b.prefill(), half_step=q8_ref.PREFILL)
 
 
 def test_prefill_captured():
     b = Batch(torch.float8_e4m3fn, "paged", 8, 2, [300, 700], [100, 40])
-    b.check(b.prefill(), rounded=2)
+    b.check(b.prefill(), half_step=q8_ref.PREFILL)
     out = torch.empty_like(b.q)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
@@ -296,13 +297,13 @@ def test_prefill_captured():
         b.ctx.copy_(torch.tensor(lens, dtype=torch.int32))
         b.cu.copy_(torch.tensor([0, new[0], new[0] + new[1]], dtype=torch.int32))
         g.replay()
-        b.check(out, rounded=2)
+        b.check(out, half_step=q8_ref.PREFILL)
 
 
 def test_prefill_checked():
     b = Batch(torch.int8, "paged", 8, 2, [100, 60], [50, 60])
     pkv.set_checked(True)
-    b.check(b.prefill(), rounded=2)
+    b.check(b.prefill(), half_step=q8_ref.PREFILL)
     assert pkv.get_device_error() == "none"
     b.prefill(max_new=55)
     assert pkv.get_device_error() == "context"
@@ -345,7 +346,7 @@ def test_append_and_attend(dtype):
         slots += [int(table[p // bs]) * bs + p % bs for p in range(n)]
         positions += range(n)
     step(lens, slots, positions)
-    b.check(b.prefill(), rounded=2)
+    b.check(b.prefill(), half_step=q8_ref.PREFILL)
     for _ in range(15):
         at = [bm.length(s) for s in seqs]
         slots, _ = bm.append(seqs)

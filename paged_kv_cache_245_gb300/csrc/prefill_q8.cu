@@ -89,6 +89,14 @@ struct PBars {
   uint64_t* drain;      // the MMA warp's final wait
 };
 
+// One lane of the warp (every lane calls).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r != 0u;
+}
+
 // Four bytes of shared memory from global memory, or zeros.
 __device__ __forceinline__ void cp_async_4_or_zero(void* dst, const void* src, bool copy) {
   const int n = copy ? 4 : 0;
@@ -471,85 +479,93 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(&B.qfull[qs], (last_phase >> qs) & 1u);
     }
   } else if (warp == 9) {
-    // ================= MMA issuer: lane 0 alone =================
-    // One thread issues every product, waits on single-lane barrier checks
-    // and never votes or reconverges with the other lanes inside the loop.
-    if (lane == 0) {
-    auto issue_s = [&](int t, int qs, int stage) {  // S_t = Q K^T
-      const uint32_t q_addr = smem_base + q_off(qs);
-      const uint32_t k_addr = smem_base + kOffK + stage * kStageBytes;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t koff = (kk & 3) * 32;
-        umma_ss(tmem + t * 128, smem_desc(q_addr + (kk >> 2) * kHalfBytes + koff, 16, 1024),
-                smem_desc(k_addr + (kk >> 2) * 1024 + koff, 16, 2048), kIdescS, kk > 0);
-      }
+    // ================= MMA issuer =================
+    // The whole warp walks the tiles on warp-uniform values, so that descriptors stay
+    // in uniform registers; one elected lane issues.
+    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+    const uint32_t base = __shfl_sync(kFull, smem_base, 0);
+    // the low words of the operands' descriptors (smem_desc): address, leading offset
+    const uint32_t q_lo = (((base + q_off(0)) & 0x3FFFFu) >> 4) | ((16u >> 4) << 16);
+    const uint32_t k_lo = (((base + kOffK) & 0x3FFFFu) >> 4) | ((16u >> 4) << 16);
+    const uint32_t v_lo = (((base + kOffK + kOpBytes) & 0x3FFFFu) >> 4) | ((1024u >> 4) << 16);
+    constexpr uint32_t kHiQ = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, mode
+    constexpr uint32_t kHiKV = (2048u >> 4) | (1u << 14) | (2u << 29);
+    auto desc = [](uint32_t lo, uint32_t hi) -> uint64_t {
+      return (static_cast<uint64_t>(hi) << 32) | lo;
     };
-    auto issue_pv = [&](int t, int stage, bool acc) {  // O_t (+)= P_t V
-      const uint32_t v_addr = smem_base + kOffK + stage * kStageBytes + kOpBytes;
+    auto issue_s = [&](int t, int qs, int stage) {  // S_t = Q K^T
+      const uint32_t q = q_lo + qs * (kOpBytes >> 4), k = k_lo + stage * (kStageBytes >> 4);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
-        umma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                smem_desc(v_addr + kk * 4096, 1024, 2048), kIdescPV, (acc || kk > 0));
+        umma_ss(tm + t * 128, desc(q + (kk >> 2) * (kHalfBytes >> 4) + (kk & 3) * 2, kHiQ),
+                desc(k + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, kHiKV), kIdescS, kk > 0);
+    };
+    auto issue_pv = [&](int t, int stage, bool acc) {  // O_t (+)= P_t V
+      const uint32_t v = v_lo + stage * (kStageBytes >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        umma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, desc(v + kk * (4096 >> 4), kHiKV),
+                kIdescPV, (acc || kk > 0));
     };
     auto waitb = [&](uint64_t* b, uint32_t parity) -> bool {
-      return wait_or_abort(b, parity, abort, p.err);
+      return __all_sync(kFull, wait_or_abort(b, parity, abort, p.err));
     };
-    auto read_item1 = [&](int n, PItem& it) -> bool {
-      const int slot = n & (kRing - 1);
-      if (!wait_or_abort(&B.ifull[slot], (n / kRing) & 1, abort, p.err)) return false;
-      it = ring[slot];
-      mbar_arrive(&B.iempty[slot]);
+    // what the products need of an item: its key tiles (0: the end), a second row tile
+    int ntiles = 0;
+    bool two = false;
+    auto next_item = [&](int n) -> bool {
+      PItem it;
+      if (!read_item(n, it)) return false;
+      ntiles = __shfl_sync(kFull, it.ntiles, 0);
+      two = __shfl_sync(kFull, it.rows - it.row0, 0) > TR;
       return true;
     };
-    auto has_two = [TR](const PItem& it) { return it.rows > it.row0 + TR; };
-    // S products of an item's first tile, global tile g, its Q tiles at qa, qb
-    auto first_s = [&](const PItem& it, QCursor qa, QCursor qb, int g) -> bool {
+    // S products of the item's first tile, global tile g, its Q tiles at qa, qb
+    auto first_s = [&](QCursor qa, QCursor qb, int g) -> bool {
       if (!waitb(&B.kfull[g & 1], (g >> 1) & 1) || !waitb(&B.qfull[qa.slot], qa.phase))
         return false;
       tc_fence_after();
-      {
+      if (elect_one()) {
         issue_s(0, qa.slot, g & 1);
         umma_commit(&B.sfull[0]);
-        if (it.ntiles == 1) umma_commit(&B.qempty[qa.slot]);
+        if (ntiles == 1) umma_commit(&B.qempty[qa.slot]);
+        if (!two) umma_commit(&B.kempty[g & 1]);
       }
-      if (has_two(it)) {
+      __syncwarp();
+      if (two) {
         if (!waitb(&B.qfull[qb.slot], qb.phase)) return false;
         tc_fence_after();
-        {
+        if (elect_one()) {
           issue_s(1, qb.slot, g & 1);
           umma_commit(&B.sfull[1]);
-          if (it.ntiles == 1) umma_commit(&B.qempty[qb.slot]);
+          if (ntiles == 1) umma_commit(&B.qempty[qb.slot]);
+          umma_commit(&B.kempty[g & 1]);  // both S products of tile g issued
         }
+        __syncwarp();
       }
-      umma_commit(&B.kempty[g & 1]);  // both S products of tile g issued
       return true;
     };
     int nread = 0;
-    PItem cur;
-    bool ok = read_item1(nread++, cur);
-    QCursor q0 = {0, 0};        // cur's Q tiles: row tile 0 at q0, row tile 1 at q1
+    bool ok = next_item(nread++);
+    QCursor q0 = {0, 0};        // the item's Q tiles: row tile 0 at q0, row tile 1 at q1
     QCursor q1 = q0.next(kQSlots);
     int g = 0;                  // tile index over all items (ring stage g & 1)
     uint32_t np0 = 0, np1 = 0;  // P hand-overs taken per row tile
-    if (ok && cur.ntiles > 0) ok = first_s(cur, q0, q1, g);
-    // Tile g, (cur, j): within an item PV_0(j) S_0(j+1) | PV_1(j) S_1(j+1);
-    // at an item's last tile both P V products go first, then the next
-    // item's first S products, so the current item never waits on the next.
+    if (ok && ntiles > 0) ok = first_s(q0, q1, g);
+    // Tile g, tile j of the item: within an item PV_0(j) S_0(j+1) | PV_1(j) S_1(j+1);
+    // at an item's last tile both P V products go first, then the next item's first S
+    // products, so the current item never waits on the next.
     int j = 0;
-    while (ok && cur.ntiles > 0) {
+    while (ok && ntiles > 0) {
       const int s = g & 1;
-      const bool two = has_two(cur);
-      const bool last = j == cur.ntiles - 1;
-      const bool qlast = j + 1 == cur.ntiles - 1;  // S of tile j + 1 reads cur's Q last
-      ok = waitb(&B.vfull[s], (g >> 1) & 1);
-      if (!ok) break;
-      ok = waitb(&B.pfull[0], np0 & 1);
+      const bool last = j == ntiles - 1;
+      const bool qlast = j + 1 == ntiles - 1;  // S of tile j + 1 reads the item's Q last
+      ok = waitb(&B.vfull[s], (g >> 1) & 1) && waitb(&B.pfull[0], np0 & 1);
       ++np0;
       if (ok && !last) ok = waitb(&B.kfull[s ^ 1], ((g + 1) >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      {
+      if (elect_one()) {
         issue_pv(0, s, j > 0);
         if (last) umma_commit(&B.ofull[0]);
         if (!two) umma_commit(&B.vempty[s]);
@@ -560,15 +576,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!two) umma_commit(&B.kempty[s ^ 1]);
         }
       }
+      __syncwarp();
       if (two) {
         ok = waitb(&B.pfull[1], np1 & 1);
         ++np1;
         if (!ok) break;
         tc_fence_after();
-        {
+        if (elect_one()) {
           issue_pv(1, s, j > 0);
           if (last) umma_commit(&B.ofull[1]);
-          umma_commit(&B.vempty[s]);  // the producer reuses the stage
+          umma_commit(&B.vempty[s]);  // the converters reuse the stage
           if (!last) {
             issue_s(1, q1.slot, s ^ 1);
             umma_commit(&B.sfull[1]);
@@ -576,22 +593,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(&B.kempty[s ^ 1]);
           }
         }
+        __syncwarp();
       }
       ++g;
       if (last) {
-        PItem nx;
-        ok = read_item1(nread++, nx);
+        const bool had_two = two;
+        ok = next_item(nread++);
         if (!ok) break;
-        q0 = two ? q1.next(kQSlots) : q1;  // the next item's Q tiles follow cur's
+        q0 = had_two ? q1.next(kQSlots) : q1;  // the next item's Q tiles follow
         q1 = q0.next(kQSlots);
-        cur = nx;
         j = 0;
-        if (cur.ntiles > 0) ok = first_s(cur, q0, q1, g);
+        if (ntiles > 0) ok = first_s(q0, q1, g);
       } else {
         ++j;
       }
     }
-      // every MMA issued has completed before the tensor memory is released
+    // every product issued has completed before the tensor memory is released (one
+    // lane has issued them all: elect.sync gives the same lane each time)
+    if (elect_one()) {
       umma_commit(B.drain);
       mbar_wait_bounded(B.drain, 0);
     }

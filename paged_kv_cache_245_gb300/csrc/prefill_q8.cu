@@ -15,10 +15,11 @@
 //
 // The operands hold the codes themselves, which bf16 holds exactly (int8 and e4m3
 // have at most 8 significant bits): a key's scale is uniform over 16 columns of S
-// and enters the softmax's own multiplication, and a value's is multiplied into P
-// before P is rounded to bf16 -- the one rounding that the plain kernel has too, and
-// bf16's range holds any scale.  With ks, vs the scales of key j's group:
-//   s_j = (q . kcode_j) (scale ks),   O += (P_j vs) vcode_j,   l += P_j.
+// and enters the softmax's own multiplication, and a value's enters the exponent,
+// so that P is rounded to bf16 with it -- the one rounding that the plain kernel has
+// too, and bf16's range holds any scale.  With ks, vs the scales of key j's group:
+//   s_j = (q . kcode_j) (scale ks),  P_j vs = 2^(s_j log2 e - m + log2 vs),
+//   O += (P_j vs) vcode_j,           l += (sum over a group of P_j vs) / vs.
 #include <climits>
 
 #include "pkv_device.cuh"
@@ -41,10 +42,12 @@ constexpr int kCodeTile = kKeys * kCodeRowBytes;      // 16 KiB
 constexpr int kOffCodes = kOffK + kStages * kStageBytes;  // a tile's codes of K, then of V
 constexpr int kTilesBytes = kOffCodes + 2 * kCodeTile;  // 224 KiB
 constexpr int kScaleRing = 4;                         // tiles whose scales are kept
-constexpr int kOffScales = kTilesBytes + 512;         // [4][K 8, V 8] fp32
-constexpr int kSmemBytes = kOffScales + kScaleRing * 64 + 1024;  // + alignment
+constexpr int kScaleFloats = 24;                      // of 8 groups: ks, then vs (as log2), 1 / vs
+constexpr int kOffScales = kTilesBytes + 512;
+constexpr int kSmemBytes = kOffScales + kScaleRing * kScaleFloats * 4 + 1024;  // + alignment
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KiB");
 constexpr int kThreads = 512;
+constexpr int kConvert0 = 12;                         // the first converter warp
 constexpr int kRing = 4;                              // item descriptors in flight
 constexpr int kRingUsers = 14;  // readers: softmax warps, code and MMA warps, converters
 // registers of the four warpgroups (launched with 128 each)
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar0 + kNumBars);
   volatile int* abort = reinterpret_cast<volatile int*>(bar0 + kNumBars) + 1;
   PItem* ring = reinterpret_cast<PItem*>(smem + kTilesBytes + 320);  // [kRing]
-  float* scales = reinterpret_cast<float*>(smem + kOffScales);       // [kScaleRing][K 8, V 8]
+  float* scales = reinterpret_cast<float*>(smem + kOffScales);       // [kScaleRing][kScaleFloats]
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -246,14 +249,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t smem_base = smem_addr(smem);
 
-  if (warp >= 12) {
+  if (warp >= kConvert0) {
     // ================= converters: codes -> operands =================
     // A thread takes 16 codes of rows row0, row0 + 16, ..: pass i is group i of the
     // tile.  The eight lanes of a quarter warp take four chunks of two rows, so that
     // their stores meet different banks.
     const int ct = tid - 384;
     const int row0 = (ct >> 5) * 4 + ((lane >> 4) << 1) + ((lane >> 2) & 1);
-    const int ch = (lane & 3) + (((lane >> 3) & 1) << 2);  // chunk of 16 codes
+    const int ch = (lane & 3) + (((lane >> 2) ^ (lane >> 3)) & 1) * 4;  // chunk of 16 codes
     int g = 0;  // tiles of all items
     int nread = 0;
     bool ok = true;
@@ -271,6 +274,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 c[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) c[i] = *reinterpret_cast<const uint4*>(from + i * 16 * 128);
+          if (kv == 0 && warp == kConvert0 && lane < 8) {
+            // a scale below 2^-100 is that of zeros, whose P only enters the sum
+            float* sct = scales + (g & (kScaleRing - 1)) * kScaleFloats + 8 + lane;
+            const float vs = *sct < kScaleTiny ? kScaleTiny : *sct;
+            sct[0] = log2f(vs);
+            sct[8] = 1.f / vs;
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&B.cempty[kv]);
           if (kv == 1 && left < kKeys) {  // values past the context: 0 x whatever stands there
@@ -333,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t loaded = __popc(__ballot_sync(kFull, lane < 16 && e >= 0));
         const int kpos = j * kKeys + prun * run;
         const int64_t row = e >= 0 ? cache_row(e, cur.kvh, p.Hkv, p.bs, kpos % p.bs) : 0;
-        float* sc = scales + (g & (kScaleRing - 1)) * 16 + kv * 8;
+        float* sc = scales + (g & (kScaleRing - 1)) * kScaleFloats + kv * 8;
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {  // K, then V, each when its slot is read
           if (g > 0 && !__all_sync(kFull, wait_or_abort(&B.cempty[x], (g - 1) & 1, abort, p.err))) {
@@ -652,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // general: a masked tile in this warp, or a negative scale (the maximum
         // of the scaled logits is then not the scaled maximum)
         const bool general = __any_sync(kFull, diag) || !(sc >= 0.f);
-        // the tile's scales: of 16 columns of S (with the softmax's factor), and of V
-        const float* sct = scales + ((g0 + j) & (kScaleRing - 1)) * 16;
+        // the tile's scales, of 16 columns each: ks, log2 vs, 1 / vs
+        const float* sct = scales + ((g0 + j) & (kScaleRing - 1)) * kScaleFloats;
         // pass 1: the row maximum of the scaled, masked logits
         float tmax = -INFINITY;
         if (!general) {
@@ -727,48 +737,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // pass 2: P = 2^(s * scale - m) as bf16 pairs over the columns already read
-        const float neg_m = -m_used;
+        // pass 2: P vs = 2^(s * scale - m + log2 vs) as bf16 pairs over the columns
+        // already read; the sums of P are those of a group divided by its vs
         if (!general) {
-          const uint64_t nm2 = f2_pack(__float_as_uint(neg_m), __float_as_uint(neg_m));
-          uint64_t ls2[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) ls2[u] = 0ull;  // (+0, +0)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t a[32], b[32];
             tmem_ld32(a, s_tm + 64 * h);
             tmem_ld32(b, s_tm + 64 * h + 32);
             const float4 ks4 = *reinterpret_cast<const float4*>(sct + 4 * h);
-            const float4 vs4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
+            const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
             const float ks[4] = {ks4.x * sc, ks4.y * sc, ks4.z * sc, ks4.w * sc};
-            const float vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
+            const float lv[4] = {lv4.x - m_used, lv4.y - m_used, lv4.z - m_used, lv4.w - m_used};
             tmem_wait_ld(a);
             tmem_ready(b);
             uint32_t pk[32];
+            uint64_t ls2[4];
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
               const uint32_t u0 = c < 16 ? a[2 * c] : b[2 * c - 32];
               const uint32_t u1 = c < 16 ? a[2 * c + 1] : b[2 * c - 31];
-              const uint32_t kq = __float_as_uint(ks[c >> 3]), vq = __float_as_uint(vs[c >> 3]);
+              const uint32_t kq = __float_as_uint(ks[c >> 3]), lq = __float_as_uint(lv[c >> 3]);
               float x0, x1;
-              f2_unpack(f2_fma(f2_pack(u0, u1), f2_pack(kq, kq), nm2), x0, x1);
+              f2_unpack(f2_fma(f2_pack(u0, u1), f2_pack(kq, kq), f2_pack(lq, lq)), x0, x1);
               const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
               const uint64_t e2 = f2_pack(__float_as_uint(e0), __float_as_uint(e1));
-              ls2[c & 3] = f2_add(ls2[c & 3], e2);
-              f2_unpack(f2_mul(e2, f2_pack(vq, vq)), x0, x1);
-              pk[c] = pack_bf16x2(x0, x1);
+              ls2[c >> 3] = (c & 7) == 0 ? e2 : f2_add(ls2[c >> 3], e2);
+              pk[c] = pack_bf16x2(e0, e1);
             }
             tmem_st32(s_tm + 32 * h, pk);
-          }
-          float l0, l1, l2, l3;
-          f2_unpack(f2_add(ls2[0], ls2[1]), l0, l1);
-          f2_unpack(f2_add(ls2[2], ls2[3]), l2, l3);
-          l += (l0 + l2) + (l1 + l3);
-        } else {
-          float ls[8];
+            const float4 iv4 = *reinterpret_cast<const float4*>(sct + 16 + 4 * h);
+            const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
 #pragma unroll
-          for (int u = 0; u < 8; ++u) ls[u] = 0.f;
+            for (int q = 0; q < 4; ++q) {
+              float l0, l1;
+              f2_unpack(ls2[q], l0, l1);
+              l = fmaf(l0 + l1, iv[q], l);
+            }
+          }
+        } else {
           // (not unrolled: the masked path runs once per item, and a smaller kernel
           // measured faster)
 #pragma unroll 1
@@ -785,9 +792,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(a, s_tm + 64 * h);
             tmem_ld32(b, s_tm + 64 * h + 32);
             const float4 ks4 = *reinterpret_cast<const float4*>(sct + 4 * h);
-            const float4 vs4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
+            const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
+            const float4 iv4 = *reinterpret_cast<const float4*>(sct + 16 + 4 * h);
             const float ks[4] = {ks4.x * sc, ks4.y * sc, ks4.z * sc, ks4.w * sc};
-            const float vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
+            const float lv[4] = {lv4.x - m_used, lv4.y - m_used, lv4.z - m_used, lv4.w - m_used};
+            const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
             tmem_wait_ld(a);
             tmem_ready(b);
             // keys of this half the row sees: bit c of (lo, hi) for key 64h + c
@@ -800,17 +810,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; ++c) {
               const uint32_t u0 = c < 16 ? a[2 * c] : b[2 * c - 32];
               const uint32_t u1 = c < 16 ? a[2 * c + 1] : b[2 * c - 31];
-              float e0 = fast_exp2(fmaf(__uint_as_float(u0), ks[c >> 3], neg_m));
-              float e1 = fast_exp2(fmaf(__uint_as_float(u1), ks[c >> 3], neg_m));
+              float e0 = fast_exp2(fmaf(__uint_as_float(u0), ks[c >> 3], lv[c >> 3]));
+              float e1 = fast_exp2(fmaf(__uint_as_float(u1), ks[c >> 3], lv[c >> 3]));
               const uint32_t bits = c < 16 ? lo : hi;
               e0 = (bits >> ((2 * c) & 31)) & 1u ? e0 : 0.f;
               e1 = (bits >> ((2 * c + 1) & 31)) & 1u ? e1 : 0.f;
-              ls[c & 7] += e0 + e1;
-              pk[c] = pack_bf16x2(e0 * vs[c >> 3], e1 * vs[c >> 3]);
+              ls[c >> 3] += e0 + e1;
+              pk[c] = pack_bf16x2(e0, e1);
             }
             tmem_st32(s_tm + 32 * h, pk);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) l = fmaf(ls[q], iv[q], l);
           }
-          l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
         }
         tmem_wait_st();
         tc_fence_before();

@@ -522,7 +522,8 @@ PKV_API pkv_status pkv_rope_append_q8(const int32_t *positions, const int64_t *s
  * PKV_ERR_UNSUPPORTED otherwise).  Rows at or past a context are not read into
  * the result, whatever stands there.  workspace must hold
  * pkv_q8_decode_workspace_size(num_seqs, heads, max_context) bytes (16-byte
- * aligned) when that is not 0; its contents need no initialisation.
+ * aligned) when that is not 0; its contents need no initialisation, and calls
+ * that may run at the same time need their own.
  */
 PKV_API size_t pkv_q8_decode_workspace_size(int32_t num_seqs, pkv_heads heads,
                                             int32_t max_context);
@@ -539,17 +540,25 @@ PKV_API pkv_status pkv_contig_decode_attention_q8(
 /*
  * Causal prefill attention over it: arguments, layouts, errors and checked mode
  * as for pkv_paged_prefill_attention / pkv_contig_prefill_attention.  Rows of
- * q and out behind the last chunk are left alone.
+ * q and out behind the last chunk are left alone.  Where there are few chunks
+ * their keys are dealt to all SMs and the parts joined through the workspace:
+ * it must hold pkv_q8_prefill_workspace_size(num_tokens, num_seqs, max_q_tokens,
+ * heads) bytes (32-byte aligned) when that is not 0; its contents need no
+ * initialisation, and calls that may run at the same time need their own.
  */
+PKV_API size_t pkv_q8_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs,
+                                             int32_t max_q_tokens, pkv_heads heads);
 PKV_API pkv_status pkv_paged_prefill_attention_q8(
     const void *q, const int32_t *cu_seqlens_q, int32_t num_tokens, const pkv_q8_cache *cache,
     const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t num_blocks,
     const int32_t *context_lens, int32_t num_seqs, int32_t max_q_tokens, int32_t block_size,
-    float scale, pkv_heads heads, void *out, void *stream);
+    float scale, pkv_heads heads, void *out, void *workspace, size_t workspace_bytes,
+    void *stream);
 PKV_API pkv_status pkv_contig_prefill_attention_q8(
     const void *q, const int32_t *cu_seqlens_q, int32_t num_tokens, const pkv_q8_cache *cache,
     const int32_t *req_ids, int32_t max_reqs, const int32_t *context_lens, int32_t num_seqs,
-    int32_t max_q_tokens, int64_t S, float scale, pkv_heads heads, void *out, void *stream);
+    int32_t max_q_tokens, int64_t S, float scale, pkv_heads heads, void *out, void *workspace,
+    size_t workspace_bytes, void *stream);
 
 /*
  * Copy-on-write block copy.  "Running Out of Cache" (section "Fragmentation

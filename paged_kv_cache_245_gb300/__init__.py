@@ -17,6 +17,7 @@ from .binding import (BlockManager, PkvError, VmmBuffer, block_copy, block_swap,
                       paged_decode_attention_scored, contig_decode_attention_scored,
                       paged_prefill_attention_scored, contig_prefill_attention_scored,
                       kv_append_q8, rope_append_q8, q8_decode_workspace_size,
+                      q8_prefill_workspace_size,
                       paged_decode_attention_q8, contig_decode_attention_q8,
                       paged_prefill_attention_q8, contig_prefill_attention_q8)
 
@@ -32,6 +33,7 @@ __all__ = ["BlockManager", "PkvError", "VmmBuffer", "block_copy", "block_swap", 
            "VARIANT_TC_12X2", "RopePlan", "rope_append", "scored_decode_workspace_size",
            "paged_decode_attention_scored", "contig_decode_attention_scored",
            "paged_prefill_attention_scored", "contig_prefill_attention_scored", "kv_append_q8",
-           "rope_append_q8", "q8_decode_workspace_size", "paged_decode_attention_q8",
+           "rope_append_q8", "q8_decode_workspace_size",
+           "q8_prefill_workspace_size", "paged_decode_attention_q8",
            "contig_decode_attention_q8", "paged_prefill_attention_q8",
            "contig_prefill_attention_q8"]

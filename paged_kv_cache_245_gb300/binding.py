@@ -40,6 +40,7 @@ EXPORTED = ("pkv_kv_append", "pkv_decode_num_splits", "pkv_decode_uses_tensor_co
             "pkv_contig_prefill_attention_scored",
             "pkv_kv_append_q8", "pkv_rope_append_q8", "pkv_q8_decode_workspace_size",
             "pkv_paged_decode_attention_q8", "pkv_contig_decode_attention_q8",
+            "pkv_q8_prefill_workspace_size",
             "pkv_paged_prefill_attention_q8", "pkv_contig_prefill_attention_q8",
             "pkv_get_device_error", "pkv_status_string", "pkv_last_error")
 
@@ -148,10 +149,12 @@ def lib():
                                                 ctypes.c_float, Heads, vp, vp, sz, vp]
     L.pkv_contig_decode_attention_q8.argtypes = [vp, qp, vp, i32, vp, i32, i32, i64,
                                                  ctypes.c_float, Heads, vp, vp, sz, vp]
+    L.pkv_q8_prefill_workspace_size.argtypes = [i32, i32, i32, Heads]
+    L.pkv_q8_prefill_workspace_size.restype = sz
     L.pkv_paged_prefill_attention_q8.argtypes = [vp, vp, i32, qp, vp, i32, i32, vp, i32, i32, i32,
-                                                 ctypes.c_float, Heads, vp, vp]
+                                                 ctypes.c_float, Heads, vp, vp, sz, vp]
     L.pkv_contig_prefill_attention_q8.argtypes = [vp, vp, i32, qp, vp, i32, vp, i32, i32, i64,
-                                                  ctypes.c_float, Heads, vp, vp]
+                                                  ctypes.c_float, Heads, vp, vp, sz, vp]
     L.pkv_set_checked.argtypes = [ctypes.c_int]
     L.pkv_set_checked.restype = None
     L.pkv_get_checked.restype = ctypes.c_int
@@ -871,21 +874,28 @@ def _attention_q8(contig, q, k, v, k_scale, v_scale, where, context_lens, out):
     return dev, B, cache, shape, Heads(hq, shape[1], d), out
 
 
+def _workspace_q8(workspace, q, dev, size_of, *args):
+    """(Pointer, bytes, the tensor that holds them): the caller's workspace, or one of
+    this call's own (the C ABI itself never allocates)."""
+    if workspace is None:
+        size = size_of(*args)
+        if not size:
+            return 0, 0, None
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev \
+            or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
 def _decode_q8(contig, q, k, v, k_scale, v_scale, where, context_lens, max_context, scale, out,
                workspace):
     dev, B, cache, (n, _, rows, _), h, out = _attention_q8(contig, q, k, v, k_scale, v_scale,
                                                            where, context_lens, out)
     if q.shape[0] != B:
         raise ValueError("q must have one row per sequence")
-    ws, ws_len = 0, 0
-    if workspace is None:
-        size = lib().pkv_q8_decode_workspace_size(B, h, max_context)
-        if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on q's device")
-    if workspace is not None:
-        ws, ws_len = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    ws, ws_len, workspace = _workspace_q8(
+        workspace, q, dev, lib().pkv_q8_decode_workspace_size, B, h, max_context)
     if contig:
         _on_device(dev, lib().pkv_contig_decode_attention_q8, q.data_ptr(), cache,
                    where.data_ptr(), n, context_lens.data_ptr(), B, max_context, rows, scale, h,
@@ -911,36 +921,47 @@ def contig_decode_attention_q8(q, k_buf, v_buf, k_scale, v_scale, req_ids, conte
                       scale, out, workspace)
 
 
+def q8_prefill_workspace_size(num_tokens, num_seqs, max_q_tokens, num_q_heads, num_kv_heads,
+                              head_dim=128):
+    """Bytes of workspace that prefill attention over an 8-bit cache needs."""
+    return int(lib().pkv_q8_prefill_workspace_size(
+        num_tokens, num_seqs, max_q_tokens, heads(num_q_heads, num_kv_heads, head_dim)))
+
+
 def _prefill_q8(contig, q, cu_seqlens_q, k, v, k_scale, v_scale, where, context_lens,
-                max_q_tokens, scale, out):
+                max_q_tokens, scale, out, workspace):
     dev, B, cache, (n, _, rows, _), h, out = _attention_q8(contig, q, k, v, k_scale, v_scale,
                                                            where, context_lens, out)
     _check_in(cu_seqlens_q, torch.int32, 1, dev, "cu_seqlens_q")
     if cu_seqlens_q.numel() != B + 1:
         raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
+    ws, ws_len, workspace = _workspace_q8(
+        workspace, q, dev, lib().pkv_q8_prefill_workspace_size, q.shape[0], B, max_q_tokens, h)
     if contig:
         _on_device(dev, lib().pkv_contig_prefill_attention_q8, q.data_ptr(),
                    cu_seqlens_q.data_ptr(), q.shape[0], cache, where.data_ptr(), n,
-                   context_lens.data_ptr(), B, max_q_tokens, rows, scale, h, out.data_ptr())
+                   context_lens.data_ptr(), B, max_q_tokens, rows, scale, h, out.data_ptr(), ws,
+                   ws_len)
     else:
         _on_device(dev, lib().pkv_paged_prefill_attention_q8, q.data_ptr(),
                    cu_seqlens_q.data_ptr(), q.shape[0], cache, where.data_ptr(), where.shape[1],
-                   n, context_lens.data_ptr(), B, max_q_tokens, rows, scale, h, out.data_ptr())
+                   n, context_lens.data_ptr(), B, max_q_tokens, rows, scale, h, out.data_ptr(),
+                   ws, ws_len)
     return out
 
 
 def paged_prefill_attention_q8(q, cu_seqlens_q, k_cache, v_cache, k_scale, v_scale, block_tables,
-                               context_lens, max_q_tokens, scale, out=None):
+                               context_lens, max_q_tokens, scale, out=None, workspace=None):
     """paged_prefill_attention over an 8-bit cache (kv_append_q8)."""
     return _prefill_q8(False, q, cu_seqlens_q, k_cache, v_cache, k_scale, v_scale, block_tables,
-                       context_lens, max_q_tokens, scale, out)
+                       context_lens, max_q_tokens, scale, out, workspace)
 
 
 def contig_prefill_attention_q8(q, cu_seqlens_q, k_buf, v_buf, k_scale, v_scale, req_ids,
-                                context_lens, max_q_tokens, scale, out=None):
+                                context_lens, max_q_tokens, scale, out=None, workspace=None):
     """contig_prefill_attention over an 8-bit cache [max_reqs, Hkv, S, D]."""
     return _prefill_q8(True, q, cu_seqlens_q, k_buf, v_buf, k_scale, v_scale, req_ids,
-                       context_lens, max_q_tokens, scale, out)
+                       context_lens, max_q_tokens, scale, out, workspace)
 
 
 def debug_gather_paged(cache, block_tables, context_lens, max_context):

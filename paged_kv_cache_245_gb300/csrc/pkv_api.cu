@@ -1542,9 +1542,17 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
     if (ts != pkv::TcStatus::kOk) return cuda_fail(ce, "q8 decode launch");
     return PKV_OK;
   }
+  const size_t need =
+      pkv::prefill_q8_workspace(num_tokens, num_seqs, p.max_q, h.num_kv_heads, p.G, sms);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
+                  workspace ? workspace_bytes : size_t{0});
+    if (!aligned(workspace, 32)) return fail(PKV_ERR_WORKSPACE, "workspace must be 32-byte aligned");
+  }
   cudaError_t ce = cudaSuccess;
   const pkv::TcStatus ts =
-      pkv::launch_prefill_q8(p, cache->format == PKV_Q8_E4M3, contig, num_tokens, sms,
+      pkv::launch_prefill_q8(p, cache->format == PKV_Q8_E4M3, contig, num_tokens, sms, workspace,
                              static_cast<cudaStream_t>(stream), &ce);
   if (ts == pkv::TcStatus::kEncodeFailed)
     return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for q");
@@ -1609,25 +1617,37 @@ pkv_status pkv_contig_decode_attention_q8(
                              workspace_bytes, stream);
 }
 
+size_t pkv_q8_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t max_q_tokens,
+                                     pkv_heads heads) {
+  int sms = 0;
+  if (check_heads(heads) != PKV_OK || num_tokens <= 0 || num_seqs <= 0 || max_q_tokens <= 0 ||
+      device_info(nullptr, nullptr, &sms) != PKV_OK)
+    return 0;
+  return pkv::prefill_q8_workspace(num_tokens, num_seqs, max_q_tokens, heads.num_kv_heads,
+                                   heads.num_q_heads / heads.num_kv_heads, sms);
+}
+
 pkv_status pkv_paged_prefill_attention_q8(
     const void* q, const int32_t* cu_seqlens_q, int32_t num_tokens, const pkv_q8_cache* cache,
     const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t num_blocks,
     const int32_t* context_lens, int32_t num_seqs, int32_t max_q_tokens, int32_t block_size,
-    float scale, pkv_heads heads, void* out, void* stream) {
+    float scale, pkv_heads heads, void* out, void* workspace, size_t workspace_bytes,
+    void* stream) {
   if (num_seqs > 0 && !cu_seqlens_q) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
   return attention_q8_common(q, cu_seqlens_q, num_tokens, cache, false, block_tables,
                              max_blocks_per_seq, num_blocks, context_lens, num_seqs, max_q_tokens,
-                             0, block_size, scale, heads, out, nullptr, 0, stream);
+                             0, block_size, scale, heads, out, workspace, workspace_bytes, stream);
 }
 
 pkv_status pkv_contig_prefill_attention_q8(
     const void* q, const int32_t* cu_seqlens_q, int32_t num_tokens, const pkv_q8_cache* cache,
     const int32_t* req_ids, int32_t max_reqs, const int32_t* context_lens, int32_t num_seqs,
-    int32_t max_q_tokens, int64_t S, float scale, pkv_heads heads, void* out, void* stream) {
+    int32_t max_q_tokens, int64_t S, float scale, pkv_heads heads, void* out, void* workspace,
+    size_t workspace_bytes, void* stream) {
   if (num_seqs > 0 && !cu_seqlens_q) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
   return attention_q8_common(q, cu_seqlens_q, num_tokens, cache, true, req_ids, 1, max_reqs,
-                             context_lens, num_seqs, max_q_tokens, 0, S, scale, heads, out, nullptr,
-                             0, stream);
+                             context_lens, num_seqs, max_q_tokens, 0, S, scale, heads, out,
+                             workspace, workspace_bytes, stream);
 }
 
 pkv_status pkv_block_copy(const int64_t* src_dst_pairs, int64_t n, void* const* k_caches,

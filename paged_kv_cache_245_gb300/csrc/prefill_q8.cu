@@ -1,17 +1,17 @@
 // prefill_q8.cu -- causal prefill attention over the 8-bit KV cache (q8.cuh) on the
 // fifth-generation tensor cores.
 //
-// Work items, roles, tensor memory and the order of products are those of the
-// plain kernel (prefill.cu): two row tiles of 128 (token, query head) rows of one
-// KV head and sequence, key tiles of 128 positions, S_t and O_t in tensor memory.
-// What is added is a warpgroup that turns codes into operands:
+// Work items, tensor memory and the order of products are those of the plain
+// kernel (prefill.cu): two row tiles of 128 (token, query head) rows of one KV head
+// and sequence, key tiles of 128 positions, S_t and O_t in tensor memory.  What is
+// added turns codes into operands:
 //
 //   warps 0-3    softmax and output of row tile 0   warps 4-7  of row tile 1
-//   warp 8       codes of K and V (16 KiB a tile each) by bulk copies into one
-//                slot each, and the tile's 16 scales by cp.async
-//   warp 9       tensor-memory owner and MMA issuer (one thread)
-//   warp 10      the item list and the Q rows
-//   warps 12-15  codes -> bf16 into the two stages of K and V operands
+//   warp 8       tensor-memory owner and MMA issuer
+//   warp 9       the item list and the Q rows
+//   warp 10      codes of K and V (16 KiB a tile each) by bulk copies into one slot
+//                each, and the tile's 16 scales by cp.async
+//   warps 11-14  codes -> bf16 into the two stages of K and V operands
 //
 // The operands hold the codes themselves, which bf16 holds exactly (int8 and e4m3
 // have at most 8 significant bits): a key's scale is uniform over 16 columns of S
@@ -20,6 +20,13 @@
 // too, and bf16's range holds any scale.  With ks, vs the scales of key j's group:
 //   s_j = (q . kcode_j) (scale ks),  P_j vs = 2^(s_j log2 e - m + log2 vs),
 //   O += (P_j vs) vcode_j,           l += (sum over a group of P_j vs) / vs.
+//
+// Schedule.  Many items: dealt to the CTAs (one an SM) in rounds of alternating
+// direction, latest rows first.  Few items (a host bound of kSplitItems an SM): the
+// flattened list of all items' key tiles is cut evenly over the CTAs, an item
+// counting as kItemCost tiles more; an item that is cut leaves its pieces' (O, m, l)
+// in the workspace, and a second kernel joins them:
+//   O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.
 #include <climits>
 
 #include "pkv_device.cuh"
@@ -35,29 +42,41 @@ using namespace umma;
 namespace {
 
 constexpr int kStages = 2;
-constexpr int kQSlots = 2;                            // Q tiles in rotation (a third measured slower)
+constexpr int kQSlots = 2;                            // Q tiles in rotation
 constexpr int kOffK = kQSlots * kOpBytes;             // after the Q slots
 constexpr int kStageBytes = 2 * kOpBytes;             // K then V
 constexpr int kCodeTile = kKeys * kCodeRowBytes;      // 16 KiB
 constexpr int kOffCodes = kOffK + kStages * kStageBytes;  // a tile's codes of K, then of V
 constexpr int kTilesBytes = kOffCodes + 2 * kCodeTile;  // 224 KiB
 constexpr int kScaleRing = 4;                         // tiles whose scales are kept
-constexpr int kScaleFloats = 24;                      // of 8 groups: ks, then vs (as log2), 1 / vs
+constexpr int kScaleFloats = 24;                      // of 8 groups: ks, log2 vs, 1 / vs
 constexpr int kOffScales = kTilesBytes + 512;
 constexpr int kSmemBytes = kOffScales + kScaleRing * kScaleFloats * 4 + 1024;  // + alignment
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KiB");
-constexpr int kThreads = 512;
-constexpr int kConvert0 = 12;                         // the first converter warp
+constexpr int kProducer = 10;                         // the code producer
+constexpr int kConvert0 = 11, kConverters = 4;        // converter warps
+constexpr int kThreads = 32 * (kConvert0 + kConverters);
+static_assert(kProducer == 10 && kConvert0 == 11, "every warp has a role: 0-7 are the softmax's, 8 and 9 the next two");
 constexpr int kRing = 4;                              // item descriptors in flight
-constexpr int kRingUsers = 14;  // readers: softmax warps, code and MMA warps, converters
-// registers of the four warpgroups (launched with 128 each)
-constexpr int kRegsSoftmax = 168, kRegsRoles = 80, kRegsConvert = 96;
-static_assert(2 * kRegsSoftmax + kRegsRoles + kRegsConvert <= 4 * 128, "the launch's registers");
+constexpr int kRingUsers = 10 + kConverters;  // readers: softmax, MMA, producer, converters
+constexpr int kSplitItems = 8;               // items an SM up to which they are cut
+constexpr int kSplitPairs = 1024;            // (sequence, row tiles) pairs up to which they are
+constexpr int kItemCost = 2;                 // what an item costs, in key tiles
+constexpr int kLeastUnits = 6;               // a CTA's share is at least this
+constexpr int kPieceRow = 136;               // floats of a piece's row: o[128], m, l
 
-// One work item as the scheduling warp (10) publishes it; ntiles == 0 ends
-// the list.
+// One work item, or a piece of one, as the item warp publishes it: key tiles t0 ..
+// t0 + ntiles - 1 (ntiles 0 ends the list); part: the record that its sums go to, or
+// -1 (the whole item).
 struct PItem {
-  int32_t seq, kvh, row0, rows, base, ntiles, q0, ctx;
+  int32_t seq, kvh, row0, rows, base, ntiles, q0, ctx, t0, part;
+};
+
+// What a CTA leaves for the join: the item whose first tiles are its last (rows 0:
+// none), and whether its first tiles continue an earlier CTA's item (1), and end it
+// (2).
+struct PieceDesc {
+  int32_t q0, kvh, row0, rows, continues, pad[3];
 };
 
 // A Q tile's slot in the rotation and the phase of that slot's barriers.
@@ -76,16 +95,16 @@ struct QCursor {
 
 // The mbarriers after the tiles.
 struct PBars {
-  uint64_t* cfull;      // [2] a tile's codes and scales of K, of V landed
+  uint64_t* cfull;      // [2] a tile's codes and scales of K, its codes of V landed
   uint64_t* cempty;     // [2] the converters hold them in registers
-  uint64_t* kfull;      // [2] K of a stage written (every converter thread arrives)
+  uint64_t* kfull;      // [2] K of a stage written (one arrival per converter warp)
   uint64_t* vfull;      // [2] V of a stage written
   uint64_t* kempty;     // [2] both S products reading a stage's K completed
   uint64_t* vempty;     // [2] both P V products reading a stage's V completed
   uint64_t* sfull;      // [2] S_t of the next key tile (and PV_t before it) done
   uint64_t* pfull;      // [2] P_t written (one arrival per warp)
   uint64_t* ofull;      // [2] an item's last PV_t completed
-  uint64_t* qfull;      // [2] a Q slot written (every lane of warp 10 arrives)
+  uint64_t* qfull;      // [2] a Q slot written (every lane of the item warp arrives)
   uint64_t* qempty;     // [2] the last S product reading a Q slot completed
   uint64_t* ifull;      // [4] an item descriptor published
   uint64_t* iempty;     // [4] every reader took its copy
@@ -148,6 +167,9 @@ struct PrefillQ8Params : PrefillParams {
   const uint8_t* v_codes;
   const float* k_scale;
   const float* v_scale;
+  PieceDesc* desc;      // [CTAs] and
+  float* rec;           // [CTAs][2][rec_rows][kPieceRow]: items are cut; null: they are not
+  int32_t rec_rows;     // rows of an item at most
 };
 
 template <bool kE4m3>
@@ -202,14 +224,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  // Setup: barriers (warp 8) and the tensor memory (warp 9).
-  if (warp == 8) {
+  // Setup: barriers, the Q slots' padding, the tensor memory.
+  if (warp == kProducer) {
     if (lane == 0) {
       for (int s = 0; s < 2; ++s) {
-        mbar_init(&B.kfull[s], 128);  // the converters' threads
-        mbar_init(&B.vfull[s], 128);
         mbar_init(&B.cfull[s], s == 0 ? 1 + 32 : 1);  // the copies; K: and the lanes' scales
-        mbar_init(&B.cempty[s], 4);      // the converters' warps
+        mbar_init(&B.cempty[s], kConverters);
+        mbar_init(&B.kfull[s], kConverters);
+        mbar_init(&B.vfull[s], kConverters);
         mbar_init(&B.kempty[s], 1);
         mbar_init(&B.vempty[s], 1);
         mbar_init(&B.sfull[s], 1);
@@ -217,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&B.ofull[s], 1);
       }
       for (int s = 0; s < kQSlots; ++s) {
-        mbar_init(&B.qfull[s], 32);  // every lane of the Q warp
+        mbar_init(&B.qfull[s], 32);  // every lane of the item warp
         mbar_init(&B.qempty[s], 1);
       }
       for (int s = 0; s < kRing; ++s) {
@@ -229,14 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_barrier_init();
       prefetch_tensormap(&tmq);
     }
-  } else if (warp == 10 && TR < kRowTile) {
+  } else if (warp == 9 && TR < kRowTile) {
     // rows TR .. 127 of every Q slot are padding that no copy writes: zero
     for (int slot = 0; slot < kQSlots; ++slot)
       for (int x = lane; x < (kRowTile - TR) * 16; x += 32)
         *reinterpret_cast<uint4*>(smem + q_off(slot) + q_chunk_offset(TR + (x >> 4), x & 15)) =
             make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
-  } else if (warp == 9) {
+  } else if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tmem_slot)),
                  "r"(kTmemCols)
@@ -251,11 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kConvert0) {
     // ================= converters: codes -> operands =================
-    // A thread takes 16 codes of rows row0, row0 + 16, ..: pass i is group i of the
-    // tile.  The eight lanes of a quarter warp take four chunks of two rows, so that
-    // their stores meet different banks.
-    const int ct = tid - 384;
-    const int row0 = (ct >> 5) * 4 + ((lane >> 4) << 1) + ((lane >> 2) & 1);
+    // A thread takes 16 codes of rows row0, row0 + 16, ..  The eight lanes of a quarter
+    // warp take chunks 0-3 of one row and 4-7 of the next (or the other way), whose
+    // loads and swizzled stores meet different banks.
+    const int row0 = (warp - kConvert0) * 4 + ((lane >> 4) << 1) + ((lane >> 2) & 1);
     const int ch = (lane & 3) + (((lane >> 2) ^ (lane >> 3)) & 1) * 4;  // chunk of 16 codes
     int g = 0;  // tiles of all items
     int nread = 0;
@@ -265,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!read_item(nread++, it) || it.ntiles == 0) break;
       for (int j = 0; j < it.ntiles && ok; ++j, ++g) {
         const int s = g & 1;
-        const int left = it.ctx - j * kKeys;  // rows of the tile that hold positions
+        const int left = it.ctx - (it.t0 + j) * kKeys;  // rows of the tile that hold positions
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {  // K, then V
           ok = __all_sync(kFull, wait_or_abort(&B.cfull[kv], g & 1, abort, p.err));
@@ -274,6 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 c[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) c[i] = *reinterpret_cast<const uint4*>(from + i * 16 * 128);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.cempty[kv]);
           if (kv == 0 && warp == kConvert0 && lane < 8) {
             // a scale below 2^-100 is that of zeros, whose P only enters the sum
             float* sct = scales + (g & (kScaleRing - 1)) * kScaleFloats + 8 + lane;
@@ -281,8 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             sct[0] = log2f(vs);
             sct[8] = 1.f / vs;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&B.cempty[kv]);
           if (kv == 1 && left < kKeys) {  // values past the context: 0 x whatever stands there
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -304,12 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(to + kv_chunk_offset(r, 2 * ch + 1)) = hi;
           }
           fence_proxy_async_smem();  // the products read them through the async proxy
-          mbar_arrive(kv == 0 ? &B.kfull[s] : &B.vfull[s]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv == 0 ? &B.kfull[s] : &B.vfull[s]);
         }
       }
     }
-  } else if (warp >= 8) {
-  if (warp == 8) {
+  } else if (warp == kProducer) {
     // ================= code producer =================
     // Every row tile of a sequence and KV head reads the same tiles: keep them in
     // L2 for the items after.
@@ -318,16 +339,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int runs = kKeys / run;  // copies per tile and tensor (<= 8)
     const int prun = lane & 15;    // lanes 0-15 copy K of run prun, lanes 16-31 V
     const int kv = lane >> 4;
-    // block-table entry of run prun of tile j of `it` (-1: past the context or rejected)
-    auto entry = [&](const PItem& it, int j) -> int32_t {
-      const int kpos = j * kKeys + prun * run;
+    const uint32_t bs = static_cast<uint32_t>(p.bs);
+    // block-table entry of run prun of tile j of `it` (-1: past the context or
+    // rejected); *off: its first row's place in the block
+    auto entry = [&](const PItem& it, int j, uint32_t* off) -> int32_t {
+      const int kpos = (it.t0 + j) * kKeys + prun * run;
       int32_t e = -1;
       if (prun < runs && kpos < it.ctx) {
-        e = p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks + kpos / p.bs];
-        if (p.checked && (e < 0 || e >= p.num_blocks)) {
-          record_error(p.err, p.err_code);
-          e = -1;  // skip the copy: stale rows, undefined output, no fault
-        }
+        const uint32_t at = static_cast<uint32_t>(kpos) / bs;
+        *off = static_cast<uint32_t>(kpos) - at * bs;
+        e = p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks + at];
       }
       return e;
     };
@@ -336,13 +357,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int nread = 0;
     PItem cur;
     bool ok = read_item(nread++, cur);
-    int32_t e = ok && cur.ntiles > 0 ? entry(cur, 0) : -1;  // entries of the next tile
+    uint32_t off = 0;
+    int32_t e = ok && cur.ntiles > 0 ? entry(cur, 0, &off) : -1;  // of the next tile
     while (ok && cur.ntiles > 0) {
       PItem nx = cur;
       for (int j = 0; j < cur.ntiles; ++j) {
+        if (p.checked && e >= p.num_blocks) e = -1;  // (and below 0:) skip the copy: stale
+        const int kpos = (cur.t0 + j) * kKeys + prun * run;  // rows, undefined output, no fault
+        if (p.checked && e < 0 && prun < runs && kpos < cur.ctx) record_error(p.err, p.err_code);
         const uint32_t loaded = __popc(__ballot_sync(kFull, lane < 16 && e >= 0));
-        const int kpos = j * kKeys + prun * run;
-        const int64_t row = e >= 0 ? cache_row(e, cur.kvh, p.Hkv, p.bs, kpos % p.bs) : 0;
+        const int64_t row = e >= 0 ? cache_row(e, cur.kvh, p.Hkv, bs, off) : 0;
         float* sc = scales + (g & (kScaleRing - 1)) * kScaleFloats + kv * 8;
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {  // K, then V, each when its slot is read
@@ -378,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++g;
         // the next tile's entries load while this one lands
         if (j + 1 < cur.ntiles) {
-          e = entry(cur, j + 1);
+          e = entry(cur, j + 1, &off);
         } else {
           ok = read_item(nread++, nx);
-          e = ok && nx.ntiles > 0 ? entry(nx, 0) : -1;
+          e = ok && nx.ntiles > 0 ? entry(nx, 0, &off) : -1;
         }
       }
       cur = nx;
@@ -394,17 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (half) mbar_wait_bounded(&B.cfull[0], g & 1);
     }
-  } else if (warp == 10) {
+  } else if (warp == 9) {
     // ================= item list and Q rows =================
-    // Items in order of index: row tile rt (latest first), then sequence,
-    // then KV head.  Round k deals items k P .. k P + P - 1 to the P CTAs,
-    // forwards in even rounds and backwards in odd ones.  Q tile n (row tile
-    // 0 of an item, then row tile 1 if it has rows) goes to slot n % 2 once
-    // the last S product reading tile n - 2 completed.
+    // Q tile n (row tile 0 of an item, then row tile 1 if it has rows) goes to slot
+    // n % 2 once the last S product reading tile n - 2 completed.
     const int P = gridDim.x;
     const int R = (p.max_q * G + 2 * TR - 1) / (2 * TR);
-    const int per = p.num_seqs * p.Hkv;
-    const int total = R * per;
     const uint64_t qpolicy = l2_policy_evict_first();  // every Q row is read once
     int published = 0;
     uint32_t nq = 0;      // Q tiles loaded
@@ -425,44 +444,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++published;
       return true;
     };
-    for (int k = 0; ok && k * P < total; ++k) {
-      const int idx = k * P + ((k & 1) ? P - 1 - static_cast<int>(blockIdx.x) : blockIdx.x);
-      if (idx >= total) continue;
-      const int rt = R - 1 - idx / per;
-      const int rem = idx - (idx / per) * per;
-      PItem it;
-      it.seq = rem / p.Hkv;
-      it.kvh = rem - it.seq * p.Hkv;
-      it.q0 = p.cu_q[it.seq];
-      const int Lq = p.cu_q[it.seq + 1] - it.q0;
-      it.ctx = p.ctx_lens[it.seq];
-      if (p.checked) {
-        const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.bs;
-        if (Lq < 0 || Lq > p.max_q || it.ctx < Lq || it.ctx > cap) {
-          if (lane == 0 && rt == 0 && it.kvh == 0) record_error(p.err, kErrContext);
-          continue;  // the sequence is left unwritten
-        }
-      }
-      it.rows = Lq * G;
-      it.row0 = rt * 2 * TR;
-      if (it.row0 >= it.rows) continue;  // this item's rows lie past the chunk
-      it.base = it.ctx - Lq;             // position of the chunk's first token
-      const int last_row = min(it.row0 + 2 * TR, it.rows) - 1;
-      const int kend = it.base + last_row / G + 1;  // keys the item needs
-      if (kend <= 0) continue;  // only when ctx < Lq (caught in checked mode)
-      it.ntiles = (kend + kKeys - 1) / kKeys;
-      if (!publish(it)) {
-        ok = false;
-        break;
-      }
+    // Publishes an item and brings its Q rows; false when a wait gave up.
+    auto serve = [&](const PItem& it) -> bool {
+      if (!publish(it)) return false;
       const int nt = it.rows > it.row0 + TR ? 2 : 1;
       for (int t = 0; t < nt; ++t, ++nq, qc = qc.next(kQSlots)) {
         const int qs = qc.slot;
         if (nq >= static_cast<uint32_t>(kQSlots) &&
-            !__all_sync(kFull, wait_or_abort(&B.qempty[qs], qc.phase ^ 1u, abort, p.err))) {
-          ok = false;
-          break;
-        }
+            !__all_sync(kFull, wait_or_abort(&B.qempty[qs], qc.phase ^ 1u, abort, p.err)))
+          return false;
         last_phase = (last_phase & ~(1u << qs)) | (qc.phase << qs);
         unsigned char* dst = smem + q_off(qs);
         // the tile is TR / G whole tokens, each column half one box of
@@ -478,6 +468,140 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&B.qfull[qs]);
         }
       }
+      return true;
+    };
+    // Row tiles rt of a sequence (any KV head); false if there are none.
+    auto describe = [&](int rt, int seq, bool report, PItem& it) -> bool {
+      it.seq = seq;
+      it.kvh = 0;
+      it.t0 = 0;
+      it.part = -1;
+      it.q0 = p.cu_q[seq];
+      const int Lq = p.cu_q[seq + 1] - it.q0;
+      it.ctx = p.ctx_lens[seq];
+      if (p.checked) {
+        const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.bs;
+        if (Lq < 0 || Lq > p.max_q || it.ctx < Lq || it.ctx > cap) {
+          if (report) record_error(p.err, kErrContext);
+          return false;  // the sequence is left unwritten
+        }
+      }
+      it.rows = Lq * G;
+      it.row0 = rt * 2 * TR;
+      if (it.row0 >= it.rows) return false;  // past the chunk
+      it.base = it.ctx - Lq;                 // position of the chunk's first token
+      const int last_row = min(it.row0 + 2 * TR, it.rows) - 1;
+      const int kend = it.base + last_row / G + 1;  // keys the item needs
+      it.ntiles = (kend + kKeys - 1) / kKeys;
+      return kend > 0;  // (not only when ctx < Lq, caught in checked mode)
+    };
+    // the item of lane src
+    auto of_lane = [&](const PItem& mine, int src) -> PItem {
+      PItem it;
+      it.seq = __shfl_sync(kFull, mine.seq, src);
+      it.kvh = __shfl_sync(kFull, mine.kvh, src);
+      it.row0 = __shfl_sync(kFull, mine.row0, src);
+      it.rows = __shfl_sync(kFull, mine.rows, src);
+      it.base = __shfl_sync(kFull, mine.base, src);
+      it.ntiles = __shfl_sync(kFull, mine.ntiles, src);
+      it.q0 = __shfl_sync(kFull, mine.q0, src);
+      it.ctx = __shfl_sync(kFull, mine.ctx, src);
+      it.t0 = 0;
+      it.part = -1;
+      return it;
+    };
+    if (p.rec != nullptr) {
+      // Pairs c = (sequence c / R, row tiles c % R) in order, 32 at a time, one a
+      // lane; a pair's items (its KV heads) of kItemCost + ntiles units each.  A CTA's
+      // units [u0, u1) hold a run of key tiles; those of an item that it has not
+      // whole are a piece.
+      const int pairs = R * p.num_seqs;
+      auto pair_of_lane = [&](int c0, bool report, PItem& it) -> int64_t {
+        const int c = c0 + lane;
+        it = PItem{};
+        if (c >= pairs || !describe(c % R, c / R, report && c % R == 0, it)) return 0;
+        return static_cast<int64_t>(p.Hkv) * (kItemCost + it.ntiles);
+      };
+      PItem mine;
+      int64_t V = 0;
+      for (int c0 = 0; c0 < pairs; c0 += 32) {
+        int64_t units = pair_of_lane(c0, blockIdx.x == 0, mine);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(kFull, units, o);
+        V += units;
+      }
+      const int64_t shares = max(static_cast<int64_t>(1), min(static_cast<int64_t>(P), V / kLeastUnits));
+      const int64_t me = blockIdx.x;
+      const int64_t u0 = me < shares ? me * V / shares : V;
+      const int64_t u1 = me < shares ? (me + 1) * V / shares : V;
+      PieceDesc desc = {};
+      int64_t at = 0;
+      for (int c0 = 0; ok && c0 < pairs && at < u1; c0 += 32) {
+        const int64_t units = pair_of_lane(c0, false, mine);
+        int64_t end = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(kFull, end, o);
+          if (lane >= o) end += v;
+        }
+        const int64_t begin = at + end - units;
+        for (uint32_t hit = __ballot_sync(kFull, units > 0 && begin < u1 && begin + units > u0);
+             ok && hit != 0u; hit &= hit - 1) {
+          const int src = __ffs(hit) - 1;
+          PItem it = of_lane(mine, src);
+          const int64_t b = __shfl_sync(kFull, begin, src);
+          const int n = it.ntiles, span = kItemCost + n;
+          for (int h = u0 > b ? static_cast<int>((u0 - b) / span) : 0; ok && h < p.Hkv; ++h) {
+            const int64_t first = b + static_cast<int64_t>(h) * span + kItemCost;  // unit of tile 0
+            if (first >= u1) break;
+            const int from = u0 > first ? static_cast<int>(u0 - first) : 0;
+            const int to = u1 - first < n ? static_cast<int>(u1 - first) : n;
+            if (from >= to) continue;
+            it.kvh = h;
+            it.t0 = from;
+            it.ntiles = to - from;
+            it.part = -1;
+            if (to - from < n) {
+              it.part = 2 * blockIdx.x + (from == 0 ? 1 : 0);
+              if (from == 0) {
+                desc.q0 = it.q0;
+                desc.kvh = h;
+                desc.row0 = it.row0;
+                desc.rows = min(it.rows - it.row0, 2 * TR);
+              } else {
+                desc.continues = to == n ? 2 : 1;
+              }
+            }
+            ok = serve(it);
+          }
+        }
+        at += __shfl_sync(kFull, end, 31);
+      }
+      if (lane == 0) p.desc[blockIdx.x] = desc;
+    } else {
+      // Items in order of index: row tile (latest first), then sequence, then KV head.
+      // Round k deals items k P .. k P + P - 1 to the P CTAs, forwards in even rounds and
+      // backwards in odd ones; 32 rounds at a time, one a lane, so that items whose rows
+      // lie past their chunk cost one latency.
+      const int per = p.num_seqs * p.Hkv;
+      const int total = R * per;
+      for (int64_t k0 = 0; ok && k0 * P < total; k0 += 32) {
+        const int64_t k = k0 + lane;
+        const int64_t slot = k * P + ((k & 1) ? P - 1 - static_cast<int>(blockIdx.x)
+                                              : static_cast<int>(blockIdx.x));
+        PItem mine = {};
+        bool there = slot < total;
+        if (there) {
+          const int idx = static_cast<int>(slot);
+          const int rt = R - 1 - idx / per;
+          const int rem = idx - (idx / per) * per;
+          const int seq = rem / p.Hkv;
+          there = describe(rt, seq, rt == 0 && rem == seq * p.Hkv, mine);
+          mine.kvh = rem - seq * p.Hkv;
+        }
+        for (uint32_t left = __ballot_sync(kFull, there); ok && left != 0u; left &= left - 1)
+          ok = serve(of_lane(mine, __ffs(left) - 1));
+      }
     }
     if (ok) {
       PItem end = {};  // ntiles 0: the end of this CTA's list
@@ -488,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int qs = 0; qs < kQSlots && static_cast<uint32_t>(qs) < nq; ++qs)
         mbar_wait_bounded(&B.qfull[qs], (last_phase >> qs) & 1u);
     }
-  } else if (warp == 9) {
+  } else if (warp == 8) {
     // ================= MMA issuer =================
     // The whole warp walks the tiles on warp-uniform values, so that descriptors stay
     // in uniform registers; one elected lane issues.
@@ -625,7 +749,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(B.drain, 0);
     }
     __syncwarp();
-  }
   } else {
     // ================= softmax warpgroups (warps 0-7) =================
     const int t = warp >> 2;                      // row tile
@@ -657,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
         if (!ok) break;
         tc_fence_after();
-        const int k0 = j * kKeys;
+        const int k0 = (it.t0 + j) * kKeys;
         const bool diag = k0 + kKeys - 1 > pos;  // some key of the tile lies past the row
         // general: a masked tile in this warp, or a negative scale (the maximum
         // of the scaled logits is then not the scaled maximum)
@@ -717,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float m_new = fmaxf(m_used, tmax);
         if (j == 0) {
-          m_used = m_new;  // finite: position 0 is visible to every row
+          m_used = m_new;  // finite, but in a piece that the row sees nothing of
         } else {
           const bool grow = m_new > m_used + kRescaleLog2;
           if (__any_sync(kFull, grow)) {
@@ -832,11 +955,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(kFull, wait_or_abort(&B.ofull[t], no & 1, abort, p.err));
       ++no;
       if (!ok) break;
-      // the item's output rows; the next item's first P V product overwrites
-      // O_t only after these warps hand over its first P
+      // the item's output rows, or a piece's sums; the next item's first P V product
+      // overwrites O_t only after these warps hand over its first P
       tc_fence_after();
-      const float inv = l != 0.f ? 1.f / l : 0.f;
-      {
+      if (it.part < 0) {
+        const float inv = l != 0.f ? 1.f / l : 0.f;
         uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * kHeadDim);
 #pragma unroll 1
         for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
@@ -861,6 +984,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+      } else {
+        float* rec = p.rec + (static_cast<int64_t>(it.part) * p.rec_rows + t * TR + lr) * kPieceRow;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
+          uint32_t w[32];
+          tmem_ld32(w, o_tm + c0);
+          tmem_wait_ld(w);
+          if (valid) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              st_global_v8(rec + c0 + 8 * q,
+                           make_uint4(w[8 * q], w[8 * q + 1], w[8 * q + 2], w[8 * q + 3]),
+                           make_uint4(w[8 * q + 4], w[8 * q + 5], w[8 * q + 6], w[8 * q + 7]));
+          }
+        }
+        if (valid) {
+          rec[128] = m_used;
+          rec[129] = l;
+        }
       }
       tc_fence_before();
     }
@@ -868,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 8) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols)
@@ -878,8 +1020,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
+// Joins the pieces of the item that CTA blockIdx.x began and did not end: a warp a
+// row, rows dealt to the warps of grid y.
+__global__ void __launch_bounds__(256) prefill_q8_join_kernel(const __grid_constant__ PrefillQ8Params p,
+                                                              int ctas) {
+  grid_dependency_trigger();
+  grid_dependency_wait();
+  const PieceDesc d = p.desc[blockIdx.x];
+  const int lane = threadIdx.x & 31;
+  if (d.rows <= static_cast<int>(blockIdx.y) * 8) return;
+  // the CTA of the item's last piece: the first after this one that does not go on
+  int last = blockIdx.x + 1;
+  for (bool found = false; !found; last += 32) {
+    const int c = last + lane;
+    const uint32_t ends = __ballot_sync(kFull, c >= ctas - 1 || p.desc[c].continues != 1);
+    found = ends != 0u;
+    if (found) last += __ffs(ends) - 1 - 32;
+  }
+  const int64_t stride = static_cast<int64_t>(2) * p.rec_rows * kPieceRow;  // CTA to CTA
+  const int n = last - static_cast<int>(blockIdx.x) + 1;  // pieces
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < d.rows; r += gridDim.y * 8) {
+    // piece k's row: record 1 of this CTA, then record 0 of the next ones
+    const float* base = p.rec + blockIdx.x * stride + static_cast<int64_t>(r) * kPieceRow;
+    auto row_of = [&](int k) {
+      return base + (k == 0 ? static_cast<int64_t>(p.rec_rows) * kPieceRow : k * stride);
+    };
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(row_of(k) + 128);
+      if (ml.y != 0.f) M = fmaxf(M, ml.x);  // (0: the row sees nothing of the piece)
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float2 ml = *reinterpret_cast<const float2*>(row_of(k) + 128);
+      const float4 v = *reinterpret_cast<const float4*>(row_of(k) + 4 * lane);
+      const float w = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;
+      L = fmaf(w, ml.y, L);
+      o.x = fmaf(w, v.x, o.x);
+      o.y = fmaf(w, v.y, o.y);
+      o.z = fmaf(w, v.z, o.z);
+      o.w = fmaf(w, v.w, o.w);
+    }
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    const int tok = (d.row0 + r) / p.G;
+    const int64_t qrow = (static_cast<int64_t>(d.q0) + tok) * p.Hq + d.kvh * p.G + d.row0 + r - tok * p.G;
+    *reinterpret_cast<uint2*>(p.out + qrow * kHeadDim + 4 * lane) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  }
+}
+
 template <bool kE4m3>
-cudaError_t launch(const CUtensorMap& tq, const PrefillQ8Params& p, int sms, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tq, const PrefillQ8Params& p, int grid, cudaStream_t stream) {
   static unsigned long long done_mask = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -891,18 +1086,38 @@ cudaError_t launch(const CUtensorMap& tq, const PrefillQ8Params& p, int sms, cud
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
   }
-  const int64_t row_tiles =
-      (static_cast<int64_t>(p.max_q) * p.G + 2 * p.tile_rows - 1) / (2 * p.tile_rows);
-  const int64_t items = row_tiles * p.Hkv * p.num_seqs;
-  if (items > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads),
-                    kSmemBytes, stream, tq, p);
+  return launch_pdl_if(pdl_decode_enabled(), kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                       kSmemBytes, stream, tq, p);
 }
+
+int64_t row_tile_pairs(int64_t max_q, int G, int tile_rows) {
+  return (max_q * G + 2 * tile_rows - 1) / (2 * tile_rows);
+}
+
+// Rows of a piece's record; 0: items are not cut.
+int split_rows(int num_tokens, int num_seqs, int max_q, int Hkv, int G, int sms) {
+  const int tile_rows = (kRowTile / G) * G;
+  const int64_t R = row_tile_pairs(max_q, G, tile_rows);
+  const int64_t most = static_cast<int64_t>(num_tokens) * G / (2 * tile_rows) + num_seqs;
+  const int64_t pairs = R * num_seqs;
+  if (pairs > kSplitPairs || (most < pairs ? most : pairs) * Hkv > static_cast<int64_t>(kSplitItems) * sms)
+    return 0;
+  const int64_t rows = static_cast<int64_t>(max_q) * G;
+  return static_cast<int>(rows < 2 * tile_rows ? rows : 2 * tile_rows);
+}
+
+size_t desc_bytes(int sms) { return static_cast<size_t>(sms) * sizeof(PieceDesc); }
 
 }  // namespace
 
-TcStatus launch_prefill_q8(const AttentionQ8Params& a, bool e4m3, bool contig, int num_tokens,
-                           int sms, cudaStream_t stream, cudaError_t* cuda_err) {
+size_t prefill_q8_workspace(int num_tokens, int num_seqs, int max_q, int Hkv, int G, int sms) {
+  const int rows = split_rows(num_tokens, num_seqs, max_q < num_tokens ? max_q : num_tokens, Hkv, G, sms);
+  if (rows == 0) return 0;
+  return desc_bytes(sms) + static_cast<size_t>(sms) * 2 * rows * kPieceRow * sizeof(float);
+}
+
+TcStatus launch_prefill_q8(const AttentionQ8Params& a, bool e4m3, bool contig, int num_tokens, int sms,
+                           void* workspace, cudaStream_t stream, cudaError_t* cuda_err) {
   *cuda_err = cudaSuccess;
   PrefillQ8Params p = {};
   p.q = a.q;
@@ -936,7 +1151,23 @@ TcStatus launch_prefill_q8(const AttentionQ8Params& a, bool e4m3, bool contig, i
   alignas(64) CUtensorMap tq;
   if (!encode_prefill_rows(&tq, a.q, num_tokens, a.Hq, a.G, p.tile_rows))
     return TcStatus::kEncodeFailed;
-  *cuda_err = e4m3 ? launch<true>(tq, p, sms, stream) : launch<false>(tq, p, sms, stream);
+  const int64_t items = row_tile_pairs(p.max_q, p.G, p.tile_rows) * p.Hkv * p.num_seqs;
+  if (items > INT32_MAX) {
+    *cuda_err = cudaErrorInvalidValue;
+    return TcStatus::kCudaError;
+  }
+  int grid = static_cast<int>(items < sms ? items : sms);
+  p.rec_rows = split_rows(num_tokens, p.num_seqs, p.max_q, p.Hkv, p.G, sms);
+  if (p.rec_rows > 0) {
+    grid = sms;
+    p.desc = static_cast<PieceDesc*>(workspace);
+    p.rec = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + desc_bytes(sms));
+  }
+  *cuda_err = e4m3 ? launch<true>(tq, p, grid, stream) : launch<false>(tq, p, grid, stream);
+  if (*cuda_err == cudaSuccess && p.rec_rows > 0)
+    *cuda_err = launch_pdl_if(pdl_decode_enabled(), prefill_q8_join_kernel,
+                              dim3(static_cast<unsigned>(grid), static_cast<unsigned>((p.rec_rows + 7) / 8)),
+                              dim3(256), 0, stream, p, grid);
   return *cuda_err == cudaSuccess ? TcStatus::kOk : TcStatus::kCudaError;
 }
 

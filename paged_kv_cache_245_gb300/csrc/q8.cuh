@@ -77,9 +77,11 @@ constexpr int kQ8SmallCtas = 3;
 cudaError_t room_decode_q8_cluster(bool e4m3, ClusterRoom* out);
 cudaError_t launch_decode_q8_cluster(const AttentionQ8Params& p, bool e4m3, int cluster, int warps,
                                      cudaStream_t stream);
-// Prefill (prefill_q8.cu).
+// Prefill (prefill_q8.cu).  workspace (16-byte aligned): prefill_q8_workspace bytes, if
+// that is not 0.
+size_t prefill_q8_workspace(int num_tokens, int num_seqs, int max_q, int Hkv, int G, int sms);
 TcStatus launch_prefill_q8(const AttentionQ8Params& p, bool e4m3, bool contig, int num_tokens,
-                           int sms, cudaStream_t stream, cudaError_t* cuda_err);
+                           int sms, void* workspace, cudaStream_t stream, cudaError_t* cuda_err);
 
 #ifdef __CUDACC__
 

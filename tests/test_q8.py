@@ -86,7 +86,7 @@ def decode(L, q=FAKE, c=None, tables=FAKE, maxb=4, nb=8, ctx=FAKE, B=2, top=64, 
 def prefill(L, q=FAKE, cu=FAKE, T=4, c=None, tables=FAKE, maxb=4, nb=8, ctx=FAKE, B=2, max_q=2,
             bs=16, scale=0.1, h=H, out=FAKE):
     return L.pkv_paged_prefill_attention_q8(q, cu, T, cache() if c is None else c, tables, maxb, nb,
-                                            ctx, B, max_q, bs, scale, h, out, None)
+                                            ctx, B, max_q, bs, scale, h, out, None, 0, None)
 
 
 COMMON = [(dict(q=None), INVALID), (dict(q=FAKE + 8), INVALID), (dict(tables=None), INVALID),
@@ -119,9 +119,9 @@ def test_contig_refuses(L):
     assert L.pkv_contig_decode_attention_q8(FAKE, c, FAKE, 4, FAKE, 2, 30, 40, 0.1, H, FAKE, None, 0,
                                             None) == UNSUPPORTED
     assert L.pkv_contig_prefill_attention_q8(FAKE, FAKE, 4, c, FAKE, 0, FAKE, 2, 2, 64, 0.1, H, FAKE,
-                                             None) == INVALID
+                                             None, 0, None) == INVALID
     assert L.pkv_contig_prefill_attention_q8(FAKE, FAKE, 4, c, FAKE, 4, FAKE, 2, 2, 2 ** 31, 0.1, H,
-                                             FAKE, None) == UNSUPPORTED
+                                             FAKE, None, 0, None) == UNSUPPORTED
 
 
 def test_binding_refuses():

@@ -51,7 +51,8 @@ constexpr int kTilesBytes = kOffCodes + 2 * kCodeTile;  // 224 KiB
 constexpr int kScaleRing = 4;                         // tiles whose scales are kept
 constexpr int kScaleFloats = 24;                      // of 8 groups: ks, log2 vs, 1 / vs
 constexpr int kOffScales = kTilesBytes + 512;
-constexpr int kSmemBytes = kOffScales + kScaleRing * kScaleFloats * 4 + 1024;  // + alignment
+constexpr int kOffHeld = kOffScales + kScaleRing * kScaleFloats * 4;  // a word a converter thread
+constexpr int kSmemBytes = kOffHeld + 32 * 4 * 4 + 1024;              // + alignment
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KiB");
 constexpr int kProducer = 10;                         // the code producer
 constexpr int kConvert0 = 11, kConverters = 4;        // converter warps
@@ -117,6 +118,21 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                : "=r"(r));
   return r != 0u;
+}
+
+// 64 consecutive columns of this warp's 32 lanes, loaded and waited for in one
+// statement: until the wait the registers are not to be touched, and what the compiler
+// puts between a load and a wait of their own (a copy of the first is enough) would.
+__device__ __forceinline__ void tmem_ld64(uint32_t (&a)[32], uint32_t (&b)[32], uint32_t taddr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,"
+      "%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+      "}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : PKV_R32(PKV_OUT, a), PKV_R32(PKV_OUT, b)
+      : "r"(taddr)
+      : "memory");
 }
 
 // Four bytes of shared memory from global memory, or zeros.
@@ -278,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // loads and swizzled stores meet different banks.
     const int row0 = (warp - kConvert0) * 4 + ((lane >> 4) << 1) + ((lane >> 2) & 1);
     const int ch = (lane & 3) + (((lane >> 2) ^ (lane >> 3)) & 1) * 4;  // chunk of 16 codes
+    volatile uint32_t* held = reinterpret_cast<uint32_t*>(smem + kOffHeld);
     int g = 0;  // tiles of all items
     int nread = 0;
     bool ok = true;
@@ -295,6 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 c[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) c[i] = *reinterpret_cast<const uint4*>(from + i * 16 * 128);
+          // The arrival must not overtake the loads, whose values are needed only later:
+          // a store of something made of all of them comes between (without it the next
+          // codes now and then came in first).
+          held[tid - 32 * kConvert0] =
+              c[0].x ^ c[1].x ^ c[2].x ^ c[3].x ^ c[4].x ^ c[5].x ^ c[6].x ^ c[7].x;
           __syncwarp();
           if (lane == 0) mbar_arrive(&B.cempty[kv]);
           if (kv == 0 && warp == kConvert0 && lane < 8) {
@@ -756,7 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + t * 128;
     const uint32_t o_tm = tmem + lane_base + 256 + t * 128;
-    const float sc = p.qscale;
+    const bool negative = p.qscale < 0.f;
+    const float sc = fabsf(p.qscale);
     uint32_t ns = 0, no = 0;  // S tiles and items this row tile took
     int g = 0;                // tiles of all items, this one's first
     bool ok = true;
@@ -781,62 +804,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const int k0 = (it.t0 + j) * kKeys;
-        const bool diag = k0 + kKeys - 1 > pos;  // some key of the tile lies past the row
-        // general: a masked tile in this warp, or a negative scale (the maximum
-        // of the scaled logits is then not the scaled maximum)
-        const bool general = __any_sync(kFull, diag) || !(sc >= 0.f);
+        // columns of the tile that this row sees, and that all / any of the warp's do
+        const int seen = min(max(pos - k0 + 1, 0), kKeys);
+        const int all = __reduce_min_sync(kFull, seen), any = __reduce_max_sync(kFull, seen);
         // the tile's scales, of 16 columns each: ks, log2 vs, 1 / vs
         const float* sct = scales + ((g0 + j) & (kScaleRing - 1)) * kScaleFloats;
-        // pass 1: the row maximum of the scaled, masked logits
-        float tmax = -INFINITY;
-        if (!general) {
+        // The scores' factors are positive (the sign of the softmax's own goes to S), so
+        // that the largest of 16 columns is the largest product, and not 0, so that a
+        // column that the row does not see, -inf, stays that.
+        auto factors = [&](int h, float (&ks)[4]) {
+          const float4 k4 = *reinterpret_cast<const float4*>(sct + 4 * h);
+          ks[0] = fmaxf(k4.x * sc, 1.17549435e-38f);
+          ks[1] = fmaxf(k4.y * sc, 1.17549435e-38f);
+          ks[2] = fmaxf(k4.z * sc, 1.17549435e-38f);
+          ks[3] = fmaxf(k4.w * sc, 1.17549435e-38f);
+        };
+        // columns 64 h .. 64 h + 31 (a) and + 32 .. + 63 (b) of S, with its sign and mask
+        auto load_half = [&](int h, uint32_t (&a)[32], uint32_t (&b)[32]) {
+          tmem_ld64(a, b, s_tm + 64 * h);
+          if (negative) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t a[32], b[32];
-            tmem_ld32(a, s_tm + 64 * h);
-            tmem_ld32(b, s_tm + 64 * h + 32);
-            const float4 ks4 = *reinterpret_cast<const float4*>(sct + 4 * h);
-            const float ks[4] = {ks4.x * sc, ks4.y * sc, ks4.z * sc, ks4.w * sc};
-            tmem_wait_ld(a);
-            tmem_ready(b);
+            for (int c = 0; c < 32; ++c) {
+              a[c] ^= 0x80000000u;
+              b[c] ^= 0x80000000u;
+            }
+          }
+          if (all < 64 * h + 64) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const uint32_t* x = q < 2 ? a + 16 * q : b + 16 * (q - 2);
-              float u = __uint_as_float(x[0]), v = __uint_as_float(x[1]);
+              if (all >= 64 * h + 16 * q + 16) continue;
+              uint32_t* x = q < 2 ? a + 16 * q : b + 16 * (q - 2);
 #pragma unroll
-              for (int c = 2; c < 14; c += 4) {
-                u = fmax3(u, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-                v = fmax3(v, __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
-              }
-              u = fmax3(u, __uint_as_float(x[14]), __uint_as_float(x[15]));
-              tmax = fmaxf(tmax, fmaxf(u, v) * ks[q]);
+              for (int c = 0; c < 16; ++c) x[c] = 64 * h + 16 * q + c < seen ? x[c] : 0xff800000u;
             }
           }
-        } else {
-          float mx[8];
+        };
+        // pass 1: the row maximum of the scaled, masked logits
+        float tmax = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
-          // (not unrolled: the masked path runs once per item, and a smaller kernel
-          // measured faster)
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            // a half whose keys no row of the warp sees adds nothing to the maximum
-            if (!__any_sync(kFull, !diag || k0 + 64 * h <= pos)) continue;
-            uint32_t a[32], b[32];
-            tmem_ld32(a, s_tm + 64 * h);
-            tmem_ld32(b, s_tm + 64 * h + 32);
-            const float4 ks4 = *reinterpret_cast<const float4*>(sct + 4 * h);
-            const float ks[4] = {ks4.x * sc, ks4.y * sc, ks4.z * sc, ks4.w * sc};
-            tmem_wait_ld(a);
-            tmem_ready(b);
+        for (int h = 0; h < 2; ++h) {
+          if (any <= 64 * h) break;  // no row of the warp sees a key of this half
+          uint32_t a[32], b[32];
+          load_half(h, a, b);
+          float ks[4];
+          factors(h, ks);
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              const float x = __uint_as_float(c < 32 ? a[c] : b[c - 32]) * ks[c >> 4];
-              mx[c & 7] = fmaxf(mx[c & 7], !diag || k0 + 64 * h + c <= pos ? x : -INFINITY);
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* x = q < 2 ? a + 16 * q : b + 16 * (q - 2);
+            float u = __uint_as_float(x[0]), v = __uint_as_float(x[1]);
+#pragma unroll
+            for (int c = 2; c < 14; c += 4) {
+              u = fmax3(u, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+              v = fmax3(v, __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
             }
+            u = fmax3(u, __uint_as_float(x[14]), __uint_as_float(x[15]));
+            tmax = fmaxf(tmax, fmaxf(u, v) * ks[q]);
           }
-          tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
         }
         const float m_new = fmaxf(m_used, tmax);
         if (j == 0) {
@@ -850,100 +873,58 @@ __global__ void __launch_bounds__(kThreads, 1)
               m_used = m_new;
             }
 #pragma unroll
-            for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
-              uint32_t w[32];
-              tmem_ld32(w, o_tm + c0);
-              tmem_wait_ld(w);
+            for (int c0 = 0; c0 < kHeadDim; c0 += 64) {
+              uint32_t w[32], w2[32];
+              tmem_ld64(w, w2, o_tm + c0);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * alpha);
+              for (int c = 0; c < 32; ++c) {
+                w[c] = __float_as_uint(__uint_as_float(w[c]) * alpha);
+                w2[c] = __float_as_uint(__uint_as_float(w2[c]) * alpha);
+              }
               tmem_st32(o_tm + c0, w);
+              tmem_st32(o_tm + c0 + 32, w2);
             }
           }
         }
         // pass 2: P vs = 2^(s * scale - m + log2 vs) as bf16 pairs over the columns
         // already read; the sums of P are those of a group divided by its vs
-        if (!general) {
+        const float m = m_used == -INFINITY ? 0.f : m_used;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t a[32], b[32];
-            tmem_ld32(a, s_tm + 64 * h);
-            tmem_ld32(b, s_tm + 64 * h + 32);
-            const float4 ks4 = *reinterpret_cast<const float4*>(sct + 4 * h);
-            const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
-            const float ks[4] = {ks4.x * sc, ks4.y * sc, ks4.z * sc, ks4.w * sc};
-            const float lv[4] = {lv4.x - m_used, lv4.y - m_used, lv4.z - m_used, lv4.w - m_used};
-            tmem_wait_ld(a);
-            tmem_ready(b);
-            uint32_t pk[32];
-            uint64_t ls2[4];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+          if (any <= 64 * h) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const uint32_t u0 = c < 16 ? a[2 * c] : b[2 * c - 32];
-              const uint32_t u1 = c < 16 ? a[2 * c + 1] : b[2 * c - 31];
-              const uint32_t kq = __float_as_uint(ks[c >> 3]), lq = __float_as_uint(lv[c >> 3]);
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(u0, u1), f2_pack(kq, kq), f2_pack(lq, lq)), x0, x1);
-              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-              const uint64_t e2 = f2_pack(__float_as_uint(e0), __float_as_uint(e1));
-              ls2[c >> 3] = (c & 7) == 0 ? e2 : f2_add(ls2[c >> 3], e2);
-              pk[c] = pack_bf16x2(e0, e1);
-            }
+            for (int c = 0; c < 32; ++c) pk[c] = 0u;
             tmem_st32(s_tm + 32 * h, pk);
-            const float4 iv4 = *reinterpret_cast<const float4*>(sct + 16 + 4 * h);
-            const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float l0, l1;
-              f2_unpack(ls2[q], l0, l1);
-              l = fmaf(l0 + l1, iv[q], l);
-            }
+            continue;
           }
-        } else {
-          // (not unrolled: the masked path runs once per item, and a smaller kernel
-          // measured faster)
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (!__any_sync(kFull, !diag || k0 + 64 * h <= pos)) {
-              // no row of the warp sees a key of this half: its P is zero
-              uint32_t pz[32];
+          uint32_t a[32], b[32];
+          load_half(h, a, b);
+          float ks[4];
+          factors(h, ks);
+          const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
+          const float lv[4] = {lv4.x - m, lv4.y - m, lv4.z - m, lv4.w - m};
+          uint64_t ls2[4];
 #pragma unroll
-              for (int c = 0; c < 32; ++c) pz[c] = 0u;
-              tmem_st32(s_tm + 32 * h, pz);
-              continue;
-            }
-            uint32_t a[32], b[32];
-            tmem_ld32(a, s_tm + 64 * h);
-            tmem_ld32(b, s_tm + 64 * h + 32);
-            const float4 ks4 = *reinterpret_cast<const float4*>(sct + 4 * h);
-            const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
-            const float4 iv4 = *reinterpret_cast<const float4*>(sct + 16 + 4 * h);
-            const float ks[4] = {ks4.x * sc, ks4.y * sc, ks4.z * sc, ks4.w * sc};
-            const float lv[4] = {lv4.x - m_used, lv4.y - m_used, lv4.z - m_used, lv4.w - m_used};
-            const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
-            tmem_wait_ld(a);
-            tmem_ready(b);
-            // keys of this half the row sees: bit c of (lo, hi) for key 64h + c
-            const int seen = diag ? min(max(pos - k0 - 64 * h + 1, 0), 64) : 64;
-            const uint32_t lo = seen >= 32 ? 0xffffffffu : (1u << seen) - 1u;
-            const uint32_t hi =
-                seen >= 64 ? 0xffffffffu : (seen <= 32 ? 0u : (1u << (seen - 32)) - 1u);
-            uint32_t pk[32];
+          for (int c = 0; c < 32; ++c) {
+            const uint32_t u0 = c < 16 ? a[2 * c] : b[2 * c - 32];
+            const uint32_t u1 = c < 16 ? a[2 * c + 1] : b[2 * c - 31];
+            const uint32_t kq = __float_as_uint(ks[c >> 3]), lq = __float_as_uint(lv[c >> 3]);
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(u0, u1), f2_pack(kq, kq), f2_pack(lq, lq)), x0, x1);
+            const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+            const uint64_t e2 = f2_pack(__float_as_uint(e0), __float_as_uint(e1));
+            ls2[c >> 3] = (c & 7) == 0 ? e2 : f2_add(ls2[c >> 3], e2);
+            pk[c] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32(s_tm + 32 * h, pk);
+          const float4 iv4 = *reinterpret_cast<const float4*>(sct + 16 + 4 * h);
+          const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const uint32_t u0 = c < 16 ? a[2 * c] : b[2 * c - 32];
-              const uint32_t u1 = c < 16 ? a[2 * c + 1] : b[2 * c - 31];
-              float e0 = fast_exp2(fmaf(__uint_as_float(u0), ks[c >> 3], lv[c >> 3]));
-              float e1 = fast_exp2(fmaf(__uint_as_float(u1), ks[c >> 3], lv[c >> 3]));
-              const uint32_t bits = c < 16 ? lo : hi;
-              e0 = (bits >> ((2 * c) & 31)) & 1u ? e0 : 0.f;
-              e1 = (bits >> ((2 * c + 1) & 31)) & 1u ? e1 : 0.f;
-              ls[c >> 3] += e0 + e1;
-              pk[c] = pack_bf16x2(e0, e1);
-            }
-            tmem_st32(s_tm + 32 * h, pk);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) l = fmaf(ls[q], iv[q], l);
+          for (int q = 0; q < 4; ++q) {
+            float l0, l1;
+            f2_unpack(ls2[q], l0, l1);
+            l = fmaf(l0 + l1, iv[q], l);
           }
         }
         tmem_wait_st();
@@ -962,41 +943,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l != 0.f ? 1.f / l : 0.f;
         uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * kHeadDim);
 #pragma unroll 1
-        for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
-          uint32_t w[32];
-          tmem_ld32(w, o_tm + c0);
-          tmem_wait_ld(w);
+        for (int c0 = 0; c0 < kHeadDim; c0 += 64) {
+          uint32_t w[32], w2[32];
+          tmem_ld64(w, w2, o_tm + c0);
           if (valid) {
-            uint4 o[4];
+            uint4 o[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              o[q].x = pack_bf16x2(__uint_as_float(w[8 * q + 0]) * inv, __uint_as_float(w[8 * q + 1]) * inv);
-              o[q].y = pack_bf16x2(__uint_as_float(w[8 * q + 2]) * inv, __uint_as_float(w[8 * q + 3]) * inv);
-              o[q].z = pack_bf16x2(__uint_as_float(w[8 * q + 4]) * inv, __uint_as_float(w[8 * q + 5]) * inv);
-              o[q].w = pack_bf16x2(__uint_as_float(w[8 * q + 6]) * inv, __uint_as_float(w[8 * q + 7]) * inv);
+            for (int q = 0; q < 8; ++q) {
+              const uint32_t* x = q < 4 ? w + 8 * q : w2 + 8 * (q - 4);
+              o[q].x = pack_bf16x2(__uint_as_float(x[0]) * inv, __uint_as_float(x[1]) * inv);
+              o[q].y = pack_bf16x2(__uint_as_float(x[2]) * inv, __uint_as_float(x[3]) * inv);
+              o[q].z = pack_bf16x2(__uint_as_float(x[4]) * inv, __uint_as_float(x[5]) * inv);
+              o[q].w = pack_bf16x2(__uint_as_float(x[6]) * inv, __uint_as_float(x[7]) * inv);
             }
             if (p.out_v8) {  // out 32-byte aligned: whole 32-byte sectors
-              st_global_v8(dst + c0 / 8, o[0], o[1]);
-              st_global_v8(dst + c0 / 8 + 2, o[2], o[3]);
+#pragma unroll
+              for (int q = 0; q < 8; q += 2) st_global_v8(dst + c0 / 8 + q, o[q], o[q + 1]);
             } else {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) dst[c0 / 8 + q] = o[q];
+              for (int q = 0; q < 8; ++q) dst[c0 / 8 + q] = o[q];
             }
           }
         }
       } else {
         float* rec = p.rec + (static_cast<int64_t>(it.part) * p.rec_rows + t * TR + lr) * kPieceRow;
 #pragma unroll 1
-        for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
-          uint32_t w[32];
-          tmem_ld32(w, o_tm + c0);
-          tmem_wait_ld(w);
+        for (int c0 = 0; c0 < kHeadDim; c0 += 64) {
+          uint32_t w[32], w2[32];
+          tmem_ld64(w, w2, o_tm + c0);
           if (valid) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              st_global_v8(rec + c0 + 8 * q,
-                           make_uint4(w[8 * q], w[8 * q + 1], w[8 * q + 2], w[8 * q + 3]),
-                           make_uint4(w[8 * q + 4], w[8 * q + 5], w[8 * q + 6], w[8 * q + 7]));
+            for (int q = 0; q < 8; ++q) {
+              const uint32_t* x = q < 4 ? w + 8 * q : w2 + 8 * (q - 4);
+              st_global_v8(rec + c0 + 8 * q, make_uint4(x[0], x[1], x[2], x[3]),
+                           make_uint4(x[4], x[5], x[6], x[7]));
+            }
           }
         }
         if (valid) {

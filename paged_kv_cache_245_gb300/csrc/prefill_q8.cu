@@ -11,7 +11,7 @@
 //   warp 9       the item list and the Q rows
 //   warp 10      codes of K and V (16 KiB a tile each) by bulk copies into one slot
 //                each, and the tile's 16 scales by cp.async
-//   warps 11-14  codes -> bf16 into the two stages of K and V operands
+//   warps 12-15  codes -> bf16 into the two stages of K and V operands
 //
 // The operands hold the codes themselves, which bf16 holds exactly (int8 and e4m3
 // have at most 8 significant bits): a key's scale is uniform over 16 columns of S
@@ -22,7 +22,8 @@
 //   O += (P_j vs) vcode_j,           l += (sum over a group of P_j vs) / vs.
 //
 // Schedule.  Many items: dealt to the CTAs (one an SM) in rounds of alternating
-// direction, latest rows first.  Few items (a host bound of kSplitItems an SM): the
+// direction, sorted by cost where the list is short enough for each CTA to sort, else
+// latest rows first.  Few items (a host bound of kSplitItems an SM): the
 // flattened list of all items' key tiles is cut evenly over the CTAs, an item
 // counting as kItemCost tiles more; an item that is cut leaves its pieces' (O, m, l)
 // in the workspace, and a second kernel joins them:
@@ -55,12 +56,17 @@ constexpr int kOffHeld = kOffScales + kScaleRing * kScaleFloats * 4;  // a word 
 constexpr int kSmemBytes = kOffHeld + 32 * 4 * 4 + 1024;              // + alignment
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KiB");
 constexpr int kProducer = 10;                         // the code producer
-constexpr int kConvert0 = 11, kConverters = 4;        // converter warps
+constexpr int kConvert0 = 12, kConverters = 4;        // converter warps
 constexpr int kThreads = 32 * (kConvert0 + kConverters);
-static_assert(kProducer == 10 && kConvert0 == 11, "every warp has a role: 0-7 are the softmax's, 8 and 9 the next two");
+static_assert(kProducer == 10 && kConvert0 == 12, "warps 0-7 are the softmax's, 8 and 9 the next two");
+// Registers a thread of the four warpgroups, from the launch's 128 each: the softmax's
+// rows of S want more (315 -> 277 us with 8 x 2048 in e4m3), the others do with less.
+constexpr int kRegsSoftmax = 176, kRegsRoles = 72, kRegsConvert = 88;
+static_assert(2 * kRegsSoftmax + kRegsRoles + kRegsConvert == 4 * 128, "the launch's registers");
 constexpr int kRing = 4;                              // item descriptors in flight
 constexpr int kRingUsers = 10 + kConverters;  // readers: softmax, MMA, producer, converters
-constexpr int kSplitItems = 8;               // items an SM up to which they are cut
+constexpr int kSplitItems = 4;               // items an SM up to which they are cut
+constexpr int kSortPairs = 512;              // (row tiles, sequence) pairs that are sorted at most
 constexpr int kSplitPairs = 1024;            // (sequence, row tiles) pairs up to which they are
 constexpr int kItemCost = 2;                 // what an item costs, in key tiles
 constexpr int kLeastUnits = 6;               // a CTA's share is at least this
@@ -186,6 +192,7 @@ struct PrefillQ8Params : PrefillParams {
   PieceDesc* desc;      // [CTAs] and
   float* rec;           // [CTAs][2][rec_rows][kPieceRow]: items are cut; null: they are not
   int32_t rec_rows;     // rows of an item at most
+  int32_t sorted;       // pairs (row tiles, sequence) to sort, or 0
 };
 
 template <bool kE4m3>
@@ -240,6 +247,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
+  // Row tiles rt of a sequence (any KV head); false if there are none.
+  auto describe = [&](int rt, int seq, bool report, PItem& it) -> bool {
+    it.seq = seq;
+    it.kvh = 0;
+    it.t0 = 0;
+    it.part = -1;
+    it.q0 = p.cu_q[seq];
+    const int Lq = p.cu_q[seq + 1] - it.q0;
+    it.ctx = p.ctx_lens[seq];
+    if (p.checked) {
+      const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.bs;
+      if (Lq < 0 || Lq > p.max_q || it.ctx < Lq || it.ctx > cap) {
+        if (report) record_error(p.err, kErrContext);
+        return false;  // the sequence is left unwritten
+      }
+    }
+    it.rows = Lq * G;
+    it.row0 = rt * 2 * TR;
+    if (it.row0 >= it.rows) return false;  // past the chunk
+    it.base = it.ctx - Lq;                 // position of the chunk's first token
+    const int last_row = min(it.row0 + 2 * TR, it.rows) - 1;
+    const int kend = it.base + last_row / G + 1;  // keys the item needs
+    it.ntiles = (kend + kKeys - 1) / kKeys;
+    return kend > 0;  // (not only when ctx < Lq, caught in checked mode)
+  };
   // Setup: barriers, the Q slots' padding, the tensor memory.
   if (warp == kProducer) {
     if (lane == 0) {
@@ -281,6 +313,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // Pairs (row tiles, sequence) by what their items cost, dearest first: list[n] is the
+  // n-th one's index.  In the operand stages, which nothing writes before the item warp
+  // has read its part of the list.
+  int32_t* key = reinterpret_cast<int32_t*>(smem + kOffK);
+  int32_t* list = key + kSortPairs;
+  if (p.sorted > 0) {
+    for (int c = tid; c < kSortPairs; c += kThreads) {
+      PItem it;
+      const bool there = c < p.sorted && describe(c / p.num_seqs, c % p.num_seqs, blockIdx.x == 0 && c < p.num_seqs, it);
+      // (a tile of two row tiles costs 2 to 1.2 of one with one; an item some 3 us more)
+      key[c] = there ? it.ntiles * (it.rows > it.row0 + TR ? 5 : 3) + 8 : 0;
+      list[c] = -1;
+    }
+    __syncthreads();
+    for (int c = tid; c < p.sorted; c += kThreads) {
+      const int mine = key[c];
+      int rank = 0;
+      for (int x = 0; x < p.sorted; x += 4) {
+        const int4 k = *reinterpret_cast<const int4*>(key + x);
+        rank += (k.x > mine || (k.x == mine && x < c)) + (k.y > mine || (k.y == mine && x + 1 < c)) +
+                (k.z > mine || (k.z == mine && x + 2 < c)) + (k.w > mine || (k.w == mine && x + 3 < c));
+      }
+      if (mine > 0) list[rank] = c;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -288,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t smem_base = smem_addr(smem);
 
   if (warp >= kConvert0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
     // ================= converters: codes -> operands =================
     // A thread takes 16 codes of rows row0, row0 + 16, ..  The eight lanes of a quarter
     // warp take chunks 0-3 of one row and 4-7 of the next (or the other way), whose
@@ -352,7 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == kProducer) {
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRoles));
+  if (warp == kProducer) {
     // ================= code producer =================
     // Every row tile of a sequence and KV head reads the same tiles: keep them in
     // L2 for the items after.
@@ -492,31 +552,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    // Row tiles rt of a sequence (any KV head); false if there are none.
-    auto describe = [&](int rt, int seq, bool report, PItem& it) -> bool {
-      it.seq = seq;
-      it.kvh = 0;
-      it.t0 = 0;
-      it.part = -1;
-      it.q0 = p.cu_q[seq];
-      const int Lq = p.cu_q[seq + 1] - it.q0;
-      it.ctx = p.ctx_lens[seq];
-      if (p.checked) {
-        const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.bs;
-        if (Lq < 0 || Lq > p.max_q || it.ctx < Lq || it.ctx > cap) {
-          if (report) record_error(p.err, kErrContext);
-          return false;  // the sequence is left unwritten
-        }
-      }
-      it.rows = Lq * G;
-      it.row0 = rt * 2 * TR;
-      if (it.row0 >= it.rows) return false;  // past the chunk
-      it.base = it.ctx - Lq;                 // position of the chunk's first token
-      const int last_row = min(it.row0 + 2 * TR, it.rows) - 1;
-      const int kend = it.base + last_row / G + 1;  // keys the item needs
-      it.ntiles = (kend + kKeys - 1) / kKeys;
-      return kend > 0;  // (not only when ctx < Lq, caught in checked mode)
-    };
     // the item of lane src
     auto of_lane = [&](const PItem& mine, int src) -> PItem {
       PItem it;
@@ -601,12 +636,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0) p.desc[blockIdx.x] = desc;
     } else {
-      // Items in order of index: row tile (latest first), then sequence, then KV head.
-      // Round k deals items k P .. k P + P - 1 to the P CTAs, forwards in even rounds and
-      // backwards in odd ones; 32 rounds at a time, one a lane, so that items whose rows
-      // lie past their chunk cost one latency.
-      const int per = p.num_seqs * p.Hkv;
-      const int total = R * per;
+      // Items in order: pairs as sorted, or row tile (latest first), then sequence; then
+      // KV head.  Round k deals items k P .. k P + P - 1 to the P CTAs, forwards in even
+      // rounds and backwards in odd ones; 32 rounds at a time, one a lane, so that items
+      // whose rows lie past their chunk cost one latency (a sorted list has no more).
+      const int total = R * p.num_seqs * p.Hkv;
       for (int64_t k0 = 0; ok && k0 * P < total; k0 += 32) {
         const int64_t k = k0 + lane;
         const int64_t slot = k * P + ((k & 1) ? P - 1 - static_cast<int>(blockIdx.x)
@@ -614,12 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         PItem mine = {};
         bool there = slot < total;
         if (there) {
-          const int idx = static_cast<int>(slot);
-          const int rt = R - 1 - idx / per;
-          const int rem = idx - (idx / per) * per;
-          const int seq = rem / p.Hkv;
-          there = describe(rt, seq, rt == 0 && rem == seq * p.Hkv, mine);
-          mine.kvh = rem - seq * p.Hkv;
+          const int idx = static_cast<int>(slot), at = idx / p.Hkv;
+          const int c = p.sorted > 0 ? (at < p.sorted ? list[at] : -1)
+                                     : (R - 1 - at / p.num_seqs) * p.num_seqs + at % p.num_seqs;
+          there = c >= 0 && describe(c / p.num_seqs, c % p.num_seqs,
+                                     p.sorted == 0 && c < p.num_seqs && idx == at * p.Hkv, mine);
+          mine.kvh = idx - at * p.Hkv;
         }
         for (uint32_t left = __ballot_sync(kFull, there); ok && left != 0u; left &= left - 1)
           ok = serve(of_lane(mine, __ffs(left) - 1));
@@ -771,7 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(B.drain, 0);
     }
     __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ================= softmax warpgroups (warps 0-7) =================
     const int t = warp >> 2;                      // row tile
     const int lr = tid & (kRowTile - 1);          // row in the tile = tensor-memory lane
@@ -807,11 +843,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // columns of the tile that this row sees, and that all / any of the warp's do
         const int seen = min(max(pos - k0 + 1, 0), kKeys);
         const int all = __reduce_min_sync(kFull, seen), any = __reduce_max_sync(kFull, seen);
+        // plain: nothing is masked, and the largest of 16 columns is the largest product
+        const bool plain = all == kKeys && !negative;
         // the tile's scales, of 16 columns each: ks, log2 vs, 1 / vs
         const float* sct = scales + ((g0 + j) & (kScaleRing - 1)) * kScaleFloats;
-        // The scores' factors are positive (the sign of the softmax's own goes to S), so
-        // that the largest of 16 columns is the largest product, and not 0, so that a
-        // column that the row does not see, -inf, stays that.
+        // Else S takes the sign of the softmax's factor and -inf for the columns that the
+        // row does not see, and what follows is the same; no factor is 0, so that -inf
+        // stays that.
         auto factors = [&](int h, float (&ks)[4]) {
           const float4 k4 = *reinterpret_cast<const float4*>(sct + 4 * h);
           ks[0] = fmaxf(k4.x * sc, 1.17549435e-38f);
@@ -841,13 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // pass 1: the row maximum of the scaled, masked logits
         float tmax = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (any <= 64 * h) break;  // no row of the warp sees a key of this half
-          uint32_t a[32], b[32];
-          load_half(h, a, b);
-          float ks[4];
-          factors(h, ks);
+        auto largest = [&](const uint32_t (&a)[32], const uint32_t (&b)[32], const float (&ks)[4]) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t* x = q < 2 ? a + 16 * q : b + 16 * (q - 2);
@@ -859,6 +891,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             u = fmax3(u, __uint_as_float(x[14]), __uint_as_float(x[15]));
             tmax = fmaxf(tmax, fmaxf(u, v) * ks[q]);
+          }
+        };
+        if (plain) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t a[32], b[32];
+            tmem_ld32(a, s_tm + 64 * h);
+            tmem_ld32(b, s_tm + 64 * h + 32);
+            float ks[4];
+            factors(h, ks);
+            tmem_wait_ld(a);
+            tmem_ready(b);
+            largest(a, b, ks);
+          }
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < 2 && any > 64 * h; ++h) {
+            uint32_t a[32], b[32];
+            load_half(h, a, b);
+            float ks[4];
+            factors(h, ks);
+            largest(a, b, ks);
           }
         }
         const float m_new = fmaxf(m_used, tmax);
@@ -889,21 +943,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // pass 2: P vs = 2^(s * scale - m + log2 vs) as bf16 pairs over the columns
         // already read; the sums of P are those of a group divided by its vs
         const float m = m_used == -INFINITY ? 0.f : m_used;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-          if (any <= 64 * h) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) pk[c] = 0u;
-            tmem_st32(s_tm + 32 * h, pk);
-            continue;
-          }
-          uint32_t a[32], b[32];
-          load_half(h, a, b);
-          float ks[4];
-          factors(h, ks);
-          const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
+        auto powers = [&](int h, const uint32_t (&a)[32], const uint32_t (&b)[32],
+                          const float (&ks)[4], const float4& lv4) {
           const float lv[4] = {lv4.x - m, lv4.y - m, lv4.z - m, lv4.w - m};
+          uint32_t pk[32];
           uint64_t ls2[4];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
@@ -925,6 +968,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l0, l1;
             f2_unpack(ls2[q], l0, l1);
             l = fmaf(l0 + l1, iv[q], l);
+          }
+        };
+        if (plain) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t a[32], b[32];
+            tmem_ld32(a, s_tm + 64 * h);
+            tmem_ld32(b, s_tm + 64 * h + 32);
+            float ks[4];
+            factors(h, ks);
+            const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
+            tmem_wait_ld(a);
+            tmem_ready(b);
+            powers(h, a, b, ks, lv4);
+          }
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (any <= 64 * h) {  // no row of the warp sees a key of this half
+              uint32_t pz[32];
+#pragma unroll
+              for (int c = 0; c < 32; ++c) pz[c] = 0u;
+              tmem_st32(s_tm + 32 * h, pz);
+              continue;
+            }
+            uint32_t a[32], b[32];
+            load_half(h, a, b);
+            float ks[4];
+            factors(h, ks);
+            powers(h, a, b, ks, *reinterpret_cast<const float4*>(sct + 8 + 4 * h));
           }
         }
         tmem_wait_st();
@@ -1144,6 +1217,9 @@ TcStatus launch_prefill_q8(const AttentionQ8Params& a, bool e4m3, bool contig, i
     p.desc = static_cast<PieceDesc*>(workspace);
     p.rec = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + desc_bytes(sms));
   }
+  // (the item warp holds 32 rounds, one a lane)
+  if (p.rec_rows == 0 && items > sms && items / p.Hkv <= kSortPairs && items <= 32 * static_cast<int64_t>(sms))
+    p.sorted = static_cast<int32_t>(items / p.Hkv);
   *cuda_err = e4m3 ? launch<true>(tq, p, grid, stream) : launch<false>(tq, p, grid, stream);
   if (*cuda_err == cudaSuccess && p.rec_rows > 0)
     *cuda_err = launch_pdl_if(pdl_decode_enabled(), prefill_q8_join_kernel,

@@ -49,7 +49,7 @@ constexpr int kStageBytes = 2 * kOpBytes;             // K then V
 constexpr int kCodeTile = kKeys * kCodeRowBytes;      // 16 KiB
 constexpr int kOffCodes = kOffK + kStages * kStageBytes;  // a tile's codes of K, then of V
 constexpr int kTilesBytes = kOffCodes + 2 * kCodeTile;  // 224 KiB
-constexpr int kScaleRing = 4;                         // tiles whose scales are kept
+constexpr int kScaleRing = 8;                         // tiles whose scales are kept
 constexpr int kScaleFloats = 24;                      // of 8 groups: ks, log2 vs, 1 / vs
 constexpr int kOffScales = kTilesBytes + 512;
 constexpr int kOffHeld = kOffScales + kScaleRing * kScaleFloats * 4;  // a word a converter thread
@@ -344,12 +344,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t smem_base = smem_addr(smem);
 
-  if (warp >= kConvert0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-    // ================= converters: codes -> operands =================
-    // A thread takes 16 codes of rows row0, row0 + 16, ..  The eight lanes of a quarter
-    // warp take chunks 0-3 of one row and 4-7 of the next (or the other way), whose
-    // loads and swizzled stores meet different banks.
+  // The converters: codes -> operands.  A thread takes 16 codes of rows row0, row0 + 16, ..  The eight lanes of a quarter
+  // warp take chunks 0-3 of one row and 4-7 of the next (or the other way), whose loads
+  // and swizzled stores meet different banks.
+  auto convert = [&]() {
     const int row0 = (warp - kConvert0) * 4 + ((lane >> 4) << 1) + ((lane >> 2) & 1);
     const int ch = (lane & 3) + (((lane >> 2) ^ (lane >> 3)) & 1) * 4;  // chunk of 16 codes
     volatile uint32_t* held = reinterpret_cast<uint32_t*>(smem + kOffHeld);
@@ -367,49 +365,62 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(kFull, wait_or_abort(&B.cfull[kv], g & 1, abort, p.err));
           if (!ok) break;
           const unsigned char* from = smem + kOffCodes + kv * kCodeTile + row0 * 128 + ch * 16;
-          uint4 c[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) c[i] = *reinterpret_cast<const uint4*>(from + i * 16 * 128);
-          // The arrival must not overtake the loads, whose values are needed only later:
-          // a store of something made of all of them comes between (without it the next
-          // codes now and then came in first).
-          held[tid - 32 * kConvert0] =
-              c[0].x ^ c[1].x ^ c[2].x ^ c[3].x ^ c[4].x ^ c[5].x ^ c[6].x ^ c[7].x;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&B.cempty[kv]);
-          if (kv == 0 && warp == kConvert0 && lane < 8) {
-            // a scale below 2^-100 is that of zeros, whose P only enters the sum
-            float* sct = scales + (g & (kScaleRing - 1)) * kScaleFloats + 8 + lane;
-            const float vs = *sct < kScaleTiny ? kScaleTiny : *sct;
-            sct[0] = log2f(vs);
-            sct[8] = 1.f / vs;
-          }
-          if (kv == 1 && left < kKeys) {  // values past the context: 0 x whatever stands there
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (row0 + 16 * i >= left) c[i] = make_uint4(0u, 0u, 0u, 0u);
-          }
           uint64_t* empty = kv == 0 ? B.kempty : B.vempty;
-          if (g >= kStages && !__all_sync(kFull, wait_or_abort(&empty[s], ((g >> 1) - 1) & 1, abort,
-                                                               p.err))) {
-            ok = false;
-            break;
-          }
           unsigned char* to = smem + kOffK + s * kStageBytes + kv * kOpBytes;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            uint4 c[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4 lo, hi;
-            codes_to_bf16<kE4m3>(c[i], lo, hi);
-            const int r = row0 + 16 * i;
-            *reinterpret_cast<uint4*>(to + kv_chunk_offset(r, 2 * ch)) = lo;
-            *reinterpret_cast<uint4*>(to + kv_chunk_offset(r, 2 * ch + 1)) = hi;
+            for (int i = 0; i < 4; ++i)
+              c[i] = *reinterpret_cast<const uint4*>(from + (4 * half + i) * 16 * 128);
+            if (half == 1) {
+              // The arrival must not overtake the loads, whose values are needed only later:
+              // a store of something made of all of them comes between (without it the next
+              // codes now and then came in first).
+              held[tid - 32 * kConvert0] = c[0].x ^ c[1].x ^ c[2].x ^ c[3].x;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&B.cempty[kv]);
+            } else {
+              if (kv == 0 && warp == kConvert0 && lane < 8) {
+                // a scale below 2^-100 is that of zeros, whose P only enters the sum
+                float* sct = scales + (g & (kScaleRing - 1)) * kScaleFloats + 8 + lane;
+                const float vs = *sct < kScaleTiny ? kScaleTiny : *sct;
+                sct[0] = log2f(vs);
+                sct[8] = 1.f / vs;
+              }
+              if (g >= kStages && !__all_sync(kFull, wait_or_abort(&empty[s], ((g >> 1) - 1) & 1,
+                                                                   abort, p.err))) {
+                ok = false;
+                break;
+              }
+            }
+            if (kv == 1 && left < kKeys) {  // values past the context: 0 x whatever stands there
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (row0 + 16 * (4 * half + i) >= left) c[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 lo, hi;
+              codes_to_bf16<kE4m3>(c[i], lo, hi);
+              const int r = row0 + 16 * (4 * half + i);
+              *reinterpret_cast<uint4*>(to + kv_chunk_offset(r, 2 * ch)) = lo;
+              *reinterpret_cast<uint4*>(to + kv_chunk_offset(r, 2 * ch + 1)) = hi;
+            }
           }
+          if (!ok) break;
           fence_proxy_async_smem();  // the products read them through the async proxy
           __syncwarp();
           if (lane == 0) mbar_arrive(kv == 0 ? &B.kfull[s] : &B.vfull[s]);
         }
       }
     }
+  };
+
+  if (warp >= kConvert0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    // ================= converters: codes -> operands =================
+    convert();
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRoles));
   if (warp == kProducer) {
@@ -422,33 +433,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int prun = lane & 15;    // lanes 0-15 copy K of run prun, lanes 16-31 V
     const int kv = lane >> 4;
     const uint32_t bs = static_cast<uint32_t>(p.bs);
-    // block-table entry of run prun of tile j of `it` (-1: past the context or
-    // rejected); *off: its first row's place in the block
-    auto entry = [&](const PItem& it, int j, uint32_t* off) -> int32_t {
+    // The run's row of the cache in tile j of `it` (-1: past the context, or a bad table
+    // entry: the copy is skipped, stale rows, undefined output, no fault).  (Prefetched
+    // to L2 a tile ahead, everything got slower: 8 x 2048 281 -> 298 us.)
+    auto row_of = [&](const PItem& it, int j) -> int64_t {
       const int kpos = (it.t0 + j) * kKeys + prun * run;
-      int32_t e = -1;
-      if (prun < runs && kpos < it.ctx) {
-        const uint32_t at = static_cast<uint32_t>(kpos) / bs;
-        *off = static_cast<uint32_t>(kpos) - at * bs;
-        e = p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks + at];
+      if (prun >= runs || kpos >= it.ctx) return -1;
+      const uint32_t at = static_cast<uint32_t>(kpos) / bs;
+      const int32_t e = p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks + at];
+      if (p.checked && (e < 0 || e >= p.num_blocks)) {
+        record_error(p.err, p.err_code);
+        return -1;
       }
-      return e;
+      return cache_row(e, it.kvh, p.Hkv, bs, static_cast<uint32_t>(kpos) - at * bs);
     };
     int g = 0;             // tiles (of all items) whose K and V were both asked for
     bool half = false;     // K of tile g was asked for, not its V
     int nread = 0;
     PItem cur;
     bool ok = read_item(nread++, cur);
-    uint32_t off = 0;
-    int32_t e = ok && cur.ntiles > 0 ? entry(cur, 0, &off) : -1;  // of the next tile
+    int64_t row = ok && cur.ntiles > 0 ? row_of(cur, 0) : -1;  // of the next tile
     while (ok && cur.ntiles > 0) {
       PItem nx = cur;
       for (int j = 0; j < cur.ntiles; ++j) {
-        if (p.checked && e >= p.num_blocks) e = -1;  // (and below 0:) skip the copy: stale
-        const int kpos = (cur.t0 + j) * kKeys + prun * run;  // rows, undefined output, no fault
-        if (p.checked && e < 0 && prun < runs && kpos < cur.ctx) record_error(p.err, p.err_code);
-        const uint32_t loaded = __popc(__ballot_sync(kFull, lane < 16 && e >= 0));
-        const int64_t row = e >= 0 ? cache_row(e, cur.kvh, p.Hkv, bs, off) : 0;
+        const int kpos = (cur.t0 + j) * kKeys + prun * run;
+        const uint32_t loaded = __popc(__ballot_sync(kFull, lane < 16 && row >= 0));
         float* sc = scales + (g & (kScaleRing - 1)) * kScaleFloats + kv * 8;
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {  // K, then V, each when its slot is read
@@ -459,20 +468,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) mbar_arrive_expect_tx(&B.cfull[x], loaded * run * kCodeRowBytes);
           __syncwarp();
-          if (kv == x && e >= 0)
+          if (kv == x && row >= 0)
             bulk_copy_g2s(smem + kOffCodes + x * kCodeTile + prun * run * kCodeRowBytes,
                           (x == 0 ? p.k_codes : p.v_codes) + row * kCodeRowBytes,
                           static_cast<uint32_t>(run * kCodeRowBytes), &B.cfull[x], policy);
           if (x == 0) {
             // the scales of the run's groups, V's with K's (the softmax of S takes both);
             // 0 past the context, where P is 0.  The slot's last readers are done: the
-            // converters hold K of tile g - 1, so V of tile g - 2 is written, and
-            // the products of tile g - 4 that freed its stage are complete.
+            // converters hold K of tile g - 1, so that of tile g - 2 is written, the S of
+            // tile g - 4 that freed its stage is complete, and P of tile g - 5 was handed
+            // over before.
             if (prun < runs) {
-              const float* from = (kv == 0 ? p.k_scale : p.v_scale) + row / kGroupRows;
+              const float* from =
+                  (kv == 0 ? p.k_scale : p.v_scale) + (row >= 0 ? row / kGroupRows : 0);
               for (int i = 0; i < run / kGroupRows; ++i)
-                cp_async_4_or_zero(sc + prun * (run / kGroupRows) + i, from + (e >= 0 ? i : 0),
-                                   e >= 0 && kpos + i * kGroupRows < cur.ctx);
+                cp_async_4_or_zero(sc + prun * (run / kGroupRows) + i, from + (row >= 0 ? i : 0),
+                                   row >= 0 && kpos + i * kGroupRows < cur.ctx);
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                              smem_addr(&B.cfull[0]))
@@ -482,12 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         ++g;
-        // the next tile's entries load while this one lands
+        // the next tile is looked up while this one lands
         if (j + 1 < cur.ntiles) {
-          e = entry(cur, j + 1, &off);
+          row = row_of(cur, j + 1);
         } else {
           ok = read_item(nread++, nx);
-          e = ok && nx.ntiles > 0 ? entry(nx, 0, &off) : -1;
+          row = ok && nx.ntiles > 0 ? row_of(nx, 0) : -1;
         }
       }
       cur = nx;
@@ -580,12 +591,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         return static_cast<int64_t>(p.Hkv) * (kItemCost + it.ntiles);
       };
       PItem mine;
-      int64_t V = 0;
+      int64_t V = 0, units = 0;
       for (int c0 = 0; c0 < pairs; c0 += 32) {
-        int64_t units = pair_of_lane(c0, blockIdx.x == 0, mine);
+        units = pair_of_lane(c0, blockIdx.x == 0, mine);
+        int64_t sum = units;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(kFull, units, o);
-        V += units;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        V += sum;
       }
       const int64_t shares = max(static_cast<int64_t>(1), min(static_cast<int64_t>(P), V / kLeastUnits));
       const int64_t me = blockIdx.x;
@@ -594,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       PieceDesc desc = {};
       int64_t at = 0;
       for (int c0 = 0; ok && c0 < pairs && at < u1; c0 += 32) {
-        const int64_t units = pair_of_lane(c0, false, mine);
+        if (pairs > 32) units = pair_of_lane(c0, false, mine);
         int64_t end = units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -894,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if (plain) {
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             uint32_t a[32], b[32];
             tmem_ld32(a, s_tm + 64 * h);
@@ -971,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if (plain) {
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             uint32_t a[32], b[32];
             tmem_ld32(a, s_tm + 64 * h);

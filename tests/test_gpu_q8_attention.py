@@ -280,6 +280,18 @@ def test_prefill_rows_behind_the_last_chunk():
     b.check(out, half_step=q8_ref.PREFILL)
 
 
+@pytest.mark.parametrize("dtype", q8_ref.FORMATS)
+@pytest.mark.parametrize("new,cached", [([300] * 40, [10] * 40), ([8] * 60, [700] * 60),
+                                        ([20] * 5, [3000] * 5), ([33] * 80, [500] * 80)])
+def test_prefill_again(dtype, new, cached):
+    """Nothing depends on timing: every call gives the same bits."""
+    b = Batch(dtype, "paged", 8, 2, [n + c for n, c in zip(new, cached)], new, bs=32)
+    first = b.prefill().clone()
+    b.check(first, half_step=q8_ref.PREFILL)
+    for _ in range(20):
+        assert torch.equal(b.prefill(), first)
+
+
 def test_prefill_empty_chunks():
     b = Batch(torch.int8, "paged", 8, 2, [40, 70, 0, 5], [0, 30, 0, 5])
     b.check(b.prefill(), half_step=q8_ref.PREFILL)

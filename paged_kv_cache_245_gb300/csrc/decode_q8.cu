@@ -52,9 +52,13 @@ constexpr int kStageQ8 = kStageTiles * 2 * kTileCodes;
 struct DecodeQ8Params : TcParams {
   const float* k_scale;
   const float* v_scale;
+  // Short chunks: sequence i of the schedule is token group i % groups of chunk i /
+  // groups, group_tokens tokens, as 16 rows (token, query head) where decode has 8.
+  const int32_t* cu_q;
+  int32_t groups, group_tokens, max_q;
 };
 
-// W warps, S stages each; MH query heads of a KV head (4, or 8).
+// W warps, S stages each; MH rows (query heads) of a KV head (4, 8; chunks: 16).
 template <int W, int S, int MH>
 struct Q8Smem {
   static constexpr int kPieceFloats = MH * kRecStride;  // o[128], m, l of each head
@@ -66,7 +70,9 @@ struct Q8Smem {
   static constexpr int kPairOff = kRunOff + 2 * 8;               // pairs of the pieces [W][2]
   static constexpr int kCtxOff = kPairOff + W * 2 * 4;
   static constexpr int kReqOff = kCtxOff + kTcMaxSeqs * 4;
-  static constexpr int kPrefixOff = kReqOff + kTcMaxSeqs * 4;
+  static constexpr int kRowOff = kReqOff + kTcMaxSeqs * 4;  // chunks: a group's first row of q
+  static constexpr int kTokOff = kRowOff + (MH == 16 ? kTcMaxSeqs * 4 : 0);  // and its tokens
+  static constexpr int kPrefixOff = kTokOff + (MH == 16 ? kTcMaxSeqs * 4 : 0);
   static constexpr int kTotal = kPrefixOff + (kTcMaxSeqs + 1) * 4 + 1024;  // + 1 KiB alignment
   static_assert(kTotal <= 232448, "shared memory per CTA exceeds 227 KiB");
   static_assert(kPieceFloats * 4 <= S * kStageQ8, "a piece fits a warp's stages");
@@ -81,12 +87,14 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 
 }  // namespace
 
-template <bool kContig, bool kE4m3, int W, int S, int MH>
+template <bool kContig, bool kE4m3, bool kChunks, int W, int S, int MH>
 __global__ void __launch_bounds__(W * 32, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ DecodeQ8Params p) {
   using L = Q8Smem<W, S, MH>;
+  constexpr int NT = kChunks ? 2 : 1;  // tiles of 8 rows of queries
+  static_assert(MH <= 8 * NT && kChunks == (MH == 16), "rows of the tiles");
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
 
@@ -105,7 +113,12 @@ __global__ void __launch_bounds__(W * 32, 1)
   int32_t* piece_pair = reinterpret_cast<int32_t*>(smem + L::kPairOff);  // [W][first, last]
   int32_t* ctx_s = reinterpret_cast<int32_t*>(smem + L::kCtxOff);
   int32_t* req_s = reinterpret_cast<int32_t*>(smem + L::kReqOff);
+  int32_t* row_s = reinterpret_cast<int32_t*>(smem + L::kRowOff);  // kChunks
+  int32_t* tok_s = reinterpret_cast<int32_t*>(smem + L::kTokOff);
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefixOff);
+  // rows of sequence i, and its first row of q and out in units of Hq rows
+  auto rows_of = [&](int i) -> int { return kChunks ? tok_s[i] * G : G; };
+  auto token_of = [&](int i) -> int { return kChunks ? row_s[i] : i; };
   // the record of head h of a run's first (0) or last (1) piece
   auto piece = [&](int w, int last, int h) -> float* {
     unsigned char* base = last ? smem + L::kStagesOff + w * S * kStageQ8
@@ -128,9 +141,30 @@ __global__ void __launch_bounds__(W * 32, 1)
 
   // ---- tile counts and their prefix over sequences
   for (int i = tid; i < B; i += W * 32) {
-    const int ctx = tc_context(p, i, kContig, c == 0);
-    ctx_s[i] = ctx;
-    if (kContig) req_s[i] = ctx > 0 ? p.req_ids[i] : 0;
+    if constexpr (kChunks) {
+      // the keys that the group's last token sees
+      const int seq = i / p.groups, t0 = (i - seq * p.groups) * p.group_tokens;
+      const int q0 = p.cu_q[seq], n = p.cu_q[seq + 1] - q0;
+      int ctx = p.ctx_lens[seq], req = kContig ? p.req_ids[seq] : 0;
+      if (p.checked) {
+        const int64_t cap = kContig ? p.bs : static_cast<int64_t>(p.max_blocks) * p.bs;
+        const bool bad = n < 0 || n > p.max_q || ctx < n || ctx > cap;
+        if ((bad || req < 0 || (kContig && req >= p.max_reqs)) && n != 0) {
+          if (c == 0 && t0 == 0) record_error(p.err, bad ? kErrContext : kErrReqId);
+          ctx = 0;  // the sequence is left unwritten
+          req = 0;
+        }
+      }
+      const int tokens = min(p.group_tokens, n - t0);
+      ctx_s[i] = ctx > 0 && tokens > 0 ? max(ctx - n + t0 + tokens, 0) : 0;
+      row_s[i] = q0 + t0;
+      tok_s[i] = tokens;
+      if (kContig) req_s[i] = req;
+    } else {
+      const int ctx = tc_context(p, i, kContig, c == 0);
+      ctx_s[i] = ctx;
+      if (kContig) req_s[i] = ctx > 0 ? p.req_ids[i] : 0;
+    }
   }
   __syncthreads();
   auto seq_tiles = [&](int i) -> int { return (ctx_s[i] + 15) >> 4; };
@@ -155,7 +189,7 @@ __global__ void __launch_bounds__(W * 32, 1)
   __syncthreads();
 
   // outputs of empty contexts are zeros (sequences c, c + P, ... of this CTA)
-  for (int i = c; i < B; i += P) {
+  for (int i = c; i < B && !kChunks; i += P) {
     if (ctx_s[i] != 0) continue;
     uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(i) * p.Hq * kHeadDim);
     for (int k = tid; k < p.Hq * kHeadDim / 8; k += W * 32) o[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -204,9 +238,15 @@ __global__ void __launch_bounds__(W * 32, 1)
   const int g = lane >> 2;   // accumulator row group
   const int tq = lane & 3;   // accumulator column pair
 
-  // Elements 32 tq .. + 31 of head g's query row (g < G).
-  auto q_row = [&](int seq, int kvh) {
-    return p.q + (static_cast<int64_t>(seq) * p.Hq + kvh * G + (g < G ? g : 0)) * kHeadDim + 32 * tq;
+  // Elements 32 tq .. + 31 of query row r of a sequence (row 0's where it has fewer).
+  auto q_row = [&](int seq, int kvh, int r) {
+    int token = token_of(seq), head = r;
+    if (r >= rows_of(seq)) head = 0;
+    if (kChunks) {
+      token += head / G;
+      head %= G;
+    }
+    return p.q + (static_cast<int64_t>(token) * p.Hq + kvh * G + head) * kHeadDim + 32 * tq;
   };
   // the pair after `sg` (its tiles start at sg.pend < hi)
   auto next_seg = [&](const TcSeg& sg) -> TcSeg {
@@ -238,7 +278,9 @@ __global__ void __launch_bounds__(W * 32, 1)
       in = static_cast<int>(iseg.x0 - iseg.pstart);
       in_end = static_cast<int>(iseg.x1 - iseg.pstart);
       // its query rows, which the pair's start waits for
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(q_row(iseg.seq, iseg.kvh)));
+#pragma unroll
+      for (int y = 0; y < NT; ++y)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q_row(iseg.seq, iseg.kvh, 8 * y + g)));
       const uint32_t pos = static_cast<uint32_t>(in + lane) * 16;
       if (kContig) {
         off = pos;
@@ -246,7 +288,8 @@ __global__ void __launch_bounds__(W * 32, 1)
       } else {
         blk = pos / bs32;
         off = pos - blk * bs32;
-        table = p.block_tables + static_cast<int64_t>(iseg.seq) * p.max_blocks;
+        table = p.block_tables +
+                static_cast<int64_t>(kChunks ? iseg.seq / p.groups : iseg.seq) * p.max_blocks;
       }
     };
     auto issue = [&](int stage) {
@@ -304,23 +347,37 @@ __global__ void __launch_bounds__(W * 32, 1)
 
     TcSeg seg = tc_seg_at(lo, hi, seq_lo, prefix, Hkv);
     while (true) {
-      uint32_t qb[8][2];
-      float qs0, qs1;  // score units of heads 2 tq and 2 tq + 1
-      {
-        uint4 qn[4];
-        const uint4* row = reinterpret_cast<const uint4*>(q_row(seg.seq, seg.kvh));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) qn[k] = g < G ? __ldg(row + k) : make_uint4(0u, 0u, 0u, 0u);
-        const float down = queries_to_half(qn, qb);
-        qs0 = __shfl_sync(kFull, down, 8 * tq) * p.qscale;
-        qs1 = __shfl_sync(kFull, down, 8 * tq + 4) * p.qscale;
-      }
       const int ctx = ctx_s[seg.seq];
-      // O^T of elements 16 i + 2 g (0) and + 1 (1): heads 2 tq and 2 tq + 1 as a pair
-      uint64_t acc[8][2];
-      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      const int rows = rows_of(seg.seq);
+      uint32_t qb[NT][8][2];
+      float qs[NT][2];  // score units of rows 8 y + 2 tq and + 1
+      int lim[NT][2];   // positions that they see (chunks)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = 0ull;
+      for (int y = 0; y < NT; ++y) {
+        uint4 qn[4];
+        const uint4* row = reinterpret_cast<const uint4*>(q_row(seg.seq, seg.kvh, 8 * y + g));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          qn[k] = 8 * y + g < rows ? __ldg(row + k) : make_uint4(0u, 0u, 0u, 0u);
+        const float down = queries_to_half(qn, qb[y]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          qs[y][e] = __shfl_sync(kFull, down, 8 * tq + 4 * e) * p.qscale;
+          lim[y][e] = ctx;
+          if (kChunks)
+            lim[y][e] -= max(tok_s[seg.seq] - 1 - (8 * y + 2 * tq + e) / G, 0);
+        }
+      }
+      // O^T of elements 16 i + 2 g (0) and + 1 (1): rows 8 y + 2 tq and + 1 as a pair
+      uint64_t acc[NT][8][2];
+      float m[NT][2], l[NT][2];
+#pragma unroll
+      for (int y = 0; y < NT; ++y) {
+        m[y][0] = m[y][1] = -INFINITY;
+        l[y][0] = l[y][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[y][i][0] = acc[y][i][1] = 0ull;
+      }
 
       const int x_end = static_cast<int>(seg.x1 - seg.pstart);
       for (int x = static_cast<int>(seg.x0 - seg.pstart); x < x_end; x += kStageTiles) {
@@ -344,20 +401,25 @@ __global__ void __launch_bounds__(W * 32, 1)
           __syncwarp();
         }
 
-        // ---- S^T = K . Q^T; s[t]: scores of tokens g (0, 1) and g + 8 (2, 3) of tile
-        // t, heads 2tq and 2tq + 1
-        float s[kStageTiles][4];
+        // ---- S^T = K . Q^T; s[y][t]: scores of tokens g (0, 1) and g + 8 (2, 3) of
+        // tile t, rows 8 y + 2 tq and + 1
+        float s[NT][kStageTiles][4];
         float vs[kStageTiles];
 #pragma unroll
         for (int t = 0; t < kStageTiles; ++t) {
           if (t > 0 && !two) {
-            s[t][0] = s[t][1] = s[t][2] = s[t][3] = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < NT; ++y) s[y][t][0] = s[y][t][1] = s[y][t][2] = s[y][t][3] = -INFINITY;
             continue;
           }
           const float2 sc = scales[stage * kStageTiles + t];
           vs[t] = sc.y;
           const unsigned char* kt = st + t * 2 * kTileCodes;
-          float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+          float sa[NT][4], sb[NT][4];
+#pragma unroll
+          for (int y = 0; y < NT; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sa[y][e] = sb[y][e] = 0.f;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const unsigned char* at = kt + (half ? koff1 : koff0);
@@ -370,56 +432,73 @@ __global__ void __launch_bounds__(W * 32, 1)
               halves_of<kE4m3>(w0[e], a[0], a[2]);
               halves_of<kE4m3>(w1[e], a[1], a[3]);
               const int ks = 4 * half + e;
-              if (ks & 1) mma_f16_16816(sb, a, qb[ks][0], qb[ks][1]);
-              else mma_f16_16816(sa, a, qb[ks][0], qb[ks][1]);
+#pragma unroll
+              for (int y = 0; y < NT; ++y) {
+                if (ks & 1) mma_f16_16816(sb[y], a, qb[y][ks][0], qb[y][ks][1]);
+                else mma_f16_16816(sa[y], a, qb[y][ks][0], qb[y][ks][1]);
+              }
             }
           }
-          const float f0 = qs0 * sc.x, f1 = qs1 * sc.x;
-          const bool v0 = g + 16 * t < nvalid, v1 = g + 16 * t + 8 < nvalid;
-          s[t][0] = v0 ? (sa[0] + sb[0]) * f0 : -INFINITY;
-          s[t][1] = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;
-          s[t][2] = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;
-          s[t][3] = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;
+#pragma unroll
+          for (int y = 0; y < NT; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = g + 16 * t + (e >> 1) * 8;  // row of the stage
+              const bool seen =
+                  at < nvalid && (!kChunks || x * 16 + at < lim[y][e & 1]);
+              s[y][t][e] = seen ? (sa[y][e] + sb[y][e]) * (qs[y][e & 1] * sc.x) : -INFINITY;
+            }
         }
 
-        // ---- online softmax, per head column
-        float mx0 = m0, mx1 = m1;
+        // ---- online softmax, per row
+        uint32_t pb[NT][kStageTiles][2];
 #pragma unroll
-        for (int t = 0; t < kStageTiles; ++t) {
-          mx0 = fmaxf(mx0, fmaxf(s[t][0], s[t][2]));
-          mx1 = fmaxf(mx1, fmaxf(s[t][1], s[t][3]));
-        }
+        for (int y = 0; y < NT; ++y) {
+          float mx0 = m[y][0], mx1 = m[y][1];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, o));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, o));
-        }
-        if (mx0 > m0 || mx1 > m1) {
-          // (a maximum of -inf stays; 0 where it was that and no longer is)
-          const float a0 = mx0 > m0 ? fast_exp2(m0 - mx0) : 1.f;
-          const float a1 = mx1 > m1 ? fast_exp2(m1 - mx1) : 1.f;
-          const uint64_t a2 = umma::f2_pack(__float_as_uint(a0), __float_as_uint(a1));
-          l0 *= a0;
-          l1 *= a1;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[i][0] = umma::f2_mul(acc[i][0], a2);
-            acc[i][1] = umma::f2_mul(acc[i][1], a2);
+          for (int t = 0; t < kStageTiles; ++t) {
+            mx0 = fmaxf(mx0, fmaxf(s[y][t][0], s[y][t][2]));
+            mx1 = fmaxf(mx1, fmaxf(s[y][t][1], s[y][t][3]));
           }
-          m0 = mx0;
-          m1 = mx1;
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, o));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, o));
+          }
+          if (mx0 > m[y][0] || mx1 > m[y][1]) {
+            // (a maximum of -inf stays; 0 where it was that and no longer is)
+            const float a0 = mx0 > m[y][0] ? fast_exp2(m[y][0] - mx0) : 1.f;
+            const float a1 = mx1 > m[y][1] ? fast_exp2(m[y][1] - mx1) : 1.f;
+            const uint64_t a2 = umma::f2_pack(__float_as_uint(a0), __float_as_uint(a1));
+            l[y][0] *= a0;
+            l[y][1] *= a1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[y][i][0] = umma::f2_mul(acc[y][i][0], a2);
+              acc[y][i][1] = umma::f2_mul(acc[y][i][1], a2);
+            }
+            m[y][0] = mx0;
+            m[y][1] = mx1;
+          }
+          // (chunks: a row may see nothing of a run's part of the pair)
+          const float f0 = kChunks && m[y][0] == -INFINITY ? 0.f : m[y][0];
+          const float f1 = kChunks && m[y][1] == -INFINITY ? 0.f : m[y][1];
+#pragma unroll
+          for (int t = 0; t < kStageTiles; ++t) {
+            if (t > 0 && !two) break;
+            const float p0 = fast_exp2(s[y][t][0] - f0), p2 = fast_exp2(s[y][t][2] - f0);
+            const float p1 = fast_exp2(s[y][t][1] - f1), p3 = fast_exp2(s[y][t][3] - f1);
+            l[y][0] += p0 + p2;
+            l[y][1] += p1 + p3;
+            // P^T as the B operand, rounded to fp16 once
+            pb[y][t][0] = movmatrix_trans(pack_half2(p0, p1));  // tokens 0..7
+            pb[y][t][1] = movmatrix_trans(pack_half2(p2, p3));  // tokens 8..15
+          }
         }
         // ---- O^T += vs (V^T . P^T)
 #pragma unroll
         for (int t = 0; t < kStageTiles; ++t) {
           if (t > 0 && !two) break;
-          const float p0 = fast_exp2(s[t][0] - m0), p2 = fast_exp2(s[t][2] - m0);
-          const float p1 = fast_exp2(s[t][1] - m1), p3 = fast_exp2(s[t][3] - m1);
-          l0 += p0 + p2;
-          l1 += p1 + p3;
-          // P^T as the B operand, rounded to fp16 once
-          const uint32_t b0 = movmatrix_trans(pack_half2(p0, p1));  // tokens 0..7
-          const uint32_t b1 = movmatrix_trans(pack_half2(p2, p3));  // tokens 8..15
           const uint64_t vs2 = umma::f2_pack(__float_as_uint(vs[t]), __float_as_uint(vs[t]));
           const uint32_t vaddr = smem_addr(st) + (2 * t + 1) * kTileCodes + vrow * 128;
 #pragma unroll
@@ -431,12 +510,17 @@ __global__ void __launch_bounds__(W * 32, 1)
               uint32_t a[4];
               halves_across<kE4m3>(r[2 * k], a[0], a[1]);
               halves_across<kE4m3>(r[2 * k + 1], a[2], a[3]);
-              float d[4];
-              mma_f16_16816_zero(d, a, b0, b1);
-              acc[i + k][0] = umma::f2_fma(
-                  umma::f2_pack(__float_as_uint(d[0]), __float_as_uint(d[1])), vs2, acc[i + k][0]);
-              acc[i + k][1] = umma::f2_fma(
-                  umma::f2_pack(__float_as_uint(d[2]), __float_as_uint(d[3])), vs2, acc[i + k][1]);
+#pragma unroll
+              for (int y = 0; y < NT; ++y) {
+                float d[4];
+                mma_f16_16816_zero(d, a, pb[y][t][0], pb[y][t][1]);
+                acc[y][i + k][0] =
+                    umma::f2_fma(umma::f2_pack(__float_as_uint(d[0]), __float_as_uint(d[1])), vs2,
+                                 acc[y][i + k][0]);
+                acc[y][i + k][1] =
+                    umma::f2_fma(umma::f2_pack(__float_as_uint(d[2]), __float_as_uint(d[3])), vs2,
+                                 acc[y][i + k][1]);
+              }
             }
           }
         }
@@ -452,45 +536,48 @@ __global__ void __launch_bounds__(W * 32, 1)
 
       // ---- the pair's part in this run is done
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        l0 += __shfl_xor_sync(kFull, l0, o);
-        l1 += __shfl_xor_sync(kFull, l1, o);
-      }
-      if (seg.x0 == seg.pstart && seg.x1 == seg.pend) {  // whole
-        const float inv0 = l0 != 0.f ? 1.f / l0 : 0.f, inv1 = l1 != 0.f ? 1.f / l1 : 0.f;
-        uint16_t* row = p.out + (static_cast<int64_t>(seg.seq) * p.Hq + seg.kvh * G + 2 * tq) *
-                                    kHeadDim + 2 * g;
+      for (int y = 0; y < NT; ++y)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float x0, x1, y0, y1;
-          umma::f2_unpack(acc[i][0], x0, x1);
-          umma::f2_unpack(acc[i][1], y0, y1);
-          if (2 * tq < G) *reinterpret_cast<uint32_t*>(row + 16 * i) = pack_bf16x2(x0 * inv0, y0 * inv0);
-          if (2 * tq + 1 < G)
-            *reinterpret_cast<uint32_t*>(row + kHeadDim + 16 * i) = pack_bf16x2(x1 * inv1, y1 * inv1);
+        for (int o = 4; o < 32; o <<= 1) {
+          l[y][0] += __shfl_xor_sync(kFull, l[y][0], o);
+          l[y][1] += __shfl_xor_sync(kFull, l[y][1], o);
         }
-      } else {
-        const int last = seg.x0 != lo;  // a run's first piece, or (not first) its last
-        if (2 * tq < MH) {
-          float* r0 = piece(warp, last, 2 * tq);
-          float* r1 = r0 + kRecStride;
+      const bool whole = seg.x0 == seg.pstart && seg.x1 == seg.pend;
+      const int last = seg.x0 != lo;  // a run's first piece, or (not first) its last
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float x0, x1, y0, y1;
-            umma::f2_unpack(acc[i][0], x0, x1);
-            umma::f2_unpack(acc[i][1], y0, y1);
-            *reinterpret_cast<float2*>(r0 + 16 * i + 2 * g) = make_float2(x0, y0);
-            *reinterpret_cast<float2*>(r1 + 16 * i + 2 * g) = make_float2(x1, y1);
-          }
-          if (g == 0) {
-            r0[128] = m0;
-            r0[129] = l0;
-            r1[128] = m1;
-            r1[129] = l1;
+      for (int y = 0; y < NT; ++y)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * y + 2 * tq + e;
+          if (r >= rows) continue;
+          if (whole) {
+            const float inv = l[y][e] != 0.f ? 1.f / l[y][e] : 0.f;
+            const int token = token_of(seg.seq) + (kChunks ? r / G : 0);
+            uint16_t* row = p.out + (static_cast<int64_t>(token) * p.Hq + seg.kvh * G +
+                                     (kChunks ? r % G : r)) * kHeadDim + 2 * g;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x[2], z[2];
+              umma::f2_unpack(acc[y][i][0], x[0], x[1]);
+              umma::f2_unpack(acc[y][i][1], z[0], z[1]);
+              *reinterpret_cast<uint32_t*>(row + 16 * i) = pack_bf16x2(x[e] * inv, z[e] * inv);
+            }
+          } else {
+            float* rec = piece(warp, last, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x[2], z[2];
+              umma::f2_unpack(acc[y][i][0], x[0], x[1]);
+              umma::f2_unpack(acc[y][i][1], z[0], z[1]);
+              *reinterpret_cast<float2*>(rec + 16 * i + 2 * g) = make_float2(x[e], z[e]);
+            }
+            if (g == 0) {
+              rec[128] = m[y][e];
+              rec[129] = l[y][e];
+            }
           }
         }
-        if (lane == 0) piece_pair[2 * warp + last] = seg.seq * Hkv + seg.kvh;
-      }
+      if (!whole && lane == 0) piece_pair[2 * warp + last] = seg.seq * Hkv + seg.kvh;
       if (seg.x1 >= hi) break;
       seg = next_seg(seg);
     }
@@ -511,17 +598,19 @@ __global__ void __launch_bounds__(W * 32, 1)
   const int prev_pair = __shfl_sync(kFull, lane_pair, before != 0u ? 31 - __clz(before) : lane);
   const uint32_t starts =
       __ballot_sync(kFull, lane_pair >= 0 && (before == 0u || prev_pair != lane_pair));
-  const int tasks = __popc(starts) * G;
+  const int heads = kChunks ? p.group_tokens * G : G;  // rows of a pair at most
+  const int tasks = __popc(starts) * heads;
   // (last group first: what a later CTA waits for goes out before a wait for earlier ones)
   for (int task = tasks - 1 - warp; task >= 0; task -= W) {
-    const int grp = static_cast<uint32_t>(task) / static_cast<uint32_t>(G);
-    const int hh = task - grp * G;
+    const int grp = static_cast<uint32_t>(task) / static_cast<uint32_t>(heads);
+    const int hh = task - grp * heads;
     uint32_t rest = starts;
     for (int k = 0; k < grp; ++k) rest &= rest - 1;
     const int n = __ffs(rest) - 1;  // pieces n .. end - 1 are this pair's (or empty)
     rest &= rest - 1;
     const int end = rest != 0u ? __ffs(rest) - 1 : 2 * W;
     const int pair = __shfl_sync(kFull, lane_pair, n);
+    if (kChunks && hh >= rows_of(static_cast<uint32_t>(pair) / static_cast<uint32_t>(Hkv))) continue;
     // lane j < end - n derives the weight of piece n + j (2 W <= 32 lanes)
     const int k = n + lane;
     const bool have = k < end && (taken >> k & 1u);
@@ -559,13 +648,14 @@ __global__ void __launch_bounds__(W * 32, 1)
     int cf = c, cl = c;
     if (sg.pstart < cta_run[0] || sg.pend > cta_run[1])
       tc_pair_ctas(sg, prefix, Hkv, p.seg_cost, V, P, &cf, &cl);
-    const int qh = sg.kvh * G + hh;
+    const int token = token_of(sg.seq) + (kChunks ? hh / G : 0);
+    const int qh = sg.kvh * G + (kChunks ? hh % G : hh);
     if (cf == cl) {
-      tc_write_out(p, sg.seq, qh, lane, o4, Mr, Ls);
+      tc_write_out(p, token, qh, lane, o4, Mr, Ls);
     } else if (cl != c) {
       tc_store_piece(p.rec + (static_cast<int64_t>(c) * kTcRecHeads + hh) * kRecStride, p.tag,
                      lane, o4, Mr, Ls);
-    } else if (!tc_merge_earlier(p, sg.seq, qh, hh, cf, c, V, P, lane, o4, Mr, Ls) && lane == 0) {
+    } else if (!tc_merge_earlier(p, token, qh, hh, cf, c, V, P, lane, o4, Mr, Ls) && lane == 0) {
       record_error(p.err, kErrTimeout);
     }
   }
@@ -573,7 +663,7 @@ __global__ void __launch_bounds__(W * 32, 1)
 
 namespace {
 
-template <bool kContig, bool kE4m3, int W, int S, int MH>
+template <bool kContig, bool kE4m3, bool kChunks, int W, int S, int MH>
 cudaError_t launch_shape(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& p0,
                          int num_ctas, cudaStream_t stream) {
   using L = Q8Smem<W, S, MH>;
@@ -582,13 +672,14 @@ cudaError_t launch_shape(const CUtensorMap& tk, const CUtensorMap& tv, const Dec
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
-  auto kernel = decode_q8_kernel<kContig, kE4m3, W, S, MH>;
+  auto kernel = decode_q8_kernel<kContig, kE4m3, kChunks, W, S, MH>;
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
   }
-  const int chunk = tc_chunk_seqs(p0.max_context);
+  // (chunks come as one launch's sequences at most)
+  const int chunk = kChunks ? p0.num_seqs : tc_chunk_seqs(p0.max_context);
   for (int s0 = 0; s0 < p0.num_seqs; s0 += chunk) {
     DecodeQ8Params p = p0;
     p.num_seqs = (p0.num_seqs - s0) < chunk ? (p0.num_seqs - s0) : chunk;
@@ -608,8 +699,10 @@ cudaError_t launch_shape(const CUtensorMap& tk, const CUtensorMap& tv, const Dec
 template <bool kContig, bool kE4m3>
 cudaError_t launch_heads(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& p,
                          int num_ctas, cudaStream_t stream) {
-  return p.G <= 4 ? launch_shape<kContig, kE4m3, 12, 2, 4>(tk, tv, p, num_ctas, stream)
-                  : launch_shape<kContig, kE4m3, 10, 2, 8>(tk, tv, p, num_ctas, stream);
+  if (p.cu_q != nullptr)
+    return launch_shape<kContig, kE4m3, true, 8, 2, 16>(tk, tv, p, num_ctas, stream);
+  return p.G <= 4 ? launch_shape<kContig, kE4m3, false, 12, 2, 4>(tk, tv, p, num_ctas, stream)
+                  : launch_shape<kContig, kE4m3, false, 10, 2, 8>(tk, tv, p, num_ctas, stream);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
@@ -641,6 +734,23 @@ bool encode_codes(CUtensorMap* map, const void* base, int64_t rows) {
 
 }  // namespace
 
+// Tokens that 16 rows hold.
+static int chunk_group_tokens(int G) { return 16 / G; }
+
+// Chunks of one group of 16 rows; of two where they hold 1.5 groups' tokens on average
+// at most (drafts of 2 to 8 tokens: the second group of the shorter ones is empty).
+// More than 8 rows of few pairs spend their time in the join.  8 KV heads of 4 query
+// heads, int8, us a call, this kernel / the tiles of prefill: 64 x 4 tokens after 2000
+// 73.9 / 118, 16 x 4 28.8 / 42.2, 16 drafts 33.2 / 42; 32 x 8 (two full groups) 72.9 /
+// 68.0, 64 x 8 132 / 119; 1 x 2 16.9 / 20.4, 2 x 4 21.5 / 21.4, 1 x 4 26.3 / 20.5.
+bool chunks_by_runs(int num_tokens, int num_seqs, int max_q, int Hkv, int G, int max_context) {
+  const int group = chunk_group_tokens(G);
+  const int groups = (max_q + group - 1) / group;
+  if (groups > 1 && (groups > 2 || 2ll * num_tokens > 3ll * group * num_seqs)) return false;
+  if (max_q * G > 8 && static_cast<int64_t>(num_seqs) * Hkv < 16) return false;
+  return num_seqs <= tc_chunk_seqs(max_context) / groups;
+}
+
 TcStatus launch_decode_q8(const AttentionQ8Params& a, bool e4m3, bool contig, int num_ctas,
                           void* workspace, cudaStream_t stream, cudaError_t* cuda_err) {
   *cuda_err = cudaSuccess;
@@ -671,6 +781,13 @@ TcStatus launch_decode_q8(const AttentionQ8Params& a, bool e4m3, bool contig, in
   p.err = a.err;
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
+  if (a.cu_q != nullptr) {
+    p.cu_q = a.cu_q;
+    p.group_tokens = chunk_group_tokens(a.G);
+    p.groups = (a.max_q + p.group_tokens - 1) / p.group_tokens;
+    p.num_seqs = a.num_seqs * p.groups;
+    p.max_q = a.max_q;
+  }
   if (contig)
     *cuda_err = e4m3 ? launch_heads<true, true>(tk, tv, p, num_ctas, stream)
                      : launch_heads<true, false>(tk, tv, p, num_ctas, stream);

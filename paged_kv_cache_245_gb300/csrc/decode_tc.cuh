@@ -291,23 +291,36 @@ __device__ __forceinline__ bool tc_merge_earlier(const TcParams& p, int seq, int
     L += w;
   };
   bool ok = true;
-  for (int k = cf; k < c; ++k) {
-    if (!tc_range_nonempty(k, V, P)) continue;
-    uint64_t* rec = p.rec + (static_cast<int64_t>(k) * kTcRecHeads + hh) * kRecStride;
-    TcPieceWords pw;
-    float m, l;
-    float4 o;
-    tc_issue_piece(rec, lane, pw);
-    bool have = __all_sync(kFull, tc_parse_piece(pw, p.tag, &o, &m, &l));
-    for (const unsigned long long t0 = global_timer_ns();
-         !have && global_timer_ns() - t0 < kWaitLimitNs;) {
-      __nanosleep(128);
-      tc_issue_piece(rec, lane, pw);
-      have = __all_sync(kFull, tc_parse_piece(pw, p.tag, &o, &m, &l));
+  constexpr int kAtOnce = 4;  // records on the way at once
+  for (int k0 = cf; k0 < c; k0 += kAtOnce) {
+    TcPieceWords pw[kAtOnce];
+    bool there[kAtOnce];
+    auto record = [&](int j) {
+      return p.rec + (static_cast<int64_t>(k0 + j) * kTcRecHeads + hh) * kRecStride;
+    };
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      there[j] = k0 + j < c && tc_range_nonempty(k0 + j, V, P);
+      if (there[j]) tc_issue_piece(record(j), lane, pw[j]);
     }
-    ok = ok && have;
-    fold(m, l, o);
-    tc_clear_piece(rec, lane);
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      if (!there[j]) continue;
+      float m, l;
+      float4 o;
+      bool have = __all_sync(kFull, tc_parse_piece(pw[j], p.tag, &o, &m, &l));
+      if (!have) {
+        const unsigned long long t0 = global_timer_ns();
+        do {
+          __nanosleep(128);
+          tc_issue_piece(record(j), lane, pw[j]);
+          have = __all_sync(kFull, tc_parse_piece(pw[j], p.tag, &o, &m, &l));
+        } while (!have && global_timer_ns() - t0 < kWaitLimitNs);
+      }
+      ok = ok && have;
+      fold(m, l, o);
+      tc_clear_piece(record(j), lane);
+    }
   }
   fold(m_own, l_own, o_own);
   const float inv = empty_sum<true>(L) ? 0.f : 1.f / L;

@@ -1511,15 +1511,18 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
   p.checked = g_checked.load();
   p.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
   p.err = err;
-  if (cu_q == nullptr) {
+  const bool e4m3 = cache->format == PKV_Q8_E4M3;
+  if (cu_q == nullptr ||
+      pkv::chunks_by_runs(num_tokens, num_seqs, p.max_q, h.num_kv_heads, p.G, max_context)) {
     const size_t need = pkv::tc_workspace_bytes(tc_ctas(sms));
     if (!workspace || workspace_bytes < need)
       return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
                   workspace ? workspace_bytes : size_t{0});
-    if (!aligned(workspace, 16)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
-    const bool e4m3 = cache->format == PKV_Q8_E4M3;
+    const unsigned at = cu_q ? 32 : 16;
+    if (!aligned(workspace, at))
+      return fail(PKV_ERR_WORKSPACE, "workspace must be %u-byte aligned", at);
     const int variant = g_variant.load();
-    if (variant <= 1) {
+    if (variant <= 1 && cu_q == nullptr) {
       pkv::ClusterRoom room;
       const cudaError_t re = pkv::room_decode_q8_cluster(e4m3, &room);
       if (re != cudaSuccess) return cuda_fail(re, "cluster query");
@@ -1539,7 +1542,7 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
                               static_cast<cudaStream_t>(stream), &ce);
     if (ts == pkv::TcStatus::kEncodeFailed)
       return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for the K/V cache");
-    if (ts != pkv::TcStatus::kOk) return cuda_fail(ce, "q8 decode launch");
+    if (ts != pkv::TcStatus::kOk) return cuda_fail(ce, "q8 attention launch");
     return PKV_OK;
   }
   const size_t need =
@@ -1552,7 +1555,7 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
   }
   cudaError_t ce = cudaSuccess;
   const pkv::TcStatus ts =
-      pkv::launch_prefill_q8(p, cache->format == PKV_Q8_E4M3, contig, num_tokens, sms, workspace,
+      pkv::launch_prefill_q8(p, e4m3, contig, num_tokens, sms, workspace,
                              static_cast<cudaStream_t>(stream), &ce);
   if (ts == pkv::TcStatus::kEncodeFailed)
     return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for q");
@@ -1623,8 +1626,13 @@ size_t pkv_q8_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs, int32
   if (check_heads(heads) != PKV_OK || num_tokens <= 0 || num_seqs <= 0 || max_q_tokens <= 0 ||
       device_info(nullptr, nullptr, &sms) != PKV_OK)
     return 0;
-  return pkv::prefill_q8_workspace(num_tokens, num_seqs, max_q_tokens, heads.num_kv_heads,
-                                   heads.num_q_heads / heads.num_kv_heads, sms);
+  const int G = heads.num_q_heads / heads.num_kv_heads;
+  const size_t need = pkv::prefill_q8_workspace(num_tokens, num_seqs, max_q_tokens,
+                                                heads.num_kv_heads, G, sms);
+  // (which of the two a call needs rests with its table too)
+  const bool runs = pkv::chunks_by_runs(num_tokens, num_seqs, std::min(max_q_tokens, num_tokens),
+                                        heads.num_kv_heads, G, 1);
+  return std::max(need, runs ? pkv::tc_workspace_bytes(tc_ctas(sms)) : 0);
 }
 
 pkv_status pkv_paged_prefill_attention_q8(

@@ -66,7 +66,9 @@ struct AttentionQ8Params {
   int* err;
 };
 
-// Decode (cu_q null): workspace of tc_workspace_bytes(num_ctas).
+// Decode (cu_q null), or chunks that chunks_by_runs says: workspace of
+// tc_workspace_bytes(num_ctas).
+bool chunks_by_runs(int num_tokens, int num_seqs, int max_q, int Hkv, int G, int max_context);
 TcStatus launch_decode_q8(const AttentionQ8Params& p, bool e4m3, bool contig, int num_ctas,
                           void* workspace, cudaStream_t stream, cudaError_t* cuda_err);
 // The same for small batches: a cluster of 1, 2, 4 or 8 CTAs of 4 or 8 warps a

@@ -297,6 +297,64 @@ def test_prefill_empty_chunks():
     b.check(b.prefill(), half_step=q8_ref.PREFILL)
 
 
+@pytest.mark.parametrize("dtype", q8_ref.FORMATS)
+@pytest.mark.parametrize("layout", ["paged", "contig"])
+@pytest.mark.parametrize("hq,hkv", HEADS)
+def test_short_chunks(dtype, layout, hq, hkv):
+    """Chunks of few tokens take decode's arithmetic, 16 rows at a time."""
+    most = 2 * (16 // (hq // hkv))
+    new = [most, 1, most - 1, 0, most // 2, most // 2 + 1, 2, 1] * 2
+    cached = [0, 0, 14, 0, 100, 1000, 31, 257, 1, 20, 0, 7, 999, 15, 16, 17]
+    b = Batch(dtype, layout, hq, hkv, [n + c for n, c in zip(new, cached)], new)
+    b.check(b.prefill())
+    new = [1 + (most // 2 - 1) * (i % 2) for i in range(16)]
+    b = Batch(dtype, layout, hq, hkv, [n + c for n, c in zip(new, cached)], new)
+    b.check(b.prefill())
+
+
+@pytest.mark.parametrize("dtype", q8_ref.FORMATS)
+@pytest.mark.parametrize("new,cached", [([2], [9000]), ([1] * 300, [50] * 300), ([8, 1] * 120, [90] * 240),
+                                        ([8, 1, 5] * 3, [30000, 0, 1] * 3), ([4] * 8, [300] * 8),
+                                        ([3, 8] * 20, list(range(0, 2000, 50)))])
+def test_short_chunk_lengths(dtype, new, cached):
+    b = Batch(dtype, "paged", 8, 2, [n + c for n, c in zip(new, cached)], new, bs=32)
+    first = b.prefill().clone()
+    b.check(first)
+    for _ in range(10):
+        assert torch.equal(b.prefill(), first)
+
+
+def test_short_chunks_captured():
+    b = Batch(torch.float8_e4m3fn, "paged", 24, 6, [300, 700, 20], [4, 2, 2])
+    tail = torch.full((5, 24, D), math.nan, device=DEV).bfloat16()
+    b.q = torch.cat([b.q, tail])  # 13 rows for 3 chunks
+    out = torch.full_like(b.q, 3.0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.prefill(max_new=8, out=out)
+    for lens, new in (([300, 700, 20], [4, 2, 2]), ([290, 650, 0], [1, 7, 0]), ([140, 0, 3], [5, 0, 3])):
+        b.lens, b.new = lens, new
+        b.ctx.copy_(torch.tensor(lens, dtype=torch.int32))
+        b.cu.copy_(torch.tensor([0] + new, dtype=torch.int32).cumsum(0).to(torch.int32))
+        for _ in range(2):
+            out.fill_(3.0)
+            g.replay()
+            b.check(out)
+            assert bool((out[sum(new):] == 3.0).all())
+
+
+def test_short_chunks_checked():
+    b = Batch(torch.int8, "paged", 32, 8, [100, 60], [5, 6])
+    pkv.set_checked(True)
+    b.check(b.prefill())
+    assert pkv.get_device_error() == "none"
+    b.prefill(max_new=5)
+    assert pkv.get_device_error() == "context"
+    b.where[0, 2] = 10 ** 6
+    b.prefill()
+    assert pkv.get_device_error() == "block_id"
+
+
 def test_prefill_captured():
     b = Batch(torch.float8_e4m3fn, "paged", 8, 2, [300, 700], [100, 40])
     b.check(b.prefill(), half_step=q8_ref.PREFILL)

@@ -25,24 +25,25 @@
 
 #include "pkv_device.cuh"
 #include "q8.cuh"
+#include "rope_rows.cuh"
+#include "umma.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kRopeThreads;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTile = 64;           // tokens a CTA
 constexpr int kTable = 4 * kMaxTile;   // hash slots (a power of two)
+constexpr int kFilter = 1024;          // bits
+constexpr int kScan = 8;               // slots that a thread has on the way
+constexpr int kTogether = 304;         // tokens whose queries are turned in the same launch
 constexpr int kBatch = 2;              // groups whose sines are in shared memory at once
 constexpr unsigned kFull = 0xffffffffu;
 
-// (cos, sin) of pair i of a token at cs_at(i): padded so that lanes that read
-// 8 (half layout) or 4 (interleaved) pairs apart meet different banks.
-__device__ __forceinline__ constexpr int cs_at(int pair) { return pair + (pair >> 3) * 2; }
-constexpr int kSines = cs_at(64);
-
-__device__ __forceinline__ float2 sines(const pkv_rope& rope, int32_t position, int pair) {
+// (cos, sin) times gain of a pair at a position, as rope_rows has them.
+__device__ __forceinline__ float2 rope_sines(const pkv_rope& rope, int32_t position, int pair) {
   if (pair >= (rope.rotary_dim >> 1)) return make_float2(1.f, 0.f);
   // position times turns, exact modulo a turn; a signed fraction in units of 2^-63 half turns
   const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(position)) *
@@ -53,69 +54,14 @@ __device__ __forceinline__ float2 sines(const pkv_rope& rope, int32_t position, 
 }
 
 // An element of a turned pair; y is the other one, negated for the first.
-__device__ __forceinline__ float turned(float x, float y, float2 cs) {
+__device__ __forceinline__ float turned_one(float x, float y, float2 cs) {
   return __fmaf_rn(x, cs.x, __fmul_rn(y, cs.y));
 }
 
-// Eight elements of a row, chunk c of the 16 lanes that hold it, turned.  Every
-// lane of the warp calls; a row lies in one half of the warp.
-__device__ __forceinline__ void turn_chunk(const pkv_rope& rope, const float2* cs, int c,
-                                           float (&x)[8]) {
-  const int rd = rope.rotary_dim, half = rd >> 1;
-  if (rope.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int pair = c * 4 + i;
-      if (pair < half) {
-        const float2 f = cs[cs_at(pair)];
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = turned(a, -b, f);
-        x[2 * i + 1] = turned(b, a, f);
-      }
-    }
-    return;
-  }
-  // partner of element e: e + half below half, e - half from there to rd.  It is
-  // element (e +- half) & 7 of chunk (e +- half) >> 3 of the same row.
-  float y[8];
-  const int lane = threadIdx.x & 31;
-  if ((half & 7) == 0) {
-    const int by = half >> 3;
-    const int other = c < by ? c + by : (c < 2 * by ? c - by : c);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(kFull, x[i], (lane & 16) | other);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = c * 8 + i;
-      const int want = e < half ? e + half : (e < rd ? e - half : e);
-      float got = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float v = __shfl_sync(kFull, x[j], (lane & 16) | (want >> 3));
-        if (j == (want & 7)) got = v;
-      }
-      y[i] = got;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = c * 8 + i;
-    if (e < rd) {
-      const bool lower = e < half;
-      const float2 f = cs[cs_at(lower ? e : e - half)];
-      x[i] = turned(x[i], lower ? -y[i] : y[i], f);
-    }
-  }
-}
-
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(u[i]);
-    x[2 * i + 1] = bf16_hi(u[i]);
-  }
+__device__ __forceinline__ void turn_pair(float& x, float& y, float2 cs) {
+  const float a = turned_one(x, -y, cs);
+  y = turned_one(y, x, cs);
+  x = a;
 }
 
 // Four values in units of the scale as codes.
@@ -146,9 +92,10 @@ __device__ __forceinline__ float code_value(uint32_t byte) {
 }
 
 struct GroupTable {
+  alignas(16) int32_t token[kTable][kGroupRows];  // token that writes the row, or -1
   unsigned long long key[kTable];  // group + 1, or 0
   int32_t first[kTable];           // lowest token of the group
-  int32_t token[kTable][kGroupRows];  // token that writes the row, or -1
+  uint32_t filter[kFilter / 32];   // a bit for each group of the table
   int32_t owned[kTable];           // table slots of the groups that this CTA does
   int32_t num_owned;
 };
@@ -157,119 +104,294 @@ __device__ __forceinline__ int hash_of(unsigned long long key) {
   return static_cast<int>((key * 0x9E3779B97F4A7C15ull) >> 40) & (kTable - 1);
 }
 
-// One (group, head, tensor) of the call, by a warp.
-template <bool kE4m3, bool kRope>
-__device__ __forceinline__ void put_unit(const AppendQ8Params& p, const int32_t* token,
-                                         const float2 (*cs)[kSines], int64_t group, int h,
-                                         bool is_v) {
-  constexpr float kMax = kE4m3 ? kE4m3Max : kInt8Max;
-  const int lane = threadIdx.x & 31, c = lane & 15, odd = lane >> 4;
-  const uint16_t* src = (is_v ? p.v : p.k) + h * kHeadDim + c * 8;
-  const int64_t stride = is_v ? p.v_stride : p.k_stride;
-  const int64_t slot = group * kGroupRows;
-  const int64_t row0 = cache_row(slot / p.bs, h, p.Hkv, p.bs, slot % p.bs);
-  uint8_t* dst = (is_v ? p.v_codes : p.k_codes) + row0 * kCodeRowBytes + c * 8;
-  float* scale = (is_v ? p.v_scale : p.k_scale) + row0 / kGroupRows;
-  const bool started = token[0] >= 0;
-  float old = started ? 0.f : *scale;
-  if (!(old > 0.f && old <= 3.402823466e38f)) old = 0.f;
+// Bit of the filter of a slot's group.
+__device__ __forceinline__ uint32_t filter_bit(int64_t slot) {
+  return (static_cast<uint32_t>(slot >> 4) * 0x9E3779B9u) >> 22;
+}
+static_assert(kGroupRows == 16 && kFilter == 1 << 10, "filter_bit");
 
-  uint4 raw[8];
+// A unit of the call: a (group, head, K or V), by a warp.  Lane 8 r + l holds rows
+// 4 i + r, of each two chunks of 8 elements.
+struct Unit {
+  const int32_t* token;  // [16]
+  const uint16_t* src;   // the head's elements of token 0
+  int64_t stride;
+  uint8_t* codes;        // of the group's first row
+  float* scale;
+};
+
+template <bool kV>
+__device__ __forceinline__ Unit unit_at(const AppendQ8Params& p, const int32_t* token, int64_t group,
+                                        int h) {
+  const int64_t slot = group * kGroupRows;
+  const int64_t row = cache_row(slot / p.bs, h, p.Hkv, p.bs, slot % p.bs);
+  Unit u;
+  u.token = token;
+  u.src = (kV ? p.v : p.k) + h * kHeadDim;
+  u.stride = kV ? p.v_stride : p.k_stride;
+  u.codes = (kV ? p.v_codes : p.k_codes) + row * kCodeRowBytes;
+  u.scale = (kV ? p.v_scale : p.k_scale) + row / kGroupRows;
+  return u;
+}
+
+// The group's scale before the call; 0 if it starts anew, or if no append wrote it.
+__device__ __forceinline__ float scale_before(const Unit& u) {
+  const float old = u.token[0] >= 0 ? 0.f : *u.scale;
+  return old > 0.f && old <= 3.402823466e38f ? old : 0.f;
+}
+
+// Eight finite values x / scale as codes: |x inv| is at most qmax (1 + 2^-22), which
+// rounds to qmax.  v: pairs.
+template <bool kE4m3>
+__device__ __forceinline__ uint2 codes8(const uint64_t (&v)[4], uint64_t inv2) {
+  uint32_t r[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int t = token[2 * i + odd];
-    raw[i] = t >= 0 ? ld_global_nc_v4(src + t * stride) : make_uint4(0u, 0u, 0u, 0u);
+  for (int k = 0; k < 2; ++k) {
+    float x, y, z, w;
+    umma::f2_unpack(umma::f2_mul(v[2 * k], inv2), x, y);
+    umma::f2_unpack(umma::f2_mul(v[2 * k + 1], inv2), z, w);
+    if (kE4m3) {
+      r[k] = to_e4m3x2(x, y) | (to_e4m3x2(z, w) << 16);
+    } else {
+      // rint by the addition of 1.5 2^23, whose low byte is then the code (one by one:
+      // a packed addition came out in one rounding with its product)
+      constexpr float kMagic = 12582912.f;
+      const uint32_t a = __float_as_uint(__fadd_rn(x, kMagic)), b = __float_as_uint(__fadd_rn(y, kMagic));
+      const uint32_t c = __float_as_uint(__fadd_rn(z, kMagic)), d = __float_as_uint(__fadd_rn(w, kMagic));
+      r[k] = __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    }
   }
-  float x[8][8];
-  float top = 0.f;
+  return make_uint2(r[0], r[1]);
+}
+
+// The rows' codes: chunk(i, half, y) gives the values of chunk `half` (0, 1) of row
+// 4 i + r.  at0, at1: the chunks' places in a row.
+template <bool kE4m3, typename Chunk>
+__device__ __forceinline__ void put_rows(const Unit& u, float old, float s, bool finite, int at0,
+                                         int at1, Chunk chunk) {
+  const int r = (threadIdx.x & 31) >> 3;
+  const bool started = u.token[0] >= 0;
+  const float inv = s >= kScaleTiny ? __frcp_rn(s) : 0.f;
+  const uint64_t inv2 = umma::f2_pack(__float_as_uint(inv), __float_as_uint(inv));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 4 * i + r;
+    uint2* const at[2] = {reinterpret_cast<uint2*>(u.codes + row * kCodeRowBytes + 8 * at0),
+                          reinterpret_cast<uint2*>(u.codes + row * kCodeRowBytes + 8 * at1)};
+    if (u.token[row] >= 0) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint64_t v[4];
+        chunk(i, k, v);
+        if (finite) {
+          *at[k] = codes8<kE4m3>(v, inv2);
+        } else {
+          float y[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            umma::f2_unpack(v[j], y[2 * j], y[2 * j + 1]);
+            y[2 * j] = __fmul_rn(y[2 * j], inv);
+            y[2 * j + 1] = __fmul_rn(y[2 * j + 1], inv);
+          }
+          *at[k] = make_uint2(codes4<kE4m3>(y[0], y[1], y[2], y[3]),
+                              codes4<kE4m3>(y[4], y[5], y[6], y[7]));
+        }
+      }
+    } else if (started) {
+      *at[0] = *at[1] = make_uint2(0u, 0u);
+    } else if (s != old) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint2 held = *at[k];
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          y[j] = __fmul_rn(
+              __fmul_rn(code_value<kE4m3>((j < 4 ? held.x : held.y) >> (8 * (j & 3))), old), inv);
+        *at[k] = make_uint2(codes4<kE4m3>(y[0], y[1], y[2], y[3]),
+                            codes4<kE4m3>(y[4], y[5], y[6], y[7]));
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void pairs_of(const uint4& w, uint64_t (&v)[4]) {
+  v[0] = umma::f2_pack(w.x << 16, w.x & 0xffff0000u);
+  v[1] = umma::f2_pack(w.y << 16, w.y & 0xffff0000u);
+  v[2] = umma::f2_pack(w.z << 16, w.z & 0xffff0000u);
+  v[3] = umma::f2_pack(w.w << 16, w.w & 0xffff0000u);
+}
+
+// Rows as they come.  The maximum is taken on the bf16 bits: without the sign they
+// order as the values do, infinities and NaN above all others.
+template <bool kE4m3>
+__device__ __forceinline__ void put_unit(const Unit& u) {
+  constexpr float kMax = kE4m3 ? kE4m3Max : kInt8Max;
+  const int lane = threadIdx.x & 31, l = lane & 7, r = lane >> 3;
+  const float old = scale_before(u);
+  uint4 raw[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = u.token[4 * i + r];
+    const uint16_t* src = u.src + t * u.stride + l * 8;
+    raw[i][0] = t >= 0 ? ld_global_nc_v4(src) : make_uint4(0u, 0u, 0u, 0u);
+    raw[i][1] = t >= 0 ? ld_global_nc_v4(src + 64) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    unpack8(raw[i], x[i]);
-    if (kRope && !is_v) turn_chunk(p.rope, cs[2 * i + odd], c, x[i]);
+    const uint4& w = raw[i >> 1][i & 1];
+    m = __vmaxu2(__vmaxu2(m, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu);
+    m = __vmaxu2(__vmaxu2(m, w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
+  }
+  uint32_t top = __reduce_max_sync(kFull, max(m << 16, m & 0xffff0000u));
+  const bool finite = top < 0x7f800000u;
+  if (!finite) {
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4& w = raw[i >> 1][i & 1];
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = (x[j] << 16) & 0x7fffffffu, b = x[j] & 0x7fff0000u;
+        top = max(top, a < 0x7f800000u ? a : 0u);
+        top = max(top, b < 0x7f800000u ? b : 0u);
+      }
+    }
+    top = __reduce_max_sync(kFull, top);
+  }
+  const float s = fmaxf(old, __fdiv_rn(__uint_as_float(top), kMax));
+  put_rows<kE4m3>(u, old, s, finite, l, l + 8,
+                  [&](int i, int k, uint64_t (&v)[4]) { pairs_of(raw[i][k], v); });
+  if (lane == 0) *u.scale = s;
+}
+
+// Keys, turned; cs: the sines of the 16 rows.  kKind as for rope_rows: interleaved, half
+// with partners in whole chunks (which a lane holds both), half with others (read one
+// by one).
+template <bool kE4m3, int kKind>
+__device__ __forceinline__ void put_turned(const Unit& u, const float2 (*cs)[cs_at(64)],
+                                           int rotary_dim) {
+  constexpr float kMax = kE4m3 ? kE4m3Max : kInt8Max;
+  const int lane = threadIdx.x & 31, l = lane & 7, r = lane >> 3;
+  const int half = rotary_dim >> 1;
+  int ca = 2 * l, cb = 2 * l + 1;
+  if (kKind == 1 && l < (rotary_dim >> 4)) {
+    ca = l;
+    cb = l + (rotary_dim >> 4);
+  }
+  const float old = scale_before(u);
+  uint4 raw[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = u.token[4 * i + r];
+    const uint16_t* src = u.src + t * u.stride;
+    raw[i][0] = t >= 0 ? ld_global_nc_v4(src + 8 * ca) : make_uint4(0u, 0u, 0u, 0u);
+    raw[i][1] = t >= 0 ? ld_global_nc_v4(src + 8 * cb) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float x[4][16];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = u.token[4 * i + r];
+    const float2* f = cs[4 * i + r];
+    const uint32_t w[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                           raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float a = fabsf(x[i][j]);
-      top = fmaxf(top, a <= 3.402823466e38f ? a : 0.f);
+      x[i][2 * j] = bf16_lo(w[j]);
+      x[i][2 * j + 1] = bf16_hi(w[j]);
     }
-  }
+    if (t >= 0) {
+      if (kKind == 2) {
+        const uint16_t* src = u.src + t * u.stride;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  const float s = fmaxf(old, __fdiv_rn(top, kMax));
-  const float inv = s >= kScaleTiny ? __frcp_rn(s) : 0.f;
-  if (lane == 0) *scale = s;
+        for (int j = 0; j < 16; ++j) {
+          const int e = 16 * l + j;
+          if (e >= rotary_dim) continue;
+          const bool lower = e < half;
+          const int other = lower ? e + half : e - half;
+          const float y = bf16_lo(src[other]);
+          const float2 c = f[cs_at(lower ? e : other)];
+          x[i][j] = turned_one(x[i][j], lower ? -y : y, c);
+        }
+      } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = 2 * i + odd;
-    uint2* at = reinterpret_cast<uint2*>(dst + row * kCodeRowBytes);
-    float y[8];
-    if (token[row] >= 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(x[i][j], inv);
-    } else if (started) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = 0.f;
-    } else {
-      if (s == old) continue;
-      const uint2 held = *at;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        y[j] = __fmul_rn(__fmul_rn(code_value<kE4m3>((j < 4 ? held.x : held.y) >> (8 * (j & 3))), old),
-                         inv);
+        for (int j = 0; j < 8; j += 2) {
+          const float4 c = *reinterpret_cast<const float4*>(&f[cs_at(8 * l) + j]);
+          const float2 c0 = make_float2(c.x, c.y), c1 = make_float2(c.z, c.w);
+          if (kKind == 0) {
+            if (8 * l + j < half) turn_pair(x[i][2 * j], x[i][2 * j + 1], c0);
+            if (8 * l + j + 1 < half) turn_pair(x[i][2 * j + 2], x[i][2 * j + 3], c1);
+          } else if (8 * l < half) {
+            turn_pair(x[i][j], x[i][8 + j], c0);
+            turn_pair(x[i][j + 1], x[i][8 + j + 1], c1);
+          }
+        }
+      }
     }
-    *at = make_uint2(codes4<kE4m3>(y[0], y[1], y[2], y[3]), codes4<kE4m3>(y[4], y[5], y[6], y[7]));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[i][j]) & 0x7fffffffu);
   }
+  top = __reduce_max_sync(kFull, top);
+  const bool finite = top < 0x7f800000u;
+  if (!finite) {
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t a = __float_as_uint(x[i][j]) & 0x7fffffffu;
+        top = max(top, a < 0x7f800000u ? a : 0u);
+      }
+    top = __reduce_max_sync(kFull, top);
+  }
+  const float s = fmaxf(old, __fdiv_rn(__uint_as_float(top), kMax));
+  put_rows<kE4m3>(u, old, s, finite, ca, cb, [&](int i, int k, uint64_t (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = umma::f2_pack(__float_as_uint(x[i][8 * k + 2 * j]),
+                           __float_as_uint(x[i][8 * k + 2 * j + 1]));
+  });
+  if (lane == 0) *u.scale = s;
 }
 
-// Query rows of tokens t0 .. t0 + n - 1 turned into q_out.
-__device__ __forceinline__ void turn_queries(const AppendQ8Params& p, int t0, int n,
-                                             float2 (*cs)[kSines]) {
-  for (int e = threadIdx.x; e < n * 64; e += kThreads)
-    cs[e >> 6][cs_at(e & 63)] = sines(p.rope, p.positions[t0 + (e >> 6)], e & 63);
-  __syncthreads();
-  const int c = threadIdx.x & 15;
-  const int rows = n * p.Hq;
-  // whole warps take part in the shuffles of turn_chunk
-  for (int r0 = (threadIdx.x >> 5) * 2; r0 < rows; r0 += kWarps * 2) {
-    const int r = min(r0 + ((threadIdx.x >> 4) & 1), rows - 1);
-    const int tok = r / p.Hq;
-    const int64_t t = t0 + tok;
-    const int h = r - tok * p.Hq;
-    const uint4 w = *reinterpret_cast<const uint4*>(p.q + t * p.q_stride + h * kHeadDim + c * 8);
-    float x[8];
-    unpack8(w, x);
-    turn_chunk(p.rope, cs[tok], c, x);
-    if (r0 + ((threadIdx.x >> 4) & 1) < rows)
-      *reinterpret_cast<uint4*>(p.q_out + (t * p.Hq + h) * kHeadDim + c * 8) =
-          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                     pack_bf16x2(x[6], x[7]));
-  }
-}
-
-constexpr int kQueryTokens = 4;  // tokens of a CTA that turns queries
-
-template <bool kE4m3, bool kRope>
-__global__ void __launch_bounds__(kThreads)
-    append_q8_kernel(const __grid_constant__ AppendQ8Params p, int tile, int kv_ctas) {
-  __shared__ GroupTable g;
-  __shared__ __align__(16) float2 cs[kRope ? kBatch * kGroupRows : 1][kSines];
+// kKind: -1 without rotary positions, else rope_rows'.
+template <bool kE4m3, int kKind>
+__global__ void __launch_bounds__(kThreads, kKind < 0 ? 3 : 2)
+    append_q8_kernel(const __grid_constant__ AppendQ8Params p, int tile, int kv_ctas, int per_token) {
+  constexpr bool kRope = kKind >= 0;
+  constexpr int kRowsKind = kRope ? kKind : 0;
+  struct KvSmem {
+    GroupTable g;
+    alignas(16) float2 cs[kRope ? kBatch * kGroupRows : 1][cs_at(64)];
+  };
+  __shared__ union Smem {
+    KvSmem kv;
+    RopeSmem<kRowsKind, 1> queries;
+    __device__ Smem() {}
+  } smem;
   grid_dependency_trigger();
   grid_dependency_wait();
   const int tid = threadIdx.x;
   if constexpr (kRope) {
-    if (static_cast<int>(blockIdx.x) >= kv_ctas) {
-      const int t0 = (static_cast<int>(blockIdx.x) - kv_ctas) * kQueryTokens;
-      turn_queries(p, t0, min(kQueryTokens, p.num_tokens - t0), cs);
+    const int b = static_cast<int>(blockIdx.x) - kv_ctas;
+    if (b >= 0) {
+      rope_rows<kRowsKind, 1>(p.queries, smem.queries, b / per_token, b % per_token, per_token);
       return;
     }
   }
+  GroupTable& g = smem.kv.g;
   const int t0 = blockIdx.x * tile;
   const int t1 = min(t0 + tile, p.num_tokens);
+  for (int i = tid; i < kTable * kGroupRows / 4; i += kThreads)
+    reinterpret_cast<int4*>(g.token)[i] = make_int4(-1, -1, -1, -1);
   for (int i = tid; i < kTable; i += kThreads) {
     g.key[i] = 0ull;
     g.first[i] = 0x7fffffff;
-#pragma unroll
-    for (int r = 0; r < kGroupRows; ++r) g.token[i][r] = -1;
   }
+  if (tid < kFilter / 32) g.filter[tid] = 0u;
   if (tid == 0) g.num_owned = 0;
   __syncthreads();
   // the slot's group + 1, or 0: a token whose rows go nowhere
@@ -282,6 +404,8 @@ __global__ void __launch_bounds__(kThreads)
     if (p.checked && slot >= p.num_slots) record_error(p.err, kErrSlot);
     const unsigned long long key = key_of(slot);
     if (key == 0ull) continue;
+    const uint32_t bit = filter_bit(slot);
+    atomicOr(&g.filter[bit >> 5], 1u << (bit & 31));
     int at = hash_of(key);
     while (true) {  // at most kMaxTile of kTable slots are taken
       const unsigned long long was = atomicCAS(&g.key[at], 0ull, key);
@@ -290,16 +414,32 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   __syncthreads();
-  for (int t = tid; t < p.num_tokens; t += kThreads) {
-    const int64_t slot = p.slot_mapping[t];
-    const unsigned long long key = key_of(slot);
-    if (key == 0ull) continue;
-    int at = hash_of(key);
-    unsigned long long have;
-    while ((have = g.key[at]) != key && have != 0ull) at = (at + 1) & (kTable - 1);
-    if (have == key) {
-      atomicMin(&g.first[at], t);
-      atomicMax(&g.token[at][slot % kGroupRows], t);
+  for (int base = tid; base < p.num_tokens; base += kScan * kThreads) {
+    int64_t slot[kScan];
+    uint32_t hits = 0;
+#pragma unroll
+    for (int j = 0; j < kScan; ++j) {
+      const int t = base + j * kThreads;
+      slot[j] = t < p.num_tokens ? __ldg(p.slot_mapping + t) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kScan; ++j) {
+      const uint32_t bit = filter_bit(slot[j]);
+      hits |= (g.filter[bit >> 5] >> (bit & 31) & 1u) << j;
+    }
+    if (hits == 0u) continue;
+#pragma unroll
+    for (int j = 0; j < kScan; ++j) {
+      if (!(hits >> j & 1u)) continue;
+      const unsigned long long key = key_of(slot[j]);
+      if (key == 0ull) continue;
+      int at = hash_of(key);
+      unsigned long long have;
+      while ((have = g.key[at]) != key && have != 0ull) at = (at + 1) & (kTable - 1);
+      if (have == key) {
+        atomicMin(&g.first[at], base + j * kThreads);
+        atomicMax(&g.token[at][slot[j] % kGroupRows], base + j * kThreads);
+      }
     }
   }
   __syncthreads();
@@ -307,36 +447,41 @@ __global__ void __launch_bounds__(kThreads)
     if (g.key[i] != 0ull && g.first[i] >= t0) g.owned[atomicAdd(&g.num_owned, 1)] = i;
   __syncthreads();
   const int n = g.num_owned;
-  const int per = 2 * p.Hkv;
+  const int per = 2 * p.Hkv;  // units of a group: K's heads, then V's
   const int warp = tid >> 5;
+  // units u of groups b0 .. b0 + nb - 1 of the CTA's
+  auto put = [&](int b0, int u) {
+    const int b = static_cast<uint32_t>(u) / static_cast<uint32_t>(per), e = u - b * per;
+    const int at = g.owned[b0 + b];
+    const int64_t group = static_cast<int64_t>(g.key[at] - 1ull);
+    if (e >= p.Hkv)
+      put_unit<kE4m3>(unit_at<true>(p, g.token[at], group, e - p.Hkv));
+    else if constexpr (kRope)
+      put_turned<kE4m3, kRowsKind>(unit_at<false>(p, g.token[at], group, e),
+                                   &smem.kv.cs[b * kGroupRows], p.queries.rope.rotary_dim);
+    else
+      put_unit<kE4m3>(unit_at<false>(p, g.token[at], group, e));
+  };
   if constexpr (!kRope) {
-    for (int u = warp; u < n * per; u += kWarps) {
-      const int at = g.owned[u / per], e = u % per;
-      put_unit<kE4m3, false>(p, g.token[at], nullptr, static_cast<int64_t>(g.key[at] - 1ull),
-                             e >> 1, e & 1);
-    }
+    for (int u = warp; u < n * per; u += kWarps) put(0, u);
   } else {
-  for (int b0 = 0; b0 < n; b0 += kBatch) {
-    const int nb = min(kBatch, n - b0);
-    for (int e = tid; e < nb * kGroupRows * 64; e += kThreads) {
-      const int row = e >> 6;
-      const int t = g.token[g.owned[b0 + row / kGroupRows]][row % kGroupRows];
-      if (t >= 0) cs[row][cs_at(e & 63)] = sines(p.rope, p.positions[t], e & 63);
+    for (int b0 = 0; b0 < n; b0 += kBatch) {
+      const int nb = min(kBatch, n - b0);
+      for (int e = tid; e < nb * kGroupRows * 64; e += kThreads) {
+        const int row = e >> 6;
+        const int t = g.token[g.owned[b0 + row / kGroupRows]][row % kGroupRows];
+        if (t >= 0)
+          smem.kv.cs[row][cs_at(e & 63)] =
+              rope_sines(p.queries.rope, p.queries.positions[t], e & 63);
+      }
+      __syncthreads();
+      for (int u = warp; u < nb * per; u += kWarps) put(b0, u);
+      __syncthreads();
     }
-    __syncthreads();
-    for (int u = warp; u < nb * per; u += kWarps) {
-      const int b = u / per, e = u % per;
-      const int at = g.owned[b0 + b];
-      put_unit<kE4m3, true>(p, g.token[at],
-                            &cs[b * kGroupRows],
-                            static_cast<int64_t>(g.key[at] - 1ull), e >> 1, e & 1);
-    }
-    __syncthreads();
-  }
   }
 }
 
-template <bool kE4m3, bool kRope>
+template <bool kE4m3, int kKind>
 cudaError_t launch(const AppendQ8Params& p, cudaStream_t stream) {
   // A few hundred CTAs where there are tokens for them, up to 32 tokens each;
   // more past 32768, so that the passes over all slots stay few.
@@ -344,17 +489,33 @@ cudaError_t launch(const AppendQ8Params& p, cudaStream_t stream) {
   tile = tile < 1 ? 1 : (tile > 32 ? 32 : tile);
   if (p.num_tokens > 32768) tile = kMaxTile;
   const int kv = (p.num_tokens + tile - 1) / tile;
-  const int qs = kRope ? (p.num_tokens + kQueryTokens - 1) / kQueryTokens : 0;
-  return launch_pdl(append_q8_kernel<kE4m3, kRope>, dim3(static_cast<unsigned>(kv) + qs),
-                    dim3(kThreads), 0, stream, p, tile, kv);
+  int queries = 0, per_token = 0;
+  if (kKind >= 0) {
+    if (p.num_tokens <= kTogether) {
+      per_token = (p.queries.Hq + kRowsPerPass - 1) / kRowsPerPass;
+      queries = p.num_tokens * per_token;
+    } else {
+      const cudaError_t e = launch_rope_append(p.queries, stream);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return launch_pdl(append_q8_kernel<kE4m3, kKind>, dim3(static_cast<unsigned>(kv + queries)),
+                    dim3(kThreads), 0, stream, p, tile, kv, per_token);
+}
+
+template <bool kE4m3>
+cudaError_t launch_kind(const AppendQ8Params& p, bool rope, cudaStream_t stream) {
+  if (!rope) return launch<kE4m3, -1>(p, stream);
+  if (p.queries.rope.interleaved) return launch<kE4m3, 0>(p, stream);
+  return p.queries.rope.rotary_dim % 16 == 0 ? launch<kE4m3, 1>(p, stream)
+                                             : launch<kE4m3, 2>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_append_q8(const AppendQ8Params& p, bool e4m3, bool rope, cudaStream_t stream) {
   if (p.num_tokens <= 0) return cudaSuccess;
-  if (e4m3) return rope ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
-  return rope ? launch<false, true>(p, stream) : launch<false, false>(p, stream);
+  return e4m3 ? launch_kind<true>(p, rope, stream) : launch_kind<false>(p, rope, stream);
 }
 
 }  // namespace pkv

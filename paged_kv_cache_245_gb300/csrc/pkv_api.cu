@@ -1409,12 +1409,18 @@ pkv_status append_q8_common(const int32_t* positions, const int64_t* slot_mappin
   p.num_tokens = static_cast<int32_t>(num_tokens);
   p.Hkv = heads.num_kv_heads;
   if (rope) {
-    p.positions = positions;
-    p.q = static_cast<const uint16_t*>(q);
-    p.q_out = static_cast<uint16_t*>(q_out);
-    p.q_stride = q_stride;
-    p.Hq = heads.num_q_heads;
-    p.rope = *rope;
+    pkv::RopeParams& r = p.queries;
+    r.positions = positions;
+    r.slot_mapping = slot_mapping;
+    r.q = static_cast<const uint16_t*>(q);
+    r.q_out = static_cast<uint16_t*>(q_out);
+    r.q_stride = q_stride;
+    r.num_tokens = num_tokens;
+    r.num_slots = num_slots;
+    r.bs = block_size;
+    r.Hq = heads.num_q_heads;
+    r.rope = *rope;
+    r.err = err;
   }
   p.checked = g_checked.load();
   p.err = err;

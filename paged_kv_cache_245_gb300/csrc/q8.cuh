@@ -12,6 +12,7 @@
 
 #include "../../include/pkv.h"
 #include "decode_tc_launch.h"
+#include "rope.cuh"
 
 namespace pkv {
 
@@ -33,13 +34,9 @@ struct AppendQ8Params {
   float* v_scale;
   int64_t num_slots, bs;
   int32_t num_tokens, Hkv;
-  // with rotary positions
-  const int32_t* positions;     // [T]
-  const uint16_t* q;            // [Hq][128] at q + t * q_stride
-  uint16_t* q_out;              // [T][Hq][128] (may be q)
-  int64_t q_stride;
-  int32_t Hq;
-  pkv_rope rope;
+  // with rotary positions: the queries' part of the call (no K or V heads), whose
+  // positions and plan are the keys' too
+  RopeParams queries;
   int32_t checked;
   int* err;
 };

@@ -23,6 +23,7 @@
 // is read once.
 #include <cuda_bf16.h>
 
+#include "decode_launch.cuh"
 #include "pkv_device.cuh"
 #include "q8.cuh"
 #include "rope_rows.cuh"
@@ -32,15 +33,17 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = kRopeThreads;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTile = 64;           // tokens a CTA
-constexpr int kTable = 4 * kMaxTile;   // hash slots (a power of two)
-constexpr int kFilter = 1024;          // bits
+constexpr int kMaxTile = 512;          // tokens a CTA
+constexpr int kMaxTable = 2 * kMaxTile;  // hash slots (a power of two)
+constexpr int kMinTable = 64;
+constexpr int kFilter = 4096;          // bits
 constexpr int kScan = 8;               // slots that a thread has on the way
 constexpr int kTogether = 304;         // tokens whose queries are turned in the same launch
-constexpr int kBatch = 2;              // groups whose sines are in shared memory at once
+constexpr int kBatch = 4;              // groups whose sines are in shared memory at once
 constexpr unsigned kFull = 0xffffffffu;
+
+// Threads of a CTA, one an SM: what the registers of a unit leave room for.
+__host__ __device__ constexpr int threads_of(int kind) { return kind < 0 ? 768 : 512; }
 
 // (cos, sin) times gain of a pair at a position, as rope_rows has them.
 __device__ __forceinline__ float2 rope_sines(const pkv_rope& rope, int32_t position, int pair) {
@@ -92,23 +95,24 @@ __device__ __forceinline__ float code_value(uint32_t byte) {
 }
 
 struct GroupTable {
-  alignas(16) int32_t token[kTable][kGroupRows];  // token that writes the row, or -1
-  unsigned long long key[kTable];  // group + 1, or 0
-  int32_t first[kTable];           // lowest token of the group
-  uint32_t filter[kFilter / 32];   // a bit for each group of the table
-  int32_t owned[kTable];           // table slots of the groups that this CTA does
+  unsigned long long key[kMaxTable];  // group + 1, or 0
+  int32_t first[kMaxTable];           // lowest token of the group
+  uint32_t filter[kFilter / 32];      // a bit for each group of the table
+  int32_t owned[kMaxTile];            // table slots of the groups that this CTA does
   int32_t num_owned;
+  // last, as only a launch's table is asked for: the token that writes a row, or -1
+  alignas(16) int32_t token[kMaxTable][kGroupRows];
 };
 
-__device__ __forceinline__ int hash_of(unsigned long long key) {
-  return static_cast<int>((key * 0x9E3779B97F4A7C15ull) >> 40) & (kTable - 1);
+__device__ __forceinline__ int hash_of(unsigned long long key, int mask) {
+  return static_cast<int>((key * 0x9E3779B97F4A7C15ull) >> 40) & mask;
 }
 
 // Bit of the filter of a slot's group.
 __device__ __forceinline__ uint32_t filter_bit(int64_t slot) {
-  return (static_cast<uint32_t>(slot >> 4) * 0x9E3779B9u) >> 22;
+  return (static_cast<uint32_t>(slot >> 4) * 0x9E3779B9u) >> 20;
 }
-static_assert(kGroupRows == 16 && kFilter == 1 << 10, "filter_bit");
+static_assert(kGroupRows == 16 && kFilter == 1 << 12, "filter_bit");
 
 // A unit of the call: a (group, head, K or V), by a warp.  Lane 8 r + l holds rows
 // 4 i + r, of each two chunks of 8 elements.
@@ -120,17 +124,16 @@ struct Unit {
   float* scale;
 };
 
-template <bool kV>
 __device__ __forceinline__ Unit unit_at(const AppendQ8Params& p, const int32_t* token, int64_t group,
-                                        int h) {
+                                        int h, bool is_v) {
   const int64_t slot = group * kGroupRows;
   const int64_t row = cache_row(slot / p.bs, h, p.Hkv, p.bs, slot % p.bs);
   Unit u;
   u.token = token;
-  u.src = (kV ? p.v : p.k) + h * kHeadDim;
-  u.stride = kV ? p.v_stride : p.k_stride;
-  u.codes = (kV ? p.v_codes : p.k_codes) + row * kCodeRowBytes;
-  u.scale = (kV ? p.v_scale : p.k_scale) + row / kGroupRows;
+  u.src = (is_v ? p.v : p.k) + h * kHeadDim;
+  u.stride = is_v ? p.v_stride : p.k_stride;
+  u.codes = (is_v ? p.v_codes : p.k_codes) + row * kCodeRowBytes;
+  u.scale = (is_v ? p.v_scale : p.k_scale) + row / kGroupRows;
   return u;
 }
 
@@ -357,41 +360,47 @@ __device__ __forceinline__ void put_turned(const Unit& u, const float2 (*cs)[cs_
   if (lane == 0) *u.scale = s;
 }
 
-// kKind: -1 without rotary positions, else rope_rows'.
+// What a CTA has in shared memory.
+template <int kKind>
+struct KvSmem {
+  alignas(16) float2 cs[kKind >= 0 ? kBatch * kGroupRows : 1][cs_at(64)];
+  GroupTable g;
+};
+
+// kKind: -1 without rotary positions, else rope_rows'.  table: hash slots, a power of
+// two, at least 2 tile.
 template <bool kE4m3, int kKind>
-__global__ void __launch_bounds__(kThreads, kKind < 0 ? 3 : 2)
-    append_q8_kernel(const __grid_constant__ AppendQ8Params p, int tile, int kv_ctas, int per_token) {
+__global__ void __launch_bounds__(threads_of(kKind), 1)
+    append_q8_kernel(const __grid_constant__ AppendQ8Params p, int tile, int table, int kv_ctas,
+                     int per_token) {
   constexpr bool kRope = kKind >= 0;
   constexpr int kRowsKind = kRope ? kKind : 0;
-  struct KvSmem {
-    GroupTable g;
-    alignas(16) float2 cs[kRope ? kBatch * kGroupRows : 1][cs_at(64)];
-  };
-  __shared__ union Smem {
-    KvSmem kv;
-    RopeSmem<kRowsKind, 1> queries;
-    __device__ Smem() {}
-  } smem;
+  constexpr int kThreads = threads_of(kKind), kWarps = kThreads / 32;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
   grid_dependency_trigger();
   grid_dependency_wait();
   const int tid = threadIdx.x;
   if constexpr (kRope) {
     const int b = static_cast<int>(blockIdx.x) - kv_ctas;
     if (b >= 0) {
-      rope_rows<kRowsKind, 1>(p.queries, smem.queries, b / per_token, b % per_token, per_token);
+      if (tid < kRopeThreads)
+        rope_rows<kRowsKind, 1>(p.queries, *reinterpret_cast<RopeSmem<kRowsKind, 1>*>(smem_raw),
+                                b / per_token, b % per_token, per_token);
       return;
     }
   }
-  GroupTable& g = smem.kv.g;
+  KvSmem<kKind>& smem = *reinterpret_cast<KvSmem<kKind>*>(smem_raw);
+  GroupTable& g = smem.g;
+  const int mask = table - 1;
   const int t0 = blockIdx.x * tile;
   const int t1 = min(t0 + tile, p.num_tokens);
-  for (int i = tid; i < kTable * kGroupRows / 4; i += kThreads)
+  for (int i = tid; i < table * kGroupRows / 4; i += kThreads)
     reinterpret_cast<int4*>(g.token)[i] = make_int4(-1, -1, -1, -1);
-  for (int i = tid; i < kTable; i += kThreads) {
+  for (int i = tid; i < table; i += kThreads) {
     g.key[i] = 0ull;
     g.first[i] = 0x7fffffff;
   }
-  if (tid < kFilter / 32) g.filter[tid] = 0u;
+  for (int i = tid; i < kFilter / 32; i += kThreads) g.filter[i] = 0u;
   if (tid == 0) g.num_owned = 0;
   __syncthreads();
   // the slot's group + 1, or 0: a token whose rows go nowhere
@@ -406,11 +415,11 @@ __global__ void __launch_bounds__(kThreads, kKind < 0 ? 3 : 2)
     if (key == 0ull) continue;
     const uint32_t bit = filter_bit(slot);
     atomicOr(&g.filter[bit >> 5], 1u << (bit & 31));
-    int at = hash_of(key);
-    while (true) {  // at most kMaxTile of kTable slots are taken
+    int at = hash_of(key, mask);
+    while (true) {  // at most half of the slots are taken
       const unsigned long long was = atomicCAS(&g.key[at], 0ull, key);
       if (was == 0ull || was == key) break;
-      at = (at + 1) & (kTable - 1);
+      at = (at + 1) & mask;
     }
   }
   __syncthreads();
@@ -433,9 +442,9 @@ __global__ void __launch_bounds__(kThreads, kKind < 0 ? 3 : 2)
       if (!(hits >> j & 1u)) continue;
       const unsigned long long key = key_of(slot[j]);
       if (key == 0ull) continue;
-      int at = hash_of(key);
+      int at = hash_of(key, mask);
       unsigned long long have;
-      while ((have = g.key[at]) != key && have != 0ull) at = (at + 1) & (kTable - 1);
+      while ((have = g.key[at]) != key && have != 0ull) at = (at + 1) & mask;
       if (have == key) {
         atomicMin(&g.first[at], base + j * kThreads);
         atomicMax(&g.token[at][slot[j] % kGroupRows], base + j * kThreads);
@@ -443,27 +452,26 @@ __global__ void __launch_bounds__(kThreads, kKind < 0 ? 3 : 2)
     }
   }
   __syncthreads();
-  for (int i = tid; i < kTable; i += kThreads)
+  for (int i = tid; i < table; i += kThreads)
     if (g.key[i] != 0ull && g.first[i] >= t0) g.owned[atomicAdd(&g.num_owned, 1)] = i;
   __syncthreads();
   const int n = g.num_owned;
-  const int per = 2 * p.Hkv;  // units of a group: K's heads, then V's
   const int warp = tid >> 5;
-  // units u of groups b0 .. b0 + nb - 1 of the CTA's
-  auto put = [&](int b0, int u) {
-    const int b = static_cast<uint32_t>(u) / static_cast<uint32_t>(per), e = u - b * per;
+  // unit u of groups b0 .. b0 + nb - 1 of the CTA's: K's heads first (turning takes longer)
+  auto put = [&](int b0, int nb, int u) {
+    const bool is_v = u >= nb * p.Hkv;
+    if (is_v) u -= nb * p.Hkv;
+    const int b = static_cast<uint32_t>(u) / static_cast<uint32_t>(p.Hkv), h = u - b * p.Hkv;
     const int at = g.owned[b0 + b];
     const int64_t group = static_cast<int64_t>(g.key[at] - 1ull);
-    if (e >= p.Hkv)
-      put_unit<kE4m3>(unit_at<true>(p, g.token[at], group, e - p.Hkv));
-    else if constexpr (kRope)
-      put_turned<kE4m3, kRowsKind>(unit_at<false>(p, g.token[at], group, e),
-                                   &smem.kv.cs[b * kGroupRows], p.queries.rope.rotary_dim);
+    if (!kRope || is_v)
+      put_unit<kE4m3>(unit_at(p, g.token[at], group, h, is_v));
     else
-      put_unit<kE4m3>(unit_at<false>(p, g.token[at], group, e));
+      put_turned<kE4m3, kRowsKind>(unit_at(p, g.token[at], group, h, false),
+                                   &smem.cs[b * kGroupRows], p.queries.rope.rotary_dim);
   };
   if constexpr (!kRope) {
-    for (int u = warp; u < n * per; u += kWarps) put(0, u);
+    for (int u = warp; u < n * 2 * p.Hkv; u += kWarps) put(0, n, u);
   } else {
     for (int b0 = 0; b0 < n; b0 += kBatch) {
       const int nb = min(kBatch, n - b0);
@@ -471,11 +479,10 @@ __global__ void __launch_bounds__(kThreads, kKind < 0 ? 3 : 2)
         const int row = e >> 6;
         const int t = g.token[g.owned[b0 + row / kGroupRows]][row % kGroupRows];
         if (t >= 0)
-          smem.kv.cs[row][cs_at(e & 63)] =
-              rope_sines(p.queries.rope, p.queries.positions[t], e & 63);
+          smem.cs[row][cs_at(e & 63)] = rope_sines(p.queries.rope, p.queries.positions[t], e & 63);
       }
       __syncthreads();
-      for (int u = warp; u < nb * per; u += kWarps) put(b0, u);
+      for (int u = warp; u < nb * 2 * p.Hkv; u += kWarps) put(b0, nb, u);
       __syncthreads();
     }
   }
@@ -483,12 +490,20 @@ __global__ void __launch_bounds__(kThreads, kKind < 0 ? 3 : 2)
 
 template <bool kE4m3, int kKind>
 cudaError_t launch(const AppendQ8Params& p, cudaStream_t stream) {
-  // A few hundred CTAs where there are tokens for them, up to 32 tokens each;
-  // more past 32768, so that the passes over all slots stay few.
-  int tile = (p.num_tokens + 303) / 304;
-  tile = tile < 1 ? 1 : (tile > 32 ? 32 : tile);
-  if (p.num_tokens > 32768) tile = kMaxTile;
+  // one CTA an SM, or several rounds of them
+  const int64_t most = static_cast<int64_t>(p.sms) * kMaxTile;
+  const int64_t ctas = p.sms * ((p.num_tokens + most - 1) / most);
+  const int tile = static_cast<int>((p.num_tokens + ctas - 1) / ctas);
   const int kv = (p.num_tokens + tile - 1) / tile;
+  int table = kMinTable;
+  while (table < 2 * tile) table *= 2;
+  constexpr size_t kRow = sizeof(GroupTable::token[0]);
+  constexpr size_t kSmem = sizeof(KvSmem<kKind>), kRest = kSmem - kMaxTable * kRow;
+  static_assert(kKind < 0 || sizeof(RopeSmem<kKind < 0 ? 0 : kKind, 1>) <= kRest, "queries fit too");
+  static unsigned long long done_mask = 0;
+  auto kernel = append_q8_kernel<kE4m3, kKind>;
+  const cudaError_t se = ensure_smem_limit(kernel, static_cast<int>(kSmem), &done_mask);
+  if (se != cudaSuccess) return se;
   int queries = 0, per_token = 0;
   if (kKind >= 0) {
     if (p.num_tokens <= kTogether) {
@@ -499,8 +514,8 @@ cudaError_t launch(const AppendQ8Params& p, cudaStream_t stream) {
       if (e != cudaSuccess) return e;
     }
   }
-  return launch_pdl(append_q8_kernel<kE4m3, kKind>, dim3(static_cast<unsigned>(kv + queries)),
-                    dim3(kThreads), 0, stream, p, tile, kv, per_token);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(kv + queries)), dim3(threads_of(kKind)),
+                    kRest + table * kRow, stream, p, tile, table, kv, per_token);
 }
 
 template <bool kE4m3>

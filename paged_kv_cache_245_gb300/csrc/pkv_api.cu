@@ -1391,7 +1391,8 @@ pkv_status append_q8_common(const int32_t* positions, const int64_t* slot_mappin
       return fail(PKV_ERR_INVALID_ARG, "q_out overlaps k or v");
   }
   int* err = nullptr;
-  st = device_info(nullptr, &err, nullptr);
+  int sms = 0;
+  st = device_info(nullptr, &err, &sms);
   if (st != PKV_OK) return st;
   pkv::AppendQ8Params p;
   std::memset(&p, 0, sizeof p);
@@ -1423,6 +1424,7 @@ pkv_status append_q8_common(const int32_t* positions, const int64_t* slot_mappin
     r.err = err;
   }
   p.checked = g_checked.load();
+  p.sms = sms;
   p.err = err;
   const cudaError_t e = pkv::launch_append_q8(p, cache->format == PKV_Q8_E4M3, rope != nullptr,
                                               static_cast<cudaStream_t>(stream));

@@ -37,7 +37,7 @@ struct AppendQ8Params {
   // with rotary positions: the queries' part of the call (no K or V heads), whose
   // positions and plan are the keys' too
   RopeParams queries;
-  int32_t checked;
+  int32_t checked, sms;
   int* err;
 };
 

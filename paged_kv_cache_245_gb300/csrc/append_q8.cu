@@ -16,11 +16,24 @@
 // slots, which gives each group's first token and, row by row, the last token
 // that writes it.  The CTA that holds a group's first token does the whole
 // group; so no two CTAs touch one group, and the result does not depend on
-// their order.
+// their order.  In the pass a bit for each of the table's groups turns most
+// slots away before the table is looked at.
 //
 // A warp takes a (group, head, K or V): 16 rows x 256 bytes are 64 elements a
 // lane, all in registers between the maximum and the rounding, so that every row
-// is read once.
+// is read once.  8 lanes hold a row, each two chunks of 8 elements, as in
+// rope_rows.cuh: a lane has both elements of its turned pairs.
+//
+// What bounds it: memory for prompts, three dependent reads (slot, slots, rows) and
+// the scale for few tokens.  One CTA an SM, as large as the registers allow, keeps
+// the passes over the slots few and every SM as busy as the next; with 32 tokens a
+// CTA and three CTAs an SM 16384 tokens took 32 us.  The maximum on the bf16 bits,
+// two at a time, took the larger part of the arithmetic away (75 to 32 us with the
+// filter).  8 KV heads, us: 1 token 4.1, 64 of as many sequences 4.4, 256 5.8; prompts
+// of 1000 5.1, 4096 10.1, 16384 22.0 (101 MB: 4.6 TB/s, 0.68 of a plain copy), 65536
+// 71 (5.7 TB/s, 0.83).  With rotary positions and 32 query heads: 1 5.6, 256 of as many
+// sequences 8.9, 1000 11.5, 4096 27, 16384 79 (369 MB: 4.7 TB/s, 0.69), 65536 285 (0.76);
+// there the keys' turn, in fp32 until they are rounded, takes 128 registers a thread.
 #include <cuda_bf16.h>
 
 #include "decode_launch.cuh"
@@ -38,7 +51,10 @@ constexpr int kMaxTable = 2 * kMaxTile;  // hash slots (a power of two)
 constexpr int kMinTable = 64;
 constexpr int kFilter = 4096;          // bits
 constexpr int kScan = 8;               // slots that a thread has on the way
-constexpr int kTogether = 304;         // tokens whose queries are turned in the same launch
+// Tokens whose queries are turned by CTAs of the same launch; past that by a launch of
+// rope.cu's, of whose CTAs an SM holds five (256 tokens 7.3 us for 9.7, 600 8.4 for 11.3,
+// 1000 11.5 for 12.3; 1300 15.2 for 13.9, 4096 38.8 for 27.2).
+constexpr int kTogether = 1000;
 constexpr int kBatch = 4;              // groups whose sines are in shared memory at once
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -381,11 +397,11 @@ __global__ void __launch_bounds__(threads_of(kKind), 1)
   grid_dependency_wait();
   const int tid = threadIdx.x;
   if constexpr (kRope) {
-    const int b = static_cast<int>(blockIdx.x) - kv_ctas;
-    if (b >= 0) {
-      if (tid < kRopeThreads)
-        rope_rows<kRowsKind, 1>(p.queries, *reinterpret_cast<RopeSmem<kRowsKind, 1>*>(smem_raw),
-                                b / per_token, b % per_token, per_token);
+    if (static_cast<int>(blockIdx.x) >= kv_ctas) {
+      const int part = tid / kRopeThreads;
+      const int b = (static_cast<int>(blockIdx.x) - kv_ctas) * (kThreads / kRopeThreads) + part;
+      rope_rows<kRowsKind, 1>(p.queries, reinterpret_cast<RopeSmem<kRowsKind, 1>*>(smem_raw)[part],
+                              tid % kRopeThreads, b / per_token, b % per_token, per_token);
       return;
     }
   }
@@ -490,7 +506,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1)
 
 template <bool kE4m3, int kKind>
 cudaError_t launch(const AppendQ8Params& p, cudaStream_t stream) {
-  // one CTA an SM, or several rounds of them
+  // one CTA an SM, or several rounds of them (what they cost: above)
   const int64_t most = static_cast<int64_t>(p.sms) * kMaxTile;
   const int64_t ctas = p.sms * ((p.num_tokens + most - 1) / most);
   const int tile = static_cast<int>((p.num_tokens + ctas - 1) / ctas);
@@ -499,7 +515,8 @@ cudaError_t launch(const AppendQ8Params& p, cudaStream_t stream) {
   while (table < 2 * tile) table *= 2;
   constexpr size_t kRow = sizeof(GroupTable::token[0]);
   constexpr size_t kSmem = sizeof(KvSmem<kKind>), kRest = kSmem - kMaxTable * kRow;
-  static_assert(kKind < 0 || sizeof(RopeSmem<kKind < 0 ? 0 : kKind, 1>) <= kRest, "queries fit too");
+  static_assert(kKind < 0 || sizeof(RopeSmem<kKind < 0 ? 0 : kKind, 1>) *
+                                     (threads_of(kKind) / kRopeThreads) <= kRest, "queries fit too");
   static unsigned long long done_mask = 0;
   auto kernel = append_q8_kernel<kE4m3, kKind>;
   const cudaError_t se = ensure_smem_limit(kernel, static_cast<int>(kSmem), &done_mask);
@@ -508,7 +525,8 @@ cudaError_t launch(const AppendQ8Params& p, cudaStream_t stream) {
   if (kKind >= 0) {
     if (p.num_tokens <= kTogether) {
       per_token = (p.queries.Hq + kRowsPerPass - 1) / kRowsPerPass;
-      queries = p.num_tokens * per_token;
+      constexpr int kParts = threads_of(kKind) / kRopeThreads;
+      queries = (p.num_tokens * per_token + kParts - 1) / kParts;
     } else {
       const cudaError_t e = launch_rope_append(p.queries, stream);
       if (e != cudaSuccess) return e;

@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const Rope
   __shared__ RopeSmem<kKind, kTokens> sm;
   grid_dependency_trigger();
   grid_dependency_wait();
-  rope_rows<kKind, kTokens>(p, sm, blockIdx.x, blockIdx.y, gridDim.y);
+  rope_rows<kKind, kTokens>(p, sm, threadIdx.x, blockIdx.x, blockIdx.y, gridDim.y);
 }
 
 template <int kKind>

@@ -41,15 +41,14 @@ struct RopeSmem {
   int64_t row0[kTokens];  // cache row of KV head 0, or -1: k and v go nowhere
 };
 
-// Rows of tokens bx * kTokens .. of the call, every gy-th pass from pass `by` on, by a
-// CTA of kRopeThreads threads.
+// Rows of tokens bx * kTokens .. of the call, every gy-th pass from pass `by` on, by
+// kRopeThreads threads.  Every thread of the CTA calls, whatever its tokens.
 template <int kKind, int kTokens>
-__device__ __forceinline__ void rope_rows(const RopeParams& p, RopeSmem<kKind, kTokens>& sm, int bx,
-                                          int by, int gy) {
+__device__ __forceinline__ void rope_rows(const RopeParams& p, RopeSmem<kKind, kTokens>& sm, int tid,
+                                          int bx, int by, int gy) {
   auto& cs = sm.cs;
   auto& rows = sm.rows;
   auto& row0 = sm.row0;
-  const int tid = threadIdx.x;
   const int64_t t0 = static_cast<int64_t>(bx) * kTokens;
   const int ntok = static_cast<int>(min(static_cast<int64_t>(kTokens), p.num_tokens - t0));
   const int rd = p.rope.rotary_dim;

@@ -485,7 +485,7 @@ enum {
  * that the call writes to, each head, K and V by themselves, in fp32:
  *   a    = largest |x| of the new rows (infinities and NaN aside)
  *   old  = 0 if the group's row 0 is written (it starts anew), else its scale
- *   s    = max(old, a / qmax), qmax 127 or 448, is the new scale
+ *   s    = max(old, a * r), r = 1 / qmax in fp32, qmax 127 or 448, is the new scale
  *   inv  = 1 / s, or 0 for s < 2^-100
  *   new rows:           code = round(x * inv)
  *   the other rows:     code = round(code * old * inv) where s > old; as they

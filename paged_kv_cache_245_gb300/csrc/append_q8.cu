@@ -5,7 +5,7 @@
 // themselves:
 //   a   = max |x| over the new rows' finite elements
 //   old = 0 if the group's first row is new (the group starts anew), else its scale
-//   s   = max(old, a / qmax), qmax = 127 (int8) or 448 (e4m3);  inv = 1 / s
+//   s   = max(old, a r), r = 1 / qmax in fp32, qmax = 127 (int8) or 448 (e4m3);  inv = 1 / s
 //   new rows x:  code = round(x inv);  kept rows: code = round(code old inv)
 // all in fp32, each product rounded once, so that the codes are the formula's
 // bit for bit.  Kept rows change only when the scale grows; rows of a group that
@@ -61,15 +61,26 @@ constexpr unsigned kFull = 0xffffffffu;
 // Threads of a CTA, one an SM: what the registers of a unit leave room for.
 __host__ __device__ constexpr int threads_of(int kind) { return kind < 0 ? 768 : 512; }
 
-// (cos, sin) times gain of a pair at a position, as rope_rows has them.
+// (cos, sin) times gain of a pair at a position.  position times turns is exact modulo
+// a turn, in units of 2^-64 turns; less the nearest quarter turn it is at most 2^61 of
+// them, 1/4 half turn, and what its conversion to fp32 leaves (2^-27 half turns at most)
+// goes in by the first term of the series: a key that lies next to the border of two
+// codes shall fall on the side of its exact value as seldom wrong as the products allow
+// (rope_rows, whose results are rounded to bf16, converts the whole fraction).
 __device__ __forceinline__ float2 rope_sines(const pkv_rope& rope, int32_t position, int pair) {
   if (pair >= (rope.rotary_dim >> 1)) return make_float2(1.f, 0.f);
-  // position times turns, exact modulo a turn; a signed fraction in units of 2^-63 half turns
-  const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(position)) *
-                                            rope.turn[pair]);
-  float2 c;
-  sincospif(static_cast<float>(turn) * 1.0842021724855044e-19f, &c.y, &c.x);
-  return make_float2(c.x * rope.gain, c.y * rope.gain);
+  const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(position)) * rope.turn[pair];
+  const int quarter = static_cast<int>((turn + (uint64_t{1} << 61)) >> 62);
+  const int64_t rest = static_cast<int64_t>(turn - (static_cast<uint64_t>(quarter) << 62));
+  const float high = static_cast<float>(rest);
+  const float low = static_cast<float>(rest - static_cast<int64_t>(high));
+  float s, c;
+  sincospif(high * 1.0842021724855044e-19f, &s, &c);  // 2^-63
+  const float by = low * 3.406121578e-19f;            // pi 2^-63
+  const float s1 = fmaf(c, by, s), c1 = fmaf(-s, by, c);
+  float2 r = quarter & 1 ? make_float2(-s1, c1) : make_float2(c1, s1);
+  if (quarter & 2) r = make_float2(-r.x, -r.y);
+  return make_float2(r.x * rope.gain, r.y * rope.gain);
 }
 
 // An element of a turned pair; y is the other one, negated for the first.
@@ -159,7 +170,7 @@ __device__ __forceinline__ float scale_before(const Unit& u) {
   return old > 0.f && old <= 3.402823466e38f ? old : 0.f;
 }
 
-// Eight finite values x / scale as codes: |x inv| is at most qmax (1 + 2^-22), which
+// Eight finite values x / scale as codes: |x inv| is at most qmax (1 + 2^-21), which
 // rounds to qmax.  v: pairs.
 template <bool kE4m3>
 __device__ __forceinline__ uint2 codes8(const uint64_t (&v)[4], uint64_t inv2) {
@@ -280,7 +291,7 @@ __device__ __forceinline__ void put_unit(const Unit& u) {
     }
     top = __reduce_max_sync(kFull, top);
   }
-  const float s = fmaxf(old, __fdiv_rn(__uint_as_float(top), kMax));
+  const float s = fmaxf(old, __fmul_rn(__uint_as_float(top), 1.f / kMax));
   put_rows<kE4m3>(u, old, s, finite, l, l + 8,
                   [&](int i, int k, uint64_t (&v)[4]) { pairs_of(raw[i][k], v); });
   if (lane == 0) *u.scale = s;
@@ -366,7 +377,7 @@ __device__ __forceinline__ void put_turned(const Unit& u, const float2 (*cs)[cs_
       }
     top = __reduce_max_sync(kFull, top);
   }
-  const float s = fmaxf(old, __fdiv_rn(__uint_as_float(top), kMax));
+  const float s = fmaxf(old, __fmul_rn(__uint_as_float(top), 1.f / kMax));
   put_rows<kE4m3>(u, old, s, finite, ca, cb, [&](int i, int k, uint64_t (&v)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)

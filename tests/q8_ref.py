@@ -35,7 +35,7 @@ def append(cache, scale, slots, x):
             new = x[list(last.values()), h].numpy()
             size = np.abs(new)
             top = np.max(size[np.isfinite(size)], initial=np.float32(0))
-            s = np.maximum(old, top / qmax)
+            s = np.maximum(old, top * (np.float32(1) / qmax))
             inv = np.float32(1) / s if s >= TINY else np.float32(0)
             held = cache[block, h, 16 * part:16 * part + 16]
             if 0 in last:

@@ -496,7 +496,8 @@ enum {
  * become the largest code; NaN stays NaN in e4m3 and becomes 0 in int8.  A slot
  * that two tokens of a call share takes the later one's row (both count for a).
  * k and v are read at k_stride and v_stride elements per token as for
- * pkv_rope_append.  num_tokens is at most 2^30.
+ * pkv_rope_append.  num_tokens is at most 2^22 (every CTA looks at
+ * all slots of a call).
  */
 PKV_API pkv_status pkv_kv_append_q8(const int64_t *slot_mapping, int64_t num_tokens,
                                     const void *k, int64_t k_stride, const void *v,

@@ -801,7 +801,7 @@ def kv_append_q8(slot_mapping, k, v, k_cache, v_cache, k_scale, v_scale):
     of torch.int8 or torch.float8_e4m3fn, their scales fp32 [num_blocks, Hkv,
     block_size / 16]: value = code * scale.  A group of 16 rows starts anew when
     its first row is written; its scale grows, and the rows that it holds are
-    rounded again, when a larger row comes."""
+    rounded again, when a larger row comes.  At most 2^22 tokens a call."""
     dev = _device_index(k, "k")
     sk, T, *dims = _token_rows(k, dev, "k")
     sv, *v_dims = _token_rows(v, dev, "v")

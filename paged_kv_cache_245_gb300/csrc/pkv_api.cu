@@ -1364,7 +1364,7 @@ pkv_status append_q8_common(const int32_t* positions, const int64_t* slot_mappin
                             pkv_heads heads, const pkv_rope* rope, void* stream) {
   if (num_tokens < 0 || num_slots < 0) return fail(PKV_ERR_INVALID_ARG, "negative size");
   if (num_tokens == 0) return PKV_OK;
-  if (num_tokens > (int64_t{1} << 30)) return fail(PKV_ERR_UNSUPPORTED, "too many tokens");
+  if (num_tokens > (int64_t{1} << 22)) return fail(PKV_ERR_UNSUPPORTED, "too many tokens");
   pkv_status st = check_q8(cache, block_size);
   if (st != PKV_OK) return st;
   if (!slot_mapping || !k || !v) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
@@ -1455,6 +1455,16 @@ Q8Cluster q8_cluster(int64_t pairs, int32_t max_context, int sms, const pkv::Clu
   return tiles > 8 * s.cluster * s.warps ? Q8Cluster{0, 0} : s;
 }
 
+// Workspace of a prefill call over the 8-bit cache.  Which of its kernels a call takes
+// rests with its table too, so it is enough for either.
+size_t q8_prefill_need(int num_tokens, int num_seqs, int max_q, pkv_heads h, int sms) {
+  const int G = h.num_q_heads / h.num_kv_heads;
+  const int top = std::min(max_q, num_tokens);
+  const bool runs = pkv::chunks_by_runs(num_tokens, num_seqs, top, h.num_kv_heads, G, 1);
+  return std::max(pkv::prefill_q8_workspace(num_tokens, num_seqs, top, h.num_kv_heads, G, sms),
+                  runs ? pkv::tc_workspace_bytes(tc_ctas(sms)) : 0);
+}
+
 // Attention over the 8-bit cache.  cu_q null: decode, a row of q per sequence.
 // contig: tables are request ids, max_blocks 1, num_blocks the requests, bs = S.
 pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_tokens,
@@ -1520,15 +1530,19 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
   p.err_code = contig ? pkv::kErrReqId : pkv::kErrBlockId;
   p.err = err;
   const bool e4m3 = cache->format == PKV_Q8_E4M3;
-  if (cu_q == nullptr ||
-      pkv::chunks_by_runs(num_tokens, num_seqs, p.max_q, h.num_kv_heads, p.G, max_context)) {
-    const size_t need = pkv::tc_workspace_bytes(tc_ctas(sms));
+  const size_t need = cu_q == nullptr
+                          ? pkv::tc_workspace_bytes(tc_ctas(sms))
+                          : q8_prefill_need(num_tokens, num_seqs, max_q, h, sms);
+  const unsigned at = cu_q == nullptr ? 16 : 32;
+  if (need > 0) {
     if (!workspace || workspace_bytes < need)
       return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
                   workspace ? workspace_bytes : size_t{0});
-    const unsigned at = cu_q ? 32 : 16;
     if (!aligned(workspace, at))
       return fail(PKV_ERR_WORKSPACE, "workspace must be %u-byte aligned", at);
+  }
+  if (cu_q == nullptr ||
+      pkv::chunks_by_runs(num_tokens, num_seqs, p.max_q, h.num_kv_heads, p.G, max_context)) {
     const int variant = g_variant.load();
     if (variant <= 1 && cu_q == nullptr) {
       pkv::ClusterRoom room;
@@ -1552,14 +1566,6 @@ pkv_status attention_q8_common(const void* q, const int32_t* cu_q, int32_t num_t
       return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for the K/V cache");
     if (ts != pkv::TcStatus::kOk) return cuda_fail(ce, "q8 attention launch");
     return PKV_OK;
-  }
-  const size_t need =
-      pkv::prefill_q8_workspace(num_tokens, num_seqs, p.max_q, h.num_kv_heads, p.G, sms);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need)
-      return fail(PKV_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
-                  workspace ? workspace_bytes : size_t{0});
-    if (!aligned(workspace, 32)) return fail(PKV_ERR_WORKSPACE, "workspace must be 32-byte aligned");
   }
   cudaError_t ce = cudaSuccess;
   const pkv::TcStatus ts =
@@ -1634,13 +1640,7 @@ size_t pkv_q8_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs, int32
   if (check_heads(heads) != PKV_OK || num_tokens <= 0 || num_seqs <= 0 || max_q_tokens <= 0 ||
       device_info(nullptr, nullptr, &sms) != PKV_OK)
     return 0;
-  const int G = heads.num_q_heads / heads.num_kv_heads;
-  const size_t need = pkv::prefill_q8_workspace(num_tokens, num_seqs, max_q_tokens,
-                                                heads.num_kv_heads, G, sms);
-  // (which of the two a call needs rests with its table too)
-  const bool runs = pkv::chunks_by_runs(num_tokens, num_seqs, std::min(max_q_tokens, num_tokens),
-                                        heads.num_kv_heads, G, 1);
-  return std::max(need, runs ? pkv::tc_workspace_bytes(tc_ctas(sms)) : 0);
+  return q8_prefill_need(num_tokens, num_seqs, max_q_tokens, heads, sms);
 }
 
 pkv_status pkv_paged_prefill_attention_q8(

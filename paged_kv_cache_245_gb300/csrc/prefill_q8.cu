@@ -195,6 +195,13 @@ struct PrefillQ8Params : PrefillParams {
   int32_t sorted;       // pairs (row tiles, sequence) to sort, or 0
 };
 
+// The larger one, or NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <bool kE4m3>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q8_kernel(const __grid_constant__ CUtensorMap tmq,
@@ -864,10 +871,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // stays that.
         auto factors = [&](int h, float (&ks)[4]) {
           const float4 k4 = *reinterpret_cast<const float4*>(sct + 4 * h);
-          ks[0] = fmaxf(k4.x * sc, 1.17549435e-38f);
-          ks[1] = fmaxf(k4.y * sc, 1.17549435e-38f);
-          ks[2] = fmaxf(k4.z * sc, 1.17549435e-38f);
-          ks[3] = fmaxf(k4.w * sc, 1.17549435e-38f);
+          ks[0] = max_nan(k4.x * sc, 1.17549435e-38f);
+          ks[1] = max_nan(k4.y * sc, 1.17549435e-38f);
+          ks[2] = max_nan(k4.z * sc, 1.17549435e-38f);
+          ks[3] = max_nan(k4.w * sc, 1.17549435e-38f);
         };
         // columns 64 h .. 64 h + 31 (a) and + 32 .. + 63 (b) of S, with its sign and mask
         auto load_half = [&](int h, uint32_t (&a)[32], uint32_t (&b)[32]) {

@@ -98,6 +98,16 @@ def test_many_tiles():
     c.put(torch.arange(7, T + 7), *rows(T, 1))
 
 
+def test_more_tokens_than_one_round():
+    """More tokens than 512 a CTA on every SM; a group's rows far apart in the call."""
+    T = 152 * 512 + 3000
+    c = Cache(T // 64 + 2, 1, 64, torch.int8)
+    slots = torch.arange(T) + 9
+    slots[100], slots[T - 1] = slots[T - 1].clone(), slots[100].clone()
+    slots[500] = slots[T - 2]  # the later token's row stays
+    c.put(slots, *rows(T, 1))
+
+
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
 def test_sizes_and_non_finite_rows(dtype):
     c = Cache(4, 2, 16, dtype)
@@ -278,6 +288,23 @@ def test_rope(dtype, rotary, interleaved, T, start):
     assert bool(((got - target).abs() <= bound)[check].all())
     empty = starts.repeat_interleave(16) & ~new_rows  # rows of a new group that nothing wrote
     assert bool((got[empty] == 0).all())
+
+
+@pytest.mark.parametrize("interleaved,rotary", [(False, 128), (False, 50), (True, 128)])
+def test_rope_one_launch_or_two(interleaved, rotary):
+    """Queries and keys of 1000 tokens in one launch, of more in two: the same bits."""
+    T, hq, hkv = 1040, 4, 1
+    plan = pkv.RopePlan(rotary, interleaved=interleaved)
+    q, k, v = (torch.randn(T, n, D, device=DEV).bfloat16() for n in (hq, hkv, hkv))
+    pos = torch.arange(T, dtype=torch.int32, device=DEV) + 70000
+    slots = torch.arange(T, device=DEV)
+    both = [Cache(66, hkv, 16, torch.int8) for _ in range(2)]
+    whole = pkv.rope_append_q8(pos, slots, q, k, v, *both[0].dev, plan)
+    parts = [pkv.rope_append_q8(*(x[at] for x in (pos, slots, q, k, v)), *both[1].dev, plan)
+             for at in (slice(0, 992), slice(992, T))]  # whole groups
+    assert torch.equal(whole, torch.cat(parts))
+    for a, b in zip(both[0].dev, both[1].dev):
+        assert torch.equal(a, b)
 
 
 def test_rope_equals_the_parts():

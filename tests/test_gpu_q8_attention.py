@@ -221,6 +221,66 @@ def test_decode_checked(variant):
     assert pkv.get_device_error() == "req_id"
 
 
+def odd_rows(b, run, half_step):
+    """Queries with NaN and infinities make their own row and head NaN, no other."""
+    clean = run().clone()
+    b.check(clean, half_step=half_step)
+    q, bad = b.q.clone(), torch.zeros(b.q.shape[:2], dtype=torch.bool, device=DEV)
+    for (t, h, e), x in (((0, 1, 3), math.nan), ((2, 0, 127), math.inf), ((2, 5, 64), -math.inf),
+                         ((b.q.shape[0] - 1, 7, 0), math.nan)):
+        b.q[t, h, e], bad[t, h] = x, True
+    got = run()
+    assert bool(got[bad].isnan().all())
+    b.q = q
+    b.check(torch.where(bad[..., None], clean, got), half_step=half_step)
+
+
+def odd_cache(b, run, half_step):
+    """A visible NaN code or scale makes its sequence's and KV head's rows NaN, no others."""
+    clean = run().clone()
+    at = b.blocks(1)[0]
+    if b.dtype == torch.float8_e4m3fn:
+        spot, odd = b.k.view(torch.int8)[at, 1, 0, 100:101], 127
+    else:
+        spot, odd = b.ks[at, 1, :1], math.nan
+    was = spot.clone()
+    spot.fill_(odd)
+    got = run()
+    spot.copy_(was)
+    first, group = sum(b.new[:1]), b.q.shape[1] // b.hkv
+    bad = torch.zeros(b.q.shape[:2], dtype=torch.bool, device=DEV)
+    bad[first:first + b.new[1], group:2 * group] = True
+    assert bool(got[bad].isnan().all())
+    b.check(torch.where(bad[..., None], clean, got), half_step=half_step)
+
+
+@pytest.mark.parametrize("dtype", q8_ref.FORMATS)
+def test_decode_non_finite(variant, dtype):
+    b = Batch(dtype, "paged", 8, 2, [900, 40, 17, 300])
+    odd_rows(b, b.decode, q8_ref.DECODE)
+    odd_cache(b, b.decode, q8_ref.DECODE)
+
+
+def test_decode_two_graphs_one_workspace(variant):
+    """Replayed one after another, graphs may share what they work in."""
+    bs = [Batch(torch.int8, "paged", 8, 2, lens, seed=i)
+          for i, lens in enumerate(([3000, 40], [10, 2000, 700]))]
+    ws = torch.empty(max(pkv.q8_decode_workspace_size(len(b.lens), 8, 2, b.top) for b in bs),
+                     dtype=torch.uint8, device=DEV)
+    graphs, outs = [], [torch.empty_like(b.q) for b in bs]
+    for b, out in zip(bs, outs):
+        b.decode(out=out, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.decode(out=out, workspace=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g, b, out in zip(graphs, bs, outs):
+            out.fill_(7.0)
+            g.replay()
+            b.check(out)
+
+
 # ------------------------------------------------------------------ chunks
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
@@ -353,6 +413,59 @@ def test_short_chunks_checked():
     b.where[0, 2] = 10 ** 6
     b.prefill()
     assert pkv.get_device_error() == "block_id"
+
+
+@pytest.mark.parametrize("dtype", q8_ref.FORMATS)
+@pytest.mark.parametrize("new,cached", [([3, 4, 2, 1] * 3, [200, 30, 14, 900] * 3),
+                                        ([200, 30, 14, 65], [800, 9, 0, 3])])
+def test_prefill_non_finite(dtype, new, cached):
+    b = Batch(dtype, "paged", 8, 2, [n + c for n, c in zip(new, cached)], new)
+    odd_rows(b, b.prefill, q8_ref.PREFILL)
+    odd_cache(b, b.prefill, q8_ref.PREFILL)
+
+
+@pytest.mark.parametrize("new,cached,heads", [
+    ([2100] * 12, [0] * 12, (32, 8)),                     # more items than are cut by tiles
+    ([70] * 600, [20] * 600, (8, 2)),                     # more pairs than are sorted
+    ([40] * 560, list(range(560)), (8, 2)), ([1000] * 6, [3, 100, 2000, 0, 64, 640], (14, 2))])
+def test_prefill_schedules(new, cached, heads):
+    b = Batch(torch.float8_e4m3fn, "paged", *heads, [n + c for n, c in zip(new, cached)], new, bs=32)
+    b.check(b.prefill(), half_step=q8_ref.PREFILL)
+
+
+@pytest.mark.parametrize("new,cached", [([64], [4000]), ([3, 4] * 6, [900] * 12)])
+def test_prefill_workspace_and_streams(new, cached):
+    b = Batch(torch.int8, "paged", 8, 2, [n + c for n, c in zip(new, cached)], new)
+    size = pkv.q8_prefill_workspace_size(sum(new), len(new), max(new), 8, 2)
+    assert size > 0
+    ws = torch.empty(size + 32, dtype=torch.uint8, device=DEV)
+    assert ws.data_ptr() % 32 == 0
+    with pytest.raises(pkv.PkvError):
+        b.prefill(workspace=ws[:size - 1])
+    with pytest.raises(pkv.PkvError):
+        b.prefill(workspace=ws[16:16 + size])
+    ws.fill_(0xff)
+    out = torch.empty_like(b.q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b.prefill(workspace=ws[:size], out=out)
+    s.synchronize()
+    b.check(out, half_step=q8_ref.PREFILL)
+    # two graphs over one workspace, replayed one after another
+    other = Batch(torch.int8, "paged", 8, 2, [c + n for n, c in zip(new, cached)], new, seed=5)
+    runs = []
+    for x in (b, other):
+        o = torch.empty_like(x.q)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.prefill(workspace=ws[:size], out=o)
+        runs.append((x, g, o))
+    for _ in range(3):
+        for x, g, o in runs:
+            o.fill_(7.0)
+            g.replay()
+            x.check(o, half_step=q8_ref.PREFILL)
 
 
 def test_prefill_captured():

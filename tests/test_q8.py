@@ -112,6 +112,12 @@ def test_prefill_refuses(L, over, code):
     assert prefill(L, **over) == code
 
 
+def test_append_refuses_too_many_tokens(L):
+    """Each CTA passes over all of a call's slots."""
+    assert L.pkv_kv_append_q8(FAKE, 2 ** 22 + 1, 2 * FAKE, 256, 3 * FAKE, 256, cache(), 64, 16, H,
+                              None) == UNSUPPORTED
+
+
 def test_contig_refuses(L):
     c = cache()
     assert L.pkv_contig_decode_attention_q8(FAKE, c, FAKE, 4, FAKE, 2, 65, 64, 0.1, H, FAKE, None, 0,
@@ -140,7 +146,7 @@ def test_plain_append(dtype):
     c, s = torch.zeros(2, 1, 16, 128).to(dtype), torch.zeros(2, 1, 1)
     x = torch.randn(12, 1, 128, generator=torch.Generator().manual_seed(2))
     q8_ref.append(c, s, torch.arange(12), x)
-    assert float(s[0, 0, 0]) == float(np.float32(x.abs().max().numpy()) / q8_ref.QMAX[dtype])
+    assert float(s[0, 0, 0]) == float(x.abs().max().numpy() * (np.float32(1) / q8_ref.QMAX[dtype]))
     got = q8_ref.values(c, s)[0, 0, :12]
     want = x[:, 0].double()
     step = float(s[0, 0, 0])

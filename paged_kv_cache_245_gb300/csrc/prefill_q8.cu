@@ -50,6 +50,9 @@ constexpr int kCodeTile = kKeys * kCodeRowBytes;      // 16 KiB
 constexpr int kOffCodes = kOffK + kStages * kStageBytes;  // a tile's codes of K, then of V
 constexpr int kTilesBytes = kOffCodes + 2 * kCodeTile;  // 224 KiB
 constexpr int kScaleRing = 8;                         // tiles whose scales are kept
+// A tile's sum of P against an older maximum, at most: past 128 keys of 2^kRescaleLog2 the
+// row is rescaled.
+constexpr float kOnePassSum = 32768.f;
 constexpr int kScaleFloats = 24;                      // of 8 groups: ks, log2 vs, 1 / vs
 constexpr int kOffScales = kTilesBytes + 512;
 constexpr int kOffHeld = kOffScales + kScaleRing * kScaleFloats * 4;  // a word a converter thread
@@ -896,76 +899,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
-        // pass 1: the row maximum of the scaled, masked logits
-        float tmax = -INFINITY;
-        auto largest = [&](const uint32_t (&a)[32], const uint32_t (&b)[32], const float (&ks)[4]) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t* x = q < 2 ? a + 16 * q : b + 16 * (q - 2);
-            float u = __uint_as_float(x[0]), v = __uint_as_float(x[1]);
-#pragma unroll
-            for (int c = 2; c < 14; c += 4) {
-              u = fmax3(u, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-              v = fmax3(v, __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
-            }
-            u = fmax3(u, __uint_as_float(x[14]), __uint_as_float(x[15]));
-            tmax = fmaxf(tmax, fmaxf(u, v) * ks[q]);
-          }
-        };
-        if (plain) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t a[32], b[32];
-            tmem_ld32(a, s_tm + 64 * h);
-            tmem_ld32(b, s_tm + 64 * h + 32);
-            float ks[4];
-            factors(h, ks);
-            tmem_wait_ld(a);
-            tmem_ready(b);
-            largest(a, b, ks);
-          }
-        } else {
-#pragma unroll 1
-          for (int h = 0; h < 2 && any > 64 * h; ++h) {
-            uint32_t a[32], b[32];
-            load_half(h, a, b);
-            float ks[4];
-            factors(h, ks);
-            largest(a, b, ks);
-          }
-        }
-        const float m_new = fmaxf(m_used, tmax);
-        if (j == 0) {
-          m_used = m_new;  // finite, but in a piece that the row sees nothing of
-        } else {
-          const bool grow = m_new > m_used + kRescaleLog2;
-          if (__any_sync(kFull, grow)) {
-            const float alpha = grow ? fast_exp2(m_used - m_new) : 1.f;
-            if (grow) {
-              l *= alpha;
-              m_used = m_new;
-            }
-#pragma unroll
-            for (int c0 = 0; c0 < kHeadDim; c0 += 64) {
-              uint32_t w[32], w2[32];
-              tmem_ld64(w, w2, o_tm + c0);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                w[c] = __float_as_uint(__uint_as_float(w[c]) * alpha);
-                w2[c] = __float_as_uint(__uint_as_float(w2[c]) * alpha);
-              }
-              tmem_st32(o_tm + c0, w);
-              tmem_st32(o_tm + c0 + 32, w2);
-            }
-          }
-        }
-        // pass 2: P vs = 2^(s * scale - m + log2 vs) as bf16 pairs over the columns
-        // already read; the sums of P are those of a group divided by its vs
-        const float m = m_used == -INFINITY ? 0.f : m_used;
-        auto powers = [&](int h, const uint32_t (&a)[32], const uint32_t (&b)[32],
-                          const float (&ks)[4], const float4& lv4) {
+        // P vs = 2^(s * scale - m + log2 vs) as bf16 pairs, and the sum of P, which is that
+        // of a group divided by its vs, to `sum`
+        auto powers = [&](int h, const uint32_t (&a)[32], const uint32_t (&b)[32], float m,
+                          uint32_t (&pk)[32], float& sum) {
+          float ks[4];
+          factors(h, ks);
+          const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
           const float lv[4] = {lv4.x - m, lv4.y - m, lv4.z - m, lv4.w - m};
-          uint32_t pk[32];
           uint64_t ls2[4];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
@@ -979,44 +920,99 @@ __global__ void __launch_bounds__(kThreads, 1)
             ls2[c >> 3] = (c & 7) == 0 ? e2 : f2_add(ls2[c >> 3], e2);
             pk[c] = pack_bf16x2(e0, e1);
           }
-          tmem_st32(s_tm + 32 * h, pk);
           const float4 iv4 = *reinterpret_cast<const float4*>(sct + 16 + 4 * h);
           const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float l0, l1;
             f2_unpack(ls2[q], l0, l1);
-            l = fmaf(l0 + l1, iv[q], l);
+            sum = fmaf(l0 + l1, iv[q], sum);
           }
         };
-        if (plain) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
+        // One pass over S against the maximum of the tiles before: P is what it would be
+        // against the tile's own, times a power of two, as long as it stays in range,
+        // which its sum tells.  S is left alone until then.
+        bool done = false;
+        if (plain && j > 0) {
+          float sum = 0.f;
+          uint32_t p0[32], p1[32];
+          {
             uint32_t a[32], b[32];
-            tmem_ld32(a, s_tm + 64 * h);
-            tmem_ld32(b, s_tm + 64 * h + 32);
-            float ks[4];
-            factors(h, ks);
-            const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
-            tmem_wait_ld(a);
-            tmem_ready(b);
-            powers(h, a, b, ks, lv4);
+            tmem_ld64(a, b, s_tm);
+            powers(0, a, b, m_used, p0, sum);
           }
-        } else {
+          {
+            uint32_t a[32], b[32];
+            tmem_ld64(a, b, s_tm + 64);
+            powers(1, a, b, m_used, p1, sum);
+          }
+          done = __all_sync(kFull, sum <= kOnePassSum);  // (not NaN)
+          if (done) {
+            tmem_st32(s_tm, p0);
+            tmem_st32(s_tm + 32, p1);
+            l += sum;
+          }
+        }
+        if (!done) {
+          // pass 1: the row maximum of the scaled, masked logits
+          float tmax = -INFINITY;
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (any <= 64 * h) {  // no row of the warp sees a key of this half
-              uint32_t pz[32];
-#pragma unroll
-              for (int c = 0; c < 32; ++c) pz[c] = 0u;
-              tmem_st32(s_tm + 32 * h, pz);
-              continue;
-            }
+          for (int h = 0; h < 2 && any > 64 * h; ++h) {
             uint32_t a[32], b[32];
             load_half(h, a, b);
             float ks[4];
             factors(h, ks);
-            powers(h, a, b, ks, *reinterpret_cast<const float4*>(sct + 8 + 4 * h));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t* x = q < 2 ? a + 16 * q : b + 16 * (q - 2);
+              float u = __uint_as_float(x[0]), v = __uint_as_float(x[1]);
+#pragma unroll
+              for (int c = 2; c < 14; c += 4) {
+                u = fmax3(u, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                v = fmax3(v, __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
+              }
+              u = fmax3(u, __uint_as_float(x[14]), __uint_as_float(x[15]));
+              tmax = fmaxf(tmax, fmaxf(u, v) * ks[q]);
+            }
+          }
+          const float m_new = fmaxf(m_used, tmax);
+          if (j == 0) {
+            m_used = m_new;  // finite, but in a piece that the row sees nothing of
+          } else {
+            const bool grow = m_new > m_used + kRescaleLog2;
+            if (__any_sync(kFull, grow)) {
+              const float alpha = grow ? fast_exp2(m_used - m_new) : 1.f;
+              if (grow) {
+                l *= alpha;
+                m_used = m_new;
+              }
+#pragma unroll
+              for (int c0 = 0; c0 < kHeadDim; c0 += 64) {
+                uint32_t w[32], w2[32];
+                tmem_ld64(w, w2, o_tm + c0);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                  w[c] = __float_as_uint(__uint_as_float(w[c]) * alpha);
+                  w2[c] = __float_as_uint(__uint_as_float(w2[c]) * alpha);
+                }
+                tmem_st32(o_tm + c0, w);
+                tmem_st32(o_tm + c0 + 32, w2);
+              }
+            }
+          }
+          // pass 2: P, over the columns already read
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+            if (any > 64 * h) {
+              uint32_t a[32], b[32];
+              load_half(h, a, b);
+              powers(h, a, b, m_used == -INFINITY ? 0.f : m_used, pk, l);
+            } else {  // no row of the warp sees a key of this half
+#pragma unroll
+              for (int c = 0; c < 32; ++c) pk[c] = 0u;
+            }
+            tmem_st32(s_tm + 32 * h, pk);
           }
         }
         tmem_wait_st();

@@ -11,7 +11,7 @@
 //   warp 9       the item list and the Q rows
 //   warp 10      codes of K and V (16 KiB a tile each) by bulk copies into one slot
 //                each, and the tile's 16 scales by cp.async
-//   warps 12-15  codes -> bf16 into the two stages of K and V operands
+//   warps 12-19  codes -> bf16 into the two stages of K and V operands
 //
 // The operands hold the codes themselves, which bf16 holds exactly (int8 and e4m3
 // have at most 8 significant bits): a key's scale is uniform over 16 columns of S
@@ -54,20 +54,24 @@ constexpr int kScaleRing = 8;                         // tiles whose scales are 
 // row is rescaled.
 constexpr float kOnePassSum = 32768.f;
 constexpr int kScaleFloats = 24;                      // of 8 groups: ks, log2 vs, 1 / vs
+constexpr int kConvert0 = 12, kConverters = 8;        // converter warps
 constexpr int kOffScales = kTilesBytes + 512;
-constexpr int kOffHeld = kOffScales + kScaleRing * kScaleFloats * 4;  // a word a converter thread
-constexpr int kSmemBytes = kOffHeld + 32 * 4 * 4 + 1024;              // + alignment
+constexpr int kOffHeld = kOffScales + kScaleRing * kScaleFloats * 4;  // a word a converter warp
+constexpr int kSmemBytes = kOffHeld + kConverters * 4 + 1024;         // + alignment
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KiB");
 constexpr int kProducer = 10;                         // the code producer
-constexpr int kConvert0 = 12, kConverters = 4;        // converter warps
-constexpr int kThreads = 32 * (kConvert0 + kConverters);
 static_assert(kProducer == 10 && kConvert0 == 12, "warps 0-7 are the softmax's, 8 and 9 the next two");
-// Registers a thread of the four warpgroups, from the launch's 128 each: the softmax's
-// rows of S want more (315 -> 277 us with 8 x 2048 in e4m3), the others do with less.
-constexpr int kRegsSoftmax = 176, kRegsRoles = 72, kRegsConvert = 88;
-static_assert(2 * kRegsSoftmax + kRegsRoles + kRegsConvert == 4 * 128, "the launch's registers");
-constexpr int kRing = 4;                              // item descriptors in flight
+constexpr int kThreads = 32 * (kConvert0 + kConverters);
+// Registers a thread of the warpgroups, from the launch's.  The softmax's rows of S want
+// many, the others do with less.  One warpgroup of converters was busy all the time (3800
+// cycles of a key tile's 4270 in int8, 3150 of 3680 in e4m3) and a second one costs the
+// softmax 8 registers: 8 x 2048 int8 282 -> 266 us, 4 x 8192 1822 -> 1611.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 168, kRegsRoles = 64, kRegsConvert = 40;
+static_assert(256 * kRegsSoftmax + 128 * kRegsRoles + 32 * kConverters * kRegsConvert <=
+                      kThreads * kRegsLaunch && kThreads * kRegsLaunch <= 65536,
+              "the launch's registers");
 constexpr int kRingUsers = 10 + kConverters;  // readers: softmax, MMA, producer, converters
+constexpr int kRing = 4;                              // item descriptors in flight
 constexpr int kSplitItems = 4;               // items an SM up to which they are cut
 constexpr int kSortPairs = 512;              // (row tiles, sequence) pairs that are sorted at most
 constexpr int kSplitPairs = 1024;            // (sequence, row tiles) pairs up to which they are
@@ -170,13 +174,19 @@ __device__ __forceinline__ void codes_to_bf16(const uint4& c, uint4& lo, uint4& 
         o[2 * i + k] = pack_bf16x2(x, y);
       }
     } else {
-      // the low seven bits u as 128 + u, less 128, or less 256 where bit 7 is set
+      // y: the byte u = code + 128 as the low byte of 128's bits, which is 128 + u below
+      // 128 and 2 u from there (the step doubles).  Less 256, and less half of what is
+      // then positive, that is the code; exact, and all but the byte's placing on the
+      // multiply-add pipe (the softmax keeps the other one busy).
+      const uint32_t u = w[i] ^ 0x80808080u;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint32_t y = __byte_perm(w[i], 0u, k == 0 ? 0x4140u : 0x4342u);
-        const uint32_t a = (y & 0x007f007fu) | 0x43004300u;
-        const uint32_t b = (y & 0x00800080u) | 0xc300c300u;
-        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * i + k]) : "r"(a), "r"(b));
+        const uint32_t y = __byte_perm(u, 0x43434343u, k == 0 ? 0x4140u : 0x4342u);
+        uint32_t d, r;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(y), "r"(0x3f803f80u), "r"(0xc380c380u));
+        asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;"
+            : "=r"(r) : "r"(y), "r"(0x3f003f00u), "r"(0xc300c300u));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o[2 * i + k]) : "r"(r), "r"(0xbf80bf80u), "r"(d));
       }
     }
   }
@@ -354,10 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t smem_base = smem_addr(smem);
 
-  // The converters: codes -> operands.  A thread takes 16 codes of rows row0, row0 + 16, ..  The eight lanes of a quarter
-  // warp take chunks 0-3 of one row and 4-7 of the next (or the other way), whose loads
-  // and swizzled stores meet different banks.
+  // The converters: codes -> operands.  A thread takes 16 codes of rows row0, row0 +
+  // kRowStep, ..  The eight lanes of a quarter warp take chunks 0-3 of one row and 4-7 of
+  // the next (or the other way), whose loads and swizzled stores meet different banks.
   auto convert = [&]() {
+    constexpr int kRowStep = 4 * kConverters;
+    static_assert(4 * kRowStep == kKeys, "four rows a thread");
     const int row0 = (warp - kConvert0) * 4 + ((lane >> 4) << 1) + ((lane >> 2) & 1);
     const int ch = (lane & 3) + (((lane >> 2) ^ (lane >> 3)) & 1) * 4;  // chunk of 16 codes
     volatile uint32_t* held = reinterpret_cast<uint32_t*>(smem + kOffHeld);
@@ -377,48 +389,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned char* from = smem + kOffCodes + kv * kCodeTile + row0 * 128 + ch * 16;
           uint64_t* empty = kv == 0 ? B.kempty : B.vempty;
           unsigned char* to = smem + kOffK + s * kStageBytes + kv * kOpBytes;
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            uint4 c[4];
+          uint4 c[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            c[i] = *reinterpret_cast<const uint4*>(from + i * kRowStep * 128);
+          // The arrival must not overtake the loads, whose values are needed only later:
+          // a store of something made of all of them comes between (without it the next
+          // codes now and then came in first).
+          held[warp - kConvert0] = c[0].x ^ c[1].x ^ c[2].x ^ c[3].x;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.cempty[kv]);
+          if (kv == 0 && warp == kConvert0 && lane < 8) {
+            // a scale below 2^-100 is that of zeros, whose P only enters the sum
+            float* sct = scales + (g & (kScaleRing - 1)) * kScaleFloats + 8 + lane;
+            const float vs = *sct < kScaleTiny ? kScaleTiny : *sct;
+            sct[0] = log2f(vs);
+            sct[8] = 1.f / vs;
+          }
+          if (g >= kStages &&
+              !__all_sync(kFull, wait_or_abort(&empty[s], ((g >> 1) - 1) & 1, abort, p.err))) {
+            ok = false;
+            break;
+          }
+          if (kv == 1 && left < kKeys) {  // values past the context: 0 x whatever stands there
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              c[i] = *reinterpret_cast<const uint4*>(from + (4 * half + i) * 16 * 128);
-            if (half == 1) {
-              // The arrival must not overtake the loads, whose values are needed only later:
-              // a store of something made of all of them comes between (without it the next
-              // codes now and then came in first).
-              held[tid - 32 * kConvert0] = c[0].x ^ c[1].x ^ c[2].x ^ c[3].x;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&B.cempty[kv]);
-            } else {
-              if (kv == 0 && warp == kConvert0 && lane < 8) {
-                // a scale below 2^-100 is that of zeros, whose P only enters the sum
-                float* sct = scales + (g & (kScaleRing - 1)) * kScaleFloats + 8 + lane;
-                const float vs = *sct < kScaleTiny ? kScaleTiny : *sct;
-                sct[0] = log2f(vs);
-                sct[8] = 1.f / vs;
-              }
-              if (g >= kStages && !__all_sync(kFull, wait_or_abort(&empty[s], ((g >> 1) - 1) & 1,
-                                                                   abort, p.err))) {
-                ok = false;
-                break;
-              }
-            }
-            if (kv == 1 && left < kKeys) {  // values past the context: 0 x whatever stands there
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (row0 + 16 * (4 * half + i) >= left) c[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 lo, hi;
-              codes_to_bf16<kE4m3>(c[i], lo, hi);
-              const int r = row0 + 16 * (4 * half + i);
-              *reinterpret_cast<uint4*>(to + kv_chunk_offset(r, 2 * ch)) = lo;
-              *reinterpret_cast<uint4*>(to + kv_chunk_offset(r, 2 * ch + 1)) = hi;
-            }
+              if (row0 + kRowStep * i >= left) c[i] = make_uint4(0u, 0u, 0u, 0u);
           }
-          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 lo, hi;
+            codes_to_bf16<kE4m3>(c[i], lo, hi);
+            const int r = row0 + kRowStep * i;
+            *reinterpret_cast<uint4*>(to + kv_chunk_offset(r, 2 * ch)) = lo;
+            *reinterpret_cast<uint4*>(to + kv_chunk_offset(r, 2 * ch + 1)) = hi;
+          }
           fence_proxy_async_smem();  // the products read them through the async proxy
           __syncwarp();
           if (lane == 0) mbar_arrive(kv == 0 ? &B.kfull[s] : &B.vfull[s]);
@@ -433,401 +438,401 @@ __global__ void __launch_bounds__(kThreads, 1)
     convert();
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRoles));
-  if (warp == kProducer) {
-    // ================= code producer =================
-    // Every row tile of a sequence and KV head reads the same tiles: keep them in
-    // L2 for the items after.
-    const uint64_t policy = l2_policy_evict_last();
-    const int run = p.run_rows;    // rows per copy (16 .. 128, divides 128 and bs)
-    const int runs = kKeys / run;  // copies per tile and tensor (<= 8)
-    const int prun = lane & 15;    // lanes 0-15 copy K of run prun, lanes 16-31 V
-    const int kv = lane >> 4;
-    const uint32_t bs = static_cast<uint32_t>(p.bs);
-    // The run's row of the cache in tile j of `it` (-1: past the context, or a bad table
-    // entry: the copy is skipped, stale rows, undefined output, no fault).  (Prefetched
-    // to L2 a tile ahead, everything got slower: 8 x 2048 281 -> 298 us.)
-    auto row_of = [&](const PItem& it, int j) -> int64_t {
-      const int kpos = (it.t0 + j) * kKeys + prun * run;
-      if (prun >= runs || kpos >= it.ctx) return -1;
-      const uint32_t at = static_cast<uint32_t>(kpos) / bs;
-      const int32_t e = p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks + at];
-      if (p.checked && (e < 0 || e >= p.num_blocks)) {
-        record_error(p.err, p.err_code);
-        return -1;
-      }
-      return cache_row(e, it.kvh, p.Hkv, bs, static_cast<uint32_t>(kpos) - at * bs);
-    };
-    int g = 0;             // tiles (of all items) whose K and V were both asked for
-    bool half = false;     // K of tile g was asked for, not its V
-    int nread = 0;
-    PItem cur;
-    bool ok = read_item(nread++, cur);
-    int64_t row = ok && cur.ntiles > 0 ? row_of(cur, 0) : -1;  // of the next tile
-    while (ok && cur.ntiles > 0) {
-      PItem nx = cur;
-      for (int j = 0; j < cur.ntiles; ++j) {
-        const int kpos = (cur.t0 + j) * kKeys + prun * run;
-        const uint32_t loaded = __popc(__ballot_sync(kFull, lane < 16 && row >= 0));
-        float* sc = scales + (g & (kScaleRing - 1)) * kScaleFloats + kv * 8;
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {  // K, then V, each when its slot is read
-          if (g > 0 && !__all_sync(kFull, wait_or_abort(&B.cempty[x], (g - 1) & 1, abort, p.err))) {
-            half = x == 1;
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&B.cfull[x], loaded * run * kCodeRowBytes);
-          __syncwarp();
-          if (kv == x && row >= 0)
-            bulk_copy_g2s(smem + kOffCodes + x * kCodeTile + prun * run * kCodeRowBytes,
-                          (x == 0 ? p.k_codes : p.v_codes) + row * kCodeRowBytes,
-                          static_cast<uint32_t>(run * kCodeRowBytes), &B.cfull[x], policy);
-          if (x == 0) {
-            // the scales of the run's groups, V's with K's (the softmax of S takes both);
-            // 0 past the context, where P is 0.  The slot's last readers are done: the
-            // converters hold K of tile g - 1, so that of tile g - 2 is written, the S of
-            // tile g - 4 that freed its stage is complete, and P of tile g - 5 was handed
-            // over before.
-            if (prun < runs) {
-              const float* from =
-                  (kv == 0 ? p.k_scale : p.v_scale) + (row >= 0 ? row / kGroupRows : 0);
-              for (int i = 0; i < run / kGroupRows; ++i)
-                cp_async_4_or_zero(sc + prun * (run / kGroupRows) + i, from + (row >= 0 ? i : 0),
-                                   row >= 0 && kpos + i * kGroupRows < cur.ctx);
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                             smem_addr(&B.cfull[0]))
-                         : "memory");
-          }
-          __syncwarp();
+    if (warp == kProducer) {
+      // ================= code producer =================
+      // Every row tile of a sequence and KV head reads the same tiles: keep them in
+      // L2 for the items after.
+      const uint64_t policy = l2_policy_evict_last();
+      const int run = p.run_rows;    // rows per copy (16 .. 128, divides 128 and bs)
+      const int runs = kKeys / run;  // copies per tile and tensor (<= 8)
+      const int prun = lane & 15;    // lanes 0-15 copy K of run prun, lanes 16-31 V
+      const int kv = lane >> 4;
+      const uint32_t bs = static_cast<uint32_t>(p.bs);
+      // The run's row of the cache in tile j of `it` (-1: past the context, or a bad table
+      // entry: the copy is skipped, stale rows, undefined output, no fault).  (Prefetched
+      // to L2 a tile ahead, everything got slower: 8 x 2048 281 -> 298 us.)
+      auto row_of = [&](const PItem& it, int j) -> int64_t {
+        const int kpos = (it.t0 + j) * kKeys + prun * run;
+        if (prun >= runs || kpos >= it.ctx) return -1;
+        const uint32_t at = static_cast<uint32_t>(kpos) / bs;
+        const int32_t e = p.block_tables[static_cast<int64_t>(it.seq) * p.max_blocks + at];
+        if (p.checked && (e < 0 || e >= p.num_blocks)) {
+          record_error(p.err, p.err_code);
+          return -1;
         }
-        if (!ok) break;
-        ++g;
-        // the next tile is looked up while this one lands
-        if (j + 1 < cur.ntiles) {
-          row = row_of(cur, j + 1);
-        } else {
-          ok = read_item(nread++, nx);
-          row = ok && nx.ntiles > 0 ? row_of(nx, 0) : -1;
-        }
-      }
-      cur = nx;
-    }
-    if (*abort && lane == 0) {
-      // let the copies in flight land before the CTA's shared memory is released
-      if (g > 0) {
-        if (!half) mbar_wait_bounded(&B.cfull[0], (g - 1) & 1);
-        mbar_wait_bounded(&B.cfull[1], (g - 1) & 1);
-      }
-      if (half) mbar_wait_bounded(&B.cfull[0], g & 1);
-    }
-  } else if (warp == 9) {
-    // ================= item list and Q rows =================
-    // Q tile n (row tile 0 of an item, then row tile 1 if it has rows) goes to slot
-    // n % 2 once the last S product reading tile n - 2 completed.
-    const int P = gridDim.x;
-    const int R = (p.max_q * G + 2 * TR - 1) / (2 * TR);
-    const uint64_t qpolicy = l2_policy_evict_first();  // every Q row is read once
-    int published = 0;
-    uint32_t nq = 0;      // Q tiles loaded
-    QCursor qc = {0, 0};  // slot of Q tile nq and its phase
-    uint32_t last_phase = 0;  // bit s: phase of the last load into slot s
-    bool ok = true;
-    auto publish = [&](const PItem& it) -> bool {
-      const int slot = published & (kRing - 1);
-      if (published >= kRing &&
-          !__all_sync(kFull, wait_or_abort(&B.iempty[slot], ((published / kRing) - 1) & 1,
-                                           abort, p.err)))
-        return false;
-      if (lane == 0) {
-        ring[slot] = it;
-        mbar_arrive(&B.ifull[slot]);
-      }
-      __syncwarp();
-      ++published;
-      return true;
-    };
-    // Publishes an item and brings its Q rows; false when a wait gave up.
-    auto serve = [&](const PItem& it) -> bool {
-      if (!publish(it)) return false;
-      const int nt = it.rows > it.row0 + TR ? 2 : 1;
-      for (int t = 0; t < nt; ++t, ++nq, qc = qc.next(kQSlots)) {
-        const int qs = qc.slot;
-        if (nq >= static_cast<uint32_t>(kQSlots) &&
-            !__all_sync(kFull, wait_or_abort(&B.qempty[qs], qc.phase ^ 1u, abort, p.err)))
-          return false;
-        last_phase = (last_phase & ~(1u << qs)) | (qc.phase << qs);
-        unsigned char* dst = smem + q_off(qs);
-        // the tile is TR / G whole tokens, each column half one box of
-        // (tokens, G heads, 64 columns); rows past the chunk bring the next
-        // tokens' rows (or zeros past the tensor) and are never written out
-        const int tok0 = it.q0 + (it.row0 + t * TR) / G;
-        if (lane == 0) {
-          // two column halves of TR rows x 128 bytes
-          mbar_arrive_expect_tx(&B.qfull[qs], static_cast<uint32_t>(TR) * kRowBytes);
-          tma_load_4d_at(dst, &tmq, 0, 0, it.kvh * G, tok0, &B.qfull[qs], qpolicy);
-          tma_load_4d_at(dst + kHalfBytes, &tmq, 0, 1, it.kvh * G, tok0, &B.qfull[qs], qpolicy);
-        } else {
-          mbar_arrive(&B.qfull[qs]);
-        }
-      }
-      return true;
-    };
-    // the item of lane src
-    auto of_lane = [&](const PItem& mine, int src) -> PItem {
-      PItem it;
-      it.seq = __shfl_sync(kFull, mine.seq, src);
-      it.kvh = __shfl_sync(kFull, mine.kvh, src);
-      it.row0 = __shfl_sync(kFull, mine.row0, src);
-      it.rows = __shfl_sync(kFull, mine.rows, src);
-      it.base = __shfl_sync(kFull, mine.base, src);
-      it.ntiles = __shfl_sync(kFull, mine.ntiles, src);
-      it.q0 = __shfl_sync(kFull, mine.q0, src);
-      it.ctx = __shfl_sync(kFull, mine.ctx, src);
-      it.t0 = 0;
-      it.part = -1;
-      return it;
-    };
-    if (p.rec != nullptr) {
-      // Pairs c = (sequence c / R, row tiles c % R) in order, 32 at a time, one a
-      // lane; a pair's items (its KV heads) of kItemCost + ntiles units each.  A CTA's
-      // units [u0, u1) hold a run of key tiles; those of an item that it has not
-      // whole are a piece.
-      const int pairs = R * p.num_seqs;
-      auto pair_of_lane = [&](int c0, bool report, PItem& it) -> int64_t {
-        const int c = c0 + lane;
-        it = PItem{};
-        if (c >= pairs || !describe(c % R, c / R, report && c % R == 0, it)) return 0;
-        return static_cast<int64_t>(p.Hkv) * (kItemCost + it.ntiles);
+        return cache_row(e, it.kvh, p.Hkv, bs, static_cast<uint32_t>(kpos) - at * bs);
       };
-      PItem mine;
-      int64_t V = 0, units = 0;
-      for (int c0 = 0; c0 < pairs; c0 += 32) {
-        units = pair_of_lane(c0, blockIdx.x == 0, mine);
-        int64_t sum = units;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        V += sum;
-      }
-      const int64_t shares = max(static_cast<int64_t>(1), min(static_cast<int64_t>(P), V / kLeastUnits));
-      const int64_t me = blockIdx.x;
-      const int64_t u0 = me < shares ? me * V / shares : V;
-      const int64_t u1 = me < shares ? (me + 1) * V / shares : V;
-      PieceDesc desc = {};
-      int64_t at = 0;
-      for (int c0 = 0; ok && c0 < pairs && at < u1; c0 += 32) {
-        if (pairs > 32) units = pair_of_lane(c0, false, mine);
-        int64_t end = units;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(kFull, end, o);
-          if (lane >= o) end += v;
-        }
-        const int64_t begin = at + end - units;
-        for (uint32_t hit = __ballot_sync(kFull, units > 0 && begin < u1 && begin + units > u0);
-             ok && hit != 0u; hit &= hit - 1) {
-          const int src = __ffs(hit) - 1;
-          PItem it = of_lane(mine, src);
-          const int64_t b = __shfl_sync(kFull, begin, src);
-          const int n = it.ntiles, span = kItemCost + n;
-          for (int h = u0 > b ? static_cast<int>((u0 - b) / span) : 0; ok && h < p.Hkv; ++h) {
-            const int64_t first = b + static_cast<int64_t>(h) * span + kItemCost;  // unit of tile 0
-            if (first >= u1) break;
-            const int from = u0 > first ? static_cast<int>(u0 - first) : 0;
-            const int to = u1 - first < n ? static_cast<int>(u1 - first) : n;
-            if (from >= to) continue;
-            it.kvh = h;
-            it.t0 = from;
-            it.ntiles = to - from;
-            it.part = -1;
-            if (to - from < n) {
-              it.part = 2 * blockIdx.x + (from == 0 ? 1 : 0);
-              if (from == 0) {
-                desc.q0 = it.q0;
-                desc.kvh = h;
-                desc.row0 = it.row0;
-                desc.rows = min(it.rows - it.row0, 2 * TR);
-              } else {
-                desc.continues = to == n ? 2 : 1;
-              }
+      int g = 0;             // tiles (of all items) whose K and V were both asked for
+      bool half = false;     // K of tile g was asked for, not its V
+      int nread = 0;
+      PItem cur;
+      bool ok = read_item(nread++, cur);
+      int64_t row = ok && cur.ntiles > 0 ? row_of(cur, 0) : -1;  // of the next tile
+      while (ok && cur.ntiles > 0) {
+        PItem nx = cur;
+        for (int j = 0; j < cur.ntiles; ++j) {
+          const int kpos = (cur.t0 + j) * kKeys + prun * run;
+          const uint32_t loaded = __popc(__ballot_sync(kFull, lane < 16 && row >= 0));
+          float* sc = scales + (g & (kScaleRing - 1)) * kScaleFloats + kv * 8;
+  #pragma unroll 1
+          for (int x = 0; x < 2; ++x) {  // K, then V, each when its slot is read
+            if (g > 0 && !__all_sync(kFull, wait_or_abort(&B.cempty[x], (g - 1) & 1, abort, p.err))) {
+              half = x == 1;
+              ok = false;
+              break;
             }
-            ok = serve(it);
+            if (lane == 0) mbar_arrive_expect_tx(&B.cfull[x], loaded * run * kCodeRowBytes);
+            __syncwarp();
+            if (kv == x && row >= 0)
+              bulk_copy_g2s(smem + kOffCodes + x * kCodeTile + prun * run * kCodeRowBytes,
+                            (x == 0 ? p.k_codes : p.v_codes) + row * kCodeRowBytes,
+                            static_cast<uint32_t>(run * kCodeRowBytes), &B.cfull[x], policy);
+            if (x == 0) {
+              // the scales of the run's groups, V's with K's (the softmax of S takes both);
+              // 0 past the context, where P is 0.  The slot's last readers are done: the
+              // converters hold K of tile g - 1, so that of tile g - 2 is written, the S of
+              // tile g - 4 that freed its stage is complete, and P of tile g - 5 was handed
+              // over before.
+              if (prun < runs) {
+                const float* from =
+                    (kv == 0 ? p.k_scale : p.v_scale) + (row >= 0 ? row / kGroupRows : 0);
+                for (int i = 0; i < run / kGroupRows; ++i)
+                  cp_async_4_or_zero(sc + prun * (run / kGroupRows) + i, from + (row >= 0 ? i : 0),
+                                     row >= 0 && kpos + i * kGroupRows < cur.ctx);
+              }
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                               smem_addr(&B.cfull[0]))
+                           : "memory");
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          ++g;
+          // the next tile is looked up while this one lands
+          if (j + 1 < cur.ntiles) {
+            row = row_of(cur, j + 1);
+          } else {
+            ok = read_item(nread++, nx);
+            row = ok && nx.ntiles > 0 ? row_of(nx, 0) : -1;
           }
         }
-        at += __shfl_sync(kFull, end, 31);
+        cur = nx;
       }
-      if (lane == 0) p.desc[blockIdx.x] = desc;
-    } else {
-      // Items in order: pairs as sorted, or row tile (latest first), then sequence; then
-      // KV head.  Round k deals items k P .. k P + P - 1 to the P CTAs, forwards in even
-      // rounds and backwards in odd ones; 32 rounds at a time, one a lane, so that items
-      // whose rows lie past their chunk cost one latency (a sorted list has no more).
-      const int total = R * p.num_seqs * p.Hkv;
-      for (int64_t k0 = 0; ok && k0 * P < total; k0 += 32) {
-        const int64_t k = k0 + lane;
-        const int64_t slot = k * P + ((k & 1) ? P - 1 - static_cast<int>(blockIdx.x)
-                                              : static_cast<int>(blockIdx.x));
-        PItem mine = {};
-        bool there = slot < total;
-        if (there) {
-          const int idx = static_cast<int>(slot), at = idx / p.Hkv;
-          const int c = p.sorted > 0 ? (at < p.sorted ? list[at] : -1)
-                                     : (R - 1 - at / p.num_seqs) * p.num_seqs + at % p.num_seqs;
-          there = c >= 0 && describe(c / p.num_seqs, c % p.num_seqs,
-                                     p.sorted == 0 && c < p.num_seqs && idx == at * p.Hkv, mine);
-          mine.kvh = idx - at * p.Hkv;
+      if (*abort && lane == 0) {
+        // let the copies in flight land before the CTA's shared memory is released
+        if (g > 0) {
+          if (!half) mbar_wait_bounded(&B.cfull[0], (g - 1) & 1);
+          mbar_wait_bounded(&B.cfull[1], (g - 1) & 1);
         }
-        for (uint32_t left = __ballot_sync(kFull, there); ok && left != 0u; left &= left - 1)
-          ok = serve(of_lane(mine, __ffs(left) - 1));
+        if (half) mbar_wait_bounded(&B.cfull[0], g & 1);
       }
-    }
-    if (ok) {
-      PItem end = {};  // ntiles 0: the end of this CTA's list
-      publish(end);
-    }
-    if (*abort && lane == 0) {
-      // let the Q copies in flight land before the shared memory is released
-      for (int qs = 0; qs < kQSlots && static_cast<uint32_t>(qs) < nq; ++qs)
-        mbar_wait_bounded(&B.qfull[qs], (last_phase >> qs) & 1u);
-    }
-  } else if (warp == 8) {
-    // ================= MMA issuer =================
-    // The whole warp walks the tiles on warp-uniform values, so that descriptors stay
-    // in uniform registers; one elected lane issues.
-    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-    const uint32_t base = __shfl_sync(kFull, smem_base, 0);
-    // the low words of the operands' descriptors (smem_desc): address, leading offset
-    const uint32_t q_lo = (((base + q_off(0)) & 0x3FFFFu) >> 4) | ((16u >> 4) << 16);
-    const uint32_t k_lo = (((base + kOffK) & 0x3FFFFu) >> 4) | ((16u >> 4) << 16);
-    const uint32_t v_lo = (((base + kOffK + kOpBytes) & 0x3FFFFu) >> 4) | ((1024u >> 4) << 16);
-    constexpr uint32_t kHiQ = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, mode
-    constexpr uint32_t kHiKV = (2048u >> 4) | (1u << 14) | (2u << 29);
-    auto desc = [](uint32_t lo, uint32_t hi) -> uint64_t {
-      return (static_cast<uint64_t>(hi) << 32) | lo;
-    };
-    auto issue_s = [&](int t, int qs, int stage) {  // S_t = Q K^T
-      const uint32_t q = q_lo + qs * (kOpBytes >> 4), k = k_lo + stage * (kStageBytes >> 4);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        umma_ss(tm + t * 128, desc(q + (kk >> 2) * (kHalfBytes >> 4) + (kk & 3) * 2, kHiQ),
-                desc(k + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, kHiKV), kIdescS, kk > 0);
-    };
-    auto issue_pv = [&](int t, int stage, bool acc) {  // O_t (+)= P_t V
-      const uint32_t v = v_lo + stage * (kStageBytes >> 4);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        umma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, desc(v + kk * (4096 >> 4), kHiKV),
-                kIdescPV, (acc || kk > 0));
-    };
-    auto waitb = [&](uint64_t* b, uint32_t parity) -> bool {
-      return __all_sync(kFull, wait_or_abort(b, parity, abort, p.err));
-    };
-    // what the products need of an item: its key tiles (0: the end), a second row tile
-    int ntiles = 0;
-    bool two = false;
-    auto next_item = [&](int n) -> bool {
-      PItem it;
-      if (!read_item(n, it)) return false;
-      ntiles = __shfl_sync(kFull, it.ntiles, 0);
-      two = __shfl_sync(kFull, it.rows - it.row0, 0) > TR;
-      return true;
-    };
-    // S products of the item's first tile, global tile g, its Q tiles at qa, qb
-    auto first_s = [&](QCursor qa, QCursor qb, int g) -> bool {
-      if (!waitb(&B.kfull[g & 1], (g >> 1) & 1) || !waitb(&B.qfull[qa.slot], qa.phase))
-        return false;
-      tc_fence_after();
-      if (elect_one()) {
-        issue_s(0, qa.slot, g & 1);
-        umma_commit(&B.sfull[0]);
-        if (ntiles == 1) umma_commit(&B.qempty[qa.slot]);
-        if (!two) umma_commit(&B.kempty[g & 1]);
-      }
-      __syncwarp();
-      if (two) {
-        if (!waitb(&B.qfull[qb.slot], qb.phase)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_s(1, qb.slot, g & 1);
-          umma_commit(&B.sfull[1]);
-          if (ntiles == 1) umma_commit(&B.qempty[qb.slot]);
-          umma_commit(&B.kempty[g & 1]);  // both S products of tile g issued
+    } else if (warp == 9) {
+      // ================= item list and Q rows =================
+      // Q tile n (row tile 0 of an item, then row tile 1 if it has rows) goes to slot
+      // n % 2 once the last S product reading tile n - 2 completed.
+      const int P = gridDim.x;
+      const int R = (p.max_q * G + 2 * TR - 1) / (2 * TR);
+      const uint64_t qpolicy = l2_policy_evict_first();  // every Q row is read once
+      int published = 0;
+      uint32_t nq = 0;      // Q tiles loaded
+      QCursor qc = {0, 0};  // slot of Q tile nq and its phase
+      uint32_t last_phase = 0;  // bit s: phase of the last load into slot s
+      bool ok = true;
+      auto publish = [&](const PItem& it) -> bool {
+        const int slot = published & (kRing - 1);
+        if (published >= kRing &&
+            !__all_sync(kFull, wait_or_abort(&B.iempty[slot], ((published / kRing) - 1) & 1,
+                                             abort, p.err)))
+          return false;
+        if (lane == 0) {
+          ring[slot] = it;
+          mbar_arrive(&B.ifull[slot]);
         }
         __syncwarp();
-      }
-      return true;
-    };
-    int nread = 0;
-    bool ok = next_item(nread++);
-    QCursor q0 = {0, 0};        // the item's Q tiles: row tile 0 at q0, row tile 1 at q1
-    QCursor q1 = q0.next(kQSlots);
-    int g = 0;                  // tile index over all items (ring stage g & 1)
-    uint32_t np0 = 0, np1 = 0;  // P hand-overs taken per row tile
-    if (ok && ntiles > 0) ok = first_s(q0, q1, g);
-    // Tile g, tile j of the item: within an item PV_0(j) S_0(j+1) | PV_1(j) S_1(j+1);
-    // at an item's last tile both P V products go first, then the next item's first S
-    // products, so the current item never waits on the next.
-    int j = 0;
-    while (ok && ntiles > 0) {
-      const int s = g & 1;
-      const bool last = j == ntiles - 1;
-      const bool qlast = j + 1 == ntiles - 1;  // S of tile j + 1 reads the item's Q last
-      ok = waitb(&B.vfull[s], (g >> 1) & 1) && waitb(&B.pfull[0], np0 & 1);
-      ++np0;
-      if (ok && !last) ok = waitb(&B.kfull[s ^ 1], ((g + 1) >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        issue_pv(0, s, j > 0);
-        if (last) umma_commit(&B.ofull[0]);
-        if (!two) umma_commit(&B.vempty[s]);
-        if (!last) {
-          issue_s(0, q0.slot, s ^ 1);
-          umma_commit(&B.sfull[0]);
-          if (qlast) umma_commit(&B.qempty[q0.slot]);
-          if (!two) umma_commit(&B.kempty[s ^ 1]);
-        }
-      }
-      __syncwarp();
-      if (two) {
-        ok = waitb(&B.pfull[1], np1 & 1);
-        ++np1;
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_pv(1, s, j > 0);
-          if (last) umma_commit(&B.ofull[1]);
-          umma_commit(&B.vempty[s]);  // the converters reuse the stage
-          if (!last) {
-            issue_s(1, q1.slot, s ^ 1);
-            umma_commit(&B.sfull[1]);
-            if (qlast) umma_commit(&B.qempty[q1.slot]);
-            umma_commit(&B.kempty[s ^ 1]);
+        ++published;
+        return true;
+      };
+      // Publishes an item and brings its Q rows; false when a wait gave up.
+      auto serve = [&](const PItem& it) -> bool {
+        if (!publish(it)) return false;
+        const int nt = it.rows > it.row0 + TR ? 2 : 1;
+        for (int t = 0; t < nt; ++t, ++nq, qc = qc.next(kQSlots)) {
+          const int qs = qc.slot;
+          if (nq >= static_cast<uint32_t>(kQSlots) &&
+              !__all_sync(kFull, wait_or_abort(&B.qempty[qs], qc.phase ^ 1u, abort, p.err)))
+            return false;
+          last_phase = (last_phase & ~(1u << qs)) | (qc.phase << qs);
+          unsigned char* dst = smem + q_off(qs);
+          // the tile is TR / G whole tokens, each column half one box of
+          // (tokens, G heads, 64 columns); rows past the chunk bring the next
+          // tokens' rows (or zeros past the tensor) and are never written out
+          const int tok0 = it.q0 + (it.row0 + t * TR) / G;
+          if (lane == 0) {
+            // two column halves of TR rows x 128 bytes
+            mbar_arrive_expect_tx(&B.qfull[qs], static_cast<uint32_t>(TR) * kRowBytes);
+            tma_load_4d_at(dst, &tmq, 0, 0, it.kvh * G, tok0, &B.qfull[qs], qpolicy);
+            tma_load_4d_at(dst + kHalfBytes, &tmq, 0, 1, it.kvh * G, tok0, &B.qfull[qs], qpolicy);
+          } else {
+            mbar_arrive(&B.qfull[qs]);
           }
         }
-        __syncwarp();
-      }
-      ++g;
-      if (last) {
-        const bool had_two = two;
-        ok = next_item(nread++);
-        if (!ok) break;
-        q0 = had_two ? q1.next(kQSlots) : q1;  // the next item's Q tiles follow
-        q1 = q0.next(kQSlots);
-        j = 0;
-        if (ntiles > 0) ok = first_s(q0, q1, g);
+        return true;
+      };
+      // the item of lane src
+      auto of_lane = [&](const PItem& mine, int src) -> PItem {
+        PItem it;
+        it.seq = __shfl_sync(kFull, mine.seq, src);
+        it.kvh = __shfl_sync(kFull, mine.kvh, src);
+        it.row0 = __shfl_sync(kFull, mine.row0, src);
+        it.rows = __shfl_sync(kFull, mine.rows, src);
+        it.base = __shfl_sync(kFull, mine.base, src);
+        it.ntiles = __shfl_sync(kFull, mine.ntiles, src);
+        it.q0 = __shfl_sync(kFull, mine.q0, src);
+        it.ctx = __shfl_sync(kFull, mine.ctx, src);
+        it.t0 = 0;
+        it.part = -1;
+        return it;
+      };
+      if (p.rec != nullptr) {
+        // Pairs c = (sequence c / R, row tiles c % R) in order, 32 at a time, one a
+        // lane; a pair's items (its KV heads) of kItemCost + ntiles units each.  A CTA's
+        // units [u0, u1) hold a run of key tiles; those of an item that it has not
+        // whole are a piece.
+        const int pairs = R * p.num_seqs;
+        auto pair_of_lane = [&](int c0, bool report, PItem& it) -> int64_t {
+          const int c = c0 + lane;
+          it = PItem{};
+          if (c >= pairs || !describe(c % R, c / R, report && c % R == 0, it)) return 0;
+          return static_cast<int64_t>(p.Hkv) * (kItemCost + it.ntiles);
+        };
+        PItem mine;
+        int64_t V = 0, units = 0;
+        for (int c0 = 0; c0 < pairs; c0 += 32) {
+          units = pair_of_lane(c0, blockIdx.x == 0, mine);
+          int64_t sum = units;
+  #pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+          V += sum;
+        }
+        const int64_t shares = max(static_cast<int64_t>(1), min(static_cast<int64_t>(P), V / kLeastUnits));
+        const int64_t me = blockIdx.x;
+        const int64_t u0 = me < shares ? me * V / shares : V;
+        const int64_t u1 = me < shares ? (me + 1) * V / shares : V;
+        PieceDesc desc = {};
+        int64_t at = 0;
+        for (int c0 = 0; ok && c0 < pairs && at < u1; c0 += 32) {
+          if (pairs > 32) units = pair_of_lane(c0, false, mine);
+          int64_t end = units;
+  #pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(kFull, end, o);
+            if (lane >= o) end += v;
+          }
+          const int64_t begin = at + end - units;
+          for (uint32_t hit = __ballot_sync(kFull, units > 0 && begin < u1 && begin + units > u0);
+               ok && hit != 0u; hit &= hit - 1) {
+            const int src = __ffs(hit) - 1;
+            PItem it = of_lane(mine, src);
+            const int64_t b = __shfl_sync(kFull, begin, src);
+            const int n = it.ntiles, span = kItemCost + n;
+            for (int h = u0 > b ? static_cast<int>((u0 - b) / span) : 0; ok && h < p.Hkv; ++h) {
+              const int64_t first = b + static_cast<int64_t>(h) * span + kItemCost;  // unit of tile 0
+              if (first >= u1) break;
+              const int from = u0 > first ? static_cast<int>(u0 - first) : 0;
+              const int to = u1 - first < n ? static_cast<int>(u1 - first) : n;
+              if (from >= to) continue;
+              it.kvh = h;
+              it.t0 = from;
+              it.ntiles = to - from;
+              it.part = -1;
+              if (to - from < n) {
+                it.part = 2 * blockIdx.x + (from == 0 ? 1 : 0);
+                if (from == 0) {
+                  desc.q0 = it.q0;
+                  desc.kvh = h;
+                  desc.row0 = it.row0;
+                  desc.rows = min(it.rows - it.row0, 2 * TR);
+                } else {
+                  desc.continues = to == n ? 2 : 1;
+                }
+              }
+              ok = serve(it);
+            }
+          }
+          at += __shfl_sync(kFull, end, 31);
+        }
+        if (lane == 0) p.desc[blockIdx.x] = desc;
       } else {
-        ++j;
+        // Items in order: pairs as sorted, or row tile (latest first), then sequence; then
+        // KV head.  Round k deals items k P .. k P + P - 1 to the P CTAs, forwards in even
+        // rounds and backwards in odd ones; 32 rounds at a time, one a lane, so that items
+        // whose rows lie past their chunk cost one latency (a sorted list has no more).
+        const int total = R * p.num_seqs * p.Hkv;
+        for (int64_t k0 = 0; ok && k0 * P < total; k0 += 32) {
+          const int64_t k = k0 + lane;
+          const int64_t slot = k * P + ((k & 1) ? P - 1 - static_cast<int>(blockIdx.x)
+                                                : static_cast<int>(blockIdx.x));
+          PItem mine = {};
+          bool there = slot < total;
+          if (there) {
+            const int idx = static_cast<int>(slot), at = idx / p.Hkv;
+            const int c = p.sorted > 0 ? (at < p.sorted ? list[at] : -1)
+                                       : (R - 1 - at / p.num_seqs) * p.num_seqs + at % p.num_seqs;
+            there = c >= 0 && describe(c / p.num_seqs, c % p.num_seqs,
+                                       p.sorted == 0 && c < p.num_seqs && idx == at * p.Hkv, mine);
+            mine.kvh = idx - at * p.Hkv;
+          }
+          for (uint32_t left = __ballot_sync(kFull, there); ok && left != 0u; left &= left - 1)
+            ok = serve(of_lane(mine, __ffs(left) - 1));
+        }
       }
+      if (ok) {
+        PItem end = {};  // ntiles 0: the end of this CTA's list
+        publish(end);
+      }
+      if (*abort && lane == 0) {
+        // let the Q copies in flight land before the shared memory is released
+        for (int qs = 0; qs < kQSlots && static_cast<uint32_t>(qs) < nq; ++qs)
+          mbar_wait_bounded(&B.qfull[qs], (last_phase >> qs) & 1u);
+      }
+    } else if (warp == 8) {
+      // ================= MMA issuer =================
+      // The whole warp walks the tiles on warp-uniform values, so that descriptors stay
+      // in uniform registers; one elected lane issues.
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+      const uint32_t base = __shfl_sync(kFull, smem_base, 0);
+      // the low words of the operands' descriptors (smem_desc): address, leading offset
+      const uint32_t q_lo = (((base + q_off(0)) & 0x3FFFFu) >> 4) | ((16u >> 4) << 16);
+      const uint32_t k_lo = (((base + kOffK) & 0x3FFFFu) >> 4) | ((16u >> 4) << 16);
+      const uint32_t v_lo = (((base + kOffK + kOpBytes) & 0x3FFFFu) >> 4) | ((1024u >> 4) << 16);
+      constexpr uint32_t kHiQ = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, mode
+      constexpr uint32_t kHiKV = (2048u >> 4) | (1u << 14) | (2u << 29);
+      auto desc = [](uint32_t lo, uint32_t hi) -> uint64_t {
+        return (static_cast<uint64_t>(hi) << 32) | lo;
+      };
+      auto issue_s = [&](int t, int qs, int stage) {  // S_t = Q K^T
+        const uint32_t q = q_lo + qs * (kOpBytes >> 4), k = k_lo + stage * (kStageBytes >> 4);
+  #pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ss(tm + t * 128, desc(q + (kk >> 2) * (kHalfBytes >> 4) + (kk & 3) * 2, kHiQ),
+                  desc(k + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, kHiKV), kIdescS, kk > 0);
+      };
+      auto issue_pv = [&](int t, int stage, bool acc) {  // O_t (+)= P_t V
+        const uint32_t v = v_lo + stage * (kStageBytes >> 4);
+  #pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, desc(v + kk * (4096 >> 4), kHiKV),
+                  kIdescPV, (acc || kk > 0));
+      };
+      auto waitb = [&](uint64_t* b, uint32_t parity) -> bool {
+        return __all_sync(kFull, wait_or_abort(b, parity, abort, p.err));
+      };
+      // what the products need of an item: its key tiles (0: the end), a second row tile
+      int ntiles = 0;
+      bool two = false;
+      auto next_item = [&](int n) -> bool {
+        PItem it;
+        if (!read_item(n, it)) return false;
+        ntiles = __shfl_sync(kFull, it.ntiles, 0);
+        two = __shfl_sync(kFull, it.rows - it.row0, 0) > TR;
+        return true;
+      };
+      // S products of the item's first tile, global tile g, its Q tiles at qa, qb
+      auto first_s = [&](QCursor qa, QCursor qb, int g) -> bool {
+        if (!waitb(&B.kfull[g & 1], (g >> 1) & 1) || !waitb(&B.qfull[qa.slot], qa.phase))
+          return false;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_s(0, qa.slot, g & 1);
+          umma_commit(&B.sfull[0]);
+          if (ntiles == 1) umma_commit(&B.qempty[qa.slot]);
+          if (!two) umma_commit(&B.kempty[g & 1]);
+        }
+        __syncwarp();
+        if (two) {
+          if (!waitb(&B.qfull[qb.slot], qb.phase)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_s(1, qb.slot, g & 1);
+            umma_commit(&B.sfull[1]);
+            if (ntiles == 1) umma_commit(&B.qempty[qb.slot]);
+            umma_commit(&B.kempty[g & 1]);  // both S products of tile g issued
+          }
+          __syncwarp();
+        }
+        return true;
+      };
+      int nread = 0;
+      bool ok = next_item(nread++);
+      QCursor q0 = {0, 0};        // the item's Q tiles: row tile 0 at q0, row tile 1 at q1
+      QCursor q1 = q0.next(kQSlots);
+      int g = 0;                  // tile index over all items (ring stage g & 1)
+      uint32_t np0 = 0, np1 = 0;  // P hand-overs taken per row tile
+      if (ok && ntiles > 0) ok = first_s(q0, q1, g);
+      // Tile g, tile j of the item: within an item PV_0(j) S_0(j+1) | PV_1(j) S_1(j+1);
+      // at an item's last tile both P V products go first, then the next item's first S
+      // products, so the current item never waits on the next.
+      int j = 0;
+      while (ok && ntiles > 0) {
+        const int s = g & 1;
+        const bool last = j == ntiles - 1;
+        const bool qlast = j + 1 == ntiles - 1;  // S of tile j + 1 reads the item's Q last
+        ok = waitb(&B.vfull[s], (g >> 1) & 1) && waitb(&B.pfull[0], np0 & 1);
+        ++np0;
+        if (ok && !last) ok = waitb(&B.kfull[s ^ 1], ((g + 1) >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_pv(0, s, j > 0);
+          if (last) umma_commit(&B.ofull[0]);
+          if (!two) umma_commit(&B.vempty[s]);
+          if (!last) {
+            issue_s(0, q0.slot, s ^ 1);
+            umma_commit(&B.sfull[0]);
+            if (qlast) umma_commit(&B.qempty[q0.slot]);
+            if (!two) umma_commit(&B.kempty[s ^ 1]);
+          }
+        }
+        __syncwarp();
+        if (two) {
+          ok = waitb(&B.pfull[1], np1 & 1);
+          ++np1;
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(1, s, j > 0);
+            if (last) umma_commit(&B.ofull[1]);
+            umma_commit(&B.vempty[s]);  // the converters reuse the stage
+            if (!last) {
+              issue_s(1, q1.slot, s ^ 1);
+              umma_commit(&B.sfull[1]);
+              if (qlast) umma_commit(&B.qempty[q1.slot]);
+              umma_commit(&B.kempty[s ^ 1]);
+            }
+          }
+          __syncwarp();
+        }
+        ++g;
+        if (last) {
+          const bool had_two = two;
+          ok = next_item(nread++);
+          if (!ok) break;
+          q0 = had_two ? q1.next(kQSlots) : q1;  // the next item's Q tiles follow
+          q1 = q0.next(kQSlots);
+          j = 0;
+          if (ntiles > 0) ok = first_s(q0, q1, g);
+        } else {
+          ++j;
+        }
+      }
+      // every product issued has completed before the tensor memory is released (one
+      // lane has issued them all: elect.sync gives the same lane each time)
+      if (elect_one()) {
+        umma_commit(B.drain);
+        mbar_wait_bounded(B.drain, 0);
+      }
+      __syncwarp();
     }
-    // every product issued has completed before the tensor memory is released (one
-    // lane has issued them all: elect.sync gives the same lane each time)
-    if (elect_one()) {
-      umma_commit(B.drain);
-      mbar_wait_bounded(B.drain, 0);
-    }
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ================= softmax warpgroups (warps 0-7) =================
@@ -1155,8 +1160,8 @@ cudaError_t launch(const CUtensorMap& tq, const PrefillQ8Params& p, int grid, cu
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
   }
-  return launch_pdl_if(pdl_decode_enabled(), kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
-                       kSmemBytes, stream, tq, p);
+  return launch_pdl_if(pdl_decode_enabled(), kernel, dim3(static_cast<unsigned>(grid)),
+                       dim3(kThreads), kSmemBytes, stream, tq, p);
 }
 
 int64_t row_tile_pairs(int64_t max_q, int G, int tile_rows) {

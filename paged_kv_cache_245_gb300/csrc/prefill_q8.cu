@@ -50,9 +50,9 @@ constexpr int kCodeTile = kKeys * kCodeRowBytes;      // 16 KiB
 constexpr int kOffCodes = kOffK + kStages * kStageBytes;  // a tile's codes of K, then of V
 constexpr int kTilesBytes = kOffCodes + 2 * kCodeTile;  // 224 KiB
 constexpr int kScaleRing = 8;                         // tiles whose scales are kept
-// A tile's sum of P against an older maximum, at most: past 128 keys of 2^kRescaleLog2 the
-// row is rescaled.
-constexpr float kOnePassSum = 32768.f;
+// One pass over a tile is taken up to this sum of P, and of P vs: fp32 (and bf16, whose
+// range is the same) then holds the sums over all tiles, and 448 times as much in O.
+constexpr float kOnePassSum = 7.9228163e28f;  // 2^96
 constexpr int kScaleFloats = 24;                      // of 8 groups: ks, log2 vs, 1 / vs
 constexpr int kConvert0 = 12, kConverters = 8;        // converter warps
 constexpr int kOffScales = kTilesBytes + 512;
@@ -905,9 +905,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         // P vs = 2^(s * scale - m + log2 vs) as bf16 pairs, and the sum of P, which is that
-        // of a group divided by its vs, to `sum`
+        // of a group divided by its vs, to `sum` (as it is to `values`)
         auto powers = [&](int h, const uint32_t (&a)[32], const uint32_t (&b)[32], float m,
-                          uint32_t (&pk)[32], float& sum) {
+                          uint32_t (&pk)[32], float& sum, float& values) {
           float ks[4];
           factors(h, ks);
           const float4 lv4 = *reinterpret_cast<const float4*>(sct + 8 + 4 * h);
@@ -932,30 +932,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l0, l1;
             f2_unpack(ls2[q], l0, l1);
             sum = fmaf(l0 + l1, iv[q], sum);
+            values += l0 + l1;
           }
         };
-        // One pass over S against the maximum of the tiles before: P is what it would be
-        // against the tile's own, times a power of two, as long as it stays in range,
-        // which its sum tells.  S is left alone until then.
+        // One pass over S against a maximum of the tiles before, 0 at first: P is what it
+        // would be against the tile's own, times a power of two, which O and l have too.
+        // That stands where the sums stay in range, and, of the first tile, reach the 1
+        // that they have against their maximum (so that no more of P underflows than
+        // there).  S is left alone until then.
         bool done = false;
-        if (plain && j > 0) {
-          float sum = 0.f;
+        if (plain) {
+          const float m = j > 0 ? m_used : 0.f;
+          float sum = 0.f, values = 0.f;
           uint32_t p0[32], p1[32];
           {
             uint32_t a[32], b[32];
             tmem_ld64(a, b, s_tm);
-            powers(0, a, b, m_used, p0, sum);
+            powers(0, a, b, m, p0, sum, values);
           }
           {
             uint32_t a[32], b[32];
             tmem_ld64(a, b, s_tm + 64);
-            powers(1, a, b, m_used, p1, sum);
+            powers(1, a, b, m, p1, sum, values);
           }
-          done = __all_sync(kFull, sum <= kOnePassSum);  // (not NaN)
+          done = __all_sync(kFull, sum <= kOnePassSum && values <= kOnePassSum &&  // (not NaN)
+                                       (j > 0 || sum >= 1.f));
           if (done) {
             tmem_st32(s_tm, p0);
             tmem_st32(s_tm + 32, p1);
             l += sum;
+            m_used = m;
           }
         }
         if (!done) {
@@ -1006,13 +1012,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           // pass 2: P, over the columns already read
+          float values = 0.f;  // (unused)
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             uint32_t pk[32];
             if (any > 64 * h) {
               uint32_t a[32], b[32];
               load_half(h, a, b);
-              powers(h, a, b, m_used == -INFINITY ? 0.f : m_used, pk, l);
+              powers(h, a, b, m_used == -INFINITY ? 0.f : m_used, pk, l, values);
             } else {  // no row of the warp sees a key of this half
 #pragma unroll
               for (int c = 0; c < 32; ++c) pk[c] = 0u;

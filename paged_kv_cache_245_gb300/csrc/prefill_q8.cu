@@ -990,7 +990,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j == 0) {
             m_used = m_new;  // finite, but in a piece that the row sees nothing of
           } else {
-            const bool grow = m_new > m_used + kRescaleLog2;
+            // (a maximum that the one pass took may be far below this one; that it stays
+            // is bounded by the values' scales)
+            const float4 v0 = *reinterpret_cast<const float4*>(sct + 8);
+            const float4 v1 = *reinterpret_cast<const float4*>(sct + 12);
+            const float far = fmaxf(fmax3(fmax3(v0.x, v0.y, v0.z), v0.w, v1.x), fmax3(v1.y, v1.z, v1.w));
+            const bool grow = m_new > m_used + (far <= 40.f ? 40.f : kRescaleLog2);
             if (__any_sync(kFull, grow)) {
               const float alpha = grow ? fast_exp2(m_used - m_new) : 1.f;
               if (grow) {

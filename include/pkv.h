@@ -496,8 +496,8 @@ enum {
  * become the largest code; NaN stays NaN in e4m3 and becomes 0 in int8.  A slot
  * that two tokens of a call share takes the later one's row (both count for a).
  * k and v are read at k_stride and v_stride elements per token as for
- * pkv_rope_append.  num_tokens is at most 2^22 (every CTA looks at
- * all slots of a call).
+ * pkv_rope_append.  num_tokens is at most 2^22 (every CTA looks at all slots of a
+ * call).
  */
 PKV_API pkv_status pkv_kv_append_q8(const int64_t *slot_mapping, int64_t num_tokens,
                                     const void *k, int64_t k_stride, const void *v,
@@ -520,8 +520,9 @@ PKV_API pkv_status pkv_rope_append_q8(const int32_t *positions, const int64_t *s
  * Decode attention over it: arguments, layouts, errors and checked mode as for
  * pkv_paged_decode_attention / pkv_contig_decode_attention, with
  * K_j = code * scale (and block_size, S multiples of 16:
- * PKV_ERR_UNSUPPORTED otherwise).  Rows at or past a context are not read into
- * the result, whatever stands there.  workspace must hold
+ * PKV_ERR_UNSUPPORTED otherwise).  Scales are 0 or positive, as the appends write
+ * them; below 2^-100 they stand for zeros.  Rows at or past a context are not read
+ * into the result, whatever stands there.  workspace must hold
  * pkv_q8_decode_workspace_size(num_seqs, heads, max_context) bytes (16-byte
  * aligned) when that is not 0; its contents need no initialisation, and calls
  * that may run at the same time need their own.
@@ -541,11 +542,14 @@ PKV_API pkv_status pkv_contig_decode_attention_q8(
 /*
  * Causal prefill attention over it: arguments, layouts, errors and checked mode
  * as for pkv_paged_prefill_attention / pkv_contig_prefill_attention.  Rows of
- * q and out behind the last chunk are left alone.  Where there are few chunks
- * their keys are dealt to all SMs and the parts joined through the workspace:
- * it must hold pkv_q8_prefill_workspace_size(num_tokens, num_seqs, max_q_tokens,
- * heads) bytes (32-byte aligned) when that is not 0; its contents need no
- * initialisation, and calls that may run at the same time need their own.
+ * q and out behind the last chunk are left alone.  A NaN code among the values of
+ * a later token of the same chunk may make earlier tokens NaN, as in those calls.
+ * Where there are few chunks their keys are dealt to all SMs and the parts joined
+ * through the workspace; so are chunks of one to some eight tokens (drafts to be
+ * verified), which run as decode does.  It must hold
+ * pkv_q8_prefill_workspace_size(num_tokens, num_seqs, max_q_tokens, heads) bytes
+ * (32-byte aligned) when that is not 0; its contents need no initialisation, and
+ * calls that may run at the same time need their own.
  */
 PKV_API size_t pkv_q8_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs,
                                              int32_t max_q_tokens, pkv_heads heads);

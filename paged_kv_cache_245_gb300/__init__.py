@@ -1,6 +1,7 @@
 """Decode and prefill attention over a paged (block-table) or contiguous
-(reqId x S) KV cache, with KV append, copy-on-write block copy and block swap
-to host memory (pre-emption), as hand-written sm_103a CUDA kernels behind a C
+(reqId x S) KV cache, in bf16 or in 8 bits with a scale for every 16 positions,
+with KV append, copy-on-write block copy and block swap to host memory
+(pre-emption), as hand-written sm_103a CUDA kernels behind a C
 ABI (include/pkv.h).  This package is the thin Python binding; build the
 library with ``build.build()``."""
 from .binding import (BlockManager, PkvError, VmmBuffer, block_copy, block_swap,

@@ -281,6 +281,49 @@ def test_decode_two_graphs_one_workspace(variant):
             b.check(out)
 
 
+@pytest.mark.parametrize("layout", ["paged", "contig"])
+def test_decode_many_sequences(variant, layout):
+    """More sequences than one launch of the warp runs takes."""
+    lens = [(37 * i) % 90 for i in range(1100)]
+    b = Batch(torch.int8, layout, 4, 1, lens)
+    b.check(b.decode())
+
+
+def test_blocks_past_32_bits():
+    """Codes beyond 2^32 bytes from the cache's start give what they give near it."""
+    hkv, bs, blocks = 8, 16, 300000
+    assert blocks * hkv * bs * D > 2 ** 32
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of device memory")
+    k, v = (torch.zeros(blocks, hkv, bs, D, dtype=torch.int8, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros(blocks, hkv, 1, device=DEV) for _ in range(2))
+    T = 100
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rows = [torch.randn(T, hkv, D, generator=g, device=DEV).bfloat16() for _ in range(2)]
+    q = torch.randn(T, 32, D, generator=g, device=DEV).bfloat16()
+    outs = []
+    for first in (0, blocks - 7):
+        table = torch.arange(first, first + 7, dtype=torch.int32, device=DEV)[None]
+        pkv.kv_append_q8(torch.arange(T, device=DEV) + first * bs, *rows, k, v, ks, vs)
+        where = (k, v, ks, vs, table.contiguous(), torch.tensor([T], dtype=torch.int32, device=DEV))
+        got = [k[first:first + 7].clone(), ks[first:first + 7].clone()]
+        for n in (T, 3):
+            cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+            got.append(pkv.paged_prefill_attention_q8(q[:n], cu, *where, n, SCALE))
+        # enough chunks for the warp runs
+        many = (where[4].expand(4, 7).contiguous(), where[5].expand(4).contiguous())
+        cu = torch.arange(0, 10, 2, dtype=torch.int32, device=DEV)
+        got.append(pkv.paged_prefill_attention_q8(q[:8], cu, *where[:4], *many, 2, SCALE))
+        for choice in VARIANTS:
+            pkv.set_decode_variant(choice)
+            got.append(pkv.paged_decode_attention_q8(q[:1], *where, T, SCALE))
+        pkv.set_decode_variant(pkv.VARIANT_AUTO)
+        outs.append(got)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert all(bool((x != 0).any()) for x in outs[0])
+
+
 # ------------------------------------------------------------------ chunks
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)

@@ -32,7 +32,7 @@
 // What bounds it: of a key tile's 3690 cycles (two row tiles, 8192 positions) the
 // products take 2500, and the rest is a row tile's chain of S, softmax (2130 cycles), P
 // and P V, since S and O of two row tiles fill the tensor memory; an item's start and end
-// cost some 4 us more.  8 x 2048 tokens, 32 / 8 heads: int8 256 us, e4m3 255 (1075
+// cost some 4 us more.  8 x 2048 tokens, 32 / 8 heads: int8 259 us, e4m3 257 (1062
 // TFLOP/s, 0.56 of the library's rate), 4 x 8192 1603 us (1372, 0.71); the bf16 kernel
 // 240 and 1529.  512 tokens after 8000 (floor 36) 69 us, 64 (4.4) 31.
 #include <climits>
@@ -962,8 +962,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld64(a, b, s_tm + 64);
             powers(1, a, b, m, p1, sum, values);
           }
-          done = __all_sync(kFull, sum <= kOnePassSum && values <= kOnePassSum &&  // (not NaN)
-                                       (j > 0 || sum >= 1.f));
+          // (not NaN; whatever a padding row holds is not asked)
+          done = __all_sync(kFull, !valid || (sum <= kOnePassSum && values <= kOnePassSum &&
+                                              (j > 0 || sum >= 1.f)));
           if (done) {
             tmem_st32(s_tm, p0);
             tmem_st32(s_tm + 32, p1);

@@ -315,13 +315,14 @@ def _on_device(index, call, *args):
 def _token_rows(t, index, name):
     """(Token stride in elements, T, H, D) of new rows [T, H, D] whose heads are
     adjacent; tokens may be further apart (a view of a wider projection output)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype is not torch.bfloat16:
-        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if t.dim() != 3:
-        raise ValueError("%s must have 3 dims" % name)
-    if t.get_device() != index:
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3
+            and t.get_device() == index):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("%s must be a CUDA tensor" % name)
+        if t.dtype is not torch.bfloat16:
+            raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+        if t.dim() != 3:
+            raise ValueError("%s must have 3 dims" % name)
         raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, index))
     T, H, d = t.shape
     st, sh, sd = t.stride()
@@ -776,6 +777,22 @@ _Q8_FORMATS = {torch.int8: 1, torch.float8_e4m3fn: 2}
 
 def _q8_cache(dev, k, v, k_scale, v_scale):
     """(Q8Cache, shape [blocks, Hkv, rows, D]) of an 8-bit cache on device `dev`."""
+    try:  # what nearly every call has, tested at once; what fails it is named below
+        shape = k.shape
+        n, hkv, rows, d = shape
+        groups = (n, hkv, rows >> 4)
+        dtype = k.dtype
+        if (v.dtype is dtype and k_scale.dtype is torch.float32 and v_scale.dtype is torch.float32
+                and v.shape == shape and k_scale.shape == groups and v_scale.shape == groups
+                and not rows & 15
+                and dev == k.get_device() == v.get_device() == k_scale.get_device()
+                == v_scale.get_device()
+                and k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous()
+                and v_scale.is_contiguous()):
+            return Q8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                           _Q8_FORMATS[dtype], 0), shape
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
     if not isinstance(k, torch.Tensor) or k.dtype not in _Q8_FORMATS:
         raise TypeError("the cache's codes must be torch.int8 or torch.float8_e4m3fn")
     _check_in(k, k.dtype, 4, dev, "k_cache")

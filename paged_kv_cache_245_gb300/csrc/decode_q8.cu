@@ -35,7 +35,7 @@
 // What bounds it: HBM, past 8 us that the launch, the schedule (contexts, table, rows
 // one after another) and the joins take.  128 sequences of 8192 with 8 KV heads (2.15
 // GB) take 328 us, 6.55 TB/s or 0.97 of a plain copy; 64 ragged ones (520 MB) 87 us,
-// 0.89; 32 of 100 to 4095 with 4 KV heads (85 MB) 25 us, 0.5.  Two tiles a stage took
+// 0.89; 32 of 100 to 4095 with 4 KV heads (85 MB) 24 us, 0.52.  Two tiles a stage took
 // the first from 453 to 334 us.  Small batches are decode_q8_cluster.cu's.
 //
 // Chunks of few tokens (kChunks) are the same with 16 rows, (token, query head) pairs of
@@ -693,16 +693,22 @@ cudaError_t launch_shape(const CUtensorMap& tk, const CUtensorMap& tv, const Dec
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
   }
-  // (chunks come as one launch's sequences at most)
-  const int chunk = kChunks ? p0.num_seqs : tc_chunk_seqs(p0.max_context);
+  // (of chunks, whole ones: their groups are the schedule's sequences)
+  const int groups = kChunks ? p0.groups : 1;
+  const int chunk = tc_chunk_seqs(p0.max_context) / groups * groups;
   for (int s0 = 0; s0 < p0.num_seqs; s0 += chunk) {
     DecodeQ8Params p = p0;
+    const int first = s0 / groups;  // sequence of the call
     p.num_seqs = (p0.num_seqs - s0) < chunk ? (p0.num_seqs - s0) : chunk;
-    p.q += static_cast<int64_t>(s0) * p.Hq * kHeadDim;
-    p.out += static_cast<int64_t>(s0) * p.Hq * kHeadDim;
-    p.ctx_lens += s0;
-    if (kContig) p.req_ids += s0;
-    else p.block_tables += static_cast<int64_t>(s0) * p.max_blocks;
+    if (kChunks) {
+      p.cu_q += first;
+    } else {
+      p.q += static_cast<int64_t>(s0) * p.Hq * kHeadDim;
+      p.out += static_cast<int64_t>(s0) * p.Hq * kHeadDim;
+    }
+    p.ctx_lens += first;
+    if (kContig) p.req_ids += first;
+    else p.block_tables += static_cast<int64_t>(first) * p.max_blocks;
     p.tag = next_launch_tag();  // every launch writes its piece records under a fresh tag
     e = launch_pdl_if(pdl_decode_enabled(), kernel, dim3(num_ctas), dim3(W * 32), L::kTotal,
                       stream, tk, tv, p);
@@ -755,15 +761,16 @@ static int chunk_group_tokens(int G) { return 16 / G; }
 // Chunks of one group of 16 rows; of two where they hold 1.5 groups' tokens on average
 // at most (drafts of 2 to 8 tokens: the second group of the shorter ones is empty).
 // More than 8 rows of few pairs spend their time in the join.  8 KV heads of 4 query
-// heads, int8, us a call, this kernel / the tiles of prefill: 64 x 4 tokens after 2000
-// 73.9 / 118, 16 x 4 28.8 / 42.2, 16 drafts 33.2 / 42; 32 x 8 (two full groups) 72.9 /
-// 68.0, 64 x 8 132 / 119; 1 x 2 16.9 / 20.4, 2 x 4 21.5 / 21.4, 1 x 4 26.3 / 20.5.
+// heads, int8, us a call, this kernel / the tiles of prefill: 600 x 4 tokens after 200
+// 111 / 182, 64 x 4 after 2000 73.6 / 106, 16 x 4 28.4 / 38.0, 4 x 4 20.5 / 21.0, 16 drafts
+// 32.8 / 37.8; 64 x 8 (two full groups) 132 / 106; 1 x 2 16.9 / 19.5, 2 x 4 21.6 / 20.3,
+// after 8000 27.7 / 24.3.
 bool chunks_by_runs(int num_tokens, int num_seqs, int max_q, int Hkv, int G, int max_context) {
   const int group = chunk_group_tokens(G);
   const int groups = (max_q + group - 1) / group;
   if (groups > 1 && (groups > 2 || 2ll * num_tokens > 3ll * group * num_seqs)) return false;
-  if (max_q * G > 8 && static_cast<int64_t>(num_seqs) * Hkv < 16) return false;
-  return num_seqs <= tc_chunk_seqs(max_context) / groups;
+  if (max_q * G > 8 && static_cast<int64_t>(num_seqs) * Hkv < 32) return false;
+  return tc_chunk_seqs(max_context) >= groups;  // (a launch takes whole chunks)
 }
 
 TcStatus launch_decode_q8(const AttentionQ8Params& a, bool e4m3, bool contig, int num_ctas,

@@ -406,18 +406,20 @@ def test_prefill_empty_chunks():
 def test_short_chunks(dtype, layout, hq, hkv):
     """Chunks of few tokens take decode's arithmetic, 16 rows at a time."""
     most = 2 * (16 // (hq // hkv))
-    new = [most, 1, most - 1, 0, most // 2, most // 2 + 1, 2, 1] * 2
-    cached = [0, 0, 14, 0, 100, 1000, 31, 257, 1, 20, 0, 7, 999, 15, 16, 17]
+    new = [most, 1, most - 1, 0, most // 2, most // 2 + 1, 2, 1] * 4
+    cached = [0, 0, 14, 0, 100, 1000, 31, 257, 1, 20, 0, 7, 999, 15, 16, 17] * 2
     b = Batch(dtype, layout, hq, hkv, [n + c for n, c in zip(new, cached)], new)
     b.check(b.prefill())
-    new = [1 + (most // 2 - 1) * (i % 2) for i in range(16)]
+    new = [1 + (most // 2 - 1) * (i % 2) for i in range(32)]
     b = Batch(dtype, layout, hq, hkv, [n + c for n, c in zip(new, cached)], new)
     b.check(b.prefill())
 
 
 @pytest.mark.parametrize("dtype", q8_ref.FORMATS)
 @pytest.mark.parametrize("new,cached", [([2], [9000]), ([1] * 300, [50] * 300), ([8, 1] * 120, [90] * 240),
-                                        ([8, 1, 5] * 3, [30000, 0, 1] * 3), ([4] * 8, [300] * 8),
+                                        ([8, 1, 5] * 6, [30000, 0, 1] * 6), ([4] * 16, [300] * 16),
+                                        ([4, 1, 2] * 400, [i % 77 for i in range(1200)]),
+                                        ([8, 1, 0] * 200, [i % 77 for i in range(600)]),
                                         ([3, 8] * 20, list(range(0, 2000, 50)))])
 def test_short_chunk_lengths(dtype, new, cached):
     b = Batch(dtype, "paged", 8, 2, [n + c for n, c in zip(new, cached)], new, bs=32)
@@ -428,8 +430,8 @@ def test_short_chunk_lengths(dtype, new, cached):
 
 
 def test_short_chunks_captured():
-    b = Batch(torch.float8_e4m3fn, "paged", 24, 6, [300, 700, 20], [4, 2, 2])
-    tail = torch.full((5, 24, D), math.nan, device=DEV).bfloat16()
+    b = Batch(torch.float8_e4m3fn, "paged", 48, 12, [300, 700, 20], [4, 2, 2])
+    tail = torch.full((5, 48, D), math.nan, device=DEV).bfloat16()
     b.q = torch.cat([b.q, tail])  # 13 rows for 3 chunks
     out = torch.full_like(b.q, 3.0)
     g = torch.cuda.CUDAGraph()
@@ -447,7 +449,7 @@ def test_short_chunks_captured():
 
 
 def test_short_chunks_checked():
-    b = Batch(torch.int8, "paged", 32, 8, [100, 60], [5, 6])
+    b = Batch(torch.int8, "paged", 64, 16, [100, 60], [5, 6])
     pkv.set_checked(True)
     b.check(b.prefill())
     assert pkv.get_device_error() == "none"

@@ -31,9 +31,9 @@
 // two at a time, took the larger part of the arithmetic away (75 to 32 us with the
 // filter).  8 KV heads, us: 1 token 4.1, 64 of as many sequences 4.4, 256 5.8; prompts
 // of 1000 5.1, 4096 10.1, 16384 22.0 (101 MB: 4.6 TB/s, 0.68 of a plain copy), 65536
-// 71 (5.7 TB/s, 0.83).  With rotary positions and 32 query heads: 1 5.6, 256 of as many
-// sequences 8.9, 1000 11.5, 4096 27, 16384 79 (369 MB: 4.7 TB/s, 0.69), 65536 285 (0.76);
-// there the keys' turn, in fp32 until they are rounded, takes 128 registers a thread.
+// 71 (5.7 TB/s, 0.83).  With rotary positions and 32 query heads: 1 5.6, 300 7.3, 1000
+// 11.8, 4096 27, 16384 77 (369 MB: 4.8 TB/s, 0.71); there the keys' turn, in fp32 until
+// they are rounded, takes some 120 registers a thread.
 #include <cuda_bf16.h>
 
 #include "decode_launch.cuh"
@@ -297,6 +297,13 @@ __device__ __forceinline__ void put_unit(const Unit& u) {
   if (lane == 0) *u.scale = s;
 }
 
+// The largest of three sizes, NaN if one is.
+__device__ __forceinline__ float larger_size(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Keys, turned; cs: the sines of the 16 rows.  kKind as for rope_rows: interleaved, half
 // with partners in whole chunks (which a lane holds both), half with others (read one
 // by one).
@@ -321,7 +328,7 @@ __device__ __forceinline__ void put_turned(const Unit& u, const float2 (*cs)[cs_
     raw[i][1] = t >= 0 ? ld_global_nc_v4(src + 8 * cb) : make_uint4(0u, 0u, 0u, 0u);
   }
   float x[4][16];
-  uint32_t top = 0;
+  float size = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = u.token[4 * i + r];
@@ -362,9 +369,10 @@ __device__ __forceinline__ void put_turned(const Unit& u, const float2 (*cs)[cs_
       }
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[i][j]) & 0x7fffffffu);
+    for (int j = 0; j < 16; j += 2) size = larger_size(size, x[i][j], x[i][j + 1]);
   }
-  top = __reduce_max_sync(kFull, top);
+  // (as bits they order as the values do, infinities and NaN above all others)
+  uint32_t top = __reduce_max_sync(kFull, __float_as_uint(size));
   const bool finite = top < 0x7f800000u;
   if (!finite) {
     top = 0;

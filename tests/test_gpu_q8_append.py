@@ -290,6 +290,33 @@ def test_rope(dtype, rotary, interleaved, T, start):
     assert bool((got[empty] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", q8_ref.FORMATS)
+@pytest.mark.parametrize("interleaved,rotary", [(False, 64), (False, 50), (True, 64)])
+def test_rope_non_finite(dtype, interleaved, rotary):
+    """NaN and infinities among the keys change no other code and no scale."""
+    T, hq, hkv = 40, 4, 2
+    plan = pkv.RopePlan(rotary, interleaved=interleaved)
+    q, k, v = (torch.randn(T, n, D, device=DEV).bfloat16() for n in (hq, hkv, hkv))
+    pos = torch.arange(T, dtype=torch.int32, device=DEV) + 77
+    slots = torch.arange(T, device=DEV)
+    odd = {(3, 0, 100): math.nan, (3, 1, 127): math.inf, (20, 0, 64): -math.inf,
+           (39, 1, 90): math.nan}  # past the rotated part
+    caches = [Cache(3, hkv, 16, dtype) for _ in range(2)]
+    for c, put in zip(caches, (False, True)):
+        for at, x in odd.items():
+            k[at] = x if put else 0.0
+        pkv.rope_append_q8(pos, slots, q, k, v, *c.dev, plan)
+    clean, got = ([x.cpu() for x in c.dev] for c in caches)
+    for (t, h, e), x in odd.items():
+        code = got[0][t // 16, h, t % 16, e].float()
+        assert code.isnan() if math.isnan(x) and dtype != torch.int8 else \
+            code == (0.0 if math.isnan(x) else math.copysign(float(q8_ref.QMAX[dtype]), x))
+        got[0].view(torch.int8)[t // 16, h, t % 16, e] = clean[0].view(torch.int8)[t // 16, h,
+                                                                                   t % 16, e]
+    for a, b in zip(clean, got):
+        assert torch.equal(a.view(torch.int8), b.view(torch.int8))
+
+
 @pytest.mark.parametrize("interleaved,rotary", [(False, 128), (False, 50), (True, 128)])
 def test_rope_one_launch_or_two(interleaved, rotary):
     """Queries and keys of 1000 tokens in one launch, of more in two: the same bits."""

@@ -542,7 +542,9 @@ PKV_API pkv_status pkv_contig_decode_attention_q8(
 /*
  * Causal prefill attention over it: arguments, layouts, errors and checked mode
  * as for pkv_paged_prefill_attention / pkv_contig_prefill_attention.  Rows of
- * q and out behind the last chunk are left alone.  A NaN code among the values of
+ * q and out behind the last chunk are left alone, and so are those of a chunk's tokens
+ * past its first max_q_tokens (checked mode reports such a chunk and leaves all of it
+ * alone).  A NaN code among the values of
  * a later token of the same chunk may make earlier tokens NaN, as in those calls.
  * Where there are few chunks their keys are dealt to all SMs and the parts joined
  * through the workspace; so are chunks of one to some eight tokens (drafts to be

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(W * 32, 1)
           req = 0;
         }
       }
-      const int tokens = min(p.group_tokens, n - t0);
+      const int tokens = min(p.group_tokens, min(n, p.max_q) - t0);
       ctx_s[i] = ctx > 0 && tokens > 0 ? max(ctx - n + t0 + tokens, 0) : 0;
       row_s[i] = q0 + t0;
       tok_s[i] = tokens;

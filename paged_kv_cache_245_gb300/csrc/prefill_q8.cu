@@ -290,7 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;  // the sequence is left unwritten
       }
     }
-    it.rows = Lq * G;
+    // (the workspace holds records for chunks of the call's bound: what a longer one has past
+    // it is left unwritten, whether its item is cut or not)
+    it.rows = min(Lq, p.max_q) * G;
     it.row0 = rt * 2 * TR;
     if (it.row0 >= it.rows) return false;  // past the chunk
     it.base = it.ctx - Lq;                 // position of the chunk's first token

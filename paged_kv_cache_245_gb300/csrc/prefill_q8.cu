@@ -63,8 +63,7 @@ constexpr float kOnePassSum = 7.9228163e28f;  // 2^96
 constexpr int kScaleFloats = 24;                      // of 8 groups: ks, log2 vs, 1 / vs
 constexpr int kConvert0 = 12, kConverters = 8;        // converter warps
 constexpr int kOffScales = kTilesBytes + 512;
-constexpr int kOffHeld = kOffScales + kScaleRing * kScaleFloats * 4;  // a word a converter warp
-constexpr int kSmemBytes = kOffHeld + kConverters * 4 + 1024;         // + alignment
+constexpr int kSmemBytes = kOffScales + kScaleRing * kScaleFloats * 4 + 1024;  // + alignment
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KiB");
 constexpr int kProducer = 10;                         // the code producer
 static_assert(kProducer == 10 && kConvert0 == 12, "warps 0-7 are the softmax's, 8 and 9 the next two");
@@ -161,6 +160,31 @@ __device__ __forceinline__ void cp_async_4_or_zero(void* dst, const void* src, b
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src),
                "r"(n)
                : "memory");
+}
+
+// Shared memory that is written anew after this warp's arrival on an mbarrier: read by
+// statements that the compiler places no later than where they stand.  What follows them
+// is __syncwarp and lane 0's arrival, which releases the reads of the whole warp to a
+// thread that waits for it and writes; a writer through the async proxy needs a proxy
+// fence between the reads and the arrival too.
+__device__ __forceinline__ uint4 ld_shared_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_addr(p))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ PItem ld_item(const PItem* p) {
+  static_assert(sizeof(PItem) == 40, "five pairs of words");
+  int32_t w[10];
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    asm volatile("ld.shared.v2.s32 {%0,%1}, [%2];"
+                 : "=r"(w[2 * i]), "=r"(w[2 * i + 1])
+                 : "r"(smem_addr(p) + 8 * i)
+                 : "memory");
+  return PItem{w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7], w[8], w[9]};
 }
 
 // Sixteen codes (a chunk of a row) as bf16, exact.
@@ -268,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int slot = n & (kRing - 1);
     if (!__all_sync(kFull, wait_or_abort(&B.ifull[slot], (n / kRing) & 1, abort, p.err)))
       return false;
-    it = ring[slot];
+    it = ld_item(&ring[slot]);
     __syncwarp();
     if (lane == 0) mbar_arrive(&B.iempty[slot]);
     return true;
@@ -381,7 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(4 * kRowStep == kKeys, "four rows a thread");
     const int row0 = (warp - kConvert0) * 4 + ((lane >> 4) << 1) + ((lane >> 2) & 1);
     const int ch = (lane & 3) + (((lane >> 2) ^ (lane >> 3)) & 1) * 4;  // chunk of 16 codes
-    volatile uint32_t* held = reinterpret_cast<uint32_t*>(smem + kOffHeld);
     int g = 0;  // tiles of all items
     int nread = 0;
     bool ok = true;
@@ -400,12 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned char* to = smem + kOffK + s * kStageBytes + kv * kOpBytes;
           uint4 c[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            c[i] = *reinterpret_cast<const uint4*>(from + i * kRowStep * 128);
-          // The arrival must not overtake the loads, whose values are needed only later:
-          // a store of something made of all of them comes between (without it the next
-          // codes now and then came in first).
-          held[warp - kConvert0] = c[0].x ^ c[1].x ^ c[2].x ^ c[3].x;
+          for (int i = 0; i < 4; ++i) c[i] = ld_shared_v4(from + i * kRowStep * 128);
+          // The next codes come by bulk copies, through the async proxy, and nothing has used
+          // these values yet: only a proxy fence of the lanes that read keeps the copies
+          // behind their reads (an arrival alone does not: without more the next codes now
+          // and then came in first).
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&B.cempty[kv]);
           if (kv == 0 && warp == kConvert0 && lane < 8) {

@@ -11,8 +11,8 @@
 // (e4m3 by the conversion instruction; int8 as 1024 + 128 + code, put together
 // from bytes, less 1152).  Queries enter as fp16 too: each row times a power of
 // two that puts its largest element at 2^14 .. 2^15, exact for bf16 elements down
-// to 2^-28 of that.  P is rounded to fp16 (2^-11 at most); a tile's product is
-// added to O in fp32 with its vs.
+// to 2^-28 of that.  P, at most 1, is rounded to fp16 times 2^15 (off by 2^-11 of it down
+// to 2^-29, by 2^-40 below); a tile's product is added to O in fp32 with its vs 2^-15.
 //
 // Schedule: that of decode_runs.cu -- the flattened list of tiles of every
 // (sequence, KV head) pair cut evenly over the warps of the grid, pieces of a
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(W * 32, 1)
             continue;
           }
           const float2 sc = scales[stage * kStageTiles + t];
-          vs[t] = sc.y;
+          vs[t] = sc.y * kPDown;
           const unsigned char* kt = st + t * 2 * kTileCodes;
           float sa[NT][4], sb[NT][4];
 #pragma unroll
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(W * 32, 1)
             l[y][0] += p0 + p2;
             l[y][1] += p1 + p3;
             // P^T as the B operand, rounded to fp16 once
-            pb[y][t][0] = movmatrix_trans(pack_half2(p0, p1));  // tokens 0..7
-            pb[y][t][1] = movmatrix_trans(pack_half2(p2, p3));  // tokens 8..15
+            pb[y][t][0] = movmatrix_trans(probabilities_to_half2(p0, p1));  // tokens 0..7
+            pb[y][t][1] = movmatrix_trans(probabilities_to_half2(p2, p3));  // tokens 8..15
           }
         }
         // ---- O^T += vs (V^T . P^T)

@@ -171,11 +171,12 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 1 : kQ8SmallCtas)
     l0 += p0 + p2;
     l1 += p1 + p3;
     // P^T as the B operand, rounded to fp16 once
-    const uint32_t b0 = movmatrix_trans(pack_half2(p0, p1));  // keys 0..7
-    const uint32_t b1 = movmatrix_trans(pack_half2(p2, p3));  // keys 8..15
+    const uint32_t b0 = movmatrix_trans(probabilities_to_half2(p0, p1));  // keys 0..7
+    const uint32_t b1 = movmatrix_trans(probabilities_to_half2(p2, p3));  // keys 8..15
 
     // ---- O^T += vs (V^T . P^T)
-    const uint64_t vs2 = umma::f2_pack(__float_as_uint(t.vs), __float_as_uint(t.vs));
+    const float vs = t.vs * kPDown;
+    const uint64_t vs2 = umma::f2_pack(__float_as_uint(vs), __float_as_uint(vs));
     const uint32_t* k0 = &t.v[0].x;
     const uint32_t* k1 = &t.v[1].x;
     const uint32_t* k8 = &t.v[2].x;

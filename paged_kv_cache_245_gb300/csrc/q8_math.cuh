@@ -31,6 +31,16 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return r;
 }
 
+// Two probabilities (0 .. 1: against the running maximum) as halves, times 2^15: rounded
+// by 2^-11 at most down to 2^-29, and by 2^-40 below.  (As they are, by 2^-11 down to 2^-14
+// and to 0 below 2^-25, while their sum kept them: under one key with nearly all of a
+// softmax the others' values were lost.)  The products with them are fp32; kPDown goes
+// into the values' scale.
+constexpr float kPUp = 32768.f, kPDown = 3.0517578125e-05f;
+__device__ __forceinline__ uint32_t probabilities_to_half2(float lo, float hi) {
+  return pack_half2(lo * kPUp, hi * kPUp);
+}
+
 // 1152 in both halves taken off: int8 code + 1152 -> code, exact.
 __device__ __forceinline__ uint32_t less_1152(uint32_t h) {
   uint32_t r;

@@ -1,0 +1,61 @@
+"""Rules of the appends to the 8-bit cache, each by its own small case: slots that tokens
+share."""
+import pytest
+import torch
+
+import paged_kv_cache_245_gb300 as pkv
+import q8_ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+D = 128
+
+
+class Group:
+    """One block of 16 rows and one head, with the append (and the rotary append)."""
+
+    def __init__(self, dtype, rope=False):
+        self.k, self.v = (torch.zeros(1, 1, 16, D, device=DEV).to(dtype) for _ in range(2))
+        self.ks, self.vs = (torch.zeros(1, 1, 1, device=DEV) for _ in range(2))
+        self.plan = pkv.RopePlan(128) if rope else None
+        self.dtype = dtype
+
+    def put(self, slots, x):
+        x = x.to(DEV).bfloat16()[:, None]
+        slots = torch.tensor(slots, device=DEV)
+        cache = (self.k, self.v, self.ks, self.vs)
+        if self.plan is None:
+            pkv.kv_append_q8(slots, x, x, *cache)
+        else:  # position 0: keys as they are
+            pos = torch.zeros(len(slots), dtype=torch.int32, device=DEV)
+            pkv.rope_append_q8(pos, slots, x, x, x, *cache, self.plan)
+        return self
+
+    def same_as(self, other):
+        for a, b in ((self.k, other.k), (self.v, other.v), (self.ks, other.ks), (self.vs, other.vs)):
+            assert torch.equal(a.view(torch.int8), b.view(torch.int8))
+
+
+def normal(n, seed=0, by=1.0):
+    return (torch.randn(n, D, generator=torch.Generator().manual_seed(seed)) * by).bfloat16().float()
+
+
+both = pytest.mark.parametrize("rope", [False, True])
+formats = pytest.mark.parametrize("dtype", q8_ref.FORMATS)
+
+
+@both
+@formats
+@pytest.mark.parametrize("slots", [[0, 1, 1], [1, 0, 1], [5, 5, 5]])
+def test_the_last_token_of_a_slot_counts_alone(dtype, rope, slots):
+    """A larger row that a later token of the call overwrites leaves no mark."""
+    x = normal(3)
+    for t in range(2):
+        if slots[t] in slots[t + 1:]:
+            x[t] *= 1000.0
+    got = Group(dtype, rope).put(slots, x)
+    last = {s: t for t, s in enumerate(slots)}
+    want = Group(dtype, rope).put(list(last), x[list(last.values())])
+    got.same_as(want)
+    assert float(got.ks) < 1.0 and float(got.vs) < 1.0

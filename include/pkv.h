@@ -493,7 +493,9 @@ enum {
  * each operation rounded once, so the codes are exact.  Appending position by
  * position therefore needs no preparation of a block (its first row starts each
  * group), and zeroed scales where a group's row 0 is never written.  Infinities
- * become the largest code; NaN stays NaN in e4m3 and becomes 0 in int8.  A slot that several tokens of a call share takes the
+ * become the largest code and NaN stays NaN in e4m3 and becomes 0 in int8, but
+ * where inv is 0 (infinities in a group that holds nothing else but zeros) x * inv
+ * is NaN for an infinity too.  A slot that several tokens of a call share takes the
  * last one's row; the others count for nothing, for a neither.
  * k and v are read at k_stride and v_stride elements per token as for
  * pkv_rope_append.  num_tokens is at most 2^22 (every CTA looks at all slots of a

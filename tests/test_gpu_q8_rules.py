@@ -1,5 +1,7 @@
 """Rules of the appends to the 8-bit cache, each by its own small case: slots that tokens
-share."""
+share, groups without a finite value but zero."""
+import math
+
 import pytest
 import torch
 
@@ -59,3 +61,20 @@ def test_the_last_token_of_a_slot_counts_alone(dtype, rope, slots):
     want = Group(dtype, rope).put(list(last), x[list(last.values())])
     got.same_as(want)
     assert float(got.ks) < 1.0 and float(got.vs) < 1.0
+
+
+@formats
+def test_infinities(dtype):
+    """The largest code beside finite values; with inv 0 what inf x 0 is: NaN, in int8 0."""
+    x = normal(2)
+    x[0, 3], x[1, 7] = math.inf, -math.inf
+    g = Group(dtype).put([0, 1], x)
+    top = float(q8_ref.QMAX[dtype])
+    assert float(g.k[0, 0, 0, 3].float()) == top and float(g.v[0, 0, 1, 7].float()) == -top
+    x = torch.zeros(2, D)
+    x[0, 3], x[1, 7] = math.inf, -math.inf
+    g = Group(dtype).put([0, 1], x)
+    assert float(g.ks) == 0.0
+    for c in (g.k[0, 0, 0, 3].float(), g.v[0, 0, 1, 7].float()):
+        assert float(c) == 0.0 if dtype == torch.int8 else bool(c.isnan())
+    assert float(g.k.float().nan_to_num().abs().sum()) == 0.0

@@ -463,9 +463,8 @@ PKV_API pkv_status pkv_contig_prefill_attention_scored(
  *   k_scale, v_scale   [num_blocks][Hkv][block_size / 16]  (contiguous: S / 16)
  *   value = code * scale
  * block_size (S) must be a multiple of 16.  Codes are 16-byte aligned, scales
- * 4-byte.  Copy-on-write copies and swaps go through pkv_block_copy /
- * pkv_block_swap, once over the codes and once over the scales (whose block is
- * Hkv * block_size / 4 bytes, which those calls want to be a multiple of 16).
+ * 4-byte.  Copy-on-write copies and swaps are pkv_block_copy / pkv_block_swap of the
+ * codes and pkv_q8_scale_copy / pkv_q8_scale_swap of the scales.
  */
 typedef struct pkv_q8_cache {
     void *k, *v;                /* codes                                        */
@@ -606,6 +605,20 @@ PKV_API pkv_status pkv_block_copy(const int64_t *src_dst_pairs, int64_t n,
  * not overlap.  Bit-exact.
  */
 PKV_API pkv_status pkv_block_swap(const int64_t *pairs, int64_t n,
+                          void *const *src_k, void *const *src_v, int64_t src_num_blocks,
+                          void *const *dst_k, void *const *dst_v, int64_t dst_num_blocks,
+                          int32_t num_layers, int64_t block_bytes, void *stream);
+
+/*
+ * The same two calls for the scales of an 8-bit cache, whose blocks of block_bytes
+ * = Hkv * block_size / 4 need not be a multiple of 16: any multiple of 4, pointers
+ * 4-byte aligned.
+ */
+PKV_API pkv_status pkv_q8_scale_copy(const int64_t *src_dst_pairs, int64_t n,
+                          void *const *k_scales, void *const *v_scales,
+                          int32_t num_layers, int64_t num_blocks,
+                          int64_t block_bytes, void *stream);
+PKV_API pkv_status pkv_q8_scale_swap(const int64_t *pairs, int64_t n,
                           void *const *src_k, void *const *src_v, int64_t src_num_blocks,
                           void *const *dst_k, void *const *dst_v, int64_t dst_num_blocks,
                           int32_t num_layers, int64_t block_bytes, void *stream);

@@ -42,6 +42,7 @@ EXPORTED = ("pkv_kv_append", "pkv_decode_num_splits", "pkv_decode_uses_tensor_co
             "pkv_paged_decode_attention_q8", "pkv_contig_decode_attention_q8",
             "pkv_q8_prefill_workspace_size",
             "pkv_paged_prefill_attention_q8", "pkv_contig_prefill_attention_q8",
+            "pkv_q8_scale_copy", "pkv_q8_scale_swap",
             "pkv_get_device_error", "pkv_status_string", "pkv_last_error")
 
 
@@ -106,6 +107,8 @@ def lib():
                                               ctypes.c_float, Heads, vp, vp, sz, vp]
     L.pkv_block_copy.argtypes = [vp, i64, vp, vp, i32, i64, i64, vp]
     L.pkv_block_swap.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i32, i64, vp]
+    L.pkv_q8_scale_copy.argtypes = L.pkv_block_copy.argtypes
+    L.pkv_q8_scale_swap.argtypes = L.pkv_block_swap.argtypes
     L.pkv_paged_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, i32, i32, i32,
                                         ctypes.c_float, Heads, vp, vp, sz, vp]
     L.pkv_contig_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i64,
@@ -1018,8 +1021,7 @@ def _block_dtype(t):
 def block_copy(src_dst_pairs, k_caches, v_caches):
     """Copy whole blocks src -> dst (pairs [n, 2] int64 on the device) in every
     layer's K and V cache (lists of [num_blocks, ...] tensors of one type: bf16,
-    or an 8-bit cache's codes, and in a call of their own its scales, whose block
-    must be a multiple of 16 bytes)."""
+    or an 8-bit cache's codes, and in a call of their own its scales)."""
     _need(src_dst_pairs, torch.int64, "src_dst_pairs", 2)
     L = len(k_caches)
     if L != len(v_caches) or L == 0:
@@ -1034,16 +1036,17 @@ def block_copy(src_dst_pairs, k_caches, v_caches):
     block_bytes = k_caches[0][0].numel() * dtype.itemsize
     kp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_caches])
     vp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_caches])
-    _check(lib().pkv_block_copy(_ptr(src_dst_pairs), src_dst_pairs.shape[0], kp, vp, L, nb,
-                                block_bytes, _stream(k_caches[0])))
+    copy = lib().pkv_q8_scale_copy if dtype is torch.float32 else lib().pkv_block_copy
+    _check(copy(_ptr(src_dst_pairs), src_dst_pairs.shape[0], kp, vp, L, nb, block_bytes,
+                _stream(k_caches[0])))
 
 
 def block_swap(pairs, src_k, src_v, dst_k, dst_v):
     """Copy whole blocks from one pool to another, pairs [n, 2] int64 of
     (src block, dst block), in every layer's K and V (lists of [blocks, ...]
-    tensors of one type, as for block_copy, one shape per side).  Either side may be page-locked host
-    memory (``tensor.pin_memory()``): that is the swap of pre-empted
-    sequences out of, and back into, the device cache.  pairs may be a
+    tensors of one type, as for block_copy, one shape per side).  Either side
+    may be page-locked host memory (``tensor.pin_memory()``): that is the swap
+    of pre-empted sequences out of, and back into, the device cache.  pairs may be a
     device tensor or a pinned host tensor."""
     if pairs.dtype != torch.int64 or pairs.dim() != 2 or pairs.shape[1] != 2 \
             or not pairs.is_contiguous():
@@ -1067,8 +1070,9 @@ def block_swap(pairs, src_k, src_v, dst_k, dst_v):
     dev = next((t for t in (src_k[0], dst_k[0], pairs) if t.is_cuda), None)
     if dev is None:
         raise ValueError("one side (or pairs) must be on the GPU")
-    _check(lib().pkv_block_swap(_ptr(pairs), pairs.shape[0], arr[0], arr[1], blocks[0][0],
-                                arr[2], arr[3], blocks[1][0], L, block_bytes, _stream(dev)))
+    swap = lib().pkv_q8_scale_swap if dtype is torch.float32 else lib().pkv_block_swap
+    _check(swap(_ptr(pairs), pairs.shape[0], arr[0], arr[1], blocks[0][0], arr[2], arr[3],
+                blocks[1][0], L, block_bytes, _stream(dev)))
 
 
 def set_checked(enable):

@@ -83,9 +83,13 @@ cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream) {
                     stream, p);
 }
 
+__device__ __forceinline__ uint4 ld_unit(const uint4* p) { return ld_global_nc_v4(p); }
+__device__ __forceinline__ uint32_t ld_unit(const uint32_t* p) { return __ldg(p); }
+
 // Block copy (within one pool) and block swap (between two): blockIdx.x
-// strides over the block's 16-byte chunks, blockIdx.y is the pair,
-// blockIdx.z = 2 * layer + (0 for K, 1 for V).
+// strides over the block's chunks (Unit: 16 bytes, or words), blockIdx.y is the
+// pair, blockIdx.z = 2 * layer + (0 for K, 1 for V).
+template <typename Unit>
 __global__ void __launch_bounds__(256) block_copy_kernel(const CopyParams p) {
   grid_dependency_trigger();
   grid_dependency_wait();
@@ -100,31 +104,32 @@ __global__ void __launch_bounds__(256) block_copy_kernel(const CopyParams p) {
   }
   const unsigned char* sbase = static_cast<const unsigned char*>(is_v ? p.v[layer] : p.k[layer]);
   unsigned char* dbase = static_cast<unsigned char*>(is_v ? p.dv[layer] : p.dk[layer]);
-  const uint4* s = reinterpret_cast<const uint4*>(sbase + src * p.block_bytes);
-  uint4* d = reinterpret_cast<uint4*>(dbase + dst * p.block_bytes);
-  const int64_t n16 = p.block_bytes / 16;
+  const Unit* s = reinterpret_cast<const Unit*>(sbase + src * p.block_bytes);
+  Unit* d = reinterpret_cast<Unit*>(dbase + dst * p.block_bytes);
+  const int64_t n = p.block_bytes / sizeof(Unit);
   constexpr int kUnroll = 4;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  for (; i + (kUnroll - 1) * stride < n16; i += kUnroll * stride) {
-    uint4 v[kUnroll];
+  for (; i + (kUnroll - 1) * stride < n; i += kUnroll * stride) {
+    Unit v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = ld_global_nc_v4(s + i + u * stride);
+    for (int u = 0; u < kUnroll; ++u) v[u] = ld_unit(s + i + u * stride);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) d[i + u * stride] = v[u];
   }
-  for (; i < n16; i += stride) d[i] = ld_global_nc_v4(s + i);
+  for (; i < n; i += stride) d[i] = ld_unit(s + i);
 }
 
 cudaError_t launch_block_copy(const CopyParams& p, int64_t num_pairs, cudaStream_t stream) {
   if (num_pairs == 0 || p.num_layers == 0) return cudaSuccess;
-  const int64_t n16 = p.block_bytes / 16;
-  int64_t bx = (n16 + 256 * 4 - 1) / (256 * 4);
+  const int64_t n = p.block_bytes / (p.by_words ? 4 : 16);
+  int64_t bx = (n + 256 * 4 - 1) / (256 * 4);
   if (bx < 1) bx = 1;
   if (bx > 64) bx = 64;
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(num_pairs),
                   static_cast<unsigned>(2 * p.num_layers));
-  return launch_pdl(block_copy_kernel, grid, dim3(256), 0, stream, p);
+  return p.by_words ? launch_pdl(block_copy_kernel<uint32_t>, grid, dim3(256), 0, stream, p)
+                    : launch_pdl(block_copy_kernel<uint4>, grid, dim3(256), 0, stream, p);
 }
 
 }  // namespace pkv

@@ -33,6 +33,7 @@ struct CopyParams {
   int64_t num_blocks;     // source ids in checked mode
   int64_t dst_num_blocks; // destination ids in checked mode
   int64_t block_bytes;
+  int32_t by_words;       // 4-byte copies (blocks or pools that 16 bytes do not divide)
   int32_t checked;
   int* err;
 };

@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <vector>
 
 #include "../../include/pkv.h"
@@ -1118,7 +1119,7 @@ namespace {
 // slices of at most 65535 pairs (grid y) and kMaxCopyLayers layers.
 pkv_status copy_blocks(const int64_t* pairs, int64_t n, void* const* sk, void* const* sv,
                        int64_t src_blocks, void* const* dk, void* const* dv, int64_t dst_blocks,
-                       int32_t num_layers, int64_t block_bytes, void* stream) {
+                       int32_t num_layers, int64_t block_bytes, bool by_words, void* stream) {
   int* err = nullptr;
   pkv_status st = device_info(nullptr, &err, nullptr);
   if (st != PKV_OK) return st;
@@ -1139,6 +1140,7 @@ pkv_status copy_blocks(const int64_t* pairs, int64_t n, void* const* sk, void* c
       p.num_blocks = src_blocks;
       p.dst_num_blocks = dst_blocks;
       p.block_bytes = block_bytes;
+      p.by_words = by_words ? 1 : 0;
       p.checked = g_checked.load();
       p.err = err;
       const cudaError_t e = pkv::launch_block_copy(p, np, s);
@@ -1666,35 +1668,52 @@ pkv_status pkv_contig_prefill_attention_q8(
                              workspace, workspace_bytes, stream);
 }
 
-pkv_status pkv_block_copy(const int64_t* src_dst_pairs, int64_t n, void* const* k_caches,
-                          void* const* v_caches, int32_t num_layers, int64_t num_blocks,
-                          int64_t block_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// Whether blocks of block_bytes in these pools go by words: `unit` bytes (16, or 4 for
+// scales) must divide them, and 16 are copied at once where they do.
+bool copy_by_words(int unit, int64_t block_bytes, std::initializer_list<void* const*> pools,
+                   int32_t num_layers) {
+  if (unit == 16) return false;
+  if (block_bytes % 16 != 0) return true;
+  for (void* const* pool : pools)
+    for (int32_t l = 0; l < num_layers; ++l)
+      if (!aligned(pool[l], 16)) return true;
+  return false;
+}
+
+pkv_status block_copy_common(const int64_t* src_dst_pairs, int64_t n, void* const* k_caches,
+                             void* const* v_caches, int32_t num_layers, int64_t num_blocks,
+                             int64_t block_bytes, int unit, void* stream) {
   if (n < 0 || num_layers < 0) return fail(PKV_ERR_INVALID_ARG, "negative size");
   if (n == 0 || num_layers == 0) return PKV_OK;
   if (!src_dst_pairs || !aligned(src_dst_pairs, 8))
     return fail(PKV_ERR_INVALID_ARG, "src_dst_pairs null or misaligned");
   if (!k_caches || !v_caches) return fail(PKV_ERR_INVALID_ARG, "null cache pointer array");
-  if (block_bytes <= 0 || block_bytes % 16 != 0)
-    return fail(PKV_ERR_INVALID_ARG, "block_bytes must be a positive multiple of 16");
+  if (block_bytes <= 0 || block_bytes % unit != 0)
+    return fail(PKV_ERR_INVALID_ARG, "block_bytes must be a positive multiple of %d", unit);
   if (num_blocks <= 0) return fail(PKV_ERR_INVALID_ARG, "num_blocks must be >= 1");
   for (int32_t l = 0; l < num_layers; ++l) {
-    if (!k_caches[l] || !v_caches[l] || !aligned(k_caches[l], 16) || !aligned(v_caches[l], 16))
+    if (!k_caches[l] || !v_caches[l] || !aligned(k_caches[l], unit) || !aligned(v_caches[l], unit))
       return fail(PKV_ERR_INVALID_ARG, "cache pointer of layer %d null or misaligned", l);
   }
   return copy_blocks(src_dst_pairs, n, k_caches, v_caches, num_blocks, k_caches, v_caches,
-                     num_blocks, num_layers, block_bytes, stream);
+                     num_blocks, num_layers, block_bytes,
+                     copy_by_words(unit, block_bytes, {k_caches, v_caches}, num_layers), stream);
 }
 
-pkv_status pkv_block_swap(const int64_t* pairs, int64_t n, void* const* src_k,
-                          void* const* src_v, int64_t src_num_blocks, void* const* dst_k,
-                          void* const* dst_v, int64_t dst_num_blocks, int32_t num_layers,
-                          int64_t block_bytes, void* stream) {
+pkv_status block_swap_common(const int64_t* pairs, int64_t n, void* const* src_k,
+                             void* const* src_v, int64_t src_num_blocks, void* const* dst_k,
+                             void* const* dst_v, int64_t dst_num_blocks, int32_t num_layers,
+                             int64_t block_bytes, int unit, void* stream) {
   if (n < 0 || num_layers < 0) return fail(PKV_ERR_INVALID_ARG, "negative size");
   if (n == 0 || num_layers == 0) return PKV_OK;
   if (!src_k || !src_v || !dst_k || !dst_v)
     return fail(PKV_ERR_INVALID_ARG, "null pool pointer array");
-  if (block_bytes <= 0 || block_bytes % 16 != 0)
-    return fail(PKV_ERR_INVALID_ARG, "block_bytes must be a positive multiple of 16");
+  if (block_bytes <= 0 || block_bytes % unit != 0)
+    return fail(PKV_ERR_INVALID_ARG, "block_bytes must be a positive multiple of %d", unit);
   if (src_num_blocks <= 0 || dst_num_blocks <= 0)
     return fail(PKV_ERR_INVALID_ARG, "pool sizes must be >= 1");
   if (num_layers > 4096) return fail(PKV_ERR_INVALID_ARG, "more than 4096 layers");
@@ -1712,15 +1731,50 @@ pkv_status pkv_block_swap(const int64_t* pairs, int64_t n, void* const* src_k,
   for (int a = 0; a < 4; ++a)
     for (int32_t l = 0; l < num_layers; ++l) {
       void* d = device_view(in[a][l], dev);
-      if (d == nullptr || !aligned(d, 16))
+      if (d == nullptr || !aligned(d, unit))
         return fail(PKV_ERR_INVALID_ARG,
-                    "%s[%d] must be device, managed or page-locked host memory, 16-byte aligned",
-                    kName[a], l);
+                    "%s[%d] must be device, managed or page-locked host memory, %d-byte aligned",
+                    kName[a], l, unit);
       view[a * num_layers + l] = d;
     }
-  return copy_blocks(pv, n, view.data(), view.data() + num_layers, src_num_blocks,
-                     view.data() + 2 * num_layers, view.data() + 3 * num_layers, dst_num_blocks,
-                     num_layers, block_bytes, stream);
+  void* const* const at = view.data();
+  return copy_blocks(pv, n, at, at + num_layers, src_num_blocks, at + 2 * num_layers,
+                     at + 3 * num_layers, dst_num_blocks, num_layers, block_bytes,
+                     copy_by_words(unit, block_bytes, {at}, 4 * num_layers), stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_block_copy(const int64_t* src_dst_pairs, int64_t n, void* const* k_caches,
+                          void* const* v_caches, int32_t num_layers, int64_t num_blocks,
+                          int64_t block_bytes, void* stream) {
+  return block_copy_common(src_dst_pairs, n, k_caches, v_caches, num_layers, num_blocks,
+                           block_bytes, 16, stream);
+}
+
+pkv_status pkv_block_swap(const int64_t* pairs, int64_t n, void* const* src_k,
+                          void* const* src_v, int64_t src_num_blocks, void* const* dst_k,
+                          void* const* dst_v, int64_t dst_num_blocks, int32_t num_layers,
+                          int64_t block_bytes, void* stream) {
+  return block_swap_common(pairs, n, src_k, src_v, src_num_blocks, dst_k, dst_v, dst_num_blocks,
+                           num_layers, block_bytes, 16, stream);
+}
+
+pkv_status pkv_q8_scale_copy(const int64_t* src_dst_pairs, int64_t n, void* const* k_scales,
+                             void* const* v_scales, int32_t num_layers, int64_t num_blocks,
+                             int64_t block_bytes, void* stream) {
+  return block_copy_common(src_dst_pairs, n, k_scales, v_scales, num_layers, num_blocks,
+                           block_bytes, 4, stream);
+}
+
+pkv_status pkv_q8_scale_swap(const int64_t* pairs, int64_t n, void* const* src_k,
+                             void* const* src_v, int64_t src_num_blocks, void* const* dst_k,
+                             void* const* dst_v, int64_t dst_num_blocks, int32_t num_layers,
+                             int64_t block_bytes, void* stream) {
+  return block_swap_common(pairs, n, src_k, src_v, src_num_blocks, dst_k, dst_v, dst_num_blocks,
+                           num_layers, block_bytes, 4, stream);
 }
 
 void pkv_set_checked(int enable) { g_checked.store(enable ? 1 : 0); }

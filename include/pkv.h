@@ -496,6 +496,12 @@ enum {
  * where inv is 0 (infinities in a group that holds nothing else but zeros) x * inv
  * is NaN for an infinity too.  A slot that several tokens of a call share takes the
  * last one's row; the others count for nothing, for a neither.
+ * A row that is written over later (a draft that was rejected) stays in its group's
+ * scale, and the rows that it made the append round again stay so, until the group
+ * starts anew: up to 15 rows beside it and those that follow are then held to half a
+ * step of the larger scale.  To take drafts back without a trace, copy the tail block
+ * (codes and scales, as below) before they are appended, and back before the tokens
+ * that were accepted are.
  * k and v are read at k_stride and v_stride elements per token as for
  * pkv_rope_append.  num_tokens is at most 2^22 (every CTA looks at all slots of a
  * call).

@@ -1,5 +1,6 @@
 """Rules of the appends to the 8-bit cache, each by its own small case: slots that tokens
-share, groups without a finite value but zero."""
+share, groups without a finite value but zero, rows that are written over later
+(rejected drafts)."""
 import math
 
 import pytest
@@ -37,6 +38,10 @@ class Group:
     def same_as(self, other):
         for a, b in ((self.k, other.k), (self.v, other.v), (self.ks, other.ks), (self.vs, other.vs)):
             assert torch.equal(a.view(torch.int8), b.view(torch.int8))
+
+
+def rows(g):
+    return [q8_ref.values(c.cpu(), s.cpu())[0, 0] for c, s in ((g.k, g.ks), (g.v, g.vs))]
 
 
 def normal(n, seed=0, by=1.0):
@@ -78,3 +83,57 @@ def test_infinities(dtype):
     for c in (g.k[0, 0, 0, 3].float(), g.v[0, 0, 1, 7].float()):
         assert float(c) == 0.0 if dtype == torch.int8 else bool(c.isnan())
     assert float(g.k.float().nan_to_num().abs().sum()) == 0.0
+
+
+def half_step(x, scale, dtype):
+    """Half a step of the codes of values x with the given scale."""
+    if dtype == torch.int8:
+        return torch.full_like(x, scale / 2)
+    return torch.maximum(x.abs() * 2.0 ** -4, torch.full_like(x, scale * 2.0 ** -10))
+
+
+@both
+@formats
+@pytest.mark.parametrize("by", [1.0, 4.0, 30.0])
+def test_rejected_drafts(dtype, rope, by):
+    """Five rows, three drafts `by` times as large, then other rows in the drafts' slots: the
+    scale stays that of the drafts.  Each row is within half a step of it, the rows before the
+    drafts by one more rounding with the smaller scale (2^-20: fp32's own)."""
+    x, drafts, after = normal(5), normal(3, 1, by), normal(4, 2)
+    g = Group(dtype, rope).put(range(5), x)
+    first = float(g.ks)
+    g.put([5, 6, 7], drafts)
+    grown = float(g.ks)
+    assert grown >= first and (by == 1.0 or grown > first)
+    g.put([5, 6, 7, 8], after)
+    assert float(g.ks) == pytest.approx(
+        max(grown, float(after.abs().max()) / float(q8_ref.QMAX[dtype])), rel=2.0 ** -22)
+    scale = float(g.ks)
+    for got in rows(g):
+        want = torch.cat([x, after]).double()
+        bound = half_step(want, scale, dtype)
+        once = half_step(want[:5], first, dtype)
+        if scale > first:  # the second rounding is of a value that the first has moved
+            bound[:5] = once + half_step(want[:5].abs() + once, scale, dtype)
+        assert bool(((got[:9] - want).abs() <= bound * (1 + 2.0 ** -20)).all())
+        assert bool((got[9:] == 0).all())
+
+
+@both
+@formats
+def test_drafts_taken_back(dtype, rope):
+    """The tail block copied before the drafts, and back, leaves no trace of them."""
+    x, drafts, after = normal(5), normal(3, 1, 30.0), normal(2, 2)
+    want = Group(dtype, rope).put(range(5), x).put([5, 6], after)
+    g = Group(dtype, rope)
+    for name in ("k", "v", "ks", "vs"):  # a second block to keep the tail in
+        t = getattr(g, name)
+        setattr(g, name, torch.cat([t.view(torch.int8), t.view(torch.int8)]).view(t.dtype))
+    g.put(range(5), x)
+    there, back = (torch.tensor([p], device=DEV) for p in ([0, 1], [1, 0]))
+    for pairs, put in ((there, lambda: g.put([5, 6, 7], drafts)), (back, lambda: g.put([5, 6], after))):
+        pkv.block_copy(pairs, [g.k], [g.v])
+        pkv.block_copy(pairs, [g.ks], [g.vs])
+        put()
+    for name in ("k", "v", "ks", "vs"):
+        assert torch.equal(getattr(g, name)[:1].view(torch.int8), getattr(want, name).view(torch.int8))

@@ -42,10 +42,7 @@
 // up to 16 / G tokens, in two columns of products; each row masks the positions past its
 // token.  64 chunks of 4 tokens after 2000 take 74 us for 39 us of reads: eight warps of
 // 255 registers, two a scheduler, wait for their own results (issue slots 39 % busy).
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
+#include "decode_launch.cuh"
 #include "decode_tc.cuh"
 #include "q8.cuh"
 #include "q8_math.cuh"
@@ -683,16 +680,9 @@ cudaError_t launch_shape(const CUtensorMap& tk, const CUtensorMap& tv, const Dec
                          int num_ctas, cudaStream_t stream) {
   using L = Q8Smem<W, S, MH>;
   static unsigned long long done_mask = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
   auto kernel = decode_q8_kernel<kContig, kE4m3, kChunks, W, S, MH>;
-  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
-    if (e != cudaSuccess) return e;
-    __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
-  }
+  cudaError_t e = ensure_smem_limit(kernel, L::kTotal, &done_mask);
+  if (e != cudaSuccess) return e;
   // (of chunks, whole ones: their groups are the schedule's sequences)
   const int groups = kChunks ? p0.groups : 1;
   const int chunk = tc_chunk_seqs(p0.max_context) / groups * groups;
@@ -726,23 +716,9 @@ cudaError_t launch_heads(const CUtensorMap& tk, const CUtensorMap& tv, const Dec
                   : launch_shape<kContig, kE4m3, false, 10, 2, 8>(tk, tv, p, num_ctas, stream);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
 // Codes [rows][128] as a 2-D tensor; boxes of 16 rows, 128-byte swizzle.
 bool encode_codes(CUtensorMap* map, const void* base, int64_t rows) {
-  auto enc = map_encoder();
+  auto enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kCodeRowBytes), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kCodeRowBytes)};

@@ -12,8 +12,6 @@
 
 namespace pkv {
 
-namespace {
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -27,8 +25,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
-
-}  // namespace
 
 // [rows][128] bf16 viewed as a 2-D tensor; boxes of 16 rows x 64 columns
 // (128 bytes), 128-byte swizzle.

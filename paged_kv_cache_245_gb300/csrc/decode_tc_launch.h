@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -10,6 +11,9 @@
 #include "score.h"
 
 namespace pkv {
+
+// cuTensorMapEncodeTiled, looked up once; null if the driver lacks it.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 constexpr int kTcMaxSeqs = 512;  // sequences per launch (larger batches run in chunks)
 constexpr int kRecStride = 132;  // floats per head record: o[128], m, l, pad

@@ -37,6 +37,7 @@
 // 240 and 1529.  512 tokens after 8000 (floor 36) 69 us, 64 (4.4) 31.
 #include <climits>
 
+#include "decode_launch.cuh"
 #include "pkv_device.cuh"
 #include "prefill.cuh"
 #include "q8.cuh"
@@ -79,8 +80,8 @@ static_assert(256 * kRegsSoftmax + 128 * kRegsRoles + 32 * kConverters * kRegsCo
 constexpr int kRingUsers = 10 + kConverters;  // readers: softmax, MMA, producer, converters
 constexpr int kRing = 4;                              // item descriptors in flight
 constexpr int kSplitItems = 4;               // items an SM up to which they are cut
-constexpr int kSortPairs = 512;              // (row tiles, sequence) pairs that are sorted at most
-constexpr int kSplitPairs = 1024;            // (sequence, row tiles) pairs up to which they are
+constexpr int kSplitPairs = 1024;            // (sequence, row tiles) pairs up to which they are cut
+constexpr int kSortPairs = 512;              // such pairs up to which whole items are sorted
 constexpr int kItemCost = 2;                 // what an item costs, in key tiles
 constexpr int kLeastUnits = 6;               // a CTA's share is at least this
 constexpr int kPieceRow = 136;               // floats of a piece's row: o[128], m, l
@@ -1195,16 +1196,9 @@ __global__ void __launch_bounds__(256) prefill_q8_join_kernel(const __grid_const
 template <bool kE4m3>
 cudaError_t launch(const CUtensorMap& tq, const PrefillQ8Params& p, int grid, cudaStream_t stream) {
   static unsigned long long done_mask = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
   auto kernel = prefill_q8_kernel<kE4m3>;
-  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    __atomic_fetch_or(&done_mask, bit, __ATOMIC_ACQ_REL);
-  }
+  const cudaError_t e = ensure_smem_limit(kernel, kSmemBytes, &done_mask);
+  if (e != cudaSuccess) return e;
   return launch_pdl_if(pdl_decode_enabled(), kernel, dim3(static_cast<unsigned>(grid)),
                        dim3(kThreads), kSmemBytes, stream, tq, p);
 }

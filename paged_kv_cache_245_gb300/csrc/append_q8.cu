@@ -24,14 +24,15 @@
 // is read once.  8 lanes hold a row, each two chunks of 8 elements, as in
 // rope_rows.cuh: a lane has both elements of its turned pairs.
 //
-// What bounds it: memory for prompts, three dependent reads (slot, slots, rows) and
-// the scale for few tokens.  One CTA an SM, as large as the registers allow, keeps
-// the passes over the slots few and every SM as busy as the next; with 32 tokens a
-// CTA and three CTAs an SM 16384 tokens took 32 us.  The maximum on the bf16 bits,
-// two at a time, took the larger part of the arithmetic away (75 to 32 us with the
-// filter).  8 KV heads, us: 1 token 4.1, 64 of as many sequences 4.4, 256 5.8; prompts
-// of 1000 5.1, 4096 10.1, 16384 22.0 (101 MB: 4.6 TB/s, 0.68 of a plain copy), 65536
-// 71 (5.7 TB/s, 0.83).  With rotary positions and 32 query heads: 1 5.6, 300 7.3, 1000
+// What bounds it: for few tokens three dependent reads (slot, slots, rows) and the scale;
+// for prompts the wait for rows (a warp loads a unit, takes its maximum, rounds and stores
+// it, and only then asks for the next; DRAM is at 42 % of its peak).  One CTA an SM, as
+// large as the registers allow, keeps the passes over the slots few and every SM as busy
+// as the next; with 32 tokens a CTA and three CTAs an SM 16384 tokens took 32 us.  The
+// maximum on the bf16 bits, two at a time, took the larger part of the arithmetic away (75
+// to 32 us with the filter).  8 KV heads, us: 1 token 4.1, 64 of as many sequences 4.4, 256
+// 5.8; prompts of 1000 5.1, 4096 10.1, 16384 21.6 (101 MB: 4.7 TB/s, 0.69 of a plain copy),
+// 65536 70 (5.7 TB/s, 0.85).  With rotary positions and 32 query heads: 1 5.7, 300 7.3, 1000
 // 11.8, 4096 27, 16384 77 (369 MB: 4.8 TB/s, 0.71); there the keys' turn, in fp32 until
 // they are rounded, takes some 120 registers a thread.
 #include <cuda_bf16.h>

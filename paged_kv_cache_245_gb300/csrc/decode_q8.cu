@@ -33,10 +33,12 @@
 // neighbours meet in one lane.
 //
 // What bounds it: HBM, past 8 us that the launch, the schedule (contexts, table, rows
-// one after another) and the joins take.  128 sequences of 8192 with 8 KV heads (2.15
-// GB) take 328 us, 6.55 TB/s or 0.97 of a plain copy; 64 ragged ones (520 MB) 87 us,
-// 0.89; 32 of 100 to 4095 with 4 KV heads (85 MB) 24 us, 0.52.  Two tiles a stage took
-// the first from 453 to 334 us.  Small batches are decode_q8_cluster.cu's.
+// one after another) and the joins take.  128 sequences of 8000 to 8192 with 8 KV heads of
+// 7 query heads (2.13 GB, e4m3) take 328 us, 6.5 TB/s or 0.96 of a plain copy; 64 ragged
+// ones up to 8192 (157 MB) 33 us, 0.70; 32 of 100 to 4095 with 4 KV heads (36 MB) 16 us,
+// 0.33; long contexts (int8, 4 query heads): 8 of 131072 (2.15 GB) 336 us, 0.94, 8 of
+// 32768 90 us, one of 131072 55 us, of 32768 25 us.  Two tiles a stage took the first from
+// 453 to 334 us.  Small batches are decode_q8_cluster.cu's.
 //
 // Chunks of few tokens (kChunks) are the same with 16 rows, (token, query head) pairs of
 // up to 16 / G tokens, in two columns of products; each row masks the positions past its

@@ -11,9 +11,9 @@
 // warp about 1 us (its loads wait for one another more than its products do; two
 // or three more tiles in flight, or two tiles a step, did not change that), so the
 // host takes this kernel only where a warp has few tiles.  8 KV heads, us a call,
-// this kernel / decode_q8.cu: 1 sequence of 1000 4.6 / 17.2, of 8000 12.0 / 21.3, 4
-// of 1000 6.2 / 11.3, 8 of 512 6.0 / 10.3, 16 of 512 7.3 / 11.8, 8 of 2000 12.1 /
-// 15.6.
+// this kernel / decode_q8.cu: 1 sequence of 1000 5.2 / 14.7, of 8000 11.2 / 17.8, 4
+// of 1000 5.8 / 11.3, 8 of 512 5.6 / 10.3, 16 of 512 6.2 / 11.2, 8 of 2000 10.8 /
+// 14.0.
 //
 // Math of a tile: as in decode_q8.cu.  A lane's part of K is 32 elements of rows
 // g and g + 8; of V, 16 elements (16 g ..) of keys 2 tq, 2 tq + 1, 2 tq + 8 and 2 tq

@@ -1438,10 +1438,10 @@ pkv_status append_q8_common(const int32_t* positions, const int64_t* slot_mappin
 // cluster of 8-warp CTAs that the device holds for every pair at once, or, past one
 // such CTA an SM, 4-warp CTAs alone; where a warp then has at most 8 tiles (warps 0
 // if not).  8 KV heads, us a call, that kernel / the other: 8 tiles a warp (1
-// sequence of 8000, 4 of 4000, 8 of 2000) 12.0 / 21.3, 12.3 / 16.6, 12.1 / 15.6, 4
-// heads and 32 ragged sequences up to 4095 (32 tiles) 27.4 / 17.8; 4-warp CTAs: 32
-// of 128 (2) 5.6 / 8.9, 32 of 512 (8) 13.0 / 14.3.  In two rounds of CTAs it is the
-// slower one: 64 of 256 18.1 / 15.1.
+// sequence of 8000, 4 of 4000, 8 of 2000) 11.2 / 17.8, 11.0 / 15.2, 10.8 / 14.0, 4
+// heads and 32 ragged sequences up to 4095 (32 tiles) 30.2 / 16.1; 4-warp CTAs: 32
+// of 128 (2) 5.2 / 8.9, 32 of 512 (8) 11.4 / 13.0.  In two rounds of CTAs it is the
+// slower one: 64 of 256 14.7 / 13.8.
 struct Q8Cluster {
   int cluster, warps;
 };

@@ -32,9 +32,10 @@
 // What bounds it: of a key tile's 3690 cycles (two row tiles, 8192 positions) the
 // products take 2500, and the rest is a row tile's chain of S, softmax (2130 cycles), P
 // and P V, since S and O of two row tiles fill the tensor memory; an item's start and end
-// cost some 4 us more.  8 x 2048 tokens, 32 / 8 heads: int8 259 us, e4m3 257 (1062
-// TFLOP/s, 0.56 of the library's rate), 4 x 8192 1603 us (1372, 0.71); the bf16 kernel
-// 240 and 1529.  512 tokens after 8000 (floor 36) 69 us, 64 (4.4) 31.
+// cost some 4 us more.  8 x 2048 tokens, 32 / 8 heads: int8 264 us, e4m3 260 (1060
+// TFLOP/s, 0.55 of the library's rate), 4 x 8192 1624 and 1608 us (1368, 0.71); the bf16
+// kernel 240 and 1529.  512 tokens after 8000 (floor 36) 70 us, after 100000 (436) 595;
+// 64 after 8000 (4.4) 31.  The converters' proxy fence costs int8 1 % of the first.
 #include <climits>
 
 #include "decode_launch.cuh"
